@@ -30,6 +30,20 @@ from ._lib import (  # noqa: F401
     status_string,
     std_forward,
 )
+from ._paged import (  # noqa: F401
+    RopeAxes,
+    cache_append,
+    cache_compact,
+    cache_copy_pages,
+    cache_fork,
+    cache_free,
+    cache_reserve,
+    cache_workspace_bytes,
+    decode_paged,
+    decode_paged_workspace_bytes,
+    rope,
+    rope_backward,
+)
 
 __all__ = [
     "ZERO", "COPY_FIRST", "GIVEN", "CsaError", "forward", "forward_host", "HostForwardPipeline",
@@ -40,4 +54,7 @@ __all__ = [
     "logphi2_eval",
     "segment_weights_eval", "device_status", "selftest_forward_delay", "selftest_wait_timeout",
     "status_string",
+    "decode_paged", "decode_paged_workspace_bytes", "RopeAxes", "rope", "rope_backward",
+    "cache_append", "cache_reserve", "cache_free", "cache_fork", "cache_compact",
+    "cache_copy_pages", "cache_workspace_bytes",
 ]

@@ -45,6 +45,7 @@ def load():
             "`python -m continuous_softmax_attention_gb300.build` (no other compute path exists)")
     lib = ctypes.CDLL(LIB_PATH)
     p, i, f, u = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_uint
+    ll = ctypes.c_longlong
     fwd = [p, p, p, p, p, p, p, i, i, i, i, f, i, p]
     std = [p, p, p, p, p, i, i, i, i, f, p]
     bwd = [p, p, p, p, p, p, p, p, p, p, p, p, p, p, ctypes.c_longlong, i, i, i, i, f, i, p]
@@ -70,16 +71,29 @@ def load():
                        ("csa_forward_host", [p, p, p, p, p, p, p, p, ctypes.c_longlong, i, i, i,
                                              i, f, i, i, p, p, p]),
                        ("csa_forward_host_ex", [p, p, p, p, p, p, p, p, ctypes.c_longlong, i, i,
-                                                i, i, f, i, i, u, p, p, p])):
+                                                i, i, f, i, i, u, p, p, p]),
+                       ("csa_decode_paged", [p] * 10 + [ll] + [i] * 7 + [f, i, p]),
+                       ("csa_rope_plan_init", [p, p, i, ctypes.c_double, i]),
+                       ("csa_rope", [p] * 11 + [i] * 6 + [p]),
+                       ("csa_rope_f32", [p] * 11 + [i] * 6 + [p]),
+                       ("csa_cache_append", [p] * 16 + [i] * 8 + [p]),
+                       ("csa_cache_append_f32", [p] * 16 + [i] * 8 + [p]),
+                       ("csa_cache_reserve", [p] * 6 + [ll] + [i] * 4 + [p]),
+                       ("csa_cache_free", [p] * 4 + [i] * 5 + [p]),
+                       ("csa_cache_fork", [p] * 5 + [i] + [p] * 4 + [ll] + [i] * 4 + [p]),
+                       ("csa_cache_compact", [p] * 7 + [ll] + [i] * 4 + [p]),
+                       ("csa_cache_copy_pages", [p, p, ll, i, i, p, p, i, p, p])):
         fn = getattr(lib, name)
         fn.argtypes = args
         fn.restype = i
     for name in ("csa_decode_workspace_bytes", "csa_backward_workspace_bytes",
-                 "csa_forward_host_workspace_bytes"):
+                 "csa_forward_host_workspace_bytes", "csa_decode_paged_workspace_bytes"):
         getattr(lib, name).argtypes = [i, i, i, i]
         getattr(lib, name).restype = ctypes.c_longlong
     lib.csa_decode_range_workspace_bytes.argtypes = [i, i, i, i, i]
     lib.csa_decode_range_workspace_bytes.restype = ctypes.c_longlong
+    lib.csa_cache_workspace_bytes.argtypes = [i, i, i]
+    lib.csa_cache_workspace_bytes.restype = ctypes.c_longlong
     lib.csa_status_string.argtypes = [i]
     lib.csa_status_string.restype = ctypes.c_char_p
     _lib = lib

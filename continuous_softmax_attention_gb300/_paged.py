@@ -1,0 +1,422 @@
+"""ctypes binding of libcsa.so's paged cache and rotary positions
+(include/csa.h, "Paged key-value caches" and csa_rope_plan).
+
+Argument marshalling only, as in _lib.py.  Every call runs on the device of
+its tensors and is asynchronous on torch's current stream there, or on
+``stream``; what it allocates (outputs, workspaces) belongs to that stream.
+"""
+from __future__ import annotations
+
+import ctypes
+import functools
+
+import torch
+
+from ._lib import CSA_ERR_UNSUPPORTED, CsaError, _check, _check_tensor, _ptr, load
+
+MAX_PAIRS, MAX_AXES = 128, 8
+_FLAG_ADJACENT, _FLAG_DEALT = 1, 2
+
+
+class _Plan(ctypes.Structure):
+    """csa_rope_plan."""
+
+    _fields_ = [("pairs", ctypes.c_int), ("axes", ctypes.c_int), ("adjacent", ctypes.c_int),
+                ("axis", ctypes.c_ubyte * MAX_PAIRS), ("turn", ctypes.c_ulonglong * MAX_PAIRS)]
+
+
+class RopeAxes:
+    """Rotary positions with several axes: the plan that rope, rope_backward
+    and cache_append take.
+
+    d: row length; sections: how many pairs of a row turn by each axis (one to
+    eight axes, n = sum(sections) <= d / 2 pairs); pair i turns by
+    position * base^(-i / n).  adjacent: pairs (2i, 2i + 1) instead of
+    (i, i + n).  dealt: pairs dealt to the axes in turn instead of section
+    after section.  Columns from 2n on are left as they are."""
+
+    def __init__(self, d: int, sections, *, base: float = 10000.0, adjacent: bool = False,
+                 dealt: bool = False):
+        sections = [int(s) for s in sections]
+        if not 1 <= len(sections) <= MAX_AXES or min(sections) < 0 or sum(sections) < 1:
+            raise ValueError("sections: one to eight counts of pairs, not all 0")
+        if 2 * sum(sections) > d or d > 2 * MAX_PAIRS:
+            raise ValueError(f"{sum(sections)} pairs do not fit a row of {d} (at most "
+                             f"{2 * MAX_PAIRS} columns)")
+        self.d, self.sections, self.base = int(d), tuple(sections), float(base)
+        self.adjacent, self.dealt, self.axes = bool(adjacent), bool(dealt), len(sections)
+        self._plan = _Plan()
+        flags = (_FLAG_ADJACENT if adjacent else 0) | (_FLAG_DEALT if dealt else 0)
+        _check(load().csa_rope_plan_init(ctypes.byref(self._plan), (ctypes.c_int * self.axes)(*sections),
+                                         self.axes, self.base, flags), "csa_rope_plan_init")
+        self._ref = ctypes.byref(self._plan)
+
+
+def _launches(fn):
+    """The call `fn` on the device of its first tensor and on `stream`."""
+
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        dev = next((a.device for a in (*args, *kw.values()) if isinstance(a, torch.Tensor)), None)
+        if dev is None or dev.type != "cuda":
+            raise ValueError(f"{fn.__name__} takes CUDA tensors")
+        if stream is None and dev.index == torch.cuda.current_device():
+            return fn(*args, **kw)
+        if stream is not None and stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+        with torch.cuda.device(dev):
+            if stream is None:
+                return fn(*args, **kw)
+            with torch.cuda.stream(stream):
+                return fn(*args, **kw)
+
+    return call
+
+
+def _stream():
+    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+
+def _workspace(workspace, nbytes, dev):
+    if workspace is None:
+        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=dev)
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    return workspace
+
+
+def _nbytes(t):
+    return t.numel() * t.element_size()
+
+
+def _out(t, name, dtype, shape, dev):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _check_tensor(t, name, dtype, shape, dev)
+    return t
+
+
+def decode_paged_workspace_bytes(B: int, Hq: int, Hkv: int, d: int) -> int:
+    """Bytes of workspace csa_decode_paged needs (host-side, no device needed)."""
+    n = int(load().csa_decode_paged_workspace_bytes(int(B), int(Hq), int(Hkv), int(d)))
+    if n < 0:
+        raise CsaError(CSA_ERR_UNSUPPORTED, "csa_decode_paged_workspace_bytes")
+    return n
+
+
+@_launches
+def decode_paged(q, k_pages, v_pages, block_table, seqlens, k0=None, v0=None, *, mode: int = 0,
+                 scale=None, out=None, lse=None, workspace=None, want_lse: bool = True):
+    """One decode step over a paged cache: the newest token of each sequence
+    against the rows in its pages.  Returns (o [B, Hq, d], lse [B, Hq]).
+
+    q: bf16 CUDA [B, Hq, d]; k_pages, v_pages: bf16 [P, Hkv, S, d], query head
+    h reading cached head h // (Hq // Hkv); block_table: int32 [B, M], the
+    pages of each sequence in order; seqlens: int32 [B], the tokens held with
+    the newest one (0: an empty place in the batch, o = 0 and lse = -inf).
+    k0, v0: [Hkv, d] in mode GIVEN (2).  d in {64, 128, 256}, S a multiple of
+    8.  workspace: a CUDA tensor of decode_paged_workspace_bytes(B, Hq, Hkv,
+    d) bytes (allocated when None); stream: as everywhere, torch's current
+    stream when None."""
+    if q.dim() != 3 or k_pages.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("q is [B, Hq, d], the pools [P, Hkv, S, d], block_table [B, M]")
+    B, Hq, d = q.shape
+    P, Hkv, S, _ = k_pages.shape
+    M = block_table.shape[1]
+    dev, bf = q.device, torch.bfloat16
+    _check_tensor(q, "q", bf, (B, Hq, d), dev)
+    _check_tensor(k_pages, "k_pages", bf, (P, Hkv, S, d), dev)
+    _check_tensor(v_pages, "v_pages", bf, (P, Hkv, S, d), dev)
+    _check_tensor(block_table, "block_table", torch.int32, (B, M), dev)
+    _check_tensor(seqlens, "seqlens", torch.int32, (B,), dev)
+    if mode == 2:
+        if k0 is None or v0 is None:
+            raise ValueError("mode 2 (given sink) needs k0 and v0")
+        _check_tensor(k0, "k0", bf, (Hkv, d), dev)
+        _check_tensor(v0, "v0", bf, (Hkv, d), dev)
+    else:
+        k0 = v0 = None
+    if scale is None:
+        scale = 1.0 / d ** 0.5
+    out = _out(out, "out", bf, (B, Hq, d), dev)
+    if lse is not None or want_lse:
+        lse = _out(lse, "lse", torch.float32, (B, Hq), dev)
+    lib = load()
+    if workspace is None:
+        workspace = _workspace(None, max(0, lib.csa_decode_paged_workspace_bytes(B, Hq, Hkv, d)), dev)
+    else:
+        _workspace(workspace, 0, dev)
+    _check(lib.csa_decode_paged(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(k0), _ptr(v0),
+                                _ptr(block_table), _ptr(seqlens), _ptr(out), _ptr(lse),
+                                _ptr(workspace), _nbytes(workspace), B, Hq, Hkv, P, S, M, d,
+                                float(scale), int(mode), _stream()), "csa_decode_paged")
+    return out, lse
+
+
+# ------------------------------------------------------------ rotary positions
+_Strides = ctypes.c_longlong * 3
+
+
+def _rows(t, name, dtype, shape, dev, written=False):
+    """Checks a tensor of rows [B, H, T, d] of any strides and returns its
+    strides over batch, head and time."""
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    sb, sh, st, sd = t.stride()
+    if sd != 1 and shape[3] > 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    if written and not t.is_contiguous():
+        reach = shape[3]
+        for stride, size in sorted(zip((sb, sh, st), shape)):
+            if size > 1:
+                if stride < reach:
+                    raise ValueError(f"rows of {name} overlap")
+                reach += stride * (size - 1)
+    return _Strides(sb, sh, st)
+
+
+def _position_strides(positions, plan, B, T, dev):
+    if positions.device != dev or positions.dtype != torch.int32:
+        raise ValueError(f"positions must be int32 on {dev}, got {positions.dtype} on {positions.device}")
+    shape, stride = tuple(positions.shape), positions.stride()
+    if shape == (plan.axes, B, T):
+        return _Strides(*stride)
+    if plan.axes == 1 and shape == (B, T):
+        return _Strides(0, *stride)
+    if plan.axes == 1 and shape == (T,):
+        return _Strides(0, 0, *stride)
+    raise ValueError(f"positions must have shape {(plan.axes, B, T)}"
+                     + (f", {(B, T)} or {(T,)}" if plan.axes == 1 else "") + f", got {shape}")
+
+
+def _check_plan(plan, d):
+    if not isinstance(plan, RopeAxes):
+        raise ValueError("the plan must be a RopeAxes")
+    if plan.d != d:
+        raise ValueError(f"the plan is for rows of {plan.d}, got {d}")
+
+
+def _float_kind(dtype):
+    if dtype == torch.bfloat16:
+        return ""
+    if dtype == torch.float32:
+        return "_f32"
+    raise ValueError(f"unsupported dtype {dtype}")
+
+
+def _rope(q, k, positions, plan, q_out, k_out, inverse):
+    if q.dim() != 4 or (k is not None and k.dim() != 4):
+        raise ValueError("q and k are [B, H, T, d]")
+    B, Hq, T, d = q.shape
+    dev, dtype = q.device, q.dtype
+    where = "csa_rope" + _float_kind(dtype)
+    _check_plan(plan, d)
+    qs, ks, kos, Hkv = _rows(q, "q", dtype, q.shape, dev), None, None, 0
+    ps = _position_strides(positions, plan, B, T, dev)
+    if q_out is None:
+        q_out = torch.empty((B, Hq, T, d), dtype=dtype, device=dev)
+    qos = _rows(q_out, "q_out", dtype, q.shape, dev, True)
+    if k is None:
+        k_out = None
+    else:
+        Hkv = k.shape[1]
+        shape = torch.Size((B, Hkv, T, d))
+        ks = _rows(k, "k", dtype, shape, dev)
+        if k_out is None:
+            k_out = torch.empty((B, Hkv, T, d), dtype=dtype, device=dev)
+        kos = _rows(k_out, "k_out", dtype, shape, dev, True)
+    _check(getattr(load(), where)(plan._ref, _ptr(q), qs, _ptr(q_out), qos, _ptr(k), ks, _ptr(k_out), kos,
+                                  _ptr(positions), ps, B, Hq, Hkv, T, d, int(inverse), _stream()), where)
+    return q_out, k_out
+
+
+@_launches
+def rope(q, k, positions, plan, *, q_out=None, k_out=None):
+    """Rotary positions on queries and keys.  Returns (q', k').
+
+    q: CUDA [B, Hq, T, d], k: [B, Hkv, T, d] or None, both bf16 or both fp32,
+    with any strides whose last one is 1 (for instance slices of one fused
+    projection); positions: int32 [axes, B, T] of any strides ([B, T] or [T]
+    too for a plan of one axis); plan: a RopeAxes.  q_out, k_out: where the
+    results go, the input itself among them (contiguous tensors when None)."""
+    return _rope(q, k, positions, plan, q_out, k_out, False)
+
+
+@_launches
+def rope_backward(dq, dk, positions, plan, *, q_out=None, k_out=None):
+    """Backward pass of rope: the gradients of q and k from the gradients of
+    rope's results, rotated by the negative angles.  Arguments as rope."""
+    return _rope(dq, dk, positions, plan, q_out, k_out, True)
+
+
+@_launches
+def cache_append(k, v, k_pages, v_pages, block_table, seqlens, *, counts=None, rope=None,
+                 positions=None, q=None, q_out=None):
+    """Writes the rows of new tokens into their pages, the keys rotated if a
+    plan is given, and rotates their queries beside.  Returns q' (None without q).
+
+    k, v: CUDA [B, Hkv, T, d] of any strides whose last one is 1, bf16 or
+    fp32; row t < counts[b] (int32 [B]; T each when None) becomes token
+    seqlens[b] - counts[b] + t of sequence b: seqlens counts the new tokens
+    already, as cache_reserve leaves it.  k_pages, v_pages: [P, Hkv, S, d];
+    block_table: int32 [B, M].  rope: a RopeAxes; positions as in rope(), or
+    None for a token's place in the cache.  q: [B, Hq, T, d], with rope only."""
+    if k.dim() != 4 or k_pages.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("k and v are [B, Hkv, T, d], the pools [P, Hkv, S, d], block_table [B, M]")
+    B, Hkv, T, d = k.shape
+    P, _, S, _ = k_pages.shape
+    M = block_table.shape[1]
+    dev, dtype = k.device, k.dtype
+    where = "csa_cache_append" + _float_kind(dtype)
+    ks = _rows(k, "k", dtype, k.shape, dev)
+    vs = _rows(v, "v", dtype, k.shape, dev)
+    _check_tensor(k_pages, "k_pages", dtype, (P, Hkv, S, d), dev)
+    _check_tensor(v_pages, "v_pages", dtype, (P, Hkv, S, d), dev)
+    _check_tensor(block_table, "block_table", torch.int32, (B, M), dev)
+    _check_tensor(seqlens, "seqlens", torch.int32, (B,), dev)
+    if counts is not None:
+        _check_tensor(counts, "counts", torch.int32, (B,), dev)
+    ref = ps = qs = qos = None
+    Hq = 0
+    if rope is None:
+        if q is not None or positions is not None:
+            raise ValueError("q and positions go with a rope plan")
+        q_out = None
+    else:
+        _check_plan(rope, d)
+        ref = rope._ref
+        if positions is not None:
+            ps = _position_strides(positions, rope, B, T, dev)
+        if q is None:
+            q_out = None
+        else:
+            if q.dim() != 4:
+                raise ValueError("q is [B, Hq, T, d]")
+            Hq = q.shape[1]
+            shape = torch.Size((B, Hq, T, d))
+            qs = _rows(q, "q", dtype, shape, dev)
+            if q_out is None:
+                q_out = torch.empty((B, Hq, T, d), dtype=dtype, device=dev)
+            qos = _rows(q_out, "q_out", dtype, shape, dev, True)
+    _check(getattr(load(), where)(ref, _ptr(q), qs, _ptr(q_out), qos, _ptr(k), ks, _ptr(v), vs,
+                                  _ptr(k_pages), _ptr(v_pages), _ptr(block_table), _ptr(seqlens),
+                                  _ptr(counts), _ptr(positions), ps, B, Hq, Hkv, T, d, P, S, M,
+                                  _stream()), where)
+    return q_out
+
+
+# ------------------------------------------------------------------------ pages
+def cache_workspace_bytes(B: int, P: int, n: int = 0) -> int:
+    """Bytes of workspace cache_reserve, cache_fork (n pairs) and cache_compact
+    need (host-side, no device needed)."""
+    r = int(load().csa_cache_workspace_bytes(int(B), int(P), int(n)))
+    if r < 0:
+        raise CsaError(CSA_ERR_UNSUPPORTED, "csa_cache_workspace_bytes")
+    return r
+
+
+def _books(page_refs, block_table, seqlens):
+    dev = page_refs.device
+    if page_refs.dim() != 1 or block_table.dim() != 2:
+        raise ValueError("page_refs is [P], block_table [B, M]")
+    P, (B, M) = page_refs.shape[0], block_table.shape
+    _check_tensor(page_refs, "page_refs", torch.int32, (P,), dev)
+    _check_tensor(block_table, "block_table", torch.int32, (B, M), dev)
+    _check_tensor(seqlens, "seqlens", torch.int32, (B,), dev)
+    return dev, P, B, M
+
+
+@_launches
+def cache_reserve(page_refs, block_table, seqlens, page_size: int, counts, *, shortfall=None,
+                  workspace=None):
+    """Room for counts[b] more tokens of every sequence: takes the missing pages
+    (lowest-numbered free ones first), enters them into the table and adds
+    counts to seqlens.  Returns shortfall (int32 [1], on the device): 0 if it
+    was done, else nothing has changed and it is the number of pages missing
+    from the pool, or -1 for a count that does not fit the table.
+
+    page_refs: int32 [P]; block_table: int32 [B, M]; seqlens, counts: int32 [B]."""
+    dev, P, B, M = _books(page_refs, block_table, seqlens)
+    _check_tensor(counts, "counts", torch.int32, (B,), dev)
+    shortfall = _out(shortfall, "shortfall", torch.int32, (1,), dev)
+    workspace = _workspace(workspace, cache_workspace_bytes(B, P), dev)
+    _check(load().csa_cache_reserve(_ptr(page_refs), _ptr(block_table), _ptr(seqlens), _ptr(counts),
+                                    _ptr(shortfall), _ptr(workspace), _nbytes(workspace), B, P,
+                                    int(page_size), M, _stream()), "csa_cache_reserve")
+    return shortfall
+
+
+@_launches
+def cache_free(page_refs, block_table, seqlens, page_size: int, rows):
+    """The listed sequences (int32 [R]; -1 is padding) give their pages back:
+    their entries become -1, their lengths 0."""
+    dev, P, B, M = _books(page_refs, block_table, seqlens)
+    _check_tensor(rows, "rows", torch.int32, (rows.numel(),), dev)
+    _check(load().csa_cache_free(_ptr(page_refs), _ptr(block_table), _ptr(seqlens), _ptr(rows),
+                                 rows.numel(), B, P, int(page_size), M, _stream()), "csa_cache_free")
+
+
+@_launches
+def cache_fork(page_refs, block_table, seqlens, page_size: int, parents, children, *,
+               workspace=None):
+    """children[i] (an empty sequence) becomes a copy of parents[i] (int32 [n]
+    both; a negative entry is padding): full pages are shared, a partly filled
+    last page gets a page of its own.  Returns (src, dst, shortfall): the pages
+    to copy with cache_copy_pages in every pool (-1 where there is none), and
+    shortfall as in cache_reserve."""
+    dev, P, B, M = _books(page_refs, block_table, seqlens)
+    n = parents.numel()
+    _check_tensor(parents, "parents", torch.int32, (n,), dev)
+    _check_tensor(children, "children", torch.int32, (n,), dev)
+    src, dst = torch.empty((2, n), dtype=torch.int32, device=dev).unbind()
+    shortfall = torch.empty(1, dtype=torch.int32, device=dev)
+    workspace = _workspace(workspace, cache_workspace_bytes(B, P, n), dev)
+    _check(load().csa_cache_fork(_ptr(page_refs), _ptr(block_table), _ptr(seqlens), _ptr(parents),
+                                 _ptr(children), n, _ptr(src), _ptr(dst), _ptr(shortfall),
+                                 _ptr(workspace), _nbytes(workspace), B, P, int(page_size), M,
+                                 _stream()), "csa_cache_fork")
+    return src, dst, shortfall
+
+
+@_launches
+def cache_compact(page_refs, block_table, seqlens, page_size: int, *, workspace=None):
+    """Gives the U held pages the numbers 0 .. U - 1.  Returns (src, dst,
+    moved): int32 [P // 2] twice and [1]; the pools follow with
+    cache_copy_pages(..., src, dst, count=moved) before they are read again."""
+    dev, P, B, M = _books(page_refs, block_table, seqlens)
+    src, dst = torch.empty((2, P // 2), dtype=torch.int32, device=dev).unbind()
+    moved = torch.empty(1, dtype=torch.int32, device=dev)
+    workspace = _workspace(workspace, cache_workspace_bytes(B, P), dev)
+    _check(load().csa_cache_compact(_ptr(page_refs), _ptr(block_table), _ptr(seqlens), _ptr(src),
+                                    _ptr(dst), _ptr(moved), _ptr(workspace), _nbytes(workspace), B,
+                                    P, int(page_size), M, _stream()), "csa_cache_compact")
+    return src, dst, moved
+
+
+@_launches
+def cache_copy_pages(k_pages, v_pages, src, dst, *, count=None):
+    """Copies page src[i] onto page dst[i] (int32 [n]; a negative entry is
+    padding) for i < min(n, count) in both pools, [P, Hkv, S, d] or, for
+    several layers at once, [L, P, Hkv, S, d]; any type.  v_pages may be None;
+    count: int32 [1] on the device.  A page that is a dst must not occur in
+    another pair."""
+    dev = k_pages.device
+    if k_pages.dim() not in (4, 5):
+        raise ValueError("the pools are [P, Hkv, S, d] or [L, P, Hkv, S, d]")
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        if t is not None:
+            _check_tensor(t, name, k_pages.dtype, k_pages.shape, dev)
+    L = k_pages.shape[0] if k_pages.dim() == 5 else 1
+    P, Hkv, S, d = k_pages.shape[-4:]
+    n = src.numel()
+    _check_tensor(src, "src", torch.int32, (n,), dev)
+    _check_tensor(dst, "dst", torch.int32, (n,), dev)
+    if count is not None:
+        _check_tensor(count, "count", torch.int32, (1,), dev)
+    _check(load().csa_cache_copy_pages(_ptr(k_pages), _ptr(v_pages), Hkv * S * d * k_pages.element_size(),
+                                       L, P, _ptr(src), _ptr(dst), n, _ptr(count), _stream()),
+           "csa_cache_copy_pages")

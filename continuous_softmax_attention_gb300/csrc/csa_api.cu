@@ -6,6 +6,7 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 
 #include "csa.h"
 #include "csa_internal.h"
@@ -225,9 +226,247 @@ int backward_any(const void *q, const void *k, const void *v, const void *k0, co
         static_cast<float *>(dv), dk0, dv0, workspace, B, H, T, d, scale, mode, s));
 }
 
+// ------------------------------------------------------ paged cache and rope
+constexpr long long kIntMax = 0x7fffffffLL;
+
+// Sizes of a paged cache's tables.
+int check_tables(int B, int P, int S, int M) {
+    if (B < 0 || P < 0 || S < 1 || M < 1) return CSA_ERR_INVALID_ARG;
+    if ((long long)B * M > kIntMax || (long long)M * S > kIntMax) return CSA_ERR_UNSUPPORTED;
+    return CSA_OK;
+}
+
+int check_books(const int *refs, const int *table, const int *seqlens, int B, int P, int S, int M) {
+    int rc = check_tables(B, P, S, M);
+    if (rc != CSA_OK) return rc;
+    if ((!refs && P > 0) || ((!table || !seqlens) && B > 0)) return CSA_ERR_INVALID_ARG;
+    if (!aligned(refs, 4) || !aligned(table, 4) || !aligned(seqlens, 4)) return CSA_ERR_ALIGNMENT;
+    return CSA_OK;
+}
+
+int check_cache_workspace(const void *workspace, long long bytes, int B, int P, int n) {
+    if (!workspace || bytes < csa_cache_scratch_bytes(B, P, n)) return CSA_ERR_INVALID_ARG;
+    return aligned(workspace, 4) ? CSA_OK : CSA_ERR_ALIGNMENT;
+}
+
+// A plan that csa_rope_plan_init can have made: the kernels index by its fields.
+bool sound_plan(const csa_rope_plan *plan) {
+    if (plan->pairs < 1 || plan->pairs > CSA_ROPE_MAX_PAIRS || plan->axes < 1 ||
+        plan->axes > CSA_ROPE_MAX_AXES)
+        return false;
+    for (int i = 0; i < plan->pairs; ++i)
+        if (plan->axis[i] >= plan->axes) return false;
+    return true;
+}
+
+int rope_any(const csa_rope_plan *plan, const void *q, const long long *q_strides, void *q_out,
+             const long long *q_out_strides, const void *k, const long long *k_strides,
+             void *k_out, const long long *k_out_strides, const int *positions,
+             const long long *pos_strides, int B, int Hq, int Hkv, int T, int d, int inverse,
+             bool bf16, csa_stream_t stream) {
+    if (!plan || !sound_plan(plan)) return CSA_ERR_INVALID_ARG;
+    if (B < 0 || Hq < 0 || Hkv < 0 || T < 0 || d < 1 || 2 * plan->pairs > d) return CSA_ERR_INVALID_ARG;
+    if (d > 256 || (long long)B * T > kIntMax || (long long)Hq + Hkv > 65535) return CSA_ERR_UNSUPPORTED;
+    if ((long long)B * T == 0 || (long long)Hq + Hkv == 0) return CSA_OK;
+    if ((Hq > 0 && (!q || !q_out)) || (Hkv > 0 && (!k || !k_out)) || !positions)
+        return CSA_ERR_INVALID_ARG;
+    const uintptr_t al = bf16 ? 2 : 4;
+    if (!aligned(q, al) || !aligned(q_out, al) || !aligned(k, al) || !aligned(k_out, al) ||
+        !aligned(positions, 4))
+        return CSA_ERR_ALIGNMENT;
+    int rc = device_ok();
+    if (rc != CSA_OK) return rc;
+    return csa_rope_run(plan, q, q_strides, q_out, q_out_strides, k, k_strides, k_out,
+                        k_out_strides, positions, pos_strides, B, Hq, Hkv, T, d, inverse != 0, bf16,
+                        reinterpret_cast<cudaStream_t>(stream));
+}
+
+int append_any(const csa_rope_plan *plan, const void *q, const long long *q_strides, void *q_out,
+               const long long *q_out_strides, const void *k, const long long *k_strides,
+               const void *v, const long long *v_strides, void *k_pages, void *v_pages,
+               const int *block_table, const int *seqlens, const int *counts, const int *positions,
+               const long long *pos_strides, int B, int Hq, int Hkv, int T, int d, int P, int S,
+               int M, bool bf16, csa_stream_t stream) {
+    if (plan && !sound_plan(plan)) return CSA_ERR_INVALID_ARG;
+    if (B < 0 || Hq < 0 || Hkv < 1 || T < 0 || d < 1) return CSA_ERR_INVALID_ARG;
+    if (plan ? 2 * plan->pairs > d : Hq > 0) return CSA_ERR_INVALID_ARG;
+    int rc = check_tables(B, P, S, M);
+    if (rc != CSA_OK) return rc;
+    if (d > 256 || (long long)B * T > kIntMax || (long long)Hq + 2LL * Hkv > 65535)
+        return CSA_ERR_UNSUPPORTED;
+    if ((long long)B * T == 0) return CSA_OK;
+    if (!k || !v || !k_pages || !v_pages || !block_table || !seqlens || (Hq > 0 && (!q || !q_out)))
+        return CSA_ERR_INVALID_ARG;
+    const uintptr_t al = bf16 ? 2 : 4;
+    if (!aligned(q, al) || !aligned(q_out, al) || !aligned(k, al) || !aligned(v, al) ||
+        !aligned(k_pages, al) || !aligned(v_pages, al) || !aligned(block_table, 4) ||
+        !aligned(seqlens, 4) || !aligned(counts, 4) || !aligned(positions, 4))
+        return CSA_ERR_ALIGNMENT;
+    if ((rc = device_ok()) != CSA_OK) return rc;
+    return csa_cache_append_run(plan, q, q_strides, q_out, q_out_strides, k, k_strides, v, v_strides,
+                                k_pages, v_pages, block_table, seqlens, counts, positions,
+                                pos_strides, B, Hq, Hkv, T, d, P, S, M, bf16,
+                                reinterpret_cast<cudaStream_t>(stream));
+}
+
 }  // namespace
 
 extern "C" {
+
+long long csa_decode_paged_workspace_bytes(int B, int Hq, int Hkv, int d) {
+    if (B < 0 || Hq < 0 || Hkv < 1 || Hq % Hkv != 0) return -1;
+    return csa_decode_paged_scratch_bytes(B, Hq, Hkv, d);
+}
+
+int csa_decode_paged(const void *q, const void *k_pages, const void *v_pages, const void *k0,
+                     const void *v0, const int *block_table, const int *seqlens, void *out,
+                     float *lse, void *workspace, long long workspace_bytes, int B, int Hq,
+                     int Hkv, int P, int S, int M, int d, float scale, int k0_mode,
+                     csa_stream_t stream) {
+    if (Hq < 0 || Hkv < 1 || Hq % Hkv != 0 || d < 1) return CSA_ERR_INVALID_ARG;
+    if (!std::isfinite(scale)) return CSA_ERR_INVALID_ARG;
+    if (k0_mode < CSA_K0_ZERO || k0_mode > CSA_K0_GIVEN) return CSA_ERR_INVALID_ARG;
+    int rc = check_tables(B, P, S, M);
+    if (rc != CSA_OK) return rc;
+    if (!(d == 64 || d == 128 || d == 256) || S % 8 != 0) return CSA_ERR_UNSUPPORTED;
+    if ((long double)P * Hkv * S > kIntMax) return CSA_ERR_UNSUPPORTED;
+    if ((long long)B * Hq > kIntMax) return CSA_ERR_UNSUPPORTED;
+    if ((long long)B * Hq == 0) return CSA_OK;
+    if (!q || !k_pages || !v_pages || !block_table || !seqlens || !out) return CSA_ERR_INVALID_ARG;
+    if (k0_mode == CSA_K0_GIVEN && (!k0 || !v0)) return CSA_ERR_INVALID_ARG;
+    const long long need = csa_decode_paged_scratch_bytes(B, Hq, Hkv, d);
+    if (need < 0) return CSA_ERR_UNSUPPORTED;
+    if (!workspace || workspace_bytes < need) return CSA_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(out, 16) ||
+        !aligned(workspace, 16) || !aligned(lse, 4) || !aligned(seqlens, 4) ||
+        !aligned(block_table, 4))
+        return CSA_ERR_ALIGNMENT;
+    if (k0_mode == CSA_K0_GIVEN && (!aligned(k0, 16) || !aligned(v0, 16))) return CSA_ERR_ALIGNMENT;
+    if ((rc = device_ok()) != CSA_OK) return rc;
+    return csa_decode_paged_run(q, k_pages, v_pages, k0, v0, block_table, seqlens, out, lse,
+                                workspace, B, Hq, Hkv, P, S, M, d, scale, k0_mode,
+                                reinterpret_cast<cudaStream_t>(stream));
+}
+
+int csa_rope_plan_init(csa_rope_plan *plan, const int *sections, int axes, double base, int flags) {
+    if (!plan || !sections || axes < 1 || axes > CSA_ROPE_MAX_AXES) return CSA_ERR_INVALID_ARG;
+    if (!std::isfinite(base) || base <= 0.0 || (flags & ~(CSA_ROPE_ADJACENT | CSA_ROPE_DEALT)))
+        return CSA_ERR_INVALID_ARG;
+    return csa_rope_plan_make(plan, sections, axes, base, flags);
+}
+
+int csa_rope(const csa_rope_plan *plan, const void *q, const long long *q_strides, void *q_out,
+             const long long *q_out_strides, const void *k, const long long *k_strides,
+             void *k_out, const long long *k_out_strides, const int *positions,
+             const long long *pos_strides, int B, int Hq, int Hkv, int T, int d, int inverse,
+             csa_stream_t stream) {
+    return rope_any(plan, q, q_strides, q_out, q_out_strides, k, k_strides, k_out, k_out_strides,
+                    positions, pos_strides, B, Hq, Hkv, T, d, inverse, true, stream);
+}
+
+int csa_rope_f32(const csa_rope_plan *plan, const float *q, const long long *q_strides,
+                 float *q_out, const long long *q_out_strides, const float *k,
+                 const long long *k_strides, float *k_out, const long long *k_out_strides,
+                 const int *positions, const long long *pos_strides, int B, int Hq, int Hkv, int T,
+                 int d, int inverse, csa_stream_t stream) {
+    return rope_any(plan, q, q_strides, q_out, q_out_strides, k, k_strides, k_out, k_out_strides,
+                    positions, pos_strides, B, Hq, Hkv, T, d, inverse, false, stream);
+}
+
+int csa_cache_append(const csa_rope_plan *plan, const void *q, const long long *q_strides,
+                     void *q_out, const long long *q_out_strides, const void *k,
+                     const long long *k_strides, const void *v, const long long *v_strides,
+                     void *k_pages, void *v_pages, const int *block_table, const int *seqlens,
+                     const int *counts, const int *positions, const long long *pos_strides, int B,
+                     int Hq, int Hkv, int T, int d, int P, int S, int M, csa_stream_t stream) {
+    return append_any(plan, q, q_strides, q_out, q_out_strides, k, k_strides, v, v_strides, k_pages,
+                      v_pages, block_table, seqlens, counts, positions, pos_strides, B, Hq, Hkv, T,
+                      d, P, S, M, true, stream);
+}
+
+int csa_cache_append_f32(const csa_rope_plan *plan, const float *q, const long long *q_strides,
+                         float *q_out, const long long *q_out_strides, const float *k,
+                         const long long *k_strides, const float *v, const long long *v_strides,
+                         float *k_pages, float *v_pages, const int *block_table,
+                         const int *seqlens, const int *counts, const int *positions,
+                         const long long *pos_strides, int B, int Hq, int Hkv, int T, int d, int P,
+                         int S, int M, csa_stream_t stream) {
+    return append_any(plan, q, q_strides, q_out, q_out_strides, k, k_strides, v, v_strides, k_pages,
+                      v_pages, block_table, seqlens, counts, positions, pos_strides, B, Hq, Hkv, T,
+                      d, P, S, M, false, stream);
+}
+
+int csa_cache_reserve(int *page_refs, int *block_table, int *seqlens, const int *counts,
+                      int *shortfall, void *workspace, long long workspace_bytes, int B, int P,
+                      int S, int M, csa_stream_t stream) {
+    int rc = check_books(page_refs, block_table, seqlens, B, P, S, M);
+    if (rc != CSA_OK) return rc;
+    if ((!counts && B > 0) || !shortfall) return CSA_ERR_INVALID_ARG;
+    if ((rc = check_cache_workspace(workspace, workspace_bytes, B, P, 0)) != CSA_OK) return rc;
+    if (!aligned(counts, 4) || !aligned(shortfall, 4)) return CSA_ERR_ALIGNMENT;
+    if ((rc = device_ok()) != CSA_OK) return rc;
+    return csa_cache_reserve_run(page_refs, block_table, seqlens, counts, shortfall, workspace, B, P,
+                                 S, M, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int csa_cache_free(int *page_refs, int *block_table, int *seqlens, const int *rows, int R, int B,
+                   int P, int S, int M, csa_stream_t stream) {
+    int rc = check_books(page_refs, block_table, seqlens, B, P, S, M);
+    if (rc != CSA_OK) return rc;
+    if (R < 0 || (R > 0 && !rows)) return CSA_ERR_INVALID_ARG;
+    if (!aligned(rows, 4)) return CSA_ERR_ALIGNMENT;
+    if (R == 0) return CSA_OK;
+    if ((rc = device_ok()) != CSA_OK) return rc;
+    return csa_cache_free_run(page_refs, block_table, seqlens, rows, R, B, P, S, M,
+                              reinterpret_cast<cudaStream_t>(stream));
+}
+
+int csa_cache_fork(int *page_refs, int *block_table, int *seqlens, const int *parents,
+                   const int *children, int n, int *src, int *dst, int *shortfall,
+                   void *workspace, long long workspace_bytes, int B, int P, int S, int M,
+                   csa_stream_t stream) {
+    int rc = check_books(page_refs, block_table, seqlens, B, P, S, M);
+    if (rc != CSA_OK) return rc;
+    if (n < 0 || !shortfall || (n > 0 && (!parents || !children || !src || !dst)))
+        return CSA_ERR_INVALID_ARG;
+    if ((rc = check_cache_workspace(workspace, workspace_bytes, B, P, n)) != CSA_OK) return rc;
+    if (!aligned(parents, 4) || !aligned(children, 4) || !aligned(src, 4) || !aligned(dst, 4) ||
+        !aligned(shortfall, 4))
+        return CSA_ERR_ALIGNMENT;
+    if ((rc = device_ok()) != CSA_OK) return rc;
+    return csa_cache_fork_run(page_refs, block_table, seqlens, parents, children, n, src, dst,
+                              shortfall, workspace, B, P, S, M,
+                              reinterpret_cast<cudaStream_t>(stream));
+}
+
+int csa_cache_compact(int *page_refs, int *block_table, const int *seqlens, int *src, int *dst,
+                      int *moved, void *workspace, long long workspace_bytes, int B, int P, int S,
+                      int M, csa_stream_t stream) {
+    int rc = check_books(page_refs, block_table, seqlens, B, P, S, M);
+    if (rc != CSA_OK) return rc;
+    if (!moved || (P > 1 && (!src || !dst))) return CSA_ERR_INVALID_ARG;
+    if ((rc = check_cache_workspace(workspace, workspace_bytes, B, P, 0)) != CSA_OK) return rc;
+    if (!aligned(src, 4) || !aligned(dst, 4) || !aligned(moved, 4)) return CSA_ERR_ALIGNMENT;
+    if ((rc = device_ok()) != CSA_OK) return rc;
+    return csa_cache_compact_run(page_refs, block_table, seqlens, src, dst, moved, workspace, B, P,
+                                 S, M, reinterpret_cast<cudaStream_t>(stream));
+}
+
+long long csa_cache_workspace_bytes(int B, int P, int n) { return csa_cache_scratch_bytes(B, P, n); }
+
+int csa_cache_copy_pages(void *k_pages, void *v_pages, long long page_bytes, int layers, int P,
+                         const int *src, const int *dst, int n, const int *count,
+                         csa_stream_t stream) {
+    if (page_bytes < 0 || layers < 0 || P < 0 || n < 0) return CSA_ERR_INVALID_ARG;
+    if (page_bytes == 0 || layers == 0 || P == 0 || n == 0) return CSA_OK;
+    if (!k_pages || !src || !dst) return CSA_ERR_INVALID_ARG;
+    if ((long double)page_bytes * layers * P > 9.0e18L) return CSA_ERR_UNSUPPORTED;
+    if (!aligned(src, 4) || !aligned(dst, 4) || !aligned(count, 4)) return CSA_ERR_ALIGNMENT;
+    int rc = device_ok();
+    if (rc != CSA_OK) return rc;
+    return csa_cache_copy_pages_run(k_pages, v_pages, page_bytes, layers, P, src, dst, n, count,
+                                    reinterpret_cast<cudaStream_t>(stream));
+}
 
 long long csa_backward_workspace_bytes(int B, int H, int T, int d) {
     return backward_scratch_bytes(B, H, T, d);
@@ -412,7 +651,12 @@ int csa_device_status(void) {
     const int b = csa_tc_std_take_status();
     const int c = csa_decode_take_status();
     const int e = csa_tc_backward_take_status();
-    return a != CSA_OK ? a : b != CSA_OK ? b : c != CSA_OK ? c : e;
+    const int f = csa_paged_take_status();
+    const int g = csa_rope_take_status();
+    const int h = csa_cache_take_status();
+    for (const int word : {a, b, c, e, f, g, h})
+        if (word != CSA_OK) return word;
+    return CSA_OK;
 }
 
 int csa_selftest_wait_timeout(unsigned timeout_us, csa_stream_t stream) {

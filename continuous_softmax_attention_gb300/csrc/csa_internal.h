@@ -4,6 +4,8 @@
 
 #include <cuda_runtime.h>
 
+#include "csa.h"
+
 // Forms of the forward pass: eq. (10)/(11), the short-conv reading of
 // eq. (13) (b replaced by its first-order term), eq. (12), eq. (2) over
 // the symmetric interval [1/2, t + 1/2] (constant end half-cells, no sink),
@@ -99,3 +101,43 @@ int csa_host_forward(const void *q_h, const void *k_h, const void *v_h, const vo
                      const void *v0, void *out_h, float *lse_h, void *scratch, int B, int H, int T,
                      int d, float scale, int mode, int heads_per_chunk, bool entry_wait,
                      cudaStream_t s_compute, cudaStream_t s_h2d, cudaStream_t s_d2h);
+
+// Decode step over a paged cache (csa_paged.cu), bf16, d in {64, 128, 256}.
+long long csa_decode_paged_scratch_bytes(int B, int Hq, int Hkv, int d);
+int csa_decode_paged_run(const void *q, const void *k_pages, const void *v_pages, const void *k0,
+                         const void *v0, const int *block_table, const int *seqlens, void *out,
+                         float *lse, void *scratch, int B, int Hq, int Hkv, int P, int S, int M,
+                         int d, float scale, int mode, cudaStream_t stream);
+int csa_paged_take_status(void);
+
+// Rotary positions and the rows of new tokens into pages (csa_rope.cu).
+int csa_rope_plan_make(csa_rope_plan *plan, const int *sections, int axes, double base, int flags);
+int csa_rope_run(const csa_rope_plan *plan, const void *q, const long long *q_strides, void *q_out,
+                 const long long *q_out_strides, const void *k, const long long *k_strides,
+                 void *k_out, const long long *k_out_strides, const int *positions,
+                 const long long *pos_strides, int B, int Hq, int Hkv, int T, int d, bool inverse,
+                 bool bf16, cudaStream_t stream);
+int csa_cache_append_run(const csa_rope_plan *plan, const void *q, const long long *q_strides,
+                         void *q_out, const long long *q_out_strides, const void *k,
+                         const long long *k_strides, const void *v, const long long *v_strides,
+                         void *k_pages, void *v_pages, const int *block_table, const int *seqlens,
+                         const int *counts, const int *positions, const long long *pos_strides,
+                         int B, int Hq, int Hkv, int T, int d, int P, int S, int M, bool bf16,
+                         cudaStream_t stream);
+int csa_rope_take_status(void);
+
+// Pages: who holds them, and their movement (csa_cache.cu).
+long long csa_cache_scratch_bytes(int B, int P, int n);
+int csa_cache_reserve_run(int *refs, int *table, int *seqlens, const int *counts, int *shortfall,
+                          void *scratch, int B, int P, int S, int M, cudaStream_t stream);
+int csa_cache_free_run(int *refs, int *table, int *seqlens, const int *rows, int R, int B, int P,
+                       int S, int M, cudaStream_t stream);
+int csa_cache_fork_run(int *refs, int *table, int *seqlens, const int *parents, const int *children,
+                       int n, int *src, int *dst, int *shortfall, void *scratch, int B, int P,
+                       int S, int M, cudaStream_t stream);
+int csa_cache_compact_run(int *refs, int *table, const int *seqlens, int *src, int *dst, int *moved,
+                          void *scratch, int B, int P, int S, int M, cudaStream_t stream);
+int csa_cache_copy_pages_run(void *k_pages, void *v_pages, long long page_bytes, int layers, int P,
+                             const int *src, const int *dst, int n, const int *count,
+                             cudaStream_t stream);
+int csa_cache_take_status(void);

@@ -1,0 +1,355 @@
+// Rotary positions with several axes, on queries and keys of any strides, and
+// the rows of new tokens written into the pages of a cache.
+//
+// The first 2n columns of a row are n pairs; pair i of a token at position
+// p = positions[axis(i)] turns by the angle p * base^(-i/n):
+//     (u, w) -> (u cos - w sin, u sin + w cos),
+// and the backward pass is the same turn by the negative angle (a rotation's
+// transpose).  Pairs are (i, i + n), or (2i, 2i + 1) when adjacent.
+//
+// Angles.  Far positions lose an angle formed in fp32 (at 2^20 radians a step
+// of fp32 is 1/16), so the angle is formed in turns, in integers: the plan
+// holds base^(-i/n) / 2 pi as a 64-bit fraction F of a turn, and p * F modulo
+// 2^64 is the angle's fraction of a turn, exact up to p * 2^-65.  Its top 32
+// bits, as a signed number, go to sincospif.
+//
+// What bounds it.  Each element is read once and written once: HBM bandwidth.
+// A thread owns 16 bytes twice (the two members of 8 bf16 or 4 fp32 pairs) of
+// one token and walks over a range of heads, so that the sines and cosines of
+// a token are formed once for all of those heads.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "csa.h"
+#include "csa_internal.h"
+
+namespace {
+
+constexpr int kThreads = 256;
+
+__device__ int g_rope_status;  // sticky status word of this file's kernels
+
+struct RopeTensor {
+    const void *in;
+    void *out;
+    long long ib, ih, it;  // strides of in over batch, head, time, in elements
+    long long ob, oh, ot;
+    int H;
+};
+
+struct RopeParams {
+    csa_rope_plan plan;
+    RopeTensor x[3];  // queries, keys, values
+    const int *positions;
+    long long pa, pb, pt;  // strides over axes, batch, time
+    int B, T, d;
+    float sign;
+    int heads, heads_per_block;
+    // pages of keys (x[1]) and values (x[2]); null: every tensor goes to its out
+    void *k_pages, *v_pages;
+    const int *table, *seqlens, *counts;
+    int P, S, M;
+};
+
+template <int BYTES>
+struct Chunk;
+template <>
+struct Chunk<16> {
+    using type = uint4;
+};
+template <>
+struct Chunk<4> {
+    using type = uint32_t;
+};
+template <>
+struct Chunk<2> {
+    using type = uint16_t;
+};
+
+template <typename T>
+__device__ __forceinline__ float widen(T v);
+template <>
+__device__ __forceinline__ float widen<float>(float v) {
+    return v;
+}
+template <>
+__device__ __forceinline__ float widen<__nv_bfloat16>(__nv_bfloat16 v) {
+    return __bfloat162float(v);
+}
+template <typename T>
+__device__ __forceinline__ T narrow(float v);
+template <>
+__device__ __forceinline__ float narrow<float>(float v) {
+    return v;
+}
+template <>
+__device__ __forceinline__ __nv_bfloat16 narrow<__nv_bfloat16>(float v) {
+    return __float2bfloat16_rn(v);
+}
+
+// One block: a range of tokens (rows of B x T) and a range of heads of the
+// tensors taken one after the other.  V elements of type T per chunk; a
+// thread's unit of a row is two chunks, at columns c0 and c1.  Units [0, n/V)
+// are rotated, the ones behind copy the columns from 2n on.
+template <typename T, int V, bool ADJ, bool PAGED>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+    using C = typename Chunk<V * sizeof(T)>::type;
+    __shared__ unsigned long long turn[CSA_ROPE_MAX_PAIRS];
+    __shared__ unsigned char axis[CSA_ROPE_MAX_PAIRS];
+    const int n = p.plan.pairs;
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        turn[i] = p.plan.turn[i];
+        axis[i] = p.plan.axis[i];
+    }
+    __syncthreads();
+    const int rest = (p.d - 2 * n) / V;  // chunks that are not rotated
+    const int units = n / V + (rest + 1) / 2, rows = kThreads / units;
+    const int r = threadIdx.x / units, u = threadIdx.x - r * units;
+    const unsigned token = blockIdx.x * rows + r;  // B * T fits 31 bits
+    if (r >= rows || token >= (unsigned)p.B * p.T) return;
+    const int b = token / (unsigned)p.T, t = token - (unsigned)b * p.T;
+    const bool turned = u < n / V;
+    int c0, c1;
+    bool two = true;
+    if (turned) {
+        c0 = ADJ ? 2 * V * u : V * u;
+        c1 = ADJ ? c0 + V : c0 + n;
+    } else {
+        c0 = 2 * n + 2 * V * (u - n / V);
+        c1 = c0 + V;
+        two = c1 < p.d;
+    }
+    long long page_row = -1;  // ((page * H) * S + place) of this token; + h * S for head h
+    int cache_row = 0;
+    if (PAGED) {
+        const int len = p.seqlens[b], count = p.counts ? p.counts[b] : p.T;
+        cache_row = len - count + t;
+        const bool sound = count >= 0 && count <= p.T && len >= count && len <= (long long)p.M * p.S;
+        if (sound && t < count) {
+            const int page = p.table[(long long)b * p.M + cache_row / p.S];
+            if (page >= 0 && page < p.P)
+                page_row = (long long)page * p.x[1].H * p.S + cache_row % p.S;
+            else if (u == 0)
+                atomicCAS(&g_rope_status, 0, CSA_ERR_INVALID_ARG);
+        } else if (!sound && t == 0 && u == 0) {
+            atomicCAS(&g_rope_status, 0, CSA_ERR_INVALID_ARG);
+        }
+    }
+    const int g0 = blockIdx.y * p.heads_per_block, g1 = min(g0 + p.heads_per_block, p.heads);
+    float cs[V], sn[V];
+    if (turned && g0 < p.x[0].H + p.x[1].H) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int i = V * u + j;
+            const int pos = PAGED && !p.positions
+                                ? cache_row
+                                : p.positions[axis[i] * p.pa + b * p.pb + t * p.pt];
+            const unsigned long long f = (unsigned long long)(long long)pos * turn[i];
+            const float half_turns = (float)(int)(f >> 32) * 4.656612873077393e-10f;  // 2^-31
+            sincospif(half_turns, &sn[j], &cs[j]);
+            sn[j] *= p.sign;
+        }
+    }
+#pragma unroll 4
+    for (int g = g0; g < g1; ++g) {
+        const int which = g < p.x[0].H ? 0 : g < p.x[0].H + p.x[1].H ? 1 : 2;
+        const RopeTensor &x = p.x[which];
+        const int h = g - (which > 0 ? p.x[0].H : 0) - (which > 1 ? p.x[1].H : 0);
+        const T *in = static_cast<const T *>(x.in) + b * x.ib + h * x.ih + t * x.it;
+        T *out;
+        if (PAGED && which > 0) {
+            if (page_row < 0) continue;
+            out = static_cast<T *>(which == 1 ? p.k_pages : p.v_pages) +
+                  (page_row + (long long)h * p.S) * p.d;
+        } else {
+            out = static_cast<T *>(x.out) + b * x.ob + h * x.oh + t * x.ot;
+        }
+        union {
+            C raw;
+            T e[V];
+        } a, c;
+        a.raw = *reinterpret_cast<const C *>(in + c0);
+        if (two) c.raw = *reinterpret_cast<const C *>(in + c1);
+        if (turned && which < 2) {
+            if (ADJ) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) {  // pair j: elements 2j, 2j + 1 of the two chunks
+                    T &eu = 2 * j < V ? a.e[(2 * j) % V] : c.e[(2 * j) % V];
+                    T &ew = 2 * j + 1 < V ? a.e[(2 * j + 1) % V] : c.e[(2 * j + 1) % V];
+                    const float xu = widen(eu), xw = widen(ew);
+                    eu = narrow<T>(xu * cs[j] - xw * sn[j]);
+                    ew = narrow<T>(xu * sn[j] + xw * cs[j]);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const float xu = widen(a.e[j]), xw = widen(c.e[j]);
+                    a.e[j] = narrow<T>(xu * cs[j] - xw * sn[j]);
+                    c.e[j] = narrow<T>(xu * sn[j] + xw * cs[j]);
+                }
+            }
+        }
+        *reinterpret_cast<C *>(out + c0) = a.raw;
+        if (two) *reinterpret_cast<C *>(out + c1) = c.raw;
+    }
+}
+
+template <typename T, int V>
+int launch(RopeParams &p, cudaStream_t stream) {
+    const int n = p.plan.pairs, rest = (p.d - 2 * n) / V;
+    const int units = n / V + (rest + 1) / 2, rows = kThreads / units;
+    const long long tokens = (long long)p.B * p.T, bx = (tokens + rows - 1) / rows;
+    p.heads_per_block = 8;
+    while (p.heads_per_block > 1 &&
+           bx * ((p.heads + p.heads_per_block - 1) / p.heads_per_block) < 4 * 152)
+        p.heads_per_block /= 2;
+    const int by = (p.heads + p.heads_per_block - 1) / p.heads_per_block;
+    const dim3 grid((unsigned)bx, (unsigned)by);
+    const bool adj = p.plan.adjacent != 0;
+    if (p.k_pages) {
+        if (adj)
+            rope_kernel<T, V, true, true><<<grid, kThreads, 0, stream>>>(p);
+        else
+            rope_kernel<T, V, false, true><<<grid, kThreads, 0, stream>>>(p);
+    } else {
+        if (adj)
+            rope_kernel<T, V, true, false><<<grid, kThreads, 0, stream>>>(p);
+        else
+            rope_kernel<T, V, false, false><<<grid, kThreads, 0, stream>>>(p);
+    }
+    return cudaGetLastError() == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
+}
+
+bool on16(const void *q) { return reinterpret_cast<uintptr_t>(q) % 16 == 0; }
+
+// Whether rows of x can be moved in 16-byte chunks of V elements.
+bool wide(const RopeTensor &x, int V, bool has_out) {
+    if (x.H == 0) return true;
+    return on16(x.in) && x.ib % V == 0 && x.ih % V == 0 && x.it % V == 0 &&
+           (!has_out || (on16(x.out) && x.ob % V == 0 && x.oh % V == 0 && x.ot % V == 0));
+}
+
+template <typename T>
+int run(RopeParams &p, cudaStream_t stream) {
+    constexpr int V = 16 / (int)sizeof(T);
+    const bool paged = p.k_pages != nullptr;
+    const bool ok = p.d % V == 0 && p.plan.pairs % V == 0 && wide(p.x[0], V, true) &&
+                    wide(p.x[1], V, !paged) && wide(p.x[2], V, !paged) &&
+                    (!paged || (on16(p.k_pages) && on16(p.v_pages)));
+    return ok ? launch<T, V>(p, stream) : launch<T, 1>(p, stream);
+}
+
+RopeTensor tensor(const void *in, const long long *is, void *out, const long long *os, int H, int T,
+                  int d) {
+    RopeTensor x;
+    x.in = in;
+    x.out = out;
+    x.H = H;
+    x.ib = is ? is[0] : (long long)H * T * d;
+    x.ih = is ? is[1] : (long long)T * d;
+    x.it = is ? is[2] : d;
+    x.ob = os ? os[0] : (long long)H * T * d;
+    x.oh = os ? os[1] : (long long)T * d;
+    x.ot = os ? os[2] : d;
+    return x;
+}
+
+}  // namespace
+
+int csa_rope_plan_make(csa_rope_plan *plan, const int *sections, int axes, double base, int flags) {
+    int left[CSA_ROPE_MAX_AXES], total = 0, most = 0;
+    for (int a = 0; a < axes; ++a) {
+        left[a] = sections[a];
+        if (left[a] < 0 || left[a] > CSA_ROPE_MAX_PAIRS) return CSA_ERR_INVALID_ARG;
+        total += left[a];
+        if (left[a] > most) most = left[a];
+    }
+    if (total < 1) return CSA_ERR_INVALID_ARG;
+    if (total > CSA_ROPE_MAX_PAIRS) return CSA_ERR_UNSUPPORTED;
+    *plan = csa_rope_plan{};
+    plan->pairs = total;
+    plan->axes = axes;
+    plan->adjacent = (flags & CSA_ROPE_ADJACENT) ? 1 : 0;
+    int i = 0;
+    if (flags & CSA_ROPE_DEALT) {
+        for (int turn = 0; turn < most; ++turn)
+            for (int a = 0; a < axes; ++a)
+                if (turn < left[a]) plan->axis[i++] = (unsigned char)a;
+    } else {
+        for (int a = 0; a < axes; ++a)
+            for (int j = 0; j < left[a]; ++j) plan->axis[i++] = (unsigned char)a;
+    }
+    const long double two_pi = 6.283185307179586476925286766559L;
+    for (i = 0; i < total; ++i) {
+        // the frequency in turns per position, as a fraction of a turn times 2^64
+        const long double f = powl((long double)base, -(long double)i / total) / two_pi;
+        const long double frac = f - floorl(f);
+        plan->turn[i] = (unsigned long long)(ldexpl(frac, 63) + 0.25L) * 2ull;
+    }
+    return CSA_OK;
+}
+
+int csa_rope_run(const csa_rope_plan *plan, const void *q, const long long *q_strides, void *q_out,
+                 const long long *q_out_strides, const void *k, const long long *k_strides,
+                 void *k_out, const long long *k_out_strides, const int *positions,
+                 const long long *pos_strides, int B, int Hq, int Hkv, int T, int d, bool inverse,
+                 bool bf16, cudaStream_t stream) {
+    RopeParams p = {};
+    p.plan = *plan;
+    p.x[0] = tensor(q, q_strides, q_out, q_out_strides, Hq, T, d);
+    p.x[1] = tensor(k, k_strides, k_out, k_out_strides, Hkv, T, d);
+    p.x[2] = tensor(nullptr, nullptr, nullptr, nullptr, 0, T, d);
+    p.positions = positions;
+    p.pa = pos_strides ? pos_strides[0] : (long long)B * T;
+    p.pb = pos_strides ? pos_strides[1] : T;
+    p.pt = pos_strides ? pos_strides[2] : 1;
+    p.B = B;
+    p.T = T;
+    p.d = d;
+    p.sign = inverse ? -1.0f : 1.0f;
+    p.heads = Hq + Hkv;
+    return bf16 ? run<__nv_bfloat16>(p, stream) : run<float>(p, stream);
+}
+
+int csa_cache_append_run(const csa_rope_plan *plan, const void *q, const long long *q_strides,
+                         void *q_out, const long long *q_out_strides, const void *k,
+                         const long long *k_strides, const void *v, const long long *v_strides,
+                         void *k_pages, void *v_pages, const int *block_table, const int *seqlens,
+                         const int *counts, const int *positions, const long long *pos_strides,
+                         int B, int Hq, int Hkv, int T, int d, int P, int S, int M, bool bf16,
+                         cudaStream_t stream) {
+    RopeParams p = {};
+    if (plan) p.plan = *plan;  // no plan: no pair turns, every column is copied
+    p.x[0] = tensor(q, q_strides, q_out, q_out_strides, Hq, T, d);
+    p.x[1] = tensor(k, k_strides, nullptr, nullptr, Hkv, T, d);
+    p.x[2] = tensor(v, v_strides, nullptr, nullptr, Hkv, T, d);
+    p.positions = positions;
+    p.pa = pos_strides ? pos_strides[0] : (long long)B * T;
+    p.pb = pos_strides ? pos_strides[1] : T;
+    p.pt = pos_strides ? pos_strides[2] : 1;
+    p.B = B;
+    p.T = T;
+    p.d = d;
+    p.sign = 1.0f;
+    p.heads = Hq + 2 * Hkv;
+    p.k_pages = k_pages;
+    p.v_pages = v_pages;
+    p.table = block_table;
+    p.seqlens = seqlens;
+    p.counts = counts;
+    p.P = P;
+    p.S = S;
+    p.M = M;
+    return bf16 ? run<__nv_bfloat16>(p, stream) : run<float>(p, stream);
+}
+
+int csa_rope_take_status(void) {
+    int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_rope_status, sizeof(int)) != cudaSuccess) return CSA_ERR_CUDA;
+    const int zero = 0;
+    if (cudaMemcpyToSymbol(g_rope_status, &zero, sizeof(int)) != cudaSuccess) return CSA_ERR_CUDA;
+    return v;
+}

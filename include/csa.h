@@ -417,6 +417,222 @@ int csa_decode_merge_ranges(const float *o_parts, const float *lse_parts, int R,
                             int d, void *out, float *lse, csa_stream_t stream);
 
 /*
+ * Paged key-value caches
+ * ----------------------
+ *  Pools      k_pages, v_pages: contiguous [P, Hkv, S, d], P pages of S rows
+ *             for each of Hkv cached heads.
+ *  Tables     block_table: contiguous int32 [B, M]; row b holds the page
+ *             numbers of sequence b in order, its token i being row i mod S
+ *             of page block_table[b][i / S].  seqlens: int32 [B], tokens held.
+ *             Entries behind a sequence's ceil(n / S) pages are not read.
+ *  Holders    page_refs: int32 [P], how many sequences hold a page; 0 is
+ *             free.  A partly filled page is held by one sequence only: the
+ *             calls below keep it so.
+ *  All of these are DEVICE memory and are read and written on `stream` only,
+ *  so a step of a server (free, reserve, append, decode) can be captured into
+ *  a graph.  Values on the device that the host cannot see (lengths, page
+ *  numbers, rows) are checked on the device: what each call does with bad
+ *  ones is said there, no access goes out of bounds, and the sticky status
+ *  word (csa_device_status) records CSA_ERR_INVALID_ARG.
+ *  S, M >= 1; B * M and M * S at most 2^31 - 1 (CSA_ERR_UNSUPPORTED).  The
+ *  pages of the method have no counterpart to any of these entry points but
+ *  csa_decode_paged.
+ */
+
+/*
+ * csa_decode_paged - csa_decode over a paged cache, with grouped heads: query
+ *   head h reads cached head h / (Hq / Hkv).
+ *   Defines: eq. (10)/(11) of "Continuous Softmax Attention" ("Assembly and
+ *   Simplification") for the single row t = n_b, as csa_decode.
+ *   q: bf16 [B, Hq, d]; k_pages, v_pages: bf16 [P, Hkv, S, d]; k0, v0: bf16
+ *   [Hkv, d], read in CSA_K0_GIVEN mode only (CSA_K0_COPY_FIRST: token 0 of
+ *   the cache); out: bf16 [B, Hq, d]; lse: float [B, Hq] or NULL.
+ *   seqlens: int32 [B], the tokens held, the newest one among them.  n_b = 0
+ *   is an empty place in the batch: out = 0 and lse = -inf.  A length outside
+ *   [0, M * S], or a page number outside [0, P) among the ones held, makes
+ *   that sequence's out and lse NaN and sets the status word; other
+ *   sequences are not affected.
+ *   workspace: DEVICE scratch of at least csa_decode_paged_workspace_bytes(B,
+ *   Hq, Hkv, d) bytes, 16-byte aligned, contents on entry irrelevant; calls
+ *   that can run at the same time need distinct workspaces.
+ *   d must be 64, 128 or 256 and S a multiple of 8 (CSA_ERR_UNSUPPORTED
+ *   otherwise, as for P * Hkv * S > 2^31 - 1); Hq a multiple of Hkv
+ *   (CSA_ERR_INVALID_ARG).  q, pools, out, workspace (and k0, v0 in GIVEN
+ *   mode) 16-byte aligned, the rest 4-byte.  B * Hq == 0: CSA_OK, nothing
+ *   launched.  The result does not depend on scheduling: equal inputs give
+ *   equal bits.
+ */
+int csa_decode_paged(const void *q, const void *k_pages, const void *v_pages, const void *k0,
+                     const void *v0, const int *block_table, const int *seqlens, void *out,
+                     float *lse, void *workspace, long long workspace_bytes, int B, int Hq,
+                     int Hkv, int P, int S, int M, int d, float scale, int k0_mode,
+                     csa_stream_t stream);
+
+/* csa_decode_paged_workspace_bytes - workspace bytes csa_decode_paged needs
+ * (host only), or -1 for a negative size, Hkv that does not divide Hq, or d
+ * outside {64, 128, 256}. */
+long long csa_decode_paged_workspace_bytes(int B, int Hq, int Hkv, int d);
+
+/*
+ * csa_rope_plan - which pairs of a row turn, by which axis of the positions
+ *   and how far per position; filled by csa_rope_plan_init and passed by
+ *   value into the kernels (HOST memory, not kept).
+ */
+#define CSA_ROPE_MAX_PAIRS 128
+#define CSA_ROPE_MAX_AXES 8
+#define CSA_ROPE_ADJACENT 1 /* pairs (2i, 2i + 1) instead of (i, i + n)        */
+#define CSA_ROPE_DEALT 2    /* pairs dealt to the axes in turn, an axis that
+                               has its number of pairs being passed over,
+                               instead of section after section                */
+typedef struct {
+    int pairs, axes, adjacent;
+    unsigned char axis[CSA_ROPE_MAX_PAIRS];      /* the axis of each pair      */
+    unsigned long long turn[CSA_ROPE_MAX_PAIRS]; /* turns per position, * 2^64 */
+} csa_rope_plan;
+
+/*
+ * csa_rope_plan_init - plan for rotary positions with `axes` axes (1 to 8),
+ *   sections[a] pairs turning by axis a (n pairs in all, 1 <= n <= 128); pair i
+ *   turns by positions[axis(i)] * base^(-i / n).  base finite and > 0; flags:
+ *   CSA_ROPE_ADJACENT, CSA_ROPE_DEALT.  Host only.
+ *   CSA_ERR_INVALID_ARG, or CSA_ERR_UNSUPPORTED for more than 128 pairs.
+ */
+int csa_rope_plan_init(csa_rope_plan *plan, const int *sections, int axes, double base, int flags);
+
+/*
+ * csa_rope - turns the first 2n columns of every row of q and k by the plan,
+ *   the other columns copied: (u, w) -> (u cos - w sin, u sin + w cos) per
+ *   pair, by the negative angle if `inverse` (the backward pass: the gradient
+ *   of the input from the gradient of the output).  fp32 arithmetic, one
+ *   rounding; angles exact to fp32 for every int32 position.
+ *   q, q_out: bf16 [B, Hq, T, d]; k, k_out: bf16 [B, Hkv, T, d], not read
+ *   where the head count is 0.  *_strides: HOST long long[3], the strides over
+ *   batch, head and time in elements (the last dimension is contiguous); NULL
+ *   for contiguous tensors.  An output may be its input with the same strides;
+ *   otherwise outputs overlap neither inputs nor themselves.
+ *   positions: DEVICE int32, strides pos_strides (HOST long long[3]) over axis,
+ *   batch and time, NULL for contiguous [axes, B, T]; stride 0 broadcasts.
+ *   1 <= d <= 256 and 2n <= d; B * T at most 2^31 - 1.  2-byte aligned; the
+ *   fast path wants 16-byte alignment of every row and d and n multiples of 8.
+ */
+int csa_rope(const csa_rope_plan *plan, const void *q, const long long *q_strides, void *q_out,
+             const long long *q_out_strides, const void *k, const long long *k_strides,
+             void *k_out, const long long *k_out_strides, const int *positions,
+             const long long *pos_strides, int B, int Hq, int Hkv, int T, int d, int inverse,
+             csa_stream_t stream);
+
+/* csa_rope_f32 - the same on fp32 tensors (4-byte aligned; fast path: d and n
+ * multiples of 4). */
+int csa_rope_f32(const csa_rope_plan *plan, const float *q, const long long *q_strides,
+                 float *q_out, const long long *q_out_strides, const float *k,
+                 const long long *k_strides, float *k_out, const long long *k_out_strides,
+                 const int *positions, const long long *pos_strides, int B, int Hq, int Hkv, int T,
+                 int d, int inverse, csa_stream_t stream);
+
+/*
+ * csa_cache_append - writes the rows of new tokens into their pages: row t of
+ *   k and v (t < counts[b]) becomes token seqlens[b] - counts[b] + t of
+ *   sequence b, so seqlens already counts the new tokens (csa_cache_reserve
+ *   sets it).  With a plan the keys are turned on the way, and q, if given, is
+ *   turned into q_out by the same positions (all T rows).
+ *   k, v: bf16 [B, Hkv, T, d]; q, q_out: bf16 [B, Hq, T, d] or Hq = 0; strides
+ *   as csa_rope.  counts: int32 [B], or NULL for T each.  positions, strides as
+ *   csa_rope, or NULL: a token's place in the cache, on every axis.  plan NULL:
+ *   nothing turns (then Hq must be 0).  Pages may have any S >= 1.
+ *   A sequence whose count is outside [0, T] or whose length is outside
+ *   [count, M * S], and a row whose page number is outside [0, P), is not
+ *   written and sets the status word.
+ */
+int csa_cache_append(const csa_rope_plan *plan, const void *q, const long long *q_strides,
+                     void *q_out, const long long *q_out_strides, const void *k,
+                     const long long *k_strides, const void *v, const long long *v_strides,
+                     void *k_pages, void *v_pages, const int *block_table, const int *seqlens,
+                     const int *counts, const int *positions, const long long *pos_strides, int B,
+                     int Hq, int Hkv, int T, int d, int P, int S, int M, csa_stream_t stream);
+
+/* csa_cache_append_f32 - the same on fp32 tensors and pools. */
+int csa_cache_append_f32(const csa_rope_plan *plan, const float *q, const long long *q_strides,
+                         float *q_out, const long long *q_out_strides, const float *k,
+                         const long long *k_strides, const float *v, const long long *v_strides,
+                         float *k_pages, float *v_pages, const int *block_table,
+                         const int *seqlens, const int *counts, const int *positions,
+                         const long long *pos_strides, int B, int Hq, int Hkv, int T, int d, int P,
+                         int S, int M, csa_stream_t stream);
+
+/*
+ * csa_cache_reserve - room for counts[b] >= 0 more tokens of every sequence:
+ *   the pages that are missing are the lowest-numbered free ones, given out in
+ *   the order of the sequences; their refs become 1, the table gets them, and
+ *   seqlens[b] += counts[b].
+ *   shortfall: DEVICE int32 [1]: 0 if it was done; the number of pages missing
+ *   if the pool has too few, or -1 for a negative count or length or one that
+ *   does not fit a row of the table (which also sets the status word).  Where
+ *   it is not 0, nothing has changed.
+ *   workspace: csa_cache_workspace_bytes(B, P, 0) bytes, 4-byte aligned.
+ */
+int csa_cache_reserve(int *page_refs, int *block_table, int *seqlens, const int *counts,
+                      int *shortfall, void *workspace, long long workspace_bytes, int B, int P,
+                      int S, int M, csa_stream_t stream);
+
+/*
+ * csa_cache_free - the listed sequences give their pages back: their refs fall
+ *   by one each, the entries become -1 and the lengths 0.  rows: int32 [R];
+ *   -1 is padding, a row listed twice is freed once.  A row outside [-1, B),
+ *   or with a length outside [0, M * S], sets the status word and nothing
+ *   changes; a page number outside [0, P), or of a page that nobody holds, is
+ *   passed over and sets the status word.
+ */
+int csa_cache_free(int *page_refs, int *block_table, int *seqlens, const int *rows, int R, int B,
+                   int P, int S, int M, csa_stream_t stream);
+
+/*
+ * csa_cache_fork - children[i] becomes a copy of parents[i]: full pages are
+ *   shared (refs + 1), a partly filled last page gets a page of its own, the
+ *   lowest-numbered free ones in the order of the pairs.  src[i], dst[i] are
+ *   the pages to copy then (csa_cache_copy_pages, once per pool), or -1, -1.
+ *   parents, children: int32 [n]; a pair with a negative entry is padding.
+ *   A parent may have several children; a child must be empty (length 0) and
+ *   listed once.  The child's row of the table is -1 behind its pages.
+ *   shortfall as csa_cache_reserve (-1: a row out of range, a bad length or
+ *   page, a child that is not empty or listed twice); where it is not 0,
+ *   nothing has changed and src, dst are -1.
+ *   workspace: csa_cache_workspace_bytes(B, P, n) bytes, 4-byte aligned.
+ */
+int csa_cache_fork(int *page_refs, int *block_table, int *seqlens, const int *parents,
+                   const int *children, int n, int *src, int *dst, int *shortfall,
+                   void *workspace, long long workspace_bytes, int B, int P, int S, int M,
+                   csa_stream_t stream);
+
+/*
+ * csa_cache_compact - moves the held pages together: with U pages held, those
+ *   numbered U or more take the free numbers below U, both in ascending order.
+ *   src, dst: int32 [P / 2], the moves, then -1; moved: int32 [1], how many.
+ *   page_refs and the held entries of the table are already renamed; the
+ *   caller moves the data (csa_cache_copy_pages with count = moved, once per
+ *   pool) before anything reads the pools.  workspace:
+ *   csa_cache_workspace_bytes(B, P, 0) bytes, 4-byte aligned.
+ */
+int csa_cache_compact(int *page_refs, int *block_table, const int *seqlens, int *src, int *dst,
+                      int *moved, void *workspace, long long workspace_bytes, int B, int P, int S,
+                      int M, csa_stream_t stream);
+
+/* csa_cache_workspace_bytes - workspace bytes csa_cache_reserve, _fork and
+ * _compact need (host only), or -1 for a negative size. */
+long long csa_cache_workspace_bytes(int B, int P, int n);
+
+/*
+ * csa_cache_copy_pages - copies page src[i] onto page dst[i] for i < min(n,
+ *   *count) (count: DEVICE int32 [1], or NULL for n), in k_pages and, unless
+ *   it is NULL, v_pages: pools of `layers` times P pages of page_bytes bytes.
+ *   A pair with a negative entry is padding; one with a number >= P is passed
+ *   over and sets the status word.  Pairs are copied in no particular order:
+ *   a page that is a dst must not be the src or dst of another pair.
+ */
+int csa_cache_copy_pages(void *k_pages, void *v_pages, long long page_bytes, int layers, int P,
+                         const int *src, const int *dst, int n, const int *count,
+                         csa_stream_t stream);
+
+/*
  * csa_logphi2_eval - y[i] = log phi2(x[i]) with the library's fp32 device
  *   function (phi2 of eq. (6), "Preliminaries").  x, y: device float arrays
  *   of n elements (n >= 0).  A test hook for the numerics of b.
@@ -440,8 +656,9 @@ int csa_segment_weights_eval(const float *u0, const float *u1, float *right, flo
  *   words of the current device: CSA_OK; CSA_ERR_TIMEOUT if a kernel's
  *   bounded wait expired since the last read (that kernel then skipped the
  *   rest of its work and its outputs are undefined); CSA_ERR_INVALID_ARG if
- *   csa_decode met a sequence length outside [1, T].  Synchronises the
- *   device.  Returns CSA_ERR_CUDA if the read itself fails.
+ *   csa_decode met a sequence length outside [1, T], or one of the paged
+ *   cache's calls a length, row or page number out of range.  Synchronises
+ *   the device.  Returns CSA_ERR_CUDA if the read itself fails.
  */
 int csa_device_status(void);
 
