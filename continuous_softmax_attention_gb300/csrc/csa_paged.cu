@@ -6,7 +6,31 @@
 // Between neighbouring logits a and a' = a + x the interval gives the key at a
 // the weight e^{a-m} phi2(x) and the key at a' the weight e^{a'-m} phi2(-x)
 // (eq. (9)); with p = e^{a-m} and p' = e^{a'-m} these are ((p'-p)/x - p)/x and
-// (p' - (p'-p)/x)/x.
+// (p' - (p'-p)/x)/x.  A key's weight is the sum over its two intervals, so a
+// row's weight is complete once the next row's logit is known.
+//
+// What bounds it: the cached rows are read once, HBM bandwidth.  What follows
+// from that:
+//  - A warp is a worker of its own.  It has a ring of tiles in shared memory
+//    that it fills itself by TMA (its lane 0), runs over a contiguous range of
+//    tiles and never waits for another warp, so some warp's copies are always
+//    in flight: 8 warps x 24 KiB per SM.
+//  - The tiles of all (sequence, cached head, block of query heads) in a row
+//    are cut into equal ranges, one per worker, whatever the lengths.  The
+//    lengths are on the device, so every block forms the cut itself.
+//  - The query heads of a group are the rows of the matrix instruction (16, of
+//    which 8 are used for up to 8 heads), the cached rows its columns, so one
+//    read of a cached row serves all heads of the group.  mma.sync rather than
+//    tcgen05: with 16 rows at most the products take a few percent of the time
+//    either way, and mma.sync leaves logits and sums in the registers of the
+//    warp that needs them.
+//  - The weights enter the second product as a sum of two bf16 numbers (16
+//    bits of the weight).  For up to 8 heads both halves fit one instruction:
+//    rows 0..7 hold the high parts and rows 8..15 the low ones.
+//  - A part of a sequence leaves its unnormalised sums, maximum and weight sum
+//    in the workspace; a second kernel, launched early, joins the parts in
+//    order.  A sequence that one worker had whole is written at once.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -16,6 +40,7 @@
 #include "csa.h"
 #include "csa_device.cuh"
 #include "csa_internal.h"
+#include "csa_tc_common.cuh"
 
 namespace {
 
@@ -23,25 +48,48 @@ using namespace csa_dev;
 
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
+constexpr int kGrid = 152;        // one block per SM
+constexpr int kStages = 3;        // tiles in a worker's ring
+constexpr int kMaxThreads = 256;
+constexpr int kMinRows = 64;      // rows per worker that a split leaves, at least
+constexpr float kRaise = 16.0f;   // log2 units a logit may pass the running maximum by
 
 __device__ int g_paged_status;  // sticky status word of this file's kernels
+
+template <int D>
+struct Cfg {
+    static constexpr int KT = D == 64 ? 32 : 16;       // rows per tile: 8 KiB (16 at d = 256)
+    static constexpr int Warps = D == 256 ? 4 : 8;     // workers per block
+    static constexpr int Tile = KT * D * 2;            // bytes of a tile of keys, or of values
+    static constexpr int Stage = 2 * Tile;
+    static constexpr int Smem = Warps * kStages * Stage + 1024;  // + alignment
+    static constexpr int Workers = Warps * kGrid;
+    static_assert(Smem <= 227 * 1024 - 4096, "one block per SM");
+};
 
 struct PagedParams {
     const __nv_bfloat16 *q, *k, *v, *k0, *v0;
     const int *table, *seqlens;
     __nv_bfloat16 *out;
     float *lse;
-    int B, Hq, Hkv, P, S, M, d;
-    float qscale;  // scale * log2(e): logits come out in log2 units
+    float *part_o;    // [2 * workers][HB][D]: unnormalised sums of a part
+    float *part_ml;   // [2 * workers][HB][2]: its maximum (log2 units) and weight sum
+    long long *cut;   // [kMaxThreads + 2]: tiles before each chunk of sequences, all, workers in use
+    int B, Hq, Hkv, P, S, M;
+    int G, GB, HB;    // query heads of a group, blocks of them, heads per block
+    int R;            // rows per copy: divides S and the tile
+    float qscale;     // scale * log2(e): logits come out in log2 units
     int mode;
 };
 
-// The weights that the interval between logits a and a1 (log2 units, both at
-// most about m) gives its two keys.  |x| < 1 (natural units): the power series
-// sum x^j/(j+2)!, j = 0..9, truncated below 3e-9 relative, split into its even
-// and odd terms, which the two keys share.
-__device__ __forceinline__ void interval(float a, float a1, float m, float &left, float &right) {
-    const float x = (a1 - a) * kLn2, p = ex2_approx(a - m), p1 = ex2_approx(a1 - m), y = x * x;
+// The weights that the interval between logits a and a1 (log2 units) gives its
+// two keys, with p = 2^{a-m}, p1 = 2^{a1-m}.  |x| < 1 (natural units): the
+// power series sum x^j/(j+2)!, j = 0..9, truncated below 3e-9 relative, split
+// into its even and odd terms, which the two keys share.
+__device__ __forceinline__ void interval(float a, float a1, float p, float p1, float &left,
+                                         float &right) {
+    const float x = (a1 - a) * kLn2, y = x * x;
     float even = 2.755731922398589e-07f;             // 1/10!
     even = fmaf(even, y, 2.48015873015873e-05f);     // 1/8!
     even = fmaf(even, y, 1.388888888888889e-03f);    // 1/6!
@@ -58,98 +106,722 @@ __device__ __forceinline__ void interval(float a, float a1, float m, float &left
     right = near ? p1 * fmaf(-odd, x, even) : (p1 - s) * r;
 }
 
-constexpr int kThreads = 128;
-
-// One block per (sequence, query head), the whole sequence in tiles of
-// kThreads - 1 rows: a thread forms one row's logit (the last one the logit of
-// the row behind the tile), then one weight, then sums columns.
-__global__ void __launch_bounds__(kThreads) paged_kernel(const PagedParams p) {
-    __shared__ float qs[256], a[kThreads + 1], w[kThreads], red[8];
-    __shared__ int pg[kThreads];
-    const int b = blockIdx.x / p.Hq, hq = blockIdx.x - b * p.Hq, tid = threadIdx.x;
-    const int hk = hq / (p.Hq / p.Hkv), n = p.seqlens[b], d = p.d;
-    __nv_bfloat16 *out = p.out + (long long)blockIdx.x * d;
-    bool bad = n < 0 || n > (long long)p.M * p.S;
-    const int held = bad ? 0 : (int)(((long long)n + p.S - 1) / p.S);
-    for (int j = tid; j < held; j += kThreads) {
-        const int page = p.table[(long long)b * p.M + j];
-        bad |= page < 0 || page >= p.P;
-    }
-    bad = __syncthreads_or(bad);
-    if (bad || n == 0) {
-        for (int c = tid; c < d; c += kThreads) out[c] = __float2bfloat16_rn(bad ? NAN : 0.0f);
-        if (tid == 0 && p.lse) p.lse[blockIdx.x] = bad ? NAN : -INFINITY;
-        if (tid == 0 && bad) atomicCAS(&g_paged_status, 0, CSA_ERR_INVALID_ARG);
-        return;
-    }
-    for (int c = tid; c < d; c += kThreads)
-        qs[c] = __bfloat162float(p.q[(long long)blockIdx.x * d + c]) * p.qscale;
-    __syncthreads();
-    auto row_of = [&](const __nv_bfloat16 *pages, int r) {
-        const int page = p.table[(long long)b * p.M + r / p.S];
-        return pages + (((long long)page * p.Hkv + hk) * p.S + r % p.S) * d;
-    };
-    auto dot = [&](const __nv_bfloat16 *row) {
-        float s = 0.f;
-        for (int c = 0; c < d; ++c) s = fmaf(qs[c], __bfloat162float(row[c]), s);
-        return s;
-    };
-    const __nv_bfloat16 *k0 = p.mode == CSA_K0_GIVEN ? p.k0 + (long long)hk * d : row_of(p.k, 0);
-    const __nv_bfloat16 *v0 = p.mode == CSA_K0_GIVEN ? p.v0 + (long long)hk * d : row_of(p.v, 0);
-    float prev = p.mode == CSA_K0_ZERO ? 0.f : dot(k0);  // logit of the position before the tile
-    float m = prev, l = 0.f, o[2] = {0.f, 0.f};
-    constexpr int kTile = kThreads - 1;
-    for (int r0 = 0; r0 < n; r0 += kTile) {
-        const int have = min(kTile + 1, n - r0), own = min(kTile, n - r0);
-        if (tid < have) {
-            a[tid + 1] = dot(row_of(p.k, r0 + tid));
-            pg[tid] = p.table[(long long)b * p.M + (r0 + tid) / p.S];
-        }
-        if (tid == 0) a[0] = prev;
-        float mx = tid < have ? a[tid + 1] : -INFINITY;
-        for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, off));
-        if ((tid & 31) == 0) red[tid >> 5] = mx;
-        __syncthreads();
-        const float m1 = fmaxf(fmaxf(fmaxf(m, red[0]), fmaxf(red[1], red[2])), red[3]);
-        const float f = ex2_approx(m - m1);
-        m = m1;
-        l *= f;
-        o[0] *= f;
-        o[1] *= f;
-        float left = 0.f, right = 0.f, from_left = 0.f, sink = 0.f;
-        if (tid < own) {
-            interval(a[tid], a[tid + 1], m, sink, from_left);
-            if (tid + 1 < have) interval(a[tid + 1], a[tid + 2], m, left, right);
-            w[tid] = from_left + left;
-        }
-        if (tid == 0 && r0 == 0) red[4] = sink;
-        __syncthreads();
-        if (r0 == 0) {
-            l += red[4];
-            if (p.mode != CSA_K0_ZERO)
-                for (int i = 0; i < 2; ++i)
-                    if (tid + i * kThreads < d) o[i] = red[4] * __bfloat162float(v0[tid + i * kThreads]);
-        }
-        for (int r = 0; r < own; ++r) {
-            l += w[r];
-            const __nv_bfloat16 *row =
-                p.v + (((long long)pg[r] * p.Hkv + hk) * p.S + (r0 + r) % p.S) * d;
-            for (int i = 0; i < 2; ++i)
-                if (tid + i * kThreads < d) o[i] = fmaf(w[r], __bfloat162float(row[tid + i * kThreads]), o[i]);
-        }
-        prev = a[own];
-        __syncthreads();
-    }
-    for (int i = 0; i < 2; ++i)
-        if (tid + i * kThreads < d) out[tid + i * kThreads] = __float2bfloat16_rn(o[i] / l);
-    if (tid == 0 && p.lse) p.lse[blockIdx.x] = (m + log2f(l)) * kLn2;
+// D (+)= A B, 16 x 8 x 16, bf16 in, fp32 out.
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void ldsm(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm_t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+__device__ __forceinline__ int tiles_of(int n, int KT, long long most) {
+    return n < 0 || n > most ? 0 : (int)(((long long)n + KT - 1) / KT);
+}
+
+// Tiles (per head) of the sequences before each thread's chunk of sequences,
+// in s_cut[0 .. blockDim.x], the last entry the total.  Whole block.
+__device__ void form_cut(const int *seqlens, int B, int KT, long long most, long long *s_cut) {
+    const int tid = threadIdx.x, per = (B + blockDim.x - 1) / blockDim.x;
+    const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) mine += tiles_of(seqlens[b], KT, most);
+    __shared__ long long sums[32];
+    long long s = mine;
+    const int lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, s, off);
+        if (lane >= off) s += o;
+    }
+    if (lane == 31) sums[warp] = s;
+    __syncthreads();
+    long long before = 0;
+    for (int w = 0; w < warps; ++w) before += w < warp ? sums[w] : 0;
+    s_cut[tid] = before + s - mine;
+    if (tid == (int)blockDim.x - 1) s_cut[blockDim.x] = before + s;
+    __syncthreads();
+}
+
+// The sequence that holds unit u (of tiles x heads), and the units before it.
+// cut has `chunks` + 1 entries.
+__device__ __forceinline__ int find_sequence(long long u, const long long *cut, int chunks,
+                                             const int *seqlens, int B, int KT, long long most,
+                                             int heads, long long &before) {
+    int lo = 0, hi = chunks - 1;  // the last chunk that begins at or before u
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (cut[mid] * heads <= u)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    // chunks without tiles begin where the next one does: the last one is taken
+    int b = lo * ((B + chunks - 1) / chunks);
+    before = cut[lo] * heads;
+    while (true) {
+        const long long mine = (long long)tiles_of(seqlens[b], KT, most) * heads;
+        if (u < before + mine) return b;
+        before += mine;
+        ++b;
+    }
+}
+
+template <int D, int RH>
+__global__ void __launch_bounds__(Cfg<D>::Warps * 32, 1)
+paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUtensorMap map_k,
+             const __grid_constant__ CUtensorMap map_v) {
+    using C = Cfg<D>;
+    constexpr int KT = C::KT, NT = KT / 8, KS = D / 16, ON = D / 8;
+    extern __shared__ uint8_t raw[];
+    __shared__ long long s_cut[C::Warps * 32 + 1];
+    __shared__ __align__(8) uint64_t bars[C::Warps][kStages];
+    __shared__ int s_abort;
+    volatile int *abort_flag = &s_abort;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
+    const int heads = p.Hkv * p.GB;
+    const long long most = (long long)p.M * p.S;
+
+    if (lane == 0) {
+        for (int s = 0; s < kStages; ++s) mbar_init(smem_u32(&bars[warp][s]), 1);
+        fence_mbar_init();
+    }
+    if (threadIdx.x == 0) s_abort = 0;
+    form_cut(p.seqlens, p.B, KT, most, s_cut);
+    const long long U = s_cut[blockDim.x] * heads;
+    // workers in use: at least kMinRows rows each
+    long long in_use = U / (kMinRows / KT);
+    const long long all = (long long)C::Warps * gridDim.x;
+    in_use = in_use < 1 ? 1 : in_use > all ? all : in_use;
+    if (blockIdx.x == 0) {
+        p.cut[threadIdx.x] = s_cut[threadIdx.x];
+        if (threadIdx.x == 0) {
+            p.cut[blockDim.x] = s_cut[blockDim.x];
+            p.cut[blockDim.x + 1] = in_use;
+        }
+    }
+    // sequences without rows, and lengths out of range
+    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+        const int n = p.seqlens[b];
+        if (n > 0 && n <= most) continue;
+        const float v = n == 0 ? 0.0f : NAN;
+        for (int i = threadIdx.x; i < p.Hq * D; i += blockDim.x)
+            p.out[(long long)b * p.Hq * D + i] = __float2bfloat16_rn(v);
+        if (p.lse)
+            for (int h = threadIdx.x; h < p.Hq; h += blockDim.x)
+                p.lse[(long long)b * p.Hq + h] = n == 0 ? -INFINITY : NAN;
+        if (threadIdx.x == 0 && n != 0) atomicCAS(&g_paged_status, 0, CSA_ERR_INVALID_ARG);
+    }
+
+    // workers are numbered across blocks first, so that few of them spread over all SMs
+    const long long worker = (long long)warp * gridDim.x + blockIdx.x;
+    if (worker >= in_use) return;
+    const long long u0 = worker * U / in_use, u1 = (worker + 1) * U / in_use;
+    if (u0 >= u1) return;
+
+    // ---- position in the range of tiles: what is copied next, and what is consumed
+    long long before;
+    int b = find_sequence(u0, s_cut, blockDim.x, p.seqlens, p.B, KT, most, heads, before);
+    int n = p.seqlens[b], tiles = tiles_of(n, KT, most);
+    int head = (int)((u0 - before) / tiles);  // hk * GB + block of query heads
+    int tile = (int)((u0 - before) - (long long)head * tiles);
+
+    const uint32_t ring = (smem_u32(raw) + 1023) / 1024 * 1024 + warp * (kStages * C::Stage);
+    const int R = p.R, pieces = KT / R;
+    const uint32_t half = (uint32_t)R * 128;  // bytes of one 64-column box of a copy
+
+    int c_b = b, c_n = n, c_tiles = tiles, c_head = head, c_tile = tile;  // the copies' position
+    int held_b = -1, held_at = -1, held = 0;                              // page numbers, one per lane
+    long long to_copy = u1 - u0;
+    unsigned copied = 0, used = 0, bad_stages = 0;
+    int copy_stage = 0;
+    auto copy_next = [&]() {
+        if (to_copy == 0) return;
+        const int first = c_tile * pieces;
+        if (c_b != held_b || (first & ~31) != held_at) {
+            held_b = c_b;
+            held_at = first & ~31;
+            const long long row = (long long)(held_at + lane) * R;
+            held = row < c_n ? __ldg(p.table + (long long)c_b * p.M + (int)row / p.S) : 0;
+        }
+        const uint32_t bar = smem_u32(&bars[warp][copy_stage]), at = ring + copy_stage * C::Stage;
+        int bytes = 0, place[KT / 8];
+#pragma unroll
+        for (int i = 0; i < KT / 8; ++i) {
+            place[i] = -1;
+            if (i < pieces) {
+                const int row = c_tile * KT + i * R;
+                const int page = __shfl_sync(0xffffffffu, held, (first + i) & 31);
+                if (row < c_n) {
+                    if (page >= 0 && page < p.P) {
+                        place[i] = (page * p.Hkv + c_head / p.GB) * p.S + row % p.S;
+                        bytes += 2 * R * D * 2;
+                    } else {
+                        bad_stages |= 1u << copy_stage;
+                    }
+                }
+            }
+        }
+        if (lane == 0) {
+            mbar_arrive_expect_tx(bar, bytes);
+#pragma unroll
+            for (int i = 0; i < KT / 8; ++i)
+                if (place[i] >= 0) {
+                    tma_load_3d(at + i * R * D * 2, &map_k, 0, place[i], 0, bar);
+                    tma_load_3d(at + C::Tile + i * R * D * 2, &map_v, 0, place[i], 0, bar);
+                }
+        }
+        copy_stage = copy_stage + 1 == kStages ? 0 : copy_stage + 1;
+        ++copied;
+        --to_copy;
+        if (++c_tile == c_tiles && to_copy > 0) {
+            c_tile = 0;
+            if (++c_head == heads) {
+                c_head = 0;
+                do {
+                    c_n = p.seqlens[++c_b];
+                    c_tiles = tiles_of(c_n, KT, most);
+                } while (c_tiles == 0);
+            }
+        }
+    };
+    for (int s = 0; s < kStages; ++s) copy_next();
+
+    // ldmatrix addresses: keys, lane -> row (lane & 7) + 8 * (lane >> 4) of a pair of column
+    // tiles, chunk (lane >> 3) & 1; values, lane -> row (lane & 15), chunk lane >> 4.  Row r of a
+    // tile lies in copy r / R; its 16-byte chunks are permuted by r & 7.
+    auto row_at = [&](int r) { return (uint32_t)((r / R) * (R * D * 2) + (r % R) * 128); };
+    uint32_t k_row[NT / 2], v_row[KT / 16];
+#pragma unroll
+    for (int i = 0; i < NT / 2; ++i) k_row[i] = row_at(16 * i + (lane & 7) + 8 * (lane >> 4));
+#pragma unroll
+    for (int i = 0; i < KT / 16; ++i) v_row[i] = row_at(16 * i + (lane & 15));
+    const uint32_t x7 = lane & 7, k_chunk = (lane >> 3) & 1, v_chunk = lane >> 4;
+    auto chunk_at = [&](uint32_t c) { return (c >> 3) * half + (((c & 7) ^ x7) << 4); };
+
+    long long left_units = u1 - u0;
+    int stage = 0, which = 0;
+    uint32_t parity = 0;
+    while (left_units > 0) {
+        const int hk = head / p.GB, hb = head - hk * p.GB;
+        const int rows_h = min(p.HB, p.G - hb * p.HB);  // query heads of this block
+        const int q0 = hk * p.G + hb * p.HB;            // the first of them
+        const int last = (int)min((long long)tiles, tile + left_units);  // tiles [tile, last)
+        const int r0 = tile * KT, r1 = min(n, last * KT);
+        bool bad = false;
+
+        // queries: A operand, rows g (and g + 8)
+        uint32_t qa[KS][4];
+        {
+            const uint32_t *qg = reinterpret_cast<const uint32_t *>(p.q + ((long long)b * p.Hq + q0 + g) * D);
+#pragma unroll
+            for (int i = 0; i < KS; ++i) {
+                qa[i][0] = g < rows_h ? __ldg(qg + i * 8 + q) : 0u;
+                qa[i][2] = g < rows_h ? __ldg(qg + i * 8 + 4 + q) : 0u;
+                qa[i][1] = RH == 2 && g + 8 < rows_h ? __ldg(qg + 4 * D + i * 8 + q) : 0u;
+                qa[i][3] = RH == 2 && g + 8 < rows_h ? __ldg(qg + 4 * D + i * 8 + 4 + q) : 0u;
+            }
+        }
+        // logits of the row before the range, the row behind it and the sink: one more column
+        // tile whose "keys" 0, 1, 2 are read straight from memory
+        const __nv_bfloat16 *sink_v = nullptr;
+        float edge[4] = {0.f, 0.f, 0.f, 0.f};
+        if (r0 > 0 || r1 < n || p.mode != CSA_K0_ZERO) {
+            const int row = g == 0 ? r0 - 1 : g == 1 ? r1 : 0;
+            const __nv_bfloat16 *at = nullptr;
+            const bool cached = (g == 0 && r0 > 0) || (g == 1 && r1 < n) ||
+                                (g == 2 && r0 == 0 && p.mode == CSA_K0_COPY_FIRST);
+            if (cached) {
+                const int page = __ldg(p.table + (long long)b * p.M + row / p.S);
+                const long long place = ((long long)page * p.Hkv + hk) * p.S + row % p.S;
+                if (page >= 0 && page < p.P) {
+                    at = p.k + place * D;
+                    if (g == 2) sink_v = p.v + place * D;
+                } else {
+                    bad = true;
+                }
+            } else if (g == 2 && r0 == 0 && p.mode == CSA_K0_GIVEN) {
+                at = p.k0 + (long long)hk * D;
+                sink_v = p.v0 + (long long)hk * D;
+            }
+            const uint32_t *kg = reinterpret_cast<const uint32_t *>(at);
+#pragma unroll
+            for (int i = 0; i < KS; ++i)
+                mma(edge, qa[i], at ? __ldg(kg + i * 8 + q) : 0u, at ? __ldg(kg + i * 8 + 4 + q) : 0u);
+        }
+        sink_v = reinterpret_cast<const __nv_bfloat16 *>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(sink_v), 8));
+        float prev[RH], behind[RH], m[RH], pm[RH], l[RH], w0[RH];
+#pragma unroll
+        for (int h = 0; h < RH; ++h) {
+            const float before_a = __shfl_sync(0xffffffffu, edge[2 * h], lane & ~3);
+            const float sink_a = __shfl_sync(0xffffffffu, edge[2 * h], (lane & ~3) | 1);
+            behind[h] = __shfl_sync(0xffffffffu, edge[2 * h + 1], lane & ~3) * p.qscale;
+            prev[h] = (r0 > 0 ? before_a : sink_a) * p.qscale;
+            m[h] = prev[h];
+            pm[h] = 1.0f;  // 2^{prev - m}
+            l[h] = w0[h] = 0.f;
+        }
+        float o[ON][4];
+#pragma unroll
+        for (int i = 0; i < ON; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+        float w[RH][NT][2];  // weights of the tile before, its last one without the next interval
+        uint32_t v_at = 0;   // that tile's values
+
+        // all weights relative to a raised maximum
+        auto raise = [&](const float (&top)[RH]) {
+            float f[RH];
+#pragma unroll
+            for (int h = 0; h < RH; ++h) {
+                float t = top[h];
+                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+                t = fmaxf(t, m[h]);
+                f[h] = ex2_approx(m[h] - t);
+                m[h] = t;
+                l[h] *= f[h];
+                w0[h] *= f[h];
+                pm[h] *= f[h];
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    w[h][i][0] *= f[h];
+                    w[h][i][1] *= f[h];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < ON; ++i) {
+                o[i][0] *= f[0];
+                o[i][1] *= f[0];
+                o[i][2] *= f[RH - 1];
+                o[i][3] *= f[RH - 1];
+            }
+        };
+        // the second product for the tile before
+        auto values = [&]() {
+#pragma unroll
+            for (int h = 0; h < RH; ++h)
+#pragma unroll
+                for (int i = 0; i < NT; ++i) l[h] += w[h][i][0] + w[h][i][1];
+#pragma unroll
+            for (int ks = 0; ks < KT / 16; ++ks) {
+                uint32_t hi[RH][2], lo[RH][2];
+#pragma unroll
+                for (int h = 0; h < RH; ++h)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float a = w[h][2 * ks + i][0], c = w[h][2 * ks + i][1];
+                        hi[h][i] = pack_bf16x2(a, c);
+                        lo[h][i] = pack_bf16x2(a - __uint_as_float(hi[h][i] << 16),
+                                               c - __uint_as_float(hi[h][i] & 0xffff0000u));
+                    }
+#pragma unroll
+                for (int i = 0; i < ON / 2; ++i) {
+                    uint32_t vb[4];
+                    ldsm_t(v_at + v_row[ks] + chunk_at(2 * i + v_chunk), vb);
+                    if (RH == 1) {
+                        const uint32_t a[4] = {hi[0][0], lo[0][0], hi[0][1], lo[0][1]};
+                        mma(o[2 * i], a, vb[0], vb[1]);
+                        mma(o[2 * i + 1], a, vb[2], vb[3]);
+                    } else {
+                        const uint32_t a[4] = {hi[0][0], hi[RH - 1][0], hi[0][1], hi[RH - 1][1]};
+                        const uint32_t c[4] = {lo[0][0], lo[RH - 1][0], lo[0][1], lo[RH - 1][1]};
+                        mma(o[2 * i], a, vb[0], vb[1]);
+                        mma(o[2 * i + 1], a, vb[2], vb[3]);
+                        mma(o[2 * i], c, vb[0], vb[1]);
+                        mma(o[2 * i + 1], c, vb[2], vb[3]);
+                    }
+                }
+            }
+        };
+
+        for (int j = tile; j < last; ++j) {
+            const bool arrived = mbar_wait_bounded(smem_u32(&bars[warp][stage]), parity, abort_flag,
+                                                   &g_paged_status, kWaitLimitNs);
+            if (!__all_sync(0xffffffffu, arrived)) {
+                // keeps the ring alive until its copies have landed, for at most one more limit each
+                if (lane == 0)
+                    for (unsigned i = used; i < copied; ++i) {
+                        const uint32_t bar = smem_u32(&bars[warp][i % kStages]);
+                        const uint64_t t0 = globaltimer_ns();
+                        while (!mbar_try_wait(bar, (i / kStages) & 1) && globaltimer_ns() - t0 < kWaitLimitNs) {
+                        }
+                    }
+                __syncwarp();
+                return;
+            }
+            if (bad_stages >> stage & 1) {
+                bad = true;
+                bad_stages &= ~(1u << stage);
+            }
+            const uint32_t k_at = ring + stage * C::Stage;
+            const int own = n - j * KT;  // rows of this tile that exist, if fewer than KT
+            if (own < KT) {
+                // rows behind the end: their weights are 0, and 0 * NaN is not
+                uint8_t *vt = raw + (k_at + C::Tile - smem_u32(raw));
+                for (int i = lane; i < (KT - own) * (D / 8); i += 32) {
+                    const int r = own + i / (D / 8), c = i % (D / 8);
+                    *reinterpret_cast<uint4 *>(vt + row_at(r) + (c >> 3) * half + ((c & 7) << 4)) =
+                        make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
+            // logits
+            float s[NT][4];
+#pragma unroll
+            for (int i = 0; i < NT; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                for (int i = 0; i < NT / 2; ++i) {
+                    uint32_t kb[4];
+                    ldsm(k_at + k_row[i] + chunk_at(2 * ks + k_chunk), kb);
+                    mma(s[2 * i], qa[ks], kb[0], kb[1]);
+                    mma(s[2 * i + 1], qa[ks], kb[2], kb[3]);
+                }
+            float top[RH];
+            bool over = false;
+#pragma unroll
+            for (int h = 0; h < RH; ++h) {
+                top[h] = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        s[i][2 * h + e] *= p.qscale;
+                        if (8 * i + 2 * q + e < own) top[h] = fmaxf(top[h], s[i][2 * h + e]);
+                    }
+                }
+                over |= top[h] > m[h] + kRaise;
+            }
+            if (j == tile) {
+#pragma unroll
+                for (int h = 0; h < RH; ++h)
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) w[h][i][0] = w[h][i][1] = 0.f;
+            }
+            if (__any_sync(0xffffffffu, over)) raise(top);
+
+            // this tile's weights, and the share of its first interval that the row before gets
+            float nw[RH][NT][2], to_before[RH];
+#pragma unroll
+            for (int h = 0; h < RH; ++h) {
+                float pe[NT][2], even_left[NT];
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    pe[i][0] = ex2_approx(s[i][2 * h] - m[h]);
+                    pe[i][1] = ex2_approx(s[i][2 * h + 1] - m[h]);
+                }
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    // the logit and power before this lane's first row: from the lane to the left, for
+                    // q = 0 from q = 3 of the column tile before
+                    const float a_src = q == 3 ? (i == 0 ? prev[h] : s[i > 0 ? i - 1 : 0][2 * h + 1]) : s[i][2 * h + 1];
+                    const float p_src = q == 3 ? (i == 0 ? pm[h] : pe[i > 0 ? i - 1 : 0][1]) : pe[i][1];
+                    const float a_b = __shfl_sync(0xffffffffu, a_src, (lane & ~3) | ((q + 3) & 3));
+                    const float p_b = __shfl_sync(0xffffffffu, p_src, (lane & ~3) | ((q + 3) & 3));
+                    float r_even, l_odd, r_odd;
+                    interval(a_b, s[i][2 * h], p_b, pe[i][0], even_left[i], r_even);
+                    interval(s[i][2 * h], s[i][2 * h + 1], pe[i][0], pe[i][1], l_odd, r_odd);
+                    if (8 * i + 2 * q >= own) even_left[i] = r_even = 0.f;
+                    if (8 * i + 2 * q + 1 >= own) l_odd = r_odd = 0.f;
+                    nw[h][i][0] = r_even + l_odd;
+                    nw[h][i][1] = r_odd;
+                }
+                to_before[h] = __shfl_sync(0xffffffffu, even_left[0], lane & ~3);
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    const float src = q == 0 ? (i + 1 < NT ? even_left[i + 1 < NT ? i + 1 : 0] : 0.f) : even_left[i];
+                    nw[h][i][1] += __shfl_sync(0xffffffffu, src, (lane & ~3) | ((q + 1) & 3));
+                }
+                prev[h] = __shfl_sync(0xffffffffu, s[NT - 1][2 * h + 1], lane | 3);
+                pm[h] = __shfl_sync(0xffffffffu, pe[NT - 1][1], lane | 3);
+            }
+            if (j > tile) {
+#pragma unroll
+                for (int h = 0; h < RH; ++h)
+                    if (q == 3) w[h][NT - 1][1] += to_before[h];
+                values();
+                __syncwarp();  // every lane has read the tile before: its stage is free
+                ++used;
+                copy_next();
+            } else if (r0 == 0) {
+#pragma unroll
+                for (int h = 0; h < RH; ++h) w0[h] = to_before[h];
+            }
+#pragma unroll
+            for (int h = 0; h < RH; ++h)
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    w[h][i][0] = nw[h][i][0];
+                    w[h][i][1] = nw[h][i][1];
+                }
+            v_at = k_at + C::Tile;
+            if (++stage == kStages) {
+                stage = 0;
+                parity ^= 1;
+            }
+        }
+        if (r1 < n) {  // the range's last row has a neighbour behind it
+            bool over = false;
+#pragma unroll
+            for (int h = 0; h < RH; ++h) over |= behind[h] > m[h] + kRaise;
+            if (__any_sync(0xffffffffu, over)) raise(behind);
+#pragma unroll
+            for (int h = 0; h < RH; ++h) {
+                float left, right;
+                interval(prev[h], behind[h], pm[h], ex2_approx(behind[h] - m[h]), left, right);
+                if (q == 3) w[h][NT - 1][1] += left;
+            }
+        }
+        values();
+        __syncwarp();
+        ++used;
+        copy_next();
+
+        bad = __any_sync(0xffffffffu, bad);
+        const bool whole = r0 == 0 && r1 == n;
+        float sum[RH];
+#pragma unroll
+        for (int h = 0; h < RH; ++h) {
+            float t = l[h];
+            t += __shfl_xor_sync(0xffffffffu, t, 1);
+            t += __shfl_xor_sync(0xffffffffu, t, 2);
+            sum[h] = bad ? NAN : t + w0[h];
+        }
+        const long long slot = (worker * 2 + which) * p.HB;
+#pragma unroll
+        for (int h = 0; h < RH; ++h) {
+            const int row = g + 8 * h;
+            if (row < rows_h) {
+                const float inv = 1.0f / sum[h];
+                const long long oh = (long long)b * p.Hq + q0 + row;
+                __nv_bfloat16 *og = p.out + oh * D;
+                float *po = p.part_o + (slot + row) * D;
+#pragma unroll
+                for (int i = 0; i < ON; ++i) {
+                    float a = o[i][2 * h], c = o[i][2 * h + 1];
+                    if (RH == 1) {  // the low parts of the weights
+                        a += o[i][2];
+                        c += o[i][3];
+                    }
+                    if (sink_v) {
+                        const uint32_t v2 = __ldg(reinterpret_cast<const uint32_t *>(sink_v) + i * 4 + q);
+                        a = fmaf(w0[h], __uint_as_float(v2 << 16), a);
+                        c = fmaf(w0[h], __uint_as_float(v2 & 0xffff0000u), c);
+                    }
+                    if (whole)
+                        *reinterpret_cast<uint32_t *>(og + 8 * i + 2 * q) = pack_bf16x2(a * inv, c * inv);
+                    else
+                        *reinterpret_cast<float2 *>(po + 8 * i + 2 * q) = make_float2(a, c);
+                }
+                if (q == 0) {
+                    if (!whole) {
+                        p.part_ml[2 * (slot + row)] = m[h];
+                        p.part_ml[2 * (slot + row) + 1] = sum[h];
+                    } else if (p.lse) {
+                        p.lse[oh] = (m[h] + log2f(sum[h])) * kLn2;
+                    }
+                }
+            }
+        }
+        if (bad && lane == 0) atomicCAS(&g_paged_status, 0, CSA_ERR_INVALID_ARG);
+        which = 1;  // a later part of this worker begins at a sequence's first row
+
+        left_units -= last - tile;
+        tile = 0;
+        if (left_units > 0 && ++head == heads) {
+            head = 0;
+            do {
+                n = p.seqlens[++b];
+                tiles = tiles_of(n, KT, most);
+            } while (tiles == 0);
+        }
+    }
+}
+
+// Joins the parts of one (sequence, cached head, block of query heads), for
+// one query head per block.  With M the largest m_c: o = sum 2^{m_c-M} o_c /
+// sum 2^{m_c-M} l_c, lse = (M + log2 sum) ln 2.  Each warp takes every 8th part
+// against its own maximum; the warps meet in shared memory.  by_worker: block
+// x is a worker, and joins what its range begins in the middle of if it is
+// the second worker there; otherwise block x is the segment itself.
+constexpr int kJoinWarps = 8;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const PagedParams p, int chunks, int by_worker) {
+    using C = Cfg<D>;
+    constexpr int V = D / 32;  // columns per lane
+    __shared__ float s_o[kJoinWarps][D], s_m[kJoinWarps], s_l[kJoinWarps];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = blockIdx.y;
+    const int heads = p.Hkv * p.GB;
+    const long long most = (long long)p.M * p.S, U = p.cut[chunks] * heads, W = p.cut[chunks + 1];
+    if (U == 0) return;
+    int b, head;
+    long long before;
+    if (by_worker) {
+        const long long x = blockIdx.x;
+        if (x >= W || x == 0) return;
+        const long long u = x * U / W;
+        b = find_sequence(u, p.cut, chunks, p.seqlens, p.B, C::KT, most, heads, before);
+        head = (int)((u - before) / tiles_of(p.seqlens[b], C::KT, most));
+    } else {
+        b = blockIdx.x / heads;
+        head = blockIdx.x - b * heads;
+        const int per = (p.B + chunks - 1) / chunks;
+        before = p.cut[b / per] * heads;
+        for (int i = b / per * per; i < b; ++i) before += (long long)tiles_of(p.seqlens[i], C::KT, most) * heads;
+    }
+    const int tiles = tiles_of(p.seqlens[b], C::KT, most);
+    if (tiles == 0) return;
+    const long long s0 = before + (long long)head * tiles, s1 = s0 + tiles;
+    const long long c0 = ((s0 + 1) * W - 1) / U, c1 = (s1 * W - 1) / U;  // the first and last worker on it
+    if (c0 == c1) return;                                                  // written whole
+    if (by_worker && c0 + 1 != (long long)blockIdx.x) return;
+    const int hk = head / p.GB, hb = head - hk * p.GB;
+    if (row >= min(p.HB, p.G - hb * p.HB)) return;
+    const int first_slot = c0 * U / W < s0 ? 1 : 0;  // the first worker's range began earlier
+
+    auto slot = [&](long long c) { return ((c * 2 + (c == c0 ? first_slot : 0)) * p.HB + row); };
+    float M = -INFINITY, L = 0.f, o[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] = 0.f;
+    // 32 parts at a time: their maxima and sums one per lane, then their columns
+    for (long long base = c0 + warp; base <= c1; base += 32 * kJoinWarps) {
+        const long long mine = base + (long long)lane * kJoinWarps;
+        float m = -INFINITY, l = 0.f;
+        if (mine <= c1) {
+            const float2 ml = *reinterpret_cast<const float2 *>(p.part_ml + 2 * slot(mine));
+            m = ml.x;
+            l = ml.y;
+        }
+        float top = m;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        const float M1 = fmaxf(M, top), f = ex2_approx(M - M1), mine_f = ex2_approx(m - M1);
+        float add = l * mine_f;
+        if (mine > c1) add = 0.f;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) add += __shfl_xor_sync(0xffffffffu, add, off);
+        L = L * f + add;
+        M = M1;
+#pragma unroll
+        for (int i = 0; i < V; ++i) o[i] *= f;
+        const int count = (int)min(32LL, (c1 - base) / kJoinWarps + 1);
+#pragma unroll 8
+        for (int c = 0; c < count; ++c) {
+            const float fc = __shfl_sync(0xffffffffu, mine_f, c);
+            const float *po = p.part_o + slot(base + (long long)c * kJoinWarps) * D;
+#pragma unroll
+            for (int i = 0; i < V; i += 2) {
+                const float2 v = *reinterpret_cast<const float2 *>(po + 32 * i + 2 * lane);
+                o[i] = fmaf(fc, v.x, o[i]);
+                o[i + 1] = fmaf(fc, v.y, o[i + 1]);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; i += 2)
+        *reinterpret_cast<float2 *>(&s_o[warp][32 * i + 2 * lane]) = make_float2(o[i], o[i + 1]);
+    if (lane == 0) {
+        s_m[warp] = M;
+        s_l[warp] = L;
+    }
+    __syncthreads();
+    float top = s_m[0];
+#pragma unroll
+    for (int i = 1; i < kJoinWarps; ++i) top = fmaxf(top, s_m[i]);
+    float f[kJoinWarps], total = 0.f;
+#pragma unroll
+    for (int i = 0; i < kJoinWarps; ++i) {
+        f[i] = ex2_approx(s_m[i] - top);  // 0 for a warp without parts
+        total = fmaf(f[i], s_l[i], total);
+    }
+    const long long oh = (long long)b * p.Hq + hk * p.G + hb * p.HB + row;
+    const float inv = 1.0f / total;
+    for (int col = threadIdx.x; col < D; col += kJoinWarps * 32) {
+        float v = 0.f;
+#pragma unroll
+        for (int i = 0; i < kJoinWarps; ++i) v = fmaf(f[i], s_o[i][col], v);
+        p.out[oh * D + col] = __float2bfloat16_rn(v * inv);
+    }
+    if (threadIdx.x == 0 && p.lse) p.lse[oh] = (top + log2f(total)) * kLn2;
+}
+
+// [P * Hkv * S, D] bf16 as {64, rows, D / 64}, boxes of R rows.
+bool encode_pool(CUtensorMap *map, const void *ptr, long long rows, int D, int R) {
+    auto fn = csa_tc::get_encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)(D / 64)};
+    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, 128};
+    const cuuint32_t box[3] = {64, (cuuint32_t)R, (cuuint32_t)(D / 64)};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int RH>
+int launch(PagedParams &p, cudaStream_t stream) {
+    using C = Cfg<D>;
+    p.R = C::KT;
+    while (p.S % p.R != 0) p.R /= 2;  // S is a multiple of 8
+    CUtensorMap map_k, map_v;
+    const long long rows = (long long)p.P * p.Hkv * p.S;
+    // no pool: no sequence has a valid page, and the maps are never used
+    const void *some = p.q;
+    if (!encode_pool(&map_k, rows ? (const void *)p.k : some, rows ? rows : 8, D, p.R) ||
+        !encode_pool(&map_v, rows ? (const void *)p.v : some, rows ? rows : 8, D, p.R))
+        return CSA_ERR_CUDA;
+    const int heads = p.Hkv * p.GB;
+    // blocks that the largest possible lengths can keep busy
+    const long long most = (long long)p.B * heads * (((long long)p.M * p.S + kMinRows - 1) / kMinRows);
+    const int grid = (int)(most < kGrid ? (most < 1 ? 1 : most) : kGrid);
+    auto kern = paged_kernel<D, RH>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::Smem) != cudaSuccess)
+        return CSA_ERR_CUDA;
+    kern<<<grid, C::Warps * 32, C::Smem, stream>>>(p, map_k, map_v);
+    const long long segments = (long long)p.B * heads, workers = (long long)grid * C::Warps;
+    const int by_worker = segments > workers;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(by_worker ? workers : segments), (unsigned)p.HB);
+    cfg.blockDim = dim3(kJoinWarps * 32);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, join_kernel<D>, p, C::Warps * 32, by_worker) != cudaSuccess) return CSA_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
+}
+
+// Blocks of the query heads of a group, at most 16 each, as equal as can be.
+int head_blocks(int G) { return (G + 15) / 16; }
+
+long long workers(int d) { return d == 256 ? Cfg<256>::Workers : Cfg<128>::Workers; }
+static_assert(Cfg<64>::Workers == Cfg<128>::Workers, "");
 
 }  // namespace
 
 long long csa_decode_paged_scratch_bytes(int B, int Hq, int Hkv, int d) {
-    if (B < 0 || Hq < 0 || Hkv < 0 || !(d == 64 || d == 128 || d == 256)) return -1;
-    return 16;
+    if (B < 0 || Hq < 0 || Hkv < 1 || Hq % Hkv != 0 || !(d == 64 || d == 128 || d == 256)) return -1;
+    const int G = Hq / Hkv;
+    const int GB = head_blocks(G), HB = GB ? (G + GB - 1) / GB : 0;
+    return 2 * workers(d) * HB * (d + 2) * (long long)sizeof(float) + (kMaxThreads + 2) * (long long)sizeof(long long);
 }
 
 int csa_decode_paged_run(const void *q, const void *k_pages, const void *v_pages, const void *k0,
@@ -172,11 +844,22 @@ int csa_decode_paged_run(const void *q, const void *k_pages, const void *v_pages
     p.P = P;
     p.S = S;
     p.M = M;
-    p.d = d;
+    p.G = Hq / Hkv;
+    p.GB = head_blocks(p.G);
+    p.HB = (p.G + p.GB - 1) / p.GB;
     p.qscale = scale * kLog2e;
     p.mode = mode;
-    paged_kernel<<<(unsigned)(B * Hq), kThreads, 0, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
+    p.cut = static_cast<long long *>(scratch);
+    p.part_ml = reinterpret_cast<float *>(p.cut + kMaxThreads + 2);
+    p.part_o = p.part_ml + 2 * workers(d) * p.HB * 2;
+    if (p.HB <= 8) {
+        if (d == 64) return launch<64, 1>(p, stream);
+        if (d == 128) return launch<128, 1>(p, stream);
+        return launch<256, 1>(p, stream);
+    }
+    if (d == 64) return launch<64, 2>(p, stream);
+    if (d == 128) return launch<128, 2>(p, stream);
+    return launch<256, 2>(p, stream);
 }
 
 int csa_paged_take_status(void) {

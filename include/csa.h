@@ -459,8 +459,9 @@ int csa_decode_merge_ranges(const float *o_parts, const float *lse_parts, int R,
  *   otherwise, as for P * Hkv * S > 2^31 - 1); Hq a multiple of Hkv
  *   (CSA_ERR_INVALID_ARG).  q, pools, out, workspace (and k0, v0 in GIVEN
  *   mode) 16-byte aligned, the rest 4-byte.  B * Hq == 0: CSA_OK, nothing
- *   launched.  The result does not depend on scheduling: equal inputs give
- *   equal bits.
+ *   launched.  Equal inputs give equal bits, whatever the scheduling; how a
+ *   sequence is cut into parts goes by all lengths of the batch, so its last
+ *   bits may change with the lengths of the others.
  */
 int csa_decode_paged(const void *q, const void *k_pages, const void *v_pages, const void *k0,
                      const void *v0, const int *block_table, const int *seqlens, void *out,

@@ -158,7 +158,7 @@ def test_infinite_values_in_the_cache_pass_through():
 def test_bad_lengths_and_pages_are_reported():
     S, d = 16, 128
     x = make([100, 40, 60, 70, 0], 4, 2, d, S, seed=11)
-    good, gl = run(x, 0)
+    run(x, 0)
     assert device_status() == 0
     P, M = x["k"].shape[0], x["table"].shape[1]
     x["lens"][1] = M * S + 1
@@ -168,8 +168,8 @@ def test_bad_lengths_and_pages_are_reported():
     assert device_status() == -1 and device_status() == 0
     for b in (1, 2, 4):
         assert torch.isnan(o[b].float()).all() and torch.isnan(lse[b]).all()
-    for b in (0, 3):
-        assert torch.equal(o[b], good[b]) and torch.equal(lse[b], gl[b])
+    # the others are right; their last bits may differ, as the parts are cut by all lengths
+    check(x, o, lse, S, 0, d ** -0.5, only=(0, 3))
     x["table"][2, 1] = -1
     o, _ = run(x, 0)
     assert device_status() == -1 and torch.isnan(o[2].float()).all()
