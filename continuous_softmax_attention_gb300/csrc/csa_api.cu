@@ -3,6 +3,7 @@
 // host synchronisation on the compute entry points.
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -36,14 +37,18 @@ int check_common(const void *q, const void *k, const void *v, const void *k0, co
 }
 
 int device_ok() {
+    static std::atomic<unsigned long long> good{0};  // devices 0..63 found usable: what they are does not change
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return CSA_ERR_NO_DEVICE;
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+    if (good.load(std::memory_order_relaxed) & bit) return CSA_OK;
     int major = 0, minor = 0;
     if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
         return CSA_ERR_NO_DEVICE;
     // The binary carries sm_103a code only.
     if (major != 10 || minor != 3) return CSA_ERR_NO_DEVICE;
+    good.fetch_or(bit, std::memory_order_relaxed);
     return CSA_OK;
 }
 

@@ -51,8 +51,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
 constexpr int kGrid = 152;        // one block per SM
 constexpr int kStages = 3;        // tiles in a worker's ring
-constexpr int kMaxThreads = 256;
 constexpr int kMinRows = 64;      // rows per worker that a split leaves, at least
+// What beginning and ending a part costs, in tiles: a range of many short
+// sequences takes as long as one of a long sequence.
+constexpr int kPartCost = 3;
 constexpr float kRaise = 16.0f;   // log2 units a logit may pass the running maximum by
 
 __device__ int g_paged_status;  // sticky status word of this file's kernels
@@ -75,7 +77,6 @@ struct PagedParams {
     float *lse;
     float *part_o;    // [2 * workers][HB][D]: unnormalised sums of a part
     float *part_ml;   // [2 * workers][HB][2]: its maximum (log2 units) and weight sum
-    long long *cut;   // [kMaxThreads + 2]: tiles before each chunk of sequences, all, workers in use
     int B, Hq, Hkv, P, S, M;
     int G, GB, HB;    // query heads of a group, blocks of them, heads per block
     int R;            // rows per copy: divides S and the tile
@@ -131,13 +132,17 @@ __device__ __forceinline__ int tiles_of(int n, int KT, long long most) {
     return n < 0 || n > most ? 0 : (int)(((long long)n + KT - 1) / KT);
 }
 
-// Tiles (per head) of the sequences before each thread's chunk of sequences,
-// in s_cut[0 .. blockDim.x], the last entry the total.  Whole block.
-__device__ void form_cut(const int *seqlens, int B, int KT, long long most, long long *s_cut) {
+// What one cached head of a sequence counts for in the cut: its tiles and the
+// cost of a part.
+__device__ __forceinline__ int units_of(int tiles) { return tiles > 0 ? tiles + kPartCost : 0; }
+
+// Units (per head) of the sequences before each thread's chunk of sequences, in
+// cut[0 .. blockDim.x], the last entry the total.  Whole block.
+__device__ void form_cut(const int *seqlens, int B, int KT, long long most, long long *cut) {
     const int tid = threadIdx.x, per = (B + blockDim.x - 1) / blockDim.x;
     const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
     long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += tiles_of(seqlens[b], KT, most);
+    for (int b = b0; b < b1; ++b) mine += units_of(tiles_of(seqlens[b], KT, most));
     __shared__ long long sums[32];
     long long s = mine;
     const int lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
@@ -150,12 +155,18 @@ __device__ void form_cut(const int *seqlens, int B, int KT, long long most, long
     __syncthreads();
     long long before = 0;
     for (int w = 0; w < warps; ++w) before += w < warp ? sums[w] : 0;
-    s_cut[tid] = before + s - mine;
-    if (tid == (int)blockDim.x - 1) s_cut[blockDim.x] = before + s;
+    cut[tid] = before + s - mine;
+    if (tid == (int)blockDim.x - 1) cut[blockDim.x] = before + s;
     __syncthreads();
 }
 
-// The sequence that holds unit u (of tiles x heads), and the units before it.
+// Workers in use for U units: at least kMinRows rows each.
+__device__ __forceinline__ long long workers_for(long long U, int KT, long long all) {
+    const long long w = U / (kMinRows / KT);
+    return w < 1 ? 1 : w > all ? all : w;
+}
+
+// The sequence that holds unit u (of units x heads), and the units before it.
 // cut has `chunks` + 1 entries.
 __device__ __forceinline__ int find_sequence(long long u, const long long *cut, int chunks,
                                              const int *seqlens, int B, int KT, long long most,
@@ -168,15 +179,45 @@ __device__ __forceinline__ int find_sequence(long long u, const long long *cut, 
         else
             hi = mid - 1;
     }
-    // chunks without tiles begin where the next one does: the last one is taken
+    // chunks without units begin where the next one does: the last one is taken
     int b = lo * ((B + chunks - 1) / chunks);
     before = cut[lo] * heads;
     while (true) {
-        const long long mine = (long long)tiles_of(seqlens[b], KT, most) * heads;
+        const long long mine = (long long)units_of(tiles_of(seqlens[b], KT, most)) * heads;
         if (u < before + mine) return b;
         before += mine;
         ++b;
     }
+}
+
+// A worker's units [u0, u1) as parts: tiles [tile, last) of one head of one
+// sequence each.
+struct Part {
+    int b, head, n, tiles, tile, last;
+    long long s0;  // the segment's first unit
+};
+
+__device__ __forceinline__ void clip(Part &t, long long u0, long long u1) {
+    t.tile = (int)max(0LL, u0 - t.s0 - kPartCost);
+    t.last = (int)min((long long)t.tiles, max(0LL, u1 - t.s0 - kPartCost));
+}
+
+// The next part with tiles; false behind the last.
+__device__ __forceinline__ bool next_part(Part &t, long long u0, long long u1, const int *seqlens, int KT,
+                                          long long most, int heads) {
+    do {
+        t.s0 += units_of(t.tiles);
+        if (t.s0 >= u1) return false;
+        if (++t.head == heads) {
+            t.head = 0;
+            do {
+                t.n = seqlens[++t.b];
+                t.tiles = tiles_of(t.n, KT, most);
+            } while (t.tiles == 0);
+        }
+        clip(t, u0, u1);
+    } while (t.tile >= t.last);
+    return true;
 }
 
 template <int D, int RH>
@@ -199,19 +240,11 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
         fence_mbar_init();
     }
     if (threadIdx.x == 0) s_abort = 0;
+    // the join's blocks may take their places as this kernel's blocks end
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     form_cut(p.seqlens, p.B, KT, most, s_cut);
     const long long U = s_cut[blockDim.x] * heads;
-    // workers in use: at least kMinRows rows each
-    long long in_use = U / (kMinRows / KT);
-    const long long all = (long long)C::Warps * gridDim.x;
-    in_use = in_use < 1 ? 1 : in_use > all ? all : in_use;
-    if (blockIdx.x == 0) {
-        p.cut[threadIdx.x] = s_cut[threadIdx.x];
-        if (threadIdx.x == 0) {
-            p.cut[blockDim.x] = s_cut[blockDim.x];
-            p.cut[blockDim.x + 1] = in_use;
-        }
-    }
+    const long long in_use = workers_for(U, KT, (long long)C::Warps * gridDim.x);
     // sequences without rows, and lengths out of range
     for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
         const int n = p.seqlens[b];
@@ -231,30 +264,33 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
     const long long u0 = worker * U / in_use, u1 = (worker + 1) * U / in_use;
     if (u0 >= u1) return;
 
-    // ---- position in the range of tiles: what is copied next, and what is consumed
-    long long before;
-    int b = find_sequence(u0, s_cut, blockDim.x, p.seqlens, p.B, KT, most, heads, before);
-    int n = p.seqlens[b], tiles = tiles_of(n, KT, most);
-    int head = (int)((u0 - before) / tiles);  // hk * GB + block of query heads
-    int tile = (int)((u0 - before) - (long long)head * tiles);
+    // ---- position in the range: what is copied next, and what is consumed
+    Part now;
+    now.b = find_sequence(u0, s_cut, blockDim.x, p.seqlens, p.B, KT, most, heads, now.s0);
+    now.n = p.seqlens[now.b];
+    now.tiles = tiles_of(now.n, KT, most);
+    now.head = (int)((u0 - now.s0) / units_of(now.tiles));  // hk * GB + block of query heads
+    now.s0 += (long long)now.head * units_of(now.tiles);
+    clip(now, u0, u1);
+    if (now.tile >= now.last && !next_part(now, u0, u1, p.seqlens, KT, most, heads)) return;
 
     const uint32_t ring = (smem_u32(raw) + 1023) / 1024 * 1024 + warp * (kStages * C::Stage);
     const int R = p.R, pieces = KT / R;
     const uint32_t half = (uint32_t)R * 128;  // bytes of one 64-column box of a copy
 
-    int c_b = b, c_n = n, c_tiles = tiles, c_head = head, c_tile = tile;  // the copies' position
-    int held_b = -1, held_at = -1, held = 0;                              // page numbers, one per lane
-    long long to_copy = u1 - u0;
+    Part ahead = now;
+    bool more = true;  // something is left to copy
+    int held_b = -1, held_at = -1, held = 0;  // page numbers, one per lane
     unsigned copied = 0, used = 0, bad_stages = 0;
     int copy_stage = 0;
     auto copy_next = [&]() {
-        if (to_copy == 0) return;
-        const int first = c_tile * pieces;
-        if (c_b != held_b || (first & ~31) != held_at) {
-            held_b = c_b;
+        if (!more) return;
+        const int first = ahead.tile * pieces;
+        if (ahead.b != held_b || (first & ~31) != held_at) {
+            held_b = ahead.b;
             held_at = first & ~31;
             const long long row = (long long)(held_at + lane) * R;
-            held = row < c_n ? __ldg(p.table + (long long)c_b * p.M + (int)row / p.S) : 0;
+            held = row < ahead.n ? __ldg(p.table + (long long)ahead.b * p.M + (int)row / p.S) : 0;
         }
         const uint32_t bar = smem_u32(&bars[warp][copy_stage]), at = ring + copy_stage * C::Stage;
         int bytes = 0, place[KT / 8];
@@ -262,11 +298,11 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
         for (int i = 0; i < KT / 8; ++i) {
             place[i] = -1;
             if (i < pieces) {
-                const int row = c_tile * KT + i * R;
+                const int row = ahead.tile * KT + i * R;
                 const int page = __shfl_sync(0xffffffffu, held, (first + i) & 31);
-                if (row < c_n) {
+                if (row < ahead.n) {
                     if (page >= 0 && page < p.P) {
-                        place[i] = (page * p.Hkv + c_head / p.GB) * p.S + row % p.S;
+                        place[i] = (page * p.Hkv + ahead.head / p.GB) * p.S + row % p.S;
                         bytes += 2 * R * D * 2;
                     } else {
                         bad_stages |= 1u << copy_stage;
@@ -285,17 +321,7 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
         }
         copy_stage = copy_stage + 1 == kStages ? 0 : copy_stage + 1;
         ++copied;
-        --to_copy;
-        if (++c_tile == c_tiles && to_copy > 0) {
-            c_tile = 0;
-            if (++c_head == heads) {
-                c_head = 0;
-                do {
-                    c_n = p.seqlens[++c_b];
-                    c_tiles = tiles_of(c_n, KT, most);
-                } while (c_tiles == 0);
-            }
-        }
+        if (++ahead.tile == ahead.last) more = next_part(ahead, u0, u1, p.seqlens, KT, most, heads);
     };
     for (int s = 0; s < kStages; ++s) copy_next();
 
@@ -311,14 +337,13 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
     const uint32_t x7 = lane & 7, k_chunk = (lane >> 3) & 1, v_chunk = lane >> 4;
     auto chunk_at = [&](uint32_t c) { return (c >> 3) * half + (((c & 7) ^ x7) << 4); };
 
-    long long left_units = u1 - u0;
-    int stage = 0, which = 0;
+    int stage = 0;
     uint32_t parity = 0;
-    while (left_units > 0) {
-        const int hk = head / p.GB, hb = head - hk * p.GB;
+    do {
+        const int b = now.b, n = now.n, tile = now.tile, last = now.last;
+        const int hk = now.head / p.GB, hb = now.head - hk * p.GB;
         const int rows_h = min(p.HB, p.G - hb * p.HB);  // query heads of this block
         const int q0 = hk * p.G + hb * p.HB;            // the first of them
-        const int last = (int)min((long long)tiles, tile + left_units);  // tiles [tile, last)
         const int r0 = tile * KT, r1 = min(n, last * KT);
         bool bad = false;
 
@@ -334,35 +359,27 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
                 qa[i][3] = RH == 2 && g + 8 < rows_h ? __ldg(qg + 4 * D + i * 8 + 4 + q) : 0u;
             }
         }
-        // logits of the row before the range, the row behind it and the sink: one more column
+        // logits of the row before the range, the row behind it and a given sink: one more column
         // tile whose "keys" 0, 1, 2 are read straight from memory
-        const __nv_bfloat16 *sink_v = nullptr;
+        const bool given = r0 == 0 && p.mode == CSA_K0_GIVEN, copied_sink = r0 == 0 && p.mode == CSA_K0_COPY_FIRST;
         float edge[4] = {0.f, 0.f, 0.f, 0.f};
-        if (r0 > 0 || r1 < n || p.mode != CSA_K0_ZERO) {
-            const int row = g == 0 ? r0 - 1 : g == 1 ? r1 : 0;
+        if (r0 > 0 || r1 < n || given) {
             const __nv_bfloat16 *at = nullptr;
-            const bool cached = (g == 0 && r0 > 0) || (g == 1 && r1 < n) ||
-                                (g == 2 && r0 == 0 && p.mode == CSA_K0_COPY_FIRST);
-            if (cached) {
+            if ((g == 0 && r0 > 0) || (g == 1 && r1 < n)) {
+                const int row = g == 0 ? r0 - 1 : r1;
                 const int page = __ldg(p.table + (long long)b * p.M + row / p.S);
-                const long long place = ((long long)page * p.Hkv + hk) * p.S + row % p.S;
-                if (page >= 0 && page < p.P) {
-                    at = p.k + place * D;
-                    if (g == 2) sink_v = p.v + place * D;
-                } else {
+                if (page >= 0 && page < p.P)
+                    at = p.k + (((long long)page * p.Hkv + hk) * p.S + row % p.S) * D;
+                else
                     bad = true;
-                }
-            } else if (g == 2 && r0 == 0 && p.mode == CSA_K0_GIVEN) {
+            } else if (g == 2 && given) {
                 at = p.k0 + (long long)hk * D;
-                sink_v = p.v0 + (long long)hk * D;
             }
             const uint32_t *kg = reinterpret_cast<const uint32_t *>(at);
 #pragma unroll
             for (int i = 0; i < KS; ++i)
                 mma(edge, qa[i], at ? __ldg(kg + i * 8 + q) : 0u, at ? __ldg(kg + i * 8 + 4 + q) : 0u);
         }
-        sink_v = reinterpret_cast<const __nv_bfloat16 *>(
-            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(sink_v), 8));
         float prev[RH], behind[RH], m[RH], pm[RH], l[RH], w0[RH];
 #pragma unroll
         for (int h = 0; h < RH; ++h) {
@@ -370,7 +387,8 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
             const float sink_a = __shfl_sync(0xffffffffu, edge[2 * h], (lane & ~3) | 1);
             behind[h] = __shfl_sync(0xffffffffu, edge[2 * h + 1], lane & ~3) * p.qscale;
             prev[h] = (r0 > 0 ? before_a : sink_a) * p.qscale;
-            m[h] = prev[h];
+            // a copied sink has the first row's logit, which the first tile brings
+            m[h] = copied_sink ? -INFINITY : prev[h];
             pm[h] = 1.0f;  // 2^{prev - m}
             l[h] = w0[h] = 0.f;
         }
@@ -513,6 +531,13 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
                     for (int i = 0; i < NT; ++i) w[h][i][0] = w[h][i][1] = 0.f;
             }
             if (__any_sync(0xffffffffu, over)) raise(top);
+            if (j == tile && copied_sink) {
+#pragma unroll
+                for (int h = 0; h < RH; ++h) {
+                    prev[h] = __shfl_sync(0xffffffffu, s[0][2 * h], lane & ~3);
+                    pm[h] = ex2_approx(prev[h] - m[h]);
+                }
+            }
 
             // this tile's weights, and the share of its first interval that the row before gets
             float nw[RH][NT][2], to_before[RH];
@@ -557,6 +582,10 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
                 __syncwarp();  // every lane has read the tile before: its stage is free
                 ++used;
                 copy_next();
+            } else if (copied_sink) {  // its value is the first row's too
+#pragma unroll
+                for (int h = 0; h < RH; ++h)
+                    if (q == 0) nw[h][0][0] += to_before[h];
             } else if (r0 == 0) {
 #pragma unroll
                 for (int h = 0; h < RH; ++h) w0[h] = to_before[h];
@@ -601,7 +630,9 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
             t += __shfl_xor_sync(0xffffffffu, t, 2);
             sum[h] = bad ? NAN : t + w0[h];
         }
-        const long long slot = (worker * 2 + which) * p.HB;
+        // a worker's part that does not begin a segment is its first
+        const long long slot = (worker * 2 + (u0 < now.s0 ? 1 : 0)) * p.HB;
+        const uint32_t *sink_v = given ? reinterpret_cast<const uint32_t *>(p.v0 + (long long)hk * D) : nullptr;
 #pragma unroll
         for (int h = 0; h < RH; ++h) {
             const int row = g + 8 * h;
@@ -618,7 +649,7 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
                         c += o[i][3];
                     }
                     if (sink_v) {
-                        const uint32_t v2 = __ldg(reinterpret_cast<const uint32_t *>(sink_v) + i * 4 + q);
+                        const uint32_t v2 = __ldg(sink_v + i * 4 + q);
                         a = fmaf(w0[h], __uint_as_float(v2 << 16), a);
                         c = fmaf(w0[h], __uint_as_float(v2 & 0xffff0000u), c);
                     }
@@ -638,62 +669,63 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
             }
         }
         if (bad && lane == 0) atomicCAS(&g_paged_status, 0, CSA_ERR_INVALID_ARG);
-        which = 1;  // a later part of this worker begins at a sequence's first row
-
-        left_units -= last - tile;
-        tile = 0;
-        if (left_units > 0 && ++head == heads) {
-            head = 0;
-            do {
-                n = p.seqlens[++b];
-                tiles = tiles_of(n, KT, most);
-            } while (tiles == 0);
-        }
-    }
+    } while (next_part(now, u0, u1, p.seqlens, KT, most, heads));
 }
 
 // Joins the parts of one (sequence, cached head, block of query heads), for
 // one query head per block.  With M the largest m_c: o = sum 2^{m_c-M} o_c /
-// sum 2^{m_c-M} l_c, lse = (M + log2 sum) ln 2.  Each warp takes every 8th part
+// sum 2^{m_c-M} l_c, lse = (M + log2 sum) ln 2.  Each warp takes every kJoinWarps-th part
 // against its own maximum; the warps meet in shared memory.  by_worker: block
 // x is a worker, and joins what its range begins in the middle of if it is
 // the second worker there; otherwise block x is the segment itself.
-constexpr int kJoinWarps = 8;
+constexpr int kJoinWarps = 16;
 
 template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const PagedParams p, int chunks, int by_worker) {
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const PagedParams p, long long all, int by_worker) {
     using C = Cfg<D>;
     constexpr int V = D / 32;  // columns per lane
     __shared__ float s_o[kJoinWarps][D], s_m[kJoinWarps], s_l[kJoinWarps];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    __shared__ long long s_cut[kJoinWarps * 32 + 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = blockIdx.y;
     const int heads = p.Hkv * p.GB;
-    const long long most = (long long)p.M * p.S, U = p.cut[chunks] * heads, W = p.cut[chunks + 1];
-    if (U == 0) return;
-    int b, head;
-    long long before;
-    if (by_worker) {
-        const long long x = blockIdx.x;
-        if (x >= W || x == 0) return;
-        const long long u = x * U / W;
-        b = find_sequence(u, p.cut, chunks, p.seqlens, p.B, C::KT, most, heads, before);
-        head = (int)((u - before) / tiles_of(p.seqlens[b], C::KT, most));
-    } else {
-        b = blockIdx.x / heads;
-        head = blockIdx.x - b * heads;
-        const int per = (p.B + chunks - 1) / chunks;
-        before = p.cut[b / per] * heads;
-        for (int i = b / per * per; i < b; ++i) before += (long long)tiles_of(p.seqlens[i], C::KT, most) * heads;
-    }
-    const int tiles = tiles_of(p.seqlens[b], C::KT, most);
-    if (tiles == 0) return;
-    const long long s0 = before + (long long)head * tiles, s1 = s0 + tiles;
-    const long long c0 = ((s0 + 1) * W - 1) / U, c1 = (s1 * W - 1) / U;  // the first and last worker on it
-    if (c0 == c1) return;                                                  // written whole
-    if (by_worker && c0 + 1 != (long long)blockIdx.x) return;
-    const int hk = head / p.GB, hb = head - hk * p.GB;
-    if (row >= min(p.HB, p.G - hb * p.HB)) return;
-    const int first_slot = c0 * U / W < s0 ? 1 : 0;  // the first worker's range began earlier
+    const long long most = (long long)p.M * p.S;
+    // the cut again, from the lengths, while the parts are still being formed
+    form_cut(p.seqlens, p.B, C::KT, most, s_cut);
+    const long long U = s_cut[blockDim.x] * heads, W = workers_for(U, C::KT, all);
+    int b = 0, head = 0, hk = 0, hb = 0;
+    long long s0 = 0, c0 = 0, c1 = 0;
+    const bool mine = [&] {  // whether this block has parts to join
+        if (U == 0) return false;
+        long long before;
+        if (by_worker) {
+            const long long x = blockIdx.x;
+            if (x >= W || x == 0) return false;
+            const long long u = x * U / W;
+            b = find_sequence(u, s_cut, blockDim.x, p.seqlens, p.B, C::KT, most, heads, before);
+            head = (int)((u - before) / units_of(tiles_of(p.seqlens[b], C::KT, most)));
+        } else {
+            b = blockIdx.x / heads;
+            head = blockIdx.x - b * heads;
+            const int per = (p.B + blockDim.x - 1) / blockDim.x;
+            before = s_cut[b / per] * heads;
+            for (int i = b / per * per; i < b; ++i)
+                before += (long long)units_of(tiles_of(p.seqlens[i], C::KT, most)) * heads;
+        }
+        const int units = units_of(tiles_of(p.seqlens[b], C::KT, most));
+        if (units == 0) return false;
+        s0 = before + (long long)head * units;
+        // the first and last worker with tiles of it; one alone has written it whole
+        c0 = ((s0 + kPartCost + 1) * W - 1) / U;
+        c1 = ((s0 + units) * W - 1) / U;
+        if (c0 == c1 || (by_worker && ((s0 + 1) * W - 1) / U + 1 != (long long)blockIdx.x)) return false;
+        hk = head / p.GB;
+        hb = head - hk * p.GB;
+        return row < min(p.HB, p.G - hb * p.HB);
+    }();
+    const int first_slot = mine && c0 * U / W < s0 ? 1 : 0;  // the first worker's range began earlier
+    // every block waits: this kernel must not end before the one that forms the parts
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (!mine) return;
 
     auto slot = [&](long long c) { return ((c * 2 + (c == c0 ? first_slot : 0)) * p.HB + row); };
     float M = -INFINITY, L = 0.f, o[V];
@@ -701,19 +733,18 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const PagedParams
     for (int i = 0; i < V; ++i) o[i] = 0.f;
     // 32 parts at a time: their maxima and sums one per lane, then their columns
     for (long long base = c0 + warp; base <= c1; base += 32 * kJoinWarps) {
-        const long long mine = base + (long long)lane * kJoinWarps;
+        const long long part = base + (long long)lane * kJoinWarps;
         float m = -INFINITY, l = 0.f;
-        if (mine <= c1) {
-            const float2 ml = *reinterpret_cast<const float2 *>(p.part_ml + 2 * slot(mine));
+        if (part <= c1) {
+            const float2 ml = *reinterpret_cast<const float2 *>(p.part_ml + 2 * slot(part));
             m = ml.x;
             l = ml.y;
         }
         float top = m;
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-        const float M1 = fmaxf(M, top), f = ex2_approx(M - M1), mine_f = ex2_approx(m - M1);
-        float add = l * mine_f;
-        if (mine > c1) add = 0.f;
+        const float M1 = fmaxf(M, top), f = ex2_approx(M - M1), part_f = ex2_approx(m - M1);
+        float add = part <= c1 ? l * part_f : 0.f;
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) add += __shfl_xor_sync(0xffffffffu, add, off);
         L = L * f + add;
@@ -723,7 +754,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const PagedParams
         const int count = (int)min(32LL, (c1 - base) / kJoinWarps + 1);
 #pragma unroll 8
         for (int c = 0; c < count; ++c) {
-            const float fc = __shfl_sync(0xffffffffu, mine_f, c);
+            const float fc = __shfl_sync(0xffffffffu, part_f, c);
             const float *po = p.part_o + slot(base + (long long)c * kJoinWarps) * D;
 #pragma unroll
             for (int i = 0; i < V; i += 2) {
@@ -805,7 +836,7 @@ int launch(PagedParams &p, cudaStream_t stream) {
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, join_kernel<D>, p, C::Warps * 32, by_worker) != cudaSuccess) return CSA_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, join_kernel<D>, p, workers, by_worker) != cudaSuccess) return CSA_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
 }
 
@@ -821,7 +852,7 @@ long long csa_decode_paged_scratch_bytes(int B, int Hq, int Hkv, int d) {
     if (B < 0 || Hq < 0 || Hkv < 1 || Hq % Hkv != 0 || !(d == 64 || d == 128 || d == 256)) return -1;
     const int G = Hq / Hkv;
     const int GB = head_blocks(G), HB = GB ? (G + GB - 1) / GB : 0;
-    return 2 * workers(d) * HB * (d + 2) * (long long)sizeof(float) + (kMaxThreads + 2) * (long long)sizeof(long long);
+    return 2 * workers(d) * HB * (d + 2) * (long long)sizeof(float);
 }
 
 int csa_decode_paged_run(const void *q, const void *k_pages, const void *v_pages, const void *k0,
@@ -849,8 +880,7 @@ int csa_decode_paged_run(const void *q, const void *k_pages, const void *v_pages
     p.HB = (p.G + p.GB - 1) / p.GB;
     p.qscale = scale * kLog2e;
     p.mode = mode;
-    p.cut = static_cast<long long *>(scratch);
-    p.part_ml = reinterpret_cast<float *>(p.cut + kMaxThreads + 2);
+    p.part_ml = static_cast<float *>(scratch);
     p.part_o = p.part_ml + 2 * workers(d) * p.HB * 2;
     if (p.HB <= 8) {
         if (d == 64) return launch<64, 1>(p, stream);
