@@ -77,6 +77,10 @@ struct PagedParams {
     float *lse;
     float *part_o;    // [2 * workers][HB][D]: unnormalised sums of a part
     float *part_ml;   // [2 * workers][HB][2]: its maximum (log2 units) and weight sum
+    // the segments (heads of sequences) that several workers share: {segment or -1, first worker,
+    // last worker, the first one's slot}, by segment or by the worker that begins one
+    int4 *joins;      // [workers]
+    int by_segment;
     int B, Hq, Hkv, P, S, M;
     int G, GB, HB;    // query heads of a group, blocks of them, heads per block
     int R;            // rows per copy: divides S and the tile
@@ -255,11 +259,14 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
         if (p.lse)
             for (int h = threadIdx.x; h < p.Hq; h += blockDim.x)
                 p.lse[(long long)b * p.Hq + h] = n == 0 ? -INFINITY : NAN;
+        if (p.by_segment)
+            for (int h = threadIdx.x; h < heads; h += blockDim.x) p.joins[b * heads + h] = make_int4(-1, 0, 0, 0);
         if (threadIdx.x == 0 && n != 0) atomicCAS(&g_paged_status, 0, CSA_ERR_INVALID_ARG);
     }
 
     // workers are numbered across blocks first, so that few of them spread over all SMs
     const long long worker = (long long)warp * gridDim.x + blockIdx.x;
+    if (lane == 0 && !p.by_segment) p.joins[worker] = make_int4(-1, 0, 0, 0);
     if (worker >= in_use) return;
     const long long u0 = worker * U / in_use, u1 = (worker + 1) * U / in_use;
     if (u0 >= u1) return;
@@ -669,71 +676,31 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
             }
         }
         if (bad && lane == 0) atomicCAS(&g_paged_status, 0, CSA_ERR_INVALID_ARG);
+        if (r0 == 0 && lane == 0 && (p.by_segment || !whole)) {
+            const long long end = now.s0 + units_of(now.tiles);
+            const int segment = b * heads + now.head;
+            p.joins[p.by_segment ? segment : worker] =
+                make_int4(whole ? -1 : segment, (int)worker, (int)((end * in_use - 1) / U), u0 < now.s0 ? 1 : 0);
+        }
     } while (next_part(now, u0, u1, p.seqlens, KT, most, heads));
 }
 
-// Joins the parts of one (sequence, cached head, block of query heads), for
-// one query head per block.  With M the largest m_c: o = sum 2^{m_c-M} o_c /
-// sum 2^{m_c-M} l_c, lse = (M + log2 sum) ln 2.  Each warp takes every kJoinWarps-th part
-// against its own maximum; the warps meet in shared memory.  by_worker: block
-// x is a worker, and joins what its range begins in the middle of if it is
-// the second worker there; otherwise block x is the segment itself.
-constexpr int kJoinWarps = 16;
+// Joins the parts of a segment (a cached head of a sequence and a block of its
+// query heads) that several workers share.  With M the largest m_c:
+// o = sum 2^{m_c-M} o_c / sum 2^{m_c-M} l_c, lse = (M + log2 sum) ln 2.
+// The parts are the first worker's and the first ones of the workers behind it.
+constexpr int kJoinWarps = 8, kJoinWarpsMost = 32;
 
+// Adds the parts first, first + step, ... of one query head into (M, L, o),
+// `mine` columns per lane.
 template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const PagedParams p, long long all, int by_worker) {
-    using C = Cfg<D>;
-    constexpr int V = D / 32;  // columns per lane
-    __shared__ float s_o[kJoinWarps][D], s_m[kJoinWarps], s_l[kJoinWarps];
-    __shared__ long long s_cut[kJoinWarps * 32 + 1];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = blockIdx.y;
-    const int heads = p.Hkv * p.GB;
-    const long long most = (long long)p.M * p.S;
-    // the cut again, from the lengths, while the parts are still being formed
-    form_cut(p.seqlens, p.B, C::KT, most, s_cut);
-    const long long U = s_cut[blockDim.x] * heads, W = workers_for(U, C::KT, all);
-    int b = 0, head = 0, hk = 0, hb = 0;
-    long long s0 = 0, c0 = 0, c1 = 0;
-    const bool mine = [&] {  // whether this block has parts to join
-        if (U == 0) return false;
-        long long before;
-        if (by_worker) {
-            const long long x = blockIdx.x;
-            if (x >= W || x == 0) return false;
-            const long long u = x * U / W;
-            b = find_sequence(u, s_cut, blockDim.x, p.seqlens, p.B, C::KT, most, heads, before);
-            head = (int)((u - before) / units_of(tiles_of(p.seqlens[b], C::KT, most)));
-        } else {
-            b = blockIdx.x / heads;
-            head = blockIdx.x - b * heads;
-            const int per = (p.B + blockDim.x - 1) / blockDim.x;
-            before = s_cut[b / per] * heads;
-            for (int i = b / per * per; i < b; ++i)
-                before += (long long)units_of(tiles_of(p.seqlens[i], C::KT, most)) * heads;
-        }
-        const int units = units_of(tiles_of(p.seqlens[b], C::KT, most));
-        if (units == 0) return false;
-        s0 = before + (long long)head * units;
-        // the first and last worker with tiles of it; one alone has written it whole
-        c0 = ((s0 + kPartCost + 1) * W - 1) / U;
-        c1 = ((s0 + units) * W - 1) / U;
-        if (c0 == c1 || (by_worker && ((s0 + 1) * W - 1) / U + 1 != (long long)blockIdx.x)) return false;
-        hk = head / p.GB;
-        hb = head - hk * p.GB;
-        return row < min(p.HB, p.G - hb * p.HB);
-    }();
-    const int first_slot = mine && c0 * U / W < s0 ? 1 : 0;  // the first worker's range began earlier
-    // every block waits: this kernel must not end before the one that forms the parts
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (!mine) return;
-
-    auto slot = [&](long long c) { return ((c * 2 + (c == c0 ? first_slot : 0)) * p.HB + row); };
-    float M = -INFINITY, L = 0.f, o[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) o[i] = 0.f;
+__device__ __forceinline__ void add_parts(const PagedParams &p, int c0, int c1, int first_slot, int row,
+                                          int first, int step, float &M, float &L, float (&o)[D / 32]) {
+    const int lane = threadIdx.x & 31;
+    auto slot = [&](int c) { return ((long long)c * 2 + (c == c0 ? first_slot : 0)) * p.HB + row; };
     // 32 parts at a time: their maxima and sums one per lane, then their columns
-    for (long long base = c0 + warp; base <= c1; base += 32 * kJoinWarps) {
-        const long long part = base + (long long)lane * kJoinWarps;
+    for (int base = first; base <= c1; base += 32 * step) {
+        const int part = base + lane * step;
         float m = -INFINITY, l = 0.f;
         if (part <= c1) {
             const float2 ml = *reinterpret_cast<const float2 *>(p.part_ml + 2 * slot(part));
@@ -750,22 +717,62 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const PagedParams
         L = L * f + add;
         M = M1;
 #pragma unroll
-        for (int i = 0; i < V; ++i) o[i] *= f;
-        const int count = (int)min(32LL, (c1 - base) / kJoinWarps + 1);
+        for (int i = 0; i < D / 32; ++i) o[i] *= f;
+        const int count = min(32, (c1 - base) / step + 1);
 #pragma unroll 8
         for (int c = 0; c < count; ++c) {
             const float fc = __shfl_sync(0xffffffffu, part_f, c);
-            const float *po = p.part_o + slot(base + (long long)c * kJoinWarps) * D;
+            const float *po = p.part_o + slot(base + c * step) * D;
 #pragma unroll
-            for (int i = 0; i < V; i += 2) {
+            for (int i = 0; i < D / 32; i += 2) {
                 const float2 v = *reinterpret_cast<const float2 *>(po + 32 * i + 2 * lane);
                 o[i] = fmaf(fc, v.x, o[i]);
                 o[i + 1] = fmaf(fc, v.y, o[i + 1]);
             }
         }
     }
+}
+
+// By segment (few of them, so many parts): a block per segment and query head,
+// its warps taking every gridDim-th part each.  By worker: a block per worker,
+// for the segment that begins there, a warp per query head (few parts).
+template <int D>
+__global__ void join_kernel(const PagedParams p) {
+    __shared__ float s_o[kJoinWarpsMost][D], s_m[kJoinWarpsMost], s_l[kJoinWarpsMost];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int heads = p.Hkv * p.GB;
+    // every block waits: this kernel must not end before the one that forms the parts
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int4 seg = p.joins[blockIdx.x];
+    // none; or left over, where a wait ran out and the parts are undefined anyway
+    if (seg.x < 0 || seg.x >= p.B * heads || seg.y < 0 || seg.z < seg.y || seg.z >= Cfg<D>::Workers) return;
+    const int b = seg.x / heads, head = seg.x - b * heads, c0 = seg.y;
+    const int hk = head / p.GB, hb = head - hk * p.GB, rows = min(p.HB, p.G - hb * p.HB);
+    const long long out0 = (long long)b * p.Hq + hk * p.G + hb * p.HB;
+    float o[D / 32];
+    if (!p.by_segment) {
+        for (int row = warp; row < rows; row += warps) {
+            float M = -INFINITY, L = 0.f;
 #pragma unroll
-    for (int i = 0; i < V; i += 2)
+            for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
+            add_parts<D>(p, c0, seg.z, seg.w, row, c0, 1, M, L, o);
+            const float inv = 1.0f / L;
+#pragma unroll
+            for (int i = 0; i < D / 32; i += 2)
+                *reinterpret_cast<uint32_t *>(p.out + (out0 + row) * D + 32 * i + 2 * lane) =
+                    pack_bf16x2(o[i] * inv, o[i + 1] * inv);
+            if (lane == 0 && p.lse) p.lse[out0 + row] = (M + log2f(L)) * kLn2;
+        }
+        return;
+    }
+    const int row = blockIdx.y;
+    if (row >= rows) return;
+    float M = -INFINITY, L = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
+    add_parts<D>(p, c0, seg.z, seg.w, row, c0 + warp, warps, M, L, o);
+#pragma unroll
+    for (int i = 0; i < D / 32; i += 2)
         *reinterpret_cast<float2 *>(&s_o[warp][32 * i + 2 * lane]) = make_float2(o[i], o[i + 1]);
     if (lane == 0) {
         s_m[warp] = M;
@@ -773,23 +780,16 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const PagedParams
     }
     __syncthreads();
     float top = s_m[0];
-#pragma unroll
-    for (int i = 1; i < kJoinWarps; ++i) top = fmaxf(top, s_m[i]);
-    float f[kJoinWarps], total = 0.f;
-#pragma unroll
-    for (int i = 0; i < kJoinWarps; ++i) {
-        f[i] = ex2_approx(s_m[i] - top);  // 0 for a warp without parts
-        total = fmaf(f[i], s_l[i], total);
-    }
-    const long long oh = (long long)b * p.Hq + hk * p.G + hb * p.HB + row;
+    for (int i = 1; i < warps; ++i) top = fmaxf(top, s_m[i]);
+    float total = 0.f;
+    for (int i = 0; i < warps; ++i) total = fmaf(ex2_approx(s_m[i] - top), s_l[i], total);  // 0 without parts
     const float inv = 1.0f / total;
-    for (int col = threadIdx.x; col < D; col += kJoinWarps * 32) {
+    for (int col = threadIdx.x; col < D; col += blockDim.x) {
         float v = 0.f;
-#pragma unroll
-        for (int i = 0; i < kJoinWarps; ++i) v = fmaf(f[i], s_o[i][col], v);
-        p.out[oh * D + col] = __float2bfloat16_rn(v * inv);
+        for (int i = 0; i < warps; ++i) v = fmaf(ex2_approx(s_m[i] - top), s_o[i][col], v);
+        p.out[(out0 + row) * D + col] = __float2bfloat16_rn(v * inv);
     }
-    if (threadIdx.x == 0 && p.lse) p.lse[oh] = (top + log2f(total)) * kLn2;
+    if (threadIdx.x == 0 && p.lse) p.lse[out0 + row] = (top + log2f(total)) * kLn2;
 }
 
 // [P * Hkv * S, D] bf16 as {64, rows, D / 64}, boxes of R rows.
@@ -824,19 +824,21 @@ int launch(PagedParams &p, cudaStream_t stream) {
     auto kern = paged_kernel<D, RH>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::Smem) != cudaSuccess)
         return CSA_ERR_CUDA;
-    kern<<<grid, C::Warps * 32, C::Smem, stream>>>(p, map_k, map_v);
     const long long segments = (long long)p.B * heads, workers = (long long)grid * C::Warps;
-    const int by_worker = segments > workers;
+    p.by_segment = segments <= kGrid;
+    kern<<<grid, C::Warps * 32, C::Smem, stream>>>(p, map_k, map_v);
+    // parts of a segment, at most about
+    const long long parts = workers / segments;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(by_worker ? workers : segments), (unsigned)p.HB);
-    cfg.blockDim = dim3(kJoinWarps * 32);
+    cfg.gridDim = p.by_segment ? dim3((unsigned)segments, (unsigned)p.HB) : dim3((unsigned)workers);
+    cfg.blockDim = dim3(32 * (p.by_segment && parts > 64 ? kJoinWarpsMost : kJoinWarps));
     cfg.stream = stream;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, join_kernel<D>, p, workers, by_worker) != cudaSuccess) return CSA_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, join_kernel<D>, p) != cudaSuccess) return CSA_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
 }
 
@@ -852,7 +854,7 @@ long long csa_decode_paged_scratch_bytes(int B, int Hq, int Hkv, int d) {
     if (B < 0 || Hq < 0 || Hkv < 1 || Hq % Hkv != 0 || !(d == 64 || d == 128 || d == 256)) return -1;
     const int G = Hq / Hkv;
     const int GB = head_blocks(G), HB = GB ? (G + GB - 1) / GB : 0;
-    return 2 * workers(d) * HB * (d + 2) * (long long)sizeof(float);
+    return workers(d) * (2 * HB * (d + 2) * (long long)sizeof(float) + (long long)sizeof(int4));
 }
 
 int csa_decode_paged_run(const void *q, const void *k_pages, const void *v_pages, const void *k0,
@@ -880,7 +882,8 @@ int csa_decode_paged_run(const void *q, const void *k_pages, const void *v_pages
     p.HB = (p.G + p.GB - 1) / p.GB;
     p.qscale = scale * kLog2e;
     p.mode = mode;
-    p.part_ml = static_cast<float *>(scratch);
+    p.joins = static_cast<int4 *>(scratch);
+    p.part_ml = reinterpret_cast<float *>(p.joins + workers(d));
     p.part_o = p.part_ml + 2 * workers(d) * p.HB * 2;
     if (p.HB <= 8) {
         if (d == 64) return launch<64, 1>(p, stream);
