@@ -51,9 +51,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
 constexpr int kGrid = 152;        // one block per SM
 constexpr int kStages = 3;        // tiles in a worker's ring
-constexpr int kMinRows = 64;      // rows per worker that a split leaves, at least
-// What beginning and ending a part costs, in tiles: a range of many short
-// sequences takes as long as one of a long sequence.
+constexpr int kFew = 4;           // tiles per worker up to which latency counts, not balance
+// What beginning and ending a part costs, in tiles: with it a range of many
+// short sequences takes as long as one of a long sequence.
 constexpr int kPartCost = 3;
 constexpr float kRaise = 16.0f;   // log2 units a logit may pass the running maximum by
 
@@ -61,13 +61,13 @@ __device__ int g_paged_status;  // sticky status word of this file's kernels
 
 template <int D>
 struct Cfg {
-    static constexpr int KT = D == 64 ? 32 : 16;       // rows per tile: 8 KiB (16 at d = 256)
-    static constexpr int Warps = D == 256 ? 4 : 8;     // workers per block
+    static constexpr int KT = 16;                      // rows per tile
+    static constexpr int Warps = 1024 / D;             // workers per block: 16, 8, 4
     static constexpr int Tile = KT * D * 2;            // bytes of a tile of keys, or of values
     static constexpr int Stage = 2 * Tile;
     static constexpr int Smem = Warps * kStages * Stage + 1024;  // + alignment
     static constexpr int Workers = Warps * kGrid;
-    static_assert(Smem <= 227 * 1024 - 4096, "one block per SM");
+    static_assert(Smem <= 227 * 1024 - 6144, "one block per SM");
 };
 
 struct PagedParams {
@@ -81,6 +81,7 @@ struct PagedParams {
     // last worker, the first one's slot}, by segment or by the worker that begins one
     int4 *joins;      // [workers]
     int by_segment;
+    unsigned long long s_inv;  // 2^64 / S rounded up: row / S is the high word of row * s_inv
     int B, Hq, Hkv, P, S, M;
     int G, GB, HB;    // query heads of a group, blocks of them, heads per block
     int R;            // rows per copy: divides S and the tile
@@ -136,58 +137,83 @@ __device__ __forceinline__ int tiles_of(int n, int KT, long long most) {
     return n < 0 || n > most ? 0 : (int)(((long long)n + KT - 1) / KT);
 }
 
-// What one cached head of a sequence counts for in the cut: its tiles and the
-// cost of a part.
-__device__ __forceinline__ int units_of(int tiles) { return tiles > 0 ? tiles + kPartCost : 0; }
+// a / b for a >= 0, b > 0, mostly of 32 bits.
+__device__ __forceinline__ long long quot(long long a, long long b) {
+    return (a | b) >> 32 ? a / b : (long long)((unsigned)a / (unsigned)b);
+}
 
-// Units (per head) of the sequences before each thread's chunk of sequences, in
-// cut[0 .. blockDim.x], the last entry the total.  Whole block.
-__device__ void form_cut(const int *seqlens, int B, int KT, long long most, long long *cut) {
+// The cut of the work into ranges.  A unit is a tile of one cached head or, in
+// a large batch, a share of a part's cost: each (sequence, head) then counts
+// for its tiles and `cost` units in front of them.
+struct Cut {
+    long long U, in_use;  // units of all heads, workers in use
+    int cost;
+    __device__ __forceinline__ int units(int tiles) const { return tiles > 0 ? tiles + cost : 0; }
+    // the worker that has unit u
+    __device__ __forceinline__ long long worker_of(long long u) const { return quot((u + 1) * in_use - 1, U); }
+};
+
+// at[0 .. blockDim.x] gets the units (per head) of the sequences before each
+// thread's chunk of sequences, the last entry the total.  Whole block.
+__device__ Cut form_cut(const int *seqlens, int B, int KT, long long most, int heads, long long all, long long *at) {
     const int tid = threadIdx.x, per = (B + blockDim.x - 1) / blockDim.x;
     const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
-    long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += units_of(tiles_of(seqlens[b], KT, most));
-    __shared__ long long sums[32];
-    long long s = mine;
+    long long tiles = 0;
+    int some = 0;  // sequences with tiles
+    for (int b = b0; b < b1; ++b) {
+        const int t = tiles_of(seqlens[b], KT, most);
+        tiles += t;
+        some += t > 0;
+    }
+    __shared__ long long tile_sums[32];
+    __shared__ int some_sums[32];
+    long long s = tiles;
+    int c = some;
     const int lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
         const long long o = __shfl_up_sync(0xffffffffu, s, off);
-        if (lane >= off) s += o;
+        const int oc = __shfl_up_sync(0xffffffffu, c, off);
+        if (lane >= off) {
+            s += o;
+            c += oc;
+        }
     }
-    if (lane == 31) sums[warp] = s;
+    if (lane == 31) {
+        tile_sums[warp] = s;
+        some_sums[warp] = c;
+    }
     __syncthreads();
-    long long before = 0;
-    for (int w = 0; w < warps; ++w) before += w < warp ? sums[w] : 0;
-    cut[tid] = before + s - mine;
-    if (tid == (int)blockDim.x - 1) cut[blockDim.x] = before + s;
+    long long before = 0, total = 0;
+    int some_before = 0, some_total = 0;
+    for (int w = 0; w < warps; ++w) {
+        if (w < warp) {
+            before += tile_sums[w];
+            some_before += some_sums[w];
+        }
+        total += tile_sums[w];
+        some_total += some_sums[w];
+    }
+    Cut cut;
+    cut.cost = total * heads > kFew * all ? kPartCost : 0;
+    at[tid] = before + s - tiles + (long long)cut.cost * (some_before + c - some);
+    if (tid == (int)blockDim.x - 1) at[blockDim.x] = total + (long long)cut.cost * some_total;
     __syncthreads();
+    cut.U = at[blockDim.x] * heads;
+    cut.in_use = cut.U < all ? cut.U : all;  // few tiles: a worker each
+    return cut;
 }
 
-// Workers in use for U units: at least kMinRows rows each.
-__device__ __forceinline__ long long workers_for(long long U, int KT, long long all) {
-    const long long w = U / (kMinRows / KT);
-    return w < 1 ? 1 : w > all ? all : w;
-}
-
-// The sequence that holds unit u (of units x heads), and the units before it.
-// cut has `chunks` + 1 entries.
-__device__ __forceinline__ int find_sequence(long long u, const long long *cut, int chunks,
-                                             const int *seqlens, int B, int KT, long long most,
-                                             int heads, long long &before) {
-    int lo = 0, hi = chunks - 1;  // the last chunk that begins at or before u
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (cut[mid] * heads <= u)
-            lo = mid;
-        else
-            hi = mid - 1;
-    }
-    // chunks without units begin where the next one does: the last one is taken
-    int b = lo * ((B + chunks - 1) / chunks);
-    before = cut[lo] * heads;
+// The sequence that holds unit u, and the units before it.  Whole warp.
+__device__ __forceinline__ int find_sequence(long long u, const Cut &cut, const long long *at, const int *seqlens,
+                                             int B, int KT, long long most, int heads, long long &before) {
+    // the last chunk that begins at or before u (chunks without units begin where the next one does)
+    int begun = 0;
+    for (int i = threadIdx.x & 31; i < (int)blockDim.x; i += 32) begun += __popc(__ballot_sync(0xffffffffu, at[i] * heads <= u));
+    int b = (begun - 1) * ((B + blockDim.x - 1) / blockDim.x);
+    before = at[begun - 1] * heads;
     while (true) {
-        const long long mine = (long long)units_of(tiles_of(seqlens[b], KT, most)) * heads;
+        const long long mine = (long long)cut.units(tiles_of(seqlens[b], KT, most)) * heads;
         if (u < before + mine) return b;
         before += mine;
         ++b;
@@ -201,16 +227,16 @@ struct Part {
     long long s0;  // the segment's first unit
 };
 
-__device__ __forceinline__ void clip(Part &t, long long u0, long long u1) {
-    t.tile = (int)max(0LL, u0 - t.s0 - kPartCost);
-    t.last = (int)min((long long)t.tiles, max(0LL, u1 - t.s0 - kPartCost));
+__device__ __forceinline__ void clip(Part &t, const Cut &cut, long long u0, long long u1) {
+    t.tile = (int)max(0LL, u0 - t.s0 - cut.cost);
+    t.last = (int)min((long long)t.tiles, max(0LL, u1 - t.s0 - cut.cost));
 }
 
 // The next part with tiles; false behind the last.
-__device__ __forceinline__ bool next_part(Part &t, long long u0, long long u1, const int *seqlens, int KT,
-                                          long long most, int heads) {
+__device__ __forceinline__ bool next_part(Part &t, const Cut &cut, long long u0, long long u1, const int *seqlens,
+                                          int KT, long long most, int heads) {
     do {
-        t.s0 += units_of(t.tiles);
+        t.s0 += cut.units(t.tiles);
         if (t.s0 >= u1) return false;
         if (++t.head == heads) {
             t.head = 0;
@@ -219,7 +245,7 @@ __device__ __forceinline__ bool next_part(Part &t, long long u0, long long u1, c
                 t.tiles = tiles_of(t.n, KT, most);
             } while (t.tiles == 0);
         }
-        clip(t, u0, u1);
+        clip(t, cut, u0, u1);
     } while (t.tile >= t.last);
     return true;
 }
@@ -246,9 +272,7 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
     if (threadIdx.x == 0) s_abort = 0;
     // the join's blocks may take their places as this kernel's blocks end
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    form_cut(p.seqlens, p.B, KT, most, s_cut);
-    const long long U = s_cut[blockDim.x] * heads;
-    const long long in_use = workers_for(U, KT, (long long)C::Warps * gridDim.x);
+    const Cut cut = form_cut(p.seqlens, p.B, KT, most, heads, (long long)C::Warps * gridDim.x, s_cut);
     // sequences without rows, and lengths out of range
     for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
         const int n = p.seqlens[b];
@@ -267,19 +291,21 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
     // workers are numbered across blocks first, so that few of them spread over all SMs
     const long long worker = (long long)warp * gridDim.x + blockIdx.x;
     if (lane == 0 && !p.by_segment) p.joins[worker] = make_int4(-1, 0, 0, 0);
-    if (worker >= in_use) return;
-    const long long u0 = worker * U / in_use, u1 = (worker + 1) * U / in_use;
+    if (worker >= cut.in_use) return;
+    const long long u0 = quot(worker * cut.U, cut.in_use), u1 = quot((worker + 1) * cut.U, cut.in_use);
     if (u0 >= u1) return;
 
     // ---- position in the range: what is copied next, and what is consumed
     Part now;
-    now.b = find_sequence(u0, s_cut, blockDim.x, p.seqlens, p.B, KT, most, heads, now.s0);
+    now.b = find_sequence(u0, cut, s_cut, p.seqlens, p.B, KT, most, heads, now.s0);
     now.n = p.seqlens[now.b];
     now.tiles = tiles_of(now.n, KT, most);
-    now.head = (int)((u0 - now.s0) / units_of(now.tiles));  // hk * GB + block of query heads
-    now.s0 += (long long)now.head * units_of(now.tiles);
-    clip(now, u0, u1);
-    if (now.tile >= now.last && !next_part(now, u0, u1, p.seqlens, KT, most, heads)) return;
+    now.head = (int)quot(u0 - now.s0, cut.units(now.tiles));  // hk * GB + block of query heads
+    now.s0 += (long long)now.head * cut.units(now.tiles);
+    clip(now, cut, u0, u1);
+    if (now.tile >= now.last && !next_part(now, cut, u0, u1, p.seqlens, KT, most, heads)) return;
+    auto page_index = [&](int row) { return (int)__umul64hi((unsigned long long)row, p.s_inv); };  // row / S
+    auto cached_head = [&](int head) { return p.GB == 1 ? head : head / p.GB; };
 
     const uint32_t ring = (smem_u32(raw) + 1023) / 1024 * 1024 + warp * (kStages * C::Stage);
     const int R = p.R, pieces = KT / R;
@@ -297,7 +323,7 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
             held_b = ahead.b;
             held_at = first & ~31;
             const long long row = (long long)(held_at + lane) * R;
-            held = row < ahead.n ? __ldg(p.table + (long long)ahead.b * p.M + (int)row / p.S) : 0;
+            held = row < ahead.n ? __ldg(p.table + (long long)ahead.b * p.M + page_index((int)row)) : 0;
         }
         const uint32_t bar = smem_u32(&bars[warp][copy_stage]), at = ring + copy_stage * C::Stage;
         int bytes = 0, place[KT / 8];
@@ -309,7 +335,7 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
                 const int page = __shfl_sync(0xffffffffu, held, (first + i) & 31);
                 if (row < ahead.n) {
                     if (page >= 0 && page < p.P) {
-                        place[i] = (page * p.Hkv + ahead.head / p.GB) * p.S + row % p.S;
+                        place[i] = (page * p.Hkv + cached_head(ahead.head)) * p.S + row - page_index(row) * p.S;
                         bytes += 2 * R * D * 2;
                     } else {
                         bad_stages |= 1u << copy_stage;
@@ -328,7 +354,7 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
         }
         copy_stage = copy_stage + 1 == kStages ? 0 : copy_stage + 1;
         ++copied;
-        if (++ahead.tile == ahead.last) more = next_part(ahead, u0, u1, p.seqlens, KT, most, heads);
+        if (++ahead.tile == ahead.last) more = next_part(ahead, cut, u0, u1, p.seqlens, KT, most, heads);
     };
     for (int s = 0; s < kStages; ++s) copy_next();
 
@@ -348,7 +374,7 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
     uint32_t parity = 0;
     do {
         const int b = now.b, n = now.n, tile = now.tile, last = now.last;
-        const int hk = now.head / p.GB, hb = now.head - hk * p.GB;
+        const int hk = cached_head(now.head), hb = now.head - hk * p.GB;
         const int rows_h = min(p.HB, p.G - hb * p.HB);  // query heads of this block
         const int q0 = hk * p.G + hb * p.HB;            // the first of them
         const int r0 = tile * KT, r1 = min(n, last * KT);
@@ -374,9 +400,9 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
             const __nv_bfloat16 *at = nullptr;
             if ((g == 0 && r0 > 0) || (g == 1 && r1 < n)) {
                 const int row = g == 0 ? r0 - 1 : r1;
-                const int page = __ldg(p.table + (long long)b * p.M + row / p.S);
+                const int index = page_index(row), page = __ldg(p.table + (long long)b * p.M + index);
                 if (page >= 0 && page < p.P)
-                    at = p.k + (((long long)page * p.Hkv + hk) * p.S + row % p.S) * D;
+                    at = p.k + (((long long)page * p.Hkv + hk) * p.S + row - index * p.S) * D;
                 else
                     bad = true;
             } else if (g == 2 && given) {
@@ -504,17 +530,19 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
                 __syncwarp();
             }
             // logits
-            float s[NT][4];
+            float s[NT][4], s2[NT][4];  // two sums of every other product: the chain of dependent ones is half as long
 #pragma unroll
-            for (int i = 0; i < NT; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[i][e] = s2[i][e] = 0.f;
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
                 for (int i = 0; i < NT / 2; ++i) {
                     uint32_t kb[4];
                     ldsm(k_at + k_row[i] + chunk_at(2 * ks + k_chunk), kb);
-                    mma(s[2 * i], qa[ks], kb[0], kb[1]);
-                    mma(s[2 * i + 1], qa[ks], kb[2], kb[3]);
+                    mma(ks & 1 ? s2[2 * i] : s[2 * i], qa[ks], kb[0], kb[1]);
+                    mma(ks & 1 ? s2[2 * i + 1] : s[2 * i + 1], qa[ks], kb[2], kb[3]);
                 }
             float top[RH];
             bool over = false;
@@ -525,7 +553,7 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
                 for (int i = 0; i < NT; ++i) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        s[i][2 * h + e] *= p.qscale;
+                        s[i][2 * h + e] = (s[i][2 * h + e] + s2[i][2 * h + e]) * p.qscale;
                         if (8 * i + 2 * q + e < own) top[h] = fmaxf(top[h], s[i][2 * h + e]);
                     }
                 }
@@ -677,12 +705,12 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
         }
         if (bad && lane == 0) atomicCAS(&g_paged_status, 0, CSA_ERR_INVALID_ARG);
         if (r0 == 0 && lane == 0 && (p.by_segment || !whole)) {
-            const long long end = now.s0 + units_of(now.tiles);
+            const long long end = now.s0 + cut.units(now.tiles);
             const int segment = b * heads + now.head;
             p.joins[p.by_segment ? segment : worker] =
-                make_int4(whole ? -1 : segment, (int)worker, (int)((end * in_use - 1) / U), u0 < now.s0 ? 1 : 0);
+                make_int4(whole ? -1 : segment, (int)worker, (int)cut.worker_of(end - 1), u0 < now.s0 ? 1 : 0);
         }
-    } while (next_part(now, u0, u1, p.seqlens, KT, most, heads));
+    } while (next_part(now, cut, u0, u1, p.seqlens, KT, most, heads));
 }
 
 // Joins the parts of a segment (a cached head of a sequence and a block of its
@@ -819,8 +847,9 @@ int launch(PagedParams &p, cudaStream_t stream) {
         return CSA_ERR_CUDA;
     const int heads = p.Hkv * p.GB;
     // blocks that the largest possible lengths can keep busy
-    const long long most = (long long)p.B * heads * (((long long)p.M * p.S + kMinRows - 1) / kMinRows);
+    const long long most = (long long)p.B * heads * (((long long)p.M * p.S + C::KT - 1) / C::KT);
     const int grid = (int)(most < kGrid ? (most < 1 ? 1 : most) : kGrid);
+    p.s_inv = ~0ull / p.S + 1;
     auto kern = paged_kernel<D, RH>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::Smem) != cudaSuccess)
         return CSA_ERR_CUDA;
@@ -845,8 +874,7 @@ int launch(PagedParams &p, cudaStream_t stream) {
 // Blocks of the query heads of a group, at most 16 each, as equal as can be.
 int head_blocks(int G) { return (G + 15) / 16; }
 
-long long workers(int d) { return d == 256 ? Cfg<256>::Workers : Cfg<128>::Workers; }
-static_assert(Cfg<64>::Workers == Cfg<128>::Workers, "");
+long long workers(int d) { return d == 256 ? Cfg<256>::Workers : d == 128 ? Cfg<128>::Workers : Cfg<64>::Workers; }
 
 }  // namespace
 
