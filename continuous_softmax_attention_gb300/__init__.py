@@ -38,7 +38,6 @@ from ._paged import (  # noqa: F401
     cache_fork,
     cache_free,
     cache_reserve,
-    cache_workspace_bytes,
     decode_paged,
     decode_paged_workspace_bytes,
     rope,
@@ -56,5 +55,5 @@ __all__ = [
     "status_string",
     "decode_paged", "decode_paged_workspace_bytes", "RopeAxes", "rope", "rope_backward",
     "cache_append", "cache_reserve", "cache_free", "cache_fork", "cache_compact",
-    "cache_copy_pages", "cache_workspace_bytes",
+    "cache_copy_pages",
 ]

@@ -78,10 +78,10 @@ def load():
                        ("csa_rope_f32", [p] * 11 + [i] * 6 + [p]),
                        ("csa_cache_append", [p] * 16 + [i] * 8 + [p]),
                        ("csa_cache_append_f32", [p] * 16 + [i] * 8 + [p]),
-                       ("csa_cache_reserve", [p] * 6 + [ll] + [i] * 4 + [p]),
+                       ("csa_cache_reserve", [p] * 5 + [i] * 4 + [p]),
                        ("csa_cache_free", [p] * 4 + [i] * 5 + [p]),
-                       ("csa_cache_fork", [p] * 5 + [i] + [p] * 4 + [ll] + [i] * 4 + [p]),
-                       ("csa_cache_compact", [p] * 7 + [ll] + [i] * 4 + [p]),
+                       ("csa_cache_fork", [p] * 5 + [i] + [p] * 3 + [i] * 4 + [p]),
+                       ("csa_cache_compact", [p] * 6 + [i] * 4 + [p]),
                        ("csa_cache_copy_pages", [p, p, ll, i, i, p, p, i, p, p])):
         fn = getattr(lib, name)
         fn.argtypes = args
@@ -92,8 +92,6 @@ def load():
         getattr(lib, name).restype = ctypes.c_longlong
     lib.csa_decode_range_workspace_bytes.argtypes = [i, i, i, i, i]
     lib.csa_decode_range_workspace_bytes.restype = ctypes.c_longlong
-    lib.csa_cache_workspace_bytes.argtypes = [i, i, i]
-    lib.csa_cache_workspace_bytes.restype = ctypes.c_longlong
     lib.csa_status_string.argtypes = [i]
     lib.csa_status_string.restype = ctypes.c_char_p
     _lib = lib

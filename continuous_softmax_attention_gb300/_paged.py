@@ -319,15 +319,6 @@ def cache_append(k, v, k_pages, v_pages, block_table, seqlens, *, counts=None, r
 
 
 # ------------------------------------------------------------------------ pages
-def cache_workspace_bytes(B: int, P: int, n: int = 0) -> int:
-    """Bytes of workspace cache_reserve, cache_fork (n pairs) and cache_compact
-    need (host-side, no device needed)."""
-    r = int(load().csa_cache_workspace_bytes(int(B), int(P), int(n)))
-    if r < 0:
-        raise CsaError(CSA_ERR_UNSUPPORTED, "csa_cache_workspace_bytes")
-    return r
-
-
 def _books(page_refs, block_table, seqlens):
     dev = page_refs.device
     if page_refs.dim() != 1 or block_table.dim() != 2:
@@ -339,8 +330,7 @@ def _books(page_refs, block_table, seqlens):
     return dev, P, B, M
 
 
-def cache_reserve(page_refs, block_table, seqlens, page_size: int, counts, *, shortfall=None,
-                  workspace=None, stream=None):
+def cache_reserve(page_refs, block_table, seqlens, page_size: int, counts, *, shortfall=None, stream=None):
     """Room for counts[b] more tokens of every sequence: takes the missing pages
     (lowest-numbered free ones first), enters them into the table and adds
     counts to seqlens.  Returns shortfall (int32 [1], on the device): 0 if it
@@ -353,10 +343,8 @@ def cache_reserve(page_refs, block_table, seqlens, page_size: int, counts, *, sh
     dev, P, B, M = _books(page_refs, block_table, seqlens)
     _need(counts, "counts", torch.int32, (B,), dev)
     shortfall = _out(shortfall, "shortfall", torch.int32, (1,), dev)
-    workspace = _workspace(workspace, cache_workspace_bytes(B, P), dev)
-    _check(load().csa_cache_reserve(_at(page_refs), _at(block_table), _at(seqlens), _at(counts),
-                                    _at(shortfall), _at(workspace), workspace.nbytes, B, P,
-                                    int(page_size), M, _raw_stream(dev.index)), "csa_cache_reserve")
+    _check(load().csa_cache_reserve(page_refs.data_ptr(), block_table.data_ptr(), seqlens.data_ptr(), counts.data_ptr(),
+                                    shortfall.data_ptr(), B, P, page_size, M, _raw_stream(dev.index)), "csa_cache_reserve")
     return shortfall
 
 
@@ -366,15 +354,15 @@ def cache_free(page_refs, block_table, seqlens, page_size: int, rows, *, stream=
     if stream is not None or page_refs.device.index is None or page_refs.device.index != _current_device():
         return _there(cache_free, locals(), page_refs)
     dev, P, B, M = _books(page_refs, block_table, seqlens)
-    _need(rows, "rows", torch.int32, (rows.numel(),), dev)
-    _check(load().csa_cache_free(_at(page_refs), _at(block_table), _at(seqlens), _at(rows),
-                                 rows.numel(), B, P, int(page_size), M, _raw_stream(dev.index)), "csa_cache_free")
+    R = rows.numel()
+    _need(rows, "rows", torch.int32, (R,), dev)
+    _check(load().csa_cache_free(page_refs.data_ptr(), block_table.data_ptr(), seqlens.data_ptr(), rows.data_ptr(), R, B, P,
+                                 page_size, M, _raw_stream(dev.index)), "csa_cache_free")
 
 
-def cache_fork(page_refs, block_table, seqlens, page_size: int, parents, children, *,
-               workspace=None, stream=None):
+def cache_fork(page_refs, block_table, seqlens, page_size: int, parents, children, *, stream=None):
     """children[i] (an empty sequence) becomes a copy of parents[i] (int32 [n]
-    both; a negative entry is padding): full pages are shared, a partly filled
+    both, n <= 4096; a negative entry is padding): full pages are shared, a partly filled
     last page gets a page of its own.  Returns (src, dst, shortfall): the pages
     to copy with cache_copy_pages in every pool (-1 where there is none), and
     shortfall as in cache_reserve."""
@@ -384,29 +372,25 @@ def cache_fork(page_refs, block_table, seqlens, page_size: int, parents, childre
     n = parents.numel()
     _need(parents, "parents", torch.int32, (n,), dev)
     _need(children, "children", torch.int32, (n,), dev)
-    src, dst = torch.empty((2, n), dtype=torch.int32, device=dev).unbind()
-    shortfall = torch.empty(1, dtype=torch.int32, device=dev)
-    workspace = _workspace(workspace, cache_workspace_bytes(B, P, n), dev)
-    _check(load().csa_cache_fork(_at(page_refs), _at(block_table), _at(seqlens), _at(parents),
-                                 _at(children), n, _at(src), _at(dst), _at(shortfall),
-                                 _at(workspace), workspace.nbytes, B, P, int(page_size), M,
-                                 _raw_stream(dev.index)), "csa_cache_fork")
+    src, dst, shortfall = (torch.empty(size, dtype=torch.int32, device=dev) for size in (n, n, 1))
+    _check(load().csa_cache_fork(page_refs.data_ptr(), block_table.data_ptr(), seqlens.data_ptr(), parents.data_ptr(),
+                                 children.data_ptr(), n, src.data_ptr(), dst.data_ptr(), shortfall.data_ptr(), B, P,
+                                 page_size, M, _raw_stream(dev.index)), "csa_cache_fork")
     return src, dst, shortfall
 
 
-def cache_compact(page_refs, block_table, seqlens, page_size: int, *, workspace=None, stream=None):
+def cache_compact(page_refs, block_table, seqlens, page_size: int, *, stream=None):
     """Gives the U held pages the numbers 0 .. U - 1.  Returns (src, dst,
     moved): int32 [P // 2] twice and [1]; the pools follow with
     cache_copy_pages(..., src, dst, count=moved) before they are read again."""
     if stream is not None or page_refs.device.index is None or page_refs.device.index != _current_device():
         return _there(cache_compact, locals(), page_refs)
     dev, P, B, M = _books(page_refs, block_table, seqlens)
-    src, dst = torch.empty((2, P // 2), dtype=torch.int32, device=dev).unbind()
-    moved = torch.empty(1, dtype=torch.int32, device=dev)
-    workspace = _workspace(workspace, cache_workspace_bytes(B, P), dev)
-    _check(load().csa_cache_compact(_at(page_refs), _at(block_table), _at(seqlens), _at(src),
-                                    _at(dst), _at(moved), _at(workspace), workspace.nbytes, B,
-                                    P, int(page_size), M, _raw_stream(dev.index)), "csa_cache_compact")
+    half = P // 2
+    src, dst, moved = (torch.empty(size, dtype=torch.int32, device=dev) for size in (half, half, 1))
+    _check(load().csa_cache_compact(page_refs.data_ptr(), block_table.data_ptr(), seqlens.data_ptr(), src.data_ptr(),
+                                    dst.data_ptr(), moved.data_ptr(), B, P, page_size, M, _raw_stream(dev.index)),
+           "csa_cache_compact")
     return src, dst, moved
 
 

@@ -249,11 +249,6 @@ int check_books(const int *refs, const int *table, const int *seqlens, int B, in
     return CSA_OK;
 }
 
-int check_cache_workspace(const void *workspace, long long bytes, int B, int P, int n) {
-    if (!workspace || bytes < csa_cache_scratch_bytes(B, P, n)) return CSA_ERR_INVALID_ARG;
-    return aligned(workspace, 4) ? CSA_OK : CSA_ERR_ALIGNMENT;
-}
-
 // A plan that csa_rope_plan_init can have made: the kernels index by its fields.
 bool sound_plan(const csa_rope_plan *plan) {
     if (plan->pairs < 1 || plan->pairs > CSA_ROPE_MAX_PAIRS || plan->axes < 1 ||
@@ -402,16 +397,14 @@ int csa_cache_append_f32(const csa_rope_plan *plan, const float *q, const long l
 }
 
 int csa_cache_reserve(int *page_refs, int *block_table, int *seqlens, const int *counts,
-                      int *shortfall, void *workspace, long long workspace_bytes, int B, int P,
-                      int S, int M, csa_stream_t stream) {
+                      int *shortfall, int B, int P, int S, int M, csa_stream_t stream) {
     int rc = check_books(page_refs, block_table, seqlens, B, P, S, M);
     if (rc != CSA_OK) return rc;
     if ((!counts && B > 0) || !shortfall) return CSA_ERR_INVALID_ARG;
-    if ((rc = check_cache_workspace(workspace, workspace_bytes, B, P, 0)) != CSA_OK) return rc;
     if (!aligned(counts, 4) || !aligned(shortfall, 4)) return CSA_ERR_ALIGNMENT;
     if ((rc = device_ok()) != CSA_OK) return rc;
-    return csa_cache_reserve_run(page_refs, block_table, seqlens, counts, shortfall, workspace, B, P,
-                                 S, M, reinterpret_cast<cudaStream_t>(stream));
+    return csa_cache_reserve_run(page_refs, block_table, seqlens, counts, shortfall, B, P, S, M,
+                                 reinterpret_cast<cudaStream_t>(stream));
 }
 
 int csa_cache_free(int *page_refs, int *block_table, int *seqlens, const int *rows, int R, int B,
@@ -427,37 +420,31 @@ int csa_cache_free(int *page_refs, int *block_table, int *seqlens, const int *ro
 }
 
 int csa_cache_fork(int *page_refs, int *block_table, int *seqlens, const int *parents,
-                   const int *children, int n, int *src, int *dst, int *shortfall,
-                   void *workspace, long long workspace_bytes, int B, int P, int S, int M,
-                   csa_stream_t stream) {
+                   const int *children, int n, int *src, int *dst, int *shortfall, int B, int P,
+                   int S, int M, csa_stream_t stream) {
     int rc = check_books(page_refs, block_table, seqlens, B, P, S, M);
     if (rc != CSA_OK) return rc;
+    if (n > CSA_CACHE_MAX_FORKS) return CSA_ERR_UNSUPPORTED;
     if (n < 0 || !shortfall || (n > 0 && (!parents || !children || !src || !dst)))
         return CSA_ERR_INVALID_ARG;
-    if ((rc = check_cache_workspace(workspace, workspace_bytes, B, P, n)) != CSA_OK) return rc;
     if (!aligned(parents, 4) || !aligned(children, 4) || !aligned(src, 4) || !aligned(dst, 4) ||
         !aligned(shortfall, 4))
         return CSA_ERR_ALIGNMENT;
     if ((rc = device_ok()) != CSA_OK) return rc;
     return csa_cache_fork_run(page_refs, block_table, seqlens, parents, children, n, src, dst,
-                              shortfall, workspace, B, P, S, M,
-                              reinterpret_cast<cudaStream_t>(stream));
+                              shortfall, B, P, S, M, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int csa_cache_compact(int *page_refs, int *block_table, const int *seqlens, int *src, int *dst,
-                      int *moved, void *workspace, long long workspace_bytes, int B, int P, int S,
-                      int M, csa_stream_t stream) {
+                      int *moved, int B, int P, int S, int M, csa_stream_t stream) {
     int rc = check_books(page_refs, block_table, seqlens, B, P, S, M);
     if (rc != CSA_OK) return rc;
     if (!moved || (P > 1 && (!src || !dst))) return CSA_ERR_INVALID_ARG;
-    if ((rc = check_cache_workspace(workspace, workspace_bytes, B, P, 0)) != CSA_OK) return rc;
     if (!aligned(src, 4) || !aligned(dst, 4) || !aligned(moved, 4)) return CSA_ERR_ALIGNMENT;
     if ((rc = device_ok()) != CSA_OK) return rc;
-    return csa_cache_compact_run(page_refs, block_table, seqlens, src, dst, moved, workspace, B, P,
-                                 S, M, reinterpret_cast<cudaStream_t>(stream));
+    return csa_cache_compact_run(page_refs, block_table, seqlens, src, dst, moved, B, P, S, M,
+                                 reinterpret_cast<cudaStream_t>(stream));
 }
-
-long long csa_cache_workspace_bytes(int B, int P, int n) { return csa_cache_scratch_bytes(B, P, n); }
 
 int csa_cache_copy_pages(void *k_pages, void *v_pages, long long page_bytes, int layers, int P,
                          const int *src, const int *dst, int n, const int *count,

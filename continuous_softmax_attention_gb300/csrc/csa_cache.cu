@@ -22,65 +22,71 @@ namespace {
 
 constexpr int kBookThreads = 1024;
 constexpr int kBookWarps = kBookThreads / 32;
-constexpr int kSub = 8;  // pages per thread and step of a walk over refs
+constexpr int kSub = 16;       // pages per thread and step of a walk over refs
+constexpr int kList = 4096;    // pages that a block keeps in shared memory
+// Entries of the table up to which the block that plans a fork or a compaction
+// also writes them; above, a second kernel does.  One launch saves 2.5 us of the
+// host's time and 1.5 us on the device; one block writes about 4 entries a ns.
+constexpr long long kOneBlock = 16384;
 
 __device__ int g_cache_status;  // sticky status word of this file's kernels
 
 __device__ __forceinline__ void complain() { atomicCAS(&g_cache_status, 0, CSA_ERR_INVALID_ARG); }
 
-// Exclusive prefix sum over the block's threads; *total gets the block's sum.
-__device__ __forceinline__ int block_scan(int v, int *warp_sums, int *total) {
+// Exclusive prefix sum over the block's kBookWarps warps of one value per warp;
+// *total gets the sum.
+__device__ __forceinline__ int warps_scan(int v, int *sums, int *total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __syncthreads();  // sums may still be read from an earlier scan
+    if (lane == 0) sums[warp] = v;
+    __syncthreads();
+    const int w = sums[lane];
+    int s = w;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, s, off);
+        if (lane >= off) s += o;
+    }
+    *total = __shfl_sync(0xffffffffu, s, 31);
+    return __shfl_sync(0xffffffffu, s - w, warp);
+}
+
+// The same over the block's threads.
+__device__ __forceinline__ int block_scan(int v, int *sums, int *total) {
+    const int lane = threadIdx.x & 31;
     int s = v;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
         const int o = __shfl_up_sync(0xffffffffu, s, off);
         if (lane >= off) s += o;
     }
-    __syncthreads();  // warp_sums may still be read from an earlier scan
-    if (lane == 31) warp_sums[warp] = s;
-    __syncthreads();
-    const int w = lane < (int)(blockDim.x >> 5) ? warp_sums[lane] : 0;
-    int ws = w;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, ws, off);
-        if (lane >= off) ws += o;
-    }
-    *total = __shfl_sync(0xffffffffu, ws, 31);
-    const int before = __shfl_sync(0xffffffffu, ws - w, warp);
-    return before + s - v;
+    return warps_scan(__shfl_sync(0xffffffffu, s, 31), sums, total) + s - v;
 }
 
 // Walks over the pages [lo, hi) in ascending order, calling hit(page, rank)
-// for those of which pick(refs[page], page) holds; ranks count from 0.  Stops
-// once `most` have been found.  Returns how many were found (at least `most`
-// if it stopped early).  Called by the whole block.
+// for those of which pick(refs[page]) holds; ranks count from 0.  Stops once
+// `most` have been found (hit may be called for a few more).  Returns how many
+// were found.  Called by the whole block.
 template <typename Pick, typename Hit>
-__device__ int walk(const int *refs, int lo, int hi, int most, int *warp_sums, Pick pick, Hit hit) {
+__device__ int walk(const int *refs, int lo, int hi, int most, int *sums, Pick pick, Hit hit) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int found = 0;
     for (long long base = lo; base < hi && found < most; base += kBookThreads * kSub) {
         // a warp takes 32 * kSub consecutive pages, 32 at a time
         const long long first = base + (long long)warp * (32 * kSub) + lane;
-        int val[kSub];
+        unsigned mask[kSub];
+        int val[kSub], mine = 0;  // of the whole warp
 #pragma unroll
         for (int i = 0; i < kSub; ++i) val[i] = first + 32 * i < hi ? refs[first + 32 * i] : 0;
-        unsigned mask[kSub];
-        int mine = 0;  // of the whole warp
 #pragma unroll
         for (int i = 0; i < kSub; ++i) {
-            const long long page = first + 32 * i;
-            mask[i] = __ballot_sync(0xffffffffu, page < hi && pick(val[i], (int)page));
+            mask[i] = __ballot_sync(0xffffffffu, first + 32 * i < hi && pick(val[i]));
             mine += __popc(mask[i]);
         }
-        int total;
-        // one count per warp, on its first lane
-        int rank = found + __shfl_sync(0xffffffffu, block_scan(lane == 0 ? mine : 0, warp_sums, &total), 0);
+        int total, rank = found + warps_scan(mine, sums, &total);
 #pragma unroll
         for (int i = 0; i < kSub; ++i) {
-            if (mask[i] >> lane & 1)
-                hit((int)(first + 32 * i), rank + __popc(mask[i] & ((1u << lane) - 1)));
+            if (mask[i] >> lane & 1) hit((int)(first + 32 * i), rank + __popc(mask[i] & ((1u << lane) - 1)));
             rank += __popc(mask[i]);
         }
         found += total;
@@ -88,25 +94,31 @@ __device__ int walk(const int *refs, int lo, int hi, int most, int *warp_sums, P
     return found;
 }
 
+struct Free {
+    __device__ bool operator()(int v) const { return v == 0; }
+};
+struct Held {
+    __device__ bool operator()(int v) const { return v > 0; }
+};
+
 __device__ __forceinline__ int pages_of(int n, int S) { return (int)(((long long)n + S - 1) / S); }
 
 // ------------------------------------------------------------------ reserve
-// list: [P] ints, prefix: [B] ints of the workspace.
+// The pages are found first and given out once it is known that they suffice:
+// up to kList of them wait in shared memory, for more the pool is walked twice.
 __global__ void __launch_bounds__(kBookThreads)
 reserve_kernel(int *refs, int *table, int *seqlens, const int *counts, int *shortfall, int B, int P,
-               int S, int M, int *list, int *prefix) {
-    __shared__ int warp_sums[32];
+               int S, int M) {
+    __shared__ int sums[32], list[kList], before[kBookThreads];
     const int tid = threadIdx.x, per = (B + kBookThreads - 1) / kBookThreads;
     const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
-    long long need = 0;
+    auto need_of = [&](int b) { return pages_of(seqlens[b] + counts[b], S) - pages_of(seqlens[b], S); };
+    int need = 0;  // at most B * M in all, which fits an int
     bool bad = false;
-    for (int b = b0; b < b1; ++b) {
+    for (int b = b0; b < b1 && !bad; ++b) {
         const int n = seqlens[b], c = counts[b];
-        if (n < 0 || c < 0 || (long long)n + c > (long long)M * S) {
-            bad = true;
-            break;
-        }
-        need += pages_of(n + c, S) - pages_of(n, S);
+        bad = n < 0 || c < 0 || (long long)n + c > (long long)M * S;
+        if (!bad) need += need_of(b);
     }
     if (__syncthreads_or(bad)) {
         if (tid == 0) {
@@ -115,31 +127,41 @@ reserve_kernel(int *refs, int *table, int *seqlens, const int *counts, int *shor
         }
         return;
     }
-    int wanted;  // at most B * M, which fits an int
-    int at = block_scan((int)need, warp_sums, &wanted);
-    for (int b = b0; b < b1; ++b) {
-        prefix[b] = at;
-        at += pages_of(seqlens[b] + counts[b], S) - pages_of(seqlens[b], S);
-    }
-    const int found = walk(refs, 0, P, wanted, warp_sums, [](int v, int) { return v == 0; },
-                           [&](int page, int rank) { list[rank] = page; });
-    if (found < wanted) {
-        if (tid == 0) *shortfall = wanted - found;
-        return;
-    }
-    __syncthreads();  // list and prefix complete
-    for (int i = tid; i < wanted; i += kBookThreads) {
-        int lo = 0, hi = B - 1;  // the last b with prefix[b] <= i
+    int wanted;
+    before[tid] = block_scan(need, sums, &wanted);
+    // page `rank` goes to the sequence b with before(b) <= rank < before(b + 1)
+    auto give = [&](int page, int rank) {
+        if (rank >= wanted) return;
+        int lo = 0, hi = kBookThreads - 1;  // the last chunk that begins at or before rank
         while (lo < hi) {
             const int mid = (lo + hi + 1) / 2;
-            if (prefix[mid] <= i)
+            if (before[mid] <= rank)
                 lo = mid;
             else
                 hi = mid - 1;
         }
-        const int page = list[i];
-        table[(long long)lo * M + pages_of(seqlens[lo], S) + i - prefix[lo]] = page;
+        int b = lo * per, at = before[lo];
+        for (int k = need_of(b); rank >= at + k; k = need_of(b)) {
+            at += k;
+            ++b;
+        }
+        table[(long long)b * M + pages_of(seqlens[b], S) + rank - at] = page;
         refs[page] = 1;
+    };
+    const bool keep = wanted <= kList;
+    const int found = walk(refs, 0, P, wanted, sums, Free(), [&](int page, int rank) {
+        if (keep && rank < wanted) list[rank] = page;
+    });
+    if (found < wanted) {
+        if (tid == 0) *shortfall = wanted - found;
+        return;
+    }
+    __syncthreads();  // list complete
+    if (keep) {
+        for (int i = tid; i < wanted; i += kBookThreads) give(list[i], i);
+    } else {
+        // a page given out is written by the thread that has just read it, and not read again
+        walk(refs, 0, P, wanted, sums, Free(), give);
     }
     __syncthreads();  // the old lengths have been read
     for (int b = b0; b < b1; ++b) seqlens[b] += counts[b];
@@ -188,138 +210,182 @@ free_kernel(int *refs, int *table, int *seqlens, const int *rows, int R, int B, 
 }
 
 // --------------------------------------------------------------------- fork
-// Checks every pair, takes a page for each child whose parent's last page is
-// partly filled, and notes the lengths; all or nothing.  mark: [B] ints, lens:
-// [n] ints (-1: nothing to do), list: [P] ints of the workspace.
-__global__ void __launch_bounds__(kBookThreads)
-fork_plan_kernel(int *refs, const int *table, const int *seqlens, const int *parents,
-                 const int *children, int n, int *src, int *dst, int *shortfall, int B, int P, int S,
-                 int M, int *mark, int *lens, int *list) {
-    __shared__ int warp_sums[32];
-    const int tid = threadIdx.x, per = (n + kBookThreads - 1) / kBookThreads;
-    for (int b = tid; b < B; b += kBookThreads) mark[b] = 0;
-    __syncthreads();
-    const int i0 = min(n, tid * per), i1 = min(n, i0 + per);
-    bool bad = false;
-    int need = 0;
-    for (int i = i0; i < i1; ++i) {
-        const int p = parents[i], c = children[i];
-        lens[i] = -1;
-        src[i] = dst[i] = -1;
-        if (p < 0 || c < 0) continue;  // padding
-        if (p >= B || c >= B) {
-            bad = true;
-            continue;
-        }
-        const int len = seqlens[p];
-        bad |= len < 0 || len > (long long)M * S || seqlens[c] != 0 || atomicAdd(mark + c, 1) != 0;
-        lens[i] = len;
-        if (!bad && len % S != 0) {
-            const int page = table[(long long)p * M + len / S];
-            bad |= page < 0 || page >= P;
-            src[i] = page;
-            ++need;
-        }
-    }
-    if (__syncthreads_or(bad)) {
-        for (int i = i0; i < i1; ++i) {
-            lens[i] = -1;
-            src[i] = -1;
-        }
-        if (tid == 0) {
-            *shortfall = -1;
-            complain();
-        }
-        return;
-    }
-    int wanted;
-    int at = block_scan(need, warp_sums, &wanted);
-    const int found = walk(refs, 0, P, wanted, warp_sums, [](int v, int) { return v == 0; },
-                           [&](int page, int rank) { list[rank] = page; });
-    const bool enough = found >= wanted;
-    __syncthreads();
-    for (int i = i0; i < i1; ++i) {
-        if (!enough) {
-            lens[i] = -1;
-            src[i] = -1;
-        } else if (src[i] >= 0) {
-            dst[i] = list[at++];
-            refs[dst[i]] = 1;
-        }
-    }
-    if (tid == 0) *shortfall = enough ? 0 : wanted - found;
-}
-
-// One block per pair: the child's row of the table, its length, and one more
-// holder for each page that it shares.
-__global__ void __launch_bounds__(256)
-fork_rows_kernel(int *refs, int *table, int *seqlens, const int *parents, const int *children,
-                 const int *dst, const int *lens, int P, int S, int M) {
-    const int i = blockIdx.x, len = lens[i];
-    if (len < 0) return;
-    const int p = parents[i], c = children[i], whole = len / S;
-    for (int j = threadIdx.x; j < M; j += blockDim.x) {
+// A child's row of the table, every step-th entry from the first, and one more
+// holder of each page that it shares.
+__device__ __forceinline__ void fork_row(int *refs, int *table, int p, int c, int len, int fresh, int P, int S,
+                                         int M, int first, int step) {
+    const int whole = len / S;
+    const int *from = table + (long long)p * M;
+    int *to = table + (long long)c * M;
+    for (int j = first; j < M; j += step) {
         int page = -1;
         if (j < whole) {
-            page = table[(long long)p * M + j];
+            page = from[j];
             if (page >= 0 && page < P)
                 atomicAdd(refs + page, 1);
             else
                 complain();
         } else if (j == whole) {
-            page = dst[i];  // -1 where the last page is full
+            page = fresh;  // -1 where the last page is full
         }
-        table[(long long)c * M + j] = page;
+        to[j] = page;
     }
-    if (threadIdx.x == 0) seqlens[c] = len;
+}
+
+// Checks every pair, takes a page for each child whose parent's last page is
+// partly filled, and sets the children's lengths; all or nothing.  A thread
+// holds pairs tid, tid + 1024, ... in registers.  A pair marks its child by a
+// negative length, which finds one that is listed twice.  rows: the block
+// writes the children's rows of the table too, a warp per pair.
+constexpr int kPairs = CSA_CACHE_MAX_FORKS / kBookThreads;
+static_assert(CSA_CACHE_MAX_FORKS <= kList, "the pages taken wait in shared memory");
+
+__global__ void __launch_bounds__(kBookThreads)
+fork_plan_kernel(int *refs, int *table, int *seqlens, const int *parents, const int *children, int n,
+                 int *src, int *dst, int *shortfall, int B, int P, int S, int M, bool rows) {
+    __shared__ int sums[32], list[kList];
+    const int tid = threadIdx.x;
+    int p[kPairs], c[kPairs], len[kPairs], page[kPairs], rank[kPairs];
+    bool bad = false;
+#pragma unroll
+    for (int k = 0; k < kPairs; ++k) {
+        const int i = k * kBookThreads + tid;
+        p[k] = i < n ? parents[i] : -1;
+        c[k] = i < n ? children[i] : -1;
+    }
+#pragma unroll
+    for (int k = 0; k < kPairs; ++k) {
+        len[k] = 0;
+        page[k] = -1;
+        if (p[k] < 0 || c[k] < 0) {  // padding
+            c[k] = -1;
+            continue;
+        }
+        if (p[k] >= B || c[k] >= B) {
+            bad = true;
+            c[k] = -1;
+            continue;
+        }
+        len[k] = seqlens[p[k]];
+        bad |= seqlens[c[k]] != 0 || len[k] < 0 || len[k] > (long long)M * S;
+        if (!bad && len[k] % S != 0) {
+            page[k] = table[(long long)p[k] * M + len[k] / S];
+            bad |= page[k] < 0 || page[k] >= P;
+        }
+    }
+    bad = __syncthreads_or(bad);
+    bool twice = false;
+    int wanted = 0, found = 0;
+    if (!bad) {
+#pragma unroll
+        for (int k = 0; k < kPairs; ++k)
+            if (c[k] >= 0) twice |= atomicCAS(seqlens + c[k], 0, -1) != 0;
+        twice = __syncthreads_or(twice);
+#pragma unroll
+        for (int k = 0; k < kPairs; ++k)
+            if (k * kBookThreads < n) {
+                int total;
+                rank[k] = wanted + block_scan(page[k] >= 0, sums, &total);
+                wanted += total;
+            }
+        if (!twice)
+            found = walk(refs, 0, P, wanted, sums, Free(), [&](int free_page, int at) {
+                if (at < wanted) list[at] = free_page;
+            });
+        __syncthreads();
+    }
+    const bool done = !bad && !twice && found >= wanted;
+#pragma unroll
+    for (int k = 0; k < kPairs; ++k) {
+        const int i = k * kBookThreads + tid;
+        if (i < n) {
+            const int fresh = done && page[k] >= 0 ? list[rank[k]] : -1;
+            if (fresh >= 0) refs[fresh] = 1;
+            src[i] = done ? page[k] : -1;
+            dst[i] = fresh;
+            if (c[k] >= 0 && !bad) seqlens[c[k]] = done ? len[k] : 0;  // no mark is left
+        }
+    }
+    if (tid == 0) {
+        *shortfall = bad || twice ? -1 : found < wanted ? wanted - found : 0;
+        if (bad || twice) complain();
+    }
+    if (!done || !rows) return;
+    __syncthreads();
+    for (int i = tid >> 5; i < n; i += kBookWarps) {
+        const int from = parents[i], to = children[i];
+        if (from >= 0 && to >= 0)
+            fork_row(refs, table, from, to, seqlens[to], dst[i], P, S, M, tid & 31, 32);
+    }
+}
+
+// The children's rows, one block per pair; their lengths are set.
+__global__ void __launch_bounds__(256)
+fork_rows_kernel(int *refs, int *table, const int *seqlens, const int *parents, const int *children,
+                 const int *dst, const int *shortfall, int P, int S, int M) {
+    const int i = blockIdx.x, p = parents[i], c = children[i];
+    if (*shortfall != 0 || p < 0 || c < 0) return;
+    fork_row(refs, table, p, c, seqlens[c], dst[i], P, S, M, threadIdx.x, blockDim.x);
 }
 
 // ------------------------------------------------------------------ compact
-// The used pages [U, P) go to the free pages [0, U), both in ascending order;
-// U is the number of used pages.  src, dst: [P / 2]; moved: [1]; map: [P] ints
-// of the workspace, of which [U, P) is written; used: [1].
-__global__ void __launch_bounds__(kBookThreads)
-compact_plan_kernel(int *refs, int P, int *src, int *dst, int *moved, int *map, int *used) {
-    __shared__ int warp_sums[32];
-    const int tid = threadIdx.x;
-    const int U = walk(refs, 0, P, 0x7fffffff, warp_sums, [](int v, int) { return v > 0; },
-                       [](int, int) {});
-    const int K = walk(refs, U, P, 0x7fffffff, warp_sums, [](int v, int) { return v > 0; },
-                       [&](int page, int rank) { src[rank] = page; });
-    walk(refs, 0, U, K, warp_sums, [](int v, int) { return v <= 0; },
-         [&](int page, int rank) { dst[rank] = page; });
-    for (int p = U + tid; p < P; p += kBookThreads) map[p] = p;
-    __syncthreads();
-    for (int i = tid; i < K; i += kBookThreads) {
-        const int s = src[i], d = dst[i];
-        map[s] = d;
-        refs[d] = refs[s];
-        refs[s] = 0;
+// The new number of a held page: dst of its place in src, which ascends, or
+// its own.
+__device__ __forceinline__ int renamed(int page, const int *src, const int *dst, int moved) {
+    int lo = 0, hi = moved;
+    while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (src[mid] < page)
+            lo = mid + 1;
+        else
+            hi = mid;
     }
-    for (int i = K + tid; i < P / 2; i += kBookThreads) src[i] = dst[i] = -1;
-    if (tid == 0) {
-        *moved = K;
-        *used = U;
+    return lo < moved && src[lo] == page ? dst[lo] : page;
+}
+
+__device__ __forceinline__ void rename_row(int *table, const int *seqlens, int b, const int *src, const int *dst,
+                                           int moved, int S, int M, int first, int step) {
+    const int n = seqlens[b];
+    if (n < 0 || n > (long long)M * S) {
+        if (first == 0) complain();
+        return;
+    }
+    const int held = pages_of(n, S);
+    for (int j = first; j < held; j += step) {
+        int *entry = table + (long long)b * M + j;
+        *entry = renamed(*entry, src, dst, moved);
     }
 }
 
-// The table's entries by the map, every row's held pages.
-__global__ void __launch_bounds__(256)
-remap_kernel(int *table, const int *seqlens, const int *map, const int *used, int B, int P, int S,
-             int M) {
-    const int U = *used;
-    for (int b = blockIdx.x; b < B; b += gridDim.x) {
-        const int n = seqlens[b];
-        if (n < 0 || n > (long long)M * S) {
-            if (threadIdx.x == 0) complain();
-            continue;
-        }
-        const int held = pages_of(n, S);
-        for (int j = threadIdx.x; j < held; j += blockDim.x) {
-            const int page = table[(long long)b * M + j];
-            if (page >= U && page < P) table[(long long)b * M + j] = map[page];
-        }
+// The held pages [U, P) go to the free pages [0, U), both in ascending order;
+// U is the number of held pages.  rows: the block renames the table's entries
+// too, a warp per sequence.
+__global__ void __launch_bounds__(kBookThreads)
+compact_plan_kernel(int *refs, int *table, const int *seqlens, int *src, int *dst, int *moved, int B, int P,
+                    int S, int M, bool rows) {
+    __shared__ int sums[32];
+    const int tid = threadIdx.x, all = 0x7fffffff;
+    const int U = walk(refs, 0, P, all, sums, Held(), [](int, int) {});
+    const int K = walk(refs, U, P, all, sums, Held(), [&](int page, int rank) { src[rank] = page; });
+    walk(refs, 0, U, K, sums, [](int v) { return v <= 0; }, [&](int page, int rank) { dst[rank] = page; });
+    __syncthreads();
+    for (int i = tid; i < K; i += kBookThreads) {
+        refs[dst[i]] = refs[src[i]];
+        refs[src[i]] = 0;
     }
+    for (int i = K + tid; i < P / 2; i += kBookThreads) src[i] = dst[i] = -1;
+    if (tid == 0) *moved = K;
+    if (rows)
+        for (int b = tid >> 5; b < B; b += kBookWarps)
+            rename_row(table, seqlens, b, src, dst, K, S, M, tid & 31, 32);
+}
+
+__global__ void __launch_bounds__(256)
+rename_kernel(int *table, const int *seqlens, const int *src, const int *dst, const int *moved, int B, int S,
+              int M) {
+    const int K = *moved;
+    for (int b = blockIdx.x; b < B; b += gridDim.x)
+        rename_row(table, seqlens, b, src, dst, K, S, M, threadIdx.x, blockDim.x);
 }
 
 // --------------------------------------------------------------------- copy
@@ -376,18 +442,9 @@ int launched() { return cudaGetLastError() == cudaSuccess ? CSA_OK : CSA_ERR_CUD
 
 }  // namespace
 
-// Workspace: list or map [P], then a table of rows [B] and one of pairs [n],
-// then the used count.
-long long csa_cache_scratch_bytes(int B, int P, int n) {
-    if (B < 0 || P < 0 || n < 0) return -1;
-    return 4LL * ((long long)P + B + n + 4);
-}
-
-int csa_cache_reserve_run(int *refs, int *table, int *seqlens, const int *counts, int *shortfall,
-                          void *scratch, int B, int P, int S, int M, cudaStream_t stream) {
-    int *list = static_cast<int *>(scratch);
-    reserve_kernel<<<1, kBookThreads, 0, stream>>>(refs, table, seqlens, counts, shortfall, B, P, S,
-                                                   M, list, list + P);
+int csa_cache_reserve_run(int *refs, int *table, int *seqlens, const int *counts, int *shortfall, int B,
+                          int P, int S, int M, cudaStream_t stream) {
+    reserve_kernel<<<1, kBookThreads, 0, stream>>>(refs, table, seqlens, counts, shortfall, B, P, S, M);
     return launched();
 }
 
@@ -398,26 +455,24 @@ int csa_cache_free_run(int *refs, int *table, int *seqlens, const int *rows, int
 }
 
 int csa_cache_fork_run(int *refs, int *table, int *seqlens, const int *parents, const int *children,
-                       int n, int *src, int *dst, int *shortfall, void *scratch, int B, int P,
-                       int S, int M, cudaStream_t stream) {
-    int *list = static_cast<int *>(scratch), *mark = list + P, *lens = mark + B;
-    fork_plan_kernel<<<1, kBookThreads, 0, stream>>>(refs, table, seqlens, parents, children, n, src,
-                                                     dst, shortfall, B, P, S, M, mark, lens, list);
+                       int n, int *src, int *dst, int *shortfall, int B, int P, int S, int M,
+                       cudaStream_t stream) {
+    const bool one = (long long)n * M <= kOneBlock;
+    fork_plan_kernel<<<1, kBookThreads, 0, stream>>>(refs, table, seqlens, parents, children, n, src, dst,
+                                                     shortfall, B, P, S, M, one);
     if (launched() != CSA_OK) return CSA_ERR_CUDA;
-    if (n == 0) return CSA_OK;
-    fork_rows_kernel<<<n, 256, 0, stream>>>(refs, table, seqlens, parents, children, dst, lens, P, S,
-                                            M);
+    if (one) return CSA_OK;
+    fork_rows_kernel<<<n, 256, 0, stream>>>(refs, table, seqlens, parents, children, dst, shortfall, P, S, M);
     return launched();
 }
 
-int csa_cache_compact_run(int *refs, int *table, const int *seqlens, int *src, int *dst, int *moved,
-                          void *scratch, int B, int P, int S, int M, cudaStream_t stream) {
-    int *map = static_cast<int *>(scratch), *used = map + P;
-    compact_plan_kernel<<<1, kBookThreads, 0, stream>>>(refs, P, src, dst, moved, map, used);
+int csa_cache_compact_run(int *refs, int *table, const int *seqlens, int *src, int *dst, int *moved, int B,
+                          int P, int S, int M, cudaStream_t stream) {
+    const bool one = (long long)B * M <= kOneBlock;
+    compact_plan_kernel<<<1, kBookThreads, 0, stream>>>(refs, table, seqlens, src, dst, moved, B, P, S, M, one);
     if (launched() != CSA_OK) return CSA_ERR_CUDA;
-    if (B > 0 && M > 0)
-        remap_kernel<<<B < 152 * 8 ? B : 152 * 8, 256, 0, stream>>>(table, seqlens, map, used, B, P,
-                                                                    S, M);
+    if (one) return CSA_OK;
+    rename_kernel<<<B < 152 * 8 ? B : 152 * 8, 256, 0, stream>>>(table, seqlens, src, dst, moved, B, S, M);
     return launched();
 }
 

@@ -127,16 +127,15 @@ int csa_cache_append_run(const csa_rope_plan *plan, const void *q, const long lo
 int csa_rope_take_status(void);
 
 // Pages: who holds them, and their movement (csa_cache.cu).
-long long csa_cache_scratch_bytes(int B, int P, int n);
-int csa_cache_reserve_run(int *refs, int *table, int *seqlens, const int *counts, int *shortfall,
-                          void *scratch, int B, int P, int S, int M, cudaStream_t stream);
+int csa_cache_reserve_run(int *refs, int *table, int *seqlens, const int *counts, int *shortfall, int B,
+                          int P, int S, int M, cudaStream_t stream);
 int csa_cache_free_run(int *refs, int *table, int *seqlens, const int *rows, int R, int B, int P,
                        int S, int M, cudaStream_t stream);
 int csa_cache_fork_run(int *refs, int *table, int *seqlens, const int *parents, const int *children,
-                       int n, int *src, int *dst, int *shortfall, void *scratch, int B, int P,
-                       int S, int M, cudaStream_t stream);
-int csa_cache_compact_run(int *refs, int *table, const int *seqlens, int *src, int *dst, int *moved,
-                          void *scratch, int B, int P, int S, int M, cudaStream_t stream);
+                       int n, int *src, int *dst, int *shortfall, int B, int P, int S, int M,
+                       cudaStream_t stream);
+int csa_cache_compact_run(int *refs, int *table, const int *seqlens, int *src, int *dst, int *moved, int B,
+                          int P, int S, int M, cudaStream_t stream);
 int csa_cache_copy_pages_run(void *k_pages, void *v_pages, long long page_bytes, int layers, int P,
                              const int *src, const int *dst, int n, const int *count,
                              cudaStream_t stream);

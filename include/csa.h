@@ -569,11 +569,9 @@ int csa_cache_append_f32(const csa_rope_plan *plan, const float *q, const long l
  *   if the pool has too few, or -1 for a negative count or length or one that
  *   does not fit a row of the table (which also sets the status word).  Where
  *   it is not 0, nothing has changed.
- *   workspace: csa_cache_workspace_bytes(B, P, 0) bytes, 4-byte aligned.
  */
 int csa_cache_reserve(int *page_refs, int *block_table, int *seqlens, const int *counts,
-                      int *shortfall, void *workspace, long long workspace_bytes, int B, int P,
-                      int S, int M, csa_stream_t stream);
+                      int *shortfall, int B, int P, int S, int M, csa_stream_t stream);
 
 /*
  * csa_cache_free - the listed sequences give their pages back: their refs fall
@@ -597,12 +595,12 @@ int csa_cache_free(int *page_refs, int *block_table, int *seqlens, const int *ro
  *   shortfall as csa_cache_reserve (-1: a row out of range, a bad length or
  *   page, a child that is not empty or listed twice); where it is not 0,
  *   nothing has changed and src, dst are -1.
- *   workspace: csa_cache_workspace_bytes(B, P, n) bytes, 4-byte aligned.
+ *   n at most CSA_CACHE_MAX_FORKS (CSA_ERR_UNSUPPORTED).
  */
+#define CSA_CACHE_MAX_FORKS 4096
 int csa_cache_fork(int *page_refs, int *block_table, int *seqlens, const int *parents,
-                   const int *children, int n, int *src, int *dst, int *shortfall,
-                   void *workspace, long long workspace_bytes, int B, int P, int S, int M,
-                   csa_stream_t stream);
+                   const int *children, int n, int *src, int *dst, int *shortfall, int B, int P,
+                   int S, int M, csa_stream_t stream);
 
 /*
  * csa_cache_compact - moves the held pages together: with U pages held, those
@@ -610,16 +608,10 @@ int csa_cache_fork(int *page_refs, int *block_table, int *seqlens, const int *pa
  *   src, dst: int32 [P / 2], the moves, then -1; moved: int32 [1], how many.
  *   page_refs and the held entries of the table are already renamed; the
  *   caller moves the data (csa_cache_copy_pages with count = moved, once per
- *   pool) before anything reads the pools.  workspace:
- *   csa_cache_workspace_bytes(B, P, 0) bytes, 4-byte aligned.
+ *   pool) before anything reads the pools.
  */
 int csa_cache_compact(int *page_refs, int *block_table, const int *seqlens, int *src, int *dst,
-                      int *moved, void *workspace, long long workspace_bytes, int B, int P, int S,
-                      int M, csa_stream_t stream);
-
-/* csa_cache_workspace_bytes - workspace bytes csa_cache_reserve, _fork and
- * _compact need (host only), or -1 for a negative size. */
-long long csa_cache_workspace_bytes(int B, int P, int n);
+                      int *moved, int B, int P, int S, int M, csa_stream_t stream);
 
 /*
  * csa_cache_copy_pages - copies page src[i] onto page dst[i] for i < min(n,

@@ -51,7 +51,7 @@ def grown(B, P, S, M, counts):
 
 
 @pytest.mark.parametrize("seed", range(6))
-@pytest.mark.parametrize("B,P,S,M", [(1, 5, 8, 4), (7, 40, 16, 8), (40, 700, 8, 25), (1500, 9000, 24, 7), (33, 40000, 5, 1200)])
+@pytest.mark.parametrize("B,P,S,M", [(1, 5, 8, 4), (7, 40, 16, 8), (200, 3000, 16, 300), (40, 700, 8, 25), (1500, 9000, 24, 7), (33, 40000, 5, 1200)])
 def test_a_long_run_of_everything(B, P, S, M, seed):
     r = random.Random(seed)
     m = Books(B, P, S, M)
@@ -132,11 +132,29 @@ def test_fork_shares_and_refuses():
     m.free([0]), d.free([0])  # the pages live on with the children
     d.equals()
     assert max(m.refs) == 2
+    m, d = grown(6, 30, 16, 300, [100, 0, 0, 0, 0, 0])
+    p, c = [1, 0, 2, 4], [2, 1, 3, 5]  # parents that are children of the same call were empty: so are their children
+    src, dst, short = d.fork(p, c)
+    assert (src.tolist(), dst.tolist(), short.item()) == m.fork(p, c)
+    assert m.lens == [100, 100, 0, 0, 0, 0]
+    d.equals()
     m, d = grown(3, 3, 16, 2, [20, 3, 0])
     src, dst, short = d.fork([1], [2])  # no page left for the child's copy
     assert short.item() == 1 and src.tolist() == [-1] and m.fork([1], [2])[2] == 1
     d.equals()
     assert device_status() == 0
+
+
+def test_many_forks_at_once():
+    B, n = 5000, 4096
+    m, d = grown(B, 30000, 8, 3, [1 + b % 24 for b in range(900)] + [0] * (B - 900))
+    r = random.Random(1)
+    p, c = [r.randrange(-1, 900) for _ in range(n)], r.sample(range(900, B), n)
+    src, dst, short = d.fork(p, c)
+    assert (src.tolist(), dst.tolist(), short.item()) == m.fork(p, c) and short.item() == 0
+    d.equals()
+    with pytest.raises(CsaError):
+        d.fork([0] * (n + 1), [1] * (n + 1))
 
 
 @pytest.mark.parametrize("dtype,shape", [(torch.bfloat16, (50, 2, 16, 128)), (torch.bfloat16, (3, 50, 4, 24, 64)),
@@ -176,7 +194,6 @@ def test_refusals():
         with pytest.raises((ValueError, AttributeError)):
             bad()
     for bad in (lambda: csa.cache_reserve(refs, table, lens, 0, one),
-                lambda: csa.cache_reserve(refs, table, lens, S, one, workspace=torch.empty(8, dtype=torch.uint8, device="cuda")),
                 lambda: csa.cache_compact(refs, table, lens, -1)):
         with pytest.raises(CsaError) as e:
             bad()

@@ -140,45 +140,40 @@ def test_append_refusals(lib):
 
 
 def test_page_calls_refuse(lib):
-    def reserve(refs=FAKE, table=FAKE, lens=FAKE, counts=FAKE, short=FAKE, ws=FAKE, n=1 << 30, B=2, P=10, S=16, M=4):
-        return lib.csa_cache_reserve(refs, table, lens, counts, short, ws, n, B, P, S, M, None)
+    def reserve(refs=FAKE, table=FAKE, lens=FAKE, counts=FAKE, short=FAKE, B=2, P=10, S=16, M=4):
+        return lib.csa_cache_reserve(refs, table, lens, counts, short, B, P, S, M, None)
 
     def free(rows=FAKE, R=1, refs=FAKE, B=2, P=10, S=16, M=4):
         return lib.csa_cache_free(refs, FAKE, FAKE, rows, R, B, P, S, M, None)
 
-    def fork(parents=FAKE, n=1, src=FAKE, short=FAKE, ws=FAKE, nb=1 << 30, B=2):
-        return lib.csa_cache_fork(FAKE, FAKE, FAKE, parents, FAKE, n, src, FAKE, short, ws, nb, B, 10, 16, 4, None)
+    def fork(parents=FAKE, n=1, src=FAKE, short=FAKE, B=2, M=4):
+        return lib.csa_cache_fork(FAKE, FAKE, FAKE, parents, FAKE, n, src, FAKE, short, B, 10, 16, M, None)
 
-    def compact(src=FAKE, moved=FAKE, ws=FAKE, nb=1 << 30, P=10):
-        return lib.csa_cache_compact(FAKE, FAKE, FAKE, src, FAKE, moved, ws, nb, 2, P, 16, 4, None)
+    def compact(src=FAKE, moved=FAKE, P=10):
+        return lib.csa_cache_compact(FAKE, FAKE, FAKE, src, FAKE, moved, 2, P, 16, 4, None)
 
     def copy(k=FAKE, nbytes=64, layers=1, P=10, src=FAKE, dst=FAKE, n=1, count=NULL):
         return lib.csa_cache_copy_pages(k, NULL, nbytes, layers, P, src, dst, n, count, None)
 
-    need = csa.cache_workspace_bytes(2, 10)
-    for kw in (dict(refs=NULL), dict(table=NULL), dict(lens=NULL), dict(counts=NULL), dict(short=NULL), dict(ws=NULL), dict(n=need - 1),
-               dict(S=0), dict(M=0), dict(B=-1), dict(P=-1)):
+    for kw in (dict(refs=NULL), dict(table=NULL), dict(lens=NULL), dict(counts=NULL), dict(short=NULL), dict(S=0), dict(M=0), dict(B=-1), dict(P=-1)):
         assert reserve(**kw) == INV, kw
     assert reserve(B=2 ** 16, M=2 ** 16) == UNS and reserve(S=2 ** 30) == UNS
-    assert reserve(refs=ODD) == ALI and reserve(counts=ODD) == ALI and reserve(ws=ODD) == ALI
+    assert reserve(refs=ODD) == ALI and reserve(counts=ODD) == ALI
     assert free(rows=NULL) == INV and free(R=-1) == INV and free(rows=ODD) == ALI and free(refs=NULL) == INV and free(R=0) == OK
     assert fork(parents=NULL) == INV and fork(n=-1) == INV and fork(src=NULL) == INV and fork(short=NULL) == INV
-    assert fork(ws=NULL) == INV and fork(nb=csa.cache_workspace_bytes(2, 10, 1) - 1) == INV and fork(src=ODD) == ALI
-    assert compact(moved=NULL) == INV and compact(src=NULL) == INV and compact(nb=need - 1) == INV and compact(src=ODD) == ALI
+    assert fork(src=ODD) == ALI and fork(n=4097) == UNS
+    assert compact(moved=NULL) == INV and compact(src=NULL) == INV and compact(src=ODD) == ALI
     assert copy(k=NULL) == INV and copy(src=NULL) == INV and copy(n=-1) == INV and copy(nbytes=-1) == INV and copy(layers=-1) == INV
     assert copy(src=ODD) == ALI and copy(n=0) == OK and copy(layers=0) == OK
     assert copy(nbytes=1 << 40, layers=1 << 20, P=1 << 20) == UNS
-    assert csa.cache_workspace_bytes(3, 100, 7) >= 4 * 110
-    with pytest.raises(csa.CsaError):
-        csa.cache_workspace_bytes(-1, 1)
 
 
 def test_valid_calls_reach_the_device_check(lib, no_gpu):
     plan = csa.RopeAxes(64, (32,))._ref
     assert rope(lib, plan) == END and append(lib) == END and append(lib, plan=plan, Hq=2, q=FAKE, qo=FAKE) == END
-    assert lib.csa_cache_reserve(*[FAKE] * 6, 1 << 30, 2, 10, 16, 4, None) == END
+    assert lib.csa_cache_reserve(*[FAKE] * 5, 2, 10, 16, 4, None) == END
     assert lib.csa_cache_free(FAKE, FAKE, FAKE, FAKE, 1, 2, 10, 16, 4, None) == END
-    assert lib.csa_cache_compact(*[FAKE] * 7, 1 << 30, 2, 10, 16, 4, None) == END
+    assert lib.csa_cache_compact(*[FAKE] * 6, 2, 10, 16, 4, None) == END
 
 
 def test_cpu_tensors_are_refused():
