@@ -50,7 +50,6 @@ constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
 constexpr int kGrid = 152;        // one block per SM
-constexpr int kStages = 3;        // tiles in a worker's ring
 constexpr int kFew = 4;           // tiles per worker up to which latency counts, not balance
 // What beginning and ending a part costs, in tiles: with it a range of many
 // short sequences takes as long as one of a long sequence.
@@ -59,16 +58,23 @@ constexpr float kRaise = 16.0f;   // log2 units a logit may pass the running max
 
 __device__ int g_paged_status;  // sticky status word of this file's kernels
 
-template <int D>
+// RH: query heads per block / 8, rounded up (1 or 2).
+template <int D, int RH>
 struct Cfg {
     static constexpr int KT = 16;                      // rows per tile
-    static constexpr int Warps = 1024 / D;             // workers per block: 16, 8, 4
+    // Workers per block: as many as registers allow without spills (at d = 64 with 16 heads 16
+    // workers of 128 registers take 92 us for 268 MB where 12 of 168 take 75 us), one per
+    // scheduler at d = 256, whose sums alone are 128 registers.
+    static constexpr int Warps = D == 64 && RH == 2 ? 12 : 1024 / D;
+    static constexpr int Stages = D == 64 && RH == 2 ? 4 : 3;  // tiles in a worker's ring
     static constexpr int Tile = KT * D * 2;            // bytes of a tile of keys, or of values
     static constexpr int Stage = 2 * Tile;
-    static constexpr int Smem = Warps * kStages * Stage + 1024;  // + alignment
-    static constexpr int Workers = Warps * kGrid;
+    static constexpr int Smem = Warps * Stages * Stage + 1024;  // + alignment
     static_assert(Smem <= 227 * 1024 - 6144, "one block per SM");
 };
+
+// Workers of a full grid, at most.
+__host__ __device__ constexpr long long workers(int d) { return 1024 / d * kGrid; }
 
 struct PagedParams {
     const __nv_bfloat16 *q, *k, *v, *k0, *v0;
@@ -89,27 +95,68 @@ struct PagedParams {
     int mode;
 };
 
-// The weights that the interval between logits a and a1 (log2 units) gives its
-// two keys, with p = 2^{a-m}, p1 = 2^{a1-m}.  |x| < 1 (natural units): the
-// power series sum x^j/(j+2)!, j = 0..9, truncated below 3e-9 relative, split
-// into its even and odd terms, which the two keys share.
-__device__ __forceinline__ void interval(float a, float a1, float p, float p1, float &left,
-                                         float &right) {
-    const float x = (a1 - a) * kLn2, y = x * x;
-    float even = 2.755731922398589e-07f;             // 1/10!
-    even = fmaf(even, y, 2.48015873015873e-05f);     // 1/8!
-    even = fmaf(even, y, 1.388888888888889e-03f);    // 1/6!
-    even = fmaf(even, y, 4.166666666666667e-02f);    // 1/4!
-    even = fmaf(even, y, 0.5f);                      // 1/2!
-    float odd = 2.505210838544172e-08f;              // 1/11!
-    odd = fmaf(odd, y, 2.755731922398589e-06f);      // 1/9!
-    odd = fmaf(odd, y, 1.984126984126984e-04f);      // 1/7!
-    odd = fmaf(odd, y, 8.333333333333333e-03f);      // 1/5!
-    odd = fmaf(odd, y, 1.666666666666667e-01f);      // 1/3!
-    const float r = rcp_approx(x), s = (p1 - p) * r;
-    const bool near = fabsf(x) < 1.0f;
-    left = near ? p * fmaf(odd, x, even) : (s - p) * r;
-    right = near ? p1 * fmaf(-odd, x, even) : (p1 - s) * r;
+// Two fp32 numbers that one instruction works on.
+struct Two {
+    uint64_t v;
+};
+__device__ __forceinline__ Two two(float a, float b) {
+    Two r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ Two both(float a) { return two(a, a); }
+__device__ __forceinline__ void apart(Two x, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x.v));
+}
+__device__ __forceinline__ Two operator+(Two a, Two b) {
+    Two r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ Two operator*(Two a, Two b) {
+    Two r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+    Two r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+
+// The weights that two intervals, between logits a0 and b0 and between a1 and
+// b1 (log2 units), give their two keys each, with p = 2^{a-m} and r = 2^{b-m}.
+// |x| < 1 (natural units): the power series sum x^j/(j+2)!, j = 0..9, truncated
+// below 3e-9 relative, split into its even and odd terms, which the two keys
+// share.
+__device__ __forceinline__ void intervals(float a0, float b0, float a1, float b1, float p0, float r0, float p1,
+                                          float r1, float &left0, float &right0, float &left1, float &right1) {
+    const Two minus = both(-1.0f), p = two(p0, p1), r = two(r0, r1);
+    const Two x = fma2(two(a0, a1), minus, two(b0, b1)) * both(kLn2), y = x * x;
+    Two even = both(2.755731922398589e-07f);                    // 1/10!
+    even = fma2(even, y, both(2.48015873015873e-05f));          // 1/8!
+    even = fma2(even, y, both(1.388888888888889e-03f));         // 1/6!
+    even = fma2(even, y, both(4.166666666666667e-02f));         // 1/4!
+    even = fma2(even, y, both(0.5f));                           // 1/2!
+    Two odd = both(2.505210838544172e-08f);                     // 1/11!
+    odd = fma2(odd, y, both(2.755731922398589e-06f));           // 1/9!
+    odd = fma2(odd, y, both(1.984126984126984e-04f));           // 1/7!
+    odd = fma2(odd, y, both(8.333333333333333e-03f));           // 1/5!
+    odd = fma2(odd, y, both(1.666666666666667e-01f)) * x;       // 1/3!
+    float x0, x1;
+    apart(x, x0, x1);
+    const Two inv = two(rcp_approx(x0), rcp_approx(x1));
+    const Two s = fma2(p, minus, r) * inv;
+    float ln0, ln1, rn0, rn1, lf0, lf1, rf0, rf1;
+    apart(p * (even + odd), ln0, ln1);
+    apart(r * fma2(odd, minus, even), rn0, rn1);
+    apart(fma2(p, minus, s) * inv, lf0, lf1);
+    apart(fma2(s, minus, r) * inv, rf0, rf1);
+    const bool near0 = fabsf(x0) < 1.0f, near1 = fabsf(x1) < 1.0f;
+    left0 = near0 ? ln0 : lf0;
+    right0 = near0 ? rn0 : rf0;
+    left1 = near1 ? ln1 : lf1;
+    right1 = near1 ? rn1 : rf1;
 }
 
 // D (+)= A B, 16 x 8 x 16, bf16 in, fp32 out.
@@ -251,11 +298,11 @@ __device__ __forceinline__ bool next_part(Part &t, const Cut &cut, long long u0,
 }
 
 template <int D, int RH>
-__global__ void __launch_bounds__(Cfg<D>::Warps * 32, 1)
+__global__ void __launch_bounds__(Cfg<D, RH>::Warps * 32, 1)
 paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUtensorMap map_k,
              const __grid_constant__ CUtensorMap map_v) {
-    using C = Cfg<D>;
-    constexpr int KT = C::KT, NT = KT / 8, KS = D / 16, ON = D / 8;
+    using C = Cfg<D, RH>;
+    constexpr int KT = C::KT, NT = KT / 8, KS = D / 16, ON = D / 8, kStages = C::Stages;
     extern __shared__ uint8_t raw[];
     __shared__ long long s_cut[C::Warps * 32 + 1];
     __shared__ __align__(8) uint64_t bars[C::Warps][kStages];
@@ -593,8 +640,8 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
                     const float a_b = __shfl_sync(0xffffffffu, a_src, (lane & ~3) | ((q + 3) & 3));
                     const float p_b = __shfl_sync(0xffffffffu, p_src, (lane & ~3) | ((q + 3) & 3));
                     float r_even, l_odd, r_odd;
-                    interval(a_b, s[i][2 * h], p_b, pe[i][0], even_left[i], r_even);
-                    interval(s[i][2 * h], s[i][2 * h + 1], pe[i][0], pe[i][1], l_odd, r_odd);
+                    intervals(a_b, s[i][2 * h], s[i][2 * h], s[i][2 * h + 1], p_b, pe[i][0], pe[i][0], pe[i][1],
+                              even_left[i], r_even, l_odd, r_odd);
                     if (8 * i + 2 * q >= own) even_left[i] = r_even = 0.f;
                     if (8 * i + 2 * q + 1 >= own) l_odd = r_odd = 0.f;
                     nw[h][i][0] = r_even + l_odd;
@@ -645,8 +692,9 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
             if (__any_sync(0xffffffffu, over)) raise(behind);
 #pragma unroll
             for (int h = 0; h < RH; ++h) {
-                float left, right;
-                interval(prev[h], behind[h], pm[h], ex2_approx(behind[h] - m[h]), left, right);
+                float left, right, none0, none1;
+                const float pb = ex2_approx(behind[h] - m[h]);
+                intervals(prev[h], behind[h], prev[h], behind[h], pm[h], pb, pm[h], pb, left, right, none0, none1);
                 if (q == 3) w[h][NT - 1][1] += left;
             }
         }
@@ -773,7 +821,7 @@ __global__ void join_kernel(const PagedParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int4 seg = p.joins[blockIdx.x];
     // none; or left over, where a wait ran out and the parts are undefined anyway
-    if (seg.x < 0 || seg.x >= p.B * heads || seg.y < 0 || seg.z < seg.y || seg.z >= Cfg<D>::Workers) return;
+    if (seg.x < 0 || seg.x >= p.B * heads || seg.y < 0 || seg.z < seg.y || seg.z >= workers(D)) return;
     const int b = seg.x / heads, head = seg.x - b * heads, c0 = seg.y;
     const int hk = head / p.GB, hb = head - hk * p.GB, rows = min(p.HB, p.G - hb * p.HB);
     const long long out0 = (long long)b * p.Hq + hk * p.G + hb * p.HB;
@@ -835,7 +883,7 @@ bool encode_pool(CUtensorMap *map, const void *ptr, long long rows, int D, int R
 
 template <int D, int RH>
 int launch(PagedParams &p, cudaStream_t stream) {
-    using C = Cfg<D>;
+    using C = Cfg<D, RH>;
     p.R = C::KT;
     while (p.S % p.R != 0) p.R /= 2;  // S is a multiple of 8
     CUtensorMap map_k, map_v;
@@ -853,13 +901,13 @@ int launch(PagedParams &p, cudaStream_t stream) {
     auto kern = paged_kernel<D, RH>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::Smem) != cudaSuccess)
         return CSA_ERR_CUDA;
-    const long long segments = (long long)p.B * heads, workers = (long long)grid * C::Warps;
+    const long long segments = (long long)p.B * heads, all = (long long)grid * C::Warps;
     p.by_segment = segments <= kGrid;
     kern<<<grid, C::Warps * 32, C::Smem, stream>>>(p, map_k, map_v);
     // parts of a segment, at most about
-    const long long parts = workers / segments;
+    const long long parts = all / segments;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = p.by_segment ? dim3((unsigned)segments, (unsigned)p.HB) : dim3((unsigned)workers);
+    cfg.gridDim = p.by_segment ? dim3((unsigned)segments, (unsigned)p.HB) : dim3((unsigned)all);
     cfg.blockDim = dim3(32 * (p.by_segment && parts > 64 ? kJoinWarpsMost : kJoinWarps));
     cfg.stream = stream;
     cudaLaunchAttribute attr;
@@ -874,7 +922,6 @@ int launch(PagedParams &p, cudaStream_t stream) {
 // Blocks of the query heads of a group, at most 16 each, as equal as can be.
 int head_blocks(int G) { return (G + 15) / 16; }
 
-long long workers(int d) { return d == 256 ? Cfg<256>::Workers : d == 128 ? Cfg<128>::Workers : Cfg<64>::Workers; }
 
 }  // namespace
 
