@@ -24,8 +24,9 @@
 //    tcgen05: with 16 rows at most the products take a few percent of the time
 //    either way, and mma.sync leaves logits and sums in the registers of the
 //    warp that needs them.
-//  - The weights enter the second product as a sum of two bf16 numbers (16
-//    bits of the weight).  For up to 8 heads both halves fit one instruction:
+//  - The weights enter the second product as a sum of two bf16 numbers (15
+//    bits of the weight), the high part cut off so that neither is negative
+//    and the low one at least 2^-20 of the weight: an infinite value stays one.  For up to 8 heads both halves fit one instruction:
 //    rows 0..7 hold the high parts and rows 8..15 the low ones.
 //  - A part of a sequence leaves its unnormalised sums, maximum and weight sum
 //    in the workspace; a second kernel, launched early, joins the parts in
@@ -267,6 +268,27 @@ __device__ __forceinline__ int find_sequence(long long u, const Cut &cut, const 
     }
 }
 
+// The cut of up to 32 sequences by a warp on its own, without a barrier of the
+// block: lane b holds the units (per head) before sequence b.
+__device__ __forceinline__ Cut form_cut_warp(int n, int KT, long long most, int heads, long long all,
+                                             long long &before) {
+    const int lane = threadIdx.x & 31, tiles = tiles_of(n, KT, most);
+    const unsigned some = __ballot_sync(0xffffffffu, tiles > 0);
+    long long s = tiles;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, s, off);
+        if (lane >= off) s += o;
+    }
+    const long long total = __shfl_sync(0xffffffffu, s, 31);
+    Cut cut;
+    cut.cost = total * heads > kFew * all ? kPartCost : 0;
+    before = s - tiles + cut.cost * __popc(some & ((1u << lane) - 1));
+    cut.U = (total + cut.cost * __popc(some)) * heads;
+    cut.in_use = cut.U < all ? cut.U : all;
+    return cut;
+}
+
 // A worker's units [u0, u1) as parts: tiles [tile, last) of one head of one
 // sequence each.
 struct Part {
@@ -306,20 +328,26 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
     extern __shared__ uint8_t raw[];
     __shared__ long long s_cut[C::Warps * 32 + 1];
     __shared__ __align__(8) uint64_t bars[C::Warps][kStages];
-    __shared__ int s_abort;
-    volatile int *abort_flag = &s_abort;
+    __shared__ int s_abort[C::Warps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
     const int heads = p.Hkv * p.GB;
     const long long most = (long long)p.M * p.S;
+    volatile int *abort_flag = &s_abort[warp];
 
+    const bool few = p.B <= 32;  // sequences: every warp forms the cut
+    const int lane_n = few && lane < p.B ? p.seqlens[lane] : 0;
     if (lane == 0) {
         for (int s = 0; s < kStages; ++s) mbar_init(smem_u32(&bars[warp][s]), 1);
         fence_mbar_init();
+        s_abort[warp] = 0;
     }
-    if (threadIdx.x == 0) s_abort = 0;
+    __syncwarp();
     // the join's blocks may take their places as this kernel's blocks end
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const Cut cut = form_cut(p.seqlens, p.B, KT, most, heads, (long long)C::Warps * gridDim.x, s_cut);
+    const long long all = (long long)C::Warps * gridDim.x;
+    long long lane_before = 0;
+    const Cut cut = few ? form_cut_warp(lane_n, KT, most, heads, all, lane_before)
+                        : form_cut(p.seqlens, p.B, KT, most, heads, all, s_cut);
     // sequences without rows, and lengths out of range
     for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
         const int n = p.seqlens[b];
@@ -344,8 +372,14 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
 
     // ---- position in the range: what is copied next, and what is consumed
     Part now;
-    now.b = find_sequence(u0, cut, s_cut, p.seqlens, p.B, KT, most, heads, now.s0);
-    now.n = p.seqlens[now.b];
+    if (few) {  // the last sequence that begins at or before u0
+        now.b = __popc(__ballot_sync(0xffffffffu, lane < p.B && lane_before * heads <= u0)) - 1;
+        now.s0 = __shfl_sync(0xffffffffu, lane_before, now.b) * heads;
+        now.n = __shfl_sync(0xffffffffu, lane_n, now.b);
+    } else {
+        now.b = find_sequence(u0, cut, s_cut, p.seqlens, p.B, KT, most, heads, now.s0);
+        now.n = p.seqlens[now.b];
+    }
     now.tiles = tiles_of(now.n, KT, most);
     now.head = (int)quot(u0 - now.s0, cut.units(now.tiles));  // hk * GB + block of query heads
     now.s0 += (long long)now.head * cut.units(now.tiles);
@@ -357,6 +391,27 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
     const uint32_t ring = (smem_u32(raw) + 1023) / 1024 * 1024 + warp * (kStages * C::Stage);
     const int R = p.R, pieces = KT / R;
     const uint32_t half = (uint32_t)R * 128;  // bytes of one 64-column box of a copy
+
+    // What a part needs from memory besides its tiles, asked for before the copies are waited for.
+    // Queries: A operand, rows g (and g + 8).  The rows before and behind the range: their pages.
+    uint32_t qa[KS][4];
+    int edge_row = 0, edge_page = 0;
+    auto ask = [&]() {
+        const int hk = cached_head(now.head), hb = now.head - hk * p.GB;
+        const int rows_h = min(p.HB, p.G - hb * p.HB);
+        const uint32_t *qg = reinterpret_cast<const uint32_t *>(
+            p.q + ((long long)now.b * p.Hq + hk * p.G + hb * p.HB + g) * D);
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+            qa[i][0] = g < rows_h ? __ldg(qg + i * 8 + q) : 0u;
+            qa[i][2] = g < rows_h ? __ldg(qg + i * 8 + 4 + q) : 0u;
+            qa[i][1] = RH == 2 && g + 8 < rows_h ? __ldg(qg + 4 * D + i * 8 + q) : 0u;
+            qa[i][3] = RH == 2 && g + 8 < rows_h ? __ldg(qg + 4 * D + i * 8 + 4 + q) : 0u;
+        }
+        edge_row = g == 0 ? now.tile * KT - 1 : g == 1 && now.last * KT < now.n ? now.last * KT : -1;
+        edge_page = edge_row >= 0 ? __ldg(p.table + (long long)now.b * p.M + page_index(edge_row)) : -1;
+    };
+    ask();
 
     Part ahead = now;
     bool more = true;  // something is left to copy
@@ -419,7 +474,7 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
 
     int stage = 0;
     uint32_t parity = 0;
-    do {
+    while (true) {
         const int b = now.b, n = now.n, tile = now.tile, last = now.last;
         const int hk = cached_head(now.head), hb = now.head - hk * p.GB;
         const int rows_h = min(p.HB, p.G - hb * p.HB);  // query heads of this block
@@ -427,29 +482,16 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
         const int r0 = tile * KT, r1 = min(n, last * KT);
         bool bad = false;
 
-        // queries: A operand, rows g (and g + 8)
-        uint32_t qa[KS][4];
-        {
-            const uint32_t *qg = reinterpret_cast<const uint32_t *>(p.q + ((long long)b * p.Hq + q0 + g) * D);
-#pragma unroll
-            for (int i = 0; i < KS; ++i) {
-                qa[i][0] = g < rows_h ? __ldg(qg + i * 8 + q) : 0u;
-                qa[i][2] = g < rows_h ? __ldg(qg + i * 8 + 4 + q) : 0u;
-                qa[i][1] = RH == 2 && g + 8 < rows_h ? __ldg(qg + 4 * D + i * 8 + q) : 0u;
-                qa[i][3] = RH == 2 && g + 8 < rows_h ? __ldg(qg + 4 * D + i * 8 + 4 + q) : 0u;
-            }
-        }
         // logits of the row before the range, the row behind it and a given sink: one more column
         // tile whose "keys" 0, 1, 2 are read straight from memory
         const bool given = r0 == 0 && p.mode == CSA_K0_GIVEN, copied_sink = r0 == 0 && p.mode == CSA_K0_COPY_FIRST;
         float edge[4] = {0.f, 0.f, 0.f, 0.f};
         if (r0 > 0 || r1 < n || given) {
             const __nv_bfloat16 *at = nullptr;
-            if ((g == 0 && r0 > 0) || (g == 1 && r1 < n)) {
-                const int row = g == 0 ? r0 - 1 : r1;
-                const int index = page_index(row), page = __ldg(p.table + (long long)b * p.M + index);
-                if (page >= 0 && page < p.P)
-                    at = p.k + (((long long)page * p.Hkv + hk) * p.S + row - index * p.S) * D;
+            if (edge_row >= 0) {
+                if (edge_page >= 0 && edge_page < p.P)
+                    at = p.k + (((long long)edge_page * p.Hkv + hk) * p.S + edge_row -
+                                page_index(edge_row) * p.S) * D;
                 else
                     bad = true;
             } else if (g == 2 && given) {
@@ -520,9 +562,10 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const float a = w[h][2 * ks + i][0], c = w[h][2 * ks + i][1];
-                        hi[h][i] = pack_bf16x2(a, c);
-                        lo[h][i] = pack_bf16x2(a - __uint_as_float(hi[h][i] << 16),
-                                               c - __uint_as_float(hi[h][i] & 0xffff0000u));
+                        const uint32_t ua = __float_as_uint(a) & 0xffff0000u, uc = __float_as_uint(c) & 0xffff0000u;
+                        hi[h][i] = __byte_perm(ua, uc, 0x7632);
+                        lo[h][i] = pack_bf16x2(fmaxf(a - __uint_as_float(ua), a * 9.5367431640625e-07f),
+                                               fmaxf(c - __uint_as_float(uc), c * 9.5367431640625e-07f));
                     }
 #pragma unroll
                 for (int i = 0; i < ON / 2; ++i) {
@@ -758,7 +801,9 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
             p.joins[p.by_segment ? segment : worker] =
                 make_int4(whole ? -1 : segment, (int)worker, (int)cut.worker_of(end - 1), u0 < now.s0 ? 1 : 0);
         }
-    } while (next_part(now, cut, u0, u1, p.seqlens, KT, most, heads));
+        if (!next_part(now, cut, u0, u1, p.seqlens, KT, most, heads)) break;
+        ask();
+    }
 }
 
 // Joins the parts of a segment (a cached head of a sequence and a block of its
@@ -768,42 +813,44 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
 constexpr int kJoinWarps = 8, kJoinWarpsMost = 32;
 
 // Adds the parts first, first + step, ... of one query head into (M, L, o),
-// `mine` columns per lane.
+// V = D / 32 columns per lane, a batch of loads at a time.
 template <int D>
 __device__ __forceinline__ void add_parts(const PagedParams &p, int c0, int c1, int first_slot, int row,
                                           int first, int step, float &M, float &L, float (&o)[D / 32]) {
+    constexpr int V = D / 32, kBatch = D == 256 ? 4 : 8;
     const int lane = threadIdx.x & 31;
-    auto slot = [&](int c) { return ((long long)c * 2 + (c == c0 ? first_slot : 0)) * p.HB + row; };
-    // 32 parts at a time: their maxima and sums one per lane, then their columns
-    for (int base = first; base <= c1; base += 32 * step) {
-        const int part = base + lane * step;
-        float m = -INFINITY, l = 0.f;
-        if (part <= c1) {
-            const float2 ml = *reinterpret_cast<const float2 *>(p.part_ml + 2 * slot(part));
-            m = ml.x;
-            l = ml.y;
+    for (int base = first; base <= c1; base += kBatch * step) {
+        float2 ml[kBatch], v[kBatch][V / 2];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int c = base + k * step;
+            ml[k] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int i = 0; i < V / 2; ++i) v[k][i] = make_float2(0.f, 0.f);
+            if (c <= c1) {
+                const long long slot = ((long long)c * 2 + (c == c0 ? first_slot : 0)) * p.HB + row;
+                ml[k] = *reinterpret_cast<const float2 *>(p.part_ml + 2 * slot);
+#pragma unroll
+                for (int i = 0; i < V / 2; ++i)
+                    v[k][i] = *reinterpret_cast<const float2 *>(p.part_o + slot * D + 64 * i + 2 * lane);
+            }
         }
-        float top = m;
+        float top = M;
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-        const float M1 = fmaxf(M, top), f = ex2_approx(M - M1), part_f = ex2_approx(m - M1);
-        float add = part <= c1 ? l * part_f : 0.f;
+        for (int k = 0; k < kBatch; ++k) top = fmaxf(top, ml[k].x);
+        const float f = ex2_approx(M - top);
+        M = top;
+        L *= f;
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) add += __shfl_xor_sync(0xffffffffu, add, off);
-        L = L * f + add;
-        M = M1;
+        for (int i = 0; i < V; ++i) o[i] *= f;
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) o[i] *= f;
-        const int count = min(32, (c1 - base) / step + 1);
-#pragma unroll 8
-        for (int c = 0; c < count; ++c) {
-            const float fc = __shfl_sync(0xffffffffu, part_f, c);
-            const float *po = p.part_o + slot(base + c * step) * D;
+        for (int k = 0; k < kBatch; ++k) {
+            const float fk = ex2_approx(ml[k].x - top);
+            L = fmaf(fk, ml[k].y, L);
 #pragma unroll
-            for (int i = 0; i < D / 32; i += 2) {
-                const float2 v = *reinterpret_cast<const float2 *>(po + 32 * i + 2 * lane);
-                o[i] = fmaf(fc, v.x, o[i]);
-                o[i + 1] = fmaf(fc, v.y, o[i + 1]);
+            for (int i = 0; i < V / 2; ++i) {
+                o[2 * i] = fmaf(fk, v[k][i].x, o[2 * i]);
+                o[2 * i + 1] = fmaf(fk, v[k][i].y, o[2 * i + 1]);
             }
         }
     }
@@ -813,7 +860,7 @@ __device__ __forceinline__ void add_parts(const PagedParams &p, int c0, int c1, 
 // its warps taking every gridDim-th part each.  By worker: a block per worker,
 // for the segment that begins there, a warp per query head (few parts).
 template <int D>
-__global__ void join_kernel(const PagedParams p) {
+__global__ void __launch_bounds__(kJoinWarpsMost * 32) join_kernel(const PagedParams p) {
     __shared__ float s_o[kJoinWarpsMost][D], s_m[kJoinWarpsMost], s_l[kJoinWarpsMost];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int heads = p.Hkv * p.GB;
@@ -855,14 +902,20 @@ __global__ void join_kernel(const PagedParams p) {
         s_l[warp] = L;
     }
     __syncthreads();
-    float top = s_m[0];
-    for (int i = 1; i < warps; ++i) top = fmaxf(top, s_m[i]);
-    float total = 0.f;
-    for (int i = 0; i < warps; ++i) total = fmaf(ex2_approx(s_m[i] - top), s_l[i], total);  // 0 without parts
+    // each warp for itself: lane i has warp i's factor, 0 where it had no parts
+    const float m = lane < warps ? s_m[lane] : -INFINITY;
+    float top = m;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    const float f = ex2_approx(m - top);
+    float total = lane < warps ? f * s_l[lane] : 0.f;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
     const float inv = 1.0f / total;
-    for (int col = threadIdx.x; col < D; col += blockDim.x) {
+    for (int col = threadIdx.x; col < D; col += blockDim.x) {  // D is a multiple of 32: whole warps
         float v = 0.f;
-        for (int i = 0; i < warps; ++i) v = fmaf(ex2_approx(s_m[i] - top), s_o[i][col], v);
+#pragma unroll 8
+        for (int i = 0; i < warps; ++i) v = fmaf(__shfl_sync(0xffffffffu, f, i), s_o[i][col], v);
         p.out[(out0 + row) * D + col] = __float2bfloat16_rn(v * inv);
     }
     if (threadIdx.x == 0 && p.lse) p.lse[out0 + row] = (top + log2f(total)) * kLn2;
