@@ -1,7 +1,9 @@
-"""Builds libcsa.so in-tree with nvcc for sm_103a.
+"""Builds libcsa.so in-tree with nvcc for sm_103a, and the CPython module
+_csa_torch (csrc/csa_torch.cpp) that calls it on torch tensors.
 
 Twelve translation units compiled in parallel, then linked into one shared
-library next to this file.  The CUDA runtime is linked statically; the CUDA
+library next to this file; the module is compiled beside them against torch's
+headers and linked against that library.  The CUDA runtime is linked statically; the CUDA
 driver is reached at run time through the runtime's driver entry points, so
 the library loads on a machine without a GPU driver (calls then fail with
 CSA_ERR_NO_DEVICE).
@@ -22,6 +24,8 @@ LIB_PATH = os.path.join(HERE, "libcsa.so")
 SOURCES = ["csa_api.cu", "csa_simt.cu", "csa_tc.cu", "csa_tc_std.cu", "csa_decode.cu",
            "csa_bwd_simt.cu", "csa_tc_bwd.cu", "csa_host.cu", "csa_noalloc.cu", "csa_paged.cu",
            "csa_rope.cu", "csa_cache.cu"]
+TORCH_SOURCE = "csa_torch.cpp"
+TORCH_LIB_PATH = os.path.join(HERE, "_csa_torch.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -54,8 +58,10 @@ def build(verbose: bool = False, extra_flags=()) -> str:
             print(res.stdout + res.stderr, flush=True)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        module = ex.submit(compile_module, build_dir, verbose)
         objs = list(ex.map(compile_one, SOURCES))
+        module_obj = module.result()
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     cmd = [nvcc] + ARCH + ["-shared", "-o", tmp] + objs + ["-lcudart_static", "-ldl", "-lpthread", "-lrt"]
     if verbose:
@@ -64,7 +70,41 @@ def build(verbose: bool = False, extra_flags=()) -> str:
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, LIB_PATH)
+    link_module(module_obj, verbose)
     return LIB_PATH
+
+
+def _run(cmd, verbose, what):
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{res.stdout}\n{res.stderr}")
+
+
+def compile_module(build_dir, verbose=False):
+    import sysconfig
+
+    import torch
+
+    base = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
+    obj = os.path.join(build_dir, TORCH_SOURCE.replace(".cpp", ".o"))
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          "-I", INCLUDE, "-isystem", base, "-isystem", os.path.join(base, "torch", "csrc", "api", "include"),
+          "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda, "-c", os.path.join(CSRC, TORCH_SOURCE),
+          "-o", obj], verbose, f"g++ on {TORCH_SOURCE}")
+    return obj
+
+
+def link_module(obj, verbose=False):
+    import torch
+
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = TORCH_LIB_PATH + f".tmp{os.getpid()}"
+    _run(["g++", "-shared", "-o", tmp, obj, "-L" + HERE, "-l:" + os.path.basename(LIB_PATH), "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-lc10",
+          "-lc10_cuda", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib], verbose, "link of _csa_torch.so")
+    os.replace(tmp, TORCH_LIB_PATH)
 
 
 if __name__ == "__main__":

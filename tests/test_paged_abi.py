@@ -19,6 +19,10 @@ END = OK if torch.cuda.is_available() else L.CSA_ERR_NO_DEVICE
 IMAX = 2 ** 31 - 1
 
 
+def ref(plan):
+    return ctypes.byref(plan._plan)
+
+
 @pytest.fixture(scope="module")
 def lib():
     import os
@@ -70,7 +74,7 @@ def rope(lib, plan, *, q=FAKE, qo=FAKE, k=FAKE, ko=FAKE, pos=FAKE, B=2, Hq=4, Hk
 
 
 def test_rope_refusals(lib):
-    plan = csa.RopeAxes(64, (10, 22))._ref
+    plan = ref(csa.RopeAxes(64, (10, 22)))
     for kw in (dict(q=NULL), dict(qo=NULL), dict(k=NULL), dict(pos=NULL), dict(B=-1), dict(T=-1), dict(d=0), dict(d=63), dict(Hkv=-1)):
         assert rope(lib, plan, **kw) == INV, kw
     assert rope(lib, NULL) == INV
@@ -81,10 +85,10 @@ def test_rope_refusals(lib):
     for field, value in (("pairs", 0), ("pairs", 129), ("axes", 0), ("axes", 9)):
         broken = csa.RopeAxes(64, (10, 22))
         setattr(broken._plan, field, value)
-        assert rope(lib, broken._ref) == INV
+        assert rope(lib, ref(broken)) == INV
     broken = csa.RopeAxes(64, (10, 22))
     broken._plan.axis[5] = 2
-    assert rope(lib, broken._ref) == INV
+    assert rope(lib, ref(broken)) == INV
 
 
 def test_rope_plan():
@@ -128,7 +132,7 @@ def append(lib, *, plan=NULL, q=NULL, qo=NULL, k=FAKE, v=FAKE, kp=FAKE, vp=FAKE,
 
 
 def test_append_refusals(lib):
-    plan = csa.RopeAxes(64, (32,))._ref
+    plan = ref(csa.RopeAxes(64, (32,)))
     for kw in (dict(k=NULL), dict(v=NULL), dict(kp=NULL), dict(table=NULL), dict(lens=NULL), dict(Hkv=0), dict(S=0), dict(M=0), dict(d=0),
                dict(Hq=2), dict(plan=plan, Hq=2), dict(plan=plan, d=62), dict(T=-1)):
         assert append(lib, **kw) == INV, kw
@@ -169,7 +173,7 @@ def test_page_calls_refuse(lib):
 
 
 def test_valid_calls_reach_the_device_check(lib, no_gpu):
-    plan = csa.RopeAxes(64, (32,))._ref
+    plan = ref(csa.RopeAxes(64, (32,)))
     assert rope(lib, plan) == END and append(lib) == END and append(lib, plan=plan, Hq=2, q=FAKE, qo=FAKE) == END
     assert lib.csa_cache_reserve(*[FAKE] * 5, 2, 10, 16, 4, None) == END
     assert lib.csa_cache_free(FAKE, FAKE, FAKE, FAKE, 1, 2, 10, 16, 4, None) == END
@@ -184,6 +188,15 @@ def test_cpu_tensors_are_refused():
                  lambda: csa.decode_paged(x[:, :, 0], x, x, i[None], i[:1])):
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+def test_missing_module_is_reported(monkeypatch):
+    monkeypatch.setattr(_paged, "_native", _paged._Unloaded())
+    monkeypatch.setitem(__import__("sys").modules, "continuous_softmax_attention_gb300._csa_torch", None)
+    monkeypatch.delattr(csa, "_csa_torch", raising=False)
+    x = torch.zeros(1, 2, 3, 64, dtype=torch.bfloat16)
+    with pytest.raises(RuntimeError, match="build it"):
+        csa.rope(x, None, torch.zeros(1, 1, 3, dtype=torch.int32), csa.RopeAxes(64, (32,)))
 
 
 def test_host_model_of_the_pages():
