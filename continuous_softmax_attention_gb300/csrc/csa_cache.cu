@@ -17,8 +17,11 @@
 
 #include "csa.h"
 #include "csa_internal.h"
+#include "csa_launch.cuh"
 
 namespace {
+
+using namespace csa_dev;
 
 constexpr int kBookThreads = 1024;
 constexpr int kBookWarps = kBookThreads / 32;
@@ -109,6 +112,7 @@ __device__ __forceinline__ int pages_of(int n, int S) { return (int)(((long long
 __global__ void __launch_bounds__(kBookThreads)
 reserve_kernel(int *refs, int *table, int *seqlens, const int *counts, int *shortfall, int B, int P,
                int S, int M) {
+    after_previous();
     __shared__ int sums[32], list[kList], before[kBookThreads];
     const int tid = threadIdx.x, per = (B + kBookThreads - 1) / kBookThreads;
     const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
@@ -174,6 +178,7 @@ reserve_kernel(int *refs, int *table, int *seqlens, const int *counts, int *shor
 // rows first (a length that another block has already set to 0 is sound).
 __global__ void __launch_bounds__(256)
 free_kernel(int *refs, int *table, int *seqlens, const int *rows, int R, int B, int P, int S, int M) {
+    after_previous();
     const int me = blockIdx.x, row = rows[me];
     bool bad = false, earlier = false;
     for (int i = threadIdx.x; i < R; i += blockDim.x) {
@@ -243,6 +248,7 @@ static_assert(CSA_CACHE_MAX_FORKS <= kList, "the pages taken wait in shared memo
 __global__ void __launch_bounds__(kBookThreads)
 fork_plan_kernel(int *refs, int *table, int *seqlens, const int *parents, const int *children, int n,
                  int *src, int *dst, int *shortfall, int B, int P, int S, int M, bool rows) {
+    after_previous();
     __shared__ int sums[32], list[kList];
     const int tid = threadIdx.x;
     int p[kPairs], c[kPairs], len[kPairs], page[kPairs], rank[kPairs];
@@ -323,6 +329,7 @@ fork_plan_kernel(int *refs, int *table, int *seqlens, const int *parents, const 
 __global__ void __launch_bounds__(256)
 fork_rows_kernel(int *refs, int *table, const int *seqlens, const int *parents, const int *children,
                  const int *dst, const int *shortfall, int P, int S, int M) {
+    after_previous();
     const int i = blockIdx.x, p = parents[i], c = children[i];
     if (*shortfall != 0 || p < 0 || c < 0) return;
     fork_row(refs, table, p, c, seqlens[c], dst[i], P, S, M, threadIdx.x, blockDim.x);
@@ -363,6 +370,7 @@ __device__ __forceinline__ void rename_row(int *table, const int *seqlens, int b
 __global__ void __launch_bounds__(kBookThreads)
 compact_plan_kernel(int *refs, int *table, const int *seqlens, int *src, int *dst, int *moved, int B, int P,
                     int S, int M, bool rows) {
+    after_previous();
     __shared__ int sums[32];
     const int tid = threadIdx.x, all = 0x7fffffff;
     const int U = walk(refs, 0, P, all, sums, Held(), [](int, int) {});
@@ -383,6 +391,7 @@ compact_plan_kernel(int *refs, int *table, const int *seqlens, int *src, int *ds
 __global__ void __launch_bounds__(256)
 rename_kernel(int *table, const int *seqlens, const int *src, const int *dst, const int *moved, int B, int S,
               int M) {
+    after_previous();
     const int K = *moved;
     for (int b = blockIdx.x; b < B; b += gridDim.x)
         rename_row(table, seqlens, b, src, dst, K, S, M, threadIdx.x, blockDim.x);
@@ -398,6 +407,7 @@ template <typename C>
 __global__ void __launch_bounds__(kCopyThreads)
 copy_pages_kernel(C *k_pages, C *v_pages, long long page, int layers, int P, const int *src,
                   const int *dst, int n, const int *count, int parts) {
+    after_previous();
     if (count) n = min(n, *count);
     const int pools = v_pages ? 2 : 1;
     const long long per_pair = (long long)layers * pools * parts, items = n * per_pair;
@@ -425,6 +435,8 @@ copy_pages_kernel(C *k_pages, C *v_pages, long long page, int layers, int P, con
     }
 }
 
+int from(cudaError_t e) { return e == cudaSuccess ? CSA_OK : CSA_ERR_CUDA; }
+
 template <typename C>
 int copy_as(void *k, void *v, long long page_bytes, int layers, int P, const int *src,
             const int *dst, int n, const int *count, cudaStream_t stream) {
@@ -432,48 +444,45 @@ int copy_as(void *k, void *v, long long page_bytes, int layers, int P, const int
     const long long part = kCopyThreads * kCopyDeep, parts = (page + part - 1) / part;
     if (parts * layers * 2 > 0x7fffffffLL) return CSA_ERR_UNSUPPORTED;
     const long long items = parts * layers * (v ? 2 : 1) * n;
-    const unsigned grid = (unsigned)(items < 152 * 8 ? items : 152 * 8);
-    copy_pages_kernel<C><<<grid, kCopyThreads, 0, stream>>>(
-        static_cast<C *>(k), static_cast<C *>(v), page, layers, P, src, dst, n, count, (int)parts);
-    return cudaGetLastError() == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
+    const unsigned grid = (unsigned)(items < 152 * 32 ? items : 152 * 32);
+    return from(launch_after_previous(copy_pages_kernel<C>, grid, kCopyThreads, 0, stream, static_cast<C *>(k),
+                                      static_cast<C *>(v), page, layers, P, src, dst, n, count, (int)parts));
 }
-
-int launched() { return cudaGetLastError() == cudaSuccess ? CSA_OK : CSA_ERR_CUDA; }
 
 }  // namespace
 
 int csa_cache_reserve_run(int *refs, int *table, int *seqlens, const int *counts, int *shortfall, int B,
                           int P, int S, int M, cudaStream_t stream) {
-    reserve_kernel<<<1, kBookThreads, 0, stream>>>(refs, table, seqlens, counts, shortfall, B, P, S, M);
-    return launched();
+    return from(launch_after_previous(reserve_kernel, 1, kBookThreads, 0, stream, refs, table, seqlens, counts,
+                                      shortfall, B, P, S, M));
 }
 
 int csa_cache_free_run(int *refs, int *table, int *seqlens, const int *rows, int R, int B, int P,
                        int S, int M, cudaStream_t stream) {
-    free_kernel<<<R, 256, 0, stream>>>(refs, table, seqlens, rows, R, B, P, S, M);
-    return launched();
+    return from(launch_after_previous(free_kernel, R, 256, 0, stream, refs, table, seqlens, rows, R, B, P, S, M));
 }
 
 int csa_cache_fork_run(int *refs, int *table, int *seqlens, const int *parents, const int *children,
                        int n, int *src, int *dst, int *shortfall, int B, int P, int S, int M,
                        cudaStream_t stream) {
     const bool one = (long long)n * M <= kOneBlock;
-    fork_plan_kernel<<<1, kBookThreads, 0, stream>>>(refs, table, seqlens, parents, children, n, src, dst,
-                                                     shortfall, B, P, S, M, one);
-    if (launched() != CSA_OK) return CSA_ERR_CUDA;
+    if (launch_after_previous(fork_plan_kernel, 1, kBookThreads, 0, stream, refs, table, seqlens, parents, children, n,
+                              src, dst, shortfall, B, P, S, M, one) != cudaSuccess)
+        return CSA_ERR_CUDA;
     if (one) return CSA_OK;
-    fork_rows_kernel<<<n, 256, 0, stream>>>(refs, table, seqlens, parents, children, dst, shortfall, P, S, M);
-    return launched();
+    return from(launch_after_previous(fork_rows_kernel, n, 256, 0, stream, refs, table, seqlens, parents, children, dst,
+                                      shortfall, P, S, M));
 }
 
 int csa_cache_compact_run(int *refs, int *table, const int *seqlens, int *src, int *dst, int *moved, int B,
                           int P, int S, int M, cudaStream_t stream) {
     const bool one = (long long)B * M <= kOneBlock;
-    compact_plan_kernel<<<1, kBookThreads, 0, stream>>>(refs, table, seqlens, src, dst, moved, B, P, S, M, one);
-    if (launched() != CSA_OK) return CSA_ERR_CUDA;
+    if (launch_after_previous(compact_plan_kernel, 1, kBookThreads, 0, stream, refs, table, seqlens, src, dst, moved, B,
+                              P, S, M, one) != cudaSuccess)
+        return CSA_ERR_CUDA;
     if (one) return CSA_OK;
-    rename_kernel<<<B < 152 * 8 ? B : 152 * 8, 256, 0, stream>>>(table, seqlens, src, dst, moved, B, S, M);
-    return launched();
+    return from(launch_after_previous(rename_kernel, B < 152 * 8 ? B : 152 * 8, 256, 0, stream, table, seqlens, src, dst,
+                                      moved, B, S, M));
 }
 
 int csa_cache_copy_pages_run(void *k_pages, void *v_pages, long long page_bytes, int layers, int P,

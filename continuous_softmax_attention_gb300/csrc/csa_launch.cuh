@@ -1,0 +1,31 @@
+// Launches that overlap the end of the kernel before them on the stream: the
+// blocks may be placed while that kernel finishes, and every thread calls
+// after_previous() before it touches memory, which returns once that kernel is
+// done and its writes are visible.  Worth 0.5 to 1 us a launch between the
+// short kernels of a decode step.
+#pragma once
+
+#include <cuda_runtime.h>
+
+namespace csa_dev {
+
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... P, typename... A>
+inline cudaError_t launch_after_previous(void (*kernel)(P...), dim3 grid, int threads, size_t smem,
+                                         cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+    return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+}  // namespace csa_dev

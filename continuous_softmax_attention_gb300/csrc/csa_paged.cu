@@ -41,6 +41,7 @@
 #include "csa.h"
 #include "csa_device.cuh"
 #include "csa_internal.h"
+#include "csa_launch.cuh"
 #include "csa_tc_common.cuh"
 
 namespace {
@@ -334,14 +335,15 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
     const long long most = (long long)p.M * p.S;
     volatile int *abort_flag = &s_abort[warp];
 
-    const bool few = p.B <= 32;  // sequences: every warp forms the cut
-    const int lane_n = few && lane < p.B ? p.seqlens[lane] : 0;
     if (lane == 0) {
         for (int s = 0; s < kStages; ++s) mbar_init(smem_u32(&bars[warp][s]), 1);
         fence_mbar_init();
         s_abort[warp] = 0;
     }
     __syncwarp();
+    after_previous();
+    const bool few = p.B <= 32;  // sequences: every warp forms the cut
+    const int lane_n = few && lane < p.B ? p.seqlens[lane] : 0;
     // the join's blocks may take their places as this kernel's blocks end
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const long long all = (long long)C::Warps * gridDim.x;
@@ -865,7 +867,7 @@ __global__ void __launch_bounds__(kJoinWarpsMost * 32) join_kernel(const PagedPa
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int heads = p.Hkv * p.GB;
     // every block waits: this kernel must not end before the one that forms the parts
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    after_previous();
     const int4 seg = p.joins[blockIdx.x];
     // none; or left over, where a wait ran out and the parts are undefined anyway
     if (seg.x < 0 || seg.x >= p.B * heads || seg.y < 0 || seg.z < seg.y || seg.z >= workers(D)) return;
@@ -956,20 +958,13 @@ int launch(PagedParams &p, cudaStream_t stream) {
         return CSA_ERR_CUDA;
     const long long segments = (long long)p.B * heads, all = (long long)grid * C::Warps;
     p.by_segment = segments <= kGrid;
-    kern<<<grid, C::Warps * 32, C::Smem, stream>>>(p, map_k, map_v);
+    if (launch_after_previous(kern, grid, C::Warps * 32, C::Smem, stream, p, map_k, map_v) != cudaSuccess)
+        return CSA_ERR_CUDA;
     // parts of a segment, at most about
     const long long parts = all / segments;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = p.by_segment ? dim3((unsigned)segments, (unsigned)p.HB) : dim3((unsigned)all);
-    cfg.blockDim = dim3(32 * (p.by_segment && parts > 64 ? kJoinWarpsMost : kJoinWarps));
-    cfg.stream = stream;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    if (cudaLaunchKernelEx(&cfg, join_kernel<D>, p) != cudaSuccess) return CSA_ERR_CUDA;
-    return cudaGetLastError() == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
+    const dim3 blocks = p.by_segment ? dim3((unsigned)segments, (unsigned)p.HB) : dim3((unsigned)all);
+    const int threads = 32 * (p.by_segment && parts > 64 ? kJoinWarpsMost : kJoinWarps);
+    return launch_after_previous(join_kernel<D>, blocks, threads, 0, stream, p) == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
 }
 
 // Blocks of the query heads of a group, at most 16 each, as equal as can be.

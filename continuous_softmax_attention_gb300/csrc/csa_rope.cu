@@ -30,6 +30,7 @@
 
 #include "csa.h"
 #include "csa_internal.h"
+#include "csa_launch.cuh"
 
 namespace {
 
@@ -110,6 +111,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rope_kernel(const __grid_co
         turn[i] = p.plan.turn[i];
         axis[i] = p.plan.axis[i];
     }
+    csa_dev::after_previous();
     __syncthreads();
     const int rest = (p.d - 2 * n) / V;  // chunks that are not rotated
     const int units = n / V + (rest + 1) / 2, rows = kThreads / units;
@@ -218,18 +220,10 @@ int launch(RopeParams &p, cudaStream_t stream) {
     const int by = all();
     const dim3 grid((unsigned)bx, (unsigned)by);
     const bool adj = p.plan.adjacent != 0;
-    if (p.k_pages) {
-        if (adj)
-            rope_kernel<T, V, true, true><<<grid, kThreads, 0, stream>>>(p);
-        else
-            rope_kernel<T, V, false, true><<<grid, kThreads, 0, stream>>>(p);
-    } else {
-        if (adj)
-            rope_kernel<T, V, true, false><<<grid, kThreads, 0, stream>>>(p);
-        else
-            rope_kernel<T, V, false, false><<<grid, kThreads, 0, stream>>>(p);
-    }
-    return cudaGetLastError() == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
+    auto kernel = p.k_pages ? adj ? rope_kernel<T, V, true, true> : rope_kernel<T, V, false, true>
+                  : adj     ? rope_kernel<T, V, true, false>
+                            : rope_kernel<T, V, false, false>;
+    return csa_dev::launch_after_previous(kernel, grid, kThreads, 0, stream, p) == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
 }
 
 bool on16(const void *q) { return reinterpret_cast<uintptr_t>(q) % 16 == 0; }
