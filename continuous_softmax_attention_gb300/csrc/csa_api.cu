@@ -237,7 +237,8 @@ constexpr long long kIntMax = 0x7fffffffLL;
 // Sizes of a paged cache's tables.
 int check_tables(int B, int P, int S, int M) {
     if (B < 0 || P < 0 || S < 1 || M < 1) return CSA_ERR_INVALID_ARG;
-    if ((long long)B * M > kIntMax || (long long)M * S > kIntMax) return CSA_ERR_UNSUPPORTED;
+    // rows are counted in ints, rounded up to tiles of 16
+    if ((long long)B * M > kIntMax || (long long)M * S > kIntMax - 15) return CSA_ERR_UNSUPPORTED;
     return CSA_OK;
 }
 
@@ -295,7 +296,7 @@ int append_any(const csa_rope_plan *plan, const void *q, const long long *q_stri
     if (d > 256 || (long long)B * T > kIntMax || (long long)Hq + 2LL * Hkv > 65535)
         return CSA_ERR_UNSUPPORTED;
     if ((long long)B * T == 0) return CSA_OK;
-    if (!k || !v || !k_pages || !v_pages || !block_table || !seqlens || (Hq > 0 && (!q || !q_out)))
+    if (!k || !v || (P > 0 && (!k_pages || !v_pages)) || !block_table || !seqlens || (Hq > 0 && (!q || !q_out)))
         return CSA_ERR_INVALID_ARG;
     const uintptr_t al = bf16 ? 2 : 4;
     if (!aligned(q, al) || !aligned(q_out, al) || !aligned(k, al) || !aligned(v, al) ||
@@ -332,7 +333,7 @@ int csa_decode_paged(const void *q, const void *k_pages, const void *v_pages, co
     if ((long double)P * Hkv * S > kIntMax) return CSA_ERR_UNSUPPORTED;
     if ((long long)B * Hq > kIntMax) return CSA_ERR_UNSUPPORTED;
     if ((long long)B * Hq == 0) return CSA_OK;
-    if (!q || !k_pages || !v_pages || !block_table || !seqlens || !out) return CSA_ERR_INVALID_ARG;
+    if (!q || (P > 0 && (!k_pages || !v_pages)) || !block_table || !seqlens || !out) return CSA_ERR_INVALID_ARG;
     if (k0_mode == CSA_K0_GIVEN && (!k0 || !v0)) return CSA_ERR_INVALID_ARG;
     const long long need = csa_decode_paged_scratch_bytes(B, Hq, Hkv, d);
     if (need < 0) return CSA_ERR_UNSUPPORTED;

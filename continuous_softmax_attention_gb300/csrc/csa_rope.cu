@@ -55,7 +55,7 @@ struct RopeParams {
     float sign;
     int heads_per_block;
     int blocks[2];  // blocks of heads of the queries, and of the keys
-    // pages of keys (x[1]) and values (x[2]); null: every tensor goes to its out
+    bool paged;  // keys (x[1]) and values (x[2]) go to pages; else every tensor to its out
     void *k_pages, *v_pages;
     const int *table, *seqlens, *counts;
     int P, S, M;
@@ -220,9 +220,9 @@ int launch(RopeParams &p, cudaStream_t stream) {
     const int by = all();
     const dim3 grid((unsigned)bx, (unsigned)by);
     const bool adj = p.plan.adjacent != 0;
-    auto kernel = p.k_pages ? adj ? rope_kernel<T, V, true, true> : rope_kernel<T, V, false, true>
-                  : adj     ? rope_kernel<T, V, true, false>
-                            : rope_kernel<T, V, false, false>;
+    auto kernel = p.paged ? adj ? rope_kernel<T, V, true, true> : rope_kernel<T, V, false, true>
+                  : adj   ? rope_kernel<T, V, true, false>
+                          : rope_kernel<T, V, false, false>;
     return csa_dev::launch_after_previous(kernel, grid, kThreads, 0, stream, p) == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
 }
 
@@ -238,10 +238,9 @@ bool wide(const RopeTensor &x, int V, bool has_out) {
 template <typename T>
 int run(RopeParams &p, cudaStream_t stream) {
     constexpr int V = 16 / (int)sizeof(T);
-    const bool paged = p.k_pages != nullptr;
     const bool ok = p.d % V == 0 && p.plan.pairs % V == 0 && wide(p.x[0], V, true) &&
-                    wide(p.x[1], V, !paged) && wide(p.x[2], V, !paged) &&
-                    (!paged || (on16(p.k_pages) && on16(p.v_pages)));
+                    wide(p.x[1], V, !p.paged) && wide(p.x[2], V, !p.paged) &&
+                    (!p.paged || (on16(p.k_pages) && on16(p.v_pages)));
     return ok ? launch<T, V>(p, stream) : launch<T, 1>(p, stream);
 }
 
@@ -336,6 +335,7 @@ int csa_cache_append_run(const csa_rope_plan *plan, const void *q, const long lo
     p.T = T;
     p.d = d;
     p.sign = 1.0f;
+    p.paged = true;
     p.k_pages = k_pages;
     p.v_pages = v_pages;
     p.table = block_table;

@@ -420,7 +420,7 @@ int csa_decode_merge_ranges(const float *o_parts, const float *lse_parts, int R,
  * Paged key-value caches
  * ----------------------
  *  Pools      k_pages, v_pages: contiguous [P, Hkv, S, d], P pages of S rows
- *             for each of Hkv cached heads.
+ *             for each of Hkv cached heads (NULL allowed with P = 0).
  *  Tables     block_table: contiguous int32 [B, M]; row b holds the page
  *             numbers of sequence b in order, its token i being row i mod S
  *             of page block_table[b][i / S].  seqlens: int32 [B], tokens held.
@@ -434,8 +434,8 @@ int csa_decode_merge_ranges(const float *o_parts, const float *lse_parts, int R,
  *  numbers, rows) are checked on the device: what each call does with bad
  *  ones is said there, no access goes out of bounds, and the sticky status
  *  word (csa_device_status) records CSA_ERR_INVALID_ARG.
- *  S, M >= 1; B * M and M * S at most 2^31 - 1 (CSA_ERR_UNSUPPORTED).  The
- *  pages of the method have no counterpart to any of these entry points but
+ *  S, M >= 1; B * M at most 2^31 - 1 and M * S at most 2^31 - 16
+ *  (CSA_ERR_UNSUPPORTED).  The pages of the method have no counterpart to any of these entry points but
  *  csa_decode_paged.
  */
 

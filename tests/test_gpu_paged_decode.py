@@ -148,11 +148,62 @@ def test_pages_hold_anything_behind_the_last_token():
     assert torch.equal(o, want) and torch.equal(lse, wl)
 
 
-def test_infinite_values_in_the_cache_pass_through():
-    x = make([50], 1, 1, 128, 16, seed=10)
-    x["v"][x["table"][0, 1], 0, 3, 5] = float("inf")
-    o, _ = run(x, 0)
-    assert torch.isposinf(o[0, 0, 5]) and torch.isfinite(o[0, 0, :5].float()).all()
+@pytest.mark.parametrize("Hq", [1, 8, 16])
+@pytest.mark.parametrize("scale", [0.0, 0.1])
+def test_infinite_values_in_the_cache_pass_through(Hq, scale):
+    # scale 0: the weights are exact in bf16
+    x = make([50, 2000], Hq, 1, 128, 16, seed=10)
+    for b, n in ((0, 1), (1, 100)):
+        x["v"][x["table"][b, n], 0, 3, 5], x["v"][x["table"][b, n], 0, 4, 6] = float("inf"), float("-inf")
+    o, _ = run(x, 0, scale)
+    assert torch.isposinf(o[:, :, 5]).all() and torch.isneginf(o[:, :, 6]).all()
+    assert torch.isfinite(o[:, :, 7:].float()).all()
+
+
+def test_sequences_that_share_pages():
+    x = make([200, 75, 200], 4, 2, 64, 16, seed=30)
+    x["table"][1, :5] = x["table"][0, :5]
+    x["table"][2] = x["table"][0]
+    o, lse = run(x, 2)
+    check(x, o, lse, 16, 2, 64 ** -0.5)
+
+
+def test_no_pool():
+    e = torch.zeros(0, 2, 16, 64, dtype=torch.bfloat16, device="cuda")
+    q = torch.ones(3, 4, 64, dtype=torch.bfloat16, device="cuda")
+    table = torch.full((3, 2), -1, dtype=torch.int32, device="cuda")
+    o, lse = decode_paged(q, e, e, table, torch.zeros(3, dtype=torch.int32, device="cuda"))
+    assert not o.any() and torch.isneginf(lse).all() and device_status() == 0
+    o, lse = decode_paged(q, e, e, table, torch.tensor([0, 5, 40], dtype=torch.int32, device="cuda"))
+    assert not o[0].any() and torch.isnan(o[1:].float()).all() and device_status() == -1
+    table.zero_()
+    o, lse = decode_paged(q, e, e, table, torch.tensor([0, 5, 40], dtype=torch.int32, device="cuda"))
+    assert torch.isnan(o[1:].float()).all() and device_status() == -1
+
+
+def test_pages_beyond_32_bits():
+    # pools of 2.3e9 elements (4.7 GB); the sequences' pages lie at both ends
+    P, Hkv, S, d = 72000, 4, 64, 128
+    lens = [300, 1000, 64]
+    x = make(lens, 8, Hkv, d, S, seed=31)
+    far = {p: (P - 1 - p if p % 2 else p) for p in range(x["k"].shape[0])}
+    k, v = (torch.empty(P, Hkv, S, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    for p, f in far.items():
+        k[f], v[f] = x["k"][p].cuda(), x["v"][p].cuda()
+    table = torch.as_tensor([[far.get(int(e), -1) for e in row] for row in x["table"]], dtype=torch.int32).cuda()
+    n = torch.tensor(lens, dtype=torch.int32).cuda()
+    o, lse = decode_paged(x["q"].cuda(), k, v, table, n)
+    check(x, o, lse, S, 0, d ** -0.5)
+    # the same pages by the other calls: rows written at the far end, and pages copied there
+    from continuous_softmax_attention_gb300 import cache_append, cache_copy_pages
+
+    new = torch.randn(3, Hkv, 1, d, device="cuda").to(torch.bfloat16)
+    cache_append(new, new, k, v, table, n)
+    for b, m in enumerate(lens):
+        assert torch.equal(k[table[b, (m - 1) // S], :, (m - 1) % S], new[b, :, 0])
+    cache_copy_pages(k, v, torch.tensor([0], dtype=torch.int32).cuda(), torch.tensor([P - 2], dtype=torch.int32).cuda())
+    assert torch.equal(k[P - 2], k[0]) and torch.equal(v[P - 2], v[0])
+    assert device_status() == 0
 
 
 def test_bad_lengths_and_pages_are_reported():

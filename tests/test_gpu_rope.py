@@ -211,6 +211,19 @@ def test_append_of_bad_state_writes_nothing_there():
     assert torch.equal(kp, before)
 
 
+def test_append_without_a_pool():
+    _, k, v = tensors(2, 3, 2, 2, 64, "bf16", 20, False)
+    e = torch.zeros(0, 2, 16, 64, dtype=torch.bfloat16, device="cuda")
+    ints = dict(dtype=torch.int32, device="cuda")
+    plan = RopeAxes(64, (32,))
+    q, _, _ = tensors(2, 3, 2, 2, 64, "bf16", 21, False)
+    qo = cache_append(k, v, e, e, torch.zeros(2, 1, **ints), torch.full((2,), 3, **ints), rope=plan, q=q)
+    same(qo, q, rotated(q, torch.arange(3).expand(1, 2, 3), (32,)))
+    assert device_status() == -1
+    cache_append(k, v, e, e, torch.zeros(2, 1, **ints), torch.zeros(2, **ints), counts=torch.zeros(2, **ints))
+    assert device_status() == 0
+
+
 def test_refusals():
     plan = RopeAxes(64, (16, 16))
     q, k, v = tensors(2, 3, 2, 2, 64, "bf16", 13, False)

@@ -52,7 +52,7 @@ def test_decode_paged_refusals(lib):
                dict(scale=math.inf), dict(q=NULL), dict(v=NULL), dict(table=NULL), dict(lens=NULL), dict(out=NULL), dict(ws=NULL),
                dict(nbytes=need - 1), dict(mode=2)):
         assert decode(lib, **kw) == INV, kw
-    for kw in (dict(d=96), dict(S=12), dict(M=IMAX, B=1), dict(B=2 ** 20, M=2 ** 12), dict(P=2 ** 27, S=16)):
+    for kw in (dict(d=96), dict(S=12), dict(M=IMAX, B=1), dict(M=2 ** 27, S=16, B=1), dict(B=2 ** 20, M=2 ** 12), dict(P=2 ** 27, S=16)):
         assert decode(lib, **kw) == UNS, kw
     for kw in (dict(q=ODD), dict(k=ODD), dict(ws=ODD), dict(lens=ODD), dict(table=ODD), dict(mode=2, k0=ODD, v0=FAKE), dict(lse=ODD)):
         assert decode(lib, **kw) == ALI, kw
