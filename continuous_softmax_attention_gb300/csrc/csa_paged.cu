@@ -26,11 +26,15 @@
 //    warp that needs them.
 //  - The weights enter the second product as a sum of two bf16 numbers (15
 //    bits of the weight), the high part cut off so that neither is negative
-//    and the low one at least 2^-20 of the weight: an infinite value stays one.  For up to 8 heads both halves fit one instruction:
-//    rows 0..7 hold the high parts and rows 8..15 the low ones.
-//  - A part of a sequence leaves its unnormalised sums, maximum and weight sum
-//    in the workspace; a second kernel, launched early, joins the parts in
-//    order.  A sequence that one worker had whole is written at once.
+//    and the low one at least 2^-20 of the weight: an infinite value stays one.
+//    For up to 8 heads both halves fit one instruction: rows 0..7 hold the high
+//    parts and rows 8..15 the low ones.
+//  - Few short sequences are bound by latency: a cluster of blocks then does one
+//    cached head of one sequence in a single launch and joins its parts through
+//    distributed shared memory (8.7 -> 5.8 us for 32 heads of 333 tokens).
+//  - Otherwise a part of a sequence leaves its unnormalised sums, maximum and
+//    weight sum in the workspace; a second kernel, launched early, joins the
+//    parts in order.  A sequence that one worker had whole is written at once.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -61,6 +65,16 @@ constexpr int kFew = 2;
 // of 1 to 8192 tokens take 63.1 us with 1, 59.7 with 2, 59.5 with 3, 32 of 333
 // tokens 14.4, 13.4 and 14.2 us.
 constexpr int kPartCost = 2;
+// The one-kernel form: clusters of 1, 2, 4 and 8 blocks that run at a time.
+constexpr int kOneAtATime[4] = {152, 76, 36, 15};
+// ... and tiles per warp that the longest sequence may have in it, where it
+// keeps at least 3/4 of the SMs busy and where it does not.  Measured, this form and the other, equal lengths: 32 heads of
+// 2048 tokens (4 tiles per warp, 128 SMs) 9.3 and 14 us, of 8192 (16) 26 and
+// 30 us; 8 heads of 4096 (4, 64 SMs) 9.6 and 9.6 us, of 8192 (8) 13.5 and
+// 12.8 us; one head of 16384 (16, 8 SMs) 22.5 and 15.8 us.  A batch of one long
+// sequence among short ones waits for the long one's cluster, 0.5 us a tile,
+// where the other form would spread it: hence no more than 16.
+constexpr int kOneTiles = 16, kOneTilesLess = 4;
 constexpr float kRaise = 16.0f;   // log2 units a logit may pass the running maximum by
 
 __device__ int g_paged_status;  // sticky status word of this file's kernels
@@ -94,6 +108,7 @@ struct PagedParams {
     // last worker, the first one's slot}, by segment or by the worker that begins one
     int4 *joins;      // [workers]
     int by_segment;
+    int cluster;      // blocks per segment of the one-kernel form
     unsigned long long s_inv;  // 2^64 / S rounded up: row / S is the high word of row * s_inv
     int B, Hq, Hkv, P, S, M;
     int G, GB, HB;    // query heads of a group, blocks of them, heads per block
@@ -325,14 +340,31 @@ __device__ __forceinline__ bool next_part(Part &t, const Cut &cut, long long u0,
     return true;
 }
 
-template <int D, int RH>
+// Barrier over the blocks of a cluster.
+__device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float2 cluster_load(uint32_t addr, int rank) {  // 8 bytes of another block's shared memory
+    float2 v;
+    uint32_t at;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+    return v;
+}
+
+// ONE: a cluster of p.cluster blocks does one segment (a cached head of one
+// sequence and a block of its query heads), cut over its warps, and joins the
+// parts itself through shared memory: one launch, for few segments of bounded
+// length.  Otherwise the cut over all workers described above.
+template <int D, int RH, bool ONE>
 __global__ void __launch_bounds__(Cfg<D, RH>::Warps * 32, 1)
 paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUtensorMap map_k,
              const __grid_constant__ CUtensorMap map_v) {
     using C = Cfg<D, RH>;
     constexpr int KT = C::KT, NT = KT / 8, KS = D / 16, ON = D / 8, kStages = C::Stages;
     extern __shared__ uint8_t raw[];
-    __shared__ long long s_cut[C::Warps * 32 + 1];
+    __shared__ long long s_cut[ONE ? 1 : C::Warps * 32 + 1];
     __shared__ __align__(8) uint64_t bars[C::Warps][kStages];
     __shared__ int s_abort[C::Warps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
@@ -347,51 +379,86 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
     }
     __syncwarp();
     after_previous();
-    const bool few = p.B <= 32;  // sequences: every warp forms the cut
-    const int lane_n = few && lane < p.B ? p.seqlens[lane] : 0;
-    // the join's blocks may take their places as this kernel's blocks end
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const long long all = (long long)C::Warps * gridDim.x;
-    long long lane_before = 0;
-    const Cut cut = few ? form_cut_warp(lane_n, KT, most, heads, all, lane_before)
-                        : form_cut(p.seqlens, p.B, KT, most, heads, all, s_cut);
-    // sequences without rows, and lengths out of range
-    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-        const int n = p.seqlens[b];
-        if (n > 0 && n <= most) continue;
-        const float v = n == 0 ? 0.0f : NAN;
-        for (int i = threadIdx.x; i < p.Hq * D; i += blockDim.x)
-            p.out[(long long)b * p.Hq * D + i] = __float2bfloat16_rn(v);
-        if (p.lse)
-            for (int h = threadIdx.x; h < p.Hq; h += blockDim.x)
-                p.lse[(long long)b * p.Hq + h] = n == 0 ? -INFINITY : NAN;
-        if (p.by_segment)
-            for (int h = threadIdx.x; h < heads; h += blockDim.x) p.joins[b * heads + h] = make_int4(-1, 0, 0, 0);
-        if (threadIdx.x == 0 && n != 0) atomicCAS(&g_paged_status, 0, CSA_ERR_INVALID_ARG);
-    }
-
-    // workers are numbered across blocks first, so that few of them spread over all SMs
-    const long long worker = (long long)warp * gridDim.x + blockIdx.x;
-    if (lane == 0 && !p.by_segment) p.joins[worker] = make_int4(-1, 0, 0, 0);
-    if (worker >= cut.in_use) return;
-    const long long u0 = quot(worker * cut.U, cut.in_use), u1 = quot((worker + 1) * cut.U, cut.in_use);
-    if (u0 >= u1) return;
-
-    // ---- position in the range: what is copied next, and what is consumed
     Part now;
-    if (few) {  // the last sequence that begins at or before u0
-        now.b = __popc(__ballot_sync(0xffffffffu, lane < p.B && lane_before * heads <= u0)) - 1;
-        now.s0 = __shfl_sync(0xffffffffu, lane_before, now.b) * heads;
-        now.n = __shfl_sync(0xffffffffu, lane_n, now.b);
-    } else {
-        now.b = find_sequence(u0, cut, s_cut, p.seqlens, p.B, KT, most, heads, now.s0);
+    Cut cut = {};
+    long long worker = 0, u0 = 0, u1 = 0;
+    int parts = 1;           // of this segment (ONE)
+    bool working = true;     // whether this warp has one (ONE)
+    const int rank = ONE ? (int)(blockIdx.x % p.cluster) : 0;
+    if constexpr (ONE) {
+        const int segment = blockIdx.x / p.cluster;
+        now.b = segment / heads;
+        now.head = segment - now.b * heads;
         now.n = p.seqlens[now.b];
+        now.tiles = tiles_of(now.n, KT, most);
+        now.s0 = 0;
+        if (now.tiles == 0) {  // no rows, or a length out of range: all blocks of the cluster leave
+            const int hk = p.GB == 1 ? now.head : now.head / p.GB, hb = now.head - hk * p.GB;
+            const long long first = (long long)now.b * p.Hq + hk * p.G + hb * p.HB;
+            const int rows_h = min(p.HB, p.G - hb * p.HB);
+            if (rank == 0) {
+                for (int i = threadIdx.x; i < rows_h * D; i += blockDim.x)
+                    p.out[first * D + i] = __float2bfloat16_rn(now.n == 0 ? 0.0f : NAN);
+                if (p.lse)
+                    for (int h = threadIdx.x; h < rows_h; h += blockDim.x)
+                        p.lse[first + h] = now.n == 0 ? -INFINITY : NAN;
+                if (threadIdx.x == 0 && now.n != 0) atomicCAS(&g_paged_status, 0, CSA_ERR_INVALID_ARG);
+            }
+            return;
+        }
+        // parts across blocks first
+        parts = min(C::Warps * p.cluster, now.tiles);
+        const int mine = warp * p.cluster + rank;
+        working = mine < parts;
+        now.tile = working ? (int)quot((long long)mine * now.tiles, parts) : 0;
+        now.last = working ? (int)quot((long long)(mine + 1) * now.tiles, parts) : 1;
+    } else {
+        const bool few = p.B <= 32;  // sequences: every warp forms the cut
+        const int lane_n = few && lane < p.B ? p.seqlens[lane] : 0;
+        // the join's blocks may take their places as this kernel's blocks end
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        const long long all = (long long)C::Warps * gridDim.x;
+        long long lane_before = 0;
+        cut = few ? form_cut_warp(lane_n, KT, most, heads, all, lane_before)
+                  : form_cut(p.seqlens, p.B, KT, most, heads, all, s_cut);
+        // sequences without rows, and lengths out of range
+        for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+            const int n = p.seqlens[b];
+            if (n > 0 && n <= most) continue;
+            const float v = n == 0 ? 0.0f : NAN;
+            for (int i = threadIdx.x; i < p.Hq * D; i += blockDim.x)
+                p.out[(long long)b * p.Hq * D + i] = __float2bfloat16_rn(v);
+            if (p.lse)
+                for (int h = threadIdx.x; h < p.Hq; h += blockDim.x)
+                    p.lse[(long long)b * p.Hq + h] = n == 0 ? -INFINITY : NAN;
+            if (p.by_segment)
+                for (int h = threadIdx.x; h < heads; h += blockDim.x) p.joins[b * heads + h] = make_int4(-1, 0, 0, 0);
+            if (threadIdx.x == 0 && n != 0) atomicCAS(&g_paged_status, 0, CSA_ERR_INVALID_ARG);
+        }
+
+        // workers are numbered across blocks first, so that few of them spread over all SMs
+        worker = (long long)warp * gridDim.x + blockIdx.x;
+        if (lane == 0 && !p.by_segment) p.joins[worker] = make_int4(-1, 0, 0, 0);
+        if (worker >= cut.in_use) return;
+        u0 = quot(worker * cut.U, cut.in_use);
+        u1 = quot((worker + 1) * cut.U, cut.in_use);
+        if (u0 >= u1) return;
+
+        // ---- position in the range: what is copied next, and what is consumed
+        if (few) {  // the last sequence that begins at or before u0
+            now.b = __popc(__ballot_sync(0xffffffffu, lane < p.B && lane_before * heads <= u0)) - 1;
+            now.s0 = __shfl_sync(0xffffffffu, lane_before, now.b) * heads;
+            now.n = __shfl_sync(0xffffffffu, lane_n, now.b);
+        } else {
+            now.b = find_sequence(u0, cut, s_cut, p.seqlens, p.B, KT, most, heads, now.s0);
+            now.n = p.seqlens[now.b];
+        }
+        now.tiles = tiles_of(now.n, KT, most);
+        now.head = (int)quot(u0 - now.s0, cut.units(now.tiles));  // hk * GB + block of query heads
+        now.s0 += (long long)now.head * cut.units(now.tiles);
+        clip(now, cut, u0, u1);
+        if (now.tile >= now.last && !next_part(now, cut, u0, u1, p.seqlens, KT, most, heads)) return;
     }
-    now.tiles = tiles_of(now.n, KT, most);
-    now.head = (int)quot(u0 - now.s0, cut.units(now.tiles));  // hk * GB + block of query heads
-    now.s0 += (long long)now.head * cut.units(now.tiles);
-    clip(now, cut, u0, u1);
-    if (now.tile >= now.last && !next_part(now, cut, u0, u1, p.seqlens, KT, most, heads)) return;
     auto page_index = [&](int row) { return (int)__umul64hi((unsigned long long)row, p.s_inv); };  // row / S
     auto cached_head = [&](int head) { return p.GB == 1 ? head : head / p.GB; };
 
@@ -418,10 +485,11 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
         edge_row = g == 0 ? now.tile * KT - 1 : g == 1 && now.last * KT < now.n ? now.last * KT : -1;
         edge_page = edge_row >= 0 ? __ldg(p.table + (long long)now.b * p.M + page_index(edge_row)) : -1;
     };
+    auto next = [&](Part &t) { return !ONE && next_part(t, cut, u0, u1, p.seqlens, KT, most, heads); };
     ask();
 
     Part ahead = now;
-    bool more = true;  // something is left to copy
+    bool more = working;  // something is left to copy
     int held_b = -1, held_at = -1, held = 0;  // page numbers, one per lane
     unsigned copied = 0, used = 0, bad_stages = 0;
     int copy_stage = 0;
@@ -463,7 +531,7 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
         }
         copy_stage = copy_stage + 1 == kStages ? 0 : copy_stage + 1;
         ++copied;
-        if (++ahead.tile == ahead.last) more = next_part(ahead, cut, u0, u1, p.seqlens, KT, most, heads);
+        if (++ahead.tile == ahead.last) more = next(ahead);
     };
     for (int s = 0; s < kStages; ++s) copy_next();
 
@@ -481,7 +549,8 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
 
     int stage = 0;
     uint32_t parity = 0;
-    while (true) {
+    bool lost = false;  // a wait has run out (ONE: the block still meets its barriers)
+    while (working) {
         const int b = now.b, n = now.n, tile = now.tile, last = now.last;
         const int hk = cached_head(now.head), hb = now.head - hk * p.GB;
         const int rows_h = min(p.HB, p.G - hb * p.HB);  // query heads of this block
@@ -607,7 +676,9 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
                         }
                     }
                 __syncwarp();
-                return;
+                if (!ONE) return;
+                lost = true;
+                break;
             }
             if (bad_stages >> stage & 1) {
                 bad = true;
@@ -735,7 +806,7 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
                 parity ^= 1;
             }
         }
-        if (r1 < n) {  // the range's last row has a neighbour behind it
+        if (!lost && r1 < n) {  // the range's last row has a neighbour behind it
             bool over = false;
 #pragma unroll
             for (int h = 0; h < RH; ++h) over |= behind[h] > m[h] + kRaise;
@@ -748,12 +819,12 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
                 if (q == 3) w[h][NT - 1][1] += left;
             }
         }
-        values();
+        if (!lost) values();
         __syncwarp();
         ++used;
         copy_next();
 
-        bad = __any_sync(0xffffffffu, bad);
+        bad = __any_sync(0xffffffffu, bad || lost);
         const bool whole = r0 == 0 && r1 == n;
         float sum[RH];
 #pragma unroll
@@ -765,6 +836,8 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
         }
         // a worker's part that does not begin a segment is its first
         const long long slot = (worker * 2 + (u0 < now.s0 ? 1 : 0)) * p.HB;
+        // ONE: this warp's ring, whose copies have all been read
+        float *kept = reinterpret_cast<float *>(raw + (ring - smem_u32(raw)));
         const uint32_t *sink_v = given ? reinterpret_cast<const uint32_t *>(p.v0 + (long long)hk * D) : nullptr;
 #pragma unroll
         for (int h = 0; h < RH; ++h) {
@@ -773,7 +846,7 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
                 const float inv = 1.0f / sum[h];
                 const long long oh = (long long)b * p.Hq + q0 + row;
                 __nv_bfloat16 *og = p.out + oh * D;
-                float *po = p.part_o + (slot + row) * D;
+                float *po = ONE ? kept + row * D : p.part_o + (slot + row) * D;
 #pragma unroll
                 for (int i = 0; i < ON; ++i) {
                     float a = o[i][2 * h], c = o[i][2 * h + 1];
@@ -786,13 +859,15 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
                         a = fmaf(w0[h], __uint_as_float(v2 << 16), a);
                         c = fmaf(w0[h], __uint_as_float(v2 & 0xffff0000u), c);
                     }
-                    if (whole)
+                    if (!ONE && whole)
                         *reinterpret_cast<uint32_t *>(og + 8 * i + 2 * q) = pack_bf16x2(a * inv, c * inv);
                     else
                         *reinterpret_cast<float2 *>(po + 8 * i + 2 * q) = make_float2(a, c);
                 }
                 if (q == 0) {
-                    if (!whole) {
+                    if (ONE) {
+                        *reinterpret_cast<float2 *>(kept + p.HB * D + 2 * row) = make_float2(m[h], sum[h]);
+                    } else if (!whole) {
                         p.part_ml[2 * (slot + row)] = m[h];
                         p.part_ml[2 * (slot + row) + 1] = sum[h];
                     } else if (p.lse) {
@@ -802,14 +877,96 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
             }
         }
         if (bad && lane == 0) atomicCAS(&g_paged_status, 0, CSA_ERR_INVALID_ARG);
-        if (r0 == 0 && lane == 0 && (p.by_segment || !whole)) {
+        if (!ONE && r0 == 0 && lane == 0 && (p.by_segment || !whole)) {
             const long long end = now.s0 + cut.units(now.tiles);
             const int segment = b * heads + now.head;
             p.joins[p.by_segment ? segment : worker] =
                 make_int4(whole ? -1 : segment, (int)worker, (int)cut.worker_of(end - 1), u0 < now.s0 ? 1 : 0);
         }
-        if (!next_part(now, cut, u0, u1, p.seqlens, KT, most, heads)) break;
+        if (!next(now)) break;
         ask();
+    }
+    if constexpr (ONE) {
+        // Joins the parts: those of the block's warps through its shared memory, a warp per query
+        // head, then those of the cluster's blocks, each block a share of the columns.
+        const int hk = cached_head(now.head), hb = now.head - hk * p.GB, rows_h = min(p.HB, p.G - hb * p.HB);
+        const long long first = (long long)now.b * p.Hq + hk * p.G + hb * p.HB;
+        const int blocks = min(p.cluster, parts);                                       // with parts
+        const int count = rank < parts ? (parts - rank - 1) / p.cluster + 1 : 0;        // warps of this block with parts
+        uint8_t *rings = raw + ((smem_u32(raw) + 1023) / 1024 * 1024 - smem_u32(raw));
+        constexpr int kRing = kStages * C::Stage;
+        float *sums = reinterpret_cast<float *>(rings + kRing / 2);  // behind the first ring's part
+        static_assert(16 * (D + 2) * 4 <= kRing / 2 || RH == 1, "two sets of sums fit a ring");
+        static_assert(8 * (D + 2) * 4 <= kRing / 2, "two sets of sums fit a ring");
+        __syncthreads();
+        for (int row = warp; row < rows_h && count > 0; row += C::Warps) {
+            auto of = [&](int i) { return reinterpret_cast<const float *>(rings + i * kRing); };
+            float2 ml = make_float2(-INFINITY, 0.f);
+            if (lane < count) ml = *reinterpret_cast<const float2 *>(of(lane) + p.HB * D + 2 * row);
+            float top = ml.x;
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            const float f = ex2_approx(ml.x - top);
+            float total = f * ml.y;
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+            const float inv = 1.0f / total;
+#pragma unroll
+            for (int c = 0; c < D; c += 64) {
+                float2 v = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < C::Warps; ++i) {
+                    const float fi = __shfl_sync(0xffffffffu, f, i);
+                    if (i < count) {
+                        const float2 x = *reinterpret_cast<const float2 *>(of(i) + row * D + c + 2 * lane);
+                        v.x = fmaf(fi, x.x, v.x);
+                        v.y = fmaf(fi, x.y, v.y);
+                    }
+                }
+                if (blocks == 1)
+                    *reinterpret_cast<uint32_t *>(p.out + (first + row) * D + c + 2 * lane) =
+                        pack_bf16x2(v.x * inv, v.y * inv);
+                else
+                    *reinterpret_cast<float2 *>(sums + row * D + c + 2 * lane) = v;
+            }
+            if (lane == 0) {
+                if (blocks > 1)
+                    *reinterpret_cast<float2 *>(sums + p.HB * D + 2 * row) = make_float2(top, total);
+                else if (p.lse)
+                    p.lse[first + row] = (top + log2f(total)) * kLn2;
+            }
+        }
+        if (blocks > 1) {  // the same for every block of the cluster
+            cluster_sync();
+            const uint32_t at = smem_u32(sums);
+            for (int u = rank * blockDim.x + threadIdx.x; u < rows_h * (D / 2); u += p.cluster * blockDim.x) {
+                const int row = u / (D / 2), c = 2 * (u - row * (D / 2));
+                float2 ml[8], x[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i < blocks) {
+                        ml[i] = cluster_load(at + (p.HB * D + 2 * row) * 4, i);
+                        x[i] = cluster_load(at + (row * D + c) * 4, i);
+                    }
+                float top = ml[0].x;
+#pragma unroll
+                for (int i = 1; i < 8; ++i)
+                    if (i < blocks) top = fmaxf(top, ml[i].x);
+                float total = 0.f, a = 0.f, b = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i < blocks) {
+                        const float f = ex2_approx(ml[i].x - top);
+                        total = fmaf(f, ml[i].y, total);
+                        a = fmaf(f, x[i].x, a);
+                        b = fmaf(f, x[i].y, b);
+                    }
+                const float inv = 1.0f / total;
+                *reinterpret_cast<uint32_t *>(p.out + (first + row) * D + c) = pack_bf16x2(a * inv, b * inv);
+                if (c == 0 && p.lse) p.lse[first + row] = (top + log2f(total)) * kLn2;
+            }
+            cluster_sync();  // no block leaves while its sums are read
+        }
     }
 }
 
@@ -941,6 +1098,17 @@ bool encode_pool(CUtensorMap *map, const void *ptr, long long rows, int D, int R
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Blocks per segment of the one-kernel form, 0 where the other form is used.
+// The lengths are not known here, only the tiles that a row of the table can
+// hold.
+int cluster_for(long long segments, long long tiles, int warps) {
+    if (segments > kOneAtATime[0]) return 0;
+    int c = 8;
+    for (int i = 3; i > 0 && (segments > kOneAtATime[i] || (long long)(c / 2) * warps >= tiles); --i) c /= 2;
+    const long long most = 4 * segments * c >= 3 * kGrid ? kOneTiles : kOneTilesLess;
+    return tiles <= most * c * warps ? c : 0;
+}
+
 template <int D, int RH>
 int launch(PagedParams &p, cudaStream_t stream) {
     using C = Cfg<D, RH>;
@@ -954,14 +1122,24 @@ int launch(PagedParams &p, cudaStream_t stream) {
         !encode_pool(&map_v, rows ? (const void *)p.v : some, rows ? rows : 8, D, p.R))
         return CSA_ERR_CUDA;
     const int heads = p.Hkv * p.GB;
-    // blocks that the largest possible lengths can keep busy
-    const long long most = (long long)p.B * heads * (((long long)p.M * p.S + C::KT - 1) / C::KT);
-    const int grid = (int)(most < kGrid ? (most < 1 ? 1 : most) : kGrid);
     p.s_inv = ~0ull / p.S + 1;
-    auto kern = paged_kernel<D, RH>;
+    const long long segments = (long long)p.B * heads, tiles = ((long long)p.M * p.S + C::KT - 1) / C::KT;
+    p.cluster = cluster_for(segments, tiles, C::Warps);
+    if (p.cluster > 0) {
+        auto kern = paged_kernel<D, RH, true>;
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::Smem) != cudaSuccess ||
+            launch_clusters_after_previous(kern, (unsigned)segments * p.cluster, C::Warps * 32, C::Smem, stream,
+                                           p.cluster, p, map_k, map_v) != cudaSuccess)
+            return CSA_ERR_CUDA;
+        return CSA_OK;
+    }
+    // blocks that the largest possible lengths can keep busy
+    const long long most = segments * tiles;
+    const int grid = (int)(most < kGrid ? (most < 1 ? 1 : most) : kGrid);
+    auto kern = paged_kernel<D, RH, false>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::Smem) != cudaSuccess)
         return CSA_ERR_CUDA;
-    const long long segments = (long long)p.B * heads, all = (long long)grid * C::Warps;
+    const long long all = (long long)grid * C::Warps;
     p.by_segment = segments <= kGrid;
     if (launch_after_previous(kern, grid, C::Warps * 32, C::Smem, stream, p, map_k, map_v) != cudaSuccess)
         return CSA_ERR_CUDA;

@@ -12,12 +12,17 @@ from paged_util import decode_bounds, pages_of, rows_of, scattered
 pytestmark = pytest.mark.gpu
 
 
-def make(lens, Hq, Hkv, d, S, seed, spare=3, value=None):
+FORMS = pytest.mark.parametrize("wide", [False, True], ids=["one kernel", "parts joined"])
+
+
+def make(lens, Hq, Hkv, d, S, seed, spare=3, wide=False):
+    """wide: a table for sequences of 40000 tokens, with which even short ones are
+    cut over all workers and their parts joined by a second kernel."""
     g = torch.Generator().manual_seed(seed)
     P = sum(pages_of(n, S) for n in lens) + spare
     bf = lambda *s: torch.randn(*s, generator=g).to(torch.bfloat16)
     x = dict(q=bf(len(lens), Hq, d), k=bf(P, Hkv, S, d), v=bf(P, Hkv, S, d), k0=bf(Hkv, d), v0=bf(Hkv, d))
-    x["table"] = scattered(lens, S, P, seed)
+    x["table"] = scattered(lens, S, P, seed, M=pages_of(40000, S) if wide else None)
     x["lens"] = list(lens)
     return x
 
@@ -62,32 +67,36 @@ EDGES = [1, 2, 3, 7, 8, 9, 15, 16, 17, 31, 32, 33, 48, 63, 64, 65, 0, 127, 128, 
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("mode", [0, 1, 2])
 @pytest.mark.parametrize("S", [8, 16, 24, 64])
-def test_lengths_around_every_edge(d, mode, S):
-    x = make(EDGES, 2, 1, d, S, seed=d + S + mode)
+@FORMS
+def test_lengths_around_every_edge(d, mode, S, wide):
+    x = make(EDGES, 2, 1, d, S, seed=d + S + mode, wide=wide)
     o, lse = run(x, mode)
     check(x, o, lse, S, mode, d ** -0.5)
 
 
 @pytest.mark.parametrize("Hq,Hkv", [(1, 1), (3, 3), (3, 1), (8, 2), (10, 2), (16, 1), (9, 1), (17, 1), (40, 2), (33, 11)])
-def test_head_groups(Hq, Hkv):
-    x = make([5, 333, 0, 40, 1], Hq, Hkv, 128, 32, seed=Hq)
+@FORMS
+def test_head_groups(Hq, Hkv, wide):
+    x = make([5, 333, 0, 40, 1], Hq, Hkv, 128, 32, seed=Hq, wide=wide)
     o, lse = run(x, 2)
     check(x, o, lse, 32, 2, 128 ** -0.5)
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("scale", [0.125, 1.0, 4.0, -0.5, 0.0])
-def test_logit_ranges(d, scale):
+@FORMS
+def test_logit_ranges(d, scale, wide):
     # scale 4 gives steps between neighbouring logits of order 100
-    x = make([1, 2, 30, 300, 700], 4, 2, d, 16, seed=17)
+    x = make([1, 2, 30, 300, 700], 4, 2, d, 16, seed=17, wide=wide)
     o, lse = run(x, 1, scale)
     check(x, o, lse, 16, 1, scale)
 
 
-def test_rising_and_falling_logits():
+@FORMS
+def test_rising_and_falling_logits(wide):
     # one key direction with growing, falling and peaked weights: the running maximum moves late or never
     n, d = 500, 128
-    x = make([n, n, n], 1, 1, d, 16, seed=3)
+    x = make([n, n, n], 1, 1, d, 16, seed=3, wide=wide)
     u = torch.randn(d, generator=torch.Generator().manual_seed(1))
     ramp = torch.linspace(-30, 30, n)
     shapes = [ramp, ramp.flip(0), torch.where(torch.arange(n) == 377, torch.tensor(60.0), -ramp.abs())]
@@ -114,10 +123,11 @@ def test_many_short_sequences():
     check(x, o, lse, 16, 1, 128 ** -0.5, only=range(0, 300, 7))
 
 
-def test_matches_the_contiguous_decode():
+@FORMS
+def test_matches_the_contiguous_decode(wide):
     B, H, T, d, S = 3, 4, 700, 128, 16
     lens = [700, 333, 1]
-    x = make(lens, H, H, d, S, seed=8)
+    x = make(lens, H, H, d, S, seed=8, wide=wide)
     kc, vc = torch.zeros(2, B, H, T, d, dtype=torch.bfloat16).unbind()
     for b, n in enumerate(lens):
         kc[b, :, :n], vc[b, :, :n] = rows_of(x["k"], x["table"][b], n, S), rows_of(x["v"], x["table"][b], n, S)
@@ -130,10 +140,11 @@ def test_matches_the_contiguous_decode():
         assert (lse - lc).abs().max().item() <= 1e-5
 
 
-def test_pages_hold_anything_behind_the_last_token():
+@FORMS
+def test_pages_hold_anything_behind_the_last_token(wide):
     # rows behind a sequence's end, and pages of nobody, are NaN or infinite
     lens, S, d = [1, 17, 100, 129, 40], 16, 128
-    x = make(lens, 4, 2, d, S, seed=9)
+    x = make(lens, 4, 2, d, S, seed=9, wide=wide)
     want, wl = run(x, 0)
     held = set()
     for b, n in enumerate(lens):
@@ -150,9 +161,10 @@ def test_pages_hold_anything_behind_the_last_token():
 
 @pytest.mark.parametrize("Hq", [1, 8, 16])
 @pytest.mark.parametrize("scale", [0.0, 0.1])
-def test_infinite_values_in_the_cache_pass_through(Hq, scale):
+@FORMS
+def test_infinite_values_in_the_cache_pass_through(Hq, scale, wide):
     # scale 0: the weights are exact in bf16
-    x = make([50, 2000], Hq, 1, 128, 16, seed=10)
+    x = make([50, 2000], Hq, 1, 128, 16, seed=10, wide=wide)
     for b, n in ((0, 1), (1, 100)):
         x["v"][x["table"][b, n], 0, 3, 5], x["v"][x["table"][b, n], 0, 4, 6] = float("inf"), float("-inf")
     o, _ = run(x, 0, scale)
@@ -160,8 +172,9 @@ def test_infinite_values_in_the_cache_pass_through(Hq, scale):
     assert torch.isfinite(o[:, :, 7:].float()).all()
 
 
-def test_sequences_that_share_pages():
-    x = make([200, 75, 200], 4, 2, 64, 16, seed=30)
+@FORMS
+def test_sequences_that_share_pages(wide):
+    x = make([200, 75, 200], 4, 2, 64, 16, seed=30, wide=wide)
     x["table"][1, :5] = x["table"][0, :5]
     x["table"][2] = x["table"][0]
     o, lse = run(x, 2)
@@ -206,9 +219,10 @@ def test_pages_beyond_32_bits():
     assert device_status() == 0
 
 
-def test_bad_lengths_and_pages_are_reported():
+@FORMS
+def test_bad_lengths_and_pages_are_reported(wide):
     S, d = 16, 128
-    x = make([100, 40, 60, 70, 0], 4, 2, d, S, seed=11)
+    x = make([100, 40, 60, 70, 0], 4, 2, d, S, seed=11, wide=wide)
     run(x, 0)
     assert device_status() == 0
     P, M = x["k"].shape[0], x["table"].shape[1]
@@ -226,9 +240,10 @@ def test_bad_lengths_and_pages_are_reported():
     assert device_status() == -1 and torch.isnan(o[2].float()).all()
 
 
-def test_repeats_bit_for_bit_on_stale_workspaces():
+@FORMS
+def test_repeats_bit_for_bit_on_stale_workspaces(wide):
     lens = [3000, 17, 0, 900, 5000]
-    x = make(lens, 8, 2, 128, 32, seed=12)
+    x = make(lens, 8, 2, 128, 32, seed=12, wide=wide)
     o, lse = run(x, 0)
     n = decode_paged_workspace_bytes(5, 8, 2, 128)
     for fill in (255, 0, 127):
@@ -236,8 +251,9 @@ def test_repeats_bit_for_bit_on_stale_workspaces():
         assert torch.equal(o, o2) and torch.equal(lse, l2)
 
 
-def test_two_streams_and_a_given_stream():
-    x = make([2000, 900, 50], 8, 2, 128, 16, seed=13)
+@FORMS
+def test_two_streams_and_a_given_stream(wide):
+    x = make([2000, 900, 50], 8, 2, 128, 16, seed=13, wide=wide)
     o, lse = run(x, 0)
     c = {n: t.cuda() for n, t in x.items() if torch.is_tensor(t)}
     table, lens = torch.as_tensor(x["table"]).cuda(), torch.tensor(x["lens"], dtype=torch.int32).cuda()
@@ -250,8 +266,9 @@ def test_two_streams_and_a_given_stream():
         assert torch.equal(o, oo) and torch.equal(lse, ll)
 
 
-def test_captured_and_replayed_with_other_lengths():
-    x = make([500, 300, 20], 4, 2, 64, 16, seed=14)
+@FORMS
+def test_captured_and_replayed_with_other_lengths(wide):
+    x = make([500, 300, 20], 4, 2, 64, 16, seed=14, wide=wide)
     c = {n: t.cuda() for n, t in x.items() if torch.is_tensor(t)}
     table, lens = torch.as_tensor(x["table"]).cuda(), torch.tensor(x["lens"], dtype=torch.int32).cuda()
     decode_paged(c["q"], c["k"], c["v"], table, lens)
