@@ -14,7 +14,7 @@
 //  - A warp is a worker of its own.  It has a ring of tiles in shared memory
 //    that it fills itself by TMA (its lane 0), runs over a contiguous range of
 //    tiles and never waits for another warp, so some warp's copies are always
-//    in flight: 8 warps x 24 KiB per SM.
+//    in flight: 192 KiB of rings per SM.
 //  - The tiles of all (sequence, cached head, block of query heads) in a row
 //    are cut into equal ranges, one per worker, whatever the lengths.  The
 //    lengths are on the device, so every block forms the cut itself.
@@ -83,11 +83,11 @@ __device__ int g_paged_status;  // sticky status word of this file's kernels
 template <int D, int RH>
 struct Cfg {
     static constexpr int KT = 16;                      // rows per tile
-    // Workers per block: as many as registers allow without spills (at d = 64 with 16 heads 16
-    // workers of 128 registers take 92 us for 268 MB where 12 of 168 take 75 us), one per
-    // scheduler at d = 256, whose sums alone are 128 registers.
-    static constexpr int Warps = D == 64 && RH == 2 ? 12 : 1024 / D;
-    static constexpr int Stages = D == 64 && RH == 2 ? 4 : 3;  // tiles in a worker's ring
+    // Workers per block: one per scheduler at d = 256, whose sums alone are 128 registers, two at
+    // d = 128.  At d = 64 three: 16 workers of 128 registers spill with 16 heads (92 us for 268 MB,
+    // 75 us with 12), and with 8 leave more parts to join (2 x 131072 tokens 33.4 us, 31.4 with 12).
+    static constexpr int Warps = D == 64 ? 12 : 1024 / D;
+    static constexpr int Stages = D == 64 ? 4 : 3;     // tiles in a worker's ring
     static constexpr int Tile = KT * D * 2;            // bytes of a tile of keys, or of values
     static constexpr int Stage = 2 * Tile;
     static constexpr int Smem = Warps * Stages * Stage + 1024;  // + alignment
@@ -95,7 +95,7 @@ struct Cfg {
 };
 
 // Workers of a full grid, at most.
-__host__ __device__ constexpr long long workers(int d) { return 1024 / d * kGrid; }
+__host__ __device__ constexpr long long workers(int d) { return (d == 64 ? 12 : 1024 / d) * kGrid; }
 
 struct PagedParams {
     const __nv_bfloat16 *q, *k, *v, *k0, *v0;
