@@ -65,15 +65,16 @@ constexpr int kFew = 2;
 // of 1 to 8192 tokens take 63.1 us with 1, 59.7 with 2, 59.5 with 3, 32 of 333
 // tokens 14.4, 13.4 and 14.2 us.
 constexpr int kPartCost = 2;
-// The one-kernel form: clusters of 1, 2, 4 and 8 blocks that run at a time.
+// The one-kernel form: clusters of 1, 2, 4 and 8 blocks that run at a time ...
 constexpr int kOneAtATime[4] = {152, 76, 36, 15};
 // ... and tiles per warp that the longest sequence may have in it, where it
-// keeps at least 3/4 of the SMs busy and where it does not.  Measured, this form and the other, equal lengths: 32 heads of
-// 2048 tokens (4 tiles per warp, 128 SMs) 9.3 and 14 us, of 8192 (16) 26 and
-// 30 us; 8 heads of 4096 (4, 64 SMs) 9.6 and 9.6 us, of 8192 (8) 13.5 and
-// 12.8 us; one head of 16384 (16, 8 SMs) 22.5 and 15.8 us.  A batch of one long
-// sequence among short ones waits for the long one's cluster, 0.5 us a tile,
-// where the other form would spread it: hence no more than 16.
+// keeps at least 3/4 of the SMs busy and where it does not.  Measured, this
+// form and the other, equal lengths: 32 heads of 2048 tokens (4 tiles per warp,
+// 128 SMs) 9.3 and 14 us, of 8192 (16) 26 and 30 us; 8 heads of 4096 (4, 64
+// SMs) 9.6 and 9.6 us, of 8192 (8) 13.5 and 12.8 us; one head of 16384 (16, 8
+// SMs) 22.5 and 15.8 us.  A batch of one long sequence among short ones waits
+// for the long one's cluster, 0.5 us a tile, where the other form would spread
+// it: hence no more than 16.
 constexpr int kOneTiles = 16, kOneTilesLess = 4;
 constexpr float kRaise = 16.0f;   // log2 units a logit may pass the running maximum by
 

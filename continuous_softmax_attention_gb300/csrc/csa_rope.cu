@@ -284,12 +284,15 @@ int csa_rope_plan_make(csa_rope_plan *plan, const int *sections, int axes, doubl
         for (int a = 0; a < axes; ++a)
             for (int j = 0; j < left[a]; ++j) plan->axis[i++] = (unsigned char)a;
     }
-    const long double two_pi = 6.283185307179586476925286766559L;
+    // the frequencies in turns per position, base^(-i/n) / 2 pi, as fractions of a turn times 2^64;
+    // one power and n products (a power of this type costs 2 us where it is 128 bits wide), off by
+    // at most n 2^-63 relative
+    const long double step = powl((long double)base, -1.0L / total);
+    long double f = 0.159154943091895335768883763372514362L;
     for (i = 0; i < total; ++i) {
-        // the frequency in turns per position, as a fraction of a turn times 2^64
-        const long double f = powl((long double)base, -(long double)i / total) / two_pi;
         const long double frac = f - floorl(f);
         plan->turn[i] = (unsigned long long)(ldexpl(frac, 63) + 0.25L) * 2ull;
+        f *= step;
     }
     return CSA_OK;
 }
