@@ -294,3 +294,65 @@ def test_a_captured_step():
         m.reserve([1, 1, 0, 1])
         dev.equals()
     assert max(pages_of(n, S) for n in m.lens) == 3 and device_status() == 0
+
+
+def test_pages_in_a_graph_and_on_a_given_stream():
+    """free, fork and its copies, compaction and its moves captured once and replayed
+    from other states, then the same calls on a stream of their own."""
+    S, P, M, B = 8, 60, 6, 8
+    g = torch.Generator().manual_seed(9)
+    states = []
+    for counts in ([30, 17, 8, 0, 0, 40, 5, 1], [9, 40, 0, 0, 0, 33, 48, 0], [3, 1, 7, 0, 0, 2, 0, 8]):
+        m = Books(B, P, S, M)
+        assert m.reserve(counts) == 0
+        m.free([6])
+        states.append(m)
+    dev = Device(states[0])
+    kp = torch.randn(2, P, 2, S, 64, generator=g).to(torch.bfloat16).cuda()
+    rows, p, c = (torch.tensor(x, **INTS) for x in ([5, -1], [0, 1, 0], [3, 4, 6]))
+
+    def step(**kw):
+        csa.cache_free(*dev.state, rows, **kw)
+        src, dst, short = csa.cache_fork(*dev.state, p, c, **kw)
+        csa.cache_copy_pages(kp, None, src, dst, **kw)
+        msrc, mdst, moved = csa.cache_compact(*dev.state, **kw)
+        csa.cache_copy_pages(kp, None, msrc, mdst, count=moved, **kw)
+        return short, moved
+
+    def content(m, pages):  # what every sequence reads, whatever the pages are called
+        return [pages[:, [m.table[b][j] for j in range(pages_of(n, S))]].clone() for b, n in enumerate(m.lens)]
+
+    def load(m):
+        for t, x in ((dev.refs, m.refs), (dev.table, m.table), (dev.lens, m.lens)):
+            t.copy_(torch.tensor(x, **INTS).reshape(t.shape))
+        dev.m = m
+
+    load(states[0])
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        short, moved = step()
+    side = torch.cuda.Stream()
+    for run in ("graph", "stream"):
+        for m0 in states:
+            m = Books(B, P, S, M)
+            m.refs, m.table, m.lens = list(m0.refs), [list(r) for r in m0.table], list(m0.lens)
+            load(m)
+            pages = kp.clone()
+            m.free([5])
+            assert m.fork([0, 1, 0], [3, 4, 6])[2] == 0
+            before = content(m, pages)  # a copied page holds what its source held ...
+            for child, parent in ((3, 0), (4, 1), (6, 0)):
+                if m.lens[child] % S:
+                    before[child][:, -1] = pages[:, m.table[parent][m.lens[parent] // S]]
+            m.compact()
+            torch.cuda.synchronize()
+            if run == "graph":
+                graph.replay()
+            else:
+                short, moved = step(stream=side)
+            torch.cuda.synchronize()
+            dev.equals()
+            assert short.item() == 0
+            assert all(torch.equal(x, y) for x, y in zip(content(m, kp), before))
+    assert device_status() == 0

@@ -283,6 +283,31 @@ def test_captured_and_replayed_with_other_lengths(wide):
         check(x, o, lse, 16, 0, 64 ** -0.5)
 
 
+@FORMS
+def test_two_graphs_on_one_workspace(wide):
+    a, b = make([700, 30, 0], 8, 2, 128, 16, seed=40, wide=wide), make([5, 900], 8, 2, 128, 32, seed=41, wide=wide)
+    n = max(decode_paged_workspace_bytes(3, 8, 2, 128), decode_paged_workspace_bytes(2, 8, 2, 128))
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    held, graphs = [], []
+    for x in (a, b):
+        c = {t: x[t].cuda() for t in ("q", "k", "v")}
+        table, lens = torch.as_tensor(x["table"]).cuda(), torch.tensor(x["lens"], dtype=torch.int32).cuda()
+        want = decode_paged(c["q"], c["k"], c["v"], table, lens, workspace=ws)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = decode_paged(c["q"], c["k"], c["v"], table, lens, workspace=ws)
+        held.append((c, table, lens, want, got))
+        graphs.append(g)
+    for i in (0, 1, 1, 0, 1, 0, 0):  # one after the other on one stream
+        for t in held[i][4]:
+            t.zero_()
+        graphs[i].replay()
+        graphs[1 - i].replay()
+        torch.cuda.synchronize()
+        for _, _, _, want, got in held:
+            assert all(torch.equal(w, t) for w, t in zip(want, got))
+
+
 def test_refusals():
     x = make([40, 8], 4, 2, 128, 16, seed=15)
     c = {n: t.cuda() for n, t in x.items() if torch.is_tensor(t)}

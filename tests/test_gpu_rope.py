@@ -211,6 +211,38 @@ def test_append_of_bad_state_writes_nothing_there():
     assert torch.equal(kp, before)
 
 
+def test_a_given_stream_and_a_graph():
+    plan = RopeAxes(128, (16, 24, 24))
+    q, k, v = tensors(2, 5, 4, 2, 128, "bf16", 22, True)
+    pos = draw_positions(3, 2, 5, 1000, 23)
+    table, n = torch.arange(8, dtype=torch.int32, device="cuda").view(2, 4), torch.tensor([9, 30], dtype=torch.int32, device="cuda")
+    want = rope(q, k, pos, plan)
+    kp, vp = pools(8, 2, 8, 128, "bf16", 24)
+    ke, ve = kp.clone(), vp.clone()
+    qa = cache_append(k, v, ke, ve, table, n, rope=plan, positions=pos, q=q)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = rope(q, k, pos, plan, stream=side)
+    back = rope_backward(*got, pos, plan, stream=side)
+    k2, v2 = kp.clone(), vp.clone()
+    side.wait_stream(torch.cuda.current_stream())
+    q2 = cache_append(k, v, k2, v2, table, n, rope=plan, positions=pos, q=q, stream=side)
+    side.synchronize()
+    for a, b in zip(got + (q2, k2, v2), want + (qa, ke, ve)):
+        assert torch.equal(a, b)
+    # turned back: a rounding to bf16 of each member of a pair each way
+    assert ((back[0] - q).abs().float() <= 4 * 2.0 ** -8 * q.abs().max().float()).all()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        g1 = rope(q, k, pos, plan)
+        q3 = cache_append(k, v, kp, vp, table, n, rope=plan, positions=pos, q=q)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(g1 + (q3, kp, vp), want + (qa, ke, ve)):
+        assert torch.equal(a, b)
+
+
 def test_append_without_a_pool():
     _, k, v = tensors(2, 3, 2, 2, 64, "bf16", 20, False)
     e = torch.zeros(0, 2, 16, 64, dtype=torch.bfloat16, device="cuda")
