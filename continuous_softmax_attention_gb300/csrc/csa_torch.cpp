@@ -157,7 +157,9 @@ PyObject *decode_paged(PyObject *, PyObject *const *a, Py_ssize_t) {
     }
     Tensor o = out(optional(a[9], "out"), "out", bf, {B, Hq, d}, here.dev), lse;
     const Tensor *lse_given = optional(a[10], "lse");
-    if (lse_given || PyObject_IsTrue(a[12])) lse = out(lse_given, "lse", at::kFloat, {B, Hq}, here.dev);
+    const int want_lse = PyObject_IsTrue(a[12]);
+    if (want_lse < 0) throw python_error();
+    if (lse_given || want_lse) lse = out(lse_given, "lse", at::kFloat, {B, Hq}, here.dev);
     const int b = size(B, "B"), hq = size(Hq, "Hq"), hkv = size(Hkv, "Hkv"), dd = size(d, "d");
     const Tensor *ws = optional(a[11], "workspace");
     Tensor own;
@@ -251,6 +253,7 @@ PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t) {
     const Rows qos(qo, "q_out", dtype, {B, Hq, T, d}, here.dev, true);
     Rows ks, kos;
     Tensor ko;
+    TORCH_CHECK_VALUE(k || a[6] == Py_None, "k_out goes with k");
     if (k) {
         ks = Rows(*k, "k", dtype, {B, Hkv, T, d}, here.dev, false);
         given = optional(a[6], "k_out");
@@ -297,6 +300,7 @@ PyObject *cache_append(PyObject *, PyObject *const *a, Py_ssize_t) {
     int64_t Hq = 0;
     Rows qs, qos;
     Tensor qo;
+    TORCH_CHECK_VALUE(q || a[11] == Py_None, "q_out goes with q");
     if (a[7] == Py_None) {
         TORCH_CHECK_VALUE(!q && !positions, "q and positions go with a rope plan");
     } else {

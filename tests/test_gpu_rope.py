@@ -275,3 +275,17 @@ def test_refusals():
         RopeAxes(64, (16,), base=-1.0)
     e, _ = rope(q[:0], None, pos[:, :0], plan)
     assert e.shape == (0, 2, 3, 64)
+
+
+def test_an_output_without_its_input_is_refused():
+    plan = RopeAxes(64, (16, 16))
+    q, k, v = tensors(2, 3, 2, 2, 64, "bf16", 13, False)
+    pos = draw_positions(2, 2, 3, 10, 14)
+    pages = torch.zeros(4, 2, 8, 64, dtype=torch.bfloat16, device="cuda")
+    table = torch.arange(4, dtype=torch.int32, device="cuda").view(2, 2)
+    lens = torch.full((2,), 3, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        rope(q, None, pos, plan, k_out=torch.empty_like(k))
+    for kw in ({}, {"rope": plan, "positions": pos}):
+        with pytest.raises(ValueError):
+            cache_append(k, v, pages, pages.clone(), table, lens, q_out=torch.empty_like(q), **kw)
