@@ -494,7 +494,8 @@ typedef struct {
 /*
  * csa_rope_plan_init - plan for rotary positions with `axes` axes (1 to 8),
  *   sections[a] pairs turning by axis a (n pairs in all, 1 <= n <= 128); pair i
- *   turns by positions[axis(i)] * base^(-i / n).  base finite and > 0; flags:
+ *   turns by positions[axis(i)] * base^(-i / n).  base finite and > 0 (below 1
+ *   the turns per position grow, and their fraction loses as many bits); flags:
  *   CSA_ROPE_ADJACENT, CSA_ROPE_DEALT.  Host only.
  *   CSA_ERR_INVALID_ARG, or CSA_ERR_UNSUPPORTED for more than 128 pairs.
  */
@@ -505,7 +506,7 @@ int csa_rope_plan_init(csa_rope_plan *plan, const int *sections, int axes, doubl
  *   the other columns copied: (u, w) -> (u cos - w sin, u sin + w cos) per
  *   pair, by the negative angle if `inverse` (the backward pass: the gradient
  *   of the input from the gradient of the output).  fp32 arithmetic, one
- *   rounding; angles exact to fp32 for every int32 position.
+ *   rounding; angles exact to fp32 for every int32 position (base >= 1).
  *   q, q_out: bf16 [B, Hq, T, d]; k, k_out: bf16 [B, Hkv, T, d], not read
  *   where the head count is 0.  *_strides: HOST long long[3], the strides over
  *   batch, head and time in elements (the last dimension is contiguous); NULL
@@ -592,9 +593,11 @@ int csa_cache_free(int *page_refs, int *block_table, int *seqlens, const int *ro
  *   parents, children: int32 [n]; a pair with a negative entry is padding.
  *   A parent may have several children; a child must be empty (length 0) and
  *   listed once.  The child's row of the table is -1 behind its pages.
- *   shortfall as csa_cache_reserve (-1: a row out of range, a bad length or
- *   page, a child that is not empty or listed twice); where it is not 0,
- *   nothing has changed and src, dst are -1.
+ *   shortfall as csa_cache_reserve (-1: a row out of range, a bad length, a
+ *   last page to copy outside [0, P), a child that is not empty or listed
+ *   twice); where it is not 0, nothing has changed and src, dst are -1.  A
+ *   number outside [0, P) among the shared pages is copied as it is and sets
+ *   the status word.
  *   n at most CSA_CACHE_MAX_FORKS (CSA_ERR_UNSUPPORTED).
  */
 #define CSA_CACHE_MAX_FORKS 4096

@@ -356,3 +356,19 @@ def test_pages_in_a_graph_and_on_a_given_stream():
             assert short.item() == 0
             assert all(torch.equal(x, y) for x, y in zip(content(m, kp), before))
     assert device_status() == 0
+
+
+@pytest.mark.parametrize("M", [5, 3000])  # both forms of the rows' copy
+def test_fork_of_a_broken_row(M):
+    m, d = grown(3, 20, 16, M, [35, 32, 0])
+    d.table[0, 1] = 20  # a shared page that the pool has not got
+    src, dst, short = d.fork([0], [2])
+    assert short.item() == 0 and device_status() == -1
+    assert d.table[2].tolist()[:4] == [d.table[0, 0].item(), 20, dst.item(), -1]
+    assert d.refs[d.table[0, 0]] == 2 and d.lens.tolist() == [35, 32, 35]
+    m, d = grown(3, 20, 16, M, [35, 32, 0])
+    d.table[0, 2] = 20  # the page that would be copied
+    refs, table = d.refs.clone(), d.table.clone()
+    src, dst, short = d.fork([0], [2])
+    assert short.item() == -1 and device_status() == -1 and src.tolist() == dst.tolist() == [-1]
+    assert torch.equal(d.refs, refs) and torch.equal(d.table, table) and d.lens.tolist() == [35, 32, 0]
