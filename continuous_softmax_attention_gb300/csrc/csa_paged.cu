@@ -468,6 +468,8 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
     const uint32_t half = (uint32_t)R * 128;  // bytes of one 64-column box of a copy
 
     // What a part needs from memory besides its tiles, asked for before the copies are waited for.
+    // Plain loads here and below: __ldg says that nothing writes during the kernel, which begins
+    // while the one before still may.
     // Queries: A operand, rows g (and g + 8).  The rows before and behind the range: their pages.
     uint32_t qa[KS][4];
     int edge_row = 0, edge_page = 0;
@@ -478,13 +480,13 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
             p.q + ((long long)now.b * p.Hq + hk * p.G + hb * p.HB + g) * D);
 #pragma unroll
         for (int i = 0; i < KS; ++i) {
-            qa[i][0] = g < rows_h ? __ldg(qg + i * 8 + q) : 0u;
-            qa[i][2] = g < rows_h ? __ldg(qg + i * 8 + 4 + q) : 0u;
-            qa[i][1] = RH == 2 && g + 8 < rows_h ? __ldg(qg + 4 * D + i * 8 + q) : 0u;
-            qa[i][3] = RH == 2 && g + 8 < rows_h ? __ldg(qg + 4 * D + i * 8 + 4 + q) : 0u;
+            qa[i][0] = g < rows_h ? qg[i * 8 + q] : 0u;
+            qa[i][2] = g < rows_h ? qg[i * 8 + 4 + q] : 0u;
+            qa[i][1] = RH == 2 && g + 8 < rows_h ? qg[4 * D + i * 8 + q] : 0u;
+            qa[i][3] = RH == 2 && g + 8 < rows_h ? qg[4 * D + i * 8 + 4 + q] : 0u;
         }
         edge_row = g == 0 ? now.tile * KT - 1 : g == 1 && now.last * KT < now.n ? now.last * KT : -1;
-        edge_page = edge_row >= 0 ? __ldg(p.table + (long long)now.b * p.M + page_index(edge_row)) : -1;
+        edge_page = edge_row >= 0 ? p.table[(long long)now.b * p.M + page_index(edge_row)] : -1;
     };
     auto next = [&](Part &t) { return !ONE && next_part(t, cut, u0, u1, p.seqlens, KT, most, heads); };
     ask();
@@ -501,7 +503,7 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
             held_b = ahead.b;
             held_at = first & ~31;
             const long long row = (long long)(held_at + lane) * R;
-            held = row < ahead.n ? __ldg(p.table + (long long)ahead.b * p.M + page_index((int)row)) : 0;
+            held = row < ahead.n ? p.table[(long long)ahead.b * p.M + page_index((int)row)] : 0;
         }
         const uint32_t bar = smem_u32(&bars[warp][copy_stage]), at = ring + copy_stage * C::Stage;
         int bytes = 0, place[KT / 8];
@@ -577,7 +579,7 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
             const uint32_t *kg = reinterpret_cast<const uint32_t *>(at);
 #pragma unroll
             for (int i = 0; i < KS; ++i)
-                mma(edge, qa[i], at ? __ldg(kg + i * 8 + q) : 0u, at ? __ldg(kg + i * 8 + 4 + q) : 0u);
+                mma(edge, qa[i], at ? kg[i * 8 + q] : 0u, at ? kg[i * 8 + 4 + q] : 0u);
         }
         float prev[RH], behind[RH], m[RH], pm[RH], l[RH], w0[RH];
 #pragma unroll
@@ -856,7 +858,7 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
                         c += o[i][3];
                     }
                     if (sink_v) {
-                        const uint32_t v2 = __ldg(sink_v + i * 4 + q);
+                        const uint32_t v2 = sink_v[i * 4 + q];
                         a = fmaf(w0[h], __uint_as_float(v2 << 16), a);
                         c = fmaf(w0[h], __uint_as_float(v2 & 0xffff0000u), c);
                     }
