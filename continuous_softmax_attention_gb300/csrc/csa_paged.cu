@@ -11,10 +11,10 @@
 //
 // What bounds it: the cached rows are read once, HBM bandwidth.  What follows
 // from that:
-//  - A warp is a worker of its own.  It has a ring of tiles in shared memory
-//    that it fills itself by TMA (its lane 0), runs over a contiguous range of
-//    tiles and never waits for another warp, so some warp's copies are always
-//    in flight: 192 KiB of rings per SM.
+//  - A warp (at d = 256 two, in step) is a worker of its own.  It has a ring of
+//    tiles in shared memory that it fills itself by TMA (one lane), runs over a
+//    contiguous range of tiles and never waits for another worker, so some
+//    worker's copies are always in flight: 192 KiB of rings per SM.
 //  - The tiles of all (sequence, cached head, block of query heads) in a row
 //    are cut into equal ranges, one per worker, whatever the lengths.  The
 //    lengths are on the device, so every block forms the cut itself.
@@ -84,14 +84,21 @@ __device__ int g_paged_status;  // sticky status word of this file's kernels
 template <int D, int RH>
 struct Cfg {
     static constexpr int KT = 16;                      // rows per tile
-    // Workers per block: one per scheduler at d = 256, whose sums alone are 128 registers, two at
-    // d = 128.  At d = 64 three: 16 workers of 128 registers spill with 16 heads (92 us for 268 MB,
-    // 75 us with 12), and with 8 leave more parts to join (2 x 131072 tokens 33.4 us, 31.4 with 12).
-    static constexpr int Warps = D == 64 ? 12 : 1024 / D;
+    // Workers per block.  At d = 64 twelve: 16 of 128 registers spill with 16 heads (92 us for 268
+    // MB, 75 us with 12), and with 8 there are more parts to join (2 x 131072 tokens 33.4 us, 31.4
+    // with 12).
+    static constexpr int Workers = D == 64 ? 12 : 1024 / D;
+    // Warps of a worker: at d = 256 two, each for half of the output's columns and both for all
+    // logits: the sums of one warp alone would be 128 registers, and it would spill.  537 MB of 128
+    // cached heads with 8 and 16 query heads each take 92 and 108 us, 97 and 139 with one warp, 32
+    // heads of 333 tokens 7.8 and 8.6.  At d = 128 (6 workers of two) it is slower: 103 and 143 us, 89
+    // and 98 with one.
+    static constexpr int Pair = D == 256 ? 2 : 1;
+    static constexpr int Warps = Workers * Pair;
     static constexpr int Stages = D == 64 ? 4 : 3;     // tiles in a worker's ring
     static constexpr int Tile = KT * D * 2;            // bytes of a tile of keys, or of values
     static constexpr int Stage = 2 * Tile;
-    static constexpr int Smem = Warps * Stages * Stage + 1024;  // + alignment
+    static constexpr int Smem = Workers * Stages * Stage + 1024;  // + alignment
     static_assert(Smem <= 227 * 1024 - 6144, "one block per SM");
 };
 
@@ -363,22 +370,31 @@ __global__ void __launch_bounds__(Cfg<D, RH>::Warps * 32, 1)
 paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUtensorMap map_k,
              const __grid_constant__ CUtensorMap map_v) {
     using C = Cfg<D, RH>;
-    constexpr int KT = C::KT, NT = KT / 8, KS = D / 16, ON = D / 8, kStages = C::Stages;
+    constexpr int KT = C::KT, NT = KT / 8, KS = D / 16, kStages = C::Stages;
+    constexpr int DW = D / C::Pair, ON = DW / 8;  // columns of the output that a warp forms
     extern __shared__ uint8_t raw[];
     __shared__ long long s_cut[ONE ? 1 : C::Warps * 32 + 1];
-    __shared__ __align__(8) uint64_t bars[C::Warps][kStages];
-    __shared__ int s_abort[C::Warps];
+    __shared__ __align__(8) uint64_t bars[C::Workers][kStages];
+    __shared__ int s_abort[C::Workers];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
     const int heads = p.Hkv * p.GB;
     const long long most = (long long)p.M * p.S;
-    volatile int *abort_flag = &s_abort[warp];
+    const int mine = warp / C::Pair, half_of = warp % C::Pair;  // worker in the block, warp of the worker
+    volatile int *abort_flag = &s_abort[mine];
+    // the warps of a worker
+    auto sync_worker = [&]() {
+        if (C::Pair == 1)
+            __syncwarp();
+        else
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + mine), "n"(32 * C::Pair) : "memory");
+    };
 
-    if (lane == 0) {
-        for (int s = 0; s < kStages; ++s) mbar_init(smem_u32(&bars[warp][s]), 1);
+    if (lane == 0 && half_of == 0) {
+        for (int s = 0; s < kStages; ++s) mbar_init(smem_u32(&bars[mine][s]), 1);
         fence_mbar_init();
-        s_abort[warp] = 0;
+        s_abort[mine] = 0;
     }
-    __syncwarp();
+    sync_worker();
     after_previous();
     Part now;
     Cut cut = {};
@@ -408,17 +424,17 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
             return;
         }
         // parts across blocks first
-        parts = min(C::Warps * p.cluster, now.tiles);
-        const int mine = warp * p.cluster + rank;
-        working = mine < parts;
-        now.tile = working ? (int)quot((long long)mine * now.tiles, parts) : 0;
-        now.last = working ? (int)quot((long long)(mine + 1) * now.tiles, parts) : 1;
+        parts = min(C::Workers * p.cluster, now.tiles);
+        const int part = mine * p.cluster + rank;
+        working = part < parts;
+        now.tile = working ? (int)quot((long long)part * now.tiles, parts) : 0;
+        now.last = working ? (int)quot((long long)(part + 1) * now.tiles, parts) : 1;
     } else {
         const bool few = p.B <= 32;  // sequences: every warp forms the cut
         const int lane_n = few && lane < p.B ? p.seqlens[lane] : 0;
         // the join's blocks may take their places as this kernel's blocks end
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-        const long long all = (long long)C::Warps * gridDim.x;
+        const long long all = (long long)C::Workers * gridDim.x;
         long long lane_before = 0;
         cut = few ? form_cut_warp(lane_n, KT, most, heads, all, lane_before)
                   : form_cut(p.seqlens, p.B, KT, most, heads, all, s_cut);
@@ -438,8 +454,8 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
         }
 
         // workers are numbered across blocks first, so that few of them spread over all SMs
-        worker = (long long)warp * gridDim.x + blockIdx.x;
-        if (lane == 0 && !p.by_segment) p.joins[worker] = make_int4(-1, 0, 0, 0);
+        worker = (long long)mine * gridDim.x + blockIdx.x;
+        if (lane == 0 && half_of == 0 && !p.by_segment) p.joins[worker] = make_int4(-1, 0, 0, 0);
         if (worker >= cut.in_use) return;
         u0 = quot(worker * cut.U, cut.in_use);
         u1 = quot((worker + 1) * cut.U, cut.in_use);
@@ -463,7 +479,7 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
     auto page_index = [&](int row) { return (int)__umul64hi((unsigned long long)row, p.s_inv); };  // row / S
     auto cached_head = [&](int head) { return p.GB == 1 ? head : head / p.GB; };
 
-    const uint32_t ring = (smem_u32(raw) + 1023) / 1024 * 1024 + warp * (kStages * C::Stage);
+    const uint32_t ring = (smem_u32(raw) + 1023) / 1024 * 1024 + mine * (kStages * C::Stage);
     const int R = p.R, pieces = KT / R;
     const uint32_t half = (uint32_t)R * 128;  // bytes of one 64-column box of a copy
 
@@ -493,7 +509,8 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
 
     Part ahead = now;
     bool more = working;  // something is left to copy
-    int held_b = -1, held_at = -1, held = 0;  // page numbers, one per lane
+    // one piece per lane: its row of the pool for cached head 0, -1 on a page out of range, -2 behind the end
+    int held_b = -1, held_at = -1, held = 0;
     unsigned copied = 0, used = 0, bad_stages = 0;
     int copy_stage = 0;
     auto copy_next = [&]() {
@@ -503,27 +520,28 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
             held_b = ahead.b;
             held_at = first & ~31;
             const long long row = (long long)(held_at + lane) * R;
-            held = row < ahead.n ? p.table[(long long)ahead.b * p.M + page_index((int)row)] : 0;
+            held = -2;
+            if (row < ahead.n) {
+                const int index = page_index((int)row), page = p.table[(long long)ahead.b * p.M + index];
+                held = page >= 0 && page < p.P ? page * p.Hkv * p.S + (int)row - index * p.S : -1;
+            }
         }
-        const uint32_t bar = smem_u32(&bars[warp][copy_stage]), at = ring + copy_stage * C::Stage;
+        const uint32_t bar = smem_u32(&bars[mine][copy_stage]), at = ring + copy_stage * C::Stage;
         int bytes = 0, place[KT / 8];
 #pragma unroll
         for (int i = 0; i < KT / 8; ++i) {
             place[i] = -1;
             if (i < pieces) {
-                const int row = ahead.tile * KT + i * R;
-                const int page = __shfl_sync(0xffffffffu, held, (first + i) & 31);
-                if (row < ahead.n) {
-                    if (page >= 0 && page < p.P) {
-                        place[i] = (page * p.Hkv + cached_head(ahead.head)) * p.S + row - page_index(row) * p.S;
-                        bytes += 2 * R * D * 2;
-                    } else {
-                        bad_stages |= 1u << copy_stage;
-                    }
+                const int at = __shfl_sync(0xffffffffu, held, (first + i) & 31);
+                if (at >= 0) {
+                    place[i] = at + cached_head(ahead.head) * p.S;
+                    bytes += 2 * R * D * 2;
+                } else if (at == -1) {
+                    bad_stages |= 1u << copy_stage;
                 }
             }
         }
-        if (lane == 0) {
+        if (lane == 0 && half_of == 0) {
             mbar_arrive_expect_tx(bar, bytes);
 #pragma unroll
             for (int i = 0; i < KT / 8; ++i)
@@ -540,19 +558,21 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
 
     // ldmatrix addresses: keys, lane -> row (lane & 7) + 8 * (lane >> 4) of a pair of column
     // tiles, chunk (lane >> 3) & 1; values, lane -> row (lane & 15), chunk lane >> 4.  Row r of a
-    // tile lies in copy r / R; its 16-byte chunks are permuted by r & 7.
+    // tile lies in copy r / R; its 16-byte chunks are permuted by r & 7: tiles begin on 1024 bytes, so
+    // chunk c of a lane's row is its chunk 0 with bits 4 to 6 of the address flipped by c & 7.
     auto row_at = [&](int r) { return (uint32_t)((r / R) * (R * D * 2) + (r % R) * 128); };
     uint32_t k_row[NT / 2], v_row[KT / 16];
+    const uint32_t x7 = lane & 7;
 #pragma unroll
-    for (int i = 0; i < NT / 2; ++i) k_row[i] = row_at(16 * i + (lane & 7) + 8 * (lane >> 4));
+    for (int i = 0; i < NT / 2; ++i) k_row[i] = row_at(16 * i + (lane & 7) + 8 * (lane >> 4)) + ((x7 ^ ((lane >> 3) & 1)) << 4);
 #pragma unroll
-    for (int i = 0; i < KT / 16; ++i) v_row[i] = row_at(16 * i + (lane & 15));
-    const uint32_t x7 = lane & 7, k_chunk = (lane >> 3) & 1, v_chunk = lane >> 4;
-    auto chunk_at = [&](uint32_t c) { return (c >> 3) * half + (((c & 7) ^ x7) << 4); };
+    for (int i = 0; i < KT / 16; ++i) v_row[i] = row_at(16 * i + (lane & 15)) + ((x7 ^ (lane >> 4)) << 4);
+    const uint32_t to_half = half_of * (DW / 64) * half;
+    auto chunk = [&](uint32_t row, uint32_t c) { return (row ^ ((c & 7) << 4)) + (c >> 3) * half; };
 
     int stage = 0;
     uint32_t parity = 0;
-    bool lost = false;  // a wait has run out (ONE: the block still meets its barriers)
+    bool lost = false;  // a wait has run out
     while (working) {
         const int b = now.b, n = now.n, tile = now.tile, last = now.last;
         const int hk = cached_head(now.head), hb = now.head - hk * p.GB;
@@ -581,6 +601,7 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
             for (int i = 0; i < KS; ++i)
                 mma(edge, qa[i], at ? kg[i * 8 + q] : 0u, at ? kg[i * 8 + 4 + q] : 0u);
         }
+        // prev, and pm = 2^{prev - m}, are those of the row before (used by q = 3)
         float prev[RH], behind[RH], m[RH], pm[RH], l[RH], w0[RH];
 #pragma unroll
         for (int h = 0; h < RH; ++h) {
@@ -649,7 +670,7 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
 #pragma unroll
                 for (int i = 0; i < ON / 2; ++i) {
                     uint32_t vb[4];
-                    ldsm_t(v_at + v_row[ks] + chunk_at(2 * i + v_chunk), vb);
+                    ldsm_t(chunk(v_at + v_row[ks], 2 * i) + to_half, vb);
                     if (RH == 1) {
                         const uint32_t a[4] = {hi[0][0], lo[0][0], hi[0][1], lo[0][1]};
                         mma(o[2 * i], a, vb[0], vb[1]);
@@ -667,21 +688,27 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
         };
 
         for (int j = tile; j < last; ++j) {
-            const bool arrived = mbar_wait_bounded(smem_u32(&bars[warp][stage]), parity, abort_flag,
-                                                   &g_paged_status, kWaitLimitNs);
-            if (!__all_sync(0xffffffffu, arrived)) {
-                // keeps the ring alive until its copies have landed, for at most one more limit each
-                if (lane == 0)
-                    for (unsigned i = used; i < copied; ++i) {
-                        const uint32_t bar = smem_u32(&bars[warp][i % kStages]);
-                        const uint64_t t0 = globaltimer_ns();
-                        while (!mbar_try_wait(bar, (i / kStages) & 1) && globaltimer_ns() - t0 < kWaitLimitNs) {
+            if (C::Pair == 1 || !lost) {
+                const bool arrived = mbar_wait_bounded(smem_u32(&bars[mine][stage]), parity, abort_flag,
+                                                       &g_paged_status, kWaitLimitNs);
+                if (!__all_sync(0xffffffffu, arrived)) {
+                    // keeps the ring alive until its copies have landed, for at most one more limit each
+                    if (lane == 0 && half_of == 0)
+                        for (unsigned i = used; i < copied; ++i) {
+                            const uint32_t bar = smem_u32(&bars[mine][i % kStages]);
+                            const uint64_t t0 = globaltimer_ns();
+                            while (!mbar_try_wait(bar, (i / kStages) & 1) && globaltimer_ns() - t0 < kWaitLimitNs) {
+                            }
                         }
-                    }
-                __syncwarp();
-                if (!ONE) return;
-                lost = true;
-                break;
+                    __syncwarp();
+                    if (C::Pair == 1 && !ONE) return;
+                    lost = true;
+                    if (C::Pair == 1) break;
+                }
+            }
+            if (C::Pair > 1 && lost) {  // the worker's barriers are still met
+                if (j > tile) sync_worker();
+                continue;
             }
             if (bad_stages >> stage & 1) {
                 bad = true;
@@ -692,8 +719,8 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
             if (own < KT) {
                 // rows behind the end: their weights are 0, and 0 * NaN is not
                 uint8_t *vt = raw + (k_at + C::Tile - smem_u32(raw));
-                for (int i = lane; i < (KT - own) * (D / 8); i += 32) {
-                    const int r = own + i / (D / 8), c = i % (D / 8);
+                for (int i = lane; i < (KT - own) * ON; i += 32) {
+                    const int r = own + i / ON, c = half_of * ON + i % ON;
                     *reinterpret_cast<uint4 *>(vt + row_at(r) + (c >> 3) * half + ((c & 7) << 4)) =
                         make_uint4(0u, 0u, 0u, 0u);
                 }
@@ -711,23 +738,32 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
 #pragma unroll
                 for (int i = 0; i < NT / 2; ++i) {
                     uint32_t kb[4];
-                    ldsm(k_at + k_row[i] + chunk_at(2 * ks + k_chunk), kb);
+                    ldsm(chunk(k_at + k_row[i], 2 * ks), kb);
                     mma(ks & 1 ? s2[2 * i] : s[2 * i], qa[ks], kb[0], kb[1]);
                     mma(ks & 1 ? s2[2 * i + 1] : s[2 * i + 1], qa[ks], kb[2], kb[3]);
                 }
             float top[RH];
             bool over = false;
 #pragma unroll
+            for (int h = 0; h < RH; ++h)
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) s[i][2 * h + e] = (s[i][2 * h + e] + s2[i][2 * h + e]) * p.qscale;
+            if (own < KT) {
+#pragma unroll
+                for (int h = 0; h < RH; ++h)
+#pragma unroll
+                    for (int i = 0; i < NT; ++i)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            if (8 * i + 2 * q + e >= own) s[i][2 * h + e] = -INFINITY;
+            }
+#pragma unroll
             for (int h = 0; h < RH; ++h) {
                 top[h] = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < NT; ++i) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        s[i][2 * h + e] = (s[i][2 * h + e] + s2[i][2 * h + e]) * p.qscale;
-                        if (8 * i + 2 * q + e < own) top[h] = fmaxf(top[h], s[i][2 * h + e]);
-                    }
-                }
+                for (int i = 0; i < NT; ++i) top[h] = fmaxf(top[h], fmaxf(s[i][2 * h], s[i][2 * h + 1]));
                 over |= top[h] > m[h] + kRaise;
             }
             if (j == tile) {
@@ -745,11 +781,12 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
                 }
             }
 
-            // this tile's weights, and the share of its first interval that the row before gets
-            float nw[RH][NT][2], to_before[RH];
+            // this tile's weights, and the share of its first interval that the row before gets (for q = 3,
+            // whose w holds that row)
+            float nw[RH][NT][2], even_left[RH][NT], to_before[RH];
 #pragma unroll
             for (int h = 0; h < RH; ++h) {
-                float pe[NT][2], even_left[NT];
+                float pe[NT][2];
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
                     pe[i][0] = ex2_approx(s[i][2 * h] - m[h]);
@@ -765,36 +802,43 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
                     const float p_b = __shfl_sync(0xffffffffu, p_src, (lane & ~3) | ((q + 3) & 3));
                     float r_even, l_odd, r_odd;
                     intervals(a_b, s[i][2 * h], s[i][2 * h], s[i][2 * h + 1], p_b, pe[i][0], pe[i][0], pe[i][1],
-                              even_left[i], r_even, l_odd, r_odd);
-                    if (8 * i + 2 * q >= own) even_left[i] = r_even = 0.f;
-                    if (8 * i + 2 * q + 1 >= own) l_odd = r_odd = 0.f;
+                              even_left[h][i], r_even, l_odd, r_odd);
                     nw[h][i][0] = r_even + l_odd;
                     nw[h][i][1] = r_odd;
+                    if (own < KT) {  // nothing from intervals that end behind the last row
+                        if (8 * i + 2 * q + 1 >= own) {
+                            nw[h][i][0] = r_even;
+                            nw[h][i][1] = 0.f;
+                        }
+                        if (8 * i + 2 * q >= own) nw[h][i][0] = even_left[h][i] = 0.f;
+                    }
                 }
-                to_before[h] = __shfl_sync(0xffffffffu, even_left[0], lane & ~3);
+                // for the next tile, and for q = 3 only
+                prev[h] = s[NT - 1][2 * h + 1];
+                pm[h] = pe[NT - 1][1];
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
-                    const float src = q == 0 ? (i + 1 < NT ? even_left[i + 1 < NT ? i + 1 : 0] : 0.f) : even_left[i];
-                    nw[h][i][1] += __shfl_sync(0xffffffffu, src, (lane & ~3) | ((q + 1) & 3));
+                    const float src = q == 0 ? even_left[h][i + 1 < NT ? i + 1 : 0] : even_left[h][i];
+                    const float from = __shfl_sync(0xffffffffu, src, (lane & ~3) | ((q + 1) & 3));
+                    if (i + 1 < NT || q < 3) nw[h][i][1] += from;
+                    if (i + 1 == NT) to_before[h] = from;
                 }
-                prev[h] = __shfl_sync(0xffffffffu, s[NT - 1][2 * h + 1], lane | 3);
-                pm[h] = __shfl_sync(0xffffffffu, pe[NT - 1][1], lane | 3);
             }
             if (j > tile) {
 #pragma unroll
                 for (int h = 0; h < RH; ++h)
                     if (q == 3) w[h][NT - 1][1] += to_before[h];
                 values();
-                __syncwarp();  // every lane has read the tile before: its stage is free
+                sync_worker();  // every lane has read the tile before: its stage is free
                 ++used;
                 copy_next();
             } else if (copied_sink) {  // its value is the first row's too
 #pragma unroll
                 for (int h = 0; h < RH; ++h)
-                    if (q == 0) nw[h][0][0] += to_before[h];
+                    if (q == 0) nw[h][0][0] += even_left[h][0];
             } else if (r0 == 0) {
 #pragma unroll
-                for (int h = 0; h < RH; ++h) w0[h] = to_before[h];
+                for (int h = 0; h < RH; ++h) w0[h] = __shfl_sync(0xffffffffu, even_left[h][0], lane & ~3);
             }
 #pragma unroll
             for (int h = 0; h < RH; ++h)
@@ -823,9 +867,11 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
             }
         }
         if (!lost) values();
-        __syncwarp();
-        ++used;
-        copy_next();
+        sync_worker();
+        if (!lost) {
+            ++used;
+            copy_next();
+        }
 
         bad = __any_sync(0xffffffffu, bad || lost);
         const bool whole = r0 == 0 && r1 == n;
@@ -841,15 +887,15 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
         const long long slot = (worker * 2 + (u0 < now.s0 ? 1 : 0)) * p.HB;
         // ONE: this warp's ring, whose copies have all been read
         float *kept = reinterpret_cast<float *>(raw + (ring - smem_u32(raw)));
-        const uint32_t *sink_v = given ? reinterpret_cast<const uint32_t *>(p.v0 + (long long)hk * D) : nullptr;
+        const uint32_t *sink_v = given ? reinterpret_cast<const uint32_t *>(p.v0 + (long long)hk * D + half_of * DW) : nullptr;
 #pragma unroll
         for (int h = 0; h < RH; ++h) {
             const int row = g + 8 * h;
             if (row < rows_h) {
                 const float inv = 1.0f / sum[h];
                 const long long oh = (long long)b * p.Hq + q0 + row;
-                __nv_bfloat16 *og = p.out + oh * D;
-                float *po = ONE ? kept + row * D : p.part_o + (slot + row) * D;
+                __nv_bfloat16 *og = p.out + oh * D + half_of * DW;
+                float *po = (ONE ? kept + row * D : p.part_o + (slot + row) * D) + half_of * DW;
 #pragma unroll
                 for (int i = 0; i < ON; ++i) {
                     float a = o[i][2 * h], c = o[i][2 * h + 1];
@@ -867,7 +913,7 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
                     else
                         *reinterpret_cast<float2 *>(po + 8 * i + 2 * q) = make_float2(a, c);
                 }
-                if (q == 0) {
+                if (q == 0 && half_of == 0) {
                     if (ONE) {
                         *reinterpret_cast<float2 *>(kept + p.HB * D + 2 * row) = make_float2(m[h], sum[h]);
                     } else if (!whole) {
@@ -880,7 +926,7 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
             }
         }
         if (bad && lane == 0) atomicCAS(&g_paged_status, 0, CSA_ERR_INVALID_ARG);
-        if (!ONE && r0 == 0 && lane == 0 && (p.by_segment || !whole)) {
+        if (!ONE && r0 == 0 && lane == 0 && half_of == 0 && (p.by_segment || !whole)) {
             const long long end = now.s0 + cut.units(now.tiles);
             const int segment = b * heads + now.head;
             p.joins[p.by_segment ? segment : worker] =
@@ -918,7 +964,7 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
             for (int c = 0; c < D; c += 64) {
                 float2 v = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int i = 0; i < C::Warps; ++i) {
+                for (int i = 0; i < C::Workers; ++i) {
                     const float fi = __shfl_sync(0xffffffffu, f, i);
                     if (i < count) {
                         const float2 x = *reinterpret_cast<const float2 *>(of(i) + row * D + c + 2 * lane);
@@ -1127,7 +1173,7 @@ int launch(PagedParams &p, cudaStream_t stream) {
     const int heads = p.Hkv * p.GB;
     p.s_inv = ~0ull / p.S + 1;
     const long long segments = (long long)p.B * heads, tiles = ((long long)p.M * p.S + C::KT - 1) / C::KT;
-    p.cluster = cluster_for(segments, tiles, C::Warps);
+    p.cluster = cluster_for(segments, tiles, C::Workers);
     if (p.cluster > 0) {
         auto kern = paged_kernel<D, RH, true>;
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::Smem) != cudaSuccess ||
@@ -1142,7 +1188,7 @@ int launch(PagedParams &p, cudaStream_t stream) {
     auto kern = paged_kernel<D, RH, false>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::Smem) != cudaSuccess)
         return CSA_ERR_CUDA;
-    const long long all = (long long)grid * C::Warps;
+    const long long all = (long long)grid * C::Workers;
     p.by_segment = segments <= kGrid;
     if (launch_after_previous(kern, grid, C::Warps * 32, C::Smem, stream, p, map_k, map_v) != cudaSuccess)
         return CSA_ERR_CUDA;
