@@ -336,3 +336,41 @@ def test_refusals():
         assert e.value.code == code
     o, lse = call(q=c["q"][:0], table=table[:0], lens=lens[:0])
     assert o.shape == (0, 4, 128) and lse.shape == (0, 4)
+
+
+@pytest.mark.parametrize("d", [64, 256])
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (7, 1), (10, 2), (16, 1), (17, 1), (9, 3)])
+@FORMS
+def test_head_groups_of_other_widths(d, Hq, Hkv, wide):
+    x = make([5, 333, 0, 40, 1, 1500], Hq, Hkv, d, 24, seed=Hq + d, wide=wide)
+    for mode in (0, 1, 2):
+        o, lse = run(x, mode)
+        check(x, o, lse, 24, mode, d ** -0.5)
+
+
+@pytest.mark.parametrize("d", [64, 256])
+@pytest.mark.parametrize("Hq", [2, 24])
+@FORMS
+def test_garbage_infinities_and_repeats_of_other_widths(d, Hq, wide):
+    lens, S = [1, 17, 100, 0, 129, 2040], 8
+    x = make(lens, Hq, 2, d, S, seed=d + Hq, wide=wide)
+    want, wl = run(x, 0)
+    held = set()
+    for b, n in enumerate(lens):
+        ids = x["table"][b, :pages_of(n, S)]
+        held.update(ids.tolist())
+        if n % S:
+            x["k"][ids[-1], :, n % S:], x["v"][ids[-1], :, n % S:] = float("nan"), float("inf")
+    rest = [p for p in range(x["k"].shape[0]) if p not in held]
+    x["k"][rest], x["v"][rest] = float("nan"), float("nan")
+    need = decode_paged_workspace_bytes(len(lens), Hq, 2, d)
+    for fill in (255, 0, 127):
+        o, lse = run(x, 0, workspace=torch.full((max(need, 16),), fill, dtype=torch.uint8, device="cuda"))
+        assert torch.equal(o, want) and torch.equal(lse, wl)
+    # an infinite value in either half of the columns; a page out of range
+    x["v"][x["table"][2, 3], :, 2, 5], x["v"][x["table"][5, 9], :, 1, d - 3] = float("inf"), float("-inf")
+    x["table"][4, 1] = x["k"].shape[0]
+    o, lse = run(x, 0, 0.0)
+    assert torch.isposinf(o[2, :, 5]).all() and torch.isneginf(o[5, :, d - 3]).all()
+    assert torch.isfinite(o[2, :, 6:].float()).all() and torch.isfinite(o[5, :, :d - 3].float()).all()
+    assert torch.isnan(o[4].float()).all() and torch.isnan(lse[4]).all() and device_status() == -1
