@@ -26,7 +26,7 @@
 //    warp that needs them.
 //  - The weights enter the second product as a sum of two bf16 numbers (15
 //    bits of the weight), the high part cut off so that neither is negative
-//    and the low one at least 2^-20 of the weight: an infinite value stays one.
+//    and the low one at least 2^-23 of the weight: an infinite value stays one.
 //    For up to 8 heads both halves fit one instruction: rows 0..7 hold the high
 //    parts and rows 8..15 the low ones.
 //  - Few short sequences are bound by latency: a cluster of blocks then does one
@@ -664,8 +664,10 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
                         const float a = w[h][2 * ks + i][0], c = w[h][2 * ks + i][1];
                         const uint32_t ua = __float_as_uint(a) & 0xffff0000u, uc = __float_as_uint(c) & 0xffff0000u;
                         hi[h][i] = __byte_perm(ua, uc, 0x7632);
-                        lo[h][i] = pack_bf16x2(fmaxf(a - __uint_as_float(ua), a * 9.5367431640625e-07f),
-                                               fmaxf(c - __uint_as_float(uc), c * 9.5367431640625e-07f));
+                        float la, lc;  // a (1 + 2^-23) - high part: never 0
+                        apart(fma2(two(a, c), both(1.00000011920928955f),
+                                   two(-__uint_as_float(ua), -__uint_as_float(uc))), la, lc);
+                        lo[h][i] = pack_bf16x2(la, lc);
                     }
 #pragma unroll
                 for (int i = 0; i < ON / 2; ++i) {
