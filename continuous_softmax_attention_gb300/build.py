@@ -102,7 +102,7 @@ def link_module(obj, verbose=False):
 
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     tmp = TORCH_LIB_PATH + f".tmp{os.getpid()}"
-    _run(["g++", "-shared", "-o", tmp, obj, "-L" + HERE, "-l:" + os.path.basename(LIB_PATH), "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-lc10",
+    _run(["g++", "-shared", "-o", tmp, obj, "-L" + HERE, "-l:" + os.path.basename(LIB_PATH), "-L" + lib, "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10",
           "-lc10_cuda", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib], verbose, "link of _csa_torch.so")
     os.replace(tmp, TORCH_LIB_PATH)
 

@@ -10,7 +10,7 @@
 // outputs in Python 13 to 20 us, here 2 to 3 us.
 #include <Python.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -69,8 +69,10 @@ void need(const Tensor &t, const char *name, at::ScalarType dtype, IntArrayRef s
     TORCH_CHECK_VALUE(t.is_contiguous(), name, " must be contiguous");
 }
 
+// The allocator's tensor without the dispatcher's two hops: 0.2 us less each (rope with two outputs
+// 5.2 -> 5.0 us a call, 2.7 with given ones).
 Tensor made(IntArrayRef shape, at::ScalarType dtype, const at::Device &dev) {
-    return at::empty(shape, at::TensorOptions().dtype(dtype).device(dev));
+    return Tensor(at::detail::empty_cuda(shape, dtype, dev, std::nullopt));
 }
 
 // The given output, checked, or a new one.
