@@ -10,8 +10,9 @@
 // Angles.  Far positions lose an angle formed in fp32 (at 2^20 radians a step
 // of fp32 is 1/16), so the angle is formed in turns, in integers: the plan
 // holds base^(-i/n) / 2 pi as a 64-bit fraction F of a turn, and p * F modulo
-// 2^64 is the angle's fraction of a turn, exact up to p * 2^-65.  Its top 32
-// bits, as a signed number, go to sincospif.
+// 2^64 is the angle's fraction of a turn, off by |p| times what F is off by
+// (2^-65 turns for its rounding).  Its top 32 bits, as a signed number, go to
+// sincospif.
 //
 // What bounds it.  Each element is read once and written once: HBM bandwidth.
 // A thread owns 16 bytes twice (the two members of 8 bf16 or 4 fp32 pairs) of
@@ -25,6 +26,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 
@@ -284,15 +286,16 @@ int csa_rope_plan_make(csa_rope_plan *plan, const int *sections, int axes, doubl
         for (int a = 0; a < axes; ++a)
             for (int j = 0; j < left[a]; ++j) plan->axis[i++] = (unsigned char)a;
     }
-    // the frequencies in turns per position, base^(-i/n) / 2 pi, as fractions of a turn times 2^64;
-    // one power and n products (a power of this type costs 2 us where it is 128 bits wide), off by
-    // at most n 2^-63 relative
-    const long double step = powl((long double)base, -1.0L / total);
-    long double f = 0.159154943091895335768883763372514362L;
+    // The frequencies in turns per position, base^(-i/n) / 2 pi, as fractions of a turn times 2^64.
+    // A power each where a long double has 64 bits: (|ln base| + 4) 2^-64 relative.  Where it has 113
+    // a power is computed in software (2 us), so one power and n products: n 2^-111 relative.
+    const long double whole = 0.159154943091895335768883763372514362L, step = powl((long double)base, -1.0L / total);
+    long double f = whole;
     for (i = 0; i < total; ++i) {
-        const long double frac = f - floorl(f);
-        plan->turn[i] = (unsigned long long)(ldexpl(frac, 63) + 0.25L) * 2ull;
-        f *= step;
+        const long double units = ldexpl(f - floorl(f), 64);
+        const unsigned long long down = (unsigned long long)units;
+        plan->turn[i] = down + (units - (long double)down >= 0.5L ? 1 : 0);  // to nearest; 2^64 is 0, a whole turn
+        f = LDBL_MANT_DIG > 64 ? f * step : whole * powl((long double)base, -(long double)(i + 1) / total);
     }
     return CSA_OK;
 }
