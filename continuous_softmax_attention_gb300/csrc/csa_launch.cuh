@@ -28,8 +28,8 @@ inline cudaError_t launch_clusters_after_previous(void (*kernel)(P...), dim3 gri
     attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
     cfg.attrs = attrs;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
-    return e == cudaSuccess ? cudaGetLastError() : e;
+    (void)cudaLaunchKernelEx(&cfg, kernel, args...);
+    return cudaGetLastError();  // and taken, or the next launch would report it too
 }
 
 template <typename... P, typename... A>

@@ -506,9 +506,10 @@ int csa_rope_plan_init(csa_rope_plan *plan, const int *sections, int axes, doubl
  *   the other columns copied: (u, w) -> (u cos - w sin, u sin + w cos) per
  *   pair, by the negative angle if `inverse` (the backward pass: the gradient
  *   of the input from the gradient of the output).  fp32 arithmetic, one
- *   rounding.  The distance of an angle to the nearest quarter of a turn is
- *   right within 2^-23 relative and |position| * 2^-65 turns (base >= 1), and
- *   opposite positions turn by exactly opposite angles.
+ *   rounding.  Turns per position are right within 2^-65 and, on hosts with
+ *   64-bit long doubles, (ln base + 4) 2^-64 relative (base >= 1); the angle's
+ *   distance to the nearest quarter of a turn is then rounded by 2^-23
+ *   relative, and opposite positions turn by exactly opposite angles.
  *   q, q_out: bf16 [B, Hq, T, d]; k, k_out: bf16 [B, Hkv, T, d], not read
  *   where the head count is 0.  *_strides: HOST long long[3], the strides over
  *   batch, head and time in elements (the last dimension is contiguous); NULL
