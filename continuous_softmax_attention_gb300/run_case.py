@@ -107,12 +107,13 @@ def run_paged(a):
     table = torch.full((a.B, M), -1, dtype=torch.int32, device="cuda")
     held = torch.zeros(a.B, dtype=torch.int32, device="cuda")
     one = torch.ones(a.B, dtype=torch.int32, device="cuda")
+    sink = dict(k0=bf(kv, a.d), v0=bf(kv, a.d)) if a.mode == csa.GIVEN else {}
     plan = csa.RopeAxes(a.d, (a.d // 2,))
     short = csa.cache_reserve(refs, table, held, a.page, lens)
     for _ in range(a.iters):
         short += csa.cache_reserve(refs, table, held, a.page, one)
         q = csa.cache_append(x[:, a.H:a.H + kv], x[:, a.H + kv:], k, v, table, held, rope=plan, q=x[:, :a.H])
-        o, lse = csa.decode_paged(q[:, :, 0], k, v, table, held, mode=csa.COPY_FIRST if a.mode == 2 else a.mode)
+        o, lse = csa.decode_paged(q[:, :, 0], k, v, table, held, mode=a.mode, **sink)
     torch.cuda.synchronize()
     st = csa.device_status()
     print(f"ok status={st} short={short.item()} o_mean={o.float().abs().mean().item():.5f}")
