@@ -5,7 +5,10 @@ Signatures and documentation; the checks of the arguments and the calls are in
 csrc/csa_torch.cpp (module _csa_torch, built beside libcsa.so).  Every call
 runs on the device of its tensors and is asynchronous on torch's current
 stream there, or on ``stream``; what it allocates (outputs, workspaces)
-belongs to that stream.
+belongs to that stream.  Outside autograd, as the rest of the package: results
+have no history, also where an input requires a gradient (rope_backward gives
+it).  What a call writes gets a new version, so that autograd refuses to go
+backward through a saved tensor that was overwritten.
 """
 from __future__ import annotations
 

@@ -70,7 +70,8 @@ void need(const Tensor &t, const char *name, at::ScalarType dtype, IntArrayRef s
 }
 
 // The allocator's tensor without the dispatcher's two hops: 0.2 us less each (rope with two outputs
-// 5.2 -> 5.0 us a call, 2.7 with given ones).
+// 5.2 -> 5.0 us a call, 2.7 with given ones).  Hooks of the dispatcher do not see it, as they do not
+// see the kernels; the allocator's own statistics do.
 Tensor made(IntArrayRef shape, at::ScalarType dtype, const at::Device &dev) {
     return Tensor(at::detail::empty_cuda(shape, dtype, dev, std::nullopt));
 }
@@ -89,6 +90,12 @@ T *at_(const Tensor &t) {
 template <typename T = void>
 T *at_(const Tensor *t) {
     return t ? static_cast<T *>(t->data_ptr()) : nullptr;
+}
+
+// What a call has written: autograd compares versions to see that a saved tensor has not changed since.
+void wrote(std::initializer_list<const Tensor *> written) {
+    for (const Tensor *t : written)
+        if (t && t->defined() && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
 }
 
 // The device of the call: the first tensor's, made the current one.
@@ -175,6 +182,7 @@ PyObject *decode_paged(PyObject *, PyObject *const *a, Py_ssize_t) {
                            lse.defined() ? at_<float>(lse) : nullptr, at_(ws), (long long)ws->nbytes(), b, hq, hkv,
                            size(P, "P"), size(S, "S"), size(M, "M"), dd, (float)scale, mode, here.stream),
           "csa_decode_paged");
+    wrote({&o, &lse, ws});
     return tuple({o, lse});
     END_HANDLE_TH_ERRORS
 }
@@ -274,6 +282,7 @@ PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t) {
                            ks.strides, static_cast<float *>(kop), kos.strides, at_<int>(positions), ps, b, hq, hkv, t,
                            dd, inverse, here.stream),
               "csa_rope_f32");
+    wrote({&qo, &ko});
     return tuple({qo, ko});
     END_HANDLE_TH_ERRORS
 }
@@ -332,6 +341,7 @@ PyObject *cache_append(PyObject *, PyObject *const *a, Py_ssize_t) {
                                    at_<float>(vp), at_<int>(table), at_<int>(lens), at_<int>(counts),
                                    at_<int>(positions), ps, b, hq, hkv, t, dd, pp, ss, m, here.stream),
               "csa_cache_append_f32");
+    wrote({&kp, &vp, &qo});
     if (!qo.defined()) Py_RETURN_NONE;
     return wrap(qo);
     END_HANDLE_TH_ERRORS
@@ -340,11 +350,14 @@ PyObject *cache_append(PyObject *, PyObject *const *a, Py_ssize_t) {
 // ------------------------------------------------------------------------ pages
 struct Books {
     Here here;
+    const Tensor &t_refs, &t_table, &t_lens;
     int *refs, *table, *lens;
     int P, B, M, S;
     // page_refs, block_table, seqlens, page_size
-    Books(PyObject *const *a, const char *what) : here(tensor(a[0], "page_refs"), what) {
-        const Tensor &r = tensor(a[0], "page_refs"), &t = tensor(a[1], "block_table"), &n = tensor(a[2], "seqlens");
+    Books(PyObject *const *a, const char *what)
+        : here(tensor(a[0], "page_refs"), what), t_refs(tensor(a[0], "page_refs")),
+          t_table(tensor(a[1], "block_table")), t_lens(tensor(a[2], "seqlens")) {
+        const Tensor &r = t_refs, &t = t_table, &n = t_lens;
         TORCH_CHECK_VALUE(r.dim() == 1 && t.dim() == 2, "page_refs is [P], block_table [B, M]");
         need(r, "page_refs", at::kInt, {r.size(0)}, here.dev);
         need(t, "block_table", at::kInt, {t.size(0), t.size(1)}, here.dev);
@@ -369,6 +382,7 @@ PyObject *cache_reserve(PyObject *, PyObject *const *a, Py_ssize_t) {
     check(csa_cache_reserve(b.refs, b.table, b.lens, at_<int>(counts), at_<int>(shortfall), b.B, b.P, b.S, b.M,
                             b.here.stream),
           "csa_cache_reserve");
+    wrote({&b.t_refs, &b.t_table, &b.t_lens, &shortfall});
     return wrap(shortfall);
     END_HANDLE_TH_ERRORS
 }
@@ -382,6 +396,7 @@ PyObject *cache_free(PyObject *, PyObject *const *a, Py_ssize_t) {
     check(csa_cache_free(b.refs, b.table, b.lens, at_<int>(rows), size(rows.numel(), "rows"), b.B, b.P, b.S, b.M,
                          b.here.stream),
           "csa_cache_free");
+    wrote({&b.t_refs, &b.t_table, &b.t_lens});
     Py_RETURN_NONE;
     END_HANDLE_TH_ERRORS
 }
@@ -399,6 +414,7 @@ PyObject *cache_fork(PyObject *, PyObject *const *a, Py_ssize_t) {
     check(csa_cache_fork(b.refs, b.table, b.lens, at_<int>(parents), at_<int>(children), n, at_<int>(src),
                          at_<int>(dst), at_<int>(shortfall), b.B, b.P, b.S, b.M, b.here.stream),
           "csa_cache_fork");
+    wrote({&b.t_refs, &b.t_table, &b.t_lens});
     return tuple({src, dst, shortfall});
     END_HANDLE_TH_ERRORS
 }
@@ -411,6 +427,7 @@ PyObject *cache_compact(PyObject *, PyObject *const *a, Py_ssize_t) {
     check(csa_cache_compact(b.refs, b.table, b.lens, at_<int>(src), at_<int>(dst), at_<int>(moved), b.B, b.P, b.S, b.M,
                             b.here.stream),
           "csa_cache_compact");
+    wrote({&b.t_refs, &b.t_table});
     return tuple({src, dst, moved});
     END_HANDLE_TH_ERRORS
 }
@@ -432,6 +449,7 @@ PyObject *cache_copy_pages(PyObject *, PyObject *const *a, Py_ssize_t) {
     check(csa_cache_copy_pages(at_(k), at_(v), page, layers, size(k.size(-4), "P"), at_<int>(src), at_<int>(dst), n,
                                at_<int>(count), here.stream),
           "csa_cache_copy_pages");
+    wrote({&k, v});
     Py_RETURN_NONE;
     END_HANDLE_TH_ERRORS
 }
