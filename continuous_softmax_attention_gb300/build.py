@@ -3,7 +3,8 @@ _csa_torch (csrc/csa_torch.cpp) that calls it on torch tensors.
 
 Twelve translation units compiled in parallel, then linked into one shared
 library next to this file; the module is compiled beside them against torch's
-headers and linked against that library.  The CUDA runtime is linked statically; the CUDA
+headers and linked against that library, or left out where torch was built
+without CUDA (the library and its ctypes binding do not need it).  The CUDA runtime is linked statically; the CUDA
 driver is reached at run time through the runtime's driver entry points, so
 the library loads on a machine without a GPU driver (calls then fail with
 CSA_ERR_NO_DEVICE).
@@ -59,9 +60,8 @@ def build(verbose: bool = False, extra_flags=()) -> str:
         return obj
 
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        module = ex.submit(compile_module, build_dir, verbose)
+        module = ex.submit(compile_module, build_dir, verbose) if torch_has_cuda() else None
         objs = list(ex.map(compile_one, SOURCES))
-        module_obj = module.result()
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     cmd = [nvcc] + ARCH + ["-shared", "-o", tmp] + objs + ["-lcudart_static", "-ldl", "-lpthread", "-lrt"]
     if verbose:
@@ -70,7 +70,10 @@ def build(verbose: bool = False, extra_flags=()) -> str:
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, LIB_PATH)
-    link_module(module_obj, verbose)
+    if module is None:
+        print("torch has no CUDA half: _csa_torch is left out, its calls raise", file=sys.stderr)
+    else:  # behind the library, which does not need it
+        link_module(module.result(), verbose)
     return LIB_PATH
 
 
@@ -80,6 +83,13 @@ def _run(cmd, verbose, what):
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"{what} failed:\n{res.stdout}\n{res.stderr}")
+
+
+def torch_has_cuda():
+    """Whether torch brings the headers and libraries that the module needs."""
+    import torch
+
+    return torch.version.cuda is not None
 
 
 def compile_module(build_dir, verbose=False):
