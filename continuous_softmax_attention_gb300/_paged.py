@@ -154,7 +154,10 @@ def cache_append(k, v, k_pages, v_pages, block_table, seqlens, *, counts=None, r
     seqlens[b] - counts[b] + t of sequence b: seqlens counts the new tokens
     already, as cache_reserve leaves it.  k_pages, v_pages: [P, Hkv, S, d];
     block_table: int32 [B, M].  rope: a RopeAxes; positions as in rope(), or
-    None for a token's place in the cache.  q: [B, Hq, T, d], with rope only."""
+    None for a token's place in the cache.  q: [B, Hq, T, d], with rope only.
+    decode_paged reads bf16 pools; fp32 ones are for a caller's own attention,
+    and so is attention of a prompt's rows over the pages behind a past: the
+    calls here attend from one new token per sequence."""
     if stream is not None:
         return _there(cache_append, locals())
     if rope is None:

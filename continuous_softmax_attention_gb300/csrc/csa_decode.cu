@@ -129,7 +129,7 @@ __device__ __forceinline__ float dot8(const uint4 &q, const uint4 &k) {
 // e^{u} phi2(x) for a key at u (log2 units, u <= 0) whose neighbour is at
 // u + x2 = un (log2 units); x = x2 ln 2 is the natural-log gap and
 // pc = 2^u.  phi2(x) = (e^x - 1 - x)/x^2 ("Preliminaries", eq. (6)).
-//   |x| < 1: pc * sum_{j=0..9} x^j/(j+2)!  (truncation below 3e-9 relative);
+//   |x| < 1: pc * sum_{j=0..9} x^j/(j+2)!  (truncation below 5.3e-9 relative);
 //   x <= 20: pc * (e^x - 1 - x)/x^2, with e^x = 2^{x2};
 //   x > 20:  (2^{un} - pc (1 + x))/x^2, since pc e^x = 2^{un} <= 1 while e^x
 //            alone could overflow.

@@ -20,15 +20,26 @@
 //    lengths are on the device, so every block forms the cut itself.
 //  - The query heads of a group are the rows of the matrix instruction (16, of
 //    which 8 are used for up to 8 heads), the cached rows its columns, so one
-//    read of a cached row serves all heads of the group.  mma.sync rather than
+//    read of a cached row serves up to 16 heads of the group.  A larger group is
+//    cut into equal blocks of heads, each a segment with copies of the rows of
+//    its own: 537 MB of 8 cached heads at d = 128 take 97 us with 16 query heads
+//    each, 167 with 20 and 169 with 32.  mma.sync rather than
 //    tcgen05: with 16 rows at most the products take a few percent of the time
 //    either way, and mma.sync leaves logits and sums in the registers of the
 //    warp that needs them.
-//  - The weights enter the second product as a sum of two bf16 numbers (15
-//    bits of the weight), the high part cut off so that neither is negative
-//    and the low one at least 2^-23 of the weight: an infinite value stays one.
-//    For up to 8 heads both halves fit one instruction: rows 0..7 hold the high
-//    parts and rows 8..15 the low ones.
+//  - The weights enter the second product as a sum of two bf16 numbers, right
+//    within 2^-16 of the weight, the high part cut off so that neither is
+//    negative and the low one at least 2^-23 of the weight: an infinite value
+//    stays one.  For up to 8 heads both halves fit one instruction: rows 0..7
+//    hold the high parts and rows 8..15 the low ones.  Their sum, the
+//    denominator, is that of the fp32 weights.  Two numbers put o off by 5e-6 of
+//    its norm before it is rounded to bf16, and that rounding by 1.6e-3.  A third
+//    number makes the weights exact: o is then off by 2e-7 to 4e-7 before the
+//    rounding and by the same 1.6e-3 after it, one output in 250 being a bf16
+//    step away from what two numbers give.  It takes 122.8 us in place of 118.5
+//    (537 MB, 16 heads per group, d = 64), 98.2 of 97.2 (d = 128), 113.9 of 107.6
+//    (d = 256), 60.4 of 59.8 (64 ragged sequences), 5.8 of 5.7 (one short one):
+//    two numbers are kept.
 //  - Few short sequences are bound by latency: a cluster of blocks then does one
 //    cached head of one sequence in a single launch and joins its parts through
 //    distributed shared memory (8.7 -> 5.8 us for 32 heads of 333 tokens).
@@ -55,7 +66,9 @@ using namespace csa_dev;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
-constexpr int kGrid = 152;        // one block per SM
+// One block per SM.  Workers do not wait for one another: a part with fewer SMs
+// gives the same results, its last blocks in a second wave.
+constexpr int kGrid = 152;
 // Tiles per worker up to which latency counts: a worker per tile and no cost of
 // a part.  1024 sequences of 17 tokens x 4 heads (3.4 tiles a worker) take 21 us
 // with 2 here and 25 us with 4 or 8.
@@ -157,7 +170,7 @@ __device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
 // The weights that two intervals, between logits a0 and b0 and between a1 and
 // b1 (log2 units), give their two keys each, with p = 2^{a-m} and r = 2^{b-m}.
 // |x| < 1 (natural units): the power series sum x^j/(j+2)!, j = 0..9, truncated
-// below 3e-9 relative, split into its even and odd terms, which the two keys
+// below 5.3e-9 relative (at x = -1), split into its even and odd terms, which the two keys
 // share.
 __device__ __forceinline__ void intervals(float a0, float b0, float a1, float b1, float p0, float r0, float p1,
                                           float r1, float &left0, float &right0, float &left1, float &right1) {

@@ -555,7 +555,8 @@ int csa_cache_append(const csa_rope_plan *plan, const void *q, const long long *
                      const int *counts, const int *positions, const long long *pos_strides, int B,
                      int Hq, int Hkv, int T, int d, int P, int S, int M, csa_stream_t stream);
 
-/* csa_cache_append_f32 - the same on fp32 tensors and pools. */
+/* csa_cache_append_f32 - the same on fp32 tensors and pools, for a caller's own
+ * attention: csa_decode_paged reads bf16 pools only. */
 int csa_cache_append_f32(const csa_rope_plan *plan, const float *q, const long long *q_strides,
                          float *q_out, const long long *q_out_strides, const float *k,
                          const long long *k_strides, const float *v, const long long *v_strides,
