@@ -128,7 +128,8 @@ def rope(q, k, positions, plan, *, q_out=None, k_out=None, stream=None):
     with any strides whose last one is 1 (for instance slices of one fused
     projection); positions: int32 [axes, B, T] of any strides ([B, T] or [T]
     too for a plan of one axis); plan: a RopeAxes.  q_out, k_out: where the
-    results go, the input itself among them (contiguous tensors when None)."""
+    results go (contiguous tensors when None); each may be its own input, and
+    overlaps no input otherwise."""
     if stream is not None:
         return _there(rope, locals())
     _need_plan(plan)
