@@ -32,11 +32,14 @@ from ._lib import (  # noqa: F401
 )
 from ._paged import (  # noqa: F401
     RopeAxes,
+    cache_accept,
     cache_append,
     cache_compact,
     cache_copy_pages,
+    cache_copy_rows,
     cache_fork,
     cache_free,
+    cache_read,
     cache_reserve,
     decode_paged,
     decode_paged_workspace_bytes,
@@ -55,5 +58,5 @@ __all__ = [
     "status_string",
     "decode_paged", "decode_paged_workspace_bytes", "RopeAxes", "rope", "rope_backward",
     "cache_append", "cache_reserve", "cache_free", "cache_fork", "cache_compact",
-    "cache_copy_pages",
+    "cache_copy_pages", "cache_read", "cache_accept", "cache_copy_rows",
 ]

@@ -145,28 +145,56 @@ def rope_backward(dq, dk, positions, plan, *, q_out=None, k_out=None, stream=Non
     return _native.rope(dq, dk, positions, plan._at, plan.d, q_out, k_out, 1)
 
 
-def cache_append(k, v, k_pages, v_pages, block_table, seqlens, *, counts=None, rope=None,
-                 positions=None, q=None, q_out=None, stream=None):
+def cache_append(k, v, k_pages, v_pages, block_table, seqlens, *, row_scales=None, counts=None,
+                 rope=None, positions=None, q=None, q_out=None, stream=None):
     """Writes the rows of new tokens into their pages, the keys rotated if a
     plan is given, and rotates their queries beside.  Returns q' (None without q).
 
     k, v: CUDA [B, Hkv, T, d] of any strides whose last one is 1, bf16 or
     fp32; row t < counts[b] (int32 [B]; T each when None) becomes token
     seqlens[b] - counts[b] + t of sequence b: seqlens counts the new tokens
-    already, as cache_reserve leaves it.  k_pages, v_pages: [P, Hkv, S, d];
-    block_table: int32 [B, M].  rope: a RopeAxes; positions as in rope(), or
-    None for a token's place in the cache.  q: [B, Hq, T, d], with rope only.
-    decode_paged reads bf16 pools; fp32 ones are for a caller's own attention,
-    and so is attention of a prompt's rows over the pages behind a past: the
-    calls here attend from one new token per sequence."""
+    already, as cache_reserve leaves it.  k_pages, v_pages: [P, Hkv, S, d] of
+    the same type; block_table: int32 [B, M].  rope: a RopeAxes; positions as in
+    rope(), or None for a token's place in the cache.  q: [B, Hq, T, d], with
+    rope only.
+
+    Pools of 8 bits: k_pages, v_pages float8_e4m3fn or int8, row_scales: fp32
+    [P, Hkv, S, 2], the scales of each row of k_pages and v_pages, written with
+    the codes.  A row x is held as codes c with x ~ c * scale: e4m3 by the
+    smallest power of two with max|x| / scale <= 448, int8 by max|x| / 127, codes
+    to the nearest (ties to even), from the rotated key in fp32.  Rows below 2^-100
+    are zeros, a row with an infinity or NaN reads as NaN.
+
+    decode_paged and decode_tree read bf16 and 8-bit pools; fp32 ones are for a
+    caller's own attention."""
     if stream is not None:
         return _there(cache_append, locals())
     if rope is None:
         return _native.cache_append(k, v, k_pages, v_pages, block_table, seqlens, counts, None, 0, positions, q,
-                                    q_out)
+                                    q_out, row_scales)
     _need_plan(rope)
     return _native.cache_append(k, v, k_pages, v_pages, block_table, seqlens, counts, rope._at, rope.d, positions,
-                                q, q_out)
+                                q, q_out, row_scales)
+
+
+def cache_read(k_pages, v_pages, block_table, seqlens, T: int, *, starts=None, row_scales=None,
+               dtype=None, k_out=None, v_out=None, stream=None):
+    """Rows of the cache in order: token starts[b] + t of every sequence as row t
+    < T, zeros where there is none.  Returns (k, v), [B, Hkv, T, d] each, for a
+    caller's own attention or another cache.
+
+    k_pages, v_pages: [P, Hkv, S, d], bf16, fp32, or 8 bits with row_scales as in
+    cache_append; starts: int32 [B] (0 when None).  Results have the pools' type,
+    or of 8-bit pools ``dtype``: bf16 (when None) or fp32.  k_out, v_out: where
+    they go, of any strides whose last one is 1."""
+    if stream is not None:
+        return _there(cache_read, locals())
+    if dtype not in (None, torch.bfloat16, torch.float32):
+        raise ValueError(f"dtype must be bfloat16 or float32, got {dtype}")
+    if row_scales is None and dtype not in (None, k_pages.dtype):
+        raise ValueError(f"pools of {k_pages.dtype} read as {k_pages.dtype}")
+    return _native.cache_read(k_pages, v_pages, block_table, seqlens, T, starts, row_scales,
+                              row_scales is not None and dtype is torch.float32, k_out, v_out)
 
 
 # ------------------------------------------------------------------------ pages
@@ -221,3 +249,33 @@ def cache_copy_pages(k_pages, v_pages, src, dst, *, count=None, stream=None):
     if stream is not None:
         return _there(cache_copy_pages, locals())
     return _native.cache_copy_pages(k_pages, v_pages, src, dst, count)
+
+
+# --------------------------------------------------------------- drafted tokens
+def cache_accept(page_refs, block_table, seqlens, page_size: int, last, T: int, *, parents=None,
+                 counts=None, stream=None):
+    """Keeps the accepted branch of a tree of drafted tokens, the last counts[b]
+    (int32 [B]; T each when None) tokens of every sequence, and gives the others
+    up: the sequence then holds the tokens before the draft and those on the path
+    from a root to node last[b] (int32 [B]; -1: none), and pages behind them are
+    free again.  Returns (src, dst), int32 [B, T]: the rows to move with
+    cache_copy_rows in every pool (-1 where there is none), before anything reads
+    the pools or reserves pages.
+
+    parents: int32 [B, T] as in decode_tree, None for a chain; T <= 64.  A
+    sequence is not forked between its draft and this call."""
+    if stream is not None:
+        return _there(cache_accept, locals())
+    return _native.cache_accept(page_refs, block_table, seqlens, page_size, last, T, parents, counts)
+
+
+def cache_copy_rows(k_pages, v_pages, src, dst, *, row_scales=None, stream=None):
+    """Copies row src[b, i] onto row dst[b, i] (int32 [B, T], T <= 64, rows being
+    page * S + slot; a negative entry is padding) of every head of both pools, [P,
+    Hkv, S, d] or, for several layers at once, [L, P, Hkv, S, d]; any type.
+    v_pages may be None; row_scales: fp32 [..., Hkv, S, 2], moved with them.  All
+    rows of a group b are read before one is written; a row that is a dst must not
+    occur in another group."""
+    if stream is not None:
+        return _there(cache_copy_rows, locals())
+    return _native.cache_copy_rows(k_pages, v_pages, src, dst, row_scales)

@@ -282,12 +282,12 @@ int rope_any(const csa_rope_plan *plan, const void *q, const long long *q_stride
                         reinterpret_cast<cudaStream_t>(stream));
 }
 
-int append_any(const csa_rope_plan *plan, const void *q, const long long *q_strides, void *q_out,
-               const long long *q_out_strides, const void *k, const long long *k_strides,
-               const void *v, const long long *v_strides, void *k_pages, void *v_pages,
-               const int *block_table, const int *seqlens, const int *counts, const int *positions,
-               const long long *pos_strides, int B, int Hq, int Hkv, int T, int d, int P, int S,
-               int M, bool bf16, csa_stream_t stream) {
+// What every append checks; the tensors' elements have `in` bytes, the pools' `held`.
+int append_check(const csa_rope_plan *plan, const void *q, const void *q_out, const void *k, const void *v,
+                 const void *k_pages, const void *v_pages, const int *block_table, const int *seqlens,
+                 const int *counts, const int *positions, int B, int Hq, int Hkv, int T, int d, int P, int S, int M,
+                 uintptr_t in, uintptr_t held, bool *empty) {
+    *empty = false;
     if (plan && !sound_plan(plan)) return CSA_ERR_INVALID_ARG;
     if (B < 0 || Hq < 0 || Hkv < 1 || T < 0 || d < 1) return CSA_ERR_INVALID_ARG;
     if (plan ? 2 * plan->pairs > d : Hq > 0) return CSA_ERR_INVALID_ARG;
@@ -295,20 +295,36 @@ int append_any(const csa_rope_plan *plan, const void *q, const long long *q_stri
     if (rc != CSA_OK) return rc;
     if (d > 256 || (long long)B * T > kIntMax || (long long)Hq + 2LL * Hkv > 65535)
         return CSA_ERR_UNSUPPORTED;
-    if ((long long)B * T == 0) return CSA_OK;
+    *empty = (long long)B * T == 0;
+    if (*empty) return CSA_OK;
     if (!k || !v || (P > 0 && (!k_pages || !v_pages)) || !block_table || !seqlens || (Hq > 0 && (!q || !q_out)))
         return CSA_ERR_INVALID_ARG;
-    const uintptr_t al = bf16 ? 2 : 4;
-    if (!aligned(q, al) || !aligned(q_out, al) || !aligned(k, al) || !aligned(v, al) ||
-        !aligned(k_pages, al) || !aligned(v_pages, al) || !aligned(block_table, 4) ||
+    if (!aligned(q, in) || !aligned(q_out, in) || !aligned(k, in) || !aligned(v, in) ||
+        !aligned(k_pages, held) || !aligned(v_pages, held) || !aligned(block_table, 4) ||
         !aligned(seqlens, 4) || !aligned(counts, 4) || !aligned(positions, 4))
         return CSA_ERR_ALIGNMENT;
+    return CSA_OK;
+}
+
+int append_any(const csa_rope_plan *plan, const void *q, const long long *q_strides, void *q_out,
+               const long long *q_out_strides, const void *k, const long long *k_strides,
+               const void *v, const long long *v_strides, void *k_pages, void *v_pages,
+               const int *block_table, const int *seqlens, const int *counts, const int *positions,
+               const long long *pos_strides, int B, int Hq, int Hkv, int T, int d, int P, int S,
+               int M, bool bf16, csa_stream_t stream) {
+    const uintptr_t al = bf16 ? 2 : 4;
+    bool empty;
+    int rc = append_check(plan, q, q_out, k, v, k_pages, v_pages, block_table, seqlens, counts, positions, B, Hq, Hkv, T,
+                          d, P, S, M, al, al, &empty);
+    if (rc != CSA_OK || empty) return rc;
     if ((rc = device_ok()) != CSA_OK) return rc;
     return csa_cache_append_run(plan, q, q_strides, q_out, q_out_strides, k, k_strides, v, v_strides,
                                 k_pages, v_pages, block_table, seqlens, counts, positions,
                                 pos_strides, B, Hq, Hkv, T, d, P, S, M, bf16,
                                 reinterpret_cast<cudaStream_t>(stream));
 }
+
+bool eight_bits(int kind) { return kind == CSA_E4M3 || kind == CSA_INT8; }
 
 }  // namespace
 
@@ -395,6 +411,81 @@ int csa_cache_append_f32(const csa_rope_plan *plan, const float *q, const long l
     return append_any(plan, q, q_strides, q_out, q_out_strides, k, k_strides, v, v_strides, k_pages,
                       v_pages, block_table, seqlens, counts, positions, pos_strides, B, Hq, Hkv, T,
                       d, P, S, M, false, stream);
+}
+
+int csa_cache_append_q8(const csa_rope_plan *plan, const void *q, const long long *q_strides,
+                        void *q_out, const long long *q_out_strides, const void *k,
+                        const long long *k_strides, const void *v, const long long *v_strides,
+                        void *k_pages, void *v_pages, float *row_scales, const int *block_table,
+                        const int *seqlens, const int *counts, const int *positions,
+                        const long long *pos_strides, int B, int Hq, int Hkv, int T, int d, int P,
+                        int S, int M, int in_type, int kind, csa_stream_t stream) {
+    if ((in_type != CSA_BF16 && in_type != CSA_F32) || !eight_bits(kind)) return CSA_ERR_INVALID_ARG;
+    bool empty;
+    int rc = append_check(plan, q, q_out, k, v, k_pages, v_pages, block_table, seqlens, counts, positions, B, Hq, Hkv, T,
+                          d, P, S, M, in_type == CSA_BF16 ? 2 : 4, 1, &empty);
+    if (rc != CSA_OK || empty) return rc;
+    if (P > 0 && !row_scales) return CSA_ERR_INVALID_ARG;
+    if (!aligned(row_scales, 8)) return CSA_ERR_ALIGNMENT;
+    if ((rc = device_ok()) != CSA_OK) return rc;
+    return csa_cache_append_q8_run(plan, q, q_strides, q_out, q_out_strides, k, k_strides, v, v_strides,
+                                   k_pages, v_pages, row_scales, block_table, seqlens, counts, positions,
+                                   pos_strides, B, Hq, Hkv, T, d, P, S, M, in_type == CSA_BF16,
+                                   kind == CSA_E4M3, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int csa_cache_read(const void *k_pages, const void *v_pages, const float *row_scales,
+                   const int *block_table, const int *seqlens, const int *starts, void *k,
+                   const long long *k_strides, void *v, const long long *v_strides, int B, int Hkv,
+                   int T, int d, int P, int S, int M, int kind, int out_type, csa_stream_t stream) {
+    if (kind < CSA_BF16 || kind > CSA_INT8 || (out_type != CSA_BF16 && out_type != CSA_F32)) return CSA_ERR_INVALID_ARG;
+    if (!eight_bits(kind) && out_type != kind) return CSA_ERR_INVALID_ARG;
+    if (B < 0 || Hkv < 1 || T < 0 || d < 1) return CSA_ERR_INVALID_ARG;
+    int rc = check_tables(B, P, S, M);
+    if (rc != CSA_OK) return rc;
+    if (d > 256 || (long double)B * Hkv * T > kIntMax) return CSA_ERR_UNSUPPORTED;
+    if ((long long)B * T == 0) return CSA_OK;
+    if (!k || !v || (P > 0 && (!k_pages || !v_pages)) || !block_table || !seqlens) return CSA_ERR_INVALID_ARG;
+    if (eight_bits(kind) ? P > 0 && !row_scales : row_scales != nullptr) return CSA_ERR_INVALID_ARG;
+    const uintptr_t in = kind == CSA_BF16 ? 2 : kind == CSA_F32 ? 4 : 1, out = out_type == CSA_BF16 ? 2 : 4;
+    if (!aligned(k_pages, in) || !aligned(v_pages, in) || !aligned(k, out) || !aligned(v, out) || !aligned(row_scales, 8) ||
+        !aligned(block_table, 4) || !aligned(seqlens, 4) || !aligned(starts, 4))
+        return CSA_ERR_ALIGNMENT;
+    if ((rc = device_ok()) != CSA_OK) return rc;
+    return csa_cache_read_run(k_pages, v_pages, row_scales, block_table, seqlens, starts, k, k_strides, v, v_strides, B,
+                              Hkv, T, d, P, S, M, kind, out_type, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int csa_cache_accept(int *page_refs, int *block_table, int *seqlens, const int *parents,
+                     const int *counts, const int *last, int *src, int *dst, int T, int B, int P,
+                     int S, int M, csa_stream_t stream) {
+    int rc = check_books(page_refs, block_table, seqlens, B, P, S, M);
+    if (rc != CSA_OK) return rc;
+    if (T < 0) return CSA_ERR_INVALID_ARG;
+    if (T > CSA_TREE_MAX || (long long)P * S > kIntMax) return CSA_ERR_UNSUPPORTED;
+    if (B == 0 || T == 0) return CSA_OK;
+    if (!last || !src || !dst) return CSA_ERR_INVALID_ARG;
+    if (!aligned(parents, 4) || !aligned(counts, 4) || !aligned(last, 4) || !aligned(src, 4) || !aligned(dst, 4))
+        return CSA_ERR_ALIGNMENT;
+    if ((rc = device_ok()) != CSA_OK) return rc;
+    return csa_cache_accept_run(page_refs, block_table, seqlens, parents, counts, last, src, dst, T, B, P, S, M,
+                                reinterpret_cast<cudaStream_t>(stream));
+}
+
+int csa_cache_copy_rows(void *k_pages, void *v_pages, long long row_bytes, void *row_scales,
+                        long long scale_bytes, int layers, int P, int H, int S, const int *src,
+                        const int *dst, int groups, int T, csa_stream_t stream) {
+    if (row_bytes < 0 || scale_bytes < 0 || layers < 0 || P < 0 || H < 0 || S < 1 || groups < 0 || T < 0)
+        return CSA_ERR_INVALID_ARG;
+    if (row_bytes > 1 << 20 || scale_bytes > 1 << 20) return CSA_ERR_UNSUPPORTED;
+    if (T > CSA_TREE_MAX || layers > 65535 || 3LL * H > 65535 || (long long)P * S > kIntMax) return CSA_ERR_UNSUPPORTED;
+    if (layers == 0 || P == 0 || H == 0 || groups == 0 || T == 0) return CSA_OK;
+    if ((!k_pages && !v_pages && !row_scales) || !src || !dst) return CSA_ERR_INVALID_ARG;
+    if (!aligned(src, 4) || !aligned(dst, 4)) return CSA_ERR_ALIGNMENT;
+    int rc = device_ok();
+    if (rc != CSA_OK) return rc;
+    return csa_cache_copy_rows_run(k_pages, v_pages, row_bytes, row_scales, scale_bytes, layers, P, H, S, src, dst,
+                                   groups, T, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int csa_cache_reserve(int *page_refs, int *block_table, int *seqlens, const int *counts,
@@ -647,7 +738,8 @@ int csa_device_status(void) {
     const int f = csa_paged_take_status();
     const int g = csa_rope_take_status();
     const int h = csa_cache_take_status();
-    for (const int word : {a, b, c, e, f, g, h})
+    const int i = csa_quant_take_status();
+    for (const int word : {a, b, c, e, f, g, h, i})
         if (word != CSA_OK) return word;
     return CSA_OK;
 }

@@ -436,6 +436,143 @@ copy_pages_kernel(C *k_pages, C *v_pages, long long page, int layers, int P, con
     }
 }
 
+// ------------------------------------------------------------------- accept
+// A warp per sequence.  The path from the last accepted node up to its root is a
+// mask of 64 nodes, walked by shuffles (lane i has the parents of nodes i and i + 32);
+// a node's place on it is the number of nodes below it in the mask.
+constexpr int kAcceptWarps = 4;
+
+__global__ void __launch_bounds__(32 * kAcceptWarps)
+accept_kernel(int *refs, int *table, int *seqlens, const int *parents, const int *counts, const int *last, int *src,
+              int *dst, int T, int B, int P, int S, int M) {
+    after_previous();
+    const int b = blockIdx.x * kAcceptWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (b >= B) return;
+    const int len = seqlens[b], count = counts ? counts[b] : T, leaf = last[b];
+    int up[2], from[2] = {-1, -1}, to[2] = {-1, -1};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int t = lane + 32 * i;
+        up[i] = t >= T ? -1 : parents ? parents[(long long)b * T + t] : t - 1;
+    }
+    bool sound = count >= 0 && count <= T && len >= count && len <= (long long)M * S && leaf >= -1 && leaf < count;
+    unsigned long long path = 0;
+    for (int node = leaf; sound && node >= 0;) {  // the same on every lane
+        path |= 1ull << node;
+        const int a = __shfl_sync(0xffffffffu, up[0], node & 31), c = __shfl_sync(0xffffffffu, up[1], node & 31);
+        const int next = node < 32 ? a : c;
+        sound = next >= -1 && next < node;
+        node = next;
+    }
+    const int n = len - count, kept = __popcll(path);
+    int *row = table + (long long)b * M;
+    auto place = [&](int at) {  // the pool's row of token `at`
+        const int page = row[at / S];
+        if (page < 0 || page >= P) sound = false;
+        return page * S + at % S;
+    };
+    if (sound)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int node = lane + 32 * i;
+            if (path >> node & 1) {
+                const int at = __popcll(path & ((1ull << node) - 1));
+                if (at != node) {
+                    from[i] = place(n + node);
+                    to[i] = place(n + at);
+                }
+            }
+        }
+    sound = __all_sync(0xffffffffu, sound);
+    if (!sound && lane == 0) complain();
+    int *s = src + (long long)b * T, *d = dst + (long long)b * T;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int at = lane + 32 * i, below = __popcll(path & ((1ull << at) - 1));
+        if (at >= T) continue;
+        // a place behind the kept ones, or whose node is there already; the others get theirs below
+        if (!sound || at >= kept || (below == at && (path >> at & 1))) s[at] = d[at] = -1;
+        if (sound && to[i] >= 0) {
+            s[below] = from[i];
+            d[below] = to[i];
+        }
+    }
+    if (!sound) return;
+    for (int j = pages_of(n + kept, S) + lane; j < pages_of(len, S); j += 32) {
+        const int page = row[j];
+        if (page < 0 || page >= P) {
+            complain();
+        } else if (atomicSub(&refs[page], 1) <= 0) {  // nobody held it
+            atomicAdd(&refs[page], 1);
+            complain();
+        }
+        row[j] = -1;
+    }
+    if (lane == 0) seqlens[b] = n + kept;
+}
+
+// --------------------------------------------------------------- copied rows
+// Row r of a pool of P pages is slot r mod S of page r / S.  A block has one group of
+// pairs in one head of one tensor; it reads a range of columns of all of the group's
+// rows before it writes the first of them, so rows of a group may change places.
+struct RowTensor {
+    uint8_t *at;
+    long long bytes;  // of a row
+    int unit;         // the widest type that all rows allow: 16, 4 or 1 bytes
+};
+struct CopyRowsParams {
+    RowTensor x[3];
+    int layers, P, H, S, T;
+    const int *src, *dst;
+};
+constexpr int kRowThreads = 256, kRowDeep = 4, kRowMost = 64;
+
+template <typename C>
+__device__ __forceinline__ void copy_group(uint8_t *base, long long bytes, const long long (*pair)[2], int T) {
+    const int units = (int)(bytes / (long long)sizeof(C)), per = kRowThreads * kRowDeep / T;  // columns at a time
+    for (int c0 = 0; c0 < units; c0 += per) {
+        const int width = min(per, units - c0);
+        C val[kRowDeep];
+#pragma unroll
+        for (int j = 0; j < kRowDeep; ++j) {
+            const int i = threadIdx.x + j * kRowThreads, r = i / width, c = c0 + i - r * width;
+            if (r < T && pair[r][0] >= 0) val[j] = reinterpret_cast<const C *>(base + pair[r][0] * bytes)[c];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kRowDeep; ++j) {
+            const int i = threadIdx.x + j * kRowThreads, r = i / width, c = c0 + i - r * width;
+            if (r < T && pair[r][0] >= 0) reinterpret_cast<C *>(base + pair[r][1] * bytes)[c] = val[j];
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kRowThreads) copy_rows_kernel(const __grid_constant__ CopyRowsParams p) {
+    __shared__ long long pair[kRowMost][2];  // rows of the tensor, or -1
+    after_previous();
+    const int which = blockIdx.y / p.H, h = blockIdx.y - which * p.H, T = p.T;
+    bool some = false;
+    if (threadIdx.x < T) {
+        const int s = p.src[(long long)blockIdx.x * T + threadIdx.x], d = p.dst[(long long)blockIdx.x * T + threadIdx.x];
+        const long long rows = (long long)p.P * p.S;
+        some = s >= 0 && d >= 0 && s < rows && d < rows;
+        if (s >= 0 && d >= 0 && !some) complain();
+        auto row = [&](int r) {
+            return (((long long)blockIdx.z * p.P + r / p.S) * p.H + h) * p.S + r % p.S;
+        };
+        pair[threadIdx.x][0] = some ? row(s) : -1;
+        pair[threadIdx.x][1] = some ? row(d) : -1;
+    }
+    if (!__syncthreads_or(some)) return;
+    const RowTensor &x = p.x[which];
+    if (x.unit == 16)
+        copy_group<uint4>(x.at, x.bytes, pair, T);
+    else if (x.unit == 4)
+        copy_group<uint32_t>(x.at, x.bytes, pair, T);
+    else
+        copy_group<uint8_t>(x.at, x.bytes, pair, T);
+}
+
 int from(cudaError_t e) { return e == cudaSuccess ? CSA_OK : CSA_ERR_CUDA; }
 
 template <typename C>
@@ -496,6 +633,35 @@ int csa_cache_copy_pages_run(void *k_pages, void *v_pages, long long page_bytes,
     if (at % 4 == 0)
         return copy_as<uint32_t>(k_pages, v_pages, page_bytes, layers, P, src, dst, n, count, stream);
     return copy_as<uint8_t>(k_pages, v_pages, page_bytes, layers, P, src, dst, n, count, stream);
+}
+
+int csa_cache_accept_run(int *refs, int *table, int *seqlens, const int *parents, const int *counts, const int *last,
+                         int *src, int *dst, int T, int B, int P, int S, int M, cudaStream_t stream) {
+    return from(launch_after_previous(accept_kernel, (B + kAcceptWarps - 1) / kAcceptWarps, 32 * kAcceptWarps, 0, stream,
+                                      refs, table, seqlens, parents, counts, last, src, dst, T, B, P, S, M));
+}
+
+int csa_cache_copy_rows_run(void *k_pages, void *v_pages, long long row_bytes, void *row_scales, long long scale_bytes,
+                            int layers, int P, int H, int S, const int *src, const int *dst, int B, int T,
+                            cudaStream_t stream) {
+    CopyRowsParams p = {};
+    int tensors = 0;
+    void *at[3] = {k_pages, v_pages, row_scales};
+    for (int i = 0; i < 3; ++i) {
+        if (!at[i]) continue;
+        const long long bytes = i < 2 ? row_bytes : scale_bytes;
+        const uintptr_t bits = reinterpret_cast<uintptr_t>(at[i]) | (uintptr_t)bytes;
+        p.x[tensors++] = {static_cast<uint8_t *>(at[i]), bytes, bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 1};
+    }
+    p.layers = layers;
+    p.P = P;
+    p.H = H;
+    p.S = S;
+    p.T = T;
+    p.src = src;
+    p.dst = dst;
+    return from(launch_after_previous(copy_rows_kernel, dim3((unsigned)B, (unsigned)(tensors * H), (unsigned)layers),
+                                      kRowThreads, 0, stream, p));
 }
 
 int csa_cache_take_status(void) {

@@ -139,4 +139,24 @@ int csa_cache_compact_run(int *refs, int *table, const int *seqlens, int *src, i
 int csa_cache_copy_pages_run(void *k_pages, void *v_pages, long long page_bytes, int layers, int P,
                              const int *src, const int *dst, int n, const int *count,
                              cudaStream_t stream);
+// The accepted branch of a tree of drafted tokens: pages behind it given back, the rows to move.
+int csa_cache_accept_run(int *refs, int *table, int *seqlens, const int *parents, const int *counts, const int *last,
+                         int *src, int *dst, int T, int B, int P, int S, int M, cudaStream_t stream);
+// Any of the three tensors may be NULL; groups of T <= 64 pairs.
+int csa_cache_copy_rows_run(void *k_pages, void *v_pages, long long row_bytes, void *row_scales, long long scale_bytes,
+                            int layers, int P, int H, int S, const int *src, const int *dst, int B, int T,
+                            cudaStream_t stream);
 int csa_cache_take_status(void);
+
+// Rows in 8 bits: written into pages, and read back (csa_quant.cu).
+int csa_cache_append_q8_run(const csa_rope_plan *plan, const void *q, const long long *q_strides, void *q_out,
+                            const long long *q_out_strides, const void *k, const long long *k_strides, const void *v,
+                            const long long *v_strides, void *k_pages, void *v_pages, float *row_scales,
+                            const int *block_table, const int *seqlens, const int *counts, const int *positions,
+                            const long long *pos_strides, int B, int Hq, int Hkv, int T, int d, int P, int S, int M,
+                            bool bf16, bool e4m3, cudaStream_t stream);
+int csa_cache_read_run(const void *k_pages, const void *v_pages, const float *row_scales, const int *block_table,
+                       const int *seqlens, const int *starts, void *k, const long long *k_strides, void *v,
+                       const long long *v_strides, int B, int Hkv, int T, int d, int P, int S, int M, int kind,
+                       int out_type, cudaStream_t stream);
+int csa_quant_take_status(void);

@@ -20,6 +20,7 @@
 #include <climits>
 #include <cmath>
 #include <initializer_list>
+#include <vector>
 
 #include "csa.h"
 
@@ -287,7 +288,18 @@ PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t) {
     END_HANDLE_TH_ERRORS
 }
 
-// k, v, k_pages, v_pages, block_table, seqlens, counts, plan address or None, plan d, positions, q, q_out
+// What a pool's elements are: with row_scales 8 bits, and the scales go with them.
+int kind_of(const Tensor &pool, const Tensor *row_scales, IntArrayRef shape, const at::Device &dev) {
+    const auto t = pool.scalar_type();
+    const bool eight = t == at::kFloat8_e4m3fn || t == at::kChar;
+    TORCH_CHECK_VALUE(eight || t == at::kBFloat16 || t == at::kFloat, "pools of ", t, " are not supported");
+    TORCH_CHECK_VALUE(eight == (row_scales != nullptr), "row_scales go with pools of 8 bits, got ", t,
+                      row_scales ? " with" : " without", " them");
+    if (eight) need(*row_scales, "row_scales", at::kFloat, {shape[0], shape[1], shape[2], 2}, dev);
+    return t == at::kFloat8_e4m3fn ? CSA_E4M3 : t == at::kChar ? CSA_INT8 : t == at::kBFloat16 ? CSA_BF16 : CSA_F32;
+}
+
+// k, v, k_pages, v_pages, block_table, seqlens, counts, plan address or None, plan d, positions, q, q_out, row_scales
 PyObject *cache_append(PyObject *, PyObject *const *a, Py_ssize_t) {
     HANDLE_TH_ERRORS
     const Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v"), &kp = tensor(a[2], "k_pages"),
@@ -300,8 +312,11 @@ PyObject *cache_append(PyObject *, PyObject *const *a, Py_ssize_t) {
     const auto dtype = k.scalar_type();
     const bool bf = is_bf16(dtype);
     const Rows ks(k, "k", dtype, {B, Hkv, T, d}, here.dev, false), vs(v, "v", dtype, {B, Hkv, T, d}, here.dev, false);
-    need(kp, "k_pages", dtype, {P, Hkv, S, d}, here.dev);
-    need(vp, "v_pages", dtype, {P, Hkv, S, d}, here.dev);
+    const Tensor *scales = optional(a[12], "row_scales");
+    const int kind = kind_of(kp, scales, {P, Hkv, S, d}, here.dev);
+    const auto held = scales ? kp.scalar_type() : dtype;
+    need(kp, "k_pages", held, {P, Hkv, S, d}, here.dev);
+    need(vp, "v_pages", held, {P, Hkv, S, d}, here.dev);
     need(table, "block_table", at::kInt, {B, M}, here.dev);
     need(lens, "seqlens", at::kInt, {B}, here.dev);
     const Tensor *counts = optional(a[6], "counts"), *positions = optional(a[9], "positions"), *q = optional(a[10], "q");
@@ -330,7 +345,13 @@ PyObject *cache_append(PyObject *, PyObject *const *a, Py_ssize_t) {
     const int b = size(B, "B"), hq = size(Hq, "Hq"), hkv = size(Hkv, "Hkv"), t = size(T, "T"), dd = size(d, "d"),
               pp = size(P, "P"), ss = size(S, "S"), m = size(M, "M");
     void *qp = at_(q), *qop = qo.defined() ? at_(qo) : nullptr;
-    if (bf)
+    if (scales)
+        check(csa_cache_append_q8(plan, qp, qs.strides, qop, qos.strides, at_(k), ks.strides, at_(v), vs.strides, at_(kp),
+                                  at_(vp), at_<float>(*scales), at_<int>(table), at_<int>(lens), at_<int>(counts),
+                                  at_<int>(positions), ps, b, hq, hkv, t, dd, pp, ss, m, bf ? CSA_BF16 : CSA_F32, kind,
+                                  here.stream),
+              "csa_cache_append_q8");
+    else if (bf)
         check(csa_cache_append(plan, qp, qs.strides, qop, qos.strides, at_(k), ks.strides, at_(v), vs.strides, at_(kp),
                                at_(vp), at_<int>(table), at_<int>(lens), at_<int>(counts), at_<int>(positions), ps, b,
                                hq, hkv, t, dd, pp, ss, m, here.stream),
@@ -341,9 +362,48 @@ PyObject *cache_append(PyObject *, PyObject *const *a, Py_ssize_t) {
                                    at_<float>(vp), at_<int>(table), at_<int>(lens), at_<int>(counts),
                                    at_<int>(positions), ps, b, hq, hkv, t, dd, pp, ss, m, here.stream),
               "csa_cache_append_f32");
-    wrote({&kp, &vp, &qo});
+    wrote({&kp, &vp, scales, &qo});
     if (!qo.defined()) Py_RETURN_NONE;
     return wrap(qo);
+    END_HANDLE_TH_ERRORS
+}
+
+// k_pages, v_pages, block_table, seqlens, T, starts, row_scales, float32 results, k_out, v_out
+PyObject *cache_read(PyObject *, PyObject *const *a, Py_ssize_t) {
+    HANDLE_TH_ERRORS
+    const Tensor &kp = tensor(a[0], "k_pages"), &vp = tensor(a[1], "v_pages"), &table = tensor(a[2], "block_table"),
+                 &lens = tensor(a[3], "seqlens");
+    Here here(kp, "cache_read");
+    TORCH_CHECK_VALUE(kp.dim() == 4 && table.dim() == 2, "the pools are [P, Hkv, S, d], block_table [B, M]");
+    const int64_t P = kp.size(0), Hkv = kp.size(1), S = kp.size(2), d = kp.size(3), B = table.size(0), M = table.size(1);
+    const Tensor *starts = optional(a[5], "starts"), *scales = optional(a[6], "row_scales");
+    const int kind = kind_of(kp, scales, {P, Hkv, S, d}, here.dev);
+    need(kp, "k_pages", kp.scalar_type(), {P, Hkv, S, d}, here.dev);
+    need(vp, "v_pages", kp.scalar_type(), {P, Hkv, S, d}, here.dev);
+    need(table, "block_table", at::kInt, {B, M}, here.dev);
+    need(lens, "seqlens", at::kInt, {B}, here.dev);
+    if (starts) need(*starts, "starts", at::kInt, {B}, here.dev);
+    const int T = integer(a[4], "T");
+    TORCH_CHECK_VALUE(T >= 0, "T must not be negative, got ", T);
+    const int wide = PyObject_IsTrue(a[7]);
+    if (wide < 0) throw python_error();
+    const auto dtype = scales ? (wide ? at::kFloat : at::kBFloat16) : kp.scalar_type();
+    TORCH_CHECK_VALUE(!wide || dtype == at::kFloat, "pools of ", dtype, " read as ", dtype);
+    Tensor out[2];
+    Rows rows[2];
+    for (int i = 0; i < 2; ++i) {
+        const char *name = i ? "v_out" : "k_out";
+        const Tensor *given = optional(a[8 + i], name);
+        out[i] = given ? *given : made({B, Hkv, (int64_t)T, d}, dtype, here.dev);
+        rows[i] = Rows(out[i], name, dtype, {B, Hkv, (int64_t)T, d}, here.dev, true);
+    }
+    check(csa_cache_read(at_(kp), at_(vp), at_<float>(scales), at_<int>(table), at_<int>(lens), at_<int>(starts),
+                         at_(out[0]), rows[0].strides, at_(out[1]), rows[1].strides, size(B, "B"), size(Hkv, "Hkv"), T,
+                         size(d, "d"), size(P, "P"), size(S, "S"), size(M, "M"), kind,
+                         dtype == at::kFloat ? CSA_F32 : CSA_BF16, here.stream),
+          "csa_cache_read");
+    wrote({&out[0], &out[1]});
+    return tuple({out[0], out[1]});
     END_HANDLE_TH_ERRORS
 }
 
@@ -454,6 +514,53 @@ PyObject *cache_copy_pages(PyObject *, PyObject *const *a, Py_ssize_t) {
     END_HANDLE_TH_ERRORS
 }
 
+// ..., last, T, parents, counts
+PyObject *cache_accept(PyObject *, PyObject *const *a, Py_ssize_t) {
+    HANDLE_TH_ERRORS
+    const Books b(a, "cache_accept");
+    const Tensor &last = tensor(a[4], "last");
+    const int T = integer(a[5], "T");
+    TORCH_CHECK_VALUE(T >= 0, "T must not be negative, got ", T);
+    const Tensor *parents = optional(a[6], "parents"), *counts = optional(a[7], "counts");
+    need(last, "last", at::kInt, {b.B}, b.here.dev);
+    if (parents) need(*parents, "parents", at::kInt, {b.B, T}, b.here.dev);
+    if (counts) need(*counts, "counts", at::kInt, {b.B}, b.here.dev);
+    Tensor src = made({b.B, T}, at::kInt, b.here.dev), dst = made({b.B, T}, at::kInt, b.here.dev);
+    check(csa_cache_accept(b.refs, b.table, b.lens, at_<int>(parents), at_<int>(counts), at_<int>(last), at_<int>(src),
+                           at_<int>(dst), T, b.B, b.P, b.S, b.M, b.here.stream),
+          "csa_cache_accept");
+    wrote({&b.t_refs, &b.t_table, &b.t_lens});
+    return tuple({src, dst});
+    END_HANDLE_TH_ERRORS
+}
+
+// k_pages, v_pages, src, dst, row_scales
+PyObject *cache_copy_rows(PyObject *, PyObject *const *a, Py_ssize_t) {
+    HANDLE_TH_ERRORS
+    const Tensor &k = tensor(a[0], "k_pages"), &src = tensor(a[2], "src"), &dst = tensor(a[3], "dst");
+    const Tensor *v = optional(a[1], "v_pages"), *scales = optional(a[4], "row_scales");
+    Here here(k, "cache_copy_rows");
+    TORCH_CHECK_VALUE(k.dim() == 4 || k.dim() == 5, "the pools are [P, Hkv, S, d] or [L, P, Hkv, S, d]");
+    TORCH_CHECK_VALUE(src.dim() == 2, "src and dst are [B, T]");
+    need(k, "k_pages", k.scalar_type(), k.sizes(), here.dev);
+    if (v) need(*v, "v_pages", k.scalar_type(), k.sizes(), here.dev);
+    if (scales) {
+        std::vector<int64_t> shape = k.sizes().vec();
+        shape.back() = 2;
+        need(*scales, "row_scales", at::kFloat, shape, here.dev);
+    }
+    const int64_t B = src.size(0), T = src.size(1);
+    need(src, "src", at::kInt, {B, T}, here.dev);
+    need(dst, "dst", at::kInt, {B, T}, here.dev);
+    check(csa_cache_copy_rows(at_(k), at_(v), (long long)k.size(-1) * (long long)k.element_size(), at_(scales), 8,
+                              k.dim() == 5 ? size(k.size(0), "L") : 1, size(k.size(-4), "P"), size(k.size(-3), "Hkv"),
+                              size(k.size(-2), "S"), at_<int>(src), at_<int>(dst), size(B, "B"), size(T, "T"), here.stream),
+          "csa_cache_copy_rows");
+    wrote({&k, v, scales});
+    Py_RETURN_NONE;
+    END_HANDLE_TH_ERRORS
+}
+
 PyObject *set_error(PyObject *, PyObject *type) {
     Py_INCREF(type);
     Py_XDECREF(g_error);
@@ -474,12 +581,15 @@ PyObject *counted(PyObject *self, PyObject *const *a, Py_ssize_t n) {
 
 PyMethodDef g_methods[] = {CALL(decode_paged, 13),
                            CALL(rope, 8),
-                           CALL(cache_append, 12),
+                           CALL(cache_append, 13),
+                           CALL(cache_read, 10),
                            CALL(cache_reserve, 6),
                            CALL(cache_free, 5),
                            CALL(cache_fork, 6),
                            CALL(cache_compact, 4),
                            CALL(cache_copy_pages, 5),
+                           CALL(cache_accept, 8),
+                           CALL(cache_copy_rows, 5),
                            {"set_error", set_error, METH_O, nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_csa_torch", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

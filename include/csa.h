@@ -440,6 +440,18 @@ int csa_decode_merge_ranges(const float *o_parts, const float *lse_parts, int R,
  */
 
 /*
+ * Elements of a pool.  Pools of 8 bits have row_scales: contiguous float
+ *  [P, Hkv, S, 2], the scale of each row of k_pages and of v_pages; a row stands
+ *  for code * scale.  row_scales is NULL for the other pools.
+ */
+enum {
+    CSA_BF16 = 0,
+    CSA_F32 = 1,
+    CSA_E4M3 = 2, /* 8-bit floats of 3 fraction bits, largest 448             */
+    CSA_INT8 = 3
+};
+
+/*
  * csa_decode_paged - csa_decode over a paged cache, with grouped heads: query
  *   head h reads cached head h / (Hq / Hkv).
  *   Defines: eq. (10)/(11) of "Continuous Softmax Attention" ("Assembly and
@@ -566,6 +578,46 @@ int csa_cache_append_f32(const csa_rope_plan *plan, const float *q, const long l
                          int S, int M, csa_stream_t stream);
 
 /*
+ * csa_cache_append_q8 - csa_cache_append into pools of 8 bits: the rows of the
+ *   new tokens are quantised as they are written, after the keys have turned and
+ *   without a rounding between.  For a row x, max the largest |x_c| (fp32):
+ *     CSA_E4M3  scale = the smallest power of two with max / scale <= 448, codes
+ *               the nearest e4m3 numbers to x / scale, ties to even;
+ *     CSA_INT8  scale = max / 127 and codes the integers nearest to
+ *               x * (127 / max), ties to even, both quotients rounded to fp32.
+ *   max < 2^-100: scale 0 and codes 0.  A row with an infinity or NaN: scale NaN
+ *   and codes 0, so that it reads as NaN.
+ *   in_type: CSA_BF16 or CSA_F32, of q, k, v and q_out; kind: CSA_E4M3 or CSA_INT8.
+ *   k_pages, v_pages: 1 byte per element; row_scales as above, 8-byte aligned.
+ *   Everything else as csa_cache_append.
+ */
+int csa_cache_append_q8(const csa_rope_plan *plan, const void *q, const long long *q_strides,
+                        void *q_out, const long long *q_out_strides, const void *k,
+                        const long long *k_strides, const void *v, const long long *v_strides,
+                        void *k_pages, void *v_pages, float *row_scales, const int *block_table,
+                        const int *seqlens, const int *counts, const int *positions,
+                        const long long *pos_strides, int B, int Hq, int Hkv, int T, int d, int P,
+                        int S, int M, int in_type, int kind, csa_stream_t stream);
+
+/*
+ * csa_cache_read - rows of the cache in order: row t < T of k and v gets token
+ *   starts[b] + t of sequence b, as a value of out_type (code * scale, rounded
+ *   once), or 0 where the sequence has no such token.
+ *   k_pages, v_pages: pools of `kind`; row_scales NULL unless kind is CSA_E4M3 or
+ *   CSA_INT8; out_type: CSA_BF16 or CSA_F32 for those, else equal to kind.
+ *   starts: int32 [B], or NULL for 0.  k, v: [B, Hkv, T, d], strides as csa_rope;
+ *   outputs overlap neither inputs nor themselves.  Pages may have any S >= 1.
+ *   1 <= d <= 256; B * Hkv * T at most 2^31 - 1.
+ *   A sequence with a length outside [0, M * S] or a start outside [0, length],
+ *   and a row whose page number is outside [0, P), reads as NaN and sets the
+ *   status word.
+ */
+int csa_cache_read(const void *k_pages, const void *v_pages, const float *row_scales,
+                   const int *block_table, const int *seqlens, const int *starts, void *k,
+                   const long long *k_strides, void *v, const long long *v_strides, int B, int Hkv,
+                   int T, int d, int P, int S, int M, int kind, int out_type, csa_stream_t stream);
+
+/*
  * csa_cache_reserve - room for counts[b] >= 0 more tokens of every sequence:
  *   the pages that are missing are the lowest-numbered free ones, given out in
  *   the order of the sequences; their refs become 1, the table gets them, and
@@ -631,6 +683,45 @@ int csa_cache_compact(int *page_refs, int *block_table, const int *seqlens, int 
 int csa_cache_copy_pages(void *k_pages, void *v_pages, long long page_bytes, int layers, int P,
                          const int *src, const int *dst, int n, const int *count,
                          csa_stream_t stream);
+
+/*
+ * csa_cache_accept - keeps the accepted branch of a tree of drafted tokens (the
+ *   last counts[b] tokens of sequence b, csa_decode_tree) and gives the others up:
+ *   with n tokens before the draft and m nodes on the path from a root to node
+ *   last[b], the sequence holds n + m tokens afterwards, the path's in order; pages
+ *   behind them are given back (refs fall by one, entries become -1).
+ *   parents: int32 [B, T] as csa_decode_tree, or NULL for a chain; counts: int32 [B],
+ *   or NULL for T each; last: int32 [B], the last accepted node, -1 for none.
+ *   src, dst: int32 [B, T], the rows to move: entry i < m has the pool's rows
+ *   (page * S + slot) where the path's i-th token is and where it goes, or -1, -1
+ *   where it is there already; -1 behind.  The caller moves the data
+ *   (csa_cache_copy_rows, once per pool) before anything reads the pools or takes
+ *   pages.  A sequence must not be forked between its draft and this call.
+ *   A count outside [0, T], a length outside [count, M * S], a last node outside
+ *   [-1, count), a parent on the path outside [-1, node) or a page number outside
+ *   [0, P) of a row to move leaves that sequence as it is (src, dst -1) and sets the
+ *   status word; a page to give back that is outside [0, P) or held by nobody is
+ *   passed over and sets it.
+ *   T at most CSA_TREE_MAX and P * S at most 2^31 - 1 (CSA_ERR_UNSUPPORTED).
+ */
+#define CSA_TREE_MAX 64
+int csa_cache_accept(int *page_refs, int *block_table, int *seqlens, const int *parents,
+                     const int *counts, const int *last, int *src, int *dst, int T, int B, int P,
+                     int S, int M, csa_stream_t stream);
+
+/*
+ * csa_cache_copy_rows - copies row src[g][i] of every head onto row dst[g][i] in
+ *   k_pages and, unless they are NULL, v_pages and row_scales (any of the three may
+ *   be NULL): pools of `layers` times [P, H, S] rows of row_bytes bytes
+ *   (scale_bytes for row_scales).  src, dst: int32 [groups, T], rows page * S +
+ *   slot; a pair with a negative entry is padding, one with a row >= P * S is
+ *   passed over and sets the status word.  All rows of a group are read before any
+ *   is written; a row that is a dst must not be in another group, nor a dst twice.
+ *   T at most CSA_TREE_MAX; layers and 3 * H at most 65535 (CSA_ERR_UNSUPPORTED).
+ */
+int csa_cache_copy_rows(void *k_pages, void *v_pages, long long row_bytes, void *row_scales,
+                        long long scale_bytes, int layers, int P, int H, int S, const int *src,
+                        const int *dst, int groups, int T, csa_stream_t stream);
 
 /*
  * csa_logphi2_eval - y[i] = log phi2(x[i]) with the library's fp32 device
