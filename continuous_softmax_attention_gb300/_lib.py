@@ -83,6 +83,7 @@ def load():
                        ("csa_cache_fork", [p] * 5 + [i] + [p] * 3 + [i] * 4 + [p]),
                        ("csa_cache_compact", [p] * 6 + [i] * 4 + [p]),
                        ("csa_cache_copy_pages", [p, p, ll, i, i, p, p, i, p, p]),
+                       ("csa_decode_paged_q8", [p] * 11 + [ll] + [i] * 7 + [f, i, i, p]),
                        ("csa_cache_append_q8", [p] * 17 + [i] * 10 + [p]),
                        ("csa_cache_read", [p] * 10 + [i] * 9 + [p]),
                        ("csa_cache_accept", [p] * 8 + [i] * 5 + [p]),

@@ -100,24 +100,24 @@ def decode_paged_workspace_bytes(B: int, Hq: int, Hkv: int, d: int) -> int:
     return n
 
 
-def decode_paged(q, k_pages, v_pages, block_table, seqlens, k0=None, v0=None, *, mode: int = 0,
-                 scale=None, out=None, lse=None, workspace=None, want_lse: bool = True,
-                 stream=None):
+def decode_paged(q, k_pages, v_pages, block_table, seqlens, k0=None, v0=None, *, row_scales=None,
+                 mode: int = 0, scale=None, out=None, lse=None, workspace=None,
+                 want_lse: bool = True, stream=None):
     """One decode step over a paged cache: the newest token of each sequence
     against the rows in its pages.  Returns (o [B, Hq, d], lse [B, Hq]).
 
-    q: bf16 CUDA [B, Hq, d]; k_pages, v_pages: bf16 [P, Hkv, S, d], query head
-    h reading cached head h // (Hq // Hkv); block_table: int32 [B, M], the
-    pages of each sequence in order; seqlens: int32 [B], the tokens held with
-    the newest one (0: an empty place in the batch, o = 0 and lse = -inf).
-    k0, v0: [Hkv, d] in mode GIVEN (2).  d in {64, 128, 256}, S a multiple of
-    8.  workspace: a CUDA tensor of decode_paged_workspace_bytes(B, Hq, Hkv,
-    d) bytes (allocated when None); stream: as everywhere, torch's current
-    stream when None."""
+    q: bf16 CUDA [B, Hq, d]; k_pages, v_pages: bf16 [P, Hkv, S, d], or 8 bits with
+    row_scales as in cache_append, query head h reading cached head
+    h // (Hq // Hkv); block_table: int32 [B, M], the pages of each sequence in
+    order; seqlens: int32 [B], the tokens held with the newest one (0: an empty
+    place in the batch, o = 0 and lse = -inf).  k0, v0: bf16 [Hkv, d] in mode
+    GIVEN (2).  d in {64, 128, 256}, S a multiple of 8.  workspace: a CUDA tensor
+    of decode_paged_workspace_bytes(B, Hq, Hkv, d) bytes (allocated when None);
+    stream: as everywhere, torch's current stream when None."""
     if stream is not None:
         return _there(decode_paged, locals())
     return _native.decode_paged(q, k_pages, v_pages, block_table, seqlens, k0, v0, mode, scale, out, lse,
-                                workspace, want_lse)
+                                workspace, want_lse, row_scales)
 
 
 # ------------------------------------------------------------ rotary positions

@@ -326,6 +326,34 @@ int append_any(const csa_rope_plan *plan, const void *q, const long long *q_stri
 
 bool eight_bits(int kind) { return kind == CSA_E4M3 || kind == CSA_INT8; }
 
+int paged_check(const csa_paged_args &a, const void *workspace, long long workspace_bytes, int d, int kind, bool *empty) {
+    *empty = false;
+    if (a.Hq < 0 || a.Hkv < 1 || a.Hq % a.Hkv != 0 || d < 1) return CSA_ERR_INVALID_ARG;
+    if (!std::isfinite(a.scale)) return CSA_ERR_INVALID_ARG;
+    if (a.mode < CSA_K0_ZERO || a.mode > CSA_K0_GIVEN) return CSA_ERR_INVALID_ARG;
+    int rc = check_tables(a.B, a.P, a.S, a.M);
+    if (rc != CSA_OK) return rc;
+    if (!(d == 64 || d == 128 || d == 256) || a.S % 8 != 0) return CSA_ERR_UNSUPPORTED;
+    // tiles of 32 rows of 8 bits
+    if (eight_bits(kind) && (long long)a.M * a.S > kIntMax - 31) return CSA_ERR_UNSUPPORTED;
+    if ((long double)a.P * a.Hkv * a.S > kIntMax) return CSA_ERR_UNSUPPORTED;
+    if ((long long)a.B * a.Hq > kIntMax) return CSA_ERR_UNSUPPORTED;
+    *empty = (long long)a.B * a.Hq == 0;
+    if (*empty) return CSA_OK;
+    if (!a.q || (a.P > 0 && (!a.k_pages || !a.v_pages)) || !a.block_table || !a.seqlens || !a.out) return CSA_ERR_INVALID_ARG;
+    if (eight_bits(kind) && a.P > 0 && !a.row_scales) return CSA_ERR_INVALID_ARG;
+    if (a.mode == CSA_K0_GIVEN && (!a.k0 || !a.v0)) return CSA_ERR_INVALID_ARG;
+    const long long need = csa_decode_paged_scratch_bytes(a.B, a.Hq, a.Hkv, d);
+    if (need < 0) return CSA_ERR_UNSUPPORTED;
+    if (!workspace || workspace_bytes < need) return CSA_ERR_INVALID_ARG;
+    if (!aligned(a.q, 16) || !aligned(a.k_pages, 16) || !aligned(a.v_pages, 16) || !aligned(a.out, 16) ||
+        !aligned(workspace, 16) || !aligned(a.lse, 4) || !aligned(a.seqlens, 4) || !aligned(a.block_table, 4) ||
+        !aligned(a.row_scales, 16))
+        return CSA_ERR_ALIGNMENT;
+    if (a.mode == CSA_K0_GIVEN && (!aligned(a.k0, 16) || !aligned(a.v0, 16))) return CSA_ERR_ALIGNMENT;
+    return device_ok();
+}
+
 }  // namespace
 
 extern "C" {
@@ -340,29 +368,26 @@ int csa_decode_paged(const void *q, const void *k_pages, const void *v_pages, co
                      float *lse, void *workspace, long long workspace_bytes, int B, int Hq,
                      int Hkv, int P, int S, int M, int d, float scale, int k0_mode,
                      csa_stream_t stream) {
-    if (Hq < 0 || Hkv < 1 || Hq % Hkv != 0 || d < 1) return CSA_ERR_INVALID_ARG;
-    if (!std::isfinite(scale)) return CSA_ERR_INVALID_ARG;
-    if (k0_mode < CSA_K0_ZERO || k0_mode > CSA_K0_GIVEN) return CSA_ERR_INVALID_ARG;
-    int rc = check_tables(B, P, S, M);
-    if (rc != CSA_OK) return rc;
-    if (!(d == 64 || d == 128 || d == 256) || S % 8 != 0) return CSA_ERR_UNSUPPORTED;
-    if ((long double)P * Hkv * S > kIntMax) return CSA_ERR_UNSUPPORTED;
-    if ((long long)B * Hq > kIntMax) return CSA_ERR_UNSUPPORTED;
-    if ((long long)B * Hq == 0) return CSA_OK;
-    if (!q || (P > 0 && (!k_pages || !v_pages)) || !block_table || !seqlens || !out) return CSA_ERR_INVALID_ARG;
-    if (k0_mode == CSA_K0_GIVEN && (!k0 || !v0)) return CSA_ERR_INVALID_ARG;
-    const long long need = csa_decode_paged_scratch_bytes(B, Hq, Hkv, d);
-    if (need < 0) return CSA_ERR_UNSUPPORTED;
-    if (!workspace || workspace_bytes < need) return CSA_ERR_INVALID_ARG;
-    if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(out, 16) ||
-        !aligned(workspace, 16) || !aligned(lse, 4) || !aligned(seqlens, 4) ||
-        !aligned(block_table, 4))
-        return CSA_ERR_ALIGNMENT;
-    if (k0_mode == CSA_K0_GIVEN && (!aligned(k0, 16) || !aligned(v0, 16))) return CSA_ERR_ALIGNMENT;
-    if ((rc = device_ok()) != CSA_OK) return rc;
-    return csa_decode_paged_run(q, k_pages, v_pages, k0, v0, block_table, seqlens, out, lse,
-                                workspace, B, Hq, Hkv, P, S, M, d, scale, k0_mode,
-                                reinterpret_cast<cudaStream_t>(stream));
+    const csa_paged_args a = {q, k_pages, v_pages, nullptr, k0, v0, block_table, seqlens, out, lse, B, Hq, Hkv, P, S, M,
+                              scale, k0_mode};
+    bool empty;
+    int rc = paged_check(a, workspace, workspace_bytes, d, CSA_BF16, &empty);
+    if (rc != CSA_OK || empty) return rc;
+    return csa_decode_paged_run(a, workspace, d, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int csa_decode_paged_q8(const void *q, const void *k_pages, const void *v_pages, const float *row_scales,
+                        const void *k0, const void *v0, const int *block_table, const int *seqlens, void *out,
+                        float *lse, void *workspace, long long workspace_bytes, int B, int Hq, int Hkv, int P,
+                        int S, int M, int d, float scale, int k0_mode, int kind, csa_stream_t stream) {
+    if (!eight_bits(kind)) return CSA_ERR_INVALID_ARG;
+    const csa_paged_args a = {q, k_pages, v_pages, row_scales, k0, v0, block_table, seqlens, out, lse, B, Hq, Hkv, P, S,
+                              M, scale, k0_mode};
+    bool empty;
+    int rc = paged_check(a, workspace, workspace_bytes, d, kind, &empty);
+    if (rc != CSA_OK || empty) return rc;
+    return (kind == CSA_E4M3 ? csa_decode_paged_e4m3_run : csa_decode_paged_int8_run)(
+        a, workspace, d, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int csa_rope_plan_init(csa_rope_plan *plan, const int *sections, int axes, double base, int flags) {
@@ -739,7 +764,9 @@ int csa_device_status(void) {
     const int g = csa_rope_take_status();
     const int h = csa_cache_take_status();
     const int i = csa_quant_take_status();
-    for (const int word : {a, b, c, e, f, g, h, i})
+    const int j = csa_paged_e4m3_take_status();
+    const int k = csa_paged_int8_take_status();
+    for (const int word : {a, b, c, e, f, g, h, i, j, k})
         if (word != CSA_OK) return word;
     return CSA_OK;
 }

@@ -102,13 +102,26 @@ int csa_host_forward(const void *q_h, const void *k_h, const void *v_h, const vo
                      int d, float scale, int mode, int heads_per_chunk, bool entry_wait,
                      cudaStream_t s_compute, cudaStream_t s_h2d, cudaStream_t s_d2h);
 
-// Decode step over a paged cache (csa_paged.cu), bf16, d in {64, 128, 256}.
+// Decode step over a paged cache (csa_paged.cu and, for 8-bit pools, csa_paged_e4m3.cu
+// and csa_paged_int8.cu), d in {64, 128, 256}.
+struct csa_paged_args {
+    const void *q, *k_pages, *v_pages;
+    const float *row_scales;  // of 8-bit pools
+    const void *k0, *v0;
+    const int *block_table, *seqlens;
+    void *out;
+    float *lse;
+    int B, Hq, Hkv, P, S, M;
+    float scale;
+    int mode;
+};
 long long csa_decode_paged_scratch_bytes(int B, int Hq, int Hkv, int d);
-int csa_decode_paged_run(const void *q, const void *k_pages, const void *v_pages, const void *k0,
-                         const void *v0, const int *block_table, const int *seqlens, void *out,
-                         float *lse, void *scratch, int B, int Hq, int Hkv, int P, int S, int M,
-                         int d, float scale, int mode, cudaStream_t stream);
+int csa_decode_paged_run(const csa_paged_args &a, void *scratch, int d, cudaStream_t stream);
+int csa_decode_paged_e4m3_run(const csa_paged_args &a, void *scratch, int d, cudaStream_t stream);
+int csa_decode_paged_int8_run(const csa_paged_args &a, void *scratch, int d, cudaStream_t stream);
 int csa_paged_take_status(void);
+int csa_paged_e4m3_take_status(void);
+int csa_paged_int8_take_status(void);
 
 // Rotary positions and the rows of new tokens into pages (csa_rope.cu).
 int csa_rope_plan_make(csa_rope_plan *plan, const int *sections, int axes, double base, int flags);

@@ -135,7 +135,18 @@ PyObject *tuple(std::initializer_list<Tensor> items) {
 }
 
 // ------------------------------------------------------------------ decode
-// q, k_pages, v_pages, block_table, seqlens, k0, v0, mode, scale, out, lse, workspace, want_lse
+// What a pool's elements are: with row_scales 8 bits, and the scales go with them.
+int kind_of(const Tensor &pool, const Tensor *row_scales, IntArrayRef shape, const at::Device &dev) {
+    const auto t = pool.scalar_type();
+    const bool eight = t == at::kFloat8_e4m3fn || t == at::kChar;
+    TORCH_CHECK_VALUE(eight || t == at::kBFloat16 || t == at::kFloat, "pools of ", t, " are not supported");
+    TORCH_CHECK_VALUE(eight == (row_scales != nullptr), "row_scales go with pools of 8 bits, got ", t,
+                      row_scales ? " with" : " without", " them");
+    if (eight) need(*row_scales, "row_scales", at::kFloat, {shape[0], shape[1], shape[2], 2}, dev);
+    return t == at::kFloat8_e4m3fn ? CSA_E4M3 : t == at::kChar ? CSA_INT8 : t == at::kBFloat16 ? CSA_BF16 : CSA_F32;
+}
+
+// q, k_pages, v_pages, block_table, seqlens, k0, v0, mode, scale, out, lse, workspace, want_lse, row_scales
 PyObject *decode_paged(PyObject *, PyObject *const *a, Py_ssize_t) {
     HANDLE_TH_ERRORS
     const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k_pages"), &v = tensor(a[2], "v_pages"),
@@ -147,8 +158,11 @@ PyObject *decode_paged(PyObject *, PyObject *const *a, Py_ssize_t) {
                   M = table.size(1);
     const auto bf = at::kBFloat16;
     need(q, "q", bf, {B, Hq, d}, here.dev);
-    need(k, "k_pages", bf, {P, Hkv, S, d}, here.dev);
-    need(v, "v_pages", bf, {P, Hkv, S, d}, here.dev);
+    const Tensor *scales = optional(a[13], "row_scales");
+    const int kind = kind_of(k, scales, {P, Hkv, S, d}, here.dev);
+    const auto held = scales ? k.scalar_type() : bf;
+    need(k, "k_pages", held, {P, Hkv, S, d}, here.dev);
+    need(v, "v_pages", held, {P, Hkv, S, d}, here.dev);
     need(table, "block_table", at::kInt, {B, M}, here.dev);
     need(lens, "seqlens", at::kInt, {B}, here.dev);
     const int mode = integer(a[7], "mode");
@@ -179,10 +193,18 @@ PyObject *decode_paged(PyObject *, PyObject *const *a, Py_ssize_t) {
     }
     TORCH_CHECK_VALUE(ws->device() == here.dev && ws->is_contiguous(), "workspace must be a contiguous tensor on ",
                       here.dev);
-    check(csa_decode_paged(at_(q), at_(k), at_(v), at_(k0), at_(v0), at_<int>(table), at_<int>(lens), at_(o),
-                           lse.defined() ? at_<float>(lse) : nullptr, at_(ws), (long long)ws->nbytes(), b, hq, hkv,
-                           size(P, "P"), size(S, "S"), size(M, "M"), dd, (float)scale, mode, here.stream),
-          "csa_decode_paged");
+    const int pp = size(P, "P"), ss = size(S, "S"), m = size(M, "M");
+    float *lse_at = lse.defined() ? at_<float>(lse) : nullptr;
+    if (scales)
+        check(csa_decode_paged_q8(at_(q), at_(k), at_(v), at_<float>(*scales), at_(k0), at_(v0), at_<int>(table),
+                                  at_<int>(lens), at_(o), lse_at, at_(ws), (long long)ws->nbytes(), b, hq, hkv, pp, ss, m,
+                                  dd, (float)scale, mode, kind, here.stream),
+              "csa_decode_paged_q8");
+    else
+        check(csa_decode_paged(at_(q), at_(k), at_(v), at_(k0), at_(v0), at_<int>(table), at_<int>(lens), at_(o), lse_at,
+                               at_(ws), (long long)ws->nbytes(), b, hq, hkv, pp, ss, m, dd, (float)scale, mode,
+                               here.stream),
+              "csa_decode_paged");
     wrote({&o, &lse, ws});
     return tuple({o, lse});
     END_HANDLE_TH_ERRORS
@@ -286,17 +308,6 @@ PyObject *rope(PyObject *, PyObject *const *a, Py_ssize_t) {
     wrote({&qo, &ko});
     return tuple({qo, ko});
     END_HANDLE_TH_ERRORS
-}
-
-// What a pool's elements are: with row_scales 8 bits, and the scales go with them.
-int kind_of(const Tensor &pool, const Tensor *row_scales, IntArrayRef shape, const at::Device &dev) {
-    const auto t = pool.scalar_type();
-    const bool eight = t == at::kFloat8_e4m3fn || t == at::kChar;
-    TORCH_CHECK_VALUE(eight || t == at::kBFloat16 || t == at::kFloat, "pools of ", t, " are not supported");
-    TORCH_CHECK_VALUE(eight == (row_scales != nullptr), "row_scales go with pools of 8 bits, got ", t,
-                      row_scales ? " with" : " without", " them");
-    if (eight) need(*row_scales, "row_scales", at::kFloat, {shape[0], shape[1], shape[2], 2}, dev);
-    return t == at::kFloat8_e4m3fn ? CSA_E4M3 : t == at::kChar ? CSA_INT8 : t == at::kBFloat16 ? CSA_BF16 : CSA_F32;
 }
 
 // k, v, k_pages, v_pages, block_table, seqlens, counts, plan address or None, plan d, positions, q, q_out, row_scales
@@ -579,7 +590,7 @@ PyObject *counted(PyObject *self, PyObject *const *a, Py_ssize_t n) {
 }
 #define CALL(name, n) {#name, (PyCFunction)(void (*)(void))counted<name, n>, METH_FASTCALL, nullptr}
 
-PyMethodDef g_methods[] = {CALL(decode_paged, 13),
+PyMethodDef g_methods[] = {CALL(decode_paged, 14),
                            CALL(rope, 8),
                            CALL(cache_append, 13),
                            CALL(cache_read, 10),

@@ -481,6 +481,22 @@ int csa_decode_paged(const void *q, const void *k_pages, const void *v_pages, co
                      int Hkv, int P, int S, int M, int d, float scale, int k0_mode,
                      csa_stream_t stream);
 
+/*
+ * csa_decode_paged_q8 - csa_decode_paged over pools of 8 bits (kind CSA_E4M3 or
+ *   CSA_INT8), whose rows stand for code * scale; q, k0, v0 and out as there.
+ *   row_scales 16-byte aligned; M * S at most 2^31 - 32.  A row whose scale is NaN
+ *   makes what attends to it NaN.  Logits are formed from the codes in fp32, the
+ *   weights are fp16 numbers (with up to 8 query heads per cached head, or per block
+ *   of them, sums of two), the sums fp32.  Everything else as csa_decode_paged, the
+ *   workspace too.
+ */
+int csa_decode_paged_q8(const void *q, const void *k_pages, const void *v_pages,
+                        const float *row_scales, const void *k0, const void *v0,
+                        const int *block_table, const int *seqlens, void *out, float *lse,
+                        void *workspace, long long workspace_bytes, int B, int Hq, int Hkv, int P,
+                        int S, int M, int d, float scale, int k0_mode, int kind,
+                        csa_stream_t stream);
+
 /* csa_decode_paged_workspace_bytes - workspace bytes csa_decode_paged needs
  * (host only), or -1 for a negative size, Hkv that does not divide Hq, or d
  * outside {64, 128, 256}. */

@@ -117,3 +117,15 @@ class DraftBooks(Books):
                 self.refs[self.table[b][j]] -= 1
                 self.table[b][j] = -1
         return src, dst
+
+
+def bounds8(q, k, v, ref_o, ref_lse, scale):
+    """Bounds on |o - ref_o| and |lse - ref_lse| of one row over 8-bit pools: q [d], k, v [n + 1, d] with the sink's
+    pair, in 64 bits.  As paged_util.decode_bounds: logits off by (d + 8) 2^-24 A, the weight function by 2^-16.
+    Then weights as single fp16 numbers, 2^-12 relative, or 2^-25 absolute where they are below 2^-14 in units in which
+    the largest weight is 2^8 at least times its value's scale by the reference: 2^-33 of the largest value each."""
+    q, k, v = (np.asarray(t, np.float64) for t in (q, k, v))
+    a = abs(scale) * (np.abs(k) @ np.abs(q)).max()
+    rel = (q.size + 8) * 2.0 ** -24 * a + 2.0 ** -16
+    return (2.0 ** -8 * np.abs(ref_o) + (2 * rel + 2.0 ** -12 + len(k) * 2.0 ** -33) * np.abs(v).max(),
+            rel + 2.0 ** -22 * (1 + abs(ref_lse)))
