@@ -43,6 +43,8 @@ from ._paged import (  # noqa: F401
     cache_reserve,
     decode_paged,
     decode_paged_workspace_bytes,
+    decode_tree,
+    decode_tree_workspace_bytes,
     rope,
     rope_backward,
 )
@@ -58,5 +60,5 @@ __all__ = [
     "status_string",
     "decode_paged", "decode_paged_workspace_bytes", "RopeAxes", "rope", "rope_backward",
     "cache_append", "cache_reserve", "cache_free", "cache_fork", "cache_compact",
-    "cache_copy_pages", "cache_read", "cache_accept", "cache_copy_rows",
+    "cache_copy_pages", "cache_read", "decode_tree", "decode_tree_workspace_bytes", "cache_accept", "cache_copy_rows",
 ]

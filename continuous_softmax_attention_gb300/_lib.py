@@ -84,6 +84,7 @@ def load():
                        ("csa_cache_compact", [p] * 6 + [i] * 4 + [p]),
                        ("csa_cache_copy_pages", [p, p, ll, i, i, p, p, i, p, p]),
                        ("csa_decode_paged_q8", [p] * 11 + [ll] + [i] * 7 + [f, i, i, p]),
+                       ("csa_decode_tree", [p] * 13 + [ll] + [i] * 8 + [f, i, i, p]),
                        ("csa_cache_append_q8", [p] * 17 + [i] * 10 + [p]),
                        ("csa_cache_read", [p] * 10 + [i] * 9 + [p]),
                        ("csa_cache_accept", [p] * 8 + [i] * 5 + [p]),
@@ -95,8 +96,9 @@ def load():
                  "csa_forward_host_workspace_bytes", "csa_decode_paged_workspace_bytes"):
         getattr(lib, name).argtypes = [i, i, i, i]
         getattr(lib, name).restype = ctypes.c_longlong
-    lib.csa_decode_range_workspace_bytes.argtypes = [i, i, i, i, i]
-    lib.csa_decode_range_workspace_bytes.restype = ctypes.c_longlong
+    for name in ("csa_decode_range_workspace_bytes", "csa_decode_tree_workspace_bytes"):
+        getattr(lib, name).argtypes = [i, i, i, i, i]
+        getattr(lib, name).restype = ctypes.c_longlong
     lib.csa_status_string.argtypes = [i]
     lib.csa_status_string.restype = ctypes.c_char_p
     _lib = lib

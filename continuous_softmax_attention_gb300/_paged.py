@@ -252,6 +252,36 @@ def cache_copy_pages(k_pages, v_pages, src, dst, *, count=None, stream=None):
 
 
 # --------------------------------------------------------------- drafted tokens
+def decode_tree_workspace_bytes(B: int, Hq: int, Hkv: int, T: int, d: int) -> int:
+    """Bytes of workspace csa_decode_tree needs (host-side, no device needed)."""
+    n = int(load().csa_decode_tree_workspace_bytes(int(B), int(Hq), int(Hkv), int(T), int(d)))
+    if n < 0:
+        raise CsaError(CSA_ERR_UNSUPPORTED, "csa_decode_tree_workspace_bytes")
+    return n
+
+
+def decode_tree(q, k_pages, v_pages, block_table, seqlens, parents=None, k0=None, v0=None, *,
+                counts=None, row_scales=None, mode: int = 0, scale=None, out=None, lse=None,
+                workspace=None, want_lse: bool = True, stream=None):
+    """Attention of drafted tokens that the cache already holds (cache_append):
+    the last counts[b] tokens of every sequence are nodes of a tree, and node t
+    sees the tokens before the draft and the nodes on the path from a root to
+    itself.  Returns (o [B, Hq, T, d], lse [B, Hq, T]); rows t >= counts[b] are 0
+    and -inf.
+
+    q: bf16 CUDA [B, Hq, T, d], T <= 64; parents: int32 [B, T], the parent of
+    each node, -1 where it follows the tokens before the draft, else a node
+    before it; None for a chain, which is also how a prompt's next rows attend
+    over the pages behind a past.  counts: int32 [B] (T each when None), counted
+    in seqlens.  Everything else as decode_paged; workspace:
+    decode_tree_workspace_bytes(B, Hq, Hkv, T, d) bytes.  cache_accept keeps the
+    accepted branch afterwards."""
+    if stream is not None:
+        return _there(decode_tree, locals())
+    return _native.decode_tree(q, k_pages, v_pages, block_table, seqlens, parents, k0, v0, counts, mode, scale, out,
+                               lse, workspace, want_lse, row_scales)
+
+
 def cache_accept(page_refs, block_table, seqlens, page_size: int, last, T: int, *, parents=None,
                  counts=None, stream=None):
     """Keeps the accepted branch of a tree of drafted tokens, the last counts[b]

@@ -326,7 +326,9 @@ int append_any(const csa_rope_plan *plan, const void *q, const long long *q_stri
 
 bool eight_bits(int kind) { return kind == CSA_E4M3 || kind == CSA_INT8; }
 
-int paged_check(const csa_paged_args &a, const void *workspace, long long workspace_bytes, int d, int kind, bool *empty) {
+// The decode step's arguments; T >= 0: those of its form for T drafted tokens.
+int paged_check(const csa_paged_args &a, const void *workspace, long long workspace_bytes, int d, int kind, int T,
+                bool *empty) {
     *empty = false;
     if (a.Hq < 0 || a.Hkv < 1 || a.Hq % a.Hkv != 0 || d < 1) return CSA_ERR_INVALID_ARG;
     if (!std::isfinite(a.scale)) return CSA_ERR_INVALID_ARG;
@@ -337,13 +339,14 @@ int paged_check(const csa_paged_args &a, const void *workspace, long long worksp
     // tiles of 32 rows of 8 bits
     if (eight_bits(kind) && (long long)a.M * a.S > kIntMax - 31) return CSA_ERR_UNSUPPORTED;
     if ((long double)a.P * a.Hkv * a.S > kIntMax) return CSA_ERR_UNSUPPORTED;
-    if ((long long)a.B * a.Hq > kIntMax) return CSA_ERR_UNSUPPORTED;
-    *empty = (long long)a.B * a.Hq == 0;
+    if ((long double)a.B * a.Hq * (T > 0 ? T : 1) > kIntMax) return CSA_ERR_UNSUPPORTED;
+    *empty = (long long)a.B * a.Hq == 0 || T == 0;
     if (*empty) return CSA_OK;
     if (!a.q || (a.P > 0 && (!a.k_pages || !a.v_pages)) || !a.block_table || !a.seqlens || !a.out) return CSA_ERR_INVALID_ARG;
     if (eight_bits(kind) && a.P > 0 && !a.row_scales) return CSA_ERR_INVALID_ARG;
     if (a.mode == CSA_K0_GIVEN && (!a.k0 || !a.v0)) return CSA_ERR_INVALID_ARG;
-    const long long need = csa_decode_paged_scratch_bytes(a.B, a.Hq, a.Hkv, d);
+    const long long need = T > 0 ? csa_decode_tree_scratch_bytes(a.B, a.Hq, a.Hkv, T, d)
+                                 : csa_decode_paged_scratch_bytes(a.B, a.Hq, a.Hkv, d);
     if (need < 0) return CSA_ERR_UNSUPPORTED;
     if (!workspace || workspace_bytes < need) return CSA_ERR_INVALID_ARG;
     if (!aligned(a.q, 16) || !aligned(a.k_pages, 16) || !aligned(a.v_pages, 16) || !aligned(a.out, 16) ||
@@ -371,7 +374,7 @@ int csa_decode_paged(const void *q, const void *k_pages, const void *v_pages, co
     const csa_paged_args a = {q, k_pages, v_pages, nullptr, k0, v0, block_table, seqlens, out, lse, B, Hq, Hkv, P, S, M,
                               scale, k0_mode};
     bool empty;
-    int rc = paged_check(a, workspace, workspace_bytes, d, CSA_BF16, &empty);
+    int rc = paged_check(a, workspace, workspace_bytes, d, CSA_BF16, -1, &empty);
     if (rc != CSA_OK || empty) return rc;
     return csa_decode_paged_run(a, workspace, d, reinterpret_cast<cudaStream_t>(stream));
 }
@@ -384,10 +387,33 @@ int csa_decode_paged_q8(const void *q, const void *k_pages, const void *v_pages,
     const csa_paged_args a = {q, k_pages, v_pages, row_scales, k0, v0, block_table, seqlens, out, lse, B, Hq, Hkv, P, S,
                               M, scale, k0_mode};
     bool empty;
-    int rc = paged_check(a, workspace, workspace_bytes, d, kind, &empty);
+    int rc = paged_check(a, workspace, workspace_bytes, d, kind, -1, &empty);
     if (rc != CSA_OK || empty) return rc;
     return (kind == CSA_E4M3 ? csa_decode_paged_e4m3_run : csa_decode_paged_int8_run)(
         a, workspace, d, reinterpret_cast<cudaStream_t>(stream));
+}
+
+long long csa_decode_tree_workspace_bytes(int B, int Hq, int Hkv, int T, int d) {
+    if (B < 0 || Hq < 0 || Hkv < 1 || Hq % Hkv != 0 || T < 0 || T > CSA_TREE_MAX) return -1;
+    if (!(d == 64 || d == 128 || d == 256) || (long double)B * Hq * (T > 0 ? T : 1) > kIntMax) return -1;
+    return (long long)B * Hq * T == 0 ? 0 : csa_decode_tree_scratch_bytes(B, Hq, Hkv, T, d);
+}
+
+int csa_decode_tree(const void *q, const void *k_pages, const void *v_pages, const float *row_scales, const void *k0,
+                    const void *v0, const int *block_table, const int *seqlens, const int *parents, const int *counts,
+                    void *out, float *lse, void *workspace, long long workspace_bytes, int B, int Hq, int Hkv, int T,
+                    int P, int S, int M, int d, float scale, int k0_mode, int kind, csa_stream_t stream) {
+    if (T < 0 || (kind != CSA_BF16 && !eight_bits(kind))) return CSA_ERR_INVALID_ARG;
+    if (T > CSA_TREE_MAX) return CSA_ERR_UNSUPPORTED;
+    if (kind == CSA_BF16 && row_scales) return CSA_ERR_INVALID_ARG;
+    const csa_paged_args a = {q, k_pages, v_pages, row_scales, k0, v0, block_table, seqlens, out, lse, B, Hq, Hkv, P, S,
+                              M, scale, k0_mode};
+    bool empty;
+    int rc = paged_check(a, workspace, workspace_bytes, d, kind, T, &empty);
+    if (empty || (rc != CSA_OK && rc != CSA_ERR_NO_DEVICE)) return rc;
+    if (!aligned(parents, 4) || !aligned(counts, 4)) return CSA_ERR_ALIGNMENT;
+    if (rc != CSA_OK) return rc;
+    return csa_decode_tree_run(a, parents, counts, T, d, kind, workspace, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int csa_rope_plan_init(csa_rope_plan *plan, const int *sections, int axes, double base, int flags) {
@@ -766,7 +792,8 @@ int csa_device_status(void) {
     const int i = csa_quant_take_status();
     const int j = csa_paged_e4m3_take_status();
     const int k = csa_paged_int8_take_status();
-    for (const int word : {a, b, c, e, f, g, h, i, j, k})
+    const int l = csa_tree_take_status();
+    for (const int word : {a, b, c, e, f, g, h, i, j, k, l})
         if (word != CSA_OK) return word;
     return CSA_OK;
 }

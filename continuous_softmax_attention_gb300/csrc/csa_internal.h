@@ -114,6 +114,10 @@ struct csa_paged_args {
     int B, Hq, Hkv, P, S, M;
     float scale;
     int mode;
+    // drafted tokens: Hq counts the rows of T drafted tokens per query head; the last counts[b] tokens of a sequence (T
+    // each where it is NULL) are left out, and the parts stay in the scratch (csa_tree.cu)
+    const int *counts;
+    int T;
 };
 long long csa_decode_paged_scratch_bytes(int B, int Hq, int Hkv, int d);
 int csa_decode_paged_run(const csa_paged_args &a, void *scratch, int d, cudaStream_t stream);
@@ -122,6 +126,12 @@ int csa_decode_paged_int8_run(const csa_paged_args &a, void *scratch, int d, cud
 int csa_paged_take_status(void);
 int csa_paged_e4m3_take_status(void);
 int csa_paged_int8_take_status(void);
+
+// Rows of a tree of drafted tokens over a paged cache (csa_tree.cu), 1 <= T <= 64; a.counts and a.T are not read.
+long long csa_decode_tree_scratch_bytes(int B, int Hq, int Hkv, int T, int d);
+int csa_decode_tree_run(const csa_paged_args &a, const int *parents, const int *counts, int T, int d, int kind,
+                        void *scratch, cudaStream_t stream);
+int csa_tree_take_status(void);
 
 // Rotary positions and the rows of new tokens into pages (csa_rope.cu).
 int csa_rope_plan_make(csa_rope_plan *plan, const int *sections, int axes, double base, int flags);

@@ -53,6 +53,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -141,8 +142,13 @@ struct PagedParams {
     float *part_ml;   // [2 * workers][HB][2]: its maximum (log2 units) and weight sum
     // the segments (heads of sequences) that several workers share: {segment or -1, first worker,
     // last worker, the first one's slot}, by segment or by the worker that begins one
-    int4 *joins;      // [workers]
+    int4 *joins;      // [workers], with drafted tokens [max(workers, segments)]
     int by_segment;
+    // T > 0: rows of a tree of drafted tokens, T per query head, over the tokens before the draft: the last
+    // counts[b] tokens (T each where it is NULL) are left out, and every segment leaves parts, a whole one in
+    // slot 2 * workers + segment with a first worker of -1
+    const int *counts;
+    int T;
     int cluster;      // blocks per segment of the one-kernel form
     unsigned long long s_inv;  // 2^64 / S rounded up: row / S is the high word of row * s_inv
     int B, Hq, Hkv, P, S, M;
@@ -269,6 +275,19 @@ __device__ __forceinline__ void ldsm_t(uint32_t addr, uint32_t (&r)[4]) {
                  : "memory");
 }
 
+// The rows that each sequence is attended to, negative where its lengths make no sense.
+struct Lengths {
+    const int *seqlens, *counts;
+    int T;
+    long long most;
+    __device__ __forceinline__ int operator[](int b) const {
+        const int n = seqlens[b];
+        if (T == 0) return n;
+        const int c = counts ? counts[b] : T;
+        return c < 0 || c > T || n < c || n > most ? -1 : n - c;
+    }
+};
+
 __device__ __forceinline__ int tiles_of(int n, int KT, long long most) {
     return n < 0 || n > most ? 0 : (int)(((long long)n + KT - 1) / KT);
 }
@@ -291,7 +310,7 @@ struct Cut {
 
 // at[0 .. blockDim.x] gets the units (per head) of the sequences before each
 // thread's chunk of sequences, the last entry the total.  Whole block.
-__device__ Cut form_cut(const int *seqlens, int B, int KT, long long most, int heads, long long all, long long *at) {
+__device__ Cut form_cut(const Lengths &seqlens, int B, int KT, long long most, int heads, long long all, long long *at) {
     const int tid = threadIdx.x, per = (B + blockDim.x - 1) / blockDim.x;
     const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
     long long tiles = 0;
@@ -341,7 +360,7 @@ __device__ Cut form_cut(const int *seqlens, int B, int KT, long long most, int h
 }
 
 // The sequence that holds unit u, and the units before it.  Whole warp.
-__device__ __forceinline__ int find_sequence(long long u, const Cut &cut, const long long *at, const int *seqlens,
+__device__ __forceinline__ int find_sequence(long long u, const Cut &cut, const long long *at, const Lengths &seqlens,
                                              int B, int KT, long long most, int heads, long long &before) {
     // the last chunk that begins at or before u (chunks without units begin where the next one does)
     int begun = 0;
@@ -390,7 +409,7 @@ __device__ __forceinline__ void clip(Part &t, const Cut &cut, long long u0, long
 }
 
 // The next part with tiles; false behind the last.
-__device__ __forceinline__ bool next_part(Part &t, const Cut &cut, long long u0, long long u1, const int *seqlens,
+__device__ __forceinline__ bool next_part(Part &t, const Cut &cut, long long u0, long long u1, const Lengths &seqlens,
                                           int KT, long long most, int heads) {
     do {
         t.s0 += cut.units(t.tiles);
@@ -440,6 +459,7 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
     const int heads = p.Hkv * p.GB;
     const long long most = (long long)p.M * p.S;
+    const Lengths lens = {p.seqlens, p.counts, p.T, most};
     const int mine = warp / C::Pair, half_of = warp % C::Pair;  // worker in the block, warp of the worker
     volatile int *abort_flag = &s_abort[mine];
     // the warps of a worker
@@ -467,7 +487,7 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
         const int segment = blockIdx.x / p.cluster;
         now.b = segment / heads;
         now.head = segment - now.b * heads;
-        now.n = p.seqlens[now.b];
+        now.n = lens[now.b];
         now.tiles = tiles_of(now.n, KT, most);
         now.s0 = 0;
         if (now.tiles == 0) {  // no rows, or a length out of range: all blocks of the cluster leave
@@ -492,25 +512,26 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
         now.last = working ? (int)quot((long long)(part + 1) * now.tiles, parts) : 1;
     } else {
         const bool few = p.B <= 32;  // sequences: every warp forms the cut
-        const int lane_n = few && lane < p.B ? p.seqlens[lane] : 0;
+        const int lane_n = few && lane < p.B ? lens[lane] : 0;
         // the join's blocks may take their places as this kernel's blocks end
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         const long long all = (long long)C::Workers * gridDim.x;
         long long lane_before = 0;
         cut = few ? form_cut_warp(lane_n, KT, most, heads, all, lane_before)
-                  : form_cut(p.seqlens, p.B, KT, most, heads, all, s_cut);
+                  : form_cut(lens, p.B, KT, most, heads, all, s_cut);
         // sequences without rows, and lengths out of range
         for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-            const int n = p.seqlens[b];
+            const int n = lens[b];
             if (n > 0 && n <= most) continue;
+            if (p.by_segment)
+                for (int h = threadIdx.x; h < heads; h += blockDim.x) p.joins[b * heads + h] = make_int4(-1, 0, 0, 0);
+            if (p.T > 0) continue;
             const float v = n == 0 ? 0.0f : NAN;
             for (int i = threadIdx.x; i < p.Hq * D; i += blockDim.x)
                 p.out[(long long)b * p.Hq * D + i] = __float2bfloat16_rn(v);
             if (p.lse)
                 for (int h = threadIdx.x; h < p.Hq; h += blockDim.x)
                     p.lse[(long long)b * p.Hq + h] = n == 0 ? -INFINITY : NAN;
-            if (p.by_segment)
-                for (int h = threadIdx.x; h < heads; h += blockDim.x) p.joins[b * heads + h] = make_int4(-1, 0, 0, 0);
             if (threadIdx.x == 0 && n != 0) atomicCAS(&g_paged_status, 0, CSA_ERR_INVALID_ARG);
         }
 
@@ -528,14 +549,14 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
             now.s0 = __shfl_sync(0xffffffffu, lane_before, now.b) * heads;
             now.n = __shfl_sync(0xffffffffu, lane_n, now.b);
         } else {
-            now.b = find_sequence(u0, cut, s_cut, p.seqlens, p.B, KT, most, heads, now.s0);
-            now.n = p.seqlens[now.b];
+            now.b = find_sequence(u0, cut, s_cut, lens, p.B, KT, most, heads, now.s0);
+            now.n = lens[now.b];
         }
         now.tiles = tiles_of(now.n, KT, most);
         now.head = (int)quot(u0 - now.s0, cut.units(now.tiles));  // hk * GB + block of query heads
         now.s0 += (long long)now.head * cut.units(now.tiles);
         clip(now, cut, u0, u1);
-        if (now.tile >= now.last && !next_part(now, cut, u0, u1, p.seqlens, KT, most, heads)) return;
+        if (now.tile >= now.last && !next_part(now, cut, u0, u1, lens, KT, most, heads)) return;
     }
     auto page_index = [&](int row) { return (int)__umul64hi((unsigned long long)row, p.s_inv); };  // row / S
     auto cached_head = [&](int head) { return p.GB == 1 ? head : head / p.GB; };
@@ -586,7 +607,7 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
         edge_row = g == 0 ? now.tile * KT - 1 : g == 1 && now.last * KT < now.n ? now.last * KT : -1;
         edge_page = edge_row >= 0 ? p.table[(long long)now.b * p.M + page_index(edge_row)] : -1;
     };
-    auto next = [&](Part &t) { return !ONE && next_part(t, cut, u0, u1, p.seqlens, KT, most, heads); };
+    auto next = [&](Part &t) { return !ONE && next_part(t, cut, u0, u1, lens, KT, most, heads); };
     ask();
 
     Part ahead = now;
@@ -1196,7 +1217,7 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
         }
 
         bad = __any_sync(0xffffffffu, bad || lost);
-        const bool whole = r0 == 0 && r1 == n;
+        const bool all_rows = r0 == 0 && r1 == n, whole = all_rows && p.T == 0;
         float sum[RH];
 #pragma unroll
         for (int h = 0; h < RH; ++h) {
@@ -1206,7 +1227,7 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
             sum[h] = bad ? NAN : t + w0[h];
         }
         // a worker's part that does not begin a segment is its first
-        const long long slot = (worker * 2 + (u0 < now.s0 ? 1 : 0)) * p.HB;
+        const long long slot = (all_rows ? 2 * workers(D) + (long long)b * heads + now.head : worker * 2 + (u0 < now.s0 ? 1 : 0)) * p.HB;
         // ONE: this warp's ring, whose copies have all been read
         float *kept = reinterpret_cast<float *>(raw + (ring - smem_u32(raw)));
         const uint32_t *sink_v = given ? reinterpret_cast<const uint32_t *>(p.v0 + (long long)hk * D + half_of * DW) : nullptr;
@@ -1256,7 +1277,7 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
             const long long end = now.s0 + cut.units(now.tiles);
             const int segment = b * heads + now.head;
             p.joins[p.by_segment ? segment : worker] =
-                make_int4(whole ? -1 : segment, (int)worker, (int)cut.worker_of(end - 1), u0 < now.s0 ? 1 : 0);
+                make_int4(whole ? -1 : segment, all_rows ? -1 : (int)worker, (int)cut.worker_of(end - 1), u0 < now.s0 ? 1 : 0);
         }
         if (!next(now)) break;
         ask();
@@ -1500,7 +1521,7 @@ int launch(PagedParams &p, cudaStream_t stream) {
     const int heads = p.Hkv * p.GB;
     p.s_inv = ~0ull / p.S + 1;
     const long long segments = (long long)p.B * heads, tiles = ((long long)p.M * p.S + C::KT - 1) / C::KT;
-    p.cluster = cluster_for(segments, tiles, C::Workers);
+    p.cluster = p.T > 0 ? 0 : cluster_for(segments, tiles, C::Workers);
     if (p.cluster > 0) {
         auto kern = paged_kernel<D, RH, true, KIND>;
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::Smem) != cudaSuccess ||
@@ -1516,9 +1537,10 @@ int launch(PagedParams &p, cudaStream_t stream) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::Smem) != cudaSuccess)
         return CSA_ERR_CUDA;
     const long long all = (long long)grid * C::Workers;
-    p.by_segment = segments <= kGrid;
+    p.by_segment = p.T > 0 || segments <= kGrid;
     if (launch_after_previous(kern, grid, C::Warps * 32, C::Smem, stream, p, map_k, map_v) != cudaSuccess)
         return CSA_ERR_CUDA;
+    if (p.T > 0) return CSA_OK;  // the caller joins them
     // parts of a segment, at most about
     const long long parts = all / segments;
     const dim3 blocks = p.by_segment ? dim3((unsigned)segments, (unsigned)p.HB) : dim3((unsigned)all);
@@ -1549,6 +1571,8 @@ PagedParams paged_params(const csa_paged_args &a) {
     p.M = a.M;
     p.qscale = a.scale * kLog2e;
     p.mode = a.mode;
+    p.counts = a.counts;
+    p.T = a.T;
     return p;
 }
 
@@ -1558,9 +1582,10 @@ int run_paged(PagedParams &p, void *scratch, int d, cudaStream_t stream) {
     p.G = p.Hq / p.Hkv;
     p.GB = head_blocks(p.G);
     p.HB = (p.G + p.GB - 1) / p.GB;
+    const long long segments = p.T > 0 ? (long long)p.B * p.Hkv * p.GB : 0;  // with a slot and a note of their own
     p.joins = static_cast<int4 *>(scratch);
-    p.part_ml = reinterpret_cast<float *>(p.joins + workers(d));
-    p.part_o = p.part_ml + 2 * workers(d) * p.HB * 2;
+    p.part_ml = reinterpret_cast<float *>(p.joins + std::max(workers(d), segments));
+    p.part_o = p.part_ml + (2 * workers(d) + segments) * p.HB * 2;
     if (p.HB <= 8) {
         if (d == 64) return launch<64, 1, KIND>(p, stream);
         if (d == 128) return launch<128, 1, KIND>(p, stream);

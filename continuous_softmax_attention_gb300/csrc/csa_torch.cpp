@@ -210,6 +210,65 @@ PyObject *decode_paged(PyObject *, PyObject *const *a, Py_ssize_t) {
     END_HANDLE_TH_ERRORS
 }
 
+// q, k_pages, v_pages, block_table, seqlens, parents, k0, v0, counts, mode, scale, out, lse, workspace, want_lse, row_scales
+PyObject *decode_tree(PyObject *, PyObject *const *a, Py_ssize_t) {
+    HANDLE_TH_ERRORS
+    const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k_pages"), &v = tensor(a[2], "v_pages"),
+                 &table = tensor(a[3], "block_table"), &lens = tensor(a[4], "seqlens");
+    const Tensor *parents = optional(a[5], "parents"), *counts = optional(a[8], "counts"), *scales = optional(a[15], "row_scales");
+    Here here(q, "decode_tree");
+    TORCH_CHECK_VALUE(q.dim() == 4 && k.dim() == 4 && table.dim() == 2,
+                      "q is [B, Hq, T, d], the pools [P, Hkv, S, d], block_table [B, M]");
+    const int64_t B = q.size(0), Hq = q.size(1), T = q.size(2), d = q.size(3), P = k.size(0), Hkv = k.size(1), S = k.size(2),
+                  M = table.size(1);
+    const auto bf = at::kBFloat16;
+    need(q, "q", bf, {B, Hq, T, d}, here.dev);
+    const int kind = kind_of(k, scales, {P, Hkv, S, d}, here.dev);
+    const auto held = scales ? k.scalar_type() : bf;
+    need(k, "k_pages", held, {P, Hkv, S, d}, here.dev);
+    need(v, "v_pages", held, {P, Hkv, S, d}, here.dev);
+    need(table, "block_table", at::kInt, {B, M}, here.dev);
+    need(lens, "seqlens", at::kInt, {B}, here.dev);
+    if (parents) need(*parents, "parents", at::kInt, {B, T}, here.dev);
+    if (counts) need(*counts, "counts", at::kInt, {B}, here.dev);
+    const int mode = integer(a[9], "mode");
+    const Tensor *k0 = nullptr, *v0 = nullptr;
+    if (mode == CSA_K0_GIVEN) {
+        k0 = optional(a[6], "k0");
+        v0 = optional(a[7], "v0");
+        TORCH_CHECK_VALUE(k0 && v0, "mode 2 (given sink) needs k0 and v0");
+        need(*k0, "k0", bf, {Hkv, d}, here.dev);
+        need(*v0, "v0", bf, {Hkv, d}, here.dev);
+    }
+    double scale = 1.0 / std::sqrt((double)d);
+    if (a[10] != Py_None) {
+        scale = PyFloat_AsDouble(a[10]);
+        if (scale == -1.0 && PyErr_Occurred()) throw python_error();
+    }
+    Tensor o = out(optional(a[11], "out"), "out", bf, {B, Hq, T, d}, here.dev), lse;
+    const Tensor *lse_given = optional(a[12], "lse");
+    const int want_lse = PyObject_IsTrue(a[14]);
+    if (want_lse < 0) throw python_error();
+    if (lse_given || want_lse) lse = out(lse_given, "lse", at::kFloat, {B, Hq, T}, here.dev);
+    const int b = size(B, "B"), hq = size(Hq, "Hq"), hkv = size(Hkv, "Hkv"), t = size(T, "T"), dd = size(d, "d"),
+              pp = size(P, "P"), ss = size(S, "S"), m = size(M, "M");
+    const Tensor *ws = optional(a[13], "workspace");
+    Tensor own;
+    if (!ws) {
+        own = made({std::max<long long>(csa_decode_tree_workspace_bytes(b, hq, hkv, t, dd), 16)}, at::kByte, here.dev);
+        ws = &own;
+    }
+    TORCH_CHECK_VALUE(ws->device() == here.dev && ws->is_contiguous(), "workspace must be a contiguous tensor on ",
+                      here.dev);
+    check(csa_decode_tree(at_(q), at_(k), at_(v), at_<float>(scales), at_(k0), at_(v0), at_<int>(table), at_<int>(lens),
+                          at_<int>(parents), at_<int>(counts), at_(o), lse.defined() ? at_<float>(lse) : nullptr, at_(ws),
+                          (long long)ws->nbytes(), b, hq, hkv, t, pp, ss, m, dd, (float)scale, mode, kind, here.stream),
+          "csa_decode_tree");
+    wrote({&o, &lse, ws});
+    return tuple({o, lse});
+    END_HANDLE_TH_ERRORS
+}
+
 // ------------------------------------------------------------ rotary positions
 // A tensor of rows [B, H, T, d] whose last dimension is contiguous: its
 // strides over batch, head and time.
@@ -591,6 +650,7 @@ PyObject *counted(PyObject *self, PyObject *const *a, Py_ssize_t n) {
 #define CALL(name, n) {#name, (PyCFunction)(void (*)(void))counted<name, n>, METH_FASTCALL, nullptr}
 
 PyMethodDef g_methods[] = {CALL(decode_paged, 14),
+                           CALL(decode_tree, 16),
                            CALL(rope, 8),
                            CALL(cache_append, 13),
                            CALL(cache_read, 10),

@@ -503,6 +503,46 @@ int csa_decode_paged_q8(const void *q, const void *k_pages, const void *v_pages,
 long long csa_decode_paged_workspace_bytes(int B, int Hq, int Hkv, int d);
 
 /*
+ * csa_decode_tree - the attention of drafted tokens that the cache already holds:
+ *   the last counts[b] of sequence b's seqlens[b] tokens are nodes of a tree (or of
+ *   several, one after the other), node t at place n + t, n = seqlens[b] - counts[b].
+ *   Node t's row attends to the sink, the n tokens before the draft and the nodes on
+ *   the path from a root to t, in that order.
+ *   Defines: eq. (10)/(11) of "Continuous Softmax Attention" ("Assembly and
+ *   Simplification") for the last row of that list; with a chain (parents NULL) row t
+ *   is csa_decode_paged's of the first n + t + 1 tokens.
+ *   q: bf16 [B, Hq, T, d], the nodes' queries; out: bf16 [B, Hq, T, d]; lse: float
+ *   [B, Hq, T] or NULL.  parents: int32 [B, T], the parent of node t < counts[b],
+ *   -1 (it follows the tokens before the draft) or a node below t; NULL: t - 1 each.
+ *   counts: int32 [B], 0 <= counts[b] <= min(T, seqlens[b]); NULL: T each.  Rows
+ *   t >= counts[b] get out = 0 and lse = -inf; their q and parents do not matter.
+ *   n = 0: the sink is followed by a root (CSA_K0_COPY_FIRST: a copy of the row's own
+ *   root).  Pools, row_scales, k0, v0, block_table, scale and k0_mode as
+ *   csa_decode_paged (kind CSA_BF16, row_scales NULL) and csa_decode_paged_q8.
+ *   A count or length out of range, or a page number outside [0, P) among the ones
+ *   held, makes that sequence's out and lse NaN; a parent out of range those of the
+ *   nodes that have it on their path; both set the status word.
+ *   T at most CSA_TREE_MAX (CSA_ERR_UNSUPPORTED).  workspace: at least
+ *   csa_decode_tree_workspace_bytes(B, Hq, Hkv, T, d) bytes, 16-byte aligned, contents
+ *   on entry irrelevant; calls that can run at the same time need distinct ones.
+ *   Alignment, other refusals, and what decides the last bits as csa_decode_paged.
+ *   With more than 16 rows per cached head (T times the query heads on it) the
+ *   weights are single 16-bit numbers, as csa_forward's.
+ */
+#define CSA_TREE_MAX 64
+int csa_decode_tree(const void *q, const void *k_pages, const void *v_pages,
+                    const float *row_scales, const void *k0, const void *v0,
+                    const int *block_table, const int *seqlens, const int *parents,
+                    const int *counts, void *out, float *lse, void *workspace,
+                    long long workspace_bytes, int B, int Hq, int Hkv, int T, int P, int S, int M,
+                    int d, float scale, int k0_mode, int kind, csa_stream_t stream);
+
+/* csa_decode_tree_workspace_bytes - workspace bytes csa_decode_tree needs (host only),
+ * or -1 for a negative size, T above CSA_TREE_MAX, Hkv that does not divide Hq, or d
+ * outside {64, 128, 256}. */
+long long csa_decode_tree_workspace_bytes(int B, int Hq, int Hkv, int T, int d);
+
+/*
  * csa_rope_plan - which pairs of a row turn, by which axis of the positions
  *   and how far per position; filled by csa_rope_plan_init and passed by
  *   value into the kernels (HOST memory, not kept).
@@ -720,7 +760,6 @@ int csa_cache_copy_pages(void *k_pages, void *v_pages, long long page_bytes, int
  *   passed over and sets it.
  *   T at most CSA_TREE_MAX and P * S at most 2^31 - 1 (CSA_ERR_UNSUPPORTED).
  */
-#define CSA_TREE_MAX 64
 int csa_cache_accept(int *page_refs, int *block_table, int *seqlens, const int *parents,
                      const int *counts, const int *last, int *src, int *dst, int T, int B, int P,
                      int S, int M, csa_stream_t stream);

@@ -119,13 +119,27 @@ class DraftBooks(Books):
         return src, dst
 
 
-def bounds8(q, k, v, ref_o, ref_lse, scale):
-    """Bounds on |o - ref_o| and |lse - ref_lse| of one row over 8-bit pools: q [d], k, v [n + 1, d] with the sink's
-    pair, in 64 bits.  As paged_util.decode_bounds: logits off by (d + 8) 2^-24 A, the weight function by 2^-16.
-    Then weights as single fp16 numbers, 2^-12 relative, or 2^-25 absolute where they are below 2^-14 in units in which
-    the largest weight is 2^8 at least times its value's scale by the reference: 2^-33 of the largest value each."""
+def bounds(q, k, v, ref_o, ref_lse, scale, weights):
+    """Bounds on |o - ref_o| and |lse - ref_lse| of one row: q [d], k, v [n + 1, d] with the sink's pair, in 64 bits.
+    As paged_util.decode_bounds: logits off by (d + 8) 2^-24 A, weights by that and 2^-16 for the weight function, o by
+    twice it times max |v|.  Then `weights`, the rounding of the weights to 16 bits: it moves the numerator alone, by at
+    most that much of max |v|."""
     q, k, v = (np.asarray(t, np.float64) for t in (q, k, v))
     a = abs(scale) * (np.abs(k) @ np.abs(q)).max()
     rel = (q.size + 8) * 2.0 ** -24 * a + 2.0 ** -16
-    return (2.0 ** -8 * np.abs(ref_o) + (2 * rel + 2.0 ** -12 + len(k) * 2.0 ** -33) * np.abs(v).max(),
-            rel + 2.0 ** -22 * (1 + abs(ref_lse)))
+    return (2.0 ** -8 * np.abs(ref_o) + (2 * rel + weights) * np.abs(v).max(), rel + 2.0 ** -22 * (1 + abs(ref_lse)))
+
+
+def bounds8(q, k, v, ref_o, ref_lse, scale):
+    """The same over 8-bit pools, weights as single fp16 numbers: 2^-11 relative, or 2^-25 absolute where they are below
+    2^-14, in units in which the largest weight is 2^8 at least times its value's scale by the reference: 2^-33 of the
+    largest value each."""
+    return bounds(q, k, v, ref_o, ref_lse, scale, 2.0 ** -11 + len(k) * 2.0 ** -33)
+
+
+def bounds_tree(kind, rows, q, k, v, ref_o, ref_lse, scale):
+    """A row of a tree, `rows` = T times the query heads on a cached head: up to 16 of them weights over bf16 pools are two
+    bf16 numbers (2^-16), above one (2^-8)."""
+    if kind != "bf16":
+        return bounds8(q, k, v, ref_o, ref_lse, scale)
+    return bounds(q, k, v, ref_o, ref_lse, scale, 2.0 ** -16 if rows <= 16 else 2.0 ** -8)
