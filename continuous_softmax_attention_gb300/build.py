@@ -1,7 +1,7 @@
 """Builds libcsa.so in-tree with nvcc for sm_103a, and the CPython module
 _csa_torch (csrc/csa_torch.cpp) that calls it on torch tensors.
 
-Sixteen translation units compiled in parallel, then linked into one shared
+Nineteen translation units compiled in parallel, then linked into one shared
 library next to this file; the module is compiled beside them against torch's
 headers and linked against that library, or left out where torch was built
 without CUDA (the library and its ctypes binding do not need it).  The CUDA runtime is linked statically; the CUDA
@@ -25,7 +25,7 @@ LIB_PATH = os.path.join(HERE, "libcsa.so")
 SOURCES = ["csa_api.cu", "csa_simt.cu", "csa_tc.cu", "csa_tc_std.cu", "csa_decode.cu",
            "csa_bwd_simt.cu", "csa_tc_bwd.cu", "csa_host.cu", "csa_noalloc.cu", "csa_paged.cu",
            "csa_rope.cu", "csa_cache.cu", "csa_quant.cu", "csa_paged_e4m3.cu", "csa_paged_int8.cu",
-           "csa_tree.cu"]
+           "csa_tree.cu", "csa_rows_bf16.cu", "csa_rows_e4m3.cu", "csa_rows_int8.cu"]
 TORCH_SOURCE = "csa_torch.cpp"
 TORCH_LIB_PATH = os.path.join(HERE, "_csa_torch.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

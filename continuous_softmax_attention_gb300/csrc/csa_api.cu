@@ -336,8 +336,9 @@ int paged_check(const csa_paged_args &a, const void *workspace, long long worksp
     int rc = check_tables(a.B, a.P, a.S, a.M);
     if (rc != CSA_OK) return rc;
     if (!(d == 64 || d == 128 || d == 256) || a.S % 8 != 0) return CSA_ERR_UNSUPPORTED;
-    // tiles of 32 rows of 8 bits
+    // tiles of 32 rows of 8 bits, and for drafted tokens of 128 rows and their neighbours
     if (eight_bits(kind) && (long long)a.M * a.S > kIntMax - 31) return CSA_ERR_UNSUPPORTED;
+    if (T >= 0 && (long long)a.M * a.S > kIntMax - 255) return CSA_ERR_UNSUPPORTED;
     if ((long double)a.P * a.Hkv * a.S > kIntMax) return CSA_ERR_UNSUPPORTED;
     if ((long double)a.B * a.Hq * (T > 0 ? T : 1) > kIntMax) return CSA_ERR_UNSUPPORTED;
     *empty = (long long)a.B * a.Hq == 0 || T == 0;
@@ -793,7 +794,10 @@ int csa_device_status(void) {
     const int j = csa_paged_e4m3_take_status();
     const int k = csa_paged_int8_take_status();
     const int l = csa_tree_take_status();
-    for (const int word : {a, b, c, e, f, g, h, i, j, k, l})
+    const int m = csa_rows_bf16_take_status();
+    const int n = csa_rows_e4m3_take_status();
+    const int o = csa_rows_int8_take_status();
+    for (const int word : {a, b, c, e, f, g, h, i, j, k, l, m, n, o})
         if (word != CSA_OK) return word;
     return CSA_OK;
 }

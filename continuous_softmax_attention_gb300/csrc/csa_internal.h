@@ -132,6 +132,13 @@ long long csa_decode_tree_scratch_bytes(int B, int Hq, int Hkv, int T, int d);
 int csa_decode_tree_run(const csa_paged_args &a, const int *parents, const int *counts, int T, int d, int kind,
                         void *scratch, cudaStream_t stream);
 int csa_tree_take_status(void);
+// Its stretch before the draft with more than 16 rows per cached head (csa_rows_*.cu).
+int csa_rows_bf16_run(const csa_paged_args &a, void *scratch, int d, cudaStream_t stream);
+int csa_rows_e4m3_run(const csa_paged_args &a, void *scratch, int d, cudaStream_t stream);
+int csa_rows_int8_run(const csa_paged_args &a, void *scratch, int d, cudaStream_t stream);
+int csa_rows_bf16_take_status(void);
+int csa_rows_e4m3_take_status(void);
+int csa_rows_int8_take_status(void);
 
 // Rotary positions and the rows of new tokens into pages (csa_rope.cu).
 int csa_rope_plan_make(csa_rope_plan *plan, const int *sections, int axes, double base, int flags);

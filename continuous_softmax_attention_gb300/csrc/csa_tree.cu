@@ -21,7 +21,7 @@
 //
 // What bounds it: the first stretch (csa_paged.cuh); the second is bound by latency, a
 // few dependent trips to memory and two small products.
-#include "csa_paged.cuh"
+#include "csa_rows.cuh"
 
 namespace {
 
@@ -40,7 +40,7 @@ struct TreeParams {
     float *lse;
     const float *part_o, *part_ml;
     const int4 *joins;
-    long long whole_slot;  // of segment 0
+    int workers;           // that the parts are of
     int B, Hkv, G, T, P, S, M;
     int rows, GB, HB;      // rows of a group (G * T), blocks of them, rows per block
     int RB;                // rows per block of this kernel, at most kTreeRows
@@ -295,11 +295,11 @@ __global__ void __launch_bounds__(kTreeThreads) tree_kernel(const __grid_constan
     // the parts of the tokens before the draft
     const int4 seg = p.joins[segment];
     const bool any = n > 0;
-    if (any && (seg.x != segment || seg.y < -1 || (seg.y >= 0 && (seg.z < seg.y || seg.z >= workers(D)))))
+    if (any && (seg.x != segment || seg.y < -1 || (seg.y >= 0 && (seg.z < seg.y || seg.z >= p.workers))))
         return;  // left over, where a wait has run out and the parts are undefined
     constexpr int V = D / 32, kBatch = D == 256 ? 4 : 8;
     auto slot_of = [&](int cc) {
-        return seg.y < 0 ? (p.whole_slot + segment) * p.HB : ((long long)cc * 2 + (cc == seg.y ? seg.w : 0)) * p.HB;
+        return seg.y < 0 ? (2 * (long long)p.workers + segment) * p.HB : ((long long)cc * 2 + (cc == seg.y ? seg.w : 0)) * p.HB;
     };
     const int c0 = seg.y < 0 ? 0 : seg.y, c1 = seg.y < 0 ? 0 : seg.z;
     const int in_block = first - hb * p.HB;  // row of the parts
@@ -412,17 +412,23 @@ int launch_tree_of(TreeParams &p, int d, cudaStream_t stream) {
     return launch_tree<256, KIND>(p, stream);
 }
 
+// Rows of a cached head above which they go to the kernel of csa_rows.cuh.
+constexpr int kMany = 16;
+
 // Where the parts lie: notes, maxima and sums, unnormalised outputs.
 struct TreeScratch {
-    int GB, HB;
+    bool many;
+    int GB, HB, parts_of;  // workers that leave parts
     long long segments, slots, notes;
     TreeScratch(int B, int Hq, int Hkv, int T, int d) {
         const int rows = Hq / Hkv * T;
-        GB = head_blocks(rows);
+        many = rows > kMany;
+        GB = many ? row_blocks(rows) : head_blocks(rows);
         HB = GB ? (rows + GB - 1) / GB : 0;
+        parts_of = many ? kGrid : (int)workers(d);
         segments = (long long)B * Hkv * GB;
-        slots = 2 * workers(d) + segments;
-        notes = std::max(workers(d), segments);
+        slots = 2 * parts_of + segments;
+        notes = std::max((long long)parts_of, segments);
     }
     long long bytes(int d) const { return notes * (long long)sizeof(int4) + slots * HB * (d + 2) * (long long)sizeof(float); }
 };
@@ -440,9 +446,10 @@ int csa_decode_tree_run(const csa_paged_args &args, const int *parents, const in
     a.Hq = args.Hq * T;
     a.counts = counts;
     a.T = T;
-    const int rc = kind == CSA_BF16   ? csa_decode_paged_run(a, scratch, d, stream)
-                   : kind == CSA_E4M3 ? csa_decode_paged_e4m3_run(a, scratch, d, stream)
-                                      : csa_decode_paged_int8_run(a, scratch, d, stream);
+    auto run = kind == CSA_BF16   ? (at.many ? csa_rows_bf16_run : csa_decode_paged_run)
+               : kind == CSA_E4M3 ? (at.many ? csa_rows_e4m3_run : csa_decode_paged_e4m3_run)
+                                  : (at.many ? csa_rows_int8_run : csa_decode_paged_int8_run);
+    const int rc = run(a, scratch, d, stream);
     if (rc != CSA_OK) return rc;
     TreeParams p = {};
     p.q = static_cast<const __nv_bfloat16 *>(args.q);
@@ -460,7 +467,7 @@ int csa_decode_tree_run(const csa_paged_args &args, const int *parents, const in
     p.joins = static_cast<const int4 *>(scratch);
     p.part_ml = reinterpret_cast<const float *>(p.joins + at.notes);
     p.part_o = p.part_ml + at.slots * at.HB * 2;
-    p.whole_slot = 2 * workers(d);
+    p.workers = at.parts_of;
     p.B = args.B;
     p.Hkv = args.Hkv;
     p.G = args.Hq / args.Hkv;

@@ -522,7 +522,7 @@ long long csa_decode_paged_workspace_bytes(int B, int Hq, int Hkv, int d);
  *   A count or length out of range, or a page number outside [0, P) among the ones
  *   held, makes that sequence's out and lse NaN; a parent out of range those of the
  *   nodes that have it on their path; both set the status word.
- *   T at most CSA_TREE_MAX (CSA_ERR_UNSUPPORTED).  workspace: at least
+ *   T at most CSA_TREE_MAX and M * S at most 2^31 - 256 (CSA_ERR_UNSUPPORTED).  workspace: at least
  *   csa_decode_tree_workspace_bytes(B, Hq, Hkv, T, d) bytes, 16-byte aligned, contents
  *   on entry irrelevant; calls that can run at the same time need distinct ones.
  *   Alignment, other refusals, and what decides the last bits as csa_decode_paged.
