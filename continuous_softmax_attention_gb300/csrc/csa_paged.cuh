@@ -94,11 +94,11 @@ constexpr int kOneAtATime[4] = {152, 76, 36, 15};
 // for the long one's cluster, 0.5 us a tile, where the other form would spread
 // it: hence no more than 16.
 constexpr int kOneTiles = 16, kOneTilesLess = 4;
-// log2 units a logit may pass the running maximum by; with 8 bits the weights are fp16
-// numbers: a weight is at most 4 + 2 (a copied sink's) by it, times a value's scale of at most
-// 2 kLift by the reference
-constexpr float kRaise = 16.0f, kRaise8 = 2.0f;
-constexpr float kLift = 2048.0f;
+// log2 units a logit may pass the running maximum by.  With 8 bits the weights are fp16 numbers: 2^6 is the largest,
+// half as much more with a copied sink's, times a value's scale, which counts in kLift by the power of two at or above the
+// largest and may be twice that: 1.5 * 2^14 * 2.  Raising at 2^2 instead takes a fifth longer with 16 rows per warp.
+constexpr float kRaise = 16.0f, kRaise8 = 6.0f;
+constexpr float kLift = 128.0f;
 
 __device__ int g_paged_status;  // sticky status word of the including file's kernels
 
@@ -876,8 +876,8 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
                     most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
                     most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
                     // exponent of the power of two at or above it
-                    const uint32_t e2 = min(max((__float_as_uint(most) + 0x7fffffu) >> 23, 12u), 253u);
-                    const float to = __uint_as_float((265u - e2) << 23), f = to / lift;  // 2^(138 - e2)
+                    const uint32_t e2 = min(max((__float_as_uint(most) + 0x7fffffu) >> 23, 8u), 253u);
+                    const float to = __uint_as_float((261u - e2) << 23), f = to / lift;  // kLift 2^(127 - e2)
                     lift = to;
 #pragma unroll
                     for (int i = 0; i < ON; ++i)

@@ -35,7 +35,7 @@
 
 namespace {
 
-// TMEM: N consecutive columns of a thread's lane
+// TMEM: consecutive columns of a thread's lane
 __device__ __forceinline__ void tm_ld16(uint32_t at, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
@@ -61,6 +61,34 @@ __device__ __forceinline__ void tm_wait(uint32_t (&r)[16]) {
 __device__ __forceinline__ void tm_wait(uint32_t &a) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(a)::"memory");
 }
+__device__ __forceinline__ void tm_wait(uint32_t &a, uint32_t &b, uint32_t &c) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(a), "+r"(b), "+r"(c)::"memory");
+}
+
+// Waits of the warps beside the softmax: a thread whose phase is not complete sleeps (up to 100 us at a time) and takes
+// no issue slots from the others.
+__device__ __forceinline__ bool wait_asleep(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *status) {
+    uint64_t t0 = 0;  // the timer is slow to read: not where the phase is complete
+    while (true) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(bar), "r"(parity), "r"(100000u)
+            : "memory");
+        if (done) return true;
+        if (*abort_flag) return false;
+        if (t0 == 0) t0 = globaltimer_ns();
+        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+            *abort_flag = 1;
+            *(volatile int *)status = kStatusTimeout;
+            __threadfence();
+            return false;
+        }
+    }
+}
 
 template <int D, int KIND>
 struct RowsCfg {
@@ -68,9 +96,17 @@ struct RowsCfg {
     static constexpr int Halves = D == 256 ? 1 : 2;
     static constexpr int KT = 64 * Halves;   // cached rows per tile
     static constexpr int KR = KT + 16;       // and those of K: 8 behind, 8 before
-    static constexpr int SoftWarps = 4 * Halves, CopyWarp = SoftWarps, MmaWarp = SoftWarps + 1;
-    static constexpr int TurnWarps = Eight ? 2 : 0;
-    static constexpr int Threads = 32 * (SoftWarps + 2 + TurnWarps);
+    // warps: the softmax, the tensor core, the copies of keys and of values (which wait for different products, so each
+    // has a warp), with 8 bits the cached rows' scales (else a spare one), and the four that turn codes into fp16 numbers
+    static constexpr int SoftWarps = 4 * Halves, MmaWarp = SoftWarps, CopyWarp = SoftWarps + 1, ScaleWarp = SoftWarps + 3,
+                         TurnWarp = SoftWarps + 4;
+    static constexpr int TurnWarps = Eight ? 4 : 0;
+    static constexpr int Threads = 32 * (SoftWarps + 4 + TurnWarps);
+    // registers of the softmax warps and of the others; at launch every thread has 65536 / Threads, in eights
+    static constexpr int SoftRegs = !Eight ? (D == 256 ? 248 : 192) : D == 256 ? 248 : 160;
+    static constexpr int OtherRegs = !Eight ? 104 : D == 256 ? 120 : 96;
+    static constexpr int LaunchRegs = 65536 / Threads / 8 * 8 > 248 ? 248 : 65536 / Threads / 8 * 8;
+    static_assert(32 * SoftWarps * SoftRegs + (Threads - 32 * SoftWarps) * OtherRegs <= Threads * LaunchRegs, "the block's own registers");
     static constexpr int Boxes = D / 64;
     // operands of 16 bits: boxes of 64 columns, 128-byte swizzle
     static constexpr int QBox = 128 * 128, KBox = KR * 128, VBox = KT * 128;
@@ -83,7 +119,7 @@ struct RowsCfg {
     static constexpr int OffRing = Eight ? OffV + VBytes : QBytes;
     static constexpr int XC = D == 256 ? 16 : 32;  // columns of the sums joined at a time
     static constexpr int OffX = OffRing + Stages * StageBytes;
-    static constexpr int OffScales = OffX + 128 * Halves * (XC + 1) * 4;  // [4 tiles][KR] pairs
+    static constexpr int OffScales = OffX + 128 * Halves * XC * 4;  // [4 tiles][2][KR]
     static constexpr int Smem = OffScales + (Eight ? 4 * KR * 8 : 0) + 1024;
     static_assert(Smem <= 227 * 1024 - 4096, "one block per SM");
     // tensor memory columns
@@ -101,32 +137,48 @@ __host__ __device__ constexpr uint32_t rows_idesc(bool bf16, int N, bool b_mn_ma
            ((128u >> 4) << 24);
 }
 
-// Shares of two intervals, times (ln 2)^2: between u0 and u1 (log2 units less the maximum) with p = 2^u.
-// |X| < 1.44 (a natural step of 1): the power series of phi2, below 6e-7 relative; its even and odd parts serve both ends.
-__device__ __forceinline__ void shares(Two u0, Two u1, Two p0, Two p1, Two &left, Two &right) {
-    constexpr float l1 = kLn2, l2 = l1 * l1, l3 = l2 * l1, l4 = l2 * l2, l5 = l4 * l1, l6 = l4 * l2, l7 = l6 * l1, l8 = l4 * l4, l9 = l8 * l1;
-    const Two minus = both(-1.0f);
-    const Two X = fma2(u0, minus, u1), y = X * X;
-    Two even = fma2(both(l8 / 40320.0f), y, both(l6 / 720.0f));
-    even = fma2(even, y, both(l4 / 24.0f));
-    even = fma2(even, y, both(l2 / 2.0f));
-    Two odd = fma2(both(l9 / 362880.0f), y, both(l7 / 5040.0f));
-    odd = fma2(odd, y, both(l5 / 120.0f));
-    odd = fma2(odd, y, both(l3 / 6.0f)) * X;
-    float x0, x1;
-    apart(X, x0, x1);
-    const Two inv = two(rcp_approx(x0), rcp_approx(x1));
-    const Two sig = fma2(p0, minus, p1) * inv;
-    const Two lf = fma2(p0, both(-l1), sig) * inv, rf = fma2(sig, minus, p1 * both(l1)) * inv;
-    const Two ln = p0 * (even + odd), rn = p1 * fma2(odd, minus, even);
-    float a0, a1, b0, b1, c0, c1, d0, d1;
-    apart(lf, a0, a1);
-    apart(rf, b0, b1);
-    apart(ln, c0, c1);
-    apart(rn, d0, d1);
-    const bool near0 = fabsf(x0) < kLog2e, near1 = fabsf(x1) < kLog2e;
-    left = two(near0 ? c0 : a0, near1 ? c1 : a1);
-    right = two(near0 ? d0 : b0, near1 ? d1 : b1);
+// What 16 columns weigh, times (ln 2)^2.  u: their logits and the one behind (log2 units less the maximum); Lc: the share
+// that the interval before gives to the first, then that of the interval behind to the column behind.  first: columns
+// below it end intervals that exist.  W: pairs of columns.
+//
+// An interval from u0 to u1, X = u1 - u0, p = 2^u, has the integral S and gives R to its left and S - R to its right column:
+//   |X| >= 1/16   S ln 2 = (p1 - p0) / X,   R = ((p1 - p0) / X - p0 ln 2) / X
+//   else          S ln 2 = (p0 + p1) (ln 2) / 2 * (1 - (X ln 2)^2 / 12),   R = (ln 2)^2 (2 p0 + p1) / 6 + its share of the rest
+// as one sequence of operations with other coefficients.  S, of which the weight sum is made, is right within 2^-16.5 (the
+// exponentials' 2^-22 over X; mostly far better), the division between the two columns within 4e-4, where a weight is
+// rounded by 2^-9 (bf16) or 2^-12 (fp16) on average anyway.
+template <bool MASKED>
+__device__ __forceinline__ void weights16(const float (&u)[17], float &Lc, int columns, Two (&W)[8]) {
+    constexpr float l1 = kLn2, l2 = l1 * l1;
+    float p[17];
+#pragma unroll
+    for (int e = 0; e < 17; ++e) p[e] = ex2_approx(u[e]);
+    float before = Lc;
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) {  // intervals e and e + 1
+        const float x0 = u[e + 1] - u[e], x1 = u[e + 2] - u[e + 1];
+        const float i0 = rcp_approx(x0), i1 = rcp_approx(x1);
+        const bool s0 = fabsf(x0) < 0.0625f, s1 = fabsf(x1) < 0.0625f;
+        const Two X = two(x0, x1), P0 = two(p[e], p[e + 1]);
+        const float g0 = s0 ? 1.0f : -1.0f, g1 = s1 ? 1.0f : -1.0f;
+        const Two f1 = two(s0 ? 0.5f * l1 : i0, s1 ? 0.5f * l1 : i1), f2 = two(s0 ? l1 / 3.0f : i0, s1 ? l1 / 3.0f : i1);
+        const Two a2 = fma2(two(g0, g1), both(0.75f * l1), both(-0.25f * l1));  // (ln 2) / 2 or -ln 2
+        Two S = two(fmaf(p[e], g0, p[e + 1]), fmaf(p[e + 1], g1, p[e + 2])) * f1;
+        // 1 - (X ln 2)^2 / 12 where X is small; elsewhere the exact quotient stays
+        const Two y = X * X;
+        S = S * fma2(two(s0 ? -l2 / 12.0f : 0.0f, s1 ? -l2 / 12.0f : 0.0f), y, both(1.0f));
+        const Two R = fma2(P0, a2, S) * f2, L = fma2(S, both(l1), R * both(-1.0f));
+        float r0, r1, q0, q1;
+        apart(R, r0, r1);
+        apart(L, q0, q1);
+        if (MASKED) {
+            if (e + 1 >= columns) r0 = q0 = 0.0f;
+            if (e + 2 >= columns) r1 = q1 = 0.0f;
+        }
+        W[e / 2] = two(r0 + before, r1 + q0);
+        before = q1;
+    }
+    Lc = before;
 }
 
 template <int D, int KIND>
@@ -138,7 +190,6 @@ rows_kernel(const __grid_constant__ RowsParams rp, const __grid_constant__ CUten
     constexpr int KT = C::KT, KR = C::KR, NS = C::Stages, H = C::Halves;
     const PagedParams &p = rp.p;
     extern __shared__ uint8_t raw[];
-    __shared__ long long s_cut[C::Threads + 1];
     __shared__ __align__(8) uint64_t s_bars[4 * NS + 13];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_bad[8];
@@ -146,6 +197,8 @@ rows_kernel(const __grid_constant__ RowsParams rp, const __grid_constant__ CUten
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t base = (smem_u32(raw) + 1023) / 1024 * 1024;
     uint8_t *smem = raw + (base - smem_u32(raw));
+    long long *s_cut = reinterpret_cast<long long *>(smem + C::OffX);  // at the start only
+    static_assert((C::Threads + 1) * 8 <= 128 * C::Halves * C::XC * 4, "the cut fits");
     volatile int *abort_flag = &s_abort;
     // barriers: stages of the ring, full and empty, keys and values; then one each
     const uint32_t bars = smem_u32(s_bars);
@@ -162,14 +215,14 @@ rows_kernel(const __grid_constant__ RowsParams rp, const __grid_constant__ CUten
         for (int s = 0; s < NS; ++s) {
             mbar_init(k_full(s), 1);
             mbar_init(v_full(s), 1);
-            mbar_init(k_empty(s), EIGHT ? C::TurnWarps : 1);
+            mbar_init(k_empty(s), EIGHT ? C::TurnWarps + 1 : 1);
             mbar_init(v_empty(s), EIGHT ? C::TurnWarps : 1);
         }
         mbar_init(s_full, 1);
         mbar_init(s_empty, C::SoftWarps);
         mbar_init(q_full, C::SoftWarps);
-        mbar_init(k_ready, C::TurnWarps > 0 ? C::TurnWarps : 1);
-        mbar_init(v_ready, C::TurnWarps > 0 ? C::TurnWarps : 1);
+        mbar_init(k_ready, EIGHT ? C::TurnWarps + 1 : 1);
+        mbar_init(v_ready, EIGHT ? C::TurnWarps : 1);
         mbar_init(k_free, 1);
         mbar_init(v_free, 1);
         mbar_init(drain, 1);
@@ -197,6 +250,7 @@ rows_kernel(const __grid_constant__ RowsParams rp, const __grid_constant__ CUten
     auto wait = [&](uint32_t bar, int phase) {
         return mbar_wait_bounded(bar, phase & 1, abort_flag, &g_paged_status, kWaitLimitNs);
     };
+    auto idle = [&](uint32_t bar, int phase) { return wait_asleep(bar, phase & 1, abort_flag, &g_paged_status); };
     // the range of this CTA, by every warp for itself
     Part now;
     Cut cut;
@@ -240,6 +294,10 @@ rows_kernel(const __grid_constant__ RowsParams rp, const __grid_constant__ CUten
     auto next = [&]() { return next_part(now, cut, u0, u1, lens, KT, most, heads); };
     auto cached_head = [&](int head) { return p.GB == 1 ? head : head / p.GB; };
 
+    if (warp < C::SoftWarps)
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::SoftRegs));
+    else
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::OtherRegs));
     if (some && warp < C::SoftWarps) {
         // ---------------------------------------------------------------- softmax
         const int h = warp >> 2, i = (warp & 3) * 32 + lane;  // half, lane of tensor memory
@@ -247,7 +305,7 @@ rows_kernel(const __grid_constant__ RowsParams rp, const __grid_constant__ CUten
         const uint32_t tS = tmem + at_lane, tP = tmem + at_lane + C::ColP + 32 * h, tO = tmem + at_lane + C::ColO + D * h;
         const int R = rp.R, rep = i / R, row = i - rep * R;  // a warp has one copy
         const int CW = 64 * R / 128, c0 = 64 * h + rep * CW;  // this thread's columns
-        const float2 *ring = reinterpret_cast<const float2 *>(smem + C::OffScales);
+        const float *ring = reinterpret_cast<const float *>(smem + C::OffScales);  // [4 tiles][of keys, of values][KR]
         {  // the other copies' columns of P stay zero
             const uint32_t zero[8] = {};
             for (int j = 0; j < 4; ++j) tm_st8(tP + 8 * j, zero);
@@ -266,30 +324,38 @@ rows_kernel(const __grid_constant__ RowsParams rp, const __grid_constant__ CUten
             const int rows_h = min(p.HB, p.G - hb * p.HB);
             const long long first = (long long)b * p.Hq + hk * p.G + hb * p.HB;
             const bool mine = row < rows_h;
-            // the queries, copies side by side: this thread's half of row `row`
-            float unit = p.qscale;
+            // the queries, copies side by side: this thread's half of row `row`; of a negative scale their opposites, so
+            // that the largest product is the largest logit
+            float unit = fabsf(p.qscale);
+            const uint32_t flip = p.qscale < 0.0f ? 0x80008000u : 0u;
             {
+                constexpr int N = D / 8 / H;  // chunks of 8
                 const uint4 *qg = reinterpret_cast<const uint4 *>(p.q + (first + row) * D);
-                float up = 1.0f;
+                uint4 x[N];
+#pragma unroll
+                for (int c = 0; c < N; ++c) x[c] = mine ? qg[h * N + c] : make_uint4(0u, 0u, 0u, 0u);
                 if constexpr (EIGHT) {  // fp16 numbers, a row by the power of two that takes its largest to [2^14, 2^15)
                     uint32_t big = 0;
-                    if (mine)
-                        for (int c = 0; c < D / 8; ++c) {
-                            const uint4 x = qg[c];
-                            for (uint32_t w : {x.x, x.y, x.z, x.w}) big = max(big, max(w & 0x7fffu, (w >> 16) & 0x7fffu));
-                        }
+                    auto most = [&](const uint4 &y) {
+                        for (uint32_t w : {y.x, y.y, y.z, y.w}) big = max(big, max(w & 0x7fffu, (w >> 16) & 0x7fffu));
+                    };
+#pragma unroll
+                    for (int c = 0; c < N; ++c) most(x[c]);
+                    if (mine && H > 1)
+#pragma unroll
+                        for (int c = 0; c < N; ++c) most(qg[(1 - h) * N + c]);
                     const uint32_t e2 = min(max(big >> 7, 16u), 254u);
-                    up = __uint_as_float((268u - e2) << 23);
+                    const float up = __uint_as_float((268u - e2) << 23);
                     unit *= __uint_as_float((e2 - 14u) << 23);
+                    auto turn = [&](uint32_t w) { return pack_f16x2(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xffff0000u) * up); };
+#pragma unroll
+                    for (int c = 0; c < N; ++c) x[c] = make_uint4(turn(x[c].x), turn(x[c].y), turn(x[c].z), turn(x[c].w));
                 }
-#pragma unroll 4
-                for (int c = h * (D / 8 / H); c < (h + 1) * (D / 8 / H); ++c) {
-                    uint4 x = mine ? qg[c] : make_uint4(0u, 0u, 0u, 0u);
-                    if constexpr (EIGHT) {
-                        auto turn = [&](uint32_t w) { return pack_f16x2(__uint_as_float(w << 16) * up, __uint_as_float(w & 0xffff0000u) * up); };
-                        x = make_uint4(turn(x.x), turn(x.y), turn(x.z), turn(x.w));
-                    }
-                    *reinterpret_cast<uint4 *>(smem + C::OffQ + (c >> 3) * C::QBox + i * 128 + (((c & 7) ^ (i & 7)) << 4)) = x;
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+                    const int c = h * N + k;
+                    *reinterpret_cast<uint4 *>(smem + C::OffQ + (c >> 3) * C::QBox + i * 128 + (((c & 7) ^ (i & 7)) << 4)) =
+                        make_uint4(x[k].x ^ flip, x[k].y ^ flip, x[k].z ^ flip, x[k].w ^ flip);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -318,50 +384,91 @@ rows_kernel(const __grid_constant__ RowsParams rp, const __grid_constant__ CUten
                 tc_fence_after();
                 bad |= *(volatile int *)&s_bad[tiles & 7] != 0;
                 const int own = n - j * KT;  // rows of this tile and behind it
-                const float2 *sc = ring + (tiles & 3) * KR;
-                // a logit in log2 units
-                auto logit = [&](uint32_t x, int col) {
-                    return EIGHT ? __uint_as_float(x) * sc[col].x * unit : __uint_as_float(x) * unit;
-                };
-                // the maximum over this thread's columns and their neighbours
-                uint32_t edge;
-                float before = carry, top;
-                if (c0 > 0) {
-                    tm_ld1(tS + c0 - 1, edge);
-                    tm_wait(edge);
-                    before = logit(edge, c0 - 1);
-                } else if (j == now.tile && r0 > 0) {
-                    tm_ld1(tS + KR - 1, edge);
-                    tm_wait(edge);
-                    before = logit(edge, KR - 1);
-                }
+                const float *sk = ring + (tiles & 3) * 2 * KR, *sv = sk + KR;
                 const bool sink = j == 0 && c0 == 0, copied = sink && p.mode == CSA_K0_COPY_FIRST;
-                top = copied || (c0 > 0 && c0 - 1 >= own) ? -INFINITY : before;
-                for (int c = 0; c < CW; c += 16) {
-                    uint32_t x[16];
-                    tm_ld16(tS + c0 + c, x);
-                    tm_wait(x);
-                    float t = -INFINITY;
-                    if (c0 + CW <= own) {
+                // this thread's columns, up to 32 at a time, and their neighbours: all loads at once
+                uint32_t xa[16], xb[16], behind, edge, tail;
+                tm_ld16(tS + c0, xa);
+                if (CW >= 32) tm_ld16(tS + c0 + 16, xb);
+                tm_ld1(tS + c0 + min(CW, 32), behind);
+                tm_ld1(tS + (c0 > 0 ? c0 - 1 : KR - 1), edge);
+                tm_ld1(tS + KT - 1, tail);
+                float high = -INFINITY;  // of products
+                const bool inside = c0 + CW < own;  // every interval of this thread's exists
+                auto scaled = [&](uint32_t (&x)[16], int col) {  // 8 bits: times the cached rows' scales
+                    if constexpr (EIGHT) {
+                        const float4 *at = reinterpret_cast<const float4 *>(sk + col);
 #pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
-                            const float a = logit(x[e], c0 + c + e), a1 = logit(x[e + 1], c0 + c + e + 1);
-                            t = csa_tc::fmax3f(t, a, a1);
+                        for (int e = 0; e < 16; e += 4) {
+                            const float4 y = at[e / 4];
+                            x[e] = __float_as_uint(__uint_as_float(x[e]) * y.x);
+                            x[e + 1] = __float_as_uint(__uint_as_float(x[e + 1]) * y.y);
+                            x[e + 2] = __float_as_uint(__uint_as_float(x[e + 2]) * y.z);
+                            x[e + 3] = __float_as_uint(__uint_as_float(x[e + 3]) * y.w);
                         }
+                    }
+                };
+                auto largest = [&](const uint32_t (&x)[16], int col) {
+                    if (col + 16 <= own) {
+                        float t[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            t[e] = fmaxf(__uint_as_float(x[4 * e]), __uint_as_float(x[4 * e + 1]));
+                            t[e] = csa_tc::fmax3f(t[e], __uint_as_float(x[4 * e + 2]), __uint_as_float(x[4 * e + 3]));
+                        }
+                        high = csa_tc::fmax3f(high, csa_tc::fmax3f(t[0], t[1], t[2]), t[3]);
                     } else {
 #pragma unroll
                         for (int e = 0; e < 16; ++e)
-                            if (c0 + c + e < own) t = fmaxf(t, logit(x[e], c0 + c + e));
+                            if (col + e < own) high = fmaxf(high, __uint_as_float(x[e]));
                     }
-                    top = fmaxf(top, t);
-                    if (copied && c == 0) before = logit(x[0], 0);
+                };
+                if (CW == 64) {  // the other 32: their maximum only
+                    uint32_t ya[16], yb[16], yn;
+                    tm_ld16(tS + c0 + 32, ya);
+                    tm_ld16(tS + c0 + 48, yb);
+                    tm_ld1(tS + c0 + 64, yn);
+                    tm_wait(ya);
+                    tm_wait(yb);
+                    tm_wait(yn);
+                    scaled(ya, c0 + 32);
+                    scaled(yb, c0 + 48);
+                    largest(ya, c0 + 32);
+                    largest(yb, c0 + 48);
+                    if (EIGHT) yn = __float_as_uint(__uint_as_float(yn) * sk[c0 + 64]);
+                    if (inside) high = fmaxf(high, __uint_as_float(yn));
                 }
-                uint32_t behind;
-                tm_ld1(tS + c0 + CW, behind);
-                tm_wait(behind);
-                const float last_a = logit(behind, c0 + CW);
-                if (c0 + CW < own) top = fmaxf(top, last_a);
-                // a raised maximum: the sums of the tiles before follow it
+                tm_wait(xa);
+                if (CW >= 32) tm_wait(xb);
+                tm_wait(behind, edge, tail);
+                auto all_read = [&]() {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(s_empty);
+                };
+                if (CW < 64) all_read();
+                scaled(xa, c0);
+                largest(xa, c0);
+                if (CW >= 32) {
+                    scaled(xb, c0 + 16);
+                    largest(xb, c0 + 16);
+                }
+                if (EIGHT) {
+                    behind = __float_as_uint(__uint_as_float(behind) * sk[c0 + min(CW, 32)]);
+                    edge = __float_as_uint(__uint_as_float(edge) * sk[c0 > 0 ? c0 - 1 : KR - 1]);
+                    tail = __float_as_uint(__uint_as_float(tail) * sk[KT - 1]);
+                }
+                if (CW < 64 && inside) high = fmaxf(high, __uint_as_float(behind));
+                // the logit before the first column; the tile's last one is the next tile's
+                float before = carry;
+                if (copied)
+                    before = __uint_as_float(xa[0]) * unit;
+                else if (c0 > 0 || (j == now.tile && r0 > 0))
+                    before = __uint_as_float(edge) * unit;
+                carry = __uint_as_float(tail) * unit;
+                float top = high == -INFINITY ? high : high * unit;
+                if (c0 < own) top = fmaxf(top, before);
+                // a raised maximum, or another unit of the values: the sums of the tiles before follow
                 float f_lift = 1.0f;
                 if (EIGHT) {
                     const float to = s_lift[tiles & 3];
@@ -371,11 +478,17 @@ rows_kernel(const __grid_constant__ RowsParams rp, const __grid_constant__ CUten
                     }
                 }
                 const bool over = top > m + (EIGHT ? kRaise8 : kRaise);
-                if (j > now.tile) {  // PV of the tile before is done: P is free, and O can change
-                    if (!(ok = __all_sync(0xffffffffu, wait(o_done(h), tiles - 1)))) break;
-                    tc_fence_after();
-                }
+                bool free = j == now.tile;  // PV of the tile before is done: P can be written, and O can change
+                auto wait_free = [&]() {
+                    if (!free) {
+                        ok = __all_sync(0xffffffffu, wait(o_done(h), tiles - 1));
+                        tc_fence_after();
+                        free = true;
+                    }
+                    return ok;
+                };
                 if (__any_sync(0xffffffffu, over || f_lift != 1.0f)) {
+                    if (!wait_free()) break;
                     const float to = over ? top : m, f = m == -INFINITY ? 0.0f : ex2_approx(m - to);
                     m = to;
                     l *= f;
@@ -399,109 +512,77 @@ rows_kernel(const __grid_constant__ RowsParams rp, const __grid_constant__ CUten
                     }
                 }
                 const float nm = m == -INFINITY ? 0.0f : -m;
-                // the interval from the row before: its right share
+                // the interval from the row before
                 float Lc;
                 {
-                    uint32_t x0;
-                    tm_ld1(tS + c0, x0);
-                    tm_wait(x0);
-                    const float a = logit(x0, c0) + nm, bf = before + nm, pa = ex2_approx(a), pb = ex2_approx(bf);
-                    Two left, right;
-                    shares(both(bf), both(a), both(pb), both(pa), left, right);
-                    float lft, none;
-                    apart(left, lft, none);
-                    apart(right, Lc, none);
-                    if (c0 >= own) Lc = lft = 0.0f;
+                    float u[17];
+                    u[0] = before + nm;
+                    u[1] = fmaf(__uint_as_float(xa[0]), unit, nm);
+                    const float x = u[1] - u[0], inv = rcp_approx(x), p0 = ex2_approx(u[0]), p1 = ex2_approx(u[1]);
+                    const bool small = fabsf(x) < 0.0625f;
+                    const float g = small ? 1.0f : -1.0f, a2 = small ? 0.5f * kLn2 : -kLn2;
+                    const float S = fmaf(p0, g, p1) * (small ? 0.5f * kLn2 * fmaf(-kLn2 * kLn2 / 12.0f, x * x, 1.0f) : inv);
+                    float left = fmaf(p0, a2, S) * (small ? kLn2 / 3.0f : inv);
+                    Lc = fmaf(S, kLn2, -left);
+                    if (c0 >= own) Lc = left = 0.0f;
                     if (sink) {
-                        if (copied)
-                            Lc += lft;  // the sink's value is the first row's
-                        else
-                            w_sink = lft, l += lft;
+                        if (copied) {
+                            Lc += left;  // the sink's value is the first row's
+                        } else {
+                            w_sink = left;
+                            l += left;
+                        }
                     }
                 }
                 Two sum = both(0.0f);
-#pragma unroll 1
-                for (int c = 0; c < CW; c += 16) {
-                    uint32_t x[16], xn;
-                    tm_ld16(tS + c0 + c, x);
-                    tm_ld1(tS + c0 + c + 16, xn);
-                    tm_wait(x);
-                    tm_wait(xn);
-                    if (c + 16 == CW) {  // all of S is read
-                        if (c0 == 0) {  // the tile's last logit is the next tile's row before
-                            uint32_t y;
-                            tm_ld1(tS + KT - 1, y);
-                            tm_wait(y);
-                            carry = logit(y, KT - 1);
-                        }
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(s_empty);
-                    }
-                    float u[17], pw[17], sv[16];
-                    if constexpr (EIGHT) {
-                        const float4 *sp = reinterpret_cast<const float4 *>(sc + c0 + c);
+                auto chunk = [&](const uint32_t (&x)[16], uint32_t xn, int col, uint32_t (&pk)[8]) {
+                    float u[17];
 #pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
-                            const float4 y = sp[e / 2];
-                            u[e] = fmaf(__uint_as_float(x[e]) * y.x, unit, nm);
-                            u[e + 1] = fmaf(__uint_as_float(x[e + 1]) * y.z, unit, nm);
-                            sv[e] = y.y;
-                            sv[e + 1] = y.w;
-                        }
-                        u[16] = fmaf(__uint_as_float(xn) * sc[c0 + c + 16].x, unit, nm);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) u[e] = fmaf(__uint_as_float(x[e]), unit, nm);
-                        u[16] = fmaf(__uint_as_float(xn), unit, nm);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 17; ++e) pw[e] = ex2_approx(u[e]);
-                    const bool masked = own <= c0 + c + 16;
+                    for (int e = 0; e < 16; e += 2) apart(fma2(two(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), both(unit), both(nm)), u[e], u[e + 1]);
+                    u[16] = fmaf(__uint_as_float(xn), unit, nm);
                     Two W[8];
-                    float to_next = 0.0f, held_y = 0.0f;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {  // intervals e and e + 8
-                        Two left, right;
-                        shares(two(u[e], u[e + 8]), two(u[e + 1], u[e + 9]), two(pw[e], pw[e + 8]), two(pw[e + 1], pw[e + 9]), left, right);
-                        if (masked) {
-                            float a, d, f, g;
-                            apart(left, a, d);
-                            apart(right, f, g);
-                            if (c0 + c + e + 1 >= own) a = f = 0.0f;
-                            if (c0 + c + e + 9 >= own) d = g = 0.0f;
-                            left = two(a, d);
-                            right = two(f, g);
-                        }
-                        if (e == 0)
-                            W[0] = left;
-                        else
-                            W[e] = left + W[e];
-                        if (e < 7) {
-                            W[e + 1] = right;
-                        } else {
-                            apart(right, held_y, to_next);
-                        }
-                    }
-                    W[0] = W[0] + two(Lc, held_y);
-                    Lc = to_next;
+                    if (col + 16 < own)
+                        weights16<false>(u, Lc, 0, W);
+                    else
+                        weights16<true>(u, Lc, own - col, W);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) sum = sum + W[e];
-                    if constexpr (EIGHT) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) W[e] = W[e] * two(sv[e], sv[e + 8]);
+                    for (int e = 0; e < 8; e += 2) {
+                        if constexpr (EIGHT) {
+                            const float4 y = *reinterpret_cast<const float4 *>(sv + col + 2 * e);
+                            W[e] = W[e] * two(y.x, y.y);
+                            W[e + 1] = W[e + 1] * two(y.z, y.w);
+                        }
+                        float a, c, d, f;
+                        apart(W[e], a, c);
+                        apart(W[e + 1], d, f);
+                        pk[e] = EIGHT ? pack_f16x2(a, c) : pack_bf16x2(a, c);
+                        pk[e + 1] = EIGHT ? pack_f16x2(d, f) : pack_bf16x2(d, f);
                     }
-                    float wx[8], wy[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) apart(W[e], wx[e], wy[e]);
-                    uint32_t pk[8];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        pk[e] = EIGHT ? pack_f16x2(wx[2 * e], wx[2 * e + 1]) : pack_bf16x2(wx[2 * e], wx[2 * e + 1]);
-                        pk[4 + e] = EIGHT ? pack_f16x2(wy[2 * e], wy[2 * e + 1]) : pack_bf16x2(wy[2 * e], wy[2 * e + 1]);
+                };
+#pragma unroll 1
+                for (int c = 0; c < CW; c += 32) {
+                    if (c > 0) {
+                        tm_ld16(tS + c0 + c, xa);
+                        tm_ld16(tS + c0 + c + 16, xb);
+                        tm_ld1(tS + c0 + c + 32, behind);
+                        tm_wait(xa);
+                        tm_wait(xb);
+                        tm_wait(behind);
+                        all_read();
+                        scaled(xa, c0 + c);
+                        scaled(xb, c0 + c + 16);
+                        if (EIGHT) behind = __float_as_uint(__uint_as_float(behind) * sk[c0 + c + 32]);
                     }
+                    uint32_t pk[8], pl[8];
+                    chunk(xa, CW >= 32 ? xb[0] : behind, c0 + c, pk);
+                    if (CW >= 32) chunk(xb, behind, c0 + c + 16, pl);
+                    if (!wait_free()) break;
                     tm_st8(tP + (rep * CW + c) / 2, pk);
+                    if (CW >= 32) tm_st8(tP + (rep * CW + c) / 2 + 8, pl);
                 }
+                if (!ok) break;
                 float sx, sy;
                 apart(sum, sx, sy);
                 l += sx + sy;
@@ -530,43 +611,57 @@ rows_kernel(const __grid_constant__ RowsParams rp, const __grid_constant__ CUten
             s_m[h * 128 + i] = m;
             s_l[h * 128 + i] = bad ? NAN : l;
             if (!soft_sync()) break;
+            // the sources of a row: half s / reps, copy s mod reps
+            const int reps = 128 / R, sources = H * reps;
+            auto source = [&](int s, int r) { return (s / reps) * 128 + (s % reps) * R + r; };
             float high = -INFINITY;
-            for (int k = 0; k < H; ++k)
-                for (int c = row; c < 128; c += R) high = fmaxf(high, s_m[k * 128 + c]);
+            for (int s = 0; s < sources; ++s) high = fmaxf(high, s_m[source(s, row)]);
             constexpr float kUnit = 1.0f / (kLn2 * kLn2);
             const float f = (high == -INFINITY ? 0.0f : ex2_approx(m - high)) * kUnit, fo = EIGHT ? f / lift : f;
             const long long slot = (all_rows ? 2 * kGrid + (long long)b * heads + now.head : worker * 2 + (u0 < now.s0 ? 1 : 0)) * p.HB;
             if (tid < rows_h) {  // half 0, copy 0
                 float total = 0.0f;
-                for (int k = 0; k < H; ++k)
-                    for (int c = row; c < 128; c += R) {
-                        const float mm = s_m[k * 128 + c];
-                        total += s_l[k * 128 + c] * (mm == -INFINITY ? (isnan(s_l[k * 128 + c]) ? 1.0f : 0.0f) : ex2_approx(mm - high));
-                    }
+                for (int s = 0; s < sources; ++s) {
+                    const float mm = s_m[source(s, row)], ll = s_l[source(s, row)];
+                    // without a column: 0 or NaN
+                    total += mm == -INFINITY ? ll : ll * ex2_approx(mm - high);
+                }
                 *reinterpret_cast<float2 *>(p.part_ml + 2 * (slot + row)) = make_float2(high, total * kUnit);
             }
-            float *X = reinterpret_cast<float *>(smem + C::OffX);
+            // X: rows of XC columns, their chunks of 16 bytes permuted by the row: eight lanes meet no bank twice
+            float4 *X = reinterpret_cast<float4 *>(smem + C::OffX);
+            constexpr int E = C::XC / 4;
+            auto place = [&](int at, int e) { return at * E + (e ^ (E == 8 ? at & 7 : (at >> 1) & 3)); };
             const bool given = c0 == 0 && r0 == 0 && p.mode == CSA_K0_GIVEN;
             for (int c = 0; ok && c < D; c += C::XC) {
+                uint32_t xa[16], xb[16];
+                tm_ld16(tO + c, xa);
+                if (E == 8) tm_ld16(tO + c + 16, xb);
+                tm_wait(xa);
+                if (E == 8) tm_wait(xb);
 #pragma unroll
-                for (int k = 0; k < C::XC; k += 16) {
-                    uint32_t x[16];
-                    tm_ld16(tO + c + k, x);
-                    tm_wait(x);
+                for (int e = 0; e < E; ++e) {
+                    float y[4];
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        float y = __uint_as_float(x[e]) * fo;
-                        if (given) y = fmaf(w_sink * f, __bfloat162float(p.v0[(long long)hk * D + c + k + e]), y);
-                        X[(h * 128 + i) * (C::XC + 1) + k + e] = y;
+                    for (int k = 0; k < 4; ++k) {
+                        y[k] = __uint_as_float(e < 4 ? xa[(4 * e + k) & 15] : xb[(4 * e + k) & 15]) * fo;
+                        if (given) y[k] = fmaf(w_sink * f, __bfloat162float(p.v0[(long long)hk * D + c + 4 * e + k]), y[k]);
                     }
+                    X[place(h * 128 + i, e)] = make_float4(y[0], y[1], y[2], y[3]);
                 }
                 if (!soft_sync()) break;
-                for (int k = tid; k < rows_h * C::XC; k += 128 * H) {
-                    const int r = k / C::XC, e = k - r * C::XC;
-                    float y = 0.0f;
-                    for (int s = 0; s < H; ++s)
-                        for (int t = r; t < 128; t += R) y += X[(s * 128 + t) * (C::XC + 1) + e];
-                    p.part_o[(slot + r) * D + c + e] = y;
+                for (int k = tid; k < rows_h * E; k += 128 * H) {
+                    const int r = k / E, e = k % E;
+                    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 2
+                    for (int s = 0; s < sources; ++s) {
+                        const float4 x = X[place(source(s, r), e)];
+                        y.x += x.x;
+                        y.y += x.y;
+                        y.z += x.z;
+                        y.w += x.w;
+                    }
+                    *reinterpret_cast<float4 *>(p.part_o + (slot + r) * D + c + 4 * e) = y;
                 }
                 soft_sync();  // read, before the next columns are written
             }
@@ -579,95 +674,25 @@ rows_kernel(const __grid_constant__ RowsParams rp, const __grid_constant__ CUten
             }
             tc_fence_before();
         } while (next());
-    } else if (some && warp == C::CopyWarp) {
-        // ----------------------------------------------------------------- copies
-        const int RP = p.R, pieces = KT / RP;  // rows per copy
-        auto page_of = [&](int b, int row) {
-            const int index = row / p.S, page = p.table[(long long)b * p.M + index];
-            return page >= 0 && page < p.P ? (long long)page * p.Hkv * p.S + (row - index * p.S) : -1ll;
-        };
-        int tiles = 0;
-        bool ok = true;
-        do {
-            const int hk = cached_head(now.head);
-            for (int j = now.tile; j < now.last; ++j, ++tiles) {
-                const int stage = tiles % NS, round = tiles / NS;
-                const uint32_t at = base + C::OffRing + stage * C::StageBytes;
-                // lane i < pieces: rows of the tile; lane `pieces`: the 8 behind; the next: the 8 before
-                const int row = lane < pieces ? j * KT + lane * RP : lane == pieces ? (j + 1) * KT : j * KT - 8;
-                const bool wanted = lane < pieces + 1 ? row < now.n : lane == pieces + 1 && j == now.tile && row >= 0;
-                long long from = wanted ? page_of(now.b, row) : -1;
-                const bool lost = wanted && from < 0;
-                if (from >= 0) from += (long long)hk * p.S;
-                const bool inside = lane < pieces;
-                const int rows = inside ? RP : 8, to = inside ? lane * RP : lane == pieces ? KT : KT + 8;
-                int bytes = from >= 0 ? rows * D * (EIGHT ? 1 : 2) : 0;
-                int kb = bytes + (EIGHT && from >= 0 ? 8 * rows : 0), vb = inside ? bytes : 0;
-#pragma unroll
-                for (int off = 16; off > 0; off >>= 1) {
-                    kb += __shfl_xor_sync(0xffffffffu, kb, off);
-                    vb += __shfl_xor_sync(0xffffffffu, vb, off);
-                }
-                const bool any_lost = __any_sync(0xffffffffu, lost);
-                if (!(ok = __all_sync(0xffffffffu, wait(k_empty(stage), round + 1)))) break;
-                if (lane == 0) {
-                    *(volatile int *)&s_bad[tiles & 7] = any_lost;
-                    mbar_arrive_expect_tx(k_full(stage), kb);
-                }
-                __syncwarp();
-                if (from >= 0) {
-                    if constexpr (EIGHT) {
-                        bulk_load(at + to * D, static_cast<const uint8_t *>(p.k) + from * D, rows * D, k_full(stage));
-                        bulk_load(at + C::RawK + C::RawV + to * 8, p.scales + 2 * from, rows * 8, k_full(stage));
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < C::Boxes; ++c)
-                            tma_load_3d(at + c * C::KBox + to * 128, inside ? &map_k : &map_k8, 0, (int)from, c, k_full(stage));
-                    }
-                }
-                if (!(ok = __all_sync(0xffffffffu, wait(v_empty(stage), round + 1)))) {
-                    ++tiles;  // its keys are on their way
-                    break;
-                }
-                if (lane == 0) mbar_arrive_expect_tx(v_full(stage), vb);
-                __syncwarp();
-                if (inside && from >= 0) {
-                    if constexpr (EIGHT) {
-                        bulk_load(at + C::RawK + to * D, static_cast<const uint8_t *>(p.v) + from * D, rows * D, v_full(stage));
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < C::Boxes; ++c)
-                            tma_load_3d(at + C::KBytes + c * C::VBox + to * 128, &map_v, 0, (int)from, c, v_full(stage));
-                    }
-                }
-            }
-        } while (ok && next());
-        // the copies land before the block can end, whatever the others do
-        __syncwarp();
-        if (lane == 0)
-            for (int t = max(0, tiles - NS); t < tiles; ++t) {
-                const uint64_t began = globaltimer_ns();
-                while (!(mbar_try_wait(k_full(t % NS), (t / NS) & 1) && mbar_try_wait(v_full(t % NS), (t / NS) & 1)) &&
-                       globaltimer_ns() - began < kWaitLimitNs) {
-                }
-            }
-        __syncwarp();
     } else if (some && warp == C::MmaWarp) {
         // ------------------------------------------------------------ tensor core
         constexpr uint32_t idesc_s = rows_idesc(!EIGHT, KR, false), idesc_o = rows_idesc(!EIGHT, D, true);
         int tiles_s = 0, tiles_o = 0, parts = 0;  // products issued, parts begun
         bool ok = true;
-        const uint32_t sQ = base + C::OffQ;
+        // descriptors: an offset of n bytes is n / 16 more
+        const uint64_t q_desc = csa_tc::make_sdesc(base + C::OffQ, 16, 1024);
+        const uint64_t k_desc = csa_tc::make_sdesc(EIGHT ? base + C::OffK : base + C::OffRing, 16, 1024);
+        const uint64_t v_desc = csa_tc::make_sdesc(EIGHT ? base + C::OffV : base + C::OffRing + C::KBytes, C::VBox, 1024);
         auto issue_s = [&]() {
             const int stage = tiles_s % NS;
-            if (!wait(EIGHT ? k_ready : k_full(stage), EIGHT ? tiles_s : tiles_s / NS)) return false;
-            if (!wait(s_empty, tiles_s + 1)) return false;
+            if (!idle(EIGHT ? k_ready : k_full(stage), EIGHT ? tiles_s : tiles_s / NS)) return false;
+            if (!idle(s_empty, tiles_s + 1)) return false;
             tc_fence_after();
-            const uint32_t kb = EIGHT ? base + C::OffK : base + C::OffRing + stage * C::StageBytes;
+            const uint64_t kd = k_desc + (EIGHT ? 0 : stage * (C::StageBytes >> 4));
 #pragma unroll
             for (int k = 0; k < D / 16; ++k)
-                tc_mma_ss(tmem, csa_tc::make_sdesc(sQ + (k >> 2) * C::QBox + (k & 3) * 32, 16, 1024),
-                          csa_tc::make_sdesc(kb + (k >> 2) * C::KBox + (k & 3) * 32, 16, 1024), idesc_s, k > 0 ? 1u : 0u);
+                tc_mma_ss(tmem, q_desc + (((k >> 2) * C::QBox + (k & 3) * 32) >> 4), kd + (((k >> 2) * C::KBox + (k & 3) * 32) >> 4),
+                          idesc_s, k > 0 ? 1u : 0u);
             tc_commit(s_full);
             tc_commit(EIGHT ? k_free : k_empty(stage));
             ++tiles_s;
@@ -675,19 +700,19 @@ rows_kernel(const __grid_constant__ RowsParams rp, const __grid_constant__ CUten
         };
         do {
             if (lane == 0) {
-                ok = wait(q_full, parts) && issue_s();
+                ok = idle(q_full, parts) && issue_s();
                 for (int j = now.tile; ok && j < now.last; ++j) {
                     if (j + 1 < now.last && !(ok = issue_s())) break;
                     const int stage = tiles_o % NS;
-                    if (!(ok = wait(EIGHT ? v_ready : v_full(stage), EIGHT ? tiles_o : tiles_o / NS))) break;
-                    const uint32_t vb = EIGHT ? base + C::OffV : base + C::OffRing + stage * C::StageBytes + C::KBytes;
+                    if (!(ok = idle(EIGHT ? v_ready : v_full(stage), EIGHT ? tiles_o : tiles_o / NS))) break;
+                    const uint64_t vd = v_desc + (EIGHT ? 0 : stage * (C::StageBytes >> 4));
                     for (int h = 0; h < H && ok; ++h) {
-                        if (!(ok = wait(p_full(h), tiles_o))) break;
+                        if (!(ok = idle(p_full(h), tiles_o))) break;
                         tc_fence_after();
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             tc_mma_ts(tmem + C::ColO + D * h, tmem + C::ColP + 32 * h + 8 * k,
-                                      csa_tc::make_sdesc(vb + (64 * h + 16 * k) * 128, C::VBox, 1024), idesc_o,
+                                      vd + (((64 * h + 16 * k) * 128) >> 4), idesc_o,
                                       j > now.tile || k > 0 ? 1u : 0u);
                         tc_commit(o_done(h));
                     }
@@ -706,79 +731,185 @@ rows_kernel(const __grid_constant__ RowsParams rp, const __grid_constant__ CUten
             }
         }
         __syncwarp();
-    } else if (EIGHT && some) {
-        // ------------------------------------------- codes become fp16 numbers
+    } else if (some && (warp == C::CopyWarp || warp == C::CopyWarp + 1)) {
+        // ----------------------------------------------------------------- copies
+        const bool values = warp != C::CopyWarp;  // else keys
+        const int RP = p.R, pieces = KT / RP;     // rows per copy
+        auto full = [&](int s) { return values ? v_full(s) : k_full(s); };
+        auto empty = [&](int s) { return values ? v_empty(s) : k_empty(s); };
+        // lane i < pieces: rows of the tile; of keys lane `pieces`: the 8 behind, and, for a part's first tile, the next: the 8 before
+        const bool inside = lane < pieces;
+        const int rows = inside ? RP : 8, to = inside ? lane * RP : lane == pieces ? KT : KT + 8;
+        const int of_row = EIGHT ? D + (values ? 0 : 8) : 2 * D;
+        // a lane's rows of a tile: where they begin in the pool, -1 for none, -2 on a page out of range
+        auto look_up = [&](bool first) {
+            const int j = now.tile, row = inside ? j * KT + lane * RP : lane == pieces ? (j + 1) * KT : j * KT - 8;
+            const bool wanted = inside ? row < now.n : !values && (lane == pieces ? row < now.n : lane == pieces + 1 && first && row >= 0);
+            if (!wanted) return -1;
+            const int index = (int)__umul64hi((unsigned long long)row, p.s_inv), page = p.table[(long long)now.b * p.M + index];
+            return page >= 0 && page < p.P ? (page * p.Hkv + cached_head(now.head)) * p.S + (row - index * p.S) : -2;
+        };
+        int copied = 0;
+        bool ok = true, more = true;
+        int from = look_up(true);
+        while (more) {
+            const int stage = copied % NS, here = from;
+            const uint32_t at = base + C::OffRing + stage * C::StageBytes;
+            // the next tile's pages are asked for before this one's stage is waited for
+            const bool ends = ++now.tile == now.last;
+            if (ends) more = next();
+            if (more) from = look_up(ends);
+            if (!(ok = __all_sync(0xffffffffu, idle(empty(stage), copied / NS + 1)))) break;
+            const int bytes = __reduce_add_sync(0xffffffffu, here >= 0 ? rows * of_row : 0);
+            const bool lost = __any_sync(0xffffffffu, here == -2);
+            if (lane == 0) {
+                if (!values) *(volatile int *)&s_bad[copied & 7] = lost;
+                mbar_arrive_expect_tx(full(stage), bytes);
+            }
+            __syncwarp();
+            if (here >= 0) {
+                if constexpr (EIGHT) {
+                    const uint8_t *src = static_cast<const uint8_t *>(values ? p.v : p.k) + (long long)here * D;
+                    bulk_load(at + (values ? C::RawK : 0) + to * D, src, rows * D, full(stage));
+                    if (!values) bulk_load(at + C::RawK + C::RawV + to * 8, p.scales + 2ll * here, rows * 8, full(stage));
+                } else {
+#pragma unroll
+                    for (int c = 0; c < C::Boxes; ++c) {
+                        if (values)
+                            tma_load_3d(at + C::KBytes + c * C::VBox + to * 128, &map_v, 0, here, c, full(stage));
+                        else
+                            tma_load_3d(at + c * C::KBox + to * 128, inside ? &map_k : &map_k8, 0, here, c, full(stage));
+                    }
+                }
+            }
+            ++copied;
+        }
+        // the copies land before the block can end, whatever the others do
+        __syncwarp();
+        if (lane == 0)
+            for (int t = max(0, copied - NS); t < copied; ++t) {
+                const uint64_t began = globaltimer_ns();
+                while (!mbar_try_wait(full(t % NS), (t / NS) & 1) && globaltimer_ns() - began < kWaitLimitNs) {
+                }
+            }
+        __syncwarp();
+    } else if (EIGHT && some && warp == C::ScaleWarp) {
+        // ------------------------------------------------- the cached rows' scales
         if constexpr (EIGHT) {
-            const int t = tid - 32 * (C::SoftWarps + 2);
-            constexpr int T = 32 * C::TurnWarps, PerRow = D / 16;
-            float2 *ring = reinterpret_cast<float2 *>(smem + C::OffScales);
+            float *ring = reinterpret_cast<float *>(smem + C::OffScales);
             int tiles = 0;
             float lift = 0.0f;
             bool ok = true;
-            // 16 codes of row r, columns 16 c ..: two swizzled chunks of 16 bytes.  The odd boxes' second chunk goes
-            // first, so that eight lanes meet no bank twice.
-            auto turn = [&](const uint8_t *src, uint8_t *dst, int box_bytes, int r, int c) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(src);
-                uint4 y[2];
-                halves_of<E4M3>(x.x, y[0].x, y[0].y);
-                halves_of<E4M3>(x.y, y[0].z, y[0].w);
-                halves_of<E4M3>(x.z, y[1].x, y[1].y);
-                halves_of<E4M3>(x.w, y[1].z, y[1].w);
-                uint8_t *box = dst + (c >> 2) * box_bytes + r * 128;
-                const int k = (c >> 2) & 1;
-                *reinterpret_cast<uint4 *>(box + (((2 * (c & 3) + k) ^ (r & 7)) << 4)) = k ? y[1] : y[0];
-                *reinterpret_cast<uint4 *>(box + (((2 * (c & 3) + 1 - k) ^ (r & 7)) << 4)) = k ? y[0] : y[1];
-            };
             do {
                 for (int j = now.tile; j < now.last; ++j, ++tiles) {
-                    const int stage = tiles % NS, round = tiles / NS, own = now.n - j * KT;
-                    const uint8_t *rk = smem + C::OffRing + stage * C::StageBytes, *rv = rk + C::RawK;
-                    const float2 *rs = reinterpret_cast<const float2 *>(rv + C::RawV);
-                    if (!(ok = __all_sync(0xffffffffu, wait(k_full(stage), round) && wait(k_free, tiles + 1)))) break;
-                    // the unit of the values: see csa_paged.cuh
+                    const int stage = tiles % NS, own = now.n - j * KT;
+                    const float2 *rs = reinterpret_cast<const float2 *>(smem + C::OffRing + stage * C::StageBytes + C::RawK + C::RawV);
+                    if (!(ok = __all_sync(0xffffffffu, idle(k_full(stage), tiles / NS) && idle(k_free, tiles + 1)))) break;
+                    float2 x[(KR + 31) / 32];
                     float big = 0.0f;
-                    for (int r = lane; r < KT; r += 32)
-                        if (r < own) big = fmaxf(big, rs[r].y);
+#pragma unroll
+                    for (int i = 0; i < (KR + 31) / 32; ++i) {
+                        const int r = 32 * i + lane;
+                        x[i] = r < KR ? rs[r] : make_float2(0.0f, 0.0f);
+                        if (r < own && r < KT) big = fmaxf(big, x[i].y);
+                    }
+                    // the unit of the values: see csa_paged.cuh; a new part, a new unit
 #pragma unroll
                     for (int off = 16; off > 0; off >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
                     if (j == now.tile || big * lift > 2.0f * kLift) {
-                        const uint32_t e2 = min(max((__float_as_uint(big) + 0x7fffffu) >> 23, 12u), 253u);
-                        lift = __uint_as_float((265u - e2) << 23);
+                        const uint32_t e2 = min(max((__float_as_uint(big) + 0x7fffffu) >> 23, 8u), 253u);
+                        lift = __uint_as_float((261u - e2) << 23);
                     }
-                    for (int r = t; r < KR; r += T) {
-                        const float2 s = rs[r];
-                        ring[(tiles & 3) * KR + r] = make_float2(s.x, r < own && r < KT ? s.y * lift : 0.0f);
+                    float *to = ring + (tiles & 3) * 2 * KR;
+#pragma unroll
+                    for (int i = 0; i < (KR + 31) / 32; ++i) {
+                        const int r = 32 * i + lane;
+                        if (r < KR) {
+                            to[r] = x[i].x;
+                            to[KR + r] = r < own && r < KT ? x[i].y * lift : 0.0f;
+                        }
                     }
-                    if (t == 0) s_lift[tiles & 3] = lift;
-                    for (int k = t; k < KR * PerRow; k += T) {
-                        const int r = k / PerRow, c = k - r * PerRow;
-                        turn(rk + r * D + 16 * c, smem + C::OffK, C::KBox, r, c);
-                    }
-                    fence_proxy_async_smem();
+                    if (lane == 0) s_lift[tiles & 3] = lift;
                     __syncwarp();
                     if (lane == 0) {
                         mbar_arrive(k_ready);
                         mbar_arrive(k_empty(stage));
                     }
-                    if (!(ok = __all_sync(0xffffffffu, wait(v_full(stage), round) && wait(v_free, tiles + 1)))) break;
-                    for (int k = t; k < KT * PerRow; k += T) {
-                        const int r = k / PerRow, c = k - r * PerRow;
-                        if (r < own) {
-                            turn(rv + r * D + 16 * c, smem + C::OffV, C::VBox, r, c);
-                        } else {
-                            uint8_t *box = smem + C::OffV + (c >> 2) * C::VBox + r * 128;
-                            *reinterpret_cast<uint4 *>(box + (((2 * (c & 3)) ^ (r & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
-                            *reinterpret_cast<uint4 *>(box + (((2 * (c & 3) + 1) ^ (r & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
-                        }
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(v_ready);
-                        mbar_arrive(v_empty(stage));
-                    }
                 }
             } while (ok && next());
+        }
+    } else if (EIGHT && some && warp >= C::TurnWarp) {
+        // ------------------------------------------- codes become fp16 numbers
+        if constexpr (EIGHT) {
+            const int t = tid - 32 * C::TurnWarp;
+            constexpr int T = 32 * C::TurnWarps, PerRow = D / 16, Step = T / PerRow;
+            static_assert(Step % 8 == 0 && KT % Step == 0, "a thread has every Step-th row, alike in the swizzle");
+            // 16 codes of row r, columns 16 c ..: two swizzled chunks of 16 bytes.  The odd boxes' second chunk goes
+            // first, so that eight lanes meet no bank twice.
+            const int t0 = t / PerRow, c = t % PerRow, odd = (c >> 2) & 1;
+            const uint32_t low = ((2 * (c & 3) + odd) ^ (t0 & 7)) << 4, high = ((2 * (c & 3) + 1 - odd) ^ (t0 & 7)) << 4;
+            auto turn = [&](const uint4 &x, uint8_t *row) {
+                uint4 y[2];
+                halves_of<E4M3>(x.x, y[0].x, y[0].y);
+                halves_of<E4M3>(x.y, y[0].z, y[0].w);
+                halves_of<E4M3>(x.z, y[1].x, y[1].y);
+                halves_of<E4M3>(x.w, y[1].z, y[1].w);
+                *reinterpret_cast<uint4 *>(row + low) = odd ? y[1] : y[0];
+                *reinterpret_cast<uint4 *>(row + high) = odd ? y[0] : y[1];
+            };
+            // `rows` rows, the ones from `own` on as zeros; four of a thread's at a time
+            auto turn_rows = [&](const uint8_t *src, uint8_t *box, int rows, int own) {
+                src += t * 16;
+                box += t0 * 128;
+#pragma unroll 1
+                for (int r = t0; r < rows; r += 4 * Step, src += 4 * T * 16, box += 4 * Step * 128) {
+                    uint4 x[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        x[e] = r + e * Step < min(rows, own) ? *reinterpret_cast<const uint4 *>(src + e * T * 16) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (r + e * Step < rows) turn(x[e], box + e * Step * 128);
+                }
+            };
+            bool ok = true;
+            // keys one tile ahead of the values: the keys' buffer is free once the tile before has its logits, the values'
+            // not before its sums
+            Part ahead = now;
+            int keys = 0, values = 0;
+            bool more = true;
+            auto turn_keys = [&]() {
+                const int stage = keys % NS;
+                const uint8_t *rk = smem + C::OffRing + stage * C::StageBytes;
+                if (!(ok = __all_sync(0xffffffffu, idle(k_full(stage), keys / NS) && idle(k_free, keys + 1)))) return;
+                turn_rows(rk, smem + C::OffK + (c >> 2) * C::KBox, KR, 1 << 30);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(k_ready);
+                    mbar_arrive(k_empty(stage));
+                }
+                ++keys;
+                if (++ahead.tile == ahead.last) more = next_part(ahead, cut, u0, u1, lens, KT, most, heads);
+            };
+            turn_keys();
+            while (ok) {
+                if (more) {
+                    turn_keys();
+                    if (!ok) break;
+                }
+                const int stage = values % NS, own = now.n - now.tile * KT;
+                if (!(ok = __all_sync(0xffffffffu, idle(v_full(stage), values / NS) && idle(v_free, values + 1)))) break;
+                turn_rows(smem + C::OffRing + stage * C::StageBytes + C::RawK, smem + C::OffV + (c >> 2) * C::VBox, KT, own);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(v_ready);
+                    mbar_arrive(v_empty(stage));
+                }
+                ++values;
+                if (++now.tile == now.last && !next()) break;
+            }
         }
     }
     tc_fence_before();
@@ -805,6 +936,7 @@ int launch_rows(RowsParams &rp, cudaStream_t stream) {
     PagedParams &p = rp.p;
     p.R = C::KT;
     while (p.S % p.R != 0) p.R /= 2;  // S is a multiple of 8
+    p.s_inv = ~0ull / p.S + 1;
     CUtensorMap maps[3] = {};
     if (!C::Eight) {
         const long long rows = (long long)p.P * p.Hkv * p.S;
@@ -815,7 +947,13 @@ int launch_rows(RowsParams &rp, cudaStream_t stream) {
     const long long tiles = (long long)p.B * p.Hkv * p.GB * (((long long)p.M * p.S + C::KT - 1) / C::KT);
     const int grid = (int)(tiles < kGrid ? (tiles < 1 ? 1 : tiles) : kGrid);
     auto kern = rows_kernel<D, KIND>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::Smem) != cudaSuccess ||
+    // the shares of the registers come out of those that the block is launched with
+    static const bool fits = [&] {
+        cudaFuncAttributes attr;
+        return cudaFuncGetAttributes(&attr, kern) == cudaSuccess &&
+               32 * C::SoftWarps * C::SoftRegs + (C::Threads - 32 * C::SoftWarps) * C::OtherRegs <= C::Threads * attr.numRegs;
+    }();
+    if (!fits || cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::Smem) != cudaSuccess ||
         launch_after_previous(kern, grid, C::Threads, C::Smem, stream, rp, maps[0], maps[1], maps[2]) != cudaSuccess)
         return CSA_ERR_CUDA;
     return CSA_OK;
@@ -835,8 +973,8 @@ int run_rows(const csa_paged_args &a, void *scratch, int d, cudaStream_t stream)
     rp.R = p.HB <= 32 ? 32 : p.HB <= 64 ? 64 : 128;
     const long long segments = (long long)p.B * p.Hkv * p.GB;
     p.joins = static_cast<int4 *>(scratch);
-    p.part_ml = reinterpret_cast<float *>(p.joins + std::max((long long)kGrid, segments));
-    p.part_o = p.part_ml + (2 * kGrid + segments) * p.HB * 2;
+    p.part_o = reinterpret_cast<float *>(p.joins + std::max((long long)kGrid, segments));  // 16-byte aligned
+    p.part_ml = p.part_o + (2 * kGrid + segments) * p.HB * d;
     if (d == 64) return launch_rows<64, KIND>(rp, stream);
     if (d == 128) return launch_rows<128, KIND>(rp, stream);
     return launch_rows<256, KIND>(rp, stream);

@@ -27,8 +27,7 @@ namespace {
 
 constexpr int kTreeThreads = 256, kTreeWarps = kTreeThreads / 32;
 constexpr int kTreeRows = 16;       // rows of a block's products
-constexpr int kCols = 72, kDeep = 80;  // T + 1 positions, to whole columns and products
-constexpr int kPitch = kDeep + 4;   // of the weights, in elements
+constexpr int kDeep = 80;           // T + 1 positions at most, to whole products
 
 struct TreeParams {
     const __nv_bfloat16 *q;
@@ -48,14 +47,22 @@ struct TreeParams {
     int mode;
 };
 
+// Shared memory, by the positions that T asks for: few drafted tokens leave room for more blocks per SM.
 template <int D>
 struct TreeSmem {
     static constexpr int Row = 2 * D + 16;  // bytes of a cached row: 16 more, so that eight rows meet no bank twice
-    static constexpr int K = 0, V = K + kCols * Row, S = V + kDeep * Row;
-    static constexpr int W = S + kTreeRows * kPitch * 4, Left = W + kTreeRows * kPitch * 4;
-    static constexpr int Parts = Left + kTreeRows * kPitch * 4;  // [warps][D + 2] of a row's parts
-    static constexpr int Bytes = Parts + kTreeWarps * (D + 2) * 4;
-    static_assert(K % 16 == 0 && V % 16 == 0 && S % 16 == 0 && Row % 16 == 0, "16-byte rows");
+    int deep, pitch, S, W, Left, Parts, bytes;  // positions; pitch of the weights in elements; offsets
+    __host__ __device__ explicit TreeSmem(int T) {
+        deep = (T + 16) / 16 * 16;
+        pitch = deep + 4;
+        S = 2 * deep * Row;  // behind the keys and the values
+        W = S + kTreeRows * pitch * 4;
+        Left = W + kTreeRows * pitch * 4;
+        Parts = Left + kTreeRows * pitch * 4;  // [warps][D + 2] of a row's parts
+        bytes = Parts + kTreeWarps * (D + 2) * 4;
+        // the sums over the drafted tokens take the keys' place, if they fit
+        if (deep * Row < kTreeRows * D * 4) bytes += kTreeRows * D * 4;
+    }
 };
 
 // Eight values as bf16 numbers, exact for the codes of either 8-bit kind.
@@ -77,16 +84,18 @@ __device__ __forceinline__ bool any_not_finite(const uint4 &x) {
 }
 
 template <int D, int KIND>
-__global__ void __launch_bounds__(kTreeThreads) tree_kernel(const __grid_constant__ TreeParams p) {
-    using L = TreeSmem<D>;
+__global__ void __launch_bounds__(kTreeThreads, 4) tree_kernel(const __grid_constant__ TreeParams p) {
+    constexpr int Row = TreeSmem<D>::Row;
+    const TreeSmem<D> L(p.T);
+    const int deep = L.deep, kPitch = L.pitch, kV = deep * Row;  // the values behind the keys
     extern __shared__ __align__(16) uint8_t raw[];
     __shared__ unsigned long long s_path[64];
     __shared__ int s_jump[64], s_up[64];
     __shared__ unsigned long long s_bad;  // nodes whose parent is out of range
     __shared__ int s_page, s_wild;        // a page out of range; values that are not finite
     __shared__ float s_sk[kDeep], s_sv[kDeep], s_m[kTreeRows], s_l[kTreeRows], s_pm[kTreeWarps], s_pl[kTreeWarps];
-    float *S = reinterpret_cast<float *>(raw + L::S), *W = reinterpret_cast<float *>(raw + L::W),
-          *Lf = reinterpret_cast<float *>(raw + L::Left), *sums = reinterpret_cast<float *>(raw + L::Parts);
+    float *S = reinterpret_cast<float *>(raw + L.S), *W = reinterpret_cast<float *>(raw + L.W),
+          *Lf = reinterpret_cast<float *>(raw + L.Left), *sums = reinterpret_cast<float *>(raw + L.Parts);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q = lane & 3;
     const int segment = blockIdx.x, heads = p.Hkv * p.GB;
     const int b = segment / heads, head = segment - b * heads, hk = head / p.GB, hb = head - hk * p.GB;
@@ -123,7 +132,7 @@ __global__ void __launch_bounds__(kTreeThreads) tree_kernel(const __grid_constan
     }
     // the cached rows: position 0 is the last one before the draft, 1 + u is drafted token u
     const int have = sound ? c + 1 : 0;
-    for (int i = tid; i < kDeep * (D / 8); i += kTreeThreads) {
+    for (int i = tid; i < deep * (D / 8); i += kTreeThreads) {
         const int j = i / (D / 8), col = (i - j * (D / 8)) * 8;
         uint4 xk = make_uint4(0u, 0u, 0u, 0u), xv = xk;
         if (j < have) {
@@ -152,8 +161,8 @@ __global__ void __launch_bounds__(kTreeThreads) tree_kernel(const __grid_constan
         } else if (col == 0) {
             s_sk[j] = s_sv[j] = 0.0f;
         }
-        if (j < kCols) *reinterpret_cast<uint4 *>(raw + L::K + j * L::Row + col * 2) = xk;
-        *reinterpret_cast<uint4 *>(raw + L::V + j * L::Row + col * 2) = xv;
+        *reinterpret_cast<uint4 *>(raw + j * Row + col * 2) = xk;
+        *reinterpret_cast<uint4 *>(raw + kV + j * Row + col * 2) = xv;
     }
     __syncthreads();
     if (!sound || s_page) {
@@ -167,7 +176,7 @@ __global__ void __launch_bounds__(kTreeThreads) tree_kernel(const __grid_constan
     for (int t = warp; t < (have + 7) / 8; t += kTreeWarps) {
         float acc[4] = {0.f, 0.f, 0.f, 0.f}, acc2[4] = {0.f, 0.f, 0.f, 0.f};
         const uint32_t *q0 = reinterpret_cast<const uint32_t *>(p.q + (out0 + g) * D), *q1 = q0 + 4 * D;
-        const uint32_t *kr = reinterpret_cast<const uint32_t *>(raw + L::K + (8 * t + g) * L::Row);
+        const uint32_t *kr = reinterpret_cast<const uint32_t *>(raw + (8 * t + g) * Row);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
             const uint32_t a[4] = {g < rows ? q0[i * 8 + q] : 0u, g + 8 < rows ? q1[i * 8 + q] : 0u,
@@ -186,7 +195,7 @@ __global__ void __launch_bounds__(kTreeThreads) tree_kernel(const __grid_constan
         float *s = S + r * kPitch, *w = W + r * kPitch, *lf = Lf + r * kPitch;
         const int t = (first + r) % p.T;
         if (r >= rows || t >= c) {
-            for (int j = lane; j < kDeep; j += 32) w[j] = 0.0f;
+            for (int j = lane; j < deep; j += 32) w[j] = 0.0f;
             continue;
         }
         const unsigned long long path = s_path[t];
@@ -203,7 +212,7 @@ __global__ void __launch_bounds__(kTreeThreads) tree_kernel(const __grid_constan
             if (j > 64) in[i] = false;
             a[i] = in[i] ? s[j] : -INFINITY;
             m = fmaxf(m, a[i]);
-            if (j < kDeep) w[j] = lf[j] = 0.0f;
+            if (j < deep) w[j] = lf[j] = 0.0f;
         }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
@@ -253,8 +262,8 @@ __global__ void __launch_bounds__(kTreeThreads) tree_kernel(const __grid_constan
     float o[CW / 8][4] = {};
     if (!s_wild) {
         const int col0 = warp * CW;
-#pragma unroll
-        for (int ks = 0; ks < kDeep / 16; ++ks) {
+#pragma unroll 1
+        for (int ks = 0; ks < (have + 15) / 16; ++ks) {
             uint32_t hi[4], lo[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -265,15 +274,16 @@ __global__ void __launch_bounds__(kTreeThreads) tree_kernel(const __grid_constan
 #pragma unroll
             for (int i = 0; i < CW / 8; ++i) {
                 // rows 16 ks + 2 q (+ 1, + 8, + 9) of column col0 + 8 i + g
-                const uint16_t *at = reinterpret_cast<const uint16_t *>(raw + L::V + (16 * ks + 2 * q) * L::Row) + col0 + 8 * i + g;
-                const uint32_t b0 = at[0] | (uint32_t)at[L::Row / 2] << 16, b1 = at[8 * (L::Row / 2)] | (uint32_t)at[9 * (L::Row / 2)] << 16;
+                const uint16_t *at = reinterpret_cast<const uint16_t *>(raw + kV + (16 * ks + 2 * q) * Row) + col0 + 8 * i + g;
+                const uint32_t b0 = at[0] | (uint32_t)at[Row / 2] << 16, b1 = at[8 * (Row / 2)] | (uint32_t)at[9 * (Row / 2)] << 16;
                 mma(o[i], hi, b0, b1);
                 mma(o[i], lo, b0, b1);
             }
         }
     }
     __syncthreads();
-    float *Od = reinterpret_cast<float *>(raw + L::K);  // [kTreeRows][D], over the keys
+    // [kTreeRows][D]: over the keys, or behind everything where they are fewer
+    float *Od = reinterpret_cast<float *>(raw + (deep * Row < kTreeRows * D * 4 ? L.bytes - kTreeRows * D * 4 : 0));
     if (!s_wild) {
 #pragma unroll
         for (int i = 0; i < CW / 8; ++i)
@@ -286,7 +296,7 @@ __global__ void __launch_bounds__(kTreeThreads) tree_kernel(const __grid_constan
             float sum = 0.0f;
             for (int j = 0; j < have; ++j)
                 if (j == 0 ? W[r * kPitch] != 0.0f : path >> (j - 1) & 1)
-                    sum = fmaf(W[r * kPitch + j], __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t *>(raw + L::V + j * L::Row + col * 2) << 16), sum);
+                    sum = fmaf(W[r * kPitch + j], __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t *>(raw + kV + j * Row + col * 2) << 16), sum);
             Od[r * D + col] = sum;
         }
     }
@@ -297,7 +307,7 @@ __global__ void __launch_bounds__(kTreeThreads) tree_kernel(const __grid_constan
     const bool any = n > 0;
     if (any && (seg.x != segment || seg.y < -1 || (seg.y >= 0 && (seg.z < seg.y || seg.z >= p.workers))))
         return;  // left over, where a wait has run out and the parts are undefined
-    constexpr int V = D / 32, kBatch = D == 256 ? 4 : 8;
+    constexpr int V = D / 32, kBatch = D == 256 ? 2 : 4;
     auto slot_of = [&](int cc) {
         return seg.y < 0 ? (2 * (long long)p.workers + segment) * p.HB : ((long long)cc * 2 + (cc == seg.y ? seg.w : 0)) * p.HB;
     };
@@ -395,14 +405,15 @@ __global__ void __launch_bounds__(kTreeThreads) tree_kernel(const __grid_constan
 template <int D, int KIND>
 int launch_tree(TreeParams &p, cudaStream_t stream) {
     auto kern = tree_kernel<D, KIND>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TreeSmem<D>::Bytes) != cudaSuccess)
+    const int smem = TreeSmem<D>(p.T).bytes;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TreeSmem<D>(64).bytes) != cudaSuccess)
         return CSA_ERR_CUDA;
     // fewer rows per block where a segment has many parts
     const long long segments = (long long)p.B * p.Hkv * p.GB;
     p.RB = kTreeRows;
     while (p.RB > 1 && segments * ((p.HB + p.RB - 1) / p.RB) < kGrid) p.RB /= 2;
     const dim3 grid((unsigned)segments, (unsigned)((p.HB + p.RB - 1) / p.RB));
-    return launch_after_previous(kern, grid, kTreeThreads, TreeSmem<D>::Bytes, stream, p) == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
+    return launch_after_previous(kern, grid, kTreeThreads, smem, stream, p) == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
 }
 
 template <int KIND>
@@ -465,8 +476,9 @@ int csa_decode_tree_run(const csa_paged_args &args, const int *parents, const in
     p.out = static_cast<__nv_bfloat16 *>(args.out);
     p.lse = args.lse;
     p.joins = static_cast<const int4 *>(scratch);
-    p.part_ml = reinterpret_cast<const float *>(p.joins + at.notes);
-    p.part_o = p.part_ml + at.slots * at.HB * 2;
+    const float *parts = reinterpret_cast<const float *>(p.joins + at.notes);
+    p.part_o = at.many ? parts : parts + at.slots * at.HB * 2;
+    p.part_ml = at.many ? parts + at.slots * at.HB * d : parts;
     p.workers = at.parts_of;
     p.B = args.B;
     p.Hkv = args.Hkv;

@@ -132,14 +132,21 @@ def bounds(q, k, v, ref_o, ref_lse, scale, weights):
 
 def bounds8(q, k, v, ref_o, ref_lse, scale):
     """The same over 8-bit pools, weights as single fp16 numbers: 2^-11 relative, or 2^-25 absolute where they are below
-    2^-14, in units in which the largest weight is 2^8 at least times its value's scale by the reference: 2^-33 of the
-    largest value each."""
-    return bounds(q, k, v, ref_o, ref_lse, scale, 2.0 ** -11 + len(k) * 2.0 ** -33)
+    2^-14.  They are weights times a value's scale by a power of two (at most twice the largest scale) times 2^7, so the
+    absolute part moves o by at most 2^-32 of 448 * twice the largest scale per row, over the sum of the weights.  448 scales
+    are at most 4 max |v| here, and the weight of the largest logit alone is at least 2^-4 for steps below 16: 2^-26 max |v|
+    for each row."""
+    return bounds(q, k, v, ref_o, ref_lse, scale, 2.0 ** -11 + len(k) * 2.0 ** -26)
 
 
 def bounds_tree(kind, rows, q, k, v, ref_o, ref_lse, scale):
-    """A row of a tree, `rows` = T times the query heads on a cached head: up to 16 of them weights over bf16 pools are two
-    bf16 numbers (2^-16), above one (2^-8)."""
+    """A row of a tree, `rows` = T times the query heads on a cached head.  Up to 16 of them: weights over bf16 pools are
+    two bf16 numbers (2^-16), over 8-bit ones as bounds8.  Above: one bf16 (2^-8) or fp16 number, and an interval's integral
+    is divided between its two rows within 4e-4 < 2^-11 of the smaller share (the error of the quotients is relative
+    to the left share, and the right one is the rest): that moves the numerator by at most 4e-4 times the share times the
+    difference of two values, in all by at most 2 * 4e-4 / 2 max |v|, since the smaller shares are at most half of the sum."""
     if kind != "bf16":
-        return bounds8(q, k, v, ref_o, ref_lse, scale)
-    return bounds(q, k, v, ref_o, ref_lse, scale, 2.0 ** -16 if rows <= 16 else 2.0 ** -8)
+        if rows <= 16:
+            return bounds8(q, k, v, ref_o, ref_lse, scale)
+        return bounds(q, k, v, ref_o, ref_lse, scale, 2.0 ** -10 + len(k) * 2.0 ** -26)
+    return bounds(q, k, v, ref_o, ref_lse, scale, 2.0 ** -16 if rows <= 16 else 2.0 ** -8 + 2.0 ** -11)
