@@ -96,7 +96,7 @@ constexpr int kOneAtATime[4] = {152, 76, 36, 15};
 constexpr int kOneTiles = 16, kOneTilesLess = 4;
 // log2 units a logit may pass the running maximum by.  With 8 bits the weights are fp16 numbers: 2^6 is the largest,
 // half as much more with a copied sink's, times a value's scale, which counts in kLift by the power of two at or above the
-// largest and may be twice that: 1.5 * 2^14 * 2.  Raising at 2^2 instead takes a fifth longer with 16 rows per warp.
+// largest and may be twice that: 1.5 * 2^14 * 2.
 constexpr float kRaise = 16.0f, kRaise8 = 6.0f;
 constexpr float kLift = 128.0f;
 

@@ -31,6 +31,8 @@
 // (2^-11) over 8-bit ones.  All carry the factor (ln 2)^2, removed where parts are written.
 #pragma once
 
+#include <type_traits>
+
 #include "csa_paged.cuh"
 
 namespace {
@@ -90,6 +92,32 @@ __device__ __forceinline__ bool wait_asleep(uint32_t bar, uint32_t parity, volat
     }
 }
 
+// The tensor core's lane asks again and again: woken from a wait with a time hint it would begin 200 cycles later, three
+// times a tile.
+__device__ __forceinline__ bool wait_awake(uint32_t bar, uint32_t parity, volatile int *abort_flag, int *status) {
+    uint64_t t0 = 0;
+    for (int i = 0;; ++i) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (done) return true;
+        if ((i & 63) != 63) continue;
+        if (*abort_flag) return false;
+        if (t0 == 0) t0 = globaltimer_ns();
+        if (globaltimer_ns() - t0 > kWaitLimitNs) {
+            *abort_flag = 1;
+            *(volatile int *)status = kStatusTimeout;
+            __threadfence();
+            return false;
+        }
+    }
+}
+
 template <int D, int KIND>
 struct RowsCfg {
     static constexpr bool Eight = KIND != CSA_BF16;
@@ -103,8 +131,8 @@ struct RowsCfg {
     static constexpr int TurnWarps = Eight ? 4 : 0;
     static constexpr int Threads = 32 * (SoftWarps + 4 + TurnWarps);
     // registers of the softmax warps and of the others; at launch every thread has 65536 / Threads, in eights
-    static constexpr int SoftRegs = !Eight ? (D == 256 ? 248 : 192) : D == 256 ? 248 : 160;
-    static constexpr int OtherRegs = !Eight ? 104 : D == 256 ? 120 : 96;
+    static constexpr int SoftRegs = !Eight ? (D == 256 ? 248 : 192) : D == 256 ? 248 : 152;
+    static constexpr int OtherRegs = !Eight ? 104 : D == 256 ? 120 : 104;
     static constexpr int LaunchRegs = 65536 / Threads / 8 * 8 > 248 ? 248 : 65536 / Threads / 8 * 8;
     static_assert(32 * SoftWarps * SoftRegs + (Threads - 32 * SoftWarps) * OtherRegs <= Threads * LaunchRegs, "the block's own registers");
     static constexpr int Boxes = D / 64;
@@ -125,11 +153,6 @@ struct RowsCfg {
     // tensor memory columns
     static constexpr int ColP = KR, ColO = KR + 32 * Halves;
     static_assert(ColO + D * Halves <= 512, "tensor memory");
-};
-
-struct RowsParams {
-    PagedParams p;
-    int R;     // rows of a copy: 32, 64 or 128
 };
 
 __host__ __device__ constexpr uint32_t rows_idesc(bool bf16, int N, bool b_mn_major) {
@@ -181,14 +204,14 @@ __device__ __forceinline__ void weights16(const float (&u)[17], float &Lc, int c
     Lc = before;
 }
 
-template <int D, int KIND>
+// CW: a thread's columns of a half: 64 for 128 rows, 32 for two copies of 64, 16 for four of 32.
+template <int D, int KIND, int CW>
 __global__ void __launch_bounds__(RowsCfg<D, KIND>::Threads, 1)
-rows_kernel(const __grid_constant__ RowsParams rp, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+rows_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
             const __grid_constant__ CUtensorMap map_k8) {
     using C = RowsCfg<D, KIND>;
     constexpr bool EIGHT = C::Eight, E4M3 = KIND == CSA_E4M3;
-    constexpr int KT = C::KT, KR = C::KR, NS = C::Stages, H = C::Halves;
-    const PagedParams &p = rp.p;
+    constexpr int KT = C::KT, KR = C::KR, NS = C::Stages, H = C::Halves, R = 2 * CW;
     extern __shared__ uint8_t raw[];
     __shared__ __align__(8) uint64_t s_bars[4 * NS + 13];
     __shared__ uint32_t s_tmem;
@@ -250,6 +273,7 @@ rows_kernel(const __grid_constant__ RowsParams rp, const __grid_constant__ CUten
     auto wait = [&](uint32_t bar, int phase) {
         return mbar_wait_bounded(bar, phase & 1, abort_flag, &g_paged_status, kWaitLimitNs);
     };
+    auto awake = [&](uint32_t bar, int phase) { return wait_awake(bar, phase & 1, abort_flag, &g_paged_status); };
     auto idle = [&](uint32_t bar, int phase) { return wait_asleep(bar, phase & 1, abort_flag, &g_paged_status); };
     // the range of this CTA, by every warp for itself
     Part now;
@@ -303,8 +327,8 @@ rows_kernel(const __grid_constant__ RowsParams rp, const __grid_constant__ CUten
         const int h = warp >> 2, i = (warp & 3) * 32 + lane;  // half, lane of tensor memory
         const uint32_t at_lane = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + at_lane, tP = tmem + at_lane + C::ColP + 32 * h, tO = tmem + at_lane + C::ColO + D * h;
-        const int R = rp.R, rep = i / R, row = i - rep * R;  // a warp has one copy
-        const int CW = 64 * R / 128, c0 = 64 * h + rep * CW;  // this thread's columns
+        const int rep = i / R, row = i - rep * R;  // a warp has one copy
+        const int c0 = 64 * h + rep * CW;          // this thread's columns
         const float *ring = reinterpret_cast<const float *>(smem + C::OffScales);  // [4 tiles][of keys, of values][KR]
         {  // the other copies' columns of P stay zero
             const uint32_t zero[8] = {};
@@ -379,8 +403,10 @@ rows_kernel(const __grid_constant__ RowsParams rp, const __grid_constant__ CUten
                 carry = sum * p.qscale;
             }
             bool bad = false;
-            for (int j = now.tile; j < now.last; ++j, ++tiles) {
-                if (!(ok = __all_sync(0xffffffffu, wait(s_full, tiles)))) break;
+            // a tile; false: give up.  MASKED: not all of its intervals exist.
+            auto tile = [&](int j, auto masked) -> bool {
+                constexpr bool MASKED = decltype(masked)::value;
+                if (!(ok = __all_sync(0xffffffffu, wait(s_full, tiles)))) return false;
                 tc_fence_after();
                 bad |= *(volatile int *)&s_bad[tiles & 7] != 0;
                 const int own = n - j * KT;  // rows of this tile and behind it
@@ -388,13 +414,15 @@ rows_kernel(const __grid_constant__ RowsParams rp, const __grid_constant__ CUten
                 const bool sink = j == 0 && c0 == 0, copied = sink && p.mode == CSA_K0_COPY_FIRST;
                 // this thread's columns, up to 32 at a time, and their neighbours: all loads at once
                 uint32_t xa[16], xb[16], behind, edge, tail;
-                tm_ld16(tS + c0, xa);
-                if (CW >= 32) tm_ld16(tS + c0 + 16, xb);
-                tm_ld1(tS + c0 + min(CW, 32), behind);
-                tm_ld1(tS + (c0 > 0 ? c0 - 1 : KR - 1), edge);
-                tm_ld1(tS + KT - 1, tail);
+                auto load = [&]() {
+                    tm_ld16(tS + c0, xa);
+                    if (CW >= 32) tm_ld16(tS + c0 + 16, xb);
+                    tm_ld1(tS + c0 + (CW < 32 ? CW : 32), behind);
+                    tm_ld1(tS + (c0 > 0 ? c0 - 1 : KR - 1), edge);
+                    tm_ld1(tS + KT - 1, tail);
+                };
+                if (!(EIGHT && CW == 64)) load();  // those have no registers for 64 columns
                 float high = -INFINITY;  // of products
-                const bool inside = c0 + CW < own;  // every interval of this thread's exists
                 auto scaled = [&](uint32_t (&x)[16], int col) {  // 8 bits: times the cached rows' scales
                     if constexpr (EIGHT) {
                         const float4 *at = reinterpret_cast<const float4 *>(sk + col);
@@ -409,7 +437,7 @@ rows_kernel(const __grid_constant__ RowsParams rp, const __grid_constant__ CUten
                     }
                 };
                 auto largest = [&](const uint32_t (&x)[16], int col) {
-                    if (col + 16 <= own) {
+                    if (!MASKED || col + 16 <= own) {
                         float t[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -423,7 +451,7 @@ rows_kernel(const __grid_constant__ RowsParams rp, const __grid_constant__ CUten
                             if (col + e < own) high = fmaxf(high, __uint_as_float(x[e]));
                     }
                 };
-                if (CW == 64) {  // the other 32: their maximum only
+                if constexpr (CW == 64) {  // the other 32: their maximum only
                     uint32_t ya[16], yb[16], yn;
                     tm_ld16(tS + c0 + 32, ya);
                     tm_ld16(tS + c0 + 48, yb);
@@ -436,8 +464,9 @@ rows_kernel(const __grid_constant__ RowsParams rp, const __grid_constant__ CUten
                     largest(ya, c0 + 32);
                     largest(yb, c0 + 48);
                     if (EIGHT) yn = __float_as_uint(__uint_as_float(yn) * sk[c0 + 64]);
-                    if (inside) high = fmaxf(high, __uint_as_float(yn));
+                    if (!MASKED || c0 + CW < own) high = fmaxf(high, __uint_as_float(yn));
                 }
+                if (EIGHT && CW == 64) load();
                 tm_wait(xa);
                 if (CW >= 32) tm_wait(xb);
                 tm_wait(behind, edge, tail);
@@ -454,11 +483,11 @@ rows_kernel(const __grid_constant__ RowsParams rp, const __grid_constant__ CUten
                     largest(xb, c0 + 16);
                 }
                 if (EIGHT) {
-                    behind = __float_as_uint(__uint_as_float(behind) * sk[c0 + min(CW, 32)]);
+                    behind = __float_as_uint(__uint_as_float(behind) * sk[c0 + (CW < 32 ? CW : 32)]);
                     edge = __float_as_uint(__uint_as_float(edge) * sk[c0 > 0 ? c0 - 1 : KR - 1]);
                     tail = __float_as_uint(__uint_as_float(tail) * sk[KT - 1]);
                 }
-                if (CW < 64 && inside) high = fmaxf(high, __uint_as_float(behind));
+                if (CW < 64 && (!MASKED || c0 + CW < own)) high = fmaxf(high, __uint_as_float(behind));
                 // the logit before the first column; the tile's last one is the next tile's
                 float before = carry;
                 if (copied)
@@ -467,7 +496,7 @@ rows_kernel(const __grid_constant__ RowsParams rp, const __grid_constant__ CUten
                     before = __uint_as_float(edge) * unit;
                 carry = __uint_as_float(tail) * unit;
                 float top = high == -INFINITY ? high : high * unit;
-                if (c0 < own) top = fmaxf(top, before);
+                if (!MASKED || c0 < own) top = fmaxf(top, before);
                 // a raised maximum, or another unit of the values: the sums of the tiles before follow
                 float f_lift = 1.0f;
                 if (EIGHT) {
@@ -488,7 +517,7 @@ rows_kernel(const __grid_constant__ RowsParams rp, const __grid_constant__ CUten
                     return ok;
                 };
                 if (__any_sync(0xffffffffu, over || f_lift != 1.0f)) {
-                    if (!wait_free()) break;
+                    if (!wait_free()) return false;
                     const float to = over ? top : m, f = m == -INFINITY ? 0.0f : ex2_approx(m - to);
                     m = to;
                     l *= f;
@@ -524,7 +553,7 @@ rows_kernel(const __grid_constant__ RowsParams rp, const __grid_constant__ CUten
                     const float S = fmaf(p0, g, p1) * (small ? 0.5f * kLn2 * fmaf(-kLn2 * kLn2 / 12.0f, x * x, 1.0f) : inv);
                     float left = fmaf(p0, a2, S) * (small ? kLn2 / 3.0f : inv);
                     Lc = fmaf(S, kLn2, -left);
-                    if (c0 >= own) Lc = left = 0.0f;
+                    if (MASKED && c0 >= own) Lc = left = 0.0f;
                     if (sink) {
                         if (copied) {
                             Lc += left;  // the sink's value is the first row's
@@ -541,10 +570,7 @@ rows_kernel(const __grid_constant__ RowsParams rp, const __grid_constant__ CUten
                     for (int e = 0; e < 16; e += 2) apart(fma2(two(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), both(unit), both(nm)), u[e], u[e + 1]);
                     u[16] = fmaf(__uint_as_float(xn), unit, nm);
                     Two W[8];
-                    if (col + 16 < own)
-                        weights16<false>(u, Lc, 0, W);
-                    else
-                        weights16<true>(u, Lc, own - col, W);
+                    weights16<MASKED>(u, Lc, own - col, W);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) sum = sum + W[e];
 #pragma unroll
@@ -578,17 +604,16 @@ rows_kernel(const __grid_constant__ RowsParams rp, const __grid_constant__ CUten
                     uint32_t pk[8], pl[8];
                     chunk(xa, CW >= 32 ? xb[0] : behind, c0 + c, pk);
                     if (CW >= 32) chunk(xb, behind, c0 + c + 16, pl);
-                    if (!wait_free()) break;
+                    if (!wait_free()) return false;
                     tm_st8(tP + (rep * CW + c) / 2, pk);
                     if (CW >= 32) tm_st8(tP + (rep * CW + c) / 2 + 8, pl);
                 }
-                if (!ok) break;
                 float sx, sy;
                 apart(sum, sx, sy);
                 l += sx + sy;
-                if (!EIGHT && own < KT) {  // rows behind the end: their weights are 0, and 0 * NaN is not
+                if (!EIGHT && MASKED && own < KT) {  // rows behind the end: their weights are 0, and 0 * NaN is not
                     const int stage = tiles % NS;
-                    if (!(ok = __all_sync(0xffffffffu, wait(v_full(stage), tiles / NS)))) break;
+                    if (!(ok = __all_sync(0xffffffffu, wait(v_full(stage), tiles / NS)))) return false;
                     uint8_t *vt = smem + C::OffRing + stage * C::StageBytes + C::KBytes;
                     const int t0 = tid & 127;
                     for (int k = t0; k < 64 * (D / 8); k += 128) {
@@ -602,7 +627,10 @@ rows_kernel(const __grid_constant__ RowsParams rp, const __grid_constant__ CUten
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full(h));
-            }
+                return true;
+            };
+            for (int j = now.tile; ok && j < now.last; ++j, ++tiles)
+                if (!(n - j * KT > KT ? tile(j, std::false_type{}) : tile(j, std::true_type{}))) ok = false;
             if (!ok) break;
             if (!(ok = __all_sync(0xffffffffu, wait(o_done(h), tiles - 1)))) break;
             tc_fence_after();
@@ -612,15 +640,17 @@ rows_kernel(const __grid_constant__ RowsParams rp, const __grid_constant__ CUten
             s_l[h * 128 + i] = bad ? NAN : l;
             if (!soft_sync()) break;
             // the sources of a row: half s / reps, copy s mod reps
-            const int reps = 128 / R, sources = H * reps;
+            constexpr int reps = 128 / R, sources = H * reps;
             auto source = [&](int s, int r) { return (s / reps) * 128 + (s % reps) * R + r; };
             float high = -INFINITY;
+#pragma unroll
             for (int s = 0; s < sources; ++s) high = fmaxf(high, s_m[source(s, row)]);
             constexpr float kUnit = 1.0f / (kLn2 * kLn2);
             const float f = (high == -INFINITY ? 0.0f : ex2_approx(m - high)) * kUnit, fo = EIGHT ? f / lift : f;
             const long long slot = (all_rows ? 2 * kGrid + (long long)b * heads + now.head : worker * 2 + (u0 < now.s0 ? 1 : 0)) * p.HB;
             if (tid < rows_h) {  // half 0, copy 0
                 float total = 0.0f;
+#pragma unroll
                 for (int s = 0; s < sources; ++s) {
                     const float mm = s_m[source(s, row)], ll = s_l[source(s, row)];
                     // without a column: 0 or NaN
@@ -653,7 +683,7 @@ rows_kernel(const __grid_constant__ RowsParams rp, const __grid_constant__ CUten
                 for (int k = tid; k < rows_h * E; k += 128 * H) {
                     const int r = k / E, e = k % E;
                     float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 2
+#pragma unroll
                     for (int s = 0; s < sources; ++s) {
                         const float4 x = X[place(source(s, r), e)];
                         y.x += x.x;
@@ -685,8 +715,8 @@ rows_kernel(const __grid_constant__ RowsParams rp, const __grid_constant__ CUten
         const uint64_t v_desc = csa_tc::make_sdesc(EIGHT ? base + C::OffV : base + C::OffRing + C::KBytes, C::VBox, 1024);
         auto issue_s = [&]() {
             const int stage = tiles_s % NS;
-            if (!idle(EIGHT ? k_ready : k_full(stage), EIGHT ? tiles_s : tiles_s / NS)) return false;
-            if (!idle(s_empty, tiles_s + 1)) return false;
+            if (!awake(EIGHT ? k_ready : k_full(stage), EIGHT ? tiles_s : tiles_s / NS)) return false;
+            if (!awake(s_empty, tiles_s + 1)) return false;
             tc_fence_after();
             const uint64_t kd = k_desc + (EIGHT ? 0 : stage * (C::StageBytes >> 4));
 #pragma unroll
@@ -700,14 +730,14 @@ rows_kernel(const __grid_constant__ RowsParams rp, const __grid_constant__ CUten
         };
         do {
             if (lane == 0) {
-                ok = idle(q_full, parts) && issue_s();
+                ok = awake(q_full, parts) && issue_s();
                 for (int j = now.tile; ok && j < now.last; ++j) {
                     if (j + 1 < now.last && !(ok = issue_s())) break;
                     const int stage = tiles_o % NS;
-                    if (!(ok = idle(EIGHT ? v_ready : v_full(stage), EIGHT ? tiles_o : tiles_o / NS))) break;
+                    if (!(ok = awake(EIGHT ? v_ready : v_full(stage), EIGHT ? tiles_o : tiles_o / NS))) break;
                     const uint64_t vd = v_desc + (EIGHT ? 0 : stage * (C::StageBytes >> 4));
                     for (int h = 0; h < H && ok; ++h) {
-                        if (!(ok = idle(p_full(h), tiles_o))) break;
+                        if (!(ok = awake(p_full(h), tiles_o))) break;
                         tc_fence_after();
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
@@ -930,10 +960,9 @@ inline bool encode_boxes(CUtensorMap *map, const void *ptr, long long rows, int 
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int KIND>
-int launch_rows(RowsParams &rp, cudaStream_t stream) {
+template <int D, int KIND, int CW>
+int launch_rows(PagedParams &p, cudaStream_t stream) {
     using C = RowsCfg<D, KIND>;
-    PagedParams &p = rp.p;
     p.R = C::KT;
     while (p.S % p.R != 0) p.R /= 2;  // S is a multiple of 8
     p.s_inv = ~0ull / p.S + 1;
@@ -946,7 +975,7 @@ int launch_rows(RowsParams &rp, cudaStream_t stream) {
     }
     const long long tiles = (long long)p.B * p.Hkv * p.GB * (((long long)p.M * p.S + C::KT - 1) / C::KT);
     const int grid = (int)(tiles < kGrid ? (tiles < 1 ? 1 : tiles) : kGrid);
-    auto kern = rows_kernel<D, KIND>;
+    auto kern = rows_kernel<D, KIND, CW>;
     // the shares of the registers come out of those that the block is launched with
     static const bool fits = [&] {
         cudaFuncAttributes attr;
@@ -954,7 +983,7 @@ int launch_rows(RowsParams &rp, cudaStream_t stream) {
                32 * C::SoftWarps * C::SoftRegs + (C::Threads - 32 * C::SoftWarps) * C::OtherRegs <= C::Threads * attr.numRegs;
     }();
     if (!fits || cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::Smem) != cudaSuccess ||
-        launch_after_previous(kern, grid, C::Threads, C::Smem, stream, rp, maps[0], maps[1], maps[2]) != cudaSuccess)
+        launch_after_previous(kern, grid, C::Threads, C::Smem, stream, p, maps[0], maps[1], maps[2]) != cudaSuccess)
         return CSA_ERR_CUDA;
     return CSA_OK;
 }
@@ -962,22 +991,26 @@ int launch_rows(RowsParams &rp, cudaStream_t stream) {
 // Blocks of a group's rows, at most 128 each, as equal as can be.
 inline int row_blocks(int rows) { return (rows + 127) / 128; }
 
+template <int D, int KIND>
+int launch_rows_of(PagedParams &p, cudaStream_t stream) {
+    if (p.HB <= 32) return launch_rows<D, KIND, 16>(p, stream);
+    if (p.HB <= 64) return launch_rows<D, KIND, 32>(p, stream);
+    return launch_rows<D, KIND, 64>(p, stream);
+}
+
 template <int KIND>
 int run_rows(const csa_paged_args &a, void *scratch, int d, cudaStream_t stream) {
-    RowsParams rp = {};
-    PagedParams &p = rp.p;
-    p = paged_params(a);
+    PagedParams p = paged_params(a);
     p.G = p.Hq / p.Hkv;
     p.GB = row_blocks(p.G);
     p.HB = (p.G + p.GB - 1) / p.GB;
-    rp.R = p.HB <= 32 ? 32 : p.HB <= 64 ? 64 : 128;
     const long long segments = (long long)p.B * p.Hkv * p.GB;
     p.joins = static_cast<int4 *>(scratch);
     p.part_o = reinterpret_cast<float *>(p.joins + std::max((long long)kGrid, segments));  // 16-byte aligned
     p.part_ml = p.part_o + (2 * kGrid + segments) * p.HB * d;
-    if (d == 64) return launch_rows<64, KIND>(rp, stream);
-    if (d == 128) return launch_rows<128, KIND>(rp, stream);
-    return launch_rows<256, KIND>(rp, stream);
+    if (d == 64) return launch_rows_of<64, KIND>(p, stream);
+    if (d == 128) return launch_rows_of<128, KIND>(p, stream);
+    return launch_rows_of<256, KIND>(p, stream);
 }
 
 }  // namespace
