@@ -143,11 +143,14 @@ struct RowsCfg {
     static constexpr int Stages = Eight ? (D == 64 ? 4 : 2) : D == 64 ? 3 : 2;
     static constexpr int RawK = KR * D, RawV = KT * D, RawS = KR * 8;
     static constexpr int StageBytes = Eight ? RawK + RawV + (RawS + 1023) / 1024 * 1024 : KBytes + VBytes;
+    static constexpr int NV = Eight && D < 256 ? 2 : 1;  // buffers of turned values
     static constexpr int OffQ = 0, OffK = QBytes, OffV = OffK + KBytes;  // the operand buffers of 8-bit pools
-    static constexpr int OffRing = Eight ? OffV + VBytes : QBytes;
-    static constexpr int XC = D == 256 ? 16 : 32;  // columns of the sums joined at a time
-    static constexpr int OffX = OffRing + Stages * StageBytes;
-    static constexpr int OffScales = OffX + 128 * Halves * XC * 4;  // [4 tiles][2][KR]
+    static constexpr int OffRing = Eight ? OffV + NV * VBytes : QBytes;
+    static constexpr int XC = D == 256 || (Eight && D == 64) ? 16 : 32;  // columns of the sums joined at a time
+    static constexpr int XBytes = 128 * Halves * XC * 4;
+    static constexpr int OffX = Eight ? OffQ : OffRing + Stages * StageBytes;  // 8 bits: on the part's queries
+    static_assert(!Eight || XBytes <= QBytes, "the sums fit");
+    static constexpr int OffScales = Eight ? OffRing + Stages * StageBytes : OffX + XBytes;  // [4 tiles][2][KR]
     static constexpr int Smem = OffScales + (Eight ? 4 * KR * 8 : 0) + 1024;
     static_assert(Smem <= 227 * 1024 - 4096, "one block per SM");
     // tensor memory columns
@@ -213,7 +216,7 @@ rows_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUten
     constexpr bool EIGHT = C::Eight, E4M3 = KIND == CSA_E4M3;
     constexpr int KT = C::KT, KR = C::KR, NS = C::Stages, H = C::Halves, R = 2 * CW;
     extern __shared__ uint8_t raw[];
-    __shared__ __align__(8) uint64_t s_bars[4 * NS + 13];
+    __shared__ __align__(8) uint64_t s_bars[4 * NS + 15];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_bad[8];
     __shared__ float s_lift[4], s_m[2 * 128], s_l[2 * 128];
@@ -221,7 +224,7 @@ rows_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUten
     const uint32_t base = (smem_u32(raw) + 1023) / 1024 * 1024;
     uint8_t *smem = raw + (base - smem_u32(raw));
     long long *s_cut = reinterpret_cast<long long *>(smem + C::OffX);  // at the start only
-    static_assert((C::Threads + 1) * 8 <= 128 * C::Halves * C::XC * 4, "the cut fits");
+    static_assert((C::Threads + 1) * 8 <= C::XBytes, "the cut fits");
     volatile int *abort_flag = &s_abort;
     // barriers: stages of the ring, full and empty, keys and values; then one each
     const uint32_t bars = smem_u32(s_bars);
@@ -230,8 +233,10 @@ rows_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUten
     auto k_empty = [&](int s) { return bars + 8 * (2 * NS + s); };
     auto v_empty = [&](int s) { return bars + 8 * (3 * NS + s); };
     const uint32_t one = bars + 8 * 4 * NS;
-    const uint32_t s_full = one, s_empty = one + 8, q_full = one + 16, k_ready = one + 24, v_ready = one + 32, k_free = one + 40,
-                   v_free = one + 48, drain = one + 56, joint = one + 96;
+    const uint32_t s_full = one, s_empty = one + 8, q_full = one + 16, k_ready = one + 24, k_free = one + 40,
+                   drain = one + 56, joint = one + 96;
+    auto v_ready = [&](int s) { return s == 0 ? one + 32 : one + 104; };
+    auto v_free = [&](int s) { return s == 0 ? one + 48 : one + 112; };
     auto p_full = [&](int h) { return one + 64 + 8 * h; };
     auto o_done = [&](int h) { return one + 80 + 8 * h; };
     if (tid == 0) {
@@ -245,14 +250,14 @@ rows_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUten
         mbar_init(s_empty, C::SoftWarps);
         mbar_init(q_full, C::SoftWarps);
         mbar_init(k_ready, EIGHT ? C::TurnWarps + 1 : 1);
-        mbar_init(v_ready, EIGHT ? C::TurnWarps : 1);
         mbar_init(k_free, 1);
-        mbar_init(v_free, 1);
         mbar_init(drain, 1);
         mbar_init(joint, C::SoftWarps);
         for (int h = 0; h < 2; ++h) {
             mbar_init(p_full(h), 4);
             mbar_init(o_done(h), 1);
+            mbar_init(v_ready(h), EIGHT ? C::TurnWarps : 1);
+            mbar_init(v_free(h), 1);
         }
         s_abort = 0;
         fence_mbar_init();
@@ -315,6 +320,7 @@ rows_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUten
             if (now.tile >= now.last) some = next_part(now, cut, u0, u1, lens, KT, most, heads);
         }
     }
+    if (p.B > 32) __syncthreads();  // the cut is read; what it lies on can be written
     auto next = [&]() { return next_part(now, cut, u0, u1, lens, KT, most, heads); };
     auto cached_head = [&](int head) { return p.GB == 1 ? head : head / p.GB; };
 
@@ -601,12 +607,33 @@ rows_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUten
                         scaled(xb, c0 + c + 16);
                         if (EIGHT) behind = __float_as_uint(__uint_as_float(behind) * sk[c0 + c + 32]);
                     }
-                    uint32_t pk[8], pl[8];
-                    chunk(xa, CW >= 32 ? xb[0] : behind, c0 + c, pk);
-                    if (CW >= 32) chunk(xb, behind, c0 + c + 16, pl);
-                    if (!wait_free()) return false;
-                    tm_st8(tP + (rep * CW + c) / 2, pk);
-                    if (CW >= 32) tm_st8(tP + (rep * CW + c) / 2 + 8, pl);
+                    auto store = [&](const uint32_t (&pk)[8], int col) {
+                        if (!wait_free()) return false;
+                        tm_st8(tP + (rep * CW + col) / 2, pk);
+                        return true;
+                    };
+                    if constexpr (CW == 16) {
+                        uint32_t pk[8];
+                        chunk(xa, behind, c0, pk);
+                        if (!store(pk, 0)) return false;
+                    } else if constexpr (EIGHT) {
+                        // the second 16 by the first's instructions: with the turning and the scales two copies of them
+                        // miss the instruction caches (16 sequences of 4096 to 8192 rows, 64 rows each: 156 us, so 131;
+                        // bf16 pools have room for both, 89 us instead of 94)
+#pragma unroll 1
+                        for (int e = 0; e < 32; e += 16) {
+                            uint32_t pk[8];
+                            chunk(xa, e == 0 ? xb[0] : behind, c0 + c + e, pk);
+                            if (!store(pk, c + e)) return false;
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) xa[k] = xb[k];
+                        }
+                    } else {
+                        uint32_t pk[8], pl[8];
+                        chunk(xa, xb[0], c0 + c, pk);
+                        chunk(xb, behind, c0 + c + 16, pl);
+                        if (!store(pk, c) || !store(pl, c + 16)) return false;
+                    }
                 }
                 float sx, sy;
                 apart(sum, sx, sy);
@@ -734,8 +761,8 @@ rows_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUten
                 for (int j = now.tile; ok && j < now.last; ++j) {
                     if (j + 1 < now.last && !(ok = issue_s())) break;
                     const int stage = tiles_o % NS;
-                    if (!(ok = awake(EIGHT ? v_ready : v_full(stage), EIGHT ? tiles_o : tiles_o / NS))) break;
-                    const uint64_t vd = v_desc + (EIGHT ? 0 : stage * (C::StageBytes >> 4));
+                    if (!(ok = awake(EIGHT ? v_ready(tiles_o % C::NV) : v_full(stage), tiles_o / (EIGHT ? C::NV : NS)))) break;
+                    const uint64_t vd = v_desc + (EIGHT ? (tiles_o % C::NV) * (C::VBytes >> 4) : stage * (C::StageBytes >> 4));
                     for (int h = 0; h < H && ok; ++h) {
                         if (!(ok = awake(p_full(h), tiles_o))) break;
                         tc_fence_after();
@@ -747,7 +774,7 @@ rows_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUten
                         tc_commit(o_done(h));
                     }
                     if (!ok) break;
-                    tc_commit(EIGHT ? v_free : v_empty(stage));
+                    tc_commit(EIGHT ? v_free(tiles_o % C::NV) : v_empty(stage));
                     ++tiles_o;
                 }
             }
@@ -874,71 +901,68 @@ rows_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUten
             const int t = tid - 32 * C::TurnWarp;
             constexpr int T = 32 * C::TurnWarps, PerRow = D / 16, Step = T / PerRow;
             static_assert(Step % 8 == 0 && KT % Step == 0, "a thread has every Step-th row, alike in the swizzle");
-            // 16 codes of row r, columns 16 c ..: two swizzled chunks of 16 bytes.  The odd boxes' second chunk goes
-            // first, so that eight lanes meet no bank twice.
-            const int t0 = t / PerRow, c = t % PerRow, odd = (c >> 2) & 1;
-            const uint32_t low = ((2 * (c & 3) + odd) ^ (t0 & 7)) << 4, high = ((2 * (c & 3) + 1 - odd) ^ (t0 & 7)) << 4;
+            // 16 codes of row r, columns 16 c ..: two swizzled chunks of 16 bytes.  Of each pair of rows the odd boxes' lanes
+            // have the other one, so that eight lanes meet no bank twice, neither reading nor writing.
+            const int c = t % PerRow, t0 = (t / PerRow) ^ ((c >> 2) & 1);
+            const uint32_t low = ((2 * (c & 3)) ^ (t0 & 7)) << 4;
             auto turn = [&](const uint4 &x, uint8_t *row) {
-                uint4 y[2];
-                halves_of<E4M3>(x.x, y[0].x, y[0].y);
-                halves_of<E4M3>(x.y, y[0].z, y[0].w);
-                halves_of<E4M3>(x.z, y[1].x, y[1].y);
-                halves_of<E4M3>(x.w, y[1].z, y[1].w);
-                *reinterpret_cast<uint4 *>(row + low) = odd ? y[1] : y[0];
-                *reinterpret_cast<uint4 *>(row + high) = odd ? y[0] : y[1];
+                uint4 y;
+                halves_of<E4M3>(x.x, y.x, y.y);
+                halves_of<E4M3>(x.y, y.z, y.w);
+                *reinterpret_cast<uint4 *>(row + low) = y;
+                halves_of<E4M3>(x.z, y.x, y.y);
+                halves_of<E4M3>(x.w, y.z, y.w);
+                *reinterpret_cast<uint4 *>(row + (low ^ 16)) = y;
             };
-            // `rows` rows, the ones from `own` on as zeros; four of a thread's at a time
+            // `rows` rows, the ones from `own` on as zeros; two of a thread's at a time
             auto turn_rows = [&](const uint8_t *src, uint8_t *box, int rows, int own) {
-                src += t * 16;
+                src += t0 * D + c * 16;
                 box += t0 * 128;
 #pragma unroll 1
-                for (int r = t0; r < rows; r += 4 * Step, src += 4 * T * 16, box += 4 * Step * 128) {
-                    uint4 x[4];
+                for (int r = t0; r < rows; r += 2 * Step, src += 2 * T * 16, box += 2 * Step * 128) {
+                    uint4 x[2];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
+                    for (int e = 0; e < 2; ++e)
                         x[e] = r + e * Step < min(rows, own) ? *reinterpret_cast<const uint4 *>(src + e * T * 16) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
+                    for (int e = 0; e < 2; ++e)
                         if (r + e * Step < rows) turn(x[e], box + e * Step * 128);
                 }
             };
             bool ok = true;
-            // keys one tile ahead of the values: the keys' buffer is free once the tile before has its logits, the values'
-            // not before its sums
+            // Keys up to two tiles ahead of the values: the keys' buffer is free once the tile before has its logits, a
+            // buffer of the values not before the sums of the tile that it held.  One loop for both, that their
+            // instructions are in the caches once.
             Part ahead = now;
             int keys = 0, values = 0;
             bool more = true;
-            auto turn_keys = [&]() {
-                const int stage = keys % NS;
-                const uint8_t *rk = smem + C::OffRing + stage * C::StageBytes;
-                if (!(ok = __all_sync(0xffffffffu, idle(k_full(stage), keys / NS) && idle(k_free, keys + 1)))) return;
-                turn_rows(rk, smem + C::OffK + (c >> 2) * C::KBox, KR, 1 << 30);
+#pragma unroll 1
+            while (true) {
+                const bool k = more && keys <= values + 1;
+                const int of = k ? keys : values, stage = of % NS, buf = of % C::NV;
+                if (!(ok = __all_sync(0xffffffffu, idle(k ? k_full(stage) : v_full(stage), of / NS) &&
+                                                       idle(k ? k_free : v_free(buf), (k ? of : of / C::NV) + 1))))
+                    break;
+                turn_rows(smem + C::OffRing + stage * C::StageBytes + (k ? 0 : C::RawK),
+                          smem + (k ? C::OffK + (c >> 2) * C::KBox : C::OffV + buf * C::VBytes + (c >> 2) * C::VBox), k ? KR : KT,
+                          k ? 1 << 30 : now.n - now.tile * KT);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(k_ready);
-                    mbar_arrive(k_empty(stage));
+                    mbar_arrive(k ? k_ready : v_ready(buf));
+                    mbar_arrive(k ? k_empty(stage) : v_empty(stage));
                 }
-                ++keys;
-                if (++ahead.tile == ahead.last) more = next_part(ahead, cut, u0, u1, lens, KT, most, heads);
-            };
-            turn_keys();
-            while (ok) {
-                if (more) {
-                    turn_keys();
-                    if (!ok) break;
+                Part at = k ? ahead : now;
+                const bool goes_on = ++at.tile < at.last || next_part(at, cut, u0, u1, lens, KT, most, heads);
+                if (k) {
+                    ++keys;
+                    ahead = at;
+                    more = goes_on;
+                } else {
+                    ++values;
+                    now = at;
+                    if (!goes_on) break;
                 }
-                const int stage = values % NS, own = now.n - now.tile * KT;
-                if (!(ok = __all_sync(0xffffffffu, idle(v_full(stage), values / NS) && idle(v_free, values + 1)))) break;
-                turn_rows(smem + C::OffRing + stage * C::StageBytes + C::RawK, smem + C::OffV + (c >> 2) * C::VBox, KT, own);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(v_ready);
-                    mbar_arrive(v_empty(stage));
-                }
-                ++values;
-                if (++now.tile == now.last && !next()) break;
             }
         }
     }
