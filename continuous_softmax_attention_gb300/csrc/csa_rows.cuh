@@ -182,18 +182,21 @@ __device__ __forceinline__ void weights16(const float (&u)[17], float &Lc, int c
     float before = Lc;
 #pragma unroll
     for (int e = 0; e < 16; e += 2) {  // intervals e and e + 1
-        const float x0 = u[e + 1] - u[e], x1 = u[e + 2] - u[e + 1];
+        const float x0 = u[e] - u[e + 1], x1 = u[e + 1] - u[e + 2];  // -X
         const float i0 = rcp_approx(x0), i1 = rcp_approx(x1);
         const bool s0 = fabsf(x0) < 0.0625f, s1 = fabsf(x1) < 0.0625f;
-        const Two X = two(x0, x1), P0 = two(p[e], p[e + 1]);
+        const Two x = two(x0, x1), P0 = two(p[e], p[e + 1]);
         const float g0 = s0 ? 1.0f : -1.0f, g1 = s1 ? 1.0f : -1.0f;
-        const Two f1 = two(s0 ? 0.5f * l1 : i0, s1 ? 0.5f * l1 : i1), f2 = two(s0 ? l1 / 3.0f : i0, s1 ? l1 / 3.0f : i1);
+        float k0, k1;
+        apart(fma2(x * x, both(-l1 * l2 / 24.0f), both(0.5f * l1)), k0, k1);
+        const Two f1 = two(s0 ? k0 : i0, s1 ? k1 : i1), f2 = two(s0 ? -l1 / 3.0f : i0, s1 ? -l1 / 3.0f : i1);
+#ifdef VAR_SEL
+        const Two a2 = two(s0 ? 0.5f * l1 : -l1, s1 ? 0.5f * l1 : -l1);
+#else
         const Two a2 = fma2(two(g0, g1), both(0.75f * l1), both(-0.25f * l1));  // (ln 2) / 2 or -ln 2
-        Two S = two(fmaf(p[e], g0, p[e + 1]), fmaf(p[e + 1], g1, p[e + 2])) * f1;
-        // 1 - (X ln 2)^2 / 12 where X is small; elsewhere the exact quotient stays
-        const Two y = X * X;
-        S = S * fma2(two(s0 ? -l2 / 12.0f : 0.0f, s1 ? -l2 / 12.0f : 0.0f), y, both(1.0f));
-        const Two R = fma2(P0, a2, S) * f2, L = fma2(S, both(l1), R * both(-1.0f));
+#endif
+        const Two S = two(fmaf(p[e + 1], g0, p[e]), fmaf(p[e + 2], g1, p[e + 1])) * f1;
+        const Two R = fma2(P0, a2, S) * f2, L = fma2(S, both(l1), R);  // R: what the left gets, times -1
         float r0, r1, q0, q1;
         apart(R, r0, r1);
         apart(L, q0, q1);
@@ -201,7 +204,7 @@ __device__ __forceinline__ void weights16(const float (&u)[17], float &Lc, int c
             if (e + 1 >= columns) r0 = q0 = 0.0f;
             if (e + 2 >= columns) r1 = q1 = 0.0f;
         }
-        W[e / 2] = two(r0 + before, r1 + q0);
+        W[e / 2] = two(before - r0, q0 - r1);
         before = q1;
     }
     Lc = before;
