@@ -129,6 +129,8 @@ struct Cfg {
 
 // Workers of a full grid, at most.
 __host__ __device__ constexpr long long workers(int d) { return (d == 64 ? 12 : 1024 / d) * kGrid; }
+// And those of csa_rows.cuh: blocks.
+__host__ __device__ constexpr long long row_workers(int d) { return (d == 256 ? 1 : 2) * kGrid; }
 
 struct PagedParams {
     const __nv_bfloat16 *q;

@@ -121,7 +121,8 @@ __device__ __forceinline__ bool wait_awake(uint32_t bar, uint32_t parity, volati
 template <int D, int KIND>
 struct RowsCfg {
     static constexpr bool Eight = KIND != CSA_BF16;
-    static constexpr int Halves = D == 256 ? 1 : 2;
+    static constexpr int Halves = D == 256 || !Eight ? 1 : 2;
+    static constexpr int Blocks = Eight || D == 256 ? 1 : 2;  // per SM
     static constexpr int KT = 64 * Halves;   // cached rows per tile
     static constexpr int KR = KT + 16;       // and those of K: 8 behind, 8 before
     // warps: the softmax, the tensor core, the copies of keys and of values (which wait for different products, so each
@@ -131,31 +132,31 @@ struct RowsCfg {
     static constexpr int TurnWarps = Eight ? 4 : 0;
     static constexpr int Threads = 32 * (SoftWarps + 4 + TurnWarps);
     // registers of the softmax warps and of the others; at launch every thread has 65536 / Threads, in eights
-    static constexpr int SoftRegs = !Eight ? (D == 256 ? 248 : 192) : D == 256 ? 248 : 152;
-    static constexpr int OtherRegs = !Eight ? 104 : D == 256 ? 120 : 104;
-    static constexpr int LaunchRegs = 65536 / Threads / 8 * 8 > 248 ? 248 : 65536 / Threads / 8 * 8;
+    static constexpr int SoftRegs = D == 256 ? 248 : Eight ? 152 : 160;
+    static constexpr int OtherRegs = D == 256 && Eight ? 120 : Eight || D == 256 ? 104 : 96;
+    static constexpr int LaunchRegs = 65536 / (Threads * Blocks) / 8 * 8 > 248 ? 248 : 65536 / (Threads * Blocks) / 8 * 8;
     static_assert(32 * SoftWarps * SoftRegs + (Threads - 32 * SoftWarps) * OtherRegs <= Threads * LaunchRegs, "the block's own registers");
     static constexpr int Boxes = D / 64;
     // operands of 16 bits: boxes of 64 columns, 128-byte swizzle
     static constexpr int QBox = 128 * 128, KBox = KR * 128, VBox = KT * 128;
     static constexpr int QBytes = Boxes * QBox, KBytes = Boxes * KBox, VBytes = Boxes * VBox;
     // 8 bits: the ring holds codes and scales, one pair of operand buffers the fp16 numbers
-    static constexpr int Stages = Eight ? (D == 64 ? 4 : 2) : D == 64 ? 3 : 2;
+    static constexpr int Stages = D == 64 ? 4 : 2;
     static constexpr int RawK = KR * D, RawV = KT * D, RawS = KR * 8;
     static constexpr int StageBytes = Eight ? RawK + RawV + (RawS + 1023) / 1024 * 1024 : KBytes + VBytes;
     static constexpr int NV = Eight && D < 256 ? 2 : 1;  // buffers of turned values
     static constexpr int OffQ = 0, OffK = QBytes, OffV = OffK + KBytes;  // the operand buffers of 8-bit pools
     static constexpr int OffRing = Eight ? OffV + NV * VBytes : QBytes;
-    static constexpr int XC = D == 256 || (Eight && D == 64) ? 16 : 32;  // columns of the sums joined at a time
-    static constexpr int XBytes = 128 * Halves * XC * 4;
-    static constexpr int OffX = Eight ? OffQ : OffRing + Stages * StageBytes;  // 8 bits: on the part's queries
-    static_assert(!Eight || XBytes <= QBytes, "the sums fit");
-    static constexpr int OffScales = Eight ? OffRing + Stages * StageBytes : OffX + XBytes;  // [4 tiles][2][KR]
+    // the sums of a part are joined on its queries, XC columns at a time
+    static constexpr int XC = 128 * Halves * 32 * 4 <= QBytes ? 32 : 16, XBytes = 128 * Halves * XC * 4, OffX = OffQ;
+    static_assert(XBytes <= QBytes, "the sums fit");
+    static constexpr int OffScales = OffRing + Stages * StageBytes;  // [4 tiles][2][KR]
     static constexpr int Smem = OffScales + (Eight ? 4 * KR * 8 : 0) + 1024;
-    static_assert(Smem <= 227 * 1024 - 4096, "one block per SM");
+    static_assert(Blocks * (Smem + 4096) <= 227 * 1024, "shared memory");
     // tensor memory columns
     static constexpr int ColP = KR, ColO = KR + 32 * Halves;
-    static_assert(ColO + D * Halves <= 512, "tensor memory");
+    static constexpr int Columns = 512 / Blocks;
+    static_assert(ColO + D * Halves <= Columns, "tensor memory");
 };
 
 __host__ __device__ constexpr uint32_t rows_idesc(bool bf16, int N, bool b_mn_major) {
@@ -212,7 +213,7 @@ __device__ __forceinline__ void weights16(const float (&u)[17], float &Lc, int c
 
 // CW: a thread's columns of a half: 64 for 128 rows, 32 for two copies of 64, 16 for four of 32.
 template <int D, int KIND, int CW>
-__global__ void __launch_bounds__(RowsCfg<D, KIND>::Threads, 1)
+__global__ void __launch_bounds__(RowsCfg<D, KIND>::Threads, RowsCfg<D, KIND>::Blocks)
 rows_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
             const __grid_constant__ CUtensorMap map_k8) {
     using C = RowsCfg<D, KIND>;
@@ -266,7 +267,7 @@ rows_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUten
         fence_mbar_init();
     }
     if (warp == C::MmaWarp) {
-        csa_dev::tmem_alloc(smem_u32(&s_tmem), 512);
+        csa_dev::tmem_alloc(smem_u32(&s_tmem), C::Columns);
         csa_dev::tmem_relinquish();
     }
     tc_fence_before();
@@ -677,7 +678,7 @@ rows_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUten
             for (int s = 0; s < sources; ++s) high = fmaxf(high, s_m[source(s, row)]);
             constexpr float kUnit = 1.0f / (kLn2 * kLn2);
             const float f = (high == -INFINITY ? 0.0f : ex2_approx(m - high)) * kUnit, fo = EIGHT ? f / lift : f;
-            const long long slot = (all_rows ? 2 * kGrid + (long long)b * heads + now.head : worker * 2 + (u0 < now.s0 ? 1 : 0)) * p.HB;
+            const long long slot = (all_rows ? 2 * row_workers(D) + (long long)b * heads + now.head : worker * 2 + (u0 < now.s0 ? 1 : 0)) * p.HB;
             if (tid < rows_h) {  // half 0, copy 0
                 float total = 0.0f;
 #pragma unroll
@@ -971,7 +972,7 @@ rows_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUten
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == C::MmaWarp) csa_dev::tmem_dealloc(tmem, 512);
+    if (warp == C::MmaWarp) csa_dev::tmem_dealloc(tmem, C::Columns);
 }
 
 // [P * Hkv * S, D] bf16 as {64, rows, D / 64}, boxes of 64 columns and R rows.
@@ -1001,7 +1002,7 @@ int launch_rows(PagedParams &p, cudaStream_t stream) {
             if (!encode_boxes(&maps[i], rows ? i == 1 ? p.v : p.k : some, rows ? rows : 8, D, i == 2 ? 8 : p.R)) return CSA_ERR_CUDA;
     }
     const long long tiles = (long long)p.B * p.Hkv * p.GB * (((long long)p.M * p.S + C::KT - 1) / C::KT);
-    const int grid = (int)(tiles < kGrid ? (tiles < 1 ? 1 : tiles) : kGrid);
+    const int most = C::Blocks * kGrid, grid = (int)(tiles < most ? (tiles < 1 ? 1 : tiles) : most);
     auto kern = rows_kernel<D, KIND, CW>;
     // the shares of the registers come out of those that the block is launched with
     static const bool fits = [&] {
@@ -1010,6 +1011,7 @@ int launch_rows(PagedParams &p, cudaStream_t stream) {
                32 * C::SoftWarps * C::SoftRegs + (C::Threads - 32 * C::SoftWarps) * C::OtherRegs <= C::Threads * attr.numRegs;
     }();
     if (!fits || cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::Smem) != cudaSuccess ||
+        cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) != cudaSuccess ||
         launch_after_previous(kern, grid, C::Threads, C::Smem, stream, p, maps[0], maps[1], maps[2]) != cudaSuccess)
         return CSA_ERR_CUDA;
     return CSA_OK;
@@ -1033,8 +1035,8 @@ int run_rows(const csa_paged_args &a, void *scratch, int d, cudaStream_t stream)
     p.HB = (p.G + p.GB - 1) / p.GB;
     const long long segments = (long long)p.B * p.Hkv * p.GB;
     p.joins = static_cast<int4 *>(scratch);
-    p.part_o = reinterpret_cast<float *>(p.joins + std::max((long long)kGrid, segments));  // 16-byte aligned
-    p.part_ml = p.part_o + (2 * kGrid + segments) * p.HB * d;
+    p.part_o = reinterpret_cast<float *>(p.joins + std::max(row_workers(d), segments));  // 16-byte aligned
+    p.part_ml = p.part_o + (2 * row_workers(d) + segments) * p.HB * d;
     if (d == 64) return launch_rows_of<64, KIND>(p, stream);
     if (d == 128) return launch_rows_of<128, KIND>(p, stream);
     return launch_rows_of<256, KIND>(p, stream);

@@ -436,7 +436,7 @@ struct TreeScratch {
         many = rows > kMany;
         GB = many ? row_blocks(rows) : head_blocks(rows);
         HB = GB ? (rows + GB - 1) / GB : 0;
-        parts_of = many ? kGrid : (int)workers(d);
+        parts_of = (int)(many ? row_workers(d) : workers(d));
         segments = (long long)B * Hkv * GB;
         slots = 2 * parts_of + segments;
         notes = std::max((long long)parts_of, segments);
