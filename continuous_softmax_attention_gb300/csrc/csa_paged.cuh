@@ -445,7 +445,10 @@ __device__ __forceinline__ float2 cluster_load(uint32_t addr, int rank) {  // 8 
 // sequence and a block of its query heads), cut over its warps, and joins the
 // parts itself through shared memory: one launch, for few segments of bounded
 // length.  Otherwise the cut over all workers described above.
-template <int D, int RH, bool ONE, int KIND>
+//
+// CP: copies of the query heads among the eight rows of the first product, with few of them: a lane then
+// weighs 8 / CP of the tile's rows instead of eight.
+template <int D, int RH, bool ONE, int KIND, int CP>
 __global__ void __launch_bounds__(Cfg<D, RH, KIND>::Warps * 32, 1)
 paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUtensorMap map_k,
              const __grid_constant__ CUtensorMap map_v) {
@@ -453,6 +456,11 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
     constexpr bool EIGHT = C::Eight, E4M3 = KIND == CSA_E4M3;
     constexpr int KT = C::KT, NT = KT / 8, KS = D / 16, kStages = C::Stages;
     constexpr float kUp = EIGHT ? kRaise8 : kRaise;
+    // With copies the eight rows g are CP times N heads, and a lane has the N rows of a tile that are its copy's share:
+    // of the 16 rows of `group`, of which lane q's product has four, those from 4 q + N * sub on.
+    constexpr bool SPREAD = CP > 1;
+    static_assert(!SPREAD || (EIGHT && RH == 1), "copies are for codes, and few heads");
+    constexpr int N = 8 / CP, Subs = SPREAD ? 4 / N : 1;
     constexpr int DW = D / C::Pair, ON = DW / 8;  // columns of the output that a warp forms
     extern __shared__ uint8_t raw[];
     __shared__ long long s_cut[ONE ? 1 : C::Warps * 32 + 1];
@@ -462,6 +470,17 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
     const int heads = p.Hkv * p.GB;
     const long long most = (long long)p.M * p.S;
     const Lengths lens = {p.seqlens, p.counts, p.T, most};
+    const int copy = SPREAD ? g / N : 0, sub = copy % Subs, group = copy / Subs, own0 = 16 * group + 4 * q + N * sub;
+    // a head's lanes in the order of their rows, in a ring
+    auto lane_of = [&](int c, int qq) { return 4 * (c * N + g % N) + qq; };
+    const int lane_before = sub > 0    ? lane_of(copy - 1, q)
+                            : q > 0    ? lane_of(copy + Subs - 1, q - 1)
+                                       : lane_of((group + 1) % 2 * Subs + Subs - 1, 3);
+    const int lane_behind = sub < Subs - 1 ? lane_of(copy + 1, q)
+                            : q < 3        ? lane_of(copy - (Subs - 1), q + 1)
+                                           : lane_of((group + 1) % 2 * Subs, 0);
+    const bool has_last = own0 + N == 32;
+    const int lane_first = 4 * (g % N);
     const int mine = warp / C::Pair, half_of = warp % C::Pair;  // worker in the block, warp of the worker
     volatile int *abort_flag = &s_abort[mine];
     // the warps of a worker
@@ -578,13 +597,13 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
     auto ask = [&]() {
         const int hk = cached_head(now.head), hb = now.head - hk * p.GB;
         const int rows_h = min(p.HB, p.G - hb * p.HB);
-        const __nv_bfloat16 *qg = p.q + ((long long)now.b * p.Hq + hk * p.G + hb * p.HB + g) * D;
+        const __nv_bfloat16 *qg = p.q + ((long long)now.b * p.Hq + hk * p.G + hb * p.HB + (SPREAD ? g % N : g)) * D;
         if constexpr (EIGHT) {
             // columns 64 i + 16 q + 4 j .. + 3 for product 4 i + j, as a lane's 16 codes of a cached row lie
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const uint4 *at = reinterpret_cast<const uint4 *>(qg + (long long)h * 8 * D);
-                const bool there = h < RH && g + 8 * h < rows_h;
+                const bool there = h < RH && (SPREAD ? g % N : g + 8 * h) < rows_h;
 #pragma unroll
                 for (int i = 0; i < D / 64; ++i)
 #pragma unroll
@@ -818,6 +837,7 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
 #pragma unroll
         for (int i = 0; i < ON; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
         float w[RH][NT][2];  // weights of the tile before, its last one without the next interval
+        float ws[N] = {};    // with copies: this lane's of them
         uint32_t v_at = 0;   // that tile's values
         uint32_t s_at = 0;   // and its scales
         // 8 bits: values count in units of 1 / lift, kLift by the power of two that is at least the largest
@@ -832,16 +852,23 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
                 float t = top[h];
                 t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
                 t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+#pragma unroll
+                for (int off = SPREAD ? 4 * N : 32; off < 32; off *= 2) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, off));
                 t = fmaxf(t, m[h]);
                 f[h] = ex2_approx(m[h] - t);
                 m[h] = t;
                 l[h] *= f[h];
                 w0[h] *= f[h];
                 pm[h] *= f[h];
+                if constexpr (SPREAD) {
 #pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    w[h][i][0] *= f[h];
-                    w[h][i][1] *= f[h];
+                    for (int t = 0; t < N; ++t) ws[t] *= f[h];
+                } else {
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) {
+                        w[h][i][0] *= f[h];
+                        w[h][i][1] *= f[h];
+                    }
                 }
             }
 #pragma unroll
@@ -852,8 +879,96 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
                 o[i][3] *= f[RH - 1];
             }
         };
+        // with copies: the scales of this lane's keys and values of a tile
+        auto scales_of = [&](uint32_t at, float (&x)[N], float (&y)[N]) {
+            if constexpr (N == 1) {
+                asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(x[0]), "=f"(y[0]) : "r"(at + own0 * 8) : "memory");
+            } else {
+#pragma unroll
+                for (int t = 0; t + 1 < N; t += 2) {
+                    const uint4 z = lds16(at + (own0 + t) * 8);
+                    x[t] = __uint_as_float(z.x);
+                    y[t] = __uint_as_float(z.y);
+                    x[t + 1] = __uint_as_float(z.z);
+                    y[t + 1] = __uint_as_float(z.w);
+                }
+            }
+        };
         // the second product for the tile before
         auto values = [&]() {
+            // 8 bits: another unit of the values, whose largest scale among this lane's rows is `most`
+            auto lift_to = [&](float most) {
+                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+#pragma unroll
+                for (int off = SPREAD ? 4 * N : 32; off < 32; off *= 2) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
+                // exponent of the power of two at or above it
+                const uint32_t e2 = min(max((__float_as_uint(most) + 0x7fffffu) >> 23, 8u), 253u);
+                const float to = __uint_as_float((261u - e2) << 23), f = to / lift;  // kLift 2^(127 - e2)
+                lift = to;
+#pragma unroll
+                for (int i = 0; i < ON; ++i)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[i][e] *= f;
+            };
+            // 8 bits: the product with 16 rows, whose weights are a
+            auto product = [&](int ks, const uint32_t (&a)[4]) {
+#pragma unroll
+                for (int i = 0; i < ON / 4; ++i) {
+                    uint32_t vb[4];
+                    ldsm_t8(chunk(v_at + v_row[ks], 2 * i) + to_half, vb);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t b0, b1;
+                        halves_of<E4M3>(vb[j], b0, b1);
+                        mma<true>(o[4 * i + j], a, b0, b1);
+                    }
+                }
+            };
+            if constexpr (SPREAD) {
+                float x[N], sv[N], most = 0.f;
+                scales_of(s_at, x, sv);
+#pragma unroll
+                for (int t = 0; t < N; ++t) {
+                    l[0] += ws[t];
+                    most = fmaxf(most, sv[t]);
+                }
+                if (__any_sync(0xffffffffu, most * lift > 2.0f * kLift)) lift_to(most);
+                // weights as hi + lo, of two rows each in a register (of one row in one with N = 1), then those of
+                // all copies
+                constexpr int Regs = N > 1 ? N : 1;
+                uint32_t mine[Regs], all[8];
+                if constexpr (N > 1) {
+#pragma unroll
+                    for (int t = 0; t < N; t += 2) {
+                        const float a = ws[t] * (sv[t] * lift), c = ws[t + 1] * (sv[t + 1] * lift);
+                        mine[t] = pack_f16x2(a, c);
+                        const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&mine[t]));
+                        mine[t + 1] = pack_f16x2(a - y.x, c - y.y);
+                    }
+                } else {
+                    const float a = ws[0] * (sv[0] * lift);
+                    const uint32_t y = pack_f16x2(a, 0.f);
+                    mine[0] = y | pack_f16x2(0.f, a - __half22float2(*reinterpret_cast<const __half2 *>(&y)).x);
+                }
+#pragma unroll
+                for (int c = 0; c < CP; ++c)
+#pragma unroll
+                    for (int t = 0; t < Regs; ++t) all[c * Regs + t] = __shfl_sync(0xffffffffu, mine[t], lane_of(c, q));
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks) {
+                    const uint32_t *y = all + 4 * ks;
+                    if constexpr (N > 1) {
+                        const uint32_t a[4] = {y[0], y[1], y[2], y[3]};
+                        product(ks, a);
+                    } else {
+                        const uint32_t a[4] = {__byte_perm(y[0], y[1], 0x5410), __byte_perm(y[0], y[1], 0x7632),
+                                               __byte_perm(y[2], y[3], 0x5410), __byte_perm(y[2], y[3], 0x7632)};
+                        product(ks, a);
+                    }
+                }
+                return;
+            }
 #pragma unroll
             for (int h = 0; h < RH; ++h)
 #pragma unroll
@@ -875,16 +990,7 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
 #pragma unroll
                     for (int ks = 0; ks < KT / 16; ++ks)
                         most = fmaxf(most, fmaxf(fmaxf(sv[ks][0], sv[ks][1]), fmaxf(sv[ks][2], sv[ks][3])));
-                    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
-                    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-                    // exponent of the power of two at or above it
-                    const uint32_t e2 = min(max((__float_as_uint(most) + 0x7fffffu) >> 23, 8u), 253u);
-                    const float to = __uint_as_float((261u - e2) << 23), f = to / lift;  // kLift 2^(127 - e2)
-                    lift = to;
-#pragma unroll
-                    for (int i = 0; i < ON; ++i)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) o[i][e] *= f;
+                    lift_to(most);
                 }
 #pragma unroll
                 for (int ks = 0; ks < KT / 16; ++ks) {
@@ -903,17 +1009,7 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
                         }
                     }
                     const uint32_t a[4] = {hi[0][0], RH == 1 ? lo[0] : hi[RH - 1][0], hi[0][1], RH == 1 ? lo[1] : hi[RH - 1][1]};
-#pragma unroll
-                    for (int i = 0; i < ON / 4; ++i) {
-                        uint32_t vb[4];
-                        ldsm_t8(chunk(v_at + v_row[ks], 2 * i) + to_half, vb);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            uint32_t b0, b1;
-                            halves_of<E4M3>(vb[j], b0, b1);
-                            mma<true>(o[4 * i + j], a, b0, b1);
-                        }
-                    }
+                    product(ks, a);
                 }
             } else {
 #pragma unroll
@@ -1029,168 +1125,240 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
                         mma(ks & 1 ? s2[2 * i + 1] : s[2 * i + 1], qa[ks], kb[2], kb[3]);
                     }
             }
-            float top[RH];
-            bool over = false;
-            if constexpr (EIGHT) {
-                const uint32_t at = scale_ring + stage * C::Scales + 4 * q * 8;
+            float nws[N], even0 = 0.f, to_before0 = 0.f;  // with copies: as nw, even_left and to_before below
+            if constexpr (SPREAD) {
+                float a[N], pe[N], x[N], y[N];
+                scales_of(scale_ring + stage * C::Scales, x, y);
 #pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    const uint4 x = lds16(at + (16 * (i / 2) + 2 * (i & 1)) * 8);
+                for (int t = 0; t < N; ++t) {  // number v = N * copy + t of the lane's eight, by halves
+                    float of[CP];
+#pragma unroll
+                    for (int c = 0; c < CP; ++c) of[c] = s[(c * N + t) / 2][(c * N + t) & 1];
+#pragma unroll
+                    for (int c = CP / 2; c > 0; c /= 2)
+#pragma unroll
+                        for (int i = 0; i < c; ++i) of[i] = copy & c ? of[i + c] : of[i];
+                    a[t] = of[0] * (unit[0] * x[t]);
+                    if (own < KT && own0 + t >= own) a[t] = -INFINITY;
+                }
+                float top[1] = {a[0]};
+#pragma unroll
+                for (int t = 1; t < N; ++t) top[0] = fmaxf(top[0], a[t]);
+                if (j == tile)
+#pragma unroll
+                    for (int t = 0; t < N; ++t) ws[t] = 0.f;
+                if (__any_sync(0xffffffffu, top[0] > m[0] + kUp)) raise(top);
+                if (j == tile && copied_sink) {
+                    prev[0] = __shfl_sync(0xffffffffu, a[0], lane_first);
+                    pm[0] = ex2_approx(prev[0] - m[0]);
+                }
+#pragma unroll
+                for (int t = 0; t < N; ++t) pe[t] = ex2_approx(a[t] - m[0]);
+                const float a_b = __shfl_sync(0xffffffffu, has_last ? prev[0] : a[N - 1], lane_before);
+                const float p_b = __shfl_sync(0xffffffffu, has_last ? pm[0] : pe[N - 1], lane_before);
+                float lf[N], rt[N], none0, none1;  // what the interval before row t gives its left and right row
+                if constexpr (N == 1) {
+                    intervals(a_b, a[0], a_b, a[0], p_b, pe[0], p_b, pe[0], lf[0], rt[0], none0, none1);
+                } else {
+#pragma unroll
+                    for (int t = 0; t < N; t += 2)
+                        intervals(t == 0 ? a_b : a[t > 0 ? t - 1 : 0], a[t], a[t], a[t + 1], t == 0 ? p_b : pe[t > 0 ? t - 1 : 0], pe[t],
+                                  pe[t], pe[t + 1], lf[t], rt[t], lf[t + 1], rt[t + 1]);
+                }
+                if (own < KT) {  // nothing from intervals that end behind the last row
+#pragma unroll
+                    for (int t = 0; t < N; ++t)
+                        if (own0 + t >= own) lf[t] = rt[t] = 0.f;
+                }
+#pragma unroll
+                for (int t = 0; t < N; ++t) nws[t] = t + 1 < N ? rt[t] + lf[t + 1 < N ? t + 1 : 0] : rt[t];
+                prev[0] = a[N - 1];
+                pm[0] = pe[N - 1];
+                even0 = lf[0];
+                const float from = __shfl_sync(0xffffffffu, even0, lane_behind);
+                if (has_last)
+                    to_before0 = from;
+                else
+                    nws[N - 1] += from;
+            }
+            float nw[RH][NT][2], even_left[RH][NT], to_before[RH];
+            if constexpr (!SPREAD) {
+                float top[RH];
+                bool over = false;
+                if constexpr (EIGHT) {
+                    const uint32_t at = scale_ring + stage * C::Scales + 4 * q * 8;
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) {
+                        const uint4 x = lds16(at + (16 * (i / 2) + 2 * (i & 1)) * 8);
+#pragma unroll
+                        for (int h = 0; h < RH; ++h) {
+                            s[i][2 * h] *= unit[h] * __uint_as_float(x.x);
+                            s[i][2 * h + 1] *= unit[h] * __uint_as_float(x.z);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int h = 0; h < RH; ++h)
+#pragma unroll
+                        for (int i = 0; i < NT; ++i)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) s[i][2 * h + e] = (s[i][2 * h + e] + s2[i][2 * h + e]) * p.qscale;
+                }
+                if (own < KT) {
+#pragma unroll
+                    for (int h = 0; h < RH; ++h)
+#pragma unroll
+                        for (int i = 0; i < NT; ++i)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                if (row_of(i, e) >= own) s[i][2 * h + e] = -INFINITY;
+                }
+#pragma unroll
+                for (int h = 0; h < RH; ++h) {
+                    top[h] = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) top[h] = fmaxf(top[h], fmaxf(s[i][2 * h], s[i][2 * h + 1]));
+                    over |= top[h] > m[h] + kUp;
+                }
+                if (j == tile) {
+#pragma unroll
+                    for (int h = 0; h < RH; ++h)
+#pragma unroll
+                        for (int i = 0; i < NT; ++i) w[h][i][0] = w[h][i][1] = 0.f;
+                }
+                if (__any_sync(0xffffffffu, over)) raise(top);
+                if (j == tile && copied_sink) {
 #pragma unroll
                     for (int h = 0; h < RH; ++h) {
-                        s[i][2 * h] *= unit[h] * __uint_as_float(x.x);
-                        s[i][2 * h + 1] *= unit[h] * __uint_as_float(x.z);
+                        prev[h] = __shfl_sync(0xffffffffu, s[0][2 * h], lane & ~3);
+                        pm[h] = ex2_approx(prev[h] - m[h]);
                     }
                 }
-            } else {
-#pragma unroll
-                for (int h = 0; h < RH; ++h)
-#pragma unroll
-                    for (int i = 0; i < NT; ++i)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) s[i][2 * h + e] = (s[i][2 * h + e] + s2[i][2 * h + e]) * p.qscale;
-            }
-            if (own < KT) {
-#pragma unroll
-                for (int h = 0; h < RH; ++h)
-#pragma unroll
-                    for (int i = 0; i < NT; ++i)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            if (row_of(i, e) >= own) s[i][2 * h + e] = -INFINITY;
-            }
-#pragma unroll
-            for (int h = 0; h < RH; ++h) {
-                top[h] = -INFINITY;
-#pragma unroll
-                for (int i = 0; i < NT; ++i) top[h] = fmaxf(top[h], fmaxf(s[i][2 * h], s[i][2 * h + 1]));
-                over |= top[h] > m[h] + kUp;
-            }
-            if (j == tile) {
-#pragma unroll
-                for (int h = 0; h < RH; ++h)
-#pragma unroll
-                    for (int i = 0; i < NT; ++i) w[h][i][0] = w[h][i][1] = 0.f;
-            }
-            if (__any_sync(0xffffffffu, over)) raise(top);
-            if (j == tile && copied_sink) {
-#pragma unroll
-                for (int h = 0; h < RH; ++h) {
-                    prev[h] = __shfl_sync(0xffffffffu, s[0][2 * h], lane & ~3);
-                    pm[h] = ex2_approx(prev[h] - m[h]);
-                }
-            }
 
-            // this tile's weights, and the share of its first interval that the row before gets (for q = 3,
-            // whose w holds that row)
-            float nw[RH][NT][2], even_left[RH][NT], to_before[RH];
-            if constexpr (EIGHT) {  // four rows of a lane at a time, half as many shuffles
-                constexpr int NS = KT / 16;
+                // this tile's weights, and the share of its first interval that the row before gets (for q = 3,
+                // whose w holds that row)
+                if constexpr (EIGHT) {  // four rows of a lane at a time, half as many shuffles
+                    constexpr int NS = KT / 16;
 #pragma unroll
-                for (int h = 0; h < RH; ++h) {
-                    float pe[NS][4];
-                    auto a = [&](int k, int i) { return s[2 * k + i / 2][2 * h + (i & 1)]; };
+                    for (int h = 0; h < RH; ++h) {
+                        float pe[NS][4];
+                        auto a = [&](int k, int i) { return s[2 * k + i / 2][2 * h + (i & 1)]; };
 #pragma unroll
-                    for (int k = 0; k < NS; ++k)
+                        for (int k = 0; k < NS; ++k)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) pe[k][i] = ex2_approx(a(k, i) - m[h]);
+                            for (int i = 0; i < 4; ++i) pe[k][i] = ex2_approx(a(k, i) - m[h]);
 #pragma unroll
-                    for (int k = 0; k < NS; ++k) {
-                        const float a_src = q == 3 ? (k == 0 ? prev[h] : a(k > 0 ? k - 1 : 0, 3)) : a(k, 3);
-                        const float p_src = q == 3 ? (k == 0 ? pm[h] : pe[k > 0 ? k - 1 : 0][3]) : pe[k][3];
-                        const float a_b = __shfl_sync(0xffffffffu, a_src, (lane & ~3) | ((q + 3) & 3));
-                        const float p_b = __shfl_sync(0xffffffffu, p_src, (lane & ~3) | ((q + 3) & 3));
-                        float lf[4], rt[4];  // what interval i - 1 to i gives its left and right row
-                        intervals(a_b, a(k, 0), a(k, 0), a(k, 1), p_b, pe[k][0], pe[k][0], pe[k][1], lf[0], rt[0], lf[1], rt[1]);
-                        intervals(a(k, 1), a(k, 2), a(k, 2), a(k, 3), pe[k][1], pe[k][2], pe[k][2], pe[k][3], lf[2], rt[2], lf[3],
-                                  rt[3]);
-                        if (own < KT) {  // nothing from intervals that end behind the last row
+                        for (int k = 0; k < NS; ++k) {
+                            const float a_src = q == 3 ? (k == 0 ? prev[h] : a(k > 0 ? k - 1 : 0, 3)) : a(k, 3);
+                            const float p_src = q == 3 ? (k == 0 ? pm[h] : pe[k > 0 ? k - 1 : 0][3]) : pe[k][3];
+                            const float a_b = __shfl_sync(0xffffffffu, a_src, (lane & ~3) | ((q + 3) & 3));
+                            const float p_b = __shfl_sync(0xffffffffu, p_src, (lane & ~3) | ((q + 3) & 3));
+                            float lf[4], rt[4];  // what interval i - 1 to i gives its left and right row
+                            intervals(a_b, a(k, 0), a(k, 0), a(k, 1), p_b, pe[k][0], pe[k][0], pe[k][1], lf[0], rt[0], lf[1], rt[1]);
+                            intervals(a(k, 1), a(k, 2), a(k, 2), a(k, 3), pe[k][1], pe[k][2], pe[k][2], pe[k][3], lf[2], rt[2], lf[3],
+                                      rt[3]);
+                            if (own < KT) {  // nothing from intervals that end behind the last row
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (16 * k + 4 * q + i >= own) lf[i] = rt[i] = 0.f;
-                        }
-                        even_left[h][k] = lf[0];
-                        nw[h][2 * k][0] = rt[0] + lf[1];
-                        nw[h][2 * k][1] = rt[1] + lf[2];
-                        nw[h][2 * k + 1][0] = rt[2] + lf[3];
-                        nw[h][2 * k + 1][1] = rt[3];
-                    }
-                    // for the next tile, and for q = 3 only
-                    prev[h] = a(NS - 1, 3);
-                    pm[h] = pe[NS - 1][3];
-#pragma unroll
-                    for (int k = 0; k < NS; ++k) {
-                        const float src = q == 0 ? even_left[h][k + 1 < NS ? k + 1 : 0] : even_left[h][k];
-                        const float from = __shfl_sync(0xffffffffu, src, (lane & ~3) | ((q + 1) & 3));
-                        if (k + 1 < NS || q < 3) nw[h][2 * k + 1][1] += from;
-                        if (k + 1 == NS) to_before[h] = from;
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int h = 0; h < RH; ++h) {
-                    float pe[NT][2];
-#pragma unroll
-                    for (int i = 0; i < NT; ++i) {
-                        pe[i][0] = ex2_approx(s[i][2 * h] - m[h]);
-                        pe[i][1] = ex2_approx(s[i][2 * h + 1] - m[h]);
-                    }
-#pragma unroll
-                    for (int i = 0; i < NT; ++i) {
-                        // the logit and power before this lane's first row: from the lane to the left, for
-                        // q = 0 from q = 3 of the column tile before
-                        const float a_src = q == 3 ? (i == 0 ? prev[h] : s[i > 0 ? i - 1 : 0][2 * h + 1]) : s[i][2 * h + 1];
-                        const float p_src = q == 3 ? (i == 0 ? pm[h] : pe[i > 0 ? i - 1 : 0][1]) : pe[i][1];
-                        const float a_b = __shfl_sync(0xffffffffu, a_src, (lane & ~3) | ((q + 3) & 3));
-                        const float p_b = __shfl_sync(0xffffffffu, p_src, (lane & ~3) | ((q + 3) & 3));
-                        float r_even, l_odd, r_odd;
-                        intervals(a_b, s[i][2 * h], s[i][2 * h], s[i][2 * h + 1], p_b, pe[i][0], pe[i][0], pe[i][1],
-                                  even_left[h][i], r_even, l_odd, r_odd);
-                        nw[h][i][0] = r_even + l_odd;
-                        nw[h][i][1] = r_odd;
-                        if (own < KT) {  // nothing from intervals that end behind the last row
-                            if (8 * i + 2 * q + 1 >= own) {
-                                nw[h][i][0] = r_even;
-                                nw[h][i][1] = 0.f;
+                                for (int i = 0; i < 4; ++i)
+                                    if (16 * k + 4 * q + i >= own) lf[i] = rt[i] = 0.f;
                             }
-                            if (8 * i + 2 * q >= own) nw[h][i][0] = even_left[h][i] = 0.f;
+                            even_left[h][k] = lf[0];
+                            nw[h][2 * k][0] = rt[0] + lf[1];
+                            nw[h][2 * k][1] = rt[1] + lf[2];
+                            nw[h][2 * k + 1][0] = rt[2] + lf[3];
+                            nw[h][2 * k + 1][1] = rt[3];
+                        }
+                        // for the next tile, and for q = 3 only
+                        prev[h] = a(NS - 1, 3);
+                        pm[h] = pe[NS - 1][3];
+#pragma unroll
+                        for (int k = 0; k < NS; ++k) {
+                            const float src = q == 0 ? even_left[h][k + 1 < NS ? k + 1 : 0] : even_left[h][k];
+                            const float from = __shfl_sync(0xffffffffu, src, (lane & ~3) | ((q + 1) & 3));
+                            if (k + 1 < NS || q < 3) nw[h][2 * k + 1][1] += from;
+                            if (k + 1 == NS) to_before[h] = from;
                         }
                     }
-                    // for the next tile, and for q = 3 only
-                    prev[h] = s[NT - 1][2 * h + 1];
-                    pm[h] = pe[NT - 1][1];
+                } else {
 #pragma unroll
-                    for (int i = 0; i < NT; ++i) {
-                        const float src = q == 0 ? even_left[h][i + 1 < NT ? i + 1 : 0] : even_left[h][i];
-                        const float from = __shfl_sync(0xffffffffu, src, (lane & ~3) | ((q + 1) & 3));
-                        if (i + 1 < NT || q < 3) nw[h][i][1] += from;
-                        if (i + 1 == NT) to_before[h] = from;
+                    for (int h = 0; h < RH; ++h) {
+                        float pe[NT][2];
+#pragma unroll
+                        for (int i = 0; i < NT; ++i) {
+                            pe[i][0] = ex2_approx(s[i][2 * h] - m[h]);
+                            pe[i][1] = ex2_approx(s[i][2 * h + 1] - m[h]);
+                        }
+#pragma unroll
+                        for (int i = 0; i < NT; ++i) {
+                            // the logit and power before this lane's first row: from the lane to the left, for
+                            // q = 0 from q = 3 of the column tile before
+                            const float a_src = q == 3 ? (i == 0 ? prev[h] : s[i > 0 ? i - 1 : 0][2 * h + 1]) : s[i][2 * h + 1];
+                            const float p_src = q == 3 ? (i == 0 ? pm[h] : pe[i > 0 ? i - 1 : 0][1]) : pe[i][1];
+                            const float a_b = __shfl_sync(0xffffffffu, a_src, (lane & ~3) | ((q + 3) & 3));
+                            const float p_b = __shfl_sync(0xffffffffu, p_src, (lane & ~3) | ((q + 3) & 3));
+                            float r_even, l_odd, r_odd;
+                            intervals(a_b, s[i][2 * h], s[i][2 * h], s[i][2 * h + 1], p_b, pe[i][0], pe[i][0], pe[i][1],
+                                      even_left[h][i], r_even, l_odd, r_odd);
+                            nw[h][i][0] = r_even + l_odd;
+                            nw[h][i][1] = r_odd;
+                            if (own < KT) {  // nothing from intervals that end behind the last row
+                                if (8 * i + 2 * q + 1 >= own) {
+                                    nw[h][i][0] = r_even;
+                                    nw[h][i][1] = 0.f;
+                                }
+                                if (8 * i + 2 * q >= own) nw[h][i][0] = even_left[h][i] = 0.f;
+                            }
+                        }
+                        // for the next tile, and for q = 3 only
+                        prev[h] = s[NT - 1][2 * h + 1];
+                        pm[h] = pe[NT - 1][1];
+#pragma unroll
+                        for (int i = 0; i < NT; ++i) {
+                            const float src = q == 0 ? even_left[h][i + 1 < NT ? i + 1 : 0] : even_left[h][i];
+                            const float from = __shfl_sync(0xffffffffu, src, (lane & ~3) | ((q + 1) & 3));
+                            if (i + 1 < NT || q < 3) nw[h][i][1] += from;
+                            if (i + 1 == NT) to_before[h] = from;
+                        }
                     }
                 }
             }
             if (j > tile) {
+                if constexpr (SPREAD) {
+                    ws[N - 1] += to_before0;
+                } else {
 #pragma unroll
-                for (int h = 0; h < RH; ++h)
-                    if (q == 3) w[h][NT - 1][1] += to_before[h];
+                    for (int h = 0; h < RH; ++h)
+                        if (q == 3) w[h][NT - 1][1] += to_before[h];
+                }
                 values();
                 sync_worker();  // every lane has read the tile before: its stage is free
                 ++used;
                 copy_next();
             } else if (copied_sink) {  // its value is the first row's too
+                if constexpr (SPREAD) {
+                    if (own0 == 0) nws[0] += even0;
+                } else {
 #pragma unroll
-                for (int h = 0; h < RH; ++h)
-                    if (q == 0) nw[h][0][0] += even_left[h][0];
+                    for (int h = 0; h < RH; ++h)
+                        if (q == 0) nw[h][0][0] += even_left[h][0];
+                }
             } else if (r0 == 0) {
 #pragma unroll
-                for (int h = 0; h < RH; ++h) w0[h] = __shfl_sync(0xffffffffu, even_left[h][0], lane & ~3);
+                for (int h = 0; h < RH; ++h)
+                    w0[h] = SPREAD ? __shfl_sync(0xffffffffu, even0, lane_first) : __shfl_sync(0xffffffffu, even_left[h][0], lane & ~3);
             }
+            if constexpr (SPREAD) {
 #pragma unroll
-            for (int h = 0; h < RH; ++h)
+                for (int t = 0; t < N; ++t) ws[t] = nws[t];
+            } else {
 #pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    w[h][i][0] = nw[h][i][0];
-                    w[h][i][1] = nw[h][i][1];
-                }
+                for (int h = 0; h < RH; ++h)
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) {
+                        w[h][i][0] = nw[h][i][0];
+                        w[h][i][1] = nw[h][i][1];
+                    }
+            }
             v_at = k_at + C::Tile;
             s_at = scale_ring + stage * C::Scales;
             if (++stage == kStages) {
@@ -1208,7 +1376,7 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
                 float left, right, none0, none1;
                 const float pb = ex2_approx(behind[h] - m[h]);
                 intervals(prev[h], behind[h], prev[h], behind[h], pm[h], pb, pm[h], pb, left, right, none0, none1);
-                if (q == 3) w[h][NT - 1][1] += left;
+                if (SPREAD ? has_last : q == 3) (SPREAD ? ws[N - 1] : w[h][NT - 1][1]) += left;
             }
         }
         if (!lost) values();
@@ -1226,6 +1394,8 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
             float t = l[h];
             t += __shfl_xor_sync(0xffffffffu, t, 1);
             t += __shfl_xor_sync(0xffffffffu, t, 2);
+#pragma unroll
+            for (int off = SPREAD ? 4 * N : 32; off < 32; off *= 2) t += __shfl_xor_sync(0xffffffffu, t, off);
             sum[h] = bad ? NAN : t + w0[h];
         }
         // a worker's part that does not begin a segment is its first
@@ -1508,7 +1678,7 @@ inline int cluster_for(long long segments, long long tiles, int warps) {
     return tiles <= most * c * warps ? c : 0;
 }
 
-template <int D, int RH, int KIND>
+template <int D, int RH, int KIND, int CP = 1>
 int launch(PagedParams &p, cudaStream_t stream) {
     using C = Cfg<D, RH, KIND>;
     p.R = C::KT;
@@ -1525,7 +1695,7 @@ int launch(PagedParams &p, cudaStream_t stream) {
     const long long segments = (long long)p.B * heads, tiles = ((long long)p.M * p.S + C::KT - 1) / C::KT;
     p.cluster = p.T > 0 ? 0 : cluster_for(segments, tiles, C::Workers);
     if (p.cluster > 0) {
-        auto kern = paged_kernel<D, RH, true, KIND>;
+        auto kern = paged_kernel<D, RH, true, KIND, CP>;
         if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::Smem) != cudaSuccess ||
             launch_clusters_after_previous(kern, (unsigned)segments * p.cluster, C::Warps * 32, C::Smem, stream,
                                            p.cluster, p, map_k, map_v) != cudaSuccess)
@@ -1535,7 +1705,7 @@ int launch(PagedParams &p, cudaStream_t stream) {
     // blocks that the largest possible lengths can keep busy
     const long long most = segments * tiles;
     const int grid = (int)(most < kGrid ? (most < 1 ? 1 : most) : kGrid);
-    auto kern = paged_kernel<D, RH, false, KIND>;
+    auto kern = paged_kernel<D, RH, false, KIND, CP>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::Smem) != cudaSuccess)
         return CSA_ERR_CUDA;
     const long long all = (long long)grid * C::Workers;
@@ -1578,6 +1748,13 @@ PagedParams paged_params(const csa_paged_args &a) {
     return p;
 }
 
+template <int KIND, int CP>
+int launch_copies(PagedParams &p, int d, cudaStream_t stream) {
+    if (d == 64) return launch<64, 1, KIND, CP>(p, stream);
+    if (d == 128) return launch<128, 1, KIND, CP>(p, stream);
+    return launch<256, 1, KIND, CP>(p, stream);
+}
+
 // The launch for these heads and row lengths; scratch as csa_decode_paged_scratch_bytes.
 template <int KIND>
 int run_paged(PagedParams &p, void *scratch, int d, cudaStream_t stream) {
@@ -1588,6 +1765,15 @@ int run_paged(PagedParams &p, void *scratch, int d, cudaStream_t stream) {
     p.joins = static_cast<int4 *>(scratch);
     p.part_ml = reinterpret_cast<float *>(p.joins + std::max(workers(d), segments));
     p.part_o = p.part_ml + (2 * workers(d) + segments) * p.HB * 2;
+    // As many copies of the heads as eight rows hold.  16 sequences of 4096 to 8192 rows, d = 128, e4m3 (int8):
+    // 32 cached heads with one query head each take 136 us (157) with eight copies, 148 (166) with two and 164
+    // (183) with one; 16 with two 77 (86) with four, 81 (90) and 88 (99); 8 with four 47 (53) with two, 51 (56).
+    // Rows of 16 bits have no copies: there the copies from memory take longer than the weights.
+    if constexpr (KIND != CSA_BF16) {
+        if (p.HB == 1) return launch_copies<KIND, 8>(p, d, stream);
+        if (p.HB == 2) return launch_copies<KIND, 4>(p, d, stream);
+        if (p.HB <= 4) return launch_copies<KIND, 2>(p, d, stream);
+    }
     if (p.HB <= 8) {
         if (d == 64) return launch<64, 1, KIND>(p, stream);
         if (d == 128) return launch<128, 1, KIND>(p, stream);
