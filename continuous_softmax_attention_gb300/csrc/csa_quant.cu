@@ -87,7 +87,7 @@ __device__ __forceinline__ void store_codes(uint8_t *to, const float (&x)[N], fl
 // c1; a lane has U units.  Units [0, n/V) turn, the ones behind copy the columns
 // from 2n on.
 template <typename T, int V, int U, bool ADJ, bool E4M3>
-__global__ void __launch_bounds__(kThreads) fill_kernel(const __grid_constant__ FillParams p) {
+__global__ void __launch_bounds__(kThreads, 8) fill_kernel(const __grid_constant__ FillParams p) {
     using C = typename Chunk<V * sizeof(T)>::type;
     __shared__ unsigned long long turn[CSA_ROPE_MAX_PAIRS];
     __shared__ unsigned char axis[CSA_ROPE_MAX_PAIRS];
@@ -161,25 +161,37 @@ __global__ void __launch_bounds__(kThreads) fill_kernel(const __grid_constant__ 
         }
     }
     union Pack {
+        __device__ Pack() {}
         C raw;
         T e[V];
+        __nv_bfloat162 two[V > 1 ? V * sizeof(T) / 4 : 1];
     };
+    // the next head's values are asked for before this one's are used
+    Pack ahead[U][2];
+    auto load = [&]() {
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) ahead[i][0].e[j] = ahead[i][1].e[j] = narrow<T>(0.0f);
+            if (one[i]) ahead[i][0].raw = *reinterpret_cast<const C *>(in + c0[i]);
+            if (two[i]) ahead[i][1].raw = *reinterpret_cast<const C *>(in + c1[i]);
+        }
+        in += x.ih;
+    };
+    load();
 #pragma unroll 1
     for (int h = 0; h < count; ++h) {
         float val[U][2][V];
         unsigned most = 0;  // the bits of the largest magnitude, infinities and NaN above all
 #pragma unroll
+        for (int i = 0; i < U; ++i)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int j = 0; j < V; ++j) val[i][k][j] = widen(ahead[i][k].e[j]);
+        if (h + 1 < count) load();
+#pragma unroll
         for (int i = 0; i < U; ++i) {
-            Pack a, c;
-#pragma unroll
-            for (int j = 0; j < V; ++j) a.e[j] = c.e[j] = narrow<T>(0.0f);
-            if (one[i]) a.raw = *reinterpret_cast<const C *>(in + c0[i]);
-            if (two[i]) c.raw = *reinterpret_cast<const C *>(in + c1[i]);
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                val[i][0][j] = widen(a.e[j]);
-                val[i][1][j] = widen(c.e[j]);
-            }
             if (one[i] && turns[i]) {
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
@@ -191,24 +203,34 @@ __global__ void __launch_bounds__(kThreads) fill_kernel(const __grid_constant__ 
                     ew = xu * sn[i][j] + xw * cs[i][j];
                 }
             }
-#pragma unroll
-            for (int j = 0; j < V; ++j)
-                most = max(most, max(__float_as_uint(val[i][0][j]) & 0x7fffffffu,
-                                     __float_as_uint(val[i][1][j]) & 0x7fffffffu));
         }
         if (which == 0) {
 #pragma unroll
             for (int i = 0; i < U; ++i) {
                 Pack a, c;
+                if constexpr (sizeof(T) == 2 && V > 1) {  // two values by one instruction
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    a.e[j] = narrow<T>(val[i][0][j]);
-                    c.e[j] = narrow<T>(val[i][1][j]);
+                    for (int j = 0; j < V; j += 2) {
+                        a.two[j / 2] = __floats2bfloat162_rn(val[i][0][j], val[i][0][j + 1]);
+                        c.two[j / 2] = __floats2bfloat162_rn(val[i][1][j], val[i][1][j + 1]);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < V; ++j) {
+                        a.e[j] = narrow<T>(val[i][0][j]);
+                        c.e[j] = narrow<T>(val[i][1][j]);
+                    }
                 }
                 if (one[i]) *reinterpret_cast<C *>(out + c0[i]) = a.raw;
                 if (two[i]) *reinterpret_cast<C *>(out + c1[i]) = c.raw;
             }
         } else {
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    most = max(most, max(__float_as_uint(val[i][0][j]) & 0x7fffffffu,
+                                         __float_as_uint(val[i][1][j]) & 0x7fffffffu));
             for (int off = p.lanes / 2; off > 0; off >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, off));
             float s, factor;
             const bool zero = row_scale<E4M3>(most, s, factor);
@@ -219,7 +241,6 @@ __global__ void __launch_bounds__(kThreads) fill_kernel(const __grid_constant__ 
             }
             if (live && lane == 0) *scale = s;
         }
-        in += x.ih;
         out += x.oh;
         codes += (long long)p.S * p.d;
         scale += 2 * p.S;
@@ -234,11 +255,14 @@ int launch_fill(FillParams &p, cudaStream_t stream) {
     while (p.lanes * U < units) p.lanes *= 2;
     const int rows = kThreads / p.lanes;
     const long long tokens = (long long)p.B * p.T, bx = (tokens + rows - 1) / rows;
-    // a token's sines serve the block's heads: 4, fewer where that leaves SMs without work
+    // A token's sines serve the block's heads: 32, fewer where that leaves less than three full blocks per SM.  32
+    // heads on 8, d = 128: 16 x 3000 tokens take 161 us with 32, 167 with 16, 196 with 4; 8 x 512 22, 14.4 and 17.9
+    // us; 8 x 128 9.0, 6.6 and 6.5.
+    const long long heads = p.x[0].H + 2 * p.x[1].H;
+    p.heads_per_block = 32;
+    while (p.heads_per_block > 1 && bx * heads < 3 * 152 * p.heads_per_block) p.heads_per_block /= 2;
     auto blocks = [&](int H) { return (H + p.heads_per_block - 1) / p.heads_per_block; };
     auto all = [&] { return blocks(p.x[0].H) + blocks(p.x[1].H) + blocks(p.x[2].H); };
-    p.heads_per_block = 4;
-    while (p.heads_per_block > 1 && bx * all() < 4 * 152) p.heads_per_block /= 2;
     p.blocks[0] = blocks(p.x[0].H);
     p.blocks[1] = blocks(p.x[1].H);
     auto kernel = p.plan.adjacent ? fill_kernel<T, V, U, true, E4M3> : fill_kernel<T, V, U, false, E4M3>;
