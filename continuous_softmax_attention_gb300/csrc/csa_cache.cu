@@ -13,6 +13,7 @@
 // without any exchange between blocks.  The copies are bound by HBM bandwidth.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "csa.h"
@@ -513,8 +514,12 @@ accept_kernel(int *refs, int *table, int *seqlens, const int *parents, const int
 
 // --------------------------------------------------------------- copied rows
 // Row r of a pool of P pages is slot r mod S of page r / S.  A block has one group of
-// pairs in one head of one tensor; it reads a range of columns of all of the group's
-// rows before it writes the first of them, so rows of a group may change places.
+// pairs and a range of the planes (a head of a layer) of one tensor.  Of a plane it
+// reads a range of columns of all of the group's rows before it writes the first of
+// them, so rows of a group may change places.  The pairs that are rows come first, so
+// that a few of many leave no thread idle: as many planes at once as the threads can
+// hold.  What bounds it: with few rows, the two trips to memory (4 of 64 drafted tokens
+// of 64 sequences, 8 layers of 8 heads, d = 128: 8 us, 21 with a block per plane); with many, HBM.
 struct RowTensor {
     uint8_t *at;
     long long bytes;  // of a row
@@ -522,55 +527,78 @@ struct RowTensor {
 };
 struct CopyRowsParams {
     RowTensor x[3];
-    int layers, P, H, S, T;
+    int planes, per_block;  // of a tensor; H to a layer
+    int P, H, S, T;
     const int *src, *dst;
 };
 constexpr int kRowThreads = 256, kRowDeep = 4, kRowMost = 64;
 
+// Pairs [0, n): rows of the first plane.
 template <typename C>
-__device__ __forceinline__ void copy_group(uint8_t *base, long long bytes, const long long (*pair)[2], int T) {
-    const int units = (int)(bytes / (long long)sizeof(C)), per = kRowThreads * kRowDeep / T;  // columns at a time
-    for (int c0 = 0; c0 < units; c0 += per) {
-        const int width = min(per, units - c0);
-        C val[kRowDeep];
+__device__ __forceinline__ void copy_group(const CopyRowsParams &p, const RowTensor &x, const long long (*pair)[2], int n,
+                                           int plane, int end) {
+    constexpr int kHold = kRowThreads * kRowDeep;
+    const int units = (int)(x.bytes / (long long)sizeof(C));
+    const bool whole = units <= kHold / n;
+    const int width = whole ? units : kHold / n, at_once = whole ? kHold / (n * units) : 1;
+    for (; plane < end; plane += at_once)
+        for (int c0 = 0; c0 < units; c0 += width) {
+            const int w = min(width, units - c0), items = min(at_once, end - plane) * n * w;
+            C val[kRowDeep];
+            C *to[kRowDeep];
 #pragma unroll
-        for (int j = 0; j < kRowDeep; ++j) {
-            const int i = threadIdx.x + j * kRowThreads, r = i / width, c = c0 + i - r * width;
-            if (r < T && pair[r][0] >= 0) val[j] = reinterpret_cast<const C *>(base + pair[r][0] * bytes)[c];
-        }
-        __syncthreads();
+            for (int j = 0; j < kRowDeep; ++j) {
+                const int i = threadIdx.x + j * kRowThreads;
+                if (i >= items) break;
+                const int row = i / w, k = row / n, r = row - k * n, layer = (plane + k) / p.H, h = plane + k - layer * p.H;
+                const long long first = ((long long)layer * p.P * p.H + h) * p.S;
+                val[j] = reinterpret_cast<const C *>(x.at + (first + pair[r][0]) * x.bytes)[c0 + i - row * w];
+                to[j] = reinterpret_cast<C *>(x.at + (first + pair[r][1]) * x.bytes) + c0 + i - row * w;
+            }
+            __syncthreads();
 #pragma unroll
-        for (int j = 0; j < kRowDeep; ++j) {
-            const int i = threadIdx.x + j * kRowThreads, r = i / width, c = c0 + i - r * width;
-            if (r < T && pair[r][0] >= 0) reinterpret_cast<C *>(base + pair[r][1] * bytes)[c] = val[j];
+            for (int j = 0; j < kRowDeep; ++j)
+                if (threadIdx.x + j * kRowThreads < items) *to[j] = val[j];
         }
-    }
 }
 
 __global__ void __launch_bounds__(kRowThreads) copy_rows_kernel(const __grid_constant__ CopyRowsParams p) {
-    __shared__ long long pair[kRowMost][2];  // rows of the tensor, or -1
+    __shared__ long long pair[kRowMost][2];
+    __shared__ int some[2];
     after_previous();
-    const int which = blockIdx.y / p.H, h = blockIdx.y - which * p.H, T = p.T;
-    bool some = false;
-    if (threadIdx.x < T) {
-        const int s = p.src[(long long)blockIdx.x * T + threadIdx.x], d = p.dst[(long long)blockIdx.x * T + threadIdx.x];
-        const long long rows = (long long)p.P * p.S;
-        some = s >= 0 && d >= 0 && s < rows && d < rows;
-        if (s >= 0 && d >= 0 && !some) complain();
-        auto row = [&](int r) {
-            return (((long long)blockIdx.z * p.P + r / p.S) * p.H + h) * p.S + r % p.S;
-        };
-        pair[threadIdx.x][0] = some ? row(s) : -1;
-        pair[threadIdx.x][1] = some ? row(d) : -1;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, T = p.T;
+    int s = -1, d = -1;
+    bool moves = false;
+    unsigned all = 0;
+    if (warp < kRowMost / 32) {
+        if (threadIdx.x < T) {
+            s = p.src[(long long)blockIdx.x * T + threadIdx.x];
+            d = p.dst[(long long)blockIdx.x * T + threadIdx.x];
+            const long long rows = (long long)p.P * p.S;
+            moves = s >= 0 && d >= 0 && s < rows && d < rows;
+            if (s >= 0 && d >= 0 && !moves) complain();
+        }
+        all = __ballot_sync(0xffffffffu, moves);
+        if (lane == 0) some[warp] = __popc(all);
     }
-    if (!__syncthreads_or(some)) return;
-    const RowTensor &x = p.x[which];
+    __syncthreads();
+    const int n = some[0] + some[1];
+    if (n == 0) return;
+    if (moves) {
+        const int at = (warp > 0 ? some[0] : 0) + __popc(all & ((1u << lane) - 1));
+        auto row = [&](int r) { return (long long)(r / p.S) * p.H * p.S + r % p.S; };
+        pair[at][0] = row(s);
+        pair[at][1] = row(d);
+    }
+    __syncthreads();
+    const RowTensor &x = p.x[blockIdx.y];
+    const int plane = blockIdx.z * p.per_block, end = min(plane + p.per_block, p.planes);
     if (x.unit == 16)
-        copy_group<uint4>(x.at, x.bytes, pair, T);
+        copy_group<uint4>(p, x, pair, n, plane, end);
     else if (x.unit == 4)
-        copy_group<uint32_t>(x.at, x.bytes, pair, T);
+        copy_group<uint32_t>(p, x, pair, n, plane, end);
     else
-        copy_group<uint8_t>(x.at, x.bytes, pair, T);
+        copy_group<uint8_t>(p, x, pair, n, plane, end);
 }
 
 int from(cudaError_t e) { return e == cudaSuccess ? CSA_OK : CSA_ERR_CUDA; }
@@ -648,20 +676,24 @@ int csa_cache_copy_rows_run(void *k_pages, void *v_pages, long long row_bytes, v
     int tensors = 0;
     void *at[3] = {k_pages, v_pages, row_scales};
     for (int i = 0; i < 3; ++i) {
-        if (!at[i]) continue;
         const long long bytes = i < 2 ? row_bytes : scale_bytes;
+        if (!at[i] || bytes == 0) continue;
         const uintptr_t bits = reinterpret_cast<uintptr_t>(at[i]) | (uintptr_t)bytes;
         p.x[tensors++] = {static_cast<uint8_t *>(at[i]), bytes, bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 1};
     }
-    p.layers = layers;
+    if (tensors == 0) return CSA_OK;
     p.P = P;
     p.H = H;
     p.S = S;
     p.T = T;
     p.src = src;
     p.dst = dst;
-    return from(launch_after_previous(copy_rows_kernel, dim3((unsigned)B, (unsigned)(tensors * H), (unsigned)layers),
-                                      kRowThreads, 0, stream, p));
+    // about as many blocks as run at a time
+    p.planes = layers * H;
+    const int places = std::max(1, 8 * 152 / (int)std::min((long long)B * tensors, 8 * 152ll));
+    p.per_block = (p.planes + places - 1) / places;
+    const dim3 grid((unsigned)B, (unsigned)tensors, (unsigned)((p.planes + p.per_block - 1) / p.per_block));
+    return from(launch_after_previous(copy_rows_kernel, grid, kRowThreads, 0, stream, p));
 }
 
 int csa_cache_take_status(void) {

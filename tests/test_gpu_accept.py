@@ -133,6 +133,21 @@ def test_rows_change_places(d, dtype, T):
     device_status()
 
 
+@pytest.mark.parametrize("B,T,d,dtype", [(700, 3, 128, torch.bfloat16), (300, 20, 64, torch.float32), (130, 64, 96, torch.int8), (650, 9, 256, torch.float32)])
+def test_many_groups(B, T, d, dtype):
+    """More blocks than run at a time: a block has several planes, as many at once as fit, the last time fewer."""
+    g = torch.Generator().manual_seed(B)
+    L, H, S = 3, 5, 8
+    P = B * T // S + 2
+    k = (torch.randn(L, P, H, S, d, generator=g) * 50).to(dtype)
+    order = torch.randperm(P * S, generator=g)[:B * T].view(B, T).int()
+    dst = order[:, torch.randperm(T, generator=g)].contiguous()
+    src = torch.where(torch.rand(B, T, generator=g) < 0.4, -1, order).int()
+    u = k.cuda()
+    cache_copy_rows(u, None, src.cuda(), dst.cuda())
+    assert torch.equal(u.cpu(), moved(k, src.tolist(), dst.tolist(), S)) and device_status() == 0
+
+
 def test_arguments_are_checked():
     m, refs, table, seq = books([5, 5], 6, 4, 2, 4)
     last = torch.tensor([0, 0], **INT)
