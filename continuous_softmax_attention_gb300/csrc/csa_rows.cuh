@@ -2,12 +2,15 @@
 // tokens (csa_tree.cu) where a cached head has more than 16 rows, on tcgen05.  Rows,
 // ranges and parts as in csa_paged.cuh; a block of up to 128 rows is a segment.
 //
-// A CTA per SM is a worker: a contiguous range of tiles of KT cached rows over all
-// segments in a row.  Warps:
-//   0-3, 4-7  softmax: a thread has one lane of tensor memory, and one half of the tile's
-//             columns (at d = 256 there is one half: the sums of two do not fit)
-//   then      the copies (one warp), the tensor core (one lane), and with 8-bit pools two
-//             warps that turn codes into fp16 numbers
+// A CTA is a worker: a contiguous range of tiles of KT cached rows over all segments in
+// a row.  Over bf16 pools two CTAs per SM with tiles of 64 rows, whose phases fall where
+// they may (one CTA with two halves of 128 rows in step: 64 sequences of 300 rows with 8
+// drafted tokens 61 us, so 51); 8-bit pools, which need more warps, and d = 256, whose
+// sums fill half of the tensor memory, have one.  Warps:
+//   softmax   a thread has one lane of tensor memory and one half of the tile's columns
+//             (with bf16 pools and at d = 256 there is one half)
+//   then      the tensor core (one lane), the copies of keys, those of values, and with
+//             8-bit pools the cached rows' scales and four that turn codes into fp16 numbers
 // Tensor memory: S (KT + 16 columns), P of each half (packed 16-bit weights), the sums O
 // of each half.  Each half has its own maximum, weight sum and sums per row.
 //
@@ -20,15 +23,22 @@
 // Fewer than 128 rows: the 128 lanes hold `reps` copies of R = 32 or 64 rows, and copy i
 // weighs the i-th share of each half's columns: the threads always have 128 / reps columns
 // of a tile, none idles, and the tensor core does the copies' products, which it has time
-// for (5 of 11 parts of it at 64 rows).  The columns of the other shares in P are zeros
-// from the start.
+// for (a quarter of it at 64 rows).  The columns of the other shares in P are zeros from
+// the start.
 //
-// What bounds it.  64 rows over bf16 rows of d = 128: HBM bandwidth and the softmax about
-// alike (a tile of 128 rows is 64 KiB, 2.8 kcycles of an SM's share; its 8192 weights about
-// 18 instructions each).  More rows: the weights.
+// Weights over bf16 pools are two bf16 numbers (2^-16); tensor memory has room for one, so
+// the low parts take the high ones' place and have a product of their own, while the next
+// tile's logits are read.  One bf16 number (2^-9 off, where the output is rounded by as
+// much) left o up to 2.7e-3 of its norm off, and two 1.7e-3, which is the output's rounding;
+// it took 88 us where two take 100 (below).  Over 8-bit pools a weight is one fp16 number
+// (2^-12), and o is 1.6e-3 off.  All carry the factor (ln 2)^2, removed where parts are
+// written.
 //
-// Weights are single 16-bit numbers, as csa_forward's: bf16 (2^-8) over bf16 pools, fp16
-// (2^-11) over 8-bit ones.  All carry the factor (ln 2)^2, removed where parts are written.
+// What bounds it: the weights, 24 instructions each of which 16 are the formula's; with two
+// softmax warps per scheduler the issue slots are 56% busy.  16 sequences of 4096 to 8192
+// rows, 32 heads on 8, d = 128 (400 MB, 60 us at the copy bandwidth), with the join:
+// 4 drafted tokens 76 us, 8 85 us, 16 102 us, 32 152 us, 64 294 us; e4m3 (210 MB) 5 96 us,
+// 16 128 us, 32 165 us, int8 16 137 us; d = 64 16 82 us; d = 256 16 182 us.
 #pragma once
 
 #include <type_traits>
@@ -209,6 +219,17 @@ __device__ __forceinline__ void weights16(const float (&u)[17], float &Lc, int c
         before = q1;
     }
     Lc = before;
+}
+
+// Two weights as bf16 numbers hi + lo, right within 2^-16 of each.  The high part is cut off, so that neither is negative
+// and the low one is at least 2^-23 of the weight: an infinite value stays one.
+__device__ __forceinline__ void split(Two w, uint32_t &hi, uint32_t &lo) {
+    float a, c, la, lc;
+    apart(w, a, c);
+    const uint32_t ua = __float_as_uint(a), uc = __float_as_uint(c);
+    hi = __byte_perm(ua, uc, 0x7632);
+    apart(fma2(w, both(1.00000011920928955f), two(-__uint_as_float(ua & 0xffff0000u), -__uint_as_float(uc & 0xffff0000u))), la, lc);
+    lo = pack_bf16x2(la, lc);
 }
 
 // CW: a thread's columns of a half: 64 for 128 rows, 32 for two copies of 64, 16 for four of 32.
@@ -413,6 +434,24 @@ rows_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUten
                 carry = sum * p.qscale;
             }
             bool bad = false;
+            // bf16: the low parts of the tile before's weights, for the second of its two products
+            uint32_t low[EIGHT ? 1 : CW / 2];
+            auto second = [&]() {  // false: give up
+                if (!(ok = __all_sync(0xffffffffu, wait(o_done(h), 2 * tiles - 2)))) return false;
+                tc_fence_after();
+                if constexpr (!EIGHT) {
+#pragma unroll
+                    for (int e = 0; e < CW / 2; e += 8) {
+                        const uint32_t part[8] = {low[e], low[e + 1], low[e + 2], low[e + 3], low[e + 4], low[e + 5], low[e + 6], low[e + 7]};
+                        tm_st8(tP + rep * CW / 2 + e, part);
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full(h));
+                return true;
+            };
             // a tile; false: give up.  MASKED: not all of its intervals exist.
             auto tile = [&](int j, auto masked) -> bool {
                 constexpr bool MASKED = decltype(masked)::value;
@@ -517,17 +556,23 @@ rows_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUten
                     }
                 }
                 const bool over = top > m + (EIGHT ? kRaise8 : kRaise);
+                // The low parts of the tile before, when its first product is done: with 64 columns after the interval
+                // before them (152 us for 32 drafted tokens as above, 164 here), else here (two places spill registers:
+                // 112 us for 16 drafted, so 100)
+                bool given = EIGHT || j == now.tile;
+                auto give = [&]() { return given || (given = second()); };
+                if (CW < 64 && !give()) return false;
                 bool free = j == now.tile;  // PV of the tile before is done: P can be written, and O can change
                 auto wait_free = [&]() {
                     if (!free) {
-                        ok = __all_sync(0xffffffffu, wait(o_done(h), tiles - 1));
+                        ok = __all_sync(0xffffffffu, wait(o_done(h), EIGHT ? tiles - 1 : 2 * tiles - 1));
                         tc_fence_after();
                         free = true;
                     }
                     return ok;
                 };
                 if (__any_sync(0xffffffffu, over || f_lift != 1.0f)) {
-                    if (!wait_free()) return false;
+                    if ((CW == 64 && !give()) || !wait_free()) return false;
                     const float to = over ? top : m, f = m == -INFINITY ? 0.0f : ex2_approx(m - to);
                     m = to;
                     l *= f;
@@ -573,8 +618,10 @@ rows_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUten
                         }
                     }
                 }
+                if (CW == 64 && !give()) return false;
                 Two sum = both(0.0f);
-                auto chunk = [&](const uint32_t (&x)[16], uint32_t xn, int col, uint32_t (&pk)[8]) {
+                // `at`: of `low`
+                auto chunk = [&](const uint32_t (&x)[16], uint32_t xn, int col, int at, uint32_t (&pk)[8]) {
                     float u[17];
 #pragma unroll
                     for (int e = 0; e < 16; e += 2) apart(fma2(two(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), both(unit), both(nm)), u[e], u[e + 1]);
@@ -593,8 +640,13 @@ rows_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUten
                         float a, c, d, f;
                         apart(W[e], a, c);
                         apart(W[e + 1], d, f);
-                        pk[e] = EIGHT ? pack_f16x2(a, c) : pack_bf16x2(a, c);
-                        pk[e + 1] = EIGHT ? pack_f16x2(d, f) : pack_bf16x2(d, f);
+                        if constexpr (EIGHT) {
+                            pk[e] = pack_f16x2(a, c);
+                            pk[e + 1] = pack_f16x2(d, f);
+                        } else {
+                            split(W[e], pk[e], low[at + e]);
+                            split(W[e + 1], pk[e + 1], low[at + e + 1]);
+                        }
                     }
                 };
 #pragma unroll 1
@@ -618,7 +670,7 @@ rows_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUten
                     };
                     if constexpr (CW == 16) {
                         uint32_t pk[8];
-                        chunk(xa, behind, c0, pk);
+                        chunk(xa, behind, c0, 0, pk);
                         if (!store(pk, 0)) return false;
                     } else if constexpr (EIGHT) {
                         // the second 16 by the first's instructions: with the turning and the scales two copies of them
@@ -627,15 +679,15 @@ rows_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUten
 #pragma unroll 1
                         for (int e = 0; e < 32; e += 16) {
                             uint32_t pk[8];
-                            chunk(xa, e == 0 ? xb[0] : behind, c0 + c + e, pk);
+                            chunk(xa, e == 0 ? xb[0] : behind, c0 + c + e, 0, pk);
                             if (!store(pk, c + e)) return false;
 #pragma unroll
                             for (int k = 0; k < 16; ++k) xa[k] = xb[k];
                         }
                     } else {
                         uint32_t pk[8], pl[8];
-                        chunk(xa, xb[0], c0 + c, pk);
-                        chunk(xb, behind, c0 + c + 16, pl);
+                        chunk(xa, xb[0], c0 + c, c / 2, pk);
+                        chunk(xb, behind, c0 + c + 16, c / 2 + 8, pl);
                         if (!store(pk, c) || !store(pl, c + 16)) return false;
                     }
                 }
@@ -662,8 +714,8 @@ rows_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUten
             };
             for (int j = now.tile; ok && j < now.last; ++j, ++tiles)
                 if (!(n - j * KT > KT ? tile(j, std::false_type{}) : tile(j, std::true_type{}))) ok = false;
-            if (!ok) break;
-            if (!(ok = __all_sync(0xffffffffu, wait(o_done(h), tiles - 1)))) break;
+            if (!ok || (!EIGHT && !second())) break;
+            if (!(ok = __all_sync(0xffffffffu, wait(o_done(h), EIGHT ? tiles - 1 : 2 * tiles - 1)))) break;
             tc_fence_after();
             // ---- the copies and halves of a row joined: maxima, then sums, XC columns at a time
             const bool all_rows = r0 == 0 && min(n, now.last * KT) == n;
@@ -761,25 +813,42 @@ rows_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUten
         };
         do {
             if (lane == 0) {
-                ok = awake(q_full, parts) && issue_s();
-                for (int j = now.tile; ok && j < now.last; ++j) {
-                    if (j + 1 < now.last && !(ok = issue_s())) break;
-                    const int stage = tiles_o % NS;
-                    if (!(ok = awake(EIGHT ? v_ready(tiles_o % C::NV) : v_full(stage), tiles_o / (EIGHT ? C::NV : NS)))) break;
-                    const uint64_t vd = v_desc + (EIGHT ? (tiles_o % C::NV) * (C::VBytes >> 4) : stage * (C::StageBytes >> 4));
-                    for (int h = 0; h < H && ok; ++h) {
-                        if (!(ok = awake(p_full(h), tiles_o))) break;
-                        tc_fence_after();
+                // the product of half h's weights with the values at vd, onto sums that there are already or not
+                auto product = [&](int h, uint64_t vd, bool onto) {
+                    tc_fence_after();
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            tc_mma_ts(tmem + C::ColO + D * h, tmem + C::ColP + 32 * h + 8 * k,
-                                      vd + (((64 * h + 16 * k) * 128) >> 4), idesc_o,
-                                      j > now.tile || k > 0 ? 1u : 0u);
-                        tc_commit(o_done(h));
+                    for (int k = 0; k < 4; ++k)
+                        tc_mma_ts(tmem + C::ColO + D * h, tmem + C::ColP + 32 * h + 8 * k, vd + (((64 * h + 16 * k) * 128) >> 4), idesc_o,
+                                  onto || k > 0 ? 1u : 0u);
+                    tc_commit(o_done(h));
+                };
+                ok = awake(q_full, parts) && issue_s();
+                if constexpr (EIGHT) {
+                    for (int j = now.tile; ok && j < now.last; ++j) {
+                        if (j + 1 < now.last && !(ok = issue_s())) break;
+                        const int buf = tiles_o % C::NV;
+                        if (!(ok = awake(v_ready(buf), tiles_o / C::NV))) break;
+                        for (int h = 0; h < H && ok; ++h)
+                            if ((ok = awake(p_full(h), tiles_o))) product(h, v_desc + buf * (C::VBytes >> 4), j > now.tile);
+                        if (!ok) break;
+                        tc_commit(v_free(buf));
+                        ++tiles_o;
                     }
-                    if (!ok) break;
-                    tc_commit(EIGHT ? v_free(tiles_o % C::NV) : v_empty(stage));
-                    ++tiles_o;
+                } else {  // the low parts of a tile's weights follow while the next one's logits are read
+                    auto values = [&](int t) { return v_desc + t % NS * (C::StageBytes >> 4); };
+                    auto second = [&]() {
+                        if (!(ok = awake(p_full(0), 2 * tiles_o - 1))) return;
+                        product(0, values(tiles_o - 1), true);
+                        tc_commit(v_empty((tiles_o - 1) % NS));
+                    };
+                    for (int j = now.tile; ok && j < now.last; ++j) {
+                        if (j > now.tile) second();
+                        if (!ok || (j + 1 < now.last && !(ok = issue_s()))) break;
+                        if (!(ok = awake(v_full(tiles_o % NS), tiles_o / NS) && awake(p_full(0), 2 * tiles_o))) break;
+                        product(0, values(tiles_o), j > now.tile);
+                        ++tiles_o;
+                    }
+                    if (ok) second();
                 }
             }
             ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;

@@ -140,13 +140,12 @@ def bounds8(q, k, v, ref_o, ref_lse, scale):
 
 
 def bounds_tree(kind, rows, q, k, v, ref_o, ref_lse, scale):
-    """A row of a tree, `rows` = T times the query heads on a cached head.  Up to 16 of them: weights over bf16 pools are
-    two bf16 numbers (2^-16), over 8-bit ones as bounds8.  Above: one bf16 (2^-8) or fp16 number, and an interval's integral
-    is divided between its two rows within 4e-4 < 2^-11 of the smaller share (the error of the quotients is relative
+    """A row of a tree, `rows` = T times the query heads on a cached head.  Weights over bf16 pools are two bf16 numbers
+    (2^-16), over 8-bit ones as bounds8.  Above 16 rows an interval's integral is divided between its two rows within 4e-4 < 2^-11 of the smaller share (the error of the quotients is relative
     to the left share, and the right one is the rest): that moves the numerator by at most 4e-4 times the share times the
     difference of two values, in all by at most 2 * 4e-4 / 2 max |v|, since the smaller shares are at most half of the sum."""
     if kind != "bf16":
         if rows <= 16:
             return bounds8(q, k, v, ref_o, ref_lse, scale)
         return bounds(q, k, v, ref_o, ref_lse, scale, 2.0 ** -10 + len(k) * 2.0 ** -26)
-    return bounds(q, k, v, ref_o, ref_lse, scale, 2.0 ** -16 if rows <= 16 else 2.0 ** -8 + 2.0 ** -11)
+    return bounds(q, k, v, ref_o, ref_lse, scale, 2.0 ** -16 + (2.0 ** -11 if rows > 16 else 0.0))
