@@ -40,6 +40,15 @@
 //    (537 MB, 16 heads per group, d = 64), 98.2 of 97.2 (d = 128), 113.9 of 107.6
 //    (d = 256), 60.4 of 59.8 (64 ragged sequences), 5.8 of 5.7 (one short one):
 //    two numbers are kept.
+//  - Over 8-bit pools a tile is 32 rows: codes become fp16 numbers in registers (keys as
+//    16-byte reads with the products' columns dealt to fit, values by an 8-bit ldmatrix),
+//    the queries are fp16 numbers times a power of two, and a row's scales multiply its
+//    logits and weights.  With half the bytes per row it is bound by the instructions of two
+//    warps per scheduler, 32% of the issue slots, waiting on one another's results (16-row
+//    tiles with 12 or 10 workers: 182 and 210 us where 8 workers of 32 took 160; 32-row
+//    tiles with 12 workers spill, 224).  821 MB of 32 heads, e4m3, take 136 us (90% of the
+//    copy bandwidth), int8, whose codes take five instructions per four where e4m3 takes
+//    three, 157; 205 MB of 8 heads with 4 query heads each 47 and 53.
 //  - Few short sequences are bound by latency: a cluster of blocks then does one
 //    cached head of one sequence in a single launch and joins its parts through
 //    distributed shared memory (8.7 -> 5.8 us for 32 heads of 333 tokens).

@@ -14,7 +14,10 @@
 // Rows with max|x| < 2^-100 are zeros; a row with an infinity or NaN gets the scale
 // NaN and codes 0, so that what reads it shows it.
 //
-// What bounds it.  Each value is read once and each code written once: HBM bandwidth.
+// What bounds it.  Each value is read once and each code written once: HBM bandwidth, and
+// the instructions of the rotation (issue slots 60% busy).  8 x up to 2048 tokens, 32 heads
+// on 8, d = 128 (330 MB) take 58 us, 85% of the copy bandwidth; 64 single tokens 3.2 us.
+// Reading back is a copy: 754 MB of int8 rows as bf16 take 114 us, 99%; 25 MB 6.1 us.
 // A power of two of lanes owns a row, 16 bytes twice per lane as in csa_rope.cu (the
 // two members of 8 bf16 or 4 fp32 pairs), holds it in registers between the maximum
 // and the codes, and walks over a range of heads with the token's sines and cosines.

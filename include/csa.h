@@ -526,8 +526,8 @@ long long csa_decode_paged_workspace_bytes(int B, int Hq, int Hkv, int d);
  *   csa_decode_tree_workspace_bytes(B, Hq, Hkv, T, d) bytes, 16-byte aligned, contents
  *   on entry irrelevant; calls that can run at the same time need distinct ones.
  *   Alignment, other refusals, and what decides the last bits as csa_decode_paged.
- *   With more than 16 rows per cached head (T times the query heads on it) the
- *   weights are single 16-bit numbers, as csa_forward's.
+ *   Weights over bf16 pools are sums of two bf16 numbers; over 8-bit ones, with more
+ *   than 8 rows per cached head (T times the query heads on it), one fp16 number.
  */
 #define CSA_TREE_MAX 64
 int csa_decode_tree(const void *q, const void *k_pages, const void *v_pages,
