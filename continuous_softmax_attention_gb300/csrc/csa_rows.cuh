@@ -23,8 +23,8 @@
 // Fewer than 128 rows: the 128 lanes hold `reps` copies of R = 32 or 64 rows, and copy i
 // weighs the i-th share of each half's columns: the threads always have 128 / reps columns
 // of a tile, none idles, and the tensor core does the copies' products, which it has time
-// for (a quarter of it at 64 rows).  The columns of the other shares in P are zeros from
-// the start.
+// for (a quarter of it at 64 rows).  The columns of the other shares in P are next to zero
+// from the start.
 //
 // Weights over bf16 pools are two bf16 numbers (2^-16); tensor memory has room for one, so
 // the low parts take the high ones' place and have a product of their own, while the next
@@ -361,8 +361,9 @@ rows_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUten
         const int rep = i / R, row = i - rep * R;  // a warp has one copy
         const int c0 = 64 * h + rep * CW;          // this thread's columns
         const float *ring = reinterpret_cast<const float *>(smem + C::OffScales);  // [4 tiles][of keys, of values][KR]
-        {  // the other copies' columns of P stay zero
-            const uint32_t zero[8] = {};
+        {  // the other copies' columns of P stay as good as zero: 2^-126 over bf16 pools, as 0 times infinity is not infinity
+            constexpr uint32_t z = EIGHT ? 0u : 0x00800080u;
+            const uint32_t zero[8] = {z, z, z, z, z, z, z, z};
             for (int j = 0; j < 4; ++j) tm_st8(tP + 8 * j, zero);
             tmem_wait_st();
         }
@@ -757,7 +758,7 @@ rows_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUten
                     float y[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        y[k] = __uint_as_float(e < 4 ? xa[(4 * e + k) & 15] : xb[(4 * e + k) & 15]) * fo;
+                        y[k] = fo == 0.0f ? 0.0f : __uint_as_float(e < 4 ? xa[(4 * e + k) & 15] : xb[(4 * e + k) & 15]) * fo;
                         if (given) y[k] = fmaf(w_sink * f, __bfloat162float(p.v0[(long long)hk * D + c + 4 * e + k]), y[k]);
                     }
                     X[place(h * 128 + i, e)] = make_float4(y[0], y[1], y[2], y[3]);

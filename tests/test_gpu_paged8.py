@@ -40,7 +40,7 @@ def run(x, mode=0, scale=None, **kw):
     return o, lse
 
 
-def check(x, o, lse, S, mode, scale, only=None):
+def check(x, o, lse, S, mode, scale, only=None, heads=None):
     B, Hq, d = x["q"].shape
     Hkv = x["k"].shape[1]
     vk, vv = values(x["k"], x["v"], x["scales"])
@@ -51,7 +51,7 @@ def check(x, o, lse, S, mode, scale, only=None):
             assert (o[b] == 0).all() and np.isneginf(lse[b]).all()
             continue
         k, v = (rows_of(t, x["table"][b], n, S) for t in (vk, vv))
-        for h in range(Hq):
+        for h in range(Hq) if heads is None else heads:
             hk = h // (Hq // Hkv)
             q = torch.zeros(1, 1, n, d, dtype=torch.float64)
             q[0, 0, n - 1] = x["q"][b, h].double()
@@ -77,6 +77,35 @@ def test_lengths_around_every_edge(kind, d, mode, S, wide):
     x = make(kind, EDGES, 2, 1, d, S, seed=d + S + mode, wide=wide)
     o, lse = run(x, mode)
     check(x, o, lse, S, mode, d ** -0.5)
+
+
+@EIGHT
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("mode", [0, 1, 2])
+@pytest.mark.parametrize("Hq", [1, 3, 4, 7])
+@FORMS
+def test_edges_with_any_number_of_copies_of_the_heads(kind, d, mode, Hq, wide):
+    """Eight rows hold a head eight times, two four times, up to four twice and more once."""
+    x = make(kind, EDGES + [1000], Hq, 1, d, 16, seed=Hq + mode, wide=wide)
+    o, lse = run(x, mode)
+    check(x, o, lse, 16, mode, d ** -0.5)
+
+
+@EIGHT
+@pytest.mark.parametrize("Hq", [1, 2, 4, 6])
+def test_a_head_does_not_see_the_others(kind, Hq):
+    """Heads of a group share products: one with NaN for a query, or with far larger logits, leaves the others right.  Not
+    bit for bit: all heads of a product raise the maximum that their weights are relative to when one of them passes its
+    own, and a sum times 2^x, x not whole, is another fp32 number than the sum of the terms times it (each within 2^-22, of
+    which `bounds8` allows (d + 8) 2^-24 A + 2^-16)."""
+    x = make(kind, [700, 33], Hq, 1, 128, 16, seed=4, wide=True)
+    for h in range(Hq):
+        for factor in (float("nan"), 64.0):
+            y = dict(x, q=x["q"].clone())
+            y["q"][:, h] *= factor
+            o, lse = run(y, 0)
+            check(x, o, lse, 16, 0, 128 ** -0.5, heads=[i for i in range(Hq) if i != h])
+            assert torch.isnan(o[:, h].float()).all() if factor != factor else torch.isfinite(o[:, h].float()).all()
 
 
 @EIGHT

@@ -198,6 +198,61 @@ def test_infinite_values_on_the_path_pass_through():
     assert torch.isfinite(o[..., 7:].float()).all()
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("T", [24, 64])
+def test_infinite_values_with_many_rows(d, T):
+    """Weights over bf16 pools are two numbers, neither of which may be 0 where the weight is not."""
+    x = make("bf16", [300], [T], T, 2, 1, d, 16, seed=d)
+    want, _ = run(x, 0, 0.5)
+    for at, value in ((0, "inf"), (63, "-inf"), (64, "inf"), (200, "-inf"), (299, "inf")):
+        y = dict(x, v=x["v"].clone())
+        y["v"][x["table"][0][at // 16], 0, at % 16, 5] = float(value)
+        o, _ = run(y, 0, 0.5)
+        assert (o[..., 5].float() == float(value)).all(), at
+        rest = [i for i in range(d) if i != 5]
+        # The last row before the draft is also the tree's first position, whose values' infinities are summed one by one
+        # with weights of 32 bits instead of two bf16 numbers (2^-16 of max |v|); and both sums are rounded, by half a step of
+        # 2^-7 each.
+        off = 2.0 ** -7 * want.float().abs() + 2.0 ** -16 * x["v"].float().abs().max().item() if at == 299 else 0.0
+        assert ((o.float() - want.float()).abs() <= off)[..., rest].all(), at
+
+
+@KIND
+@pytest.mark.parametrize("d,B,Hkv,T,G", [(128, 40, 8, 64, 2), (256, 30, 8, 64, 2), (64, 60, 6, 31, 6), (256, 128, 8, 5, 3)])
+def test_many_groups_of_rows(kind, d, B, Hkv, T, G):
+    """More blocks than a few rounds of the GPU: a block then does several groups of rows.  Sequences of one tile
+    (of 16 rows over bf16 pools with up to 16 rows per cached head, else of 32 and more) have the same parts in any batch,
+    so the results are those of small batches bit for bit."""
+    r = np.random.default_rng(d)
+    past, counts = [int(n) for n in r.integers(0, 33, B)], [int(n) for n in r.integers(0, T + 1, B)]
+    x = make(kind, past, counts, T, G * Hkv, Hkv, d, 8, seed=B)
+    c = dev(x)
+    o, lse = call(c, 1)
+    for b in range(0, B, 10):
+        part = slice(b, b + 2)
+        few = dict(c, **{n: c[n][part].contiguous() for n in ("q", "table", "lens", "counts", "parents")})
+        of, lf = call(few, 1)
+        one = [n <= (16 if kind == "bf16" and G * T <= 16 else 32) for n in past[part]]
+        assert torch.equal(o[part][one], of[one]) and torch.equal(lse[part][one], lf[one])
+    check(x, o, lse, 1, only=(1, B - 1), nodes={0, T // 2, T - 1}, heads=(0, G * Hkv - 1))
+
+
+def test_calls_of_other_sizes_at_once():
+    """Kernels with other shares of an SM's tensor memory, registers and shared memory beside one another."""
+    calls = []
+    for kind, d, T, G in (("bf16", 128, 16, 4), ("bf16", 256, 64, 1), ("e4m3", 64, 31, 4), ("int8", 256, 20, 1), ("bf16", 64, 3, 2), ("e4m3", 128, 64, 2)):
+        c = dev(make(kind, [900, 40, 0, 2000], [T] * 4, T, 2 * G, 2, d, 16, seed=d + T))
+        o, lse = call(c)
+        torch.cuda.synchronize()
+        calls.append((c, o, lse, torch.cuda.Stream()))
+    got = [[call(c, stream=s) for c, _, _, s in calls] for _ in range(8)]
+    torch.cuda.synchronize()
+    for some in got:
+        for (c, o, lse, _), (a, b) in zip(calls, some):
+            assert torch.equal(o, a) and torch.equal(lse, b)
+    assert device_status() == 0
+
+
 @KIND
 @pytest.mark.parametrize("G", [1, 8])
 def test_bad_lengths_pages_and_parents_are_reported(kind, G):
