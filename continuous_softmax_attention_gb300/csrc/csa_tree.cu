@@ -547,7 +547,8 @@ int launch_tree_of(TreeParams &p, int d, cudaStream_t stream) {
 
 // Rows of a cached head above which they go to the kernel of csa_rows.cuh: at 17 the other one reads the cache twice.
 // 16 sequences of 4096 to 8192 rows, 8 cached heads, d = 128, 17 rows: 83 us here and 125 there (e4m3 96 and 116, int8
-// 108 and 125), 48 rows 99 and 175; d = 64, 32 rows 65 and 96; d = 256 161 and 283.
+// 108 and 125), 48 rows 99 and 175; d = 64, 32 rows 65 and 96; d = 256 161 and 283;
+// one sequence of 333 rows 11.9 and 13.5, of 2000 17.9 and 17.0.
 constexpr int kMany = 16;
 
 // Where the parts lie: notes, maxima and sums, unnormalised outputs.
