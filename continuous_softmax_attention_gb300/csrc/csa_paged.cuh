@@ -295,7 +295,7 @@ struct Lengths {
         const int n = seqlens[b];
         if (T == 0) return n;
         const int c = counts ? counts[b] : T;
-        return c < 0 || c > T || n < c || n > most ? -1 : n - c;
+        return c < 0 || c > T || n < c || n > most ? -1 : c == 0 ? 0 : n - c;  // without a drafted token, nothing to do
     }
 };
 

@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeBlocks<D>) tree_kernel(cons
     ask_queries(first, min(p.RB, last_row - first));
     const int len = p.seqlens[b], c = p.counts ? p.counts[b] : p.T, n = len - c;
     const bool sound = c >= 0 && c <= p.T && n >= 0 && len <= (long long)p.M * p.S;
-    const int have = sound ? c + 1 : 0;  // position 0 is the last one before the draft, 1 + u is drafted token u
+    const int have = sound && c > 0 ? c + 1 : 0;  // position 0 is the last one before the draft, 1 + u is drafted token u
     bool lost = false, wild = false;     // a page out of range; values that are not finite
     if (warp < 2) {
         int up = tid >= p.T ? -1 : p.parents ? p.parents[(long long)b * p.T + tid] : tid - 1;
@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(kTreeThreads, kTreeBlocks<D>) tree_kernel(cons
             after_previous();
             // the parts of the tokens before the draft
             const int4 seg = p.joins[segment];
-            const bool any = n > 0;
+            const bool any = n > 0 && c > 0;
             if (any && (seg.x != segment || seg.y < -1 || (seg.y >= 0 && (seg.z < seg.y || seg.z >= p.workers))))
                 return;  // left over, where a wait has run out and the parts are undefined
             auto slot_of = [&](int cc) {

@@ -515,7 +515,8 @@ long long csa_decode_paged_workspace_bytes(int B, int Hq, int Hkv, int d);
  *   [B, Hq, T] or NULL.  parents: int32 [B, T], the parent of node t < counts[b],
  *   -1 (it follows the tokens before the draft) or a node below t; NULL: t - 1 each.
  *   counts: int32 [B], 0 <= counts[b] <= min(T, seqlens[b]); NULL: T each.  Rows
- *   t >= counts[b] get out = 0 and lse = -inf; their q and parents do not matter.
+ *   t >= counts[b] get out = 0 and lse = -inf; their q and parents do not matter.  Of a
+ *   sequence with counts[b] = 0 no page is read.
  *   n = 0: the sink is followed by a root (CSA_K0_COPY_FIRST: a copy of the row's own
  *   root).  Pools, row_scales, k0, v0, block_table, scale and k0_mode as
  *   csa_decode_paged (kind CSA_BF16, row_scales NULL) and csa_decode_paged_q8.

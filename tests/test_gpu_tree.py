@@ -282,6 +282,19 @@ def test_bad_lengths_pages_and_parents_are_reported(kind, G):
 
 
 @KIND
+@pytest.mark.parametrize("T,G", [(3, 1), (6, 8)])
+def test_sequences_without_a_draft_are_passed_over(kind, T, G):
+    x = make(kind, [500, 3000, 1, 40], [T, 0, 0, T - 1], T, 2 * G, 2, 128, 16, seed=15)
+    x["table"][1, :], x["table"][2, :] = -1, 10 ** 6  # their pages are not looked at
+    o, lse = run(x, 1)
+    check(x, o, lse, 1, heads=(0, 2 * G - 1), only=(0, 3))
+    assert (o[1:3] == 0).all() and torch.isneginf(lse[1:3]).all() and device_status() == 0
+    x.update(counts=[0] * 4, lens=[500, 3000, 0, 40])
+    o, lse = run(x, 1)
+    assert (o == 0).all() and torch.isneginf(lse).all() and device_status() == 0
+
+
+@KIND
 @pytest.mark.parametrize("T", [3, 20])
 def test_repeats_bit_for_bit_on_stale_workspaces(kind, T):
     x = make(kind, [3000, 17, 0, 900], [T] * 4, T, 8, 2, 128, 32, seed=12)
