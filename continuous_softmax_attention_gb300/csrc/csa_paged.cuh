@@ -321,7 +321,8 @@ struct Cut {
 
 // at[0 .. blockDim.x] gets the units (per head) of the sequences before each
 // thread's chunk of sequences, the last entry the total.  Whole block.
-__device__ Cut form_cut(const Lengths &seqlens, int B, int KT, long long most, int heads, long long all, long long *at) {
+__device__ Cut form_cut(const Lengths &seqlens, int B, int KT, long long most, int heads, long long all, int part_cost,
+                        long long *at) {
     const int tid = threadIdx.x, per = (B + blockDim.x - 1) / blockDim.x;
     const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
     long long tiles = 0;
@@ -361,7 +362,7 @@ __device__ Cut form_cut(const Lengths &seqlens, int B, int KT, long long most, i
         some_total += some_sums[w];
     }
     Cut cut;
-    cut.cost = total * heads > kFew * all ? kPartCost : 0;
+    cut.cost = total * heads > kFew * all ? part_cost : 0;
     at[tid] = before + s - tiles + (long long)cut.cost * (some_before + c - some);
     if (tid == (int)blockDim.x - 1) at[blockDim.x] = total + (long long)cut.cost * some_total;
     __syncthreads();
@@ -388,7 +389,7 @@ __device__ __forceinline__ int find_sequence(long long u, const Cut &cut, const 
 
 // The cut of up to 32 sequences by a warp on its own, without a barrier of the
 // block: lane b holds the units (per head) before sequence b.
-__device__ __forceinline__ Cut form_cut_warp(int n, int KT, long long most, int heads, long long all,
+__device__ __forceinline__ Cut form_cut_warp(int n, int KT, long long most, int heads, long long all, int part_cost,
                                              long long &before) {
     const int lane = threadIdx.x & 31, tiles = tiles_of(n, KT, most);
     const unsigned some = __ballot_sync(0xffffffffu, tiles > 0);
@@ -400,7 +401,7 @@ __device__ __forceinline__ Cut form_cut_warp(int n, int KT, long long most, int 
     }
     const long long total = __shfl_sync(0xffffffffu, s, 31);
     Cut cut;
-    cut.cost = total * heads > kFew * all ? kPartCost : 0;
+    cut.cost = total * heads > kFew * all ? part_cost : 0;
     before = s - tiles + cut.cost * __popc(some & ((1u << lane) - 1));
     cut.U = (total + cut.cost * __popc(some)) * heads;
     cut.in_use = cut.U < all ? cut.U : all;
@@ -547,8 +548,8 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         const long long all = (long long)C::Workers * gridDim.x;
         long long lane_before = 0;
-        cut = few ? form_cut_warp(lane_n, KT, most, heads, all, lane_before)
-                  : form_cut(lens, p.B, KT, most, heads, all, s_cut);
+        cut = few ? form_cut_warp(lane_n, KT, most, heads, all, kPartCost, lane_before)
+                  : form_cut(lens, p.B, KT, most, heads, all, kPartCost, s_cut);
         // sequences without rows, and lengths out of range
         for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
             const int n = lens[b];

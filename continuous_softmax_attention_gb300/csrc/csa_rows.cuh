@@ -37,8 +37,8 @@
 // What bounds it: the weights, 24 instructions each of which 16 are the formula's; with two
 // softmax warps per scheduler the issue slots are 56% busy.  16 sequences of 4096 to 8192
 // rows, 32 heads on 8, d = 128 (400 MB, 60 us at the copy bandwidth), with the join:
-// 4 drafted tokens 76 us, 8 85 us, 16 102 us, 32 152 us, 64 294 us; e4m3 (210 MB) 5 96 us,
-// 16 128 us, 32 165 us, int8 16 137 us; d = 64 16 82 us; d = 256 16 182 us.
+// 4 drafted tokens 76 us, 8 85 us, 16 99 us, 32 152 us, 64 293 us; e4m3 (210 MB) 5 96 us,
+// 16 128 us, 32 165 us, int8 16 137 us; d = 64 16 82 us; d = 256 16 181 us.
 #pragma once
 
 #include <type_traits>
@@ -134,6 +134,10 @@ struct RowsCfg {
     static constexpr int Halves = D == 256 || !Eight ? 1 : 2;
     static constexpr int Blocks = Eight || D == 256 ? 1 : 2;  // per SM
     static constexpr int KT = 64 * Halves;   // cached rows per tile
+    // What beginning and ending a part costs, in tiles.  64 ragged sequences of 1 to 8192 rows, 32 heads on 8, 8 drafted
+    // tokens, d = 128: 104 us with 2, 84 with 4, 80 with 6, 85 with 12; e4m3 (tiles of 128 rows) 129 with 2, 107 with 4,
+    // 102 with 6, 111 with 8; 16 drafted, d = 256 (one block per SM) 207 with 4, 185 with 6, 178 with 8, 196 with 12.
+    static constexpr int PartCost = !Eight && D == 256 ? 8 : 6;
     static constexpr int KR = KT + 16;       // and those of K: 8 behind, 8 before
     // warps: the softmax, the tensor core, the copies of keys and of values (which wait for different products, so each
     // has a warp), with 8 bits the cached rows' scales (else a spare one), and the four that turn codes into fp16 numbers
@@ -316,8 +320,8 @@ rows_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUten
         const int lane_n = few && lane < p.B ? lens[lane] : 0;
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         long long lane_before = 0;
-        cut = few ? form_cut_warp(lane_n, KT, most, heads, gridDim.x, lane_before)
-                  : form_cut(lens, p.B, KT, most, heads, gridDim.x, s_cut);
+        cut = few ? form_cut_warp(lane_n, KT, most, heads, gridDim.x, C::PartCost, lane_before)
+                  : form_cut(lens, p.B, KT, most, heads, gridDim.x, C::PartCost, s_cut);
         for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
             const int n = lens[b];
             if (n > 0 && n <= most) continue;
