@@ -183,11 +183,15 @@ __host__ __device__ constexpr uint32_t rows_idesc(bool bf16, int N, bool b_mn_ma
 // below it end intervals that exist.  W: pairs of columns.
 //
 // An interval from u0 to u1, X = u1 - u0, p = 2^u, has the integral S and gives R to its left and S - R to its right column:
-//   |X| >= 1/16   S ln 2 = (p1 - p0) / X,   R = ((p1 - p0) / X - p0 ln 2) / X
+//   |X| >= 0.11   S ln 2 = (p1 - p0) / X,   R = ((p1 - p0) / X - p0 ln 2) / X
 //   else          S ln 2 = (p0 + p1) (ln 2) / 2 * (1 - (X ln 2)^2 / 12),   R = (ln 2)^2 (2 p0 + p1) / 6 + its share of the rest
-// as one sequence of operations with other coefficients.  S, of which the weight sum is made, is right within 2^-16.5 (the
-// exponentials' 2^-22 over X; mostly far better), the division between the two columns within 4e-4, where a weight is
-// rounded by 2^-9 (bf16) or 2^-12 (fp16) on average anyway.
+// as one sequence of operations with other coefficients.  The quotients make the exponentials' 2^-22 as much larger as X is
+// small, twice over in R; the series leaves out (X ln 2)^2 / 72 of 1/2 in R, always towards the left, and less than 2^-21 of
+// S.  Just above the border R is off by 2.1e-4 of itself and S by 8e-6 (2^-16.9) at most, just below it R by 1.7e-4; with the
+// border at 1/16 these were 6.4e-4, 1.4e-5 (2^-16.2) and 5e-5, at 0.14 1.3e-4, 6e-6 and 2.7e-4.  The exponentials are mostly
+// better than 2^-22: equal intervals of values -1 and 1 move o by up to 8e-5 above 1/16, by 5e-5 above 0.11.  What R gives too
+// much to one row the other gets too little.
+constexpr float kSeries = 0.11f;
 template <bool MASKED>
 __device__ __forceinline__ void weights16(const float (&u)[17], float &Lc, int columns, Two (&W)[8]) {
     constexpr float l1 = kLn2, l2 = l1 * l1;
@@ -199,7 +203,7 @@ __device__ __forceinline__ void weights16(const float (&u)[17], float &Lc, int c
     for (int e = 0; e < 16; e += 2) {  // intervals e and e + 1
         const float x0 = u[e] - u[e + 1], x1 = u[e + 1] - u[e + 2];  // -X
         const float i0 = rcp_approx(x0), i1 = rcp_approx(x1);
-        const bool s0 = fabsf(x0) < 0.0625f, s1 = fabsf(x1) < 0.0625f;
+        const bool s0 = fabsf(x0) < kSeries, s1 = fabsf(x1) < kSeries;
         const Two x = two(x0, x1), P0 = two(p[e], p[e + 1]);
         const float g0 = s0 ? 1.0f : -1.0f, g1 = s1 ? 1.0f : -1.0f;
         float k0, k1;
@@ -608,7 +612,7 @@ rows_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUten
                     u[0] = before + nm;
                     u[1] = fmaf(__uint_as_float(xa[0]), unit, nm);
                     const float x = u[1] - u[0], inv = rcp_approx(x), p0 = ex2_approx(u[0]), p1 = ex2_approx(u[1]);
-                    const bool small = fabsf(x) < 0.0625f;
+                    const bool small = fabsf(x) < kSeries;
                     const float g = small ? 1.0f : -1.0f, a2 = small ? 0.5f * kLn2 : -kLn2;
                     const float S = fmaf(p0, g, p1) * (small ? 0.5f * kLn2 * fmaf(-kLn2 * kLn2 / 12.0f, x * x, 1.0f) : inv);
                     float left = fmaf(p0, a2, S) * (small ? kLn2 / 3.0f : inv);

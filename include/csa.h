@@ -529,6 +529,8 @@ long long csa_decode_paged_workspace_bytes(int B, int Hq, int Hkv, int d);
  *   Alignment, other refusals, and what decides the last bits as csa_decode_paged.
  *   Weights over bf16 pools are sums of two bf16 numbers; over 8-bit ones, with more
  *   than 8 rows per cached head (T times the query heads on it), one fp16 number.
+ *   With more than 16 rows per cached head the interval between two neighbours is divided
+ *   between them within 2.2e-4 of the share (else within 2^-16), its whole within 2^-16.8.
  */
 #define CSA_TREE_MAX 64
 int csa_decode_tree(const void *q, const void *k_pages, const void *v_pages,
