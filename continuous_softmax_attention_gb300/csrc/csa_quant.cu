@@ -317,6 +317,25 @@ struct ReadParams {
     int tokens, blocks;       // per block, and blocks per (sequence, head)
 };
 
+// Products code * s rounded to fp32, on their way to 16 bits: rounded once in all.  A second rounding goes wrong where the
+// first ends in the middle between two bf16 numbers, one product in 2^16: there the rest of the product, which fma gives
+// exactly, decides.
+template <bool E4M3, int N, typename C>
+__device__ __forceinline__ void settle(const C &raw, float s, float (&x)[N]) {
+    bool middle = false;
+#pragma unroll
+    for (int e = 0; e < N; ++e) middle |= (__float_as_uint(x[e]) & 0xffffu) == 0x8000u;
+    if (!middle) return;
+    float code[N];
+    values_of<E4M3, N>(raw, 1.0f, code);
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        const float rest = fmaf(code[e], s, -x[e]);
+        if ((__float_as_uint(x[e]) & 0xffffu) == 0x8000u && rest != 0.0f)
+            x[e] = __uint_as_float(__float_as_uint(x[e]) + ((rest < 0.0f) == (x[e] < 0.0f) ? 1 : -1));
+    }
+}
+
 template <int KIND>
 struct Stored;
 template <>
@@ -392,7 +411,9 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constan
                 if (state[j] == 1) {
                     if constexpr (EIGHT) {
                         float x[V];
-                        values_of<KIND == CSA_E4M3, V>(raw[j][w], w ? scale[j].y : scale[j].x, x);
+                        const float s = w ? scale[j].y : scale[j].x;
+                        values_of<KIND == CSA_E4M3, V>(raw[j][w], s, x);
+                        if (sizeof(O) == 2) settle<KIND == CSA_E4M3, V>(raw[j][w], s, x);
 #pragma unroll
                         for (int e = 0; e < V; ++e) to.e[e] = narrow<O>(x[e]);
                     } else {
