@@ -17,7 +17,7 @@
 // What bounds it.  Each value is read once and each code written once: HBM bandwidth, and
 // the instructions of the rotation (issue slots 60% busy).  8 x up to 2048 tokens, 32 heads
 // on 8, d = 128 (330 MB) take 58 us, 85% of the copy bandwidth; 64 single tokens 3.2 us.
-// Reading back is a copy: 754 MB of int8 rows as bf16 take 114 us, 99%; 25 MB 6.1 us.
+// Reading back is a copy: 754 MB of int8 rows as bf16 take 117 us, 96%; 25 MB 6.4 us.
 // A power of two of lanes owns a row, 16 bytes twice per lane as in csa_rope.cu (the
 // two members of 8 bf16 or 4 fp32 pairs), holds it in registers between the maximum
 // and the codes, and walks over a range of heads with the token's sines and cosines.
@@ -317,25 +317,6 @@ struct ReadParams {
     int tokens, blocks;       // per block, and blocks per (sequence, head)
 };
 
-// Products code * s rounded to fp32, on their way to 16 bits: rounded once in all.  A second rounding goes wrong where the
-// first ends in the middle between two bf16 numbers, one product in 2^16: there the rest of the product, which fma gives
-// exactly, decides.
-template <bool E4M3, int N, typename C>
-__device__ __forceinline__ void settle(const C &raw, float s, float (&x)[N]) {
-    bool middle = false;
-#pragma unroll
-    for (int e = 0; e < N; ++e) middle |= (__float_as_uint(x[e]) & 0xffffu) == 0x8000u;
-    if (!middle) return;
-    float code[N];
-    values_of<E4M3, N>(raw, 1.0f, code);
-#pragma unroll
-    for (int e = 0; e < N; ++e) {
-        const float rest = fmaf(code[e], s, -x[e]);
-        if ((__float_as_uint(x[e]) & 0xffffu) == 0x8000u && rest != 0.0f)
-            x[e] = __uint_as_float(__float_as_uint(x[e]) + ((rest < 0.0f) == (x[e] < 0.0f) ? 1 : -1));
-    }
-}
-
 template <int KIND>
 struct Stored;
 template <>
@@ -411,9 +392,7 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const __grid_constan
                 if (state[j] == 1) {
                     if constexpr (EIGHT) {
                         float x[V];
-                        const float s = w ? scale[j].y : scale[j].x;
-                        values_of<KIND == CSA_E4M3, V>(raw[j][w], s, x);
-                        if (sizeof(O) == 2) settle<KIND == CSA_E4M3, V>(raw[j][w], s, x);
+                        values_of<KIND == CSA_E4M3, sizeof(O) == 2, V>(raw[j][w], w ? scale[j].y : scale[j].x, x);
 #pragma unroll
                         for (int e = 0; e < V; ++e) to.e[e] = narrow<O>(x[e]);
                     } else {

@@ -75,9 +75,15 @@ __device__ __forceinline__ void halves_of(uint32_t codes, uint32_t &lo, uint32_t
     }
 }
 
-// N values of a row of scale s from N codes.
-template <bool E4M3, int N, typename C>
+// N values of a row of scale s from N codes.  AGAIN: they are rounded once more, to 16 bits, and the two roundings shall be as
+// one.  Then a product is cut off, and its last bit set where the scale's fraction has one of its last eight: such a scale
+// times a code's 8 bits is nowhere in the middle between two bf16 numbers (it would be a multiple of 2^15 units of the
+// scale, a code of 2^7 at most), so that the bit stands for what was cut off or changes nothing; other products fit 24
+// bits.  754 MB of int8 rows as bf16 in 117 us, 114 with the second rounding as it falls; a look at each product for the
+// middle, and those put right that were moved: 139 us; the products two by two, in 50 registers: 121 us.
+template <bool E4M3, bool AGAIN, int N, typename C>
 __device__ __forceinline__ void values_of(const C &raw, float s, float (&x)[N]) {
+    const unsigned rest = AGAIN && (__float_as_uint(s) & 0xffu) ? 1u : 0u;
     uint32_t words[(N + 3) / 4] = {};
     static_assert(sizeof(C) == N, "one byte each");
     memcpy(words, &raw, N);
@@ -89,7 +95,8 @@ __device__ __forceinline__ void values_of(const C &raw, float s, float (&x)[N]) 
         for (int j = 0; j < 4; ++j)
             if (i + j < N) {
                 const __half2 p = *reinterpret_cast<const __half2 *>(&h[j / 2]);
-                x[i + j] = (j & 1 ? __high2float(p) : __low2float(p)) * s;
+                const float code = j & 1 ? __high2float(p) : __low2float(p);
+                x[i + j] = AGAIN ? __uint_as_float(__float_as_uint(__fmul_rz(code, s)) | rest) : code * s;
             }
     }
 }

@@ -82,7 +82,7 @@ __device__ __forceinline__ uint4 as_bf16(const void *row, int c) {
     } else {
         const uint2 raw = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(row) + c);
         float x[8];
-        values_of<KIND == CSA_E4M3, 8>(raw, 1.0f, x);
+        values_of<KIND == CSA_E4M3, false, 8>(raw, 1.0f, x);
         return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
     }
 }
