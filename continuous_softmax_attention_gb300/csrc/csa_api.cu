@@ -8,6 +8,7 @@
 #include <cmath>
 #include <cstdint>
 #include <initializer_list>
+#include <mutex>
 
 #include "csa.h"
 #include "csa_internal.h"
@@ -50,6 +51,38 @@ int device_ok() {
     if (major != 10 || minor != 3) return CSA_ERR_NO_DEVICE;
     good.fetch_or(bit, std::memory_order_relaxed);
     return CSA_OK;
+}
+
+// The status words of the paged cache's and rotary kernels, of which each translation unit has one, taken by one launch and
+// one copy: csa_device_status takes 73 us, 187 with two copies for each of the words.
+constexpr int kWords = 10;
+struct Words {
+    int *at[kWords];
+};
+__device__ int g_taken;
+__global__ void take_kernel(Words w) {
+    int first = CSA_OK;
+    for (int i = 0; i < kWords; ++i) {
+        const int word = atomicExch(w.at[i], CSA_OK);
+        if (first == CSA_OK) first = word;
+    }
+    g_taken = first;
+}
+int take_words() {
+    static std::mutex one_at_a_time;  // g_taken is a call's from its launch to its copy
+    Words w = {{csa_paged_status_word(), csa_rope_status_word(), csa_cache_status_word(), csa_quant_status_word(),
+                csa_paged_e4m3_status_word(), csa_paged_int8_status_word(), csa_tree_status_word(),
+                csa_rows_bf16_status_word(), csa_rows_e4m3_status_word(), csa_rows_int8_status_word()}};
+    for (const int *at : w.at)
+        if (!at) return CSA_ERR_CUDA;
+    const std::lock_guard<std::mutex> held(one_at_a_time);
+    void *args[] = {&w};
+    if (cudaLaunchKernel((const void *)take_kernel, dim3(1), dim3(1), args, 0, nullptr) != cudaSuccess) {
+        (void)cudaGetLastError();  // and taken, or the next launch would report it too
+        return CSA_ERR_CUDA;
+    }
+    int v = 0;
+    return cudaMemcpyFromSymbol(&v, g_taken, sizeof(int)) == cudaSuccess ? v : CSA_ERR_CUDA;
 }
 
 int from_cuda(cudaError_t e) { return e == cudaSuccess ? CSA_OK : CSA_ERR_CUDA; }
@@ -783,21 +816,12 @@ int csa_segment_weights_eval(const float *u0, const float *u1, float *right, flo
 int csa_device_status(void) {
     int rc = device_ok();
     if (rc != CSA_OK) return rc;
-    const int a = csa_tc_take_status();
+    const int a = csa_tc_take_status();  // synchronises the device
     const int b = csa_tc_std_take_status();
     const int c = csa_decode_take_status();
-    const int e = csa_tc_backward_take_status();
-    const int f = csa_paged_take_status();
-    const int g = csa_rope_take_status();
-    const int h = csa_cache_take_status();
-    const int i = csa_quant_take_status();
-    const int j = csa_paged_e4m3_take_status();
-    const int k = csa_paged_int8_take_status();
-    const int l = csa_tree_take_status();
-    const int m = csa_rows_bf16_take_status();
-    const int n = csa_rows_e4m3_take_status();
-    const int o = csa_rows_int8_take_status();
-    for (const int word : {a, b, c, e, f, g, h, i, j, k, l, m, n, o})
+    const int d = csa_tc_backward_take_status();
+    const int e = take_words();
+    for (const int word : {a, b, c, d, e})
         if (word != CSA_OK) return word;
     return CSA_OK;
 }

@@ -697,10 +697,7 @@ int csa_cache_copy_rows_run(void *k_pages, void *v_pages, long long row_bytes, v
     return from(launch_after_previous(copy_rows_kernel, grid, kRowThreads, 0, stream, p));
 }
 
-int csa_cache_take_status(void) {
-    int v = 0;
-    if (cudaMemcpyFromSymbol(&v, g_cache_status, sizeof(int)) != cudaSuccess) return CSA_ERR_CUDA;
-    const int zero = 0;
-    if (cudaMemcpyToSymbol(g_cache_status, &zero, sizeof(int)) != cudaSuccess) return CSA_ERR_CUDA;
-    return v;
+int *csa_cache_status_word(void) {
+    void *at = nullptr;
+    return cudaGetSymbolAddress(&at, g_cache_status) == cudaSuccess ? static_cast<int *>(at) : nullptr;
 }

@@ -123,22 +123,22 @@ long long csa_decode_paged_scratch_bytes(int B, int Hq, int Hkv, int d);
 int csa_decode_paged_run(const csa_paged_args &a, void *scratch, int d, cudaStream_t stream);
 int csa_decode_paged_e4m3_run(const csa_paged_args &a, void *scratch, int d, cudaStream_t stream);
 int csa_decode_paged_int8_run(const csa_paged_args &a, void *scratch, int d, cudaStream_t stream);
-int csa_paged_take_status(void);
-int csa_paged_e4m3_take_status(void);
-int csa_paged_int8_take_status(void);
+int *csa_paged_status_word(void);
+int *csa_paged_e4m3_status_word(void);
+int *csa_paged_int8_status_word(void);
 
 // Rows of a tree of drafted tokens over a paged cache (csa_tree.cu), 1 <= T <= 64; a.counts and a.T are not read.
 long long csa_decode_tree_scratch_bytes(int B, int Hq, int Hkv, int T, int d);
 int csa_decode_tree_run(const csa_paged_args &a, const int *parents, const int *counts, int T, int d, int kind,
                         void *scratch, cudaStream_t stream);
-int csa_tree_take_status(void);
+int *csa_tree_status_word(void);
 // Its stretch before the draft with more than 16 rows per cached head (csa_rows_*.cu).
 int csa_rows_bf16_run(const csa_paged_args &a, void *scratch, int d, cudaStream_t stream);
 int csa_rows_e4m3_run(const csa_paged_args &a, void *scratch, int d, cudaStream_t stream);
 int csa_rows_int8_run(const csa_paged_args &a, void *scratch, int d, cudaStream_t stream);
-int csa_rows_bf16_take_status(void);
-int csa_rows_e4m3_take_status(void);
-int csa_rows_int8_take_status(void);
+int *csa_rows_bf16_status_word(void);
+int *csa_rows_e4m3_status_word(void);
+int *csa_rows_int8_status_word(void);
 
 // Rotary positions and the rows of new tokens into pages (csa_rope.cu).
 int csa_rope_plan_make(csa_rope_plan *plan, const int *sections, int axes, double base, int flags);
@@ -154,7 +154,7 @@ int csa_cache_append_run(const csa_rope_plan *plan, const void *q, const long lo
                          const int *counts, const int *positions, const long long *pos_strides,
                          int B, int Hq, int Hkv, int T, int d, int P, int S, int M, bool bf16,
                          cudaStream_t stream);
-int csa_rope_take_status(void);
+int *csa_rope_status_word(void);
 
 // Pages: who holds them, and their movement (csa_cache.cu).
 int csa_cache_reserve_run(int *refs, int *table, int *seqlens, const int *counts, int *shortfall, int B,
@@ -176,7 +176,7 @@ int csa_cache_accept_run(int *refs, int *table, int *seqlens, const int *parents
 int csa_cache_copy_rows_run(void *k_pages, void *v_pages, long long row_bytes, void *row_scales, long long scale_bytes,
                             int layers, int P, int H, int S, const int *src, const int *dst, int B, int T,
                             cudaStream_t stream);
-int csa_cache_take_status(void);
+int *csa_cache_status_word(void);
 
 // Rows in 8 bits: written into pages, and read back (csa_quant.cu).
 int csa_cache_append_q8_run(const csa_rope_plan *plan, const void *q, const long long *q_strides, void *q_out,
@@ -189,4 +189,4 @@ int csa_cache_read_run(const void *k_pages, const void *v_pages, const float *ro
                        const int *seqlens, const int *starts, void *k, const long long *k_strides, void *v,
                        const long long *v_strides, int B, int Hkv, int T, int d, int P, int S, int M, int kind,
                        int out_type, cudaStream_t stream);
-int csa_quant_take_status(void);
+int *csa_quant_status_word(void);

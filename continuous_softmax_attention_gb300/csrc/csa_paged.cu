@@ -13,4 +13,4 @@ int csa_decode_paged_run(const csa_paged_args &a, void *scratch, int d, cudaStre
     return run_paged<CSA_BF16>(p, scratch, d, stream);
 }
 
-int csa_paged_take_status(void) { return take_status(); }
+int *csa_paged_status_word(void) { return status_word(); }

@@ -1794,12 +1794,10 @@ int run_paged(PagedParams &p, void *scratch, int d, cudaStream_t stream) {
     return launch<256, 2, KIND>(p, stream);
 }
 
-int take_status() {
-    int v = 0;
-    if (cudaMemcpyFromSymbol(&v, g_paged_status, sizeof(int)) != cudaSuccess) return CSA_ERR_CUDA;
-    const int zero = 0;
-    if (cudaMemcpyToSymbol(g_paged_status, &zero, sizeof(int)) != cudaSuccess) return CSA_ERR_CUDA;
-    return v;
+// Its address on the current device.
+int *status_word() {
+    void *at = nullptr;
+    return cudaGetSymbolAddress(&at, g_paged_status) == cudaSuccess ? static_cast<int *>(at) : nullptr;
 }
 
 }  // namespace

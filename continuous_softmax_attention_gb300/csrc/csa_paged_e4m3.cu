@@ -6,4 +6,4 @@ int csa_decode_paged_e4m3_run(const csa_paged_args &a, void *scratch, int d, cud
     return run_paged<CSA_E4M3>(p, scratch, d, stream);
 }
 
-int csa_paged_e4m3_take_status(void) { return take_status(); }
+int *csa_paged_e4m3_status_word(void) { return status_word(); }

@@ -6,4 +6,4 @@ int csa_decode_paged_int8_run(const csa_paged_args &a, void *scratch, int d, cud
     return run_paged<CSA_INT8>(p, scratch, d, stream);
 }
 
-int csa_paged_int8_take_status(void) { return take_status(); }
+int *csa_paged_int8_status_word(void) { return status_word(); }

@@ -502,10 +502,7 @@ int csa_cache_read_run(const void *k_pages, const void *v_pages, const float *ro
     return bf ? run_read<CSA_BF16, __nv_bfloat16, 8>(p, stream) : run_read<CSA_F32, float, 4>(p, stream);
 }
 
-int csa_quant_take_status(void) {
-    int v = 0;
-    if (cudaMemcpyFromSymbol(&v, g_quant_status, sizeof(int)) != cudaSuccess) return CSA_ERR_CUDA;
-    const int zero = 0;
-    if (cudaMemcpyToSymbol(g_quant_status, &zero, sizeof(int)) != cudaSuccess) return CSA_ERR_CUDA;
-    return v;
+int *csa_quant_status_word(void) {
+    void *at = nullptr;
+    return cudaGetSymbolAddress(&at, g_quant_status) == cudaSuccess ? static_cast<int *>(at) : nullptr;
 }

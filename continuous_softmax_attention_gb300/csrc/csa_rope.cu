@@ -317,10 +317,7 @@ int csa_cache_append_run(const csa_rope_plan *plan, const void *q, const long lo
     return bf16 ? run<__nv_bfloat16>(p, stream) : run<float>(p, stream);
 }
 
-int csa_rope_take_status(void) {
-    int v = 0;
-    if (cudaMemcpyFromSymbol(&v, g_rope_status, sizeof(int)) != cudaSuccess) return CSA_ERR_CUDA;
-    const int zero = 0;
-    if (cudaMemcpyToSymbol(g_rope_status, &zero, sizeof(int)) != cudaSuccess) return CSA_ERR_CUDA;
-    return v;
+int *csa_rope_status_word(void) {
+    void *at = nullptr;
+    return cudaGetSymbolAddress(&at, g_rope_status) == cudaSuccess ? static_cast<int *>(at) : nullptr;
 }

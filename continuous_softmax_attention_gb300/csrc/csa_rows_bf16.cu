@@ -5,4 +5,4 @@ int csa_rows_bf16_run(const csa_paged_args &a, void *scratch, int d, cudaStream_
     return run_rows<CSA_BF16>(a, scratch, d, stream);
 }
 
-int csa_rows_bf16_take_status(void) { return take_status(); }
+int *csa_rows_bf16_status_word(void) { return status_word(); }

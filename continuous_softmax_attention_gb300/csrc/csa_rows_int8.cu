@@ -5,4 +5,4 @@ int csa_rows_int8_run(const csa_paged_args &a, void *scratch, int d, cudaStream_
     return run_rows<CSA_INT8>(a, scratch, d, stream);
 }
 
-int csa_rows_int8_take_status(void) { return take_status(); }
+int *csa_rows_int8_status_word(void) { return status_word(); }

@@ -622,4 +622,4 @@ int csa_decode_tree_run(const csa_paged_args &args, const int *parents, const in
     return launch_tree_of<CSA_INT8>(p, d, stream);
 }
 
-int csa_tree_take_status(void) { return take_status(); }
+int *csa_tree_status_word(void) { return status_word(); }
