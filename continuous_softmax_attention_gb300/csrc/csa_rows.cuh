@@ -41,6 +41,7 @@
 // 16 128 us, 32 165 us, int8 16 137 us; d = 64 16 82 us; d = 256 16 181 us.
 #pragma once
 
+#include <atomic>
 #include <type_traits>
 
 #include "csa_paged.cuh"
@@ -1082,15 +1083,21 @@ int launch_rows(PagedParams &p, cudaStream_t stream) {
     const long long tiles = (long long)p.B * p.Hkv * p.GB * (((long long)p.M * p.S + C::KT - 1) / C::KT);
     const int most = C::Blocks * kGrid, grid = (int)(tiles < most ? (tiles < 1 ? 1 : tiles) : most);
     auto kern = rows_kernel<D, KIND, CW>;
-    // the shares of the registers come out of those that the block is launched with
-    static const bool fits = [&] {
-        cudaFuncAttributes attr;
-        return cudaFuncGetAttributes(&attr, kern) == cudaSuccess &&
-               32 * C::SoftWarps * C::SoftRegs + (C::Threads - 32 * C::SoftWarps) * C::OtherRegs <= C::Threads * attr.numRegs;
-    }();
-    if (!fits || cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::Smem) != cudaSuccess ||
-        cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) != cudaSuccess ||
-        launch_after_previous(kern, grid, C::Threads, C::Smem, stream, p, maps[0], maps[1], maps[2]) != cudaSuccess)
+    // the shares of the registers come out of those that the block is launched with; a query that fails is asked again by
+    // the next call
+    static std::atomic<bool> fits{false};
+    cudaFuncAttributes attr;
+    bool ready = fits.load(std::memory_order_relaxed);
+    if (!ready && cudaFuncGetAttributes(&attr, kern) == cudaSuccess) {
+        ready = 32 * C::SoftWarps * C::SoftRegs + (C::Threads - 32 * C::SoftWarps) * C::OtherRegs <= C::Threads * attr.numRegs;
+        fits.store(ready, std::memory_order_relaxed);
+    }
+    if (!ready || cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::Smem) != cudaSuccess ||
+        cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) != cudaSuccess) {
+        (void)cudaGetLastError();  // taken, or the next launch would report it too
+        return CSA_ERR_CUDA;
+    }
+    if (launch_after_previous(kern, grid, C::Threads, C::Smem, stream, p, maps[0], maps[1], maps[2]) != cudaSuccess)
         return CSA_ERR_CUDA;
     return CSA_OK;
 }
