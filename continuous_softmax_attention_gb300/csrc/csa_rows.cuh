@@ -210,11 +210,7 @@ __device__ __forceinline__ void weights16(const float (&u)[17], float &Lc, int c
         float k0, k1;
         apart(fma2(x * x, both(-l1 * l2 / 24.0f), both(0.5f * l1)), k0, k1);
         const Two f1 = two(s0 ? k0 : i0, s1 ? k1 : i1), f2 = two(s0 ? -l1 / 3.0f : i0, s1 ? -l1 / 3.0f : i1);
-#ifdef VAR_SEL
-        const Two a2 = two(s0 ? 0.5f * l1 : -l1, s1 ? 0.5f * l1 : -l1);
-#else
         const Two a2 = fma2(two(g0, g1), both(0.75f * l1), both(-0.25f * l1));  // (ln 2) / 2 or -ln 2
-#endif
         const Two S = two(fmaf(p[e + 1], g0, p[e]), fmaf(p[e + 2], g1, p[e + 1])) * f1;
         const Two R = fma2(P0, a2, S) * f2, L = fma2(S, both(l1), R);  // R: what the left gets, times -1
         float r0, r1, q0, q1;

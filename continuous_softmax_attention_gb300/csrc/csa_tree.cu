@@ -48,7 +48,7 @@ struct TreeParams {
     const float *part_o, *part_ml;
     const int4 *joins;
     int workers;           // that the parts are of
-    int B, Hkv, G, T, P, S, M;
+    int B, Hkv, T, P, S, M;
     int rows, GB, HB;      // rows of a group (G * T), blocks of them, rows per block
     int RB;                // rows per block of this kernel, at most kTreeRows
     float qscale;
@@ -607,12 +607,11 @@ int csa_decode_tree_run(const csa_paged_args &args, const int *parents, const in
     p.workers = at.parts_of;
     p.B = args.B;
     p.Hkv = args.Hkv;
-    p.G = args.Hq / args.Hkv;
     p.T = T;
     p.P = args.P;
     p.S = args.S;
     p.M = args.M;
-    p.rows = p.G * T;
+    p.rows = args.Hq / args.Hkv * T;
     p.GB = at.GB;
     p.HB = at.HB;
     p.qscale = args.scale * kLog2e;
