@@ -65,6 +65,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "csa.h"
 #include "csa_device.cuh"
@@ -103,11 +104,14 @@ constexpr int kOneAtATime[4] = {152, 76, 36, 15};
 // for the long one's cluster, 0.5 us a tile, where the other form would spread
 // it: hence no more than 16.
 constexpr int kOneTiles = 16, kOneTilesLess = 4;
-// log2 units a logit may pass the running maximum by.  With 8 bits the weights are fp16 numbers: 2^6 is the largest,
-// half as much more with a copied sink's, times a value's scale, which counts in kLift by the power of two at or above the
-// largest and may be twice that: 1.5 * 2^14 * 2.
+// log2 units a logit may pass the running maximum by.
 constexpr float kRaise = 16.0f, kRaise8 = 6.0f;
-constexpr float kLift = 128.0f;
+// With 8 bits a weight times its value's scale is an fp16 number, in units that make up to 2^kLift2 of the largest such
+// product (by its bound, the larger of its intervals' powers).  Scales may be kMostScale of those units: weights are 2^6 at
+// most, half as much more with a copied sink's, 1.5 * 2^14.  And no less than kLeastScale: the largest weight's product is
+// then far above 2^-14, where fp16 begins to lose bits.  Scales of a tile within 2^kSpread of one another stay within both.
+constexpr int kLift2 = 5, kSpread = 10;
+constexpr float kMostScale = 256.0f, kLeastScale = 1.0f / 64;
 
 __device__ int g_paged_status;  // sticky status word of the including file's kernels
 
@@ -850,22 +854,38 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
         float ws[N] = {};    // with copies: this lane's of them
         uint32_t v_at = 0;   // that tile's values
         uint32_t s_at = 0;   // and its scales
-        // 8 bits: values count in units of 1 / lift, kLift by the power of two that is at least the largest
-        // scale met when it was set, and at least half the largest so far
-        float lift = __uint_as_float(253u << 23);
+        // 8 bits: a head's values count in units of 1 / lift, a power of two by the largest product of a weight and a scale
+        // that it may have had: by weights or scales alone a row with a far larger scale and next to no weight would take
+        // the bits of all others
+        float lift[RH];
+#pragma unroll
+        for (int h = 0; h < RH; ++h) lift[h] = 1.0f;
+        float y_before = 0.f;  // the scale of the value in the last row of the tile before, in the lanes that have it
 
-        // all weights relative to a raised maximum
-        auto raise = [&](const float (&top)[RH]) {
-            float f[RH];
+        // the maximum over a head's lanes
+        auto of_head = [&](float t) {
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
+            t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
+#pragma unroll
+            for (int off = SPREAD ? 4 * N : 32; off < 32; off *= 2) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, off));
+            return t;
+        };
+        // All weights relative to a raised maximum.  8 bits: and values in other units, where the products of weights and
+        // scales (log2, weights' powers not relative to any maximum) may reach `peak`.  first: there are none yet.
+        auto raise = [&](const float (&top)[RH], const float (&peak)[RH], bool first) {
+            float f[RH], fo[RH];
 #pragma unroll
             for (int h = 0; h < RH; ++h) {
-                float t = top[h];
-                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
-                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
-#pragma unroll
-                for (int off = SPREAD ? 4 * N : 32; off < 32; off *= 2) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, off));
-                t = fmaxf(t, m[h]);
-                f[h] = ex2_approx(m[h] - t);
+                const float t = fmaxf(of_head(top[h]), m[h]);
+                f[h] = fo[h] = ex2_approx(m[h] - t);
+                if constexpr (EIGHT) {
+                    const float e = (float)(int)((__float_as_uint(lift[h]) >> 23) - 127u);
+                    float most = of_head(peak[h]);
+                    if (!first) most = fmaxf(most, m[h] + ((float)kLift2 - e));
+                    const float to = fminf(fmaxf((float)kLift2 - ceilf(most - t), -126.0f), 126.0f);
+                    lift[h] = __uint_as_float((uint32_t)((int)to + 127) << 23);
+                    fo[h] = first ? 0.0f : ex2_approx(m[h] - t + (to - e));
+                }
                 m[h] = t;
                 l[h] *= f[h];
                 w0[h] *= f[h];
@@ -883,10 +903,47 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
             }
 #pragma unroll
             for (int i = 0; i < ON; ++i) {
-                o[i][0] *= f[0];
-                o[i][1] *= f[0];
-                o[i][2] *= f[RH - 1];
-                o[i][3] *= f[RH - 1];
+                o[i][0] *= fo[0];
+                o[i][1] *= fo[0];
+                o[i][2] *= fo[RH - 1];
+                o[i][3] *= fo[RH - 1];
+            }
+        };
+        // 8 bits: bounds of the products with a tile's scales (at `at`), for logits a(h, i) of rows row(i), i < COUNT, of which
+        // `own` exist; `most` and `least` are this lane's largest and least scale.  A row's weight is at most the largest
+        // power of the row and its neighbours'.  first: the row before is not of a tile.
+        auto peaks = [&](auto count, auto a, auto row, const float (&top)[RH], uint32_t at, int own, float most, float least, bool first,
+                         float (&peak)[RH]) {
+            auto scale = [&](uint32_t tile_at, int r) {
+                float y;
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(y) : "r"(tile_at + r * 8 + 4) : "memory");
+                return fabsf(y);
+            };
+            const uint32_t hi = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(most, y_before)));
+            const uint32_t lo = __reduce_min_sync(0xffffffffu, __float_as_uint(least));
+            const bool alike = lo + ((uint32_t)kSpread << 23) >= hi;
+            const bool with_before = first ? !copied_sink : SPREAD ? has_last : q == 3;
+            if (alike) {
+                const float y = __log2f(__uint_as_float(hi));
+#pragma unroll
+                for (int h = 0; h < RH; ++h) peak[h] = fmaxf(top[h], with_before ? prev[h] : -INFINITY) + y;
+            } else {
+                const float y0 = __log2f(scale(at, 0));
+#pragma unroll
+                for (int h = 0; h < RH; ++h) peak[h] = with_before ? prev[h] + y0 : -INFINITY;
+#pragma unroll
+                for (int i = 0; i < decltype(count)::value; ++i) {
+                    const int r = row(i);
+                    float y = scale(at, r);
+                    if (r > 0)
+                        y = fmaxf(y, scale(at, r - 1));
+                    else if (!first)
+                        y = fmaxf(y, scale(s_at, KT - 1));
+                    if (r + 1 < min(own, KT)) y = fmaxf(y, scale(at, r + 1));
+                    y = __log2f(y);
+#pragma unroll
+                    for (int h = 0; h < RH; ++h) peak[h] = fmaxf(peak[h], a(h, i) + y);
+                }
             }
         };
         // with copies: the scales of this lane's keys and values of a tile
@@ -906,21 +963,6 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
         };
         // the second product for the tile before
         auto values = [&]() {
-            // 8 bits: another unit of the values, whose largest scale among this lane's rows is `most`
-            auto lift_to = [&](float most) {
-                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
-                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-#pragma unroll
-                for (int off = SPREAD ? 4 * N : 32; off < 32; off *= 2) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
-                // exponent of the power of two at or above it
-                const uint32_t e2 = min(max((__float_as_uint(most) + 0x7fffffu) >> 23, 8u), 253u);
-                const float to = __uint_as_float((261u - e2) << 23), f = to / lift;  // kLift 2^(127 - e2)
-                lift = to;
-#pragma unroll
-                for (int i = 0; i < ON; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[i][e] *= f;
-            };
             // 8 bits: the product with 16 rows, whose weights are a
             auto product = [&](int ks, const uint32_t (&a)[4]) {
 #pragma unroll
@@ -936,14 +978,10 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
                 }
             };
             if constexpr (SPREAD) {
-                float x[N], sv[N], most = 0.f;
+                float x[N], sv[N];
                 scales_of(s_at, x, sv);
 #pragma unroll
-                for (int t = 0; t < N; ++t) {
-                    l[0] += ws[t];
-                    most = fmaxf(most, sv[t]);
-                }
-                if (__any_sync(0xffffffffu, most * lift > 2.0f * kLift)) lift_to(most);
+                for (int t = 0; t < N; ++t) l[0] += ws[t];
                 // weights as hi + lo, of two rows each in a register (of one row in one with N = 1), then those of
                 // all copies
                 constexpr int Regs = N > 1 ? N : 1;
@@ -951,13 +989,13 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
                 if constexpr (N > 1) {
 #pragma unroll
                     for (int t = 0; t < N; t += 2) {
-                        const float a = ws[t] * (sv[t] * lift), c = ws[t + 1] * (sv[t + 1] * lift);
+                        const float a = ws[t] * (sv[t] * lift[0]), c = ws[t + 1] * (sv[t + 1] * lift[0]);
                         mine[t] = pack_f16x2(a, c);
                         const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&mine[t]));
                         mine[t + 1] = pack_f16x2(a - y.x, c - y.y);
                     }
                 } else {
-                    const float a = ws[0] * (sv[0] * lift);
+                    const float a = ws[0] * (sv[0] * lift[0]);
                     const uint32_t y = pack_f16x2(a, 0.f);
                     mine[0] = y | pack_f16x2(0.f, a - __half22float2(*reinterpret_cast<const __half2 *>(&y)).x);
                 }
@@ -985,7 +1023,6 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
                 for (int i = 0; i < NT; ++i) l[h] += w[h][i][0] + w[h][i][1];
             if constexpr (EIGHT) {
                 float sv[KT / 16][4];
-                bool over = false;
 #pragma unroll
                 for (int ks = 0; ks < KT / 16; ++ks) {
                     const uint4 x = lds16(s_at + (16 * ks + 4 * q) * 8), y = lds16(s_at + (16 * ks + 4 * q) * 8 + 16);
@@ -993,24 +1030,15 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
                     sv[ks][1] = __uint_as_float(x.w);
                     sv[ks][2] = __uint_as_float(y.y);
                     sv[ks][3] = __uint_as_float(y.w);
-                    over |= fmaxf(fmaxf(sv[ks][0], sv[ks][1]), fmaxf(sv[ks][2], sv[ks][3])) * lift > 2.0f * kLift;
-                }
-                if (__any_sync(0xffffffffu, over)) {
-                    float most = 0.f;
-#pragma unroll
-                    for (int ks = 0; ks < KT / 16; ++ks)
-                        most = fmaxf(most, fmaxf(fmaxf(sv[ks][0], sv[ks][1]), fmaxf(sv[ks][2], sv[ks][3])));
-                    lift_to(most);
                 }
 #pragma unroll
                 for (int ks = 0; ks < KT / 16; ++ks) {
                     uint32_t hi[RH][2], lo[2];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const float f0 = sv[ks][2 * i] * lift, f1 = sv[ks][2 * i + 1] * lift;
 #pragma unroll
                         for (int h = 0; h < RH; ++h) {
-                            const float a = w[h][2 * ks + i][0] * f0, c = w[h][2 * ks + i][1] * f1;
+                            const float a = w[h][2 * ks + i][0] * (sv[ks][2 * i] * lift[h]), c = w[h][2 * ks + i][1] * (sv[ks][2 * i + 1] * lift[h]);
                             hi[h][i] = pack_f16x2(a, c);
                             if (RH == 1) {
                                 const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&hi[h][i]));
@@ -1098,7 +1126,7 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
                 }
                 if (EIGHT) {
                     float2 *st = reinterpret_cast<float2 *>(raw + (scale_ring + stage * C::Scales - smem_u32(raw)));
-                    if (lane < KT - own) st[own + lane] = make_float2(0.f, 0.f);
+                    if (lane < KT - own) st[own + lane] = make_float2(0.f, st->y);  // a scale like the others'
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -1157,7 +1185,17 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
                 if (j == tile)
 #pragma unroll
                     for (int t = 0; t < N; ++t) ws[t] = 0.f;
-                if (__any_sync(0xffffffffu, top[0] > m[0] + kUp)) raise(top);
+                float most = fabsf(y[0]), least = fabsf(y[0]);
+#pragma unroll
+                for (int t = 1; t < N; ++t) most = fmaxf(most, fabsf(y[t])), least = fminf(least, fabsf(y[t]));
+                if (__any_sync(0xffffffffu, j == tile || top[0] > m[0] + kUp || fmaxf(most, y_before) * lift[0] > kMostScale ||
+                                                least * lift[0] < kLeastScale)) {
+                    float peak[1];
+                    peaks(std::integral_constant<int, N>{}, [&](int, int t) { return a[t]; }, [&](int t) { return own0 + t; }, top,
+                          scale_ring + stage * C::Scales, own, most, least, j == tile, peak);
+                    raise(top, peak, j == tile);
+                }
+                y_before = has_last ? fabsf(y[N - 1]) : 0.f;
                 if (j == tile && copied_sink) {
                     prev[0] = __shfl_sync(0xffffffffu, a[0], lane_first);
                     pm[0] = ex2_approx(prev[0] - m[0]);
@@ -1193,13 +1231,17 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
             }
             float nw[RH][NT][2], even_left[RH][NT], to_before[RH];
             if constexpr (!SPREAD) {
-                float top[RH];
-                bool over = false;
+                float top[RH], most = 0.f, least = INFINITY, y_last = 0.f;
+                bool over = EIGHT && j == tile;
                 if constexpr (EIGHT) {
                     const uint32_t at = scale_ring + stage * C::Scales + 4 * q * 8;
 #pragma unroll
                     for (int i = 0; i < NT; ++i) {
                         const uint4 x = lds16(at + (16 * (i / 2) + 2 * (i & 1)) * 8);
+                        const float y0 = fabsf(__uint_as_float(x.y)), y1 = fabsf(__uint_as_float(x.w));
+                        most = csa_tc::fmax3f(most, y0, y1);
+                        least = fminf(least, fminf(y0, y1));
+                        y_last = y1;
 #pragma unroll
                         for (int h = 0; h < RH; ++h) {
                             s[i][2 * h] *= unit[h] * __uint_as_float(x.x);
@@ -1236,7 +1278,18 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
 #pragma unroll
                         for (int i = 0; i < NT; ++i) w[h][i][0] = w[h][i][1] = 0.f;
                 }
-                if (__any_sync(0xffffffffu, over)) raise(top);
+                if constexpr (EIGHT)
+                    over |= fmaxf(most, y_before) * fmaxf(lift[0], lift[RH - 1]) > kMostScale ||
+                            least * fminf(lift[0], lift[RH - 1]) < kLeastScale;
+                if (__any_sync(0xffffffffu, over)) {
+                    float peak[RH] = {};
+                    if constexpr (EIGHT)
+                        peaks(std::integral_constant<int, 2 * NT>{}, [&](int h, int i) { return s[i / 2][2 * h + (i & 1)]; },
+                              [&](int i) { return row_of(i / 2, i & 1); }, top, scale_ring + stage * C::Scales, own, most, least, j == tile,
+                              peak);
+                    raise(top, peak, j == tile);
+                }
+                if (EIGHT) y_before = q == 3 ? y_last : 0.f;
                 if (j == tile && copied_sink) {
 #pragma unroll
                     for (int h = 0; h < RH; ++h) {
@@ -1379,8 +1432,13 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
         if (!lost && r1 < n) {  // the range's last row has a neighbour behind it
             bool over = false;
 #pragma unroll
-            for (int h = 0; h < RH; ++h) over |= behind[h] > m[h] + kUp;
-            if (__any_sync(0xffffffffu, over)) raise(behind);
+            for (int h = 0; h < RH; ++h) over |= behind[h] > m[h] + kUp || (EIGHT && y_before * lift[h] > kMostScale);
+            if (__any_sync(0xffffffffu, over)) {
+                float peak[RH];  // of the product with the last row's scale
+#pragma unroll
+                for (int h = 0; h < RH; ++h) peak[h] = behind[h] + __log2f(y_before);
+                raise(behind, peak, false);
+            }
 #pragma unroll
             for (int h = 0; h < RH; ++h) {
                 float left, right, none0, none1;
@@ -1417,7 +1475,7 @@ paged_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUte
         for (int h = 0; h < RH; ++h) {
             const int row = g + 8 * h;
             if (row < rows_h) {
-                const float inv = 1.0f / sum[h], down = 1.0f / lift;  // a power of two
+                const float inv = 1.0f / sum[h], down = 1.0f / lift[h];  // a power of two
                 const long long oh = (long long)b * p.Hq + q0 + row;
                 __nv_bfloat16 *og = p.out + oh * D + half_of * DW;
                 float *po = (ONE ? kept + row * D : p.part_o + (slot + row) * D) + half_of * DW;

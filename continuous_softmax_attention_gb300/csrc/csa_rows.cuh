@@ -136,9 +136,10 @@ struct RowsCfg {
     static constexpr int Blocks = Eight || D == 256 ? 1 : 2;  // per SM
     static constexpr int KT = 64 * Halves;   // cached rows per tile
     // What beginning and ending a part costs, in tiles.  64 ragged sequences of 1 to 8192 rows, 32 heads on 8, 8 drafted
-    // tokens, d = 128: 104 us with 2, 84 with 4, 80 with 6, 85 with 12; e4m3 (tiles of 128 rows) 129 with 2, 107 with 4,
-    // 102 with 6, 111 with 8; 16 drafted, d = 256 (one block per SM) 207 with 4, 185 with 6, 178 with 8, 196 with 12.
-    static constexpr int PartCost = !Eight && D == 256 ? 8 : 6;
+    // tokens, d = 128: 104 us with 2, 84 with 4, 80 with 6, 85 with 12; e4m3 (tiles of 128 rows) 134 with 2, 118 with 3, 110
+    // with 4, 116 with 6, 119 with 8, int8 135, 120, 112, 121 and 126; 16 drafted, d = 256 (one block per SM) 207 with 4, 185
+    // with 6, 178 with 8, 196 with 12, and e4m3 over 16 equal sequences 217 with 4, 214 with 6.
+    static constexpr int PartCost = D == 256 ? (Eight ? 6 : 8) : Eight ? 4 : 6;
     static constexpr int KR = KT + 16;       // and those of K: 8 behind, 8 before
     // warps: the softmax, the tensor core, the copies of keys and of values (which wait for different products, so each
     // has a warp), with 8 bits the cached rows' scales (else a spare one), and the four that turn codes into fp16 numbers
@@ -165,8 +166,8 @@ struct RowsCfg {
     // the sums of a part are joined on its queries, XC columns at a time
     static constexpr int XC = 128 * Halves * 32 * 4 <= QBytes ? 32 : 16, XBytes = 128 * Halves * XC * 4, OffX = OffQ;
     static_assert(XBytes <= QBytes, "the sums fit");
-    static constexpr int OffScales = OffRing + Stages * StageBytes;  // [4 tiles][2][KR]
-    static constexpr int Smem = OffScales + (Eight ? 4 * KR * 8 : 0) + 1024;
+    static constexpr int OffScales = OffRing + Stages * StageBytes;  // [4 tiles][3][KR]
+    static constexpr int Smem = OffScales + (Eight ? 4 * KR * 12 : 0) + 1024;
     static_assert(Blocks * (Smem + 4096) <= 227 * 1024, "shared memory");
     // tensor memory columns
     static constexpr int ColP = KR, ColO = KR + 32 * Halves;
@@ -365,7 +366,7 @@ rows_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUten
         const uint32_t tS = tmem + at_lane, tP = tmem + at_lane + C::ColP + 32 * h, tO = tmem + at_lane + C::ColO + D * h;
         const int rep = i / R, row = i - rep * R;  // a warp has one copy
         const int c0 = 64 * h + rep * CW;          // this thread's columns
-        const float *ring = reinterpret_cast<const float *>(smem + C::OffScales);  // [4 tiles][of keys, of values][KR]
+        const float *ring = reinterpret_cast<const float *>(smem + C::OffScales);  // [4 tiles][of keys, of values, bounds][KR]
         {  // the other copies' columns of P stay as good as zero: 2^-126 over bf16 pools, as 0 times infinity is not infinity
             constexpr uint32_t z = EIGHT ? 0u : 0x00800080u;
             const uint32_t zero[8] = {z, z, z, z, z, z, z, z};
@@ -424,6 +425,7 @@ rows_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUten
             }
             const int r0 = now.tile * KT;
             float m = -INFINITY, l = 0.0f, w_sink = 0.0f, lift = 0.0f;
+            float highest = -INFINITY;  // 8 bits: the largest logit, where m may be below it
             float carry = 0.0f;  // the logit before column 0, log2 units
             if (c0 == 0 && r0 == 0 && p.mode == CSA_K0_GIVEN && mine) {
                 const uint4 *qg = reinterpret_cast<const uint4 *>(p.q + (first + row) * D), *kg = reinterpret_cast<const uint4 *>(p.k0 + (long long)hk * D);
@@ -465,7 +467,7 @@ rows_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUten
                 tc_fence_after();
                 bad |= *(volatile int *)&s_bad[tiles & 7] != 0;
                 const int own = n - j * KT;  // rows of this tile and behind it
-                const float *sk = ring + (tiles & 3) * 2 * KR, *sv = sk + KR;
+                const float *sk = ring + (tiles & 3) * 3 * KR, *sv = sk + KR, *sb = sv + KR;
                 const bool sink = j == 0 && c0 == 0, copied = sink && p.mode == CSA_K0_COPY_FIRST;
                 // this thread's columns, up to 32 at a time, and their neighbours: all loads at once
                 uint32_t xa[16], xb[16], behind, edge, tail;
@@ -552,16 +554,24 @@ rows_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUten
                 carry = __uint_as_float(tail) * unit;
                 float top = high == -INFINITY ? high : high * unit;
                 if (!MASKED || c0 < own) top = fmaxf(top, before);
-                // a raised maximum, or another unit of the values: the sums of the tiles before follow
-                float f_lift = 1.0f;
+                // A raised maximum, or another unit of the values: the sums of the tiles before follow.  8 bits: weights are
+                // relative to 2^m such that the largest product with a scale is an fp16 number with all its bits.  Where scales
+                // are far apart that is not the largest weight's, and in another unit what the rows before may have had counts
+                // for less: m can be below the largest logit, by 2^80 at most, that the weights' sum stays finite.
+                float f_lift = 1.0f, down = 0.0f;  // down: log2 of it
+                bool uneven = false;
                 if (EIGHT) {
-                    const float to = s_lift[tiles & 3];
+                    const float its = s_lift[tiles & 3], to = fabsf(its);
+                    uneven = its < 0.0f;
                     if (to != lift) {
-                        f_lift = j > now.tile ? to / lift : 1.0f;
+                        if (j > now.tile) {
+                            f_lift = to / lift;
+                            down = (float)(((int)__float_as_uint(to) - (int)__float_as_uint(lift)) >> 23);
+                        }
                         lift = to;
                     }
                 }
-                const bool over = top > m + (EIGHT ? kRaise8 : kRaise);
+                bool over = top > m + (EIGHT ? kRaise8 : kRaise);
                 // The low parts of the tile before, when its first product is done: with 64 columns after the interval
                 // before them (152 us for 32 drafted tokens as above, 164 here), else here (two places spill registers:
                 // 112 us for 16 drafted, so 100)
@@ -577,9 +587,48 @@ rows_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUten
                     }
                     return ok;
                 };
-                if (__any_sync(0xffffffffu, over || f_lift != 1.0f)) {
+                bool change = __any_sync(0xffffffffu, over || f_lift != 1.0f || uneven);
+                if (EIGHT && change && (uneven || f_lift != 1.0f)) {
+                    highest = fmaxf(highest, fmaxf(m, top));
+                    if (uneven) {  // the logits with their rows' bounds, this thread's and the next; -infinity behind the end
+                        top = before + sb[c0 > 0 ? c0 - 1 : KR - 1];
+                        if constexpr (CW == 64) {
+#pragma unroll 1
+                            for (int c = c0; c <= c0 + CW; ++c) {
+                                uint32_t x;
+                                tm_ld1(tS + c, x);
+                                tm_wait(x);
+                                top = fmaxf(top, fmaf(__uint_as_float(x) * sk[c], unit, sb[c]));
+                            }
+                        } else {
+                            auto bound = [&](const uint32_t (&x)[16], int col) {
+                                const float4 *at = reinterpret_cast<const float4 *>(sb + col);
+#pragma unroll
+                                for (int e = 0; e < 16; e += 4) {
+                                    const float4 y = at[e / 4];
+                                    float a = __uint_as_float(x[e]), b = __uint_as_float(x[e + 1]), c = __uint_as_float(x[e + 2]), d = __uint_as_float(x[e + 3]);
+                                    if constexpr (CW == 16) {
+                                        apart(fma2(two(a, b), both(unit), two(y.x, y.y)), a, b);
+                                        apart(fma2(two(c, d), both(unit), two(y.z, y.w)), c, d);
+                                    } else {
+                                        a = fmaf(a, unit, y.x), b = fmaf(b, unit, y.y), c = fmaf(c, unit, y.z), d = fmaf(d, unit, y.w);
+                                    }
+                                    top = csa_tc::fmax3f(csa_tc::fmax3f(top, a, b), c, d);
+                                }
+                            };
+                            bound(xa, c0);
+                            if (CW == 32) bound(xb, c0 + 16);
+                            top = fmaxf(top, fmaf(__uint_as_float(behind), unit, sb[c0 + CW]));
+                        }
+                        over = top > m + kRaise8;
+                        change = __any_sync(0xffffffffu, over || f_lift != 1.0f);
+                    }
+                }
+                if (change) {
                     if ((CW == 64 && !give()) || !wait_free()) return false;
-                    const float to = over ? top : m, f = m == -INFINITY ? 0.0f : ex2_approx(m - to);
+                    float to = over ? top : m;
+                    if (EIGHT && f_lift != 1.0f) to = fmaxf(fmaxf(top, m + down), highest - 80.0f);
+                    const float f = m == -INFINITY ? 0.0f : ex2_approx(m - to);
                     m = to;
                     l *= f;
                     w_sink *= f;
@@ -942,21 +991,25 @@ rows_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUten
                     const float2 *rs = reinterpret_cast<const float2 *>(smem + C::OffRing + stage * C::StageBytes + C::RawK + C::RawV);
                     if (!(ok = __all_sync(0xffffffffu, idle(k_full(stage), tiles / NS) && idle(k_free, tiles + 1)))) break;
                     float2 x[(KR + 31) / 32];
-                    float big = 0.0f;
+                    float big = 0.0f, least = INFINITY;
 #pragma unroll
                     for (int i = 0; i < (KR + 31) / 32; ++i) {
                         const int r = 32 * i + lane;
                         x[i] = r < KR ? rs[r] : make_float2(0.0f, 0.0f);
-                        if (r < own && r < KT) big = fmaxf(big, x[i].y);
+                        if (r < own && r < KT) {
+                            big = fmaxf(big, fabsf(x[i].y));
+                            least = fminf(least, fabsf(x[i].y));
+                        }
                     }
                     // the unit of the values: see csa_paged.cuh; a new part, a new unit
-#pragma unroll
-                    for (int off = 16; off > 0; off >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
-                    if (j == now.tile || big * lift > 2.0f * kLift) {
+                    big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
+                    least = __uint_as_float(__reduce_min_sync(0xffffffffu, __float_as_uint(least)));
+                    if (j == now.tile || big * lift > kMostScale) {
+                        // 2^kLift2 by the power of two at or above the largest
                         const uint32_t e2 = min(max((__float_as_uint(big) + 0x7fffffu) >> 23, 8u), 253u);
-                        lift = __uint_as_float((261u - e2) << 23);
+                        lift = __uint_as_float((254u + kLift2 - e2) << 23);
                     }
-                    float *to = ring + (tiles & 3) * 2 * KR;
+                    float *to = ring + (tiles & 3) * 3 * KR;
 #pragma unroll
                     for (int i = 0; i < (KR + 31) / 32; ++i) {
                         const int r = 32 * i + lane;
@@ -965,8 +1018,21 @@ rows_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUten
                             to[KR + r] = r < own && r < KT ? x[i].y * lift : 0.0f;
                         }
                     }
-                    if (lane == 0) s_lift[tiles & 3] = lift;
+                    const bool uneven = least * lift < kLeastScale;
+                    if (lane == 0) s_lift[tiles & 3] = uneven ? -lift : lift;
                     __syncwarp();
+                    if (uneven) {
+                        // what a logit's power may bring to its row's product and its neighbours', log2 over 2^kLift2; the
+                        // last column is the row before the tile, whose power the first row's weight has
+                        const float *sv = to + KR;
+#pragma unroll 1
+                        for (int r = lane; r < KR; r += 32) {
+                            float y = fabsf(sv[r < KR - 1 ? r : 0]);
+                            if (r < KR - 1) y = fmaxf(y, fmaxf(r > 0 ? fabsf(sv[r - 1]) : 0.0f, fabsf(sv[r + 1])));
+                            to[2 * KR + r] = r < own || r == KR - 1 ? fmaxf(__log2f(y) - (float)kLift2, -80.0f) : -INFINITY;
+                        }
+                        __syncwarp();
+                    }
                     if (lane == 0) {
                         mbar_arrive(k_ready);
                         mbar_arrive(k_empty(stage));

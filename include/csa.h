@@ -486,9 +486,11 @@ int csa_decode_paged(const void *q, const void *k_pages, const void *v_pages, co
  *   CSA_INT8), whose rows stand for code * scale; q, k0, v0 and out as there.
  *   row_scales 16-byte aligned; M * S at most 2^31 - 32.  A row whose scale is NaN
  *   makes what attends to it NaN.  Logits are formed from the codes in fp32, the
- *   weights are fp16 numbers (with up to 8 query heads per cached head, or per block
- *   of them, sums of two), the sums fp32.  Everything else as csa_decode_paged, the
- *   workspace too.
+ *   weights times the values' scales are fp16 numbers (with up to 8 query heads per
+ *   cached head, or per block of them, sums of two), the sums fp32.  The unit of those
+ *   numbers follows the largest product of a weight and a scale that a head has, so
+ *   that they keep their 11 bits down to 2^-8 of it, whatever the scales, and are off by
+ *   2^-19 of it at most.  Everything else as csa_decode_paged, the workspace too.
  */
 int csa_decode_paged_q8(const void *q, const void *k_pages, const void *v_pages,
                         const float *row_scales, const void *k0, const void *v0,
@@ -528,7 +530,9 @@ long long csa_decode_paged_workspace_bytes(int B, int Hq, int Hkv, int d);
  *   on entry irrelevant; calls that can run at the same time need distinct ones.
  *   Alignment, other refusals, and what decides the last bits as csa_decode_paged.
  *   Weights over bf16 pools are sums of two bf16 numbers; over 8-bit ones, with more
- *   than 8 rows per cached head (T times the query heads on it), one fp16 number.
+ *   than 8 rows per cached head (T times the query heads on it), one fp16 number, its
+ *   unit as in csa_decode_paged_q8 (with more than 16 rows for values' scales that lie
+ *   within 2^80 of one another).
  *   With more than 16 rows per cached head the interval between two neighbours is divided
  *   between them within 2.2e-4 of the share (else within 2^-16), its whole within 2^-16.8.
  */
