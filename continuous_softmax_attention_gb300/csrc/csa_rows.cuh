@@ -138,8 +138,8 @@ struct RowsCfg {
     // What beginning and ending a part costs, in tiles.  64 ragged sequences of 1 to 8192 rows, 32 heads on 8, 8 drafted
     // tokens, d = 128: 104 us with 2, 84 with 4, 80 with 6, 85 with 12; e4m3 (tiles of 128 rows) 134 with 2, 118 with 3, 110
     // with 4, 116 with 6, 119 with 8, int8 135, 120, 112, 121 and 126; 16 drafted, d = 256 (one block per SM) 207 with 4, 185
-    // with 6, 178 with 8, 196 with 12, and e4m3 over 16 equal sequences 217 with 4, 214 with 6.
-    static constexpr int PartCost = D == 256 ? (Eight ? 6 : 8) : Eight ? 4 : 6;
+    // with 6, 178 with 8, 196 with 12, e4m3 244 with 4, 234 with 6, 222 with 8, 226 with 10, 238 with 13.
+    static constexpr int PartCost = D == 256 ? 8 : Eight ? 4 : 6;
     static constexpr int KR = KT + 16;       // and those of K: 8 behind, 8 before
     // warps: the softmax, the tensor core, the copies of keys and of values (which wait for different products, so each
     // has a warp), with 8 bits the cached rows' scales (else a spare one), and the four that turn codes into fp16 numbers
@@ -592,30 +592,34 @@ rows_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUten
                     highest = fmaxf(highest, fmaxf(m, top));
                     if (uneven) {  // the logits with their rows' bounds, this thread's and the next; -infinity behind the end
                         top = before + sb[c0 > 0 ? c0 - 1 : KR - 1];
+                        auto bound = [&](const uint32_t (&x)[16], int col) {
+                            const float4 *at = reinterpret_cast<const float4 *>(sb + col);
+#pragma unroll
+                            for (int e = 0; e < 16; e += 4) {
+                                const float4 y = at[e / 4];
+                                float a = __uint_as_float(x[e]), b = __uint_as_float(x[e + 1]), c = __uint_as_float(x[e + 2]), d = __uint_as_float(x[e + 3]);
+                                if constexpr (CW == 16) {
+                                    apart(fma2(two(a, b), both(unit), two(y.x, y.y)), a, b);
+                                    apart(fma2(two(c, d), both(unit), two(y.z, y.w)), c, d);
+                                } else {
+                                    a = fmaf(a, unit, y.x), b = fmaf(b, unit, y.y), c = fmaf(c, unit, y.z), d = fmaf(d, unit, y.w);
+                                }
+                                top = csa_tc::fmax3f(csa_tc::fmax3f(top, a, b), c, d);
+                            }
+                        };
                         if constexpr (CW == 64) {
+                            uint32_t x[16], next;
+                            tm_ld1(tS + c0 + 64, next);
+                            tm_wait(next);
+                            top = fmaxf(top, fmaf(__uint_as_float(next) * sk[c0 + 64], unit, sb[c0 + 64]));
 #pragma unroll 1
-                            for (int c = c0; c <= c0 + CW; ++c) {
-                                uint32_t x;
-                                tm_ld1(tS + c, x);
+                            for (int c = c0; c < c0 + CW; c += 16) {
+                                tm_ld16(tS + c, x);
                                 tm_wait(x);
-                                top = fmaxf(top, fmaf(__uint_as_float(x) * sk[c], unit, sb[c]));
+                                scaled(x, c);
+                                bound(x, c);
                             }
                         } else {
-                            auto bound = [&](const uint32_t (&x)[16], int col) {
-                                const float4 *at = reinterpret_cast<const float4 *>(sb + col);
-#pragma unroll
-                                for (int e = 0; e < 16; e += 4) {
-                                    const float4 y = at[e / 4];
-                                    float a = __uint_as_float(x[e]), b = __uint_as_float(x[e + 1]), c = __uint_as_float(x[e + 2]), d = __uint_as_float(x[e + 3]);
-                                    if constexpr (CW == 16) {
-                                        apart(fma2(two(a, b), both(unit), two(y.x, y.y)), a, b);
-                                        apart(fma2(two(c, d), both(unit), two(y.z, y.w)), c, d);
-                                    } else {
-                                        a = fmaf(a, unit, y.x), b = fmaf(b, unit, y.y), c = fmaf(c, unit, y.z), d = fmaf(d, unit, y.w);
-                                    }
-                                    top = csa_tc::fmax3f(csa_tc::fmax3f(top, a, b), c, d);
-                                }
-                            };
                             bound(xa, c0);
                             if (CW == 32) bound(xb, c0 + 16);
                             top = fmaxf(top, fmaf(__uint_as_float(behind), unit, sb[c0 + CW]));

@@ -488,9 +488,10 @@ int csa_decode_paged(const void *q, const void *k_pages, const void *v_pages, co
  *   makes what attends to it NaN.  Logits are formed from the codes in fp32, the
  *   weights times the values' scales are fp16 numbers (with up to 8 query heads per
  *   cached head, or per block of them, sums of two), the sums fp32.  The unit of those
- *   numbers follows the largest product of a weight and a scale that a head has, so
- *   that they keep their 11 bits down to 2^-8 of it, whatever the scales, and are off by
- *   2^-19 of it at most.  Everything else as csa_decode_paged, the workspace too.
+ *   numbers follows a head's largest product of a logit's exponential and the scale of
+ *   its row's value or a neighbour's, so that they keep their 11 bits down to 2^-8 of it,
+ *   whatever the scales, and are off by 2^-19 of it below.  Everything else as
+ *   csa_decode_paged, the workspace too.
  */
 int csa_decode_paged_q8(const void *q, const void *k_pages, const void *v_pages,
                         const float *row_scales, const void *k0, const void *v0,
