@@ -43,12 +43,14 @@
 //  - Over 8-bit pools a tile is 32 rows: codes become fp16 numbers in registers (keys as
 //    16-byte reads with the products' columns dealt to fit, values by an 8-bit ldmatrix),
 //    the queries are fp16 numbers times a power of two, and a row's scales multiply its
-//    logits and weights.  With half the bytes per row it is bound by the instructions of two
-//    warps per scheduler, 32% of the issue slots, waiting on one another's results (16-row
+//    logits and weights.  Weights times scales are fp16 numbers in a unit of each head's own,
+//    by its largest product.  With half the bytes per row it is bound by the instructions of
+//    two warps per scheduler, 33% of the issue slots, waiting on one another's results (16-row
 //    tiles with 12 or 10 workers: 182 and 210 us where 8 workers of 32 took 160; 32-row
-//    tiles with 12 workers spill, 224).  821 MB of 32 heads, e4m3, take 136 us (90% of the
+//    tiles with 12 workers spill, 224).  821 MB of 32 heads, e4m3, take 135 us (91% of the
 //    copy bandwidth), int8, whose codes take five instructions per four where e4m3 takes
-//    three, 157; 205 MB of 8 heads with 4 query heads each 47 and 53.
+//    three, 154; 205 MB of 8 heads with 4 query heads each 46 and 51.  Where every tile's
+//    scales are far apart (2^-20 to 2^20), e4m3 takes 158 and 52.
 //  - Few short sequences are bound by latency: a cluster of blocks then does one
 //    cached head of one sequence in a single launch and joins its parts through
 //    distributed shared memory (8.7 -> 5.8 us for 32 heads of 333 tokens).
@@ -1834,8 +1836,8 @@ int run_paged(PagedParams &p, void *scratch, int d, cudaStream_t stream) {
     p.part_ml = reinterpret_cast<float *>(p.joins + std::max(workers(d), segments));
     p.part_o = p.part_ml + (2 * workers(d) + segments) * p.HB * 2;
     // As many copies of the heads as eight rows hold.  16 sequences of 4096 to 8192 rows, d = 128, e4m3 (int8):
-    // 32 cached heads with one query head each take 136 us (157) with eight copies, 148 (166) with two and 164
-    // (183) with one; 16 with two 77 (86) with four, 81 (90) and 88 (99); 8 with four 47 (53) with two, 51 (56).
+    // 32 cached heads with one query head each take 136 us (154) with eight copies, 145 (165) with two and 159
+    // (181) with one; 16 with two 75 (85) with four, 79 (89) and 86 (97); 8 with four 46 (52) with two, 50 (55).
     // Rows of 16 bits have no copies: there the copies from memory take longer than the weights.
     if constexpr (KIND != CSA_BF16) {
         if (p.HB == 1) return launch_copies<KIND, 8>(p, d, stream);

@@ -30,15 +30,18 @@
 // the low parts take the high ones' place and have a product of their own, while the next
 // tile's logits are read.  One bf16 number (2^-9 off, where the output is rounded by as
 // much) left o up to 2.7e-3 of its norm off, and two 1.7e-3, which is the output's rounding;
-// it took 88 us where two take 100 (below).  Over 8-bit pools a weight is one fp16 number
-// (2^-12), and o is 1.6e-3 off.  All carry the factor (ln 2)^2, removed where parts are
-// written.
+// it took 88 us where two took 100 (16 drafted tokens, 16 sequences of 4096 to 8192 rows, before
+// the parts' cost was set).  Over 8-bit pools a weight times its row's scale is one fp16 number
+// (2^-12), in a unit that follows the largest, and o is 1.6e-3 off.  All carry the factor
+// (ln 2)^2, removed where parts are written.
 //
 // What bounds it: the weights, 24 instructions each of which 16 are the formula's; with two
-// softmax warps per scheduler the issue slots are 56% busy.  16 sequences of 4096 to 8192
-// rows, 32 heads on 8, d = 128 (400 MB, 60 us at the copy bandwidth), with the join:
-// 4 drafted tokens 76 us, 8 85 us, 16 99 us, 32 152 us, 64 293 us; e4m3 (210 MB) 5 96 us,
-// 16 128 us, 32 165 us, int8 16 137 us; d = 64 16 82 us; d = 256 16 181 us.
+// softmax warps per scheduler the issue slots are half busy (50%, e4m3 56%), the warps waiting
+// for tensor memory and for one another's results.  16 sequences of 4096 to 8192 rows, 32 heads
+// on 8, d = 128 (400 MB, 60 us at the copy bandwidth), with the join: 5 drafted tokens 81 us, 8
+// 82 us, 16 98 us, 32 151 us, 64 293 us; e4m3 (210 MB) 5 98 us, 16 115 us, 32 168 us, int8 16
+// 125 us; d = 64 16 84 us; d = 256 16 180 us, e4m3 215 us.  Where every tile's scales are far
+// apart (2^-20 to 2^20), e4m3 16 122 us, 32 185 us.
 #pragma once
 
 #include <atomic>

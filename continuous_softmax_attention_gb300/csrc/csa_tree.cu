@@ -24,8 +24,9 @@
 // are executed once a block and come from memory after the first kernel has streamed
 // the cache through the L2.  So loops are rolled even where they are short: with the two
 // rows of a warp and four parts of a row side by side, 16 drafted tokens over 16
-// sequences of 4096 to 8192 rows (32 heads on 8, d = 128) took 96 us instead of 90, of
-// which the second stretch and the join are 12; 64 drafted 255 and 250, of which 47.
+// sequences of 4096 to 8192 rows (32 heads on 8, d = 128) took 96 us instead of 90 and 64
+// drafted 255 instead of 250, when a weight was one number.  Now they take 98 and 293; the
+// second kernel, taken alone, 15 and 56.
 #include "csa_rows.cuh"
 
 namespace {
@@ -531,7 +532,7 @@ int launch_tree(TreeParams &p, cudaStream_t stream) {
     p.RB = kTreeRows;
     while (p.RB > 1 && segments * ((p.HB + p.RB - 1) / p.RB) < kGrid) p.RB /= 2;
     // beyond four rounds of blocks several groups each, that the drafted tokens are copied once for them (64 drafted over
-    // 16 sequences of 4096 to 8192 rows, 32 heads on 8, d = 256: 448 us, 476 with a group each)
+    // 16 sequences of 4096 to 8192 rows, 32 heads on 8, d = 256: 520 us, 549 with a group each)
     unsigned groups = (unsigned)((p.HB + p.RB - 1) / p.RB);
     while (groups > 1 && segments * groups > 4ll * kTreeBlocks<D> * kGrid) groups = (groups + 1) / 2;
     const dim3 grid((unsigned)segments, groups);
@@ -546,9 +547,9 @@ int launch_tree_of(TreeParams &p, int d, cudaStream_t stream) {
 }
 
 // Rows of a cached head above which they go to the kernel of csa_rows.cuh: at 17 the other one reads the cache twice.
-// 16 sequences of 4096 to 8192 rows, 8 cached heads, d = 128, 17 rows: 83 us here and 125 there (e4m3 96 and 116, int8
-// 108 and 125), 48 rows 99 and 175; d = 64, 32 rows 65 and 96; d = 256 161 and 283;
-// one sequence of 333 rows 11.9 and 13.5, of 2000 17.9 and 17.0.
+// 16 sequences of 4096 to 8192 rows, 8 cached heads, d = 128, 17 rows: 81 us there and 125 here (e4m3 97 and 115, int8
+// 109 and 121), 48 rows 96 and 178 (e4m3 112 and 164); d = 64, 32 rows 65 and 96; d = 256 160 and 283 (e4m3 192 and 251);
+// one sequence of 333 rows 12.3 and 14.6, of 2000 18.8 and 17.5; 64 ragged ones of 1 to 8192, e4m3, 32 rows 109 and 98.
 constexpr int kMany = 16;
 
 // Where the parts lie: notes, maxima and sums, unnormalised outputs.
