@@ -50,7 +50,8 @@ def make(kind, n, B, Hkv, d, S, seed):
             k.view(torch.uint8)[page, h, slot] = torch.where((logit >= 0)[:, None], code[h].view(torch.uint8), opposite.view(torch.uint8))
             scales[page, h, slot, 0] = logit.abs() / unit
             scales[page, h, slot, 1] *= torch.exp2(e)
-    return dict(k=k, v=v, scales=scales, table=table, u=u, lens=[n] * B, S=S)
+    k0, v0 = (torch.randn(Hkv, d, generator=g).to(torch.bfloat16) for _ in range(2))
+    return dict(k=k, v=v, scales=scales, table=table, u=u, lens=[n] * B, S=S, k0=k0, v0=v0)
 
 
 def queries(x, B, Hkv, G, T, seed):
@@ -60,7 +61,7 @@ def queries(x, B, Hkv, G, T, seed):
     return (f[..., None] * x["u"][None, :, None, None]).to(torch.bfloat16).view(B, Hkv * G, T, -1)
 
 
-def check(x, q, o, lse, rows, nodes, heads, only=None):
+def check(x, q, o, lse, rows, nodes, heads, mode=0, sign=1):
     """q, o [B, Hq, T, d]: row t of the chain that ends every sequence.
 
     Bound.  As draft_util.bounds, but by what the rows add: a weight is off by `rel` and by its rounding to fp16 (2^-11; with
@@ -70,11 +71,11 @@ def check(x, q, o, lse, rows, nodes, heads, only=None):
     the largest power of a logit times the scales of its row and the neighbours; with more than 16 rows 2^-6 or more, where
     a tile's scales lie that close together.  So each row may be off by 2^-29 M, or 2^-19 M, times its largest code."""
     B, Hq, T, d = q.shape
-    Hkv, scale = x["k"].shape[1], d ** -0.5
+    Hkv, scale = x["k"].shape[1], sign * d ** -0.5
     vk, vv = values(x["k"], x["v"], x["scales"])
     code = 448 if x["v"].dtype == KINDS["e4m3"] else 127
     o, lse = o.double().cpu().numpy(), lse.cpu().numpy()
-    for b in range(B) if only is None else only:
+    for b in range(B):
         n = x["lens"][b]
         k, v, s = (rows_of(t, x["table"][b], n, x["S"]) for t in (vk, vv, x["scales"].double()))
         for t in nodes:
@@ -83,12 +84,15 @@ def check(x, q, o, lse, rows, nodes, heads, only=None):
                 hk = h // (Hq // Hkv)
                 qq = torch.zeros(1, 1, m, d, dtype=torch.float64)
                 qq[0, 0, -1] = q[b, h, t].double()
-                one = lambda vals: oracle.forward_rows(qq, k[None, hk:hk + 1, :m], vals[None, hk:hk + 1, :m], [m - 1], scale=scale, mode=0)  # noqa: E731
-                (ro, rl), (ao, _) = one(v), one(v.abs())
+                k0, v0 = x["k0"][hk:hk + 1].double(), x["v0"][hk:hk + 1].double()
+                one = lambda f: oracle.forward_rows(qq, k[None, hk:hk + 1, :m], f(v[None, hk:hk + 1, :m]), [m - 1], k0=k0, v0=f(v0),  # noqa: E731
+                                                    scale=scale, mode=mode)
+                (ro, rl), (ao, _) = one(lambda y: y), one(torch.abs)
                 a = scale * (k[hk, :m] @ q[b, h, t].double()).numpy()
-                rel = (d + 8) * 2.0 ** -24 * np.abs(a).max() + 2.0 ** -16
+                sink = 0.0 if mode == 0 else a[0] if mode == 1 else scale * (k0[0] @ q[b, h, t].double()).item()
+                rel = (d + 8) * 2.0 ** -24 * max(np.abs(a).max(), abs(sink)) + 2.0 ** -16
                 y = np.pad(s[hk, :m, 1].numpy(), 1)
-                M = max((np.exp(a - rl[0]) * np.maximum(np.maximum(y[:-2], y[1:-1]), y[2:])).max(), np.exp(-rl[0]) * y[1])
+                M = max((np.exp(a - rl[0]) * np.maximum(np.maximum(y[:-2], y[1:-1]), y[2:])).max(), np.exp(sink - rl[0]) * y[1])
                 bound = 2.0 ** -8 * np.abs(ro[0]) + (2 * rel + 2.0 ** -11 + 2.0 ** -16 + (4.4e-4 if rows > 16 else 0.0)) * ao[0]
                 bound = bound + m * (2.0 ** -19 if rows > 16 else 2.0 ** -29) * M * code
                 err = np.abs(o[b, h, t] - ro[0])
@@ -124,4 +128,22 @@ def test_drafts(kind, d, T, G):
     o, lse = decode_tree(q.cuda(), x["k"].cuda(), x["v"].cuda(), torch.as_tensor(x["table"]).cuda(), torch.tensor(x["lens"], **INT),
                          row_scales=x["scales"].cuda())
     check(x, q, o, lse, G * T, sorted({0, T // 2, T - 1}), sorted({0, G - 1}))
+    assert device_status() == 0
+
+
+@EIGHT
+@pytest.mark.parametrize("mode", [1, 2])
+@pytest.mark.parametrize("T,G", [(1, 1), (1, 16), (3, 2), (20, 1), (12, 4), (16, 8)])
+def test_sinks_and_a_negative_scale(kind, mode, T, G):
+    """A copied sink, whose value is the first row's, and a given one; logits of the other sign."""
+    x = make(kind, 3000, 10, 1, 128, 32, seed=T + G)
+    q = queries(x, 10, 1, G, T, seed=mode)
+    for sign in (1, -1):
+        c = [t.cuda() for t in (q, x["k"], x["v"], torch.as_tensor(x["table"]), torch.tensor(x["lens"], dtype=torch.int32), x["k0"], x["v0"])]
+        kw = dict(row_scales=x["scales"].cuda(), mode=mode, scale=sign * 128 ** -0.5)
+        if T == 1:
+            o, lse = (t[:, :, None] for t in decode_paged(c[0][:, :, 0].contiguous(), *c[1:], **kw))
+        else:
+            o, lse = decode_tree(*c[:5], None, *c[5:], **kw)
+        check(x, q, o, lse, G * T, sorted({0, T - 1}), sorted({0, G - 1}), mode, sign)
     assert device_status() == 0
