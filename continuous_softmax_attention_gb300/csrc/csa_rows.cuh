@@ -36,12 +36,12 @@
 // (ln 2)^2, removed where parts are written.
 //
 // What bounds it: the weights, 24 instructions each of which 16 are the formula's; with two
-// softmax warps per scheduler the issue slots are half busy (50%, e4m3 56%), the warps waiting
+// softmax warps per scheduler the issue slots are half busy (50%, e4m3 57%), the warps waiting
 // for tensor memory and for one another's results.  16 sequences of 4096 to 8192 rows, 32 heads
 // on 8, d = 128 (400 MB, 60 us at the copy bandwidth), with the join: 5 drafted tokens 81 us, 8
-// 82 us, 16 98 us, 32 151 us, 64 293 us; e4m3 (210 MB) 5 98 us, 16 115 us, 32 168 us, int8 16
-// 125 us; d = 64 16 84 us; d = 256 16 180 us, e4m3 215 us.  Where every tile's scales are far
-// apart (2^-20 to 2^20), e4m3 16 122 us, 32 185 us.
+// 82 us, 16 98 us, 32 151 us, 64 293 us; e4m3 (210 MB) 5 97 us, 16 112 us, 32 166 us, int8 16
+// 123 us; d = 64 16 84 us; d = 256 16 180 us, e4m3 205 us.  Where every tile's scales are far
+// apart (2^-20 to 2^20), e4m3 16 118 us, 32 186 us.
 #pragma once
 
 #include <atomic>
@@ -985,70 +985,10 @@ rows_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUten
                 }
             }
         __syncwarp();
-    } else if (EIGHT && some && warp == C::ScaleWarp) {
-        // ------------------------------------------------- the cached rows' scales
-        if constexpr (EIGHT) {
-            float *ring = reinterpret_cast<float *>(smem + C::OffScales);
-            int tiles = 0;
-            float lift = 0.0f;
-            bool ok = true;
-            do {
-                for (int j = now.tile; j < now.last; ++j, ++tiles) {
-                    const int stage = tiles % NS, own = now.n - j * KT;
-                    const float2 *rs = reinterpret_cast<const float2 *>(smem + C::OffRing + stage * C::StageBytes + C::RawK + C::RawV);
-                    if (!(ok = __all_sync(0xffffffffu, idle(k_full(stage), tiles / NS) && idle(k_free, tiles + 1)))) break;
-                    float2 x[(KR + 31) / 32];
-                    float big = 0.0f, least = INFINITY;
-#pragma unroll
-                    for (int i = 0; i < (KR + 31) / 32; ++i) {
-                        const int r = 32 * i + lane;
-                        x[i] = r < KR ? rs[r] : make_float2(0.0f, 0.0f);
-                        if (r < own && r < KT) {
-                            big = fmaxf(big, fabsf(x[i].y));
-                            least = fminf(least, fabsf(x[i].y));
-                        }
-                    }
-                    // the unit of the values: see csa_paged.cuh; a new part, a new unit
-                    big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
-                    least = __uint_as_float(__reduce_min_sync(0xffffffffu, __float_as_uint(least)));
-                    if (j == now.tile || big * lift > kMostScale) {
-                        // 2^kLift2 by the power of two at or above the largest
-                        const uint32_t e2 = min(max((__float_as_uint(big) + 0x7fffffu) >> 23, 8u), 253u);
-                        lift = __uint_as_float((254u + kLift2 - e2) << 23);
-                    }
-                    float *to = ring + (tiles & 3) * 3 * KR;
-#pragma unroll
-                    for (int i = 0; i < (KR + 31) / 32; ++i) {
-                        const int r = 32 * i + lane;
-                        if (r < KR) {
-                            to[r] = x[i].x;
-                            to[KR + r] = r < own && r < KT ? x[i].y * lift : 0.0f;
-                        }
-                    }
-                    const bool uneven = least * lift < kLeastScale;
-                    if (lane == 0) s_lift[tiles & 3] = uneven ? -lift : lift;
-                    __syncwarp();
-                    if (uneven) {
-                        // what a logit's power may bring to its row's product and its neighbours', log2 over 2^kLift2; the
-                        // last column is the row before the tile, whose power the first row's weight has
-                        const float *sv = to + KR;
-#pragma unroll 1
-                        for (int r = lane; r < KR; r += 32) {
-                            float y = fabsf(sv[r < KR - 1 ? r : 0]);
-                            if (r < KR - 1) y = fmaxf(y, fmaxf(r > 0 ? fabsf(sv[r - 1]) : 0.0f, fabsf(sv[r + 1])));
-                            to[2 * KR + r] = r < own || r == KR - 1 ? fmaxf(__log2f(y) - (float)kLift2, -80.0f) : -INFINITY;
-                        }
-                        __syncwarp();
-                    }
-                    if (lane == 0) {
-                        mbar_arrive(k_ready);
-                        mbar_arrive(k_empty(stage));
-                    }
-                }
-            } while (ok && next());
-        }
     } else if (EIGHT && some && warp >= C::TurnWarp) {
         // ------------------------------------------- codes become fp16 numbers
+        // (before the scales' warp: behind its instructions these miss the caches more often, 115 us instead of 111 for 16
+        // drafted tokens as above, d = 256 217 instead of 206)
         if constexpr (EIGHT) {
             const int t = tid - 32 * C::TurnWarp;
             constexpr int T = 32 * C::TurnWarps, PerRow = D / 16, Step = T / PerRow;
@@ -1116,6 +1056,68 @@ rows_kernel(const __grid_constant__ PagedParams p, const __grid_constant__ CUten
                     if (!goes_on) break;
                 }
             }
+        }
+    } else if (EIGHT && some && warp == C::ScaleWarp) {
+        // ------------------------------------------------- the cached rows' scales
+        if constexpr (EIGHT) {
+            float *ring = reinterpret_cast<float *>(smem + C::OffScales);
+            int tiles = 0;
+            float lift = 0.0f;
+            bool ok = true;
+            do {
+                for (int j = now.tile; j < now.last; ++j, ++tiles) {
+                    const int stage = tiles % NS, own = now.n - j * KT;
+                    const float2 *rs = reinterpret_cast<const float2 *>(smem + C::OffRing + stage * C::StageBytes + C::RawK + C::RawV);
+                    if (!(ok = __all_sync(0xffffffffu, idle(k_full(stage), tiles / NS) && idle(k_free, tiles + 1)))) break;
+                    float2 x[(KR + 31) / 32];
+                    float big = 0.0f, least = INFINITY;
+#pragma unroll
+                    for (int i = 0; i < (KR + 31) / 32; ++i) {
+                        const int r = 32 * i + lane;
+                        x[i] = r < KR ? rs[r] : make_float2(0.0f, 0.0f);
+                        if (r < own && r < KT) {
+                            big = fmaxf(big, fabsf(x[i].y));
+                            least = fminf(least, fabsf(x[i].y));
+                        }
+                    }
+                    // the unit of the values: see csa_paged.cuh; a new part, a new unit
+                    big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
+                    least = __uint_as_float(__reduce_min_sync(0xffffffffu, __float_as_uint(least)));
+                    if (j == now.tile || big * lift > kMostScale) {
+                        // 2^kLift2 by the power of two at or above the largest
+                        const uint32_t e2 = min(max((__float_as_uint(big) + 0x7fffffu) >> 23, 8u), 253u);
+                        lift = __uint_as_float((254u + kLift2 - e2) << 23);
+                    }
+                    float *to = ring + (tiles & 3) * 3 * KR;
+#pragma unroll
+                    for (int i = 0; i < (KR + 31) / 32; ++i) {
+                        const int r = 32 * i + lane;
+                        if (r < KR) {
+                            to[r] = x[i].x;
+                            to[KR + r] = r < own && r < KT ? x[i].y * lift : 0.0f;
+                        }
+                    }
+                    const bool uneven = least * lift < kLeastScale;
+                    if (lane == 0) s_lift[tiles & 3] = uneven ? -lift : lift;
+                    __syncwarp();
+                    if (uneven) {
+                        // what a logit's power may bring to its row's product and its neighbours', log2 over 2^kLift2; the
+                        // last column is the row before the tile, whose power the first row's weight has
+                        const float *sv = to + KR;
+#pragma unroll 1
+                        for (int r = lane; r < KR; r += 32) {
+                            float y = fabsf(sv[r < KR - 1 ? r : 0]);
+                            if (r < KR - 1) y = fmaxf(y, fmaxf(r > 0 ? fabsf(sv[r - 1]) : 0.0f, fabsf(sv[r + 1])));
+                            to[2 * KR + r] = r < own || r == KR - 1 ? fmaxf(__log2f(y) - (float)kLift2, -80.0f) : -INFINITY;
+                        }
+                        __syncwarp();
+                    }
+                    if (lane == 0) {
+                        mbar_arrive(k_ready);
+                        mbar_arrive(k_empty(stage));
+                    }
+                }
+            } while (ok && next());
         }
     }
     tc_fence_before();

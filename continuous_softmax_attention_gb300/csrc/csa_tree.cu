@@ -548,7 +548,7 @@ int launch_tree_of(TreeParams &p, int d, cudaStream_t stream) {
 
 // Rows of a cached head above which they go to the kernel of csa_rows.cuh: at 17 the other one reads the cache twice.
 // 16 sequences of 4096 to 8192 rows, 8 cached heads, d = 128, 17 rows: 81 us there and 125 here (e4m3 97 and 115, int8
-// 109 and 121), 48 rows 96 and 178 (e4m3 112 and 164); d = 64, 32 rows 65 and 96; d = 256 160 and 283 (e4m3 192 and 251);
+// 109 and 121), 48 rows 97 and 178 (e4m3 110 and 164); d = 64, 32 rows 65 and 96; d = 256 161 and 283 (e4m3 183 and 251);
 // one sequence of 333 rows 12.3 and 14.6, of 2000 18.8 and 17.5; 64 ragged ones of 1 to 8192, e4m3, 32 rows 109 and 98.
 constexpr int kMany = 16;
 
