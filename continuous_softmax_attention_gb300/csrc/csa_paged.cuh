@@ -112,7 +112,7 @@ constexpr float kRaise = 16.0f, kRaise8 = 6.0f;
 // product (by its bound, the larger of its intervals' powers).  Scales may be kMostScale of those units: weights are 2^6 at
 // most, half as much more with a copied sink's, 1.5 * 2^14.  And no less than kLeastScale: the largest weight's product is
 // then far above 2^-14, where fp16 begins to lose bits.  Scales of a tile within 2^kSpread of one another stay within both.
-constexpr int kLift2 = 5, kSpread = 10;
+constexpr int kLift2 = 7, kSpread = 12;
 constexpr float kMostScale = 256.0f, kLeastScale = 1.0f / 64;
 
 __device__ int g_paged_status;  // sticky status word of the including file's kernels
